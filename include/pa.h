@@ -67,8 +67,10 @@ enum {
   PA_ERR_SCRATCH_LIMIT = -15, /* pa_decode_static_workspace: the call needs more
                                  split-K scratch than its fixed 16 MiB array */
   PA_ERR_POOL_EMPTY = -16,   /* pa_pool_*: not enough free pages (nothing taken) */
-  PA_ERR_POOL_STATE = -17    /* pa_pool_*: a page that is not in use (a double
+  PA_ERR_POOL_STATE = -17,   /* pa_pool_*: a page that is not in use (a double
                                 release, a share of a free page) */
+  PA_ERR_ROPE = -18          /* rot_dim not a multiple of 16 in 16 .. head_dim, or
+                                max_pos not positive */
 };
 
 /* Human-readable name of a status code.  Never NULL. */
@@ -478,6 +480,136 @@ int pa_decode_static_workspace(const void *q, const void *k_cache,
                                int page_size, int batch, int max_blocks_per_seq,
                                int num_pages, pa_dtype dtype,
                                int partition_tokens, pa_stream_t stream);
+
+/*
+ * pa_append_kv_rope -- pa_append_kv with the rotary position embedding applied
+ * on the way, to the keys and (optionally) to the step's queries.
+ *
+ * The pages have no counterpart to the rotation; it is what models whose keys
+ * carry their position this way do between the projection and the cache.
+ * The first rot_dim dimensions of a row form rot_dim / 2 pairs: (i, i +
+ * rot_dim / 2), or with interleaved != 0 the neighbours (2 i, 2 i + 1).  Pair i
+ * of token j turns by the angle of its position,
+ *   a' = a cos - b sin,  b' = b cos + a sin,
+ * with cos_sin[pos[j]][i] the cosine and cos_sin[pos[j]][rot_dim / 2 + i] the
+ * sine (any frequencies or scaling: the table is the caller's).  The arithmetic
+ * is fp32, each operation rounded, and the result rounded once to dtype.  The
+ * other dimensions, and V, keep their bits.
+ *   k_new, v_new  device; row of token j and kv head g at j * k_stride + g *
+ *                 head_dim (v_stride likewise), so views of a fused projection's
+ *                 output need no copy
+ *   q             device, rows at j * q_stride + h * head_dim; NULL: no queries
+ *   q_out         device [n_tok][n_q_heads][head_dim], the rotated queries; it
+ *                 may be q itself when q_stride is n_q_heads * head_dim, and must
+ *                 not overlap any other input.  NULL exactly when q is.
+ *   cos_sin       device float [max_pos][rot_dim]
+ *   *_stride      in elements, multiples of 8, at least heads * head_dim
+ *   rot_dim       a multiple of 16, 16 .. head_dim (PA_ERR_ROPE otherwise)
+ * k_new, v_new, q, q_out, caches and cos_sin must be 16-byte aligned.  The rest
+ * is pa_append_kv's, its rule on two tokens with one place included.  A token
+ * whose seq_idx, pos (pos >= max_pos too) or page is bad is skipped, its row of
+ * q_out left as it was, and PA_ERR_BAD_INDEX / PA_ERR_BAD_BLOCK recorded.
+ * n_q_heads is not used when q is NULL.  Asynchronous on `stream`.
+ */
+int pa_append_kv_rope(const void *k_new, const void *v_new, const void *q, void *k_cache,
+                      void *v_cache, void *q_out, const int32_t *block_table,
+                      const int32_t *seq_idx, const int32_t *pos, const float *cos_sin,
+                      int n_tok, int64_t k_stride, int64_t v_stride, int64_t q_stride,
+                      int n_q_heads, int n_kv_heads, int head_dim, int page_size, int batch,
+                      int max_blocks_per_seq, int num_pages, int max_pos, int rot_dim,
+                      int interleaved, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * The 4-bit cache.  One pool holds K and V:
+ *   kv_cache: [num_pages][n_kv_heads][pa_kv4_block_bytes(head_dim)] bytes, and a
+ *   block (one page of one kv head) is
+ *     codes  [K, V][16 tokens][head_dim / 2] bytes: dimension 2 i in the low
+ *            four bits of byte i, 2 i + 1 in the high four
+ *     then   [K, V][16 tokens][scale, zero], 16-bit floats of dtype
+ *   which stands for x = zero + scale * (code - 8).
+ * Block tables, page ids and the page pool are those of the 16-bit caches.  The
+ * pool must be 16-byte aligned.  Rows past a sequence's end may hold anything.
+ * pa_kv4_block_bytes is 16 * head_dim + 128, or 0 for an unsupported head_dim.
+ */
+size_t pa_kv4_block_bytes(int head_dim);
+
+/*
+ * pa_append_kv4 -- write the K and V rows of new tokens into their pages of a
+ * 4-bit cache, with the rotation of pa_append_kv_rope applied to K and q unless
+ * cos_sin is NULL (then rot_dim, max_pos and interleaved are not used, and q is
+ * copied to q_out).
+ *
+ * A row x of head_dim values (fp32 after the rotation, not rounded in between):
+ *   scale = r((max x - min x) * fp32(1 / 15)), zero = r(min x + 8 scale),
+ *   code  = rint((x - zero) / scale) + 8, clamped to 0 .. 15,
+ * r rounding to dtype, everything else fp32 step by step.  scale = 0 gives code
+ * 8.  A row whose range, scale or zero is not finite is stored as scale = zero =
+ * NaN: attention over it gives NaN, as a NaN key or value would.
+ * The other arguments are pa_append_kv_rope's.
+ */
+int pa_append_kv4(const void *k_new, const void *v_new, const void *q, void *kv_cache,
+                  void *q_out, const int32_t *block_table, const int32_t *seq_idx,
+                  const int32_t *pos, const float *cos_sin, int n_tok, int64_t k_stride,
+                  int64_t v_stride, int64_t q_stride, int n_q_heads, int n_kv_heads,
+                  int head_dim, int page_size, int batch, int max_blocks_per_seq,
+                  int num_pages, int max_pos, int rot_dim, int interleaved, pa_dtype dtype,
+                  pa_stream_t stream);
+
+/*
+ * pa_read_kv4 -- the values that a 4-bit cache holds for listed tokens, rounded
+ * to dtype: the inverse of pa_append_kv4 (to move a sequence into a 16-bit
+ * cache, or to look at what is stored).
+ *   k_out, v_out  device [n_tok][n_kv_heads][head_dim], 16-byte aligned
+ * Token j is (seq_idx[j], pos[j]), any order, repeats allowed.  A bad index or
+ * page leaves that token's rows as they were and is recorded as in the appends.
+ */
+int pa_read_kv4(const void *kv_cache, const int32_t *block_table, const int32_t *seq_idx,
+                const int32_t *pos, void *k_out, void *v_out, int n_tok, int n_kv_heads,
+                int head_dim, int page_size, int batch, int max_blocks_per_seq, int num_pages,
+                pa_dtype dtype, pa_stream_t stream);
+
+/* pa_copy_pages for a 4-bit cache: page src[i] to page dst[i], every kv head. */
+int pa_copy_pages_kv4(void *kv_cache, const int32_t *src, const int32_t *dst, int n,
+                      int n_kv_heads, int head_dim, int page_size, int num_pages,
+                      pa_stream_t stream);
+
+/*
+ * pa_decode_kv4 -- pa_decode over a 4-bit cache: out = softmax(q K^T scale) V of
+ * the values the cache stands for, fp32 accumulation, fp32 out.  T = 0 writes
+ * zeros.  The pages of all sequences are cut into equal runs, one a CTA, whatever
+ * the sequences' lengths, so there is no partition size to choose.
+ *   workspace  device, >= pa_decode_kv4_workspace_size(head_dim) bytes on the
+ *              current device, 16-byte aligned; contents on entry do not matter.
+ *              Two calls that overlap on the GPU must not share one.
+ * dtype is q's and that of the cache's scales and zeros.  The rest is
+ * pa_decode's.
+ */
+int pa_decode_kv4(const void *q, const void *kv_cache, const int32_t *block_table,
+                  const int32_t *ctx_lens, float *out, float scale, int n_q_heads,
+                  int n_kv_heads, int head_dim, int page_size, int batch,
+                  int max_blocks_per_seq, int num_pages, pa_dtype dtype, void *workspace,
+                  size_t workspace_bytes, pa_stream_t stream);
+/* 0 for an unsupported head_dim. */
+size_t pa_decode_kv4_workspace_size(int head_dim);
+
+/*
+ * pa_prefill_kv4 -- pa_prefill_paged over a 4-bit cache: query i of sequence b
+ * attends keys 0 .. ctx_lens[b] + i, the chunk's own rows (stored by
+ * pa_append_kv4) included; n_new from the few drafted tokens of a speculative
+ * verify to a long chunk.
+ *   out        device [batch][n_new][n_q_heads][head_dim] in q's dtype: a chunk's
+ *              rows go into a 16-bit product, and the tensor-core sums over a
+ *              long context are not good to fp32's last bits
+ *   workspace  as in pa_decode_kv4, pa_prefill_kv4_workspace_size(...) bytes
+ */
+int pa_prefill_kv4(const void *q, const void *kv_cache, const int32_t *block_table,
+                   const int32_t *ctx_lens, int n_new, void *out, float scale, int n_q_heads,
+                   int n_kv_heads, int head_dim, int page_size, int batch,
+                   int max_blocks_per_seq, int num_pages, pa_dtype dtype, void *workspace,
+                   size_t workspace_bytes, pa_stream_t stream);
+/* 0 for invalid arguments. */
+size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_kv_heads,
+                                     int head_dim, int page_size, int max_blocks_per_seq);
 
 /*
  * pa_last_device_error -- synchronise `stream`, then return and clear the

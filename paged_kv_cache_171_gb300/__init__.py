@@ -31,6 +31,10 @@ __all__ = [
     "prefill_split", "pa_decode_cascade", "pa_decode_cascade_workspace_size",
     "decode_cascade",
     "append_kv",
+    "pa_append_kv_rope", "append_kv_rope", "rope_table",
+    "pa_kv4_block_bytes", "kv4_cache", "pa_append_kv4", "append_kv4", "pa_read_kv4", "read_kv4",
+    "pa_copy_pages_kv4", "copy_pages_kv4", "pa_decode_kv4", "pa_decode_kv4_workspace_size",
+    "decode_kv4", "pa_prefill_kv4", "pa_prefill_kv4_workspace_size", "prefill_kv4",
 ]
 
 BF16 = 0
@@ -110,6 +114,25 @@ def lib():
         L.pa_decode_cascade_workspace_size.restype = Z
         L.pa_decode_static_workspace.argtypes = [P, P, P, P, P, P, F] + [I] * 9 + [P]
         L.pa_decode_static_workspace.restype = I
+        J = ctypes.c_int64
+        L.pa_append_kv_rope.argtypes = [P] * 10 + [I, J, J, J] + [I] * 11 + [P]
+        L.pa_append_kv_rope.restype = I
+        L.pa_kv4_block_bytes.argtypes = [I]
+        L.pa_kv4_block_bytes.restype = Z
+        L.pa_append_kv4.argtypes = [P] * 9 + [I, J, J, J] + [I] * 11 + [P]
+        L.pa_append_kv4.restype = I
+        L.pa_read_kv4.argtypes = [P] * 6 + [I] * 8 + [P]
+        L.pa_read_kv4.restype = I
+        L.pa_copy_pages_kv4.argtypes = [P] * 3 + [I] * 5 + [P]
+        L.pa_copy_pages_kv4.restype = I
+        L.pa_decode_kv4.argtypes = [P] * 5 + [F] + [I] * 8 + [P, Z, P]
+        L.pa_decode_kv4.restype = I
+        L.pa_decode_kv4_workspace_size.argtypes = [I]
+        L.pa_decode_kv4_workspace_size.restype = Z
+        L.pa_prefill_kv4.argtypes = [P] * 4 + [I, P, F] + [I] * 8 + [P, Z, P]
+        L.pa_prefill_kv4.restype = I
+        L.pa_prefill_kv4_workspace_size.argtypes = [I] * 7
+        L.pa_prefill_kv4_workspace_size.restype = Z
         L.pa_last_device_error.argtypes = [P]
         L.pa_last_device_error.restype = I
         L.pa_selftest_wait_timeout.argtypes = [P]
@@ -392,6 +415,80 @@ def pa_topm_retain(scores, n_layers, n_heads, n_tokens, current, budget, keep,
     return _check(rc, "pa_topm_retain")
 
 
+def pa_append_kv_rope(k_new, v_new, q, k_cache, v_cache, q_out, block_table, seq_idx, pos,
+                      cos_sin, n_tok, k_stride, v_stride, q_stride, n_q_heads, n_kv_heads,
+                      head_dim, page_size, batch, max_blocks_per_seq, num_pages, max_pos,
+                      rot_dim, interleaved, dtype, stream=None) -> int:
+    rc = lib().pa_append_kv_rope(
+        _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(q_out),
+        _ptr(block_table), _ptr(seq_idx), _ptr(pos), _ptr(cos_sin), n_tok, k_stride, v_stride,
+        q_stride, n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+        num_pages, max_pos, rot_dim, int(interleaved), dtype, _stream(stream))
+    return _check(rc, "pa_append_kv_rope")
+
+
+def pa_kv4_block_bytes(head_dim) -> int:
+    return lib().pa_kv4_block_bytes(head_dim)
+
+
+def pa_append_kv4(k_new, v_new, q, kv_cache, q_out, block_table, seq_idx, pos, cos_sin, n_tok,
+                  k_stride, v_stride, q_stride, n_q_heads, n_kv_heads, head_dim, page_size,
+                  batch, max_blocks_per_seq, num_pages, max_pos, rot_dim, interleaved, dtype,
+                  stream=None) -> int:
+    rc = lib().pa_append_kv4(
+        _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(kv_cache), _ptr(q_out), _ptr(block_table),
+        _ptr(seq_idx), _ptr(pos), _ptr(cos_sin), n_tok, k_stride, v_stride, q_stride, n_q_heads,
+        n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, num_pages, max_pos, rot_dim,
+        int(interleaved), dtype, _stream(stream))
+    return _check(rc, "pa_append_kv4")
+
+
+def pa_read_kv4(kv_cache, block_table, seq_idx, pos, k_out, v_out, n_tok, n_kv_heads, head_dim,
+                page_size, batch, max_blocks_per_seq, num_pages, dtype, stream=None) -> int:
+    rc = lib().pa_read_kv4(
+        _ptr(kv_cache), _ptr(block_table), _ptr(seq_idx), _ptr(pos), _ptr(k_out), _ptr(v_out),
+        n_tok, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, num_pages, dtype,
+        _stream(stream))
+    return _check(rc, "pa_read_kv4")
+
+
+def pa_copy_pages_kv4(kv_cache, src, dst, n, n_kv_heads, head_dim, page_size, num_pages,
+                      stream=None) -> int:
+    rc = lib().pa_copy_pages_kv4(_ptr(kv_cache), _ptr(src), _ptr(dst), n, n_kv_heads, head_dim,
+                                 page_size, num_pages, _stream(stream))
+    return _check(rc, "pa_copy_pages_kv4")
+
+
+def pa_decode_kv4(q, kv_cache, block_table, ctx_lens, out, scale, n_q_heads, n_kv_heads,
+                  head_dim, page_size, batch, max_blocks_per_seq, num_pages, dtype,
+                  workspace=None, workspace_bytes=0, stream=None) -> int:
+    rc = lib().pa_decode_kv4(
+        _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(ctx_lens), _ptr(out), float(scale),
+        n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, num_pages, dtype,
+        _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "pa_decode_kv4")
+
+
+def pa_decode_kv4_workspace_size(head_dim) -> int:
+    return lib().pa_decode_kv4_workspace_size(head_dim)
+
+
+def pa_prefill_kv4(q, kv_cache, block_table, ctx_lens, n_new, out, scale, n_q_heads, n_kv_heads,
+                   head_dim, page_size, batch, max_blocks_per_seq, num_pages, dtype,
+                   workspace=None, workspace_bytes=0, stream=None) -> int:
+    rc = lib().pa_prefill_kv4(
+        _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(ctx_lens), n_new, _ptr(out),
+        float(scale), n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+        num_pages, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "pa_prefill_kv4")
+
+
+def pa_prefill_kv4_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim, page_size,
+                                  max_blocks_per_seq) -> int:
+    return lib().pa_prefill_kv4_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim,
+                                               page_size, max_blocks_per_seq)
+
+
 def pa_last_device_error(stream=None) -> int:
     """Synchronises the stream; returns and clears the device status word."""
     return lib().pa_last_device_error(_stream(stream))
@@ -547,3 +644,246 @@ def topm_retain(scores, current, budget, keep=None, kept_per_head=None, workspac
     pa_topm_retain(scores, L, H, N, current, budget, keep, kept_per_head, workspace, ws_bytes,
                    stream)
     return keep, kept_per_head
+
+
+# --- rotated appends and the 4-bit cache --------------------------------------
+
+def _want(t, name, dtype, shape, device):
+    """t is a contiguous tensor of this type, shape (None: any extent) and device."""
+    if (t.dtype != dtype or t.dim() != len(shape) or t.device != device or
+            not t.is_contiguous() or
+            any(w is not None and n != w for n, w in zip(t.shape, shape))):
+        raise ValueError(
+            f"{name}: want a contiguous {dtype} tensor of shape "
+            f"{tuple('*' if w is None else w for w in shape)} on {device}, got {t.dtype} "
+            f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+
+
+def _token_stride(t, name, like, heads, D):
+    """Elements from one token's rows [heads, D] to the next one's."""
+    if t.dtype != like.dtype or t.device != like.device or t.dim() != 3 or \
+            t.shape[0] != like.shape[0] or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name}: want {like.dtype} [{like.shape[0]}, {heads}, {D}] on "
+                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous rows (strides "
+                         f"{tuple(t.stride())}); call .contiguous()")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+class _Launch:
+    """The device and stream of one call: the device of its tensors is made
+    current, and what the call allocates belongs to the stream it runs on."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {device}")
+        self._guards = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
+    """cos_sin of the rotated appends, float32 [max_pos, rot_dim]: the cosines of
+    position * base^(-2 i / rot_dim) for i < rot_dim / 2, then the sines (angles
+    in float64, so far positions keep their digits)."""
+    import torch
+    inv = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat((ang.cos(), ang.sin()), -1).float()
+
+
+def kv4_cache(num_pages, n_kv_heads, head_dim, device="cuda"):
+    """An empty 4-bit cache: uint8 [num_pages, n_kv_heads, block bytes]."""
+    import torch
+    block = pa_kv4_block_bytes(head_dim)
+    if not block:
+        raise PAError(-3, "kv4_cache")
+    return torch.zeros((num_pages, n_kv_heads, block), dtype=torch.uint8, device=device)
+
+
+def _kv4_dims(kv_cache, hkv=None):
+    """num_pages, n_kv_heads and head_dim of a 4-bit cache tensor."""
+    import torch
+    if kv_cache.dim() != 3 or kv_cache.dtype != torch.uint8 or not kv_cache.is_contiguous() or \
+            kv_cache.shape[2] not in (1152, 2176) or (hkv is not None and
+                                                      kv_cache.shape[1] != hkv):
+        raise ValueError("kv_cache: want contiguous uint8 [num_pages, n_kv_heads, "
+                         f"pa_kv4_block_bytes(head_dim)], got {kv_cache.dtype} "
+                         f"{tuple(kv_cache.shape)}")
+    pages, heads, block = kv_cache.shape
+    return pages, heads, (block - 128) // 16
+
+
+def _append_args(k_new, v_new, q, q_out, block_table, seq_idx, pos, cos_sin):
+    import torch
+    n_tok, hkv, D = k_new.shape
+    dev = k_new.device
+    ks = _token_stride(k_new, "k_new", k_new, hkv, D)
+    vs = _token_stride(v_new, "v_new", k_new, hkv, D)
+    _want(block_table, "block_table", torch.int32, (None, None), dev)
+    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), dev)
+    _want(pos, "pos", torch.int32, (n_tok,), dev)
+    if cos_sin is not None:
+        _want(cos_sin, "cos_sin", torch.float32, (None, None), dev)
+    hq = qs = 0
+    if q is not None:
+        hq = q.shape[1]
+        qs = _token_stride(q, "q", k_new, hq, D)
+        if q_out is not None:
+            _want(q_out, "q_out", k_new.dtype, (n_tok, hq, D), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    return n_tok, hq, hkv, D, ks, vs, qs
+
+
+def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, cos_sin, q=None,
+                   q_out=None, interleaved=False, stream=None):
+    """pa_append_kv_rope on tensors: k_new, v_new [n_tok, h_kv, D] and q
+    [n_tok, h_q, D] may be views with any token stride (a fused projection's
+    output); cos_sin float32 [max_pos, rot_dim] (rope_table).  Writes the caches
+    [pages, h_kv, 16, D]; returns the rotated q ([n_tok, h_q, D], q_out if
+    given), or None without q."""
+    import torch
+    n_tok, hq, hkv, D, ks, vs, qs = _append_args(k_new, v_new, q, q_out, block_table, seq_idx,
+                                                 pos, cos_sin)
+    _want(k_cache, "k_cache", k_new.dtype, (None, hkv, None, D), k_new.device)
+    _want(v_cache, "v_cache", k_new.dtype, tuple(k_cache.shape), k_new.device)
+    with _Launch(k_new.device, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty((n_tok, hq, D), dtype=q.dtype, device=q.device)
+        pa_append_kv_rope(k_new, v_new, q, k_cache, v_cache, q_out, block_table, seq_idx, pos,
+                          cos_sin, n_tok, ks, vs, qs, hq, hkv, D, k_cache.shape[2],
+                          block_table.shape[0], block_table.shape[1], k_cache.shape[0],
+                          cos_sin.shape[0], cos_sin.shape[1], interleaved, dtype_code(k_new))
+    return q_out
+
+
+def append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin=None, q=None,
+               q_out=None, interleaved=False, stream=None):
+    """pa_append_kv4 on tensors: as append_kv_rope, into a 4-bit cache (kv4_cache);
+    without cos_sin nothing is rotated.  The dtype of k_new is that of the cache's
+    scales and zeros: keep to one for a cache.  Returns the rotated q, or None."""
+    import torch
+    n_tok, hq, hkv, D, ks, vs, qs = _append_args(k_new, v_new, q, q_out, block_table, seq_idx,
+                                                 pos, cos_sin)
+    pages, _, D4 = _kv4_dims(kv_cache, hkv)
+    if D4 != D or kv_cache.device != k_new.device:
+        raise ValueError(f"kv_cache holds head_dim {D4} on {kv_cache.device}, k_new has {D} on "
+                         f"{k_new.device}")
+    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    with _Launch(k_new.device, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty((n_tok, hq, D), dtype=q.dtype, device=q.device)
+        pa_append_kv4(k_new, v_new, q, kv_cache, q_out, block_table, seq_idx, pos, cos_sin, n_tok,
+                      ks, vs, qs, hq, hkv, D, 16, block_table.shape[0], block_table.shape[1],
+                      pages, max_pos, rot, interleaved, dtype_code(k_new))
+    return q_out
+
+
+def read_kv4(kv_cache, block_table, seq_idx, pos, dtype=None, k_out=None, v_out=None,
+             stream=None):
+    """pa_read_kv4 on tensors: the K and V rows of tokens (seq_idx[j], pos[j]) as
+    values, each [n_tok, h_kv, D] of dtype (torch.bfloat16 or torch.float16, the
+    type the cache was written with; k_out's if given)."""
+    import torch
+    pages, hkv, D = _kv4_dims(kv_cache)
+    dev, n_tok = kv_cache.device, seq_idx.shape[0]
+    _want(block_table, "block_table", torch.int32, (None, None), dev)
+    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), dev)
+    _want(pos, "pos", torch.int32, (n_tok,), dev)
+    if dtype is None:
+        if k_out is None and v_out is None:
+            raise ValueError("read_kv4 wants dtype, k_out or v_out")
+        dtype = (k_out if k_out is not None else v_out).dtype
+    with _Launch(dev, stream):
+        if k_out is None:
+            k_out = torch.empty((n_tok, hkv, D), dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty((n_tok, hkv, D), dtype=dtype, device=dev)
+        _want(k_out, "k_out", dtype, (n_tok, hkv, D), dev)
+        _want(v_out, "v_out", dtype, (n_tok, hkv, D), dev)
+        pa_read_kv4(kv_cache, block_table, seq_idx, pos, k_out, v_out, n_tok, hkv, D, 16,
+                    block_table.shape[0], block_table.shape[1], pages, dtype_code(k_out))
+    return k_out, v_out
+
+
+def copy_pages_kv4(kv_cache, src, dst, stream=None):
+    """pa_copy_pages_kv4 on tensors: page src[i] to page dst[i] (int32, on the device)."""
+    import torch
+    pages, hkv, D = _kv4_dims(kv_cache)
+    _want(src, "src", torch.int32, (None,), kv_cache.device)
+    _want(dst, "dst", torch.int32, tuple(src.shape), kv_cache.device)
+    with _Launch(kv_cache.device, stream):
+        pa_copy_pages_kv4(kv_cache, src, dst, src.shape[0], hkv, D, 16, pages)
+
+
+def _workspace(workspace, need, device):
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: want a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def decode_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=None, stream=None):
+    """pa_decode_kv4 on tensors: q [B, h_q, D]; kv_cache uint8 [pages, h_kv, block]
+    (kv4_cache), written by append_kv4 with q's dtype; block_table int32
+    [B, max_blocks]; ctx_lens int32 [B].  Returns fp32 [B, h_q, D].  workspace:
+    any tensor of pa_decode_kv4_workspace_size(D) bytes, not shared with a call
+    that may run at the same time."""
+    import torch
+    B, hq, D = q.shape
+    dev = q.device
+    pages, hkv, D4 = _kv4_dims(kv_cache)
+    _want(q, "q", q.dtype, (B, hq, D4), dev)
+    _want(kv_cache, "kv_cache", torch.uint8, (pages, hkv, None), dev)
+    _want(block_table, "block_table", torch.int32, (B, None), dev)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    with _Launch(dev, stream):
+        if out is None:
+            out = torch.empty((B, hq, D), dtype=torch.float32, device=dev)
+        _want(out, "out", torch.float32, (B, hq, D), dev)
+        workspace, size = _workspace(workspace, pa_decode_kv4_workspace_size(D), dev)
+        pa_decode_kv4(q, kv_cache, block_table, ctx_lens, out, scale, hq, hkv, D, 16, B,
+                      block_table.shape[1], pages, dtype_code(q), workspace, size)
+    return out
+
+
+def prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=None,
+                stream=None):
+    """pa_prefill_kv4 on tensors: q [B, n_new, h_q, D], the chunk's queries, whose
+    K/V rows append_kv4 has stored at positions ctx_lens[b] ..; ctx_lens = tokens
+    cached before the chunk.  Returns [B, n_new, h_q, D] in q's dtype."""
+    import torch
+    B, n_new, hq, D = q.shape
+    dev = q.device
+    pages, hkv, D4 = _kv4_dims(kv_cache)
+    _want(q, "q", q.dtype, (B, n_new, hq, D4), dev)
+    _want(kv_cache, "kv_cache", torch.uint8, (pages, hkv, None), dev)
+    _want(block_table, "block_table", torch.int32, (B, None), dev)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    mb = block_table.shape[1]
+    with _Launch(dev, stream):
+        if out is None:
+            out = torch.empty((B, n_new, hq, D), dtype=q.dtype, device=dev)
+        _want(out, "out", q.dtype, (B, n_new, hq, D), dev)
+        workspace, size = _workspace(
+            workspace, pa_prefill_kv4_workspace_size(B, n_new, hq, hkv, D, 16, mb), dev)
+        pa_prefill_kv4(q, kv_cache, block_table, ctx_lens, n_new, out, scale, hq, hkv, D, 16, B,
+                       mb, pages, dtype_code(q), workspace, size)
+    return out

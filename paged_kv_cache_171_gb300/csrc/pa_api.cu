@@ -144,8 +144,6 @@ int launch_append(const void *k_new, const void *v_new, void *k_cache,
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-namespace {
-
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int check_common(int n_q_heads, int n_kv_heads, int head_dim, int page_size,
@@ -175,6 +173,8 @@ int sm_count() {
     return 0;
   return n;
 }
+
+namespace {
 
 // Partition plan of pa_decode: pages per partition (0 = single pass) and the
 // partition count.  Automatic mode, with R = resident CTAs (2 per SM) and
@@ -347,6 +347,9 @@ const char *pa_strerror(int status) {
       return "PA_ERR_SCRATCH_LIMIT: needs more split-K scratch than the 16 MiB static array";
     case PA_ERR_POOL_EMPTY: return "PA_ERR_POOL_EMPTY: not enough free pages in the pool";
     case PA_ERR_POOL_STATE: return "PA_ERR_POOL_STATE: a page that is not in use";
+    case PA_ERR_ROPE:
+      return "PA_ERR_ROPE: rot_dim must be a multiple of 16 up to head_dim, with a table of at "
+             "least one position";
     default: return "unknown pa status";
   }
 }

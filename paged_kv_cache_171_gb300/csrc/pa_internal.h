@@ -182,6 +182,14 @@ int launch_merge_rows(const float *partials, const int32_t *ctx_lens, float *out
 
 int launch_prefill(const PrefillLaunch &a, cudaStream_t stream);
 
+// Host checks shared by the entry points: PA_OK or the first PA_ERR_* found.
+bool aligned16(const void *p);
+int check_common(int n_q_heads, int n_kv_heads, int head_dim, int page_size, int batch,
+                 int max_blocks, int num_pages, int dtype);
+int current_status_ptr(int **status);
+// SMs of the current device, 0 if there is none.
+int sm_count();
+
 // Device address of the current context's status word (looked up once per
 // context), or nullptr if the lookup fails.
 int *device_status();

@@ -1,0 +1,172 @@
+// pa_kv4_api.cu -- the C ABI of the rotated appends and of the 4-bit cache:
+// argument validation and dispatch.
+#include "pa_kv4.cuh"
+
+using namespace pa;
+
+namespace {
+
+int check_append(const AppendRopeLaunch &a, int page_size, int dtype) {
+  const int rc = check_common(a.q ? a.n_q_heads : a.n_kv_heads, a.n_kv_heads, a.head_dim,
+                              page_size, a.batch, a.max_blocks, a.num_pages, dtype);
+  if (rc) return rc;
+  if (a.n_tok < 0) return PA_ERR_SHAPE;
+  if (a.cos_sin && (a.rot_dim < 16 || a.rot_dim > a.head_dim || a.rot_dim % 16 || a.max_pos <= 0))
+    return PA_ERR_ROPE;
+  const int64_t kv = static_cast<int64_t>(a.n_kv_heads) * a.head_dim;
+  if (a.k_stride < kv || a.v_stride < kv ||
+      (a.q && a.q_stride < static_cast<int64_t>(a.n_q_heads) * a.head_dim))
+    return PA_ERR_SHAPE;
+  if (a.k_stride % 8 || a.v_stride % 8 || (a.q && a.q_stride % 8)) return PA_ERR_ALIGN;
+  if (!aligned16(a.k_new) || !aligned16(a.v_new) || !aligned16(a.q) || !aligned16(a.q_out) ||
+      !aligned16(a.k_cache) || !aligned16(a.v_cache) || !aligned16(a.kv4_cache) ||
+      !aligned16(a.cos_sin))
+    return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+int append(AppendRopeLaunch &a, int page_size, int dtype, pa_stream_t stream) {
+  int rc = check_append(a, page_size, dtype);
+  if (rc || a.n_tok == 0) return rc;
+  if ((rc = current_status_ptr(&a.status))) return rc;
+  a.bf16 = dtype == PA_BF16;
+  return launch_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int sms_or_default() { return sm_count() > 0 ? sm_count() : 152; }
+
+int attention(Kv4AttentionLaunch &a, int page_size, int dtype, size_t workspace_bytes,
+              pa_stream_t stream) {
+  if (!a.q || !a.cache || !a.block_table || !a.ctx_lens || !a.out) return PA_ERR_NULL;
+  int rc = check_common(a.n_q_heads, a.n_kv_heads, a.head_dim, page_size, a.batch, a.max_blocks,
+                        a.num_pages, dtype);
+  if (rc) return rc;
+  if (!aligned16(a.q) || !aligned16(a.cache) || !aligned16(a.out)) return PA_ERR_ALIGN;
+  if (!a.workspace || workspace_bytes < kv4_rows_workspace_bytes(a.head_dim, sms_or_default()))
+    return PA_ERR_WORKSPACE;
+  if (!aligned16(a.workspace)) return PA_ERR_ALIGN;
+  if ((rc = current_status_ptr(&a.status))) return rc;
+  a.bf16 = dtype == PA_BF16;
+  return launch_kv4_rows(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_append_kv_rope(const void *k_new, const void *v_new, const void *q, void *k_cache,
+                      void *v_cache, void *q_out, const int32_t *block_table,
+                      const int32_t *seq_idx, const int32_t *pos, const float *cos_sin,
+                      int n_tok, int64_t k_stride, int64_t v_stride, int64_t q_stride,
+                      int n_q_heads, int n_kv_heads, int head_dim, int page_size, int batch,
+                      int max_blocks_per_seq, int num_pages, int max_pos, int rot_dim,
+                      int interleaved, pa_dtype dtype, pa_stream_t stream) {
+  if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !seq_idx || !pos || !cos_sin ||
+      !q != !q_out)
+    return PA_ERR_NULL;
+  AppendRopeLaunch a = {k_new, v_new, q, q_out, k_cache, v_cache, nullptr, block_table, seq_idx,
+                        pos, cos_sin, nullptr, k_stride, v_stride, q_stride, n_tok, n_q_heads,
+                        n_kv_heads, head_dim, batch, max_blocks_per_seq, num_pages, max_pos,
+                        rot_dim, interleaved != 0, false};
+  return append(a, page_size, dtype, stream);
+}
+
+size_t pa_kv4_block_bytes(int head_dim) {
+  return head_dim == 64 || head_dim == 128 ? kv4::block_bytes(head_dim) : 0;
+}
+
+int pa_append_kv4(const void *k_new, const void *v_new, const void *q, void *kv_cache,
+                  void *q_out, const int32_t *block_table, const int32_t *seq_idx,
+                  const int32_t *pos, const float *cos_sin, int n_tok, int64_t k_stride,
+                  int64_t v_stride, int64_t q_stride, int n_q_heads, int n_kv_heads,
+                  int head_dim, int page_size, int batch, int max_blocks_per_seq,
+                  int num_pages, int max_pos, int rot_dim, int interleaved, pa_dtype dtype,
+                  pa_stream_t stream) {
+  if (!k_new || !v_new || !kv_cache || !block_table || !seq_idx || !pos || !q != !q_out)
+    return PA_ERR_NULL;
+  AppendRopeLaunch a = {k_new, v_new, q, q_out, nullptr, nullptr,
+                        static_cast<uint8_t *>(kv_cache), block_table, seq_idx, pos, cos_sin,
+                        nullptr, k_stride, v_stride, q_stride, n_tok, n_q_heads, n_kv_heads,
+                        head_dim, batch, max_blocks_per_seq, num_pages, max_pos,
+                        cos_sin ? rot_dim : 0, interleaved != 0, false};
+  return append(a, page_size, dtype, stream);
+}
+
+int pa_read_kv4(const void *kv_cache, const int32_t *block_table, const int32_t *seq_idx,
+                const int32_t *pos, void *k_out, void *v_out, int n_tok, int n_kv_heads,
+                int head_dim, int page_size, int batch, int max_blocks_per_seq, int num_pages,
+                pa_dtype dtype, pa_stream_t stream) {
+  if (!kv_cache || !block_table || !seq_idx || !pos || !k_out || !v_out) return PA_ERR_NULL;
+  int rc = check_common(n_kv_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+                        num_pages, dtype);
+  if (rc) return rc;
+  if (n_tok < 0) return PA_ERR_SHAPE;
+  if (!aligned16(kv_cache) || !aligned16(k_out) || !aligned16(v_out)) return PA_ERR_ALIGN;
+  if (n_tok == 0) return PA_OK;
+  ReadKv4Launch a = {static_cast<const uint8_t *>(kv_cache), block_table, seq_idx, pos, k_out,
+                     v_out, nullptr, n_tok, n_kv_heads, head_dim, batch, max_blocks_per_seq,
+                     num_pages, dtype == PA_BF16};
+  if ((rc = current_status_ptr(&a.status))) return rc;
+  return launch_read_kv4(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pa_copy_pages_kv4(void *kv_cache, const int32_t *src, const int32_t *dst, int n,
+                      int n_kv_heads, int head_dim, int page_size, int num_pages,
+                      pa_stream_t stream) {
+  if (!kv_cache || !src || !dst) return PA_ERR_NULL;
+  int rc = check_common(n_kv_heads, n_kv_heads, head_dim, page_size, 1, 1, num_pages, PA_BF16);
+  if (rc) return rc;
+  if (n < 0) return PA_ERR_SHAPE;
+  if (!aligned16(kv_cache)) return PA_ERR_ALIGN;
+  if (n == 0) return PA_OK;
+  int *status = nullptr;
+  if ((rc = current_status_ptr(&status))) return rc;
+  return launch_copy_pages_kv4(static_cast<uint8_t *>(kv_cache), src, dst, status, n, n_kv_heads,
+                               head_dim, num_pages, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pa_decode_kv4_workspace_size(int head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return kv4_rows_workspace_bytes(head_dim, sms_or_default());
+}
+
+int pa_decode_kv4(const void *q, const void *kv_cache, const int32_t *block_table,
+                  const int32_t *ctx_lens, float *out, float scale, int n_q_heads,
+                  int n_kv_heads, int head_dim, int page_size, int batch,
+                  int max_blocks_per_seq, int num_pages, pa_dtype dtype, void *workspace,
+                  size_t workspace_bytes, pa_stream_t stream) {
+  Kv4AttentionLaunch a = {q, static_cast<const uint8_t *>(kv_cache), block_table, ctx_lens, out,
+                          workspace, nullptr, scale, 0, n_q_heads, n_kv_heads, head_dim, batch,
+                          max_blocks_per_seq, num_pages, false};
+  return attention(a, page_size, dtype, workspace_bytes, stream);
+}
+
+size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_kv_heads,
+                                     int head_dim, int page_size, int max_blocks_per_seq) {
+  if (check_common(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, 1,
+                   PA_BF16) ||
+      n_new <= 0 || n_new > static_cast<int64_t>(max_blocks_per_seq) * page_size)
+    return 0;
+  return kv4_rows_workspace_bytes(head_dim, sms_or_default());
+}
+
+int pa_prefill_kv4(const void *q, const void *kv_cache, const int32_t *block_table,
+                   const int32_t *ctx_lens, int n_new, void *out, float scale, int n_q_heads,
+                   int n_kv_heads, int head_dim, int page_size, int batch,
+                   int max_blocks_per_seq, int num_pages, pa_dtype dtype, void *workspace,
+                   size_t workspace_bytes, pa_stream_t stream) {
+  if (!q || !kv_cache || !block_table || !ctx_lens || !out) return PA_ERR_NULL;
+  if (n_new < 0) return PA_ERR_SHAPE;
+  if (max_blocks_per_seq > 0 && page_size == kPageSize &&
+      n_new > static_cast<int64_t>(max_blocks_per_seq) * page_size)
+    return PA_ERR_SHAPE;
+  Kv4AttentionLaunch a = {q, static_cast<const uint8_t *>(kv_cache), block_table, ctx_lens, out,
+                          workspace, nullptr, scale, n_new, n_q_heads, n_kv_heads, head_dim,
+                          batch, max_blocks_per_seq, num_pages, false};
+  if (n_new == 0)  // nothing to compute; the other arguments are still checked
+    return check_common(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+                        num_pages, dtype);
+  return attention(a, page_size, dtype, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,676 @@
+// pa_kv4_rows.cu -- attention over the 4-bit paged cache for few query rows a
+// kv head: decode (one query a sequence) and short chunks (speculative verify).
+//
+// A row is a (query, head) pair of one kv head; o = softmax(q K^T scale) V with
+// K = zero_k + scale_k (c - 8) and V alike, c the 4-bit codes.  The codes go
+// into the tensor cores as they are (exact in 16 bits) and the scales and
+// zeros are applied outside,
+//   s_t = scale_k[t] (q . c_t - 8 sum q) + zero_k[t] sum q
+//   O   = sum_t (p_t scale_v[t]) (c_t - 8),   z = sum_t p_t zero_v[t]
+// so a page costs no dequantisation beyond turning nibbles into 16-bit floats.
+//
+// Operand form.  mma.sync m16n8k16 with the tokens (then the head dimensions)
+// as the 16 rows and 8 query rows as the columns.  That uses every tensor-core
+// row for up to 8 query rows, keeps the output state in head_dim / 4 registers
+// a thread, and needs no transpose of K or V: a thread loads whole 32-bit words
+// of codes, and because the contraction index may be permuted freely (q, or the
+// order of tokens, is permuted alike) two nibbles four places apart in one
+// word, or the same nibble of two tokens' words, form an operand register.
+//   K: x & 0x000f000f as fp16 is the subnormal c 2^-24, x & 0x00f000f0 is
+//      c 2^-20: one AND gives two elements.  q is scaled by a power of two a
+//      row (its largest magnitude near 2^15, exact in fp16 down to 2^-39 of the
+//      row's largest) with the slots of the second kind divided by 16.
+//   V: the accumulation over tokens is long, and tensor-core sums round toward
+//      zero, so the codes are centred first: (x & 0x000f000f) | 0x64006400 is
+//      1024 + c, minus 1032; (x & 0x00f000f0) | 0x64006400 is 1024 + 16 c,
+//      times 1/16 minus 72; both exact.  Uncentred, the sum of 8 p would drown
+//      a diffuse row's result in rounding.
+// The weights p scale_v enter as two fp16 terms (head and remainder, 22 bits).
+// They are taken relative to a power of two above the largest |scale_v| so far
+// and multiplied by 2^7, so that they stay below 2^15 and the second term
+// reaches 2^-32 of the largest.  With at most 4 rows (WIDE false) columns 4-7
+// repeat columns 0-3 and carry the second terms: one MMA does both.  The
+// weights, in the accumulator's layout (token, row), become the second
+// product's operand (row, token) by movmatrix.
+//
+// Work split.  The pages of all (sequence, kv head, row tile) items, laid end to
+// end, are cut into equal runs, one a CTA, as many CTAs as fit the GPU at once:
+// a ragged batch takes the time of its pages, not of its longest sequence.  A
+// CTA's 4 warps take its run's pages in turn, each with its own ring of stages
+// filled by bulk copies, and merge their (m, l, O) states when an item ends.  An
+// item cut between CTAs leaves one state a CTA, and the last of them to arrive
+// merges them in order of position, so results do not depend on timing.
+#include "pa_device.cuh"
+#include "pa_kv4.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleSlack = 8.0f;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kWarps = 4, kStages = 4, kTile = 8;  // query rows a tile
+constexpr int kCtasPerSm = 4;
+constexpr int kMinPages = 8;     // least pages a CTA takes
+
+struct RowsParams {
+  const uint16_t *q;
+  const uint8_t *cache;
+  const int32_t *block_table, *ctx_lens;
+  void *out;
+  float *ws;     // [CTA][2][kTile][D + 4] partial states
+  int *ctr;      // [CTA] arrivals of the item that starts in the CTA's run and leaves it
+  int *status;
+  float qscale;  // scale * log2 e
+  int n_new, queries, n_q_heads, n_kv_heads, group, batch, max_blocks, num_pages;
+  int n_rows, n_sub, tile_rows;  // rows a kv head, row tiles, rows a tile
+};
+
+template <int D>
+struct RowsSmem {
+  static constexpr int kBlock = kv4::block_bytes(D);
+  static constexpr int kRing = kWarps * kStages * kBlock;
+  static constexpr int kRowStride = D + 4;  // floats a merged row
+  static constexpr int kMergeO = kRing;
+  static constexpr int kMergeM = kMergeO + kWarps * kTile * kRowStride * 4;
+  static constexpr int kMergeL = kMergeM + kWarps * kTile * 4;
+  static constexpr int kBars = kMergeL + kWarps * kTile * 4;
+  static constexpr int kLast = kBars + kWarps * kStages * 8;
+  static constexpr int kBytes = kLast + 16;
+  static_assert(kBlock % 16 == 0 && kBars % 8 == 0, "alignment");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t sub_1032(uint32_t x) {
+  const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&x), __float2half2_rn(1032.f));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t sixteenth_sub_72(uint32_t x) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&x), __float2half2_rn(0.0625f),
+                            __float2half2_rn(-72.f));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Physical token of score row r < 8 (row r + 8: 8 more).  The order makes the
+// rows that neighbouring lanes read from a stage alternate between its even and
+// odd rows, which is what shared memory's 32 banks want of 64-byte rows.
+__device__ __forceinline__ int token_of(int r) {
+  const int c = r >> 1, a = c >> 1, b = c & 1;
+  return (r & 1) ? 4 * a + 3 - b : 4 * a + b;
+}
+
+// One warp's ring of page blocks.  Block i of an item's run is page first +
+// kWarps i of the sequence; `issued` and `waited` number the blocks over the
+// CTA's whole run, which gives the stage and the parity.
+template <int D>
+struct BlockRing {
+  uint32_t stage0, bar0;
+  const uint8_t *cache;
+  const int32_t *bt_row;
+  int *status;
+  int64_t head_stride, head_offset;  // bytes a page, bytes of the kv head in it
+  int first, n, num_pages, ids_cur, ids_nxt;
+  uint32_t issued, waited;  // blocks over the whole run
+
+  __device__ int fetch_id(int i) const {
+    return i < n ? __ldg(bt_row + first + kWarps * i) : 0;
+  }
+  __device__ void start(int lane) {
+    ids_cur = fetch_id(lane);
+    ids_nxt = fetch_id(32 + lane);
+  }
+  // Called by the whole warp with i = 0, 1, 2, ... of the item's blocks.
+  __device__ void issue(int i, int lane) {
+    if ((i & 31) == 0 && i > 0) {
+      ids_cur = ids_nxt;
+      ids_nxt = fetch_id(i + 32 + lane);
+    }
+    int id = __shfl_sync(kFull, ids_cur, i & 31);
+    if (lane == 0) {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(num_pages)) {
+        record_error(status, PA_ERR_BAD_BLOCK);
+        id = 0;  // read a page that exists; the result is flagged as invalid
+      }
+      const uint32_t s = issued % kStages;
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(bar0 + 8 * s, kv4::block_bytes(D));
+      bulk_load(stage0 + s * kv4::block_bytes(D), cache + id * head_stride + head_offset,
+                kv4::block_bytes(D), bar0 + 8 * s);
+    }
+    ++issued;
+  }
+  // Warp-uniform wait for the next block; its stage, or 0 when the wait ran out.
+  __device__ uint32_t wait(int lane) {
+    const uint32_t s = waited % kStages, par = (waited / kStages) & 1;
+    ++waited;
+    if (__all_sync(kFull, mbar_wait(bar0 + 8 * s, par))) return stage0 + s * kv4::block_bytes(D);
+    if (lane == 0) record_error(status, PA_ERR_TIMEOUT);
+    for (uint32_t k = waited; k < issued; ++k)  // copies in flight still land
+      mbar_wait(bar0 + 8 * (k % kStages), (k / kStages) & 1);
+    return 0;
+  }
+};
+
+// Which sequence a position of the flattened page list belongs to.
+struct Cursor {
+  int b;            // sequence
+  int64_t base;     // pages of one (kv head, row tile) of the sequences before b
+};
+
+template <int D, bool BF16, bool WIDE, bool OUT16>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+    kv4_rows_kernel(const RowsParams p) {
+  using L = RowsSmem<D>;
+  constexpr int MT = D / 16;   // row tiles of the second product (head dimensions)
+  constexpr int KW = D / 32;   // 32-bit words of K codes a thread holds per token
+  constexpr int VW = D / 64;   // of V codes
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ln = lane >> 2, lc = lane & 3;
+
+  if (tid == 0) {
+    for (int s = 0; s < kWarps * kStages; ++s) mbar_init(sb + L::kBars + 8 * s, 1);
+    fence_mbar_init();
+  }
+  griddep_release();
+  griddep_wait();  // inputs may come from the previous kernel in the stream
+  __syncthreads();
+
+  // ---- this CTA's run [w0, w1) of the flattened page list: lane l sums the
+  // pages of sequences [l per, (l + 1) per), a warp scan finds the run's start
+  const int maxT = p.max_blocks * kPageSize;
+  const int extra = p.n_new;  // tokens of the chunk, behind ctx_lens
+  auto tokens_of = [&](int b, bool report) {
+    int t = __ldg(p.ctx_lens + b);
+    if (t < 0 || t > maxT - extra) {
+      if (report) record_error(p.status, PA_ERR_BAD_CTX);
+      t = t < 0 ? 0 : maxT - extra;
+    }
+    return t + extra;
+  };
+  auto pages_of = [](int tokens) { return max(1, (tokens + kPageSize - 1) / kPageSize); };
+  const int heads = p.n_kv_heads * p.n_sub;  // items a sequence
+  const int per = (p.batch + 31) / 32;
+  const int lb0 = min(p.batch, lane * per), lb1 = min(p.batch, lb0 + per);
+  int64_t sum = 0;
+#pragma unroll 4
+  for (int b = lb0; b < lb1; ++b) sum += pages_of(tokens_of(b, blockIdx.x == 0 && warp == 0));
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int64_t total = __shfl_sync(kFull, incl, 31) * heads;
+  int64_t run = (total + gridDim.x - 1) / gridDim.x;
+  if (run < kMinPages) run = kMinPages;
+  const int64_t w0 = blockIdx.x * run, w1 = min(total, w0 + run);
+  if (w0 >= w1) return;
+  const int src = __ffs(__ballot_sync(kFull, incl * heads > w0)) - 1;
+  Cursor cur;
+  cur.b = __shfl_sync(kFull, lb0, src);
+  cur.base = __shfl_sync(kFull, incl - sum, src);
+  int n_b = pages_of(tokens_of(cur.b, false));
+
+  BlockRing<D> ring;
+  ring.stage0 = sb + warp * kStages * L::kBlock;
+  ring.bar0 = sb + L::kBars + warp * kStages * 8;
+  ring.cache = p.cache;
+  ring.status = p.status;
+  ring.head_stride = static_cast<int64_t>(p.n_kv_heads) * L::kBlock;
+  ring.num_pages = p.num_pages;
+  ring.issued = ring.waited = 0;
+  bool alive = true;  // false once a wait of this warp has run out
+
+  float *mer_o = reinterpret_cast<float *>(smem + L::kMergeO);
+  float *mer_m = reinterpret_cast<float *>(smem + L::kMergeM);
+  float *mer_l = reinterpret_cast<float *>(smem + L::kMergeL);
+  volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::kLast);
+  const int tk = token_of(ln);
+
+  for (int64_t w = w0; w < w1;) {
+    // ---- the item that w lies in, and the run's pages of it
+    while ((cur.base + n_b) * heads <= w) {
+      cur.base += n_b;
+      n_b = pages_of(tokens_of(++cur.b, false));
+    }
+    const int64_t rel = w - cur.base * heads;
+    const int item = static_cast<int>(rel / n_b);
+    const int pg0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
+    const int n_pg = static_cast<int>(min(static_cast<int64_t>(n_b - pg0), w1 - w));
+    const int g = item / p.n_sub, r0 = (item % p.n_sub) * p.tile_rows;
+    const int n_r = min(p.tile_rows, p.n_rows - r0);
+    const int T = tokens_of(cur.b, false);
+    // last key (exclusive) each of this lane's two rows sees
+    auto row_of = [&](int col) { return r0 + min(WIDE ? col : (col & 3), n_r - 1); };
+    auto limit_of = [&](int r) { return OUT16 ? T - extra + 1 + r / p.group : T; };
+    const int lim0 = limit_of(row_of(2 * lc)), lim1 = limit_of(row_of(2 * lc + 1));
+    const int lim_all = limit_of(r0);  // every row sees at least this many keys
+
+    ring.bt_row = p.block_table + static_cast<size_t>(cur.b) * p.max_blocks;
+    ring.head_offset = static_cast<int64_t>(g) * L::kBlock;
+    ring.first = pg0 + warp;
+    ring.n = T > 0 && alive && warp < n_pg ? (n_pg - warp + kWarps - 1) / kWarps : 0;
+    ring.start(lane);
+    for (int i = 0; i < kStages && i < ring.n; ++i) ring.issue(i, lane);
+
+    // ---- q of this lane's column as the first product's operand
+    const size_t q_row0 = static_cast<size_t>(cur.b) * p.queries * p.n_q_heads + g * p.group;
+    auto q_row = [&](int r) {  // row r of the kv head: query r / G, head r % G
+      return q_row0 + static_cast<size_t>(r / p.group) * p.n_q_heads + r % p.group;
+    };
+    uint32_t qb[2 * KW][2];
+    float f0, f1, e0, e1;  // per column 2 lc, 2 lc + 1: score factor, scaled sum of q
+    {
+      const int col = WIDE ? ln : (ln & 3);
+      float x[8 * KW];
+      if (col < n_r) {
+        const uint4 *src4 =
+            reinterpret_cast<const uint4 *>(p.q + q_row(r0 + col) * D + (D / 4) * lc);
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+          const uint4 v = __ldg(src4 + k);
+          const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 f = unpack2<BF16>(vw[u]);
+            x[8 * k + 2 * u] = f.x;
+            x[8 * k + 2 * u + 1] = f.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8 * KW; ++k) x[k] = 0.f;
+      }
+      float top = 0.f, total_q = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8 * KW; ++k) {
+        top = fmaxf(top, fabsf(x[k]));
+        total_q += x[k];
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        total_q += __shfl_xor_sync(kFull, total_q, o);
+      }
+      // 2^ex brings the row's largest magnitude into [2^14, 2^15)
+      const int ex = min(90, max(-90, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+      const float up16 = up * 0.0625f;
+#pragma unroll
+      for (int k = 0; k < KW; ++k)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int d0 = 8 * k + 2 * s;
+          qb[2 * k + s][0] = pack2<false>(x[d0] * up, x[d0 + 4] * up);
+          qb[2 * k + s][1] = pack2<false>(x[d0 + 1] * up16, x[d0 + 5] * up16);
+        }
+      const float f = p.qscale * __uint_as_float(static_cast<uint32_t>(127 + 24 - ex) << 23);
+      const float e = p.qscale * total_q;
+      f0 = __shfl_sync(kFull, f, 8 * lc);
+      f1 = __shfl_sync(kFull, f, 8 * lc + 4);
+      e0 = __shfl_sync(kFull, e, 8 * lc);
+      e1 = __shfl_sync(kFull, e, 8 * lc + 4);
+    }
+
+    float o[MT][4];
+#pragma unroll
+    for (int k = 0; k < MT; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, z0 = 0.f, z1 = 0.f;
+    float v_ref = 0.f, v_inv = 0.f;  // reference of scale_v (a power of two), 2^7 / it
+
+    for (int i = 0; i < ring.n; ++i) {
+      const uint32_t st = ring.wait(lane);
+      if (st == 0) {
+        alive = false;
+        break;
+      }
+      const int key0 = (pg0 + warp + kWarps * i) * kPageSize;
+
+      // ---- scores: S[token][row]
+      const uint32_t kmeta0 = lds32(st + kv4::meta_offset(D, 0, tk));
+      const uint32_t kmeta1 = lds32(st + kv4::meta_offset(D, 0, tk + 8));
+      uint32_t ka[KW], kb[KW];
+      if constexpr (KW == 4) {
+        const uint4 a = lds128(st + kv4::code_offset(D, 0, tk) + 16 * lc);
+        const uint4 b = lds128(st + kv4::code_offset(D, 0, tk + 8) + 16 * lc);
+        ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
+        kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+      } else {
+        const uint2 a = lds64(st + kv4::code_offset(D, 0, tk) + 8 * lc);
+        const uint2 b = lds64(st + kv4::code_offset(D, 0, tk + 8) + 8 * lc);
+        ka[0] = a.x, ka[1] = a.y;
+        kb[0] = b.x, kb[1] = b.y;
+      }
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KW; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t xa = ka[k] >> (8 * h), xb = kb[k] >> (8 * h);
+          const uint32_t a[4] = {xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u,
+                                 xb & 0x00f000f0u};
+          mma16816<false>(s, a, qb[2 * k + h][0], qb[2 * k + h][1]);
+        }
+      // V's scales and zeros of the same two tokens, and V's codes
+      uint32_t vm0 = lds32(st + kv4::meta_offset(D, 1, tk));
+      uint32_t vm1 = lds32(st + kv4::meta_offset(D, 1, tk + 8));
+      uint32_t va[4][VW];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = token_of(2 * lc + (u & 1)) + 8 * (u >> 1);
+        if constexpr (VW == 2) {
+          const uint2 x = lds64(st + kv4::code_offset(D, 1, t) + 8 * ln);
+          va[u][0] = x.x, va[u][1] = x.y;
+        } else {
+          va[u][0] = lds32(st + kv4::code_offset(D, 1, t) + 4 * ln);
+        }
+      }
+      __syncwarp();  // the stage has been read by every lane
+      if (i + kStages < ring.n) ring.issue(i + kStages, lane);
+
+      {
+        const float2 k0 = unpack2<BF16>(kmeta0), k1 = unpack2<BF16>(kmeta1);
+        s[0] = fmaf(k0.x, fmaf(f0, s[0], -8.f * e0), k0.y * e0);
+        s[1] = fmaf(k0.x, fmaf(f1, s[1], -8.f * e1), k0.y * e1);
+        s[2] = fmaf(k1.x, fmaf(f0, s[2], -8.f * e0), k1.y * e0);
+        s[3] = fmaf(k1.x, fmaf(f1, s[3], -8.f * e1), k1.y * e1);
+      }
+      if (key0 + kPageSize > lim_all) {
+        const int t0 = key0 + tk, t1 = t0 + 8;
+        s[0] = t0 < lim0 ? s[0] : -INFINITY;
+        s[1] = t0 < lim1 ? s[1] : -INFINITY;
+        s[2] = t1 < lim0 ? s[2] : -INFINITY;
+        s[3] = t1 < lim1 ? s[3] : -INFINITY;
+        // rows past the end may hold anything: 0 * NaN must not enter
+        if (t0 >= T) vm0 = 0;
+        if (t1 >= T) vm1 = 0;
+      }
+      const float2 v0 = unpack2<BF16>(vm0), v1 = unpack2<BF16>(vm1);
+
+      // ---- move the references when a score or a scale outgrows them
+      const bool need = s[0] > m0 + kRescaleSlack || s[2] > m0 + kRescaleSlack ||
+                        s[1] > m1 + kRescaleSlack || s[3] > m1 + kRescaleSlack ||
+                        fabsf(v0.x) > v_ref || fabsf(v1.x) > v_ref;
+      if (__any_sync(kFull, need)) {
+        float a = fmaxf(s[0], s[2]), b = fmaxf(s[1], s[3]);
+        float v = fmaxf(fabsf(v0.x), fabsf(v1.x));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          a = fmaxf(a, __shfl_xor_sync(kFull, a, x));
+          b = fmaxf(b, __shfl_xor_sync(kFull, b, x));
+          v = fmaxf(v, __shfl_xor_sync(kFull, v, x));
+        }
+        const float n0 = fmaxf(m0, a), n1 = fmaxf(m1, b);
+        const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+        const float c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+        m0 = n0, m1 = n1;
+        l0 *= c0, z0 *= c0, l1 *= c1, z1 *= c1;
+        float cv = 1.f;
+        if (v > v_ref) {
+          // a power of two above v, and at least 2^-100
+          const float up = fmaxf(
+              __uint_as_float((__float_as_uint(v) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
+          cv = v_ref / up;
+          v_ref = up;
+          v_inv = 128.f / up;
+        }
+#pragma unroll
+        for (int k = 0; k < MT; ++k) {
+          o[k][0] *= c0 * cv;
+          o[k][1] *= c1 * cv;
+          o[k][2] *= c0 * cv;
+          o[k][3] *= c1 * cv;
+        }
+      }
+      // A row with no key so far keeps m = -inf: its weights are 0, not e^(-inf + inf).
+      const float a0 = m0 == -INFINITY ? 0.f : m0, a1 = m1 == -INFINITY ? 0.f : m1;
+      const float p0 = ex2(s[0] - a0), p1 = ex2(s[1] - a1);
+      const float p2 = ex2(s[2] - a0), p3 = ex2(s[3] - a1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      z0 = fmaf(p0, v0.y, fmaf(p2, v1.y, z0));
+      z1 = fmaf(p1, v0.y, fmaf(p3, v1.y, z1));
+      const float x0 = v0.x * v_inv, x1 = v1.x * v_inv;
+      const float w0a = p0 * x0, w1a = p1 * x0, w2a = p2 * x1, w3a = p3 * x1;
+      const uint32_t ha = pack2<false>(w0a, w1a), hb = pack2<false>(w2a, w3a);
+      const float2 ra = unpack2<false>(ha), rb = unpack2<false>(hb);
+      const uint32_t la = pack2<false>(w0a - ra.x, w1a - ra.y);
+      const uint32_t lb = pack2<false>(w2a - rb.x, w3a - rb.y);
+      uint32_t b0, b1, b2 = 0, b3 = 0;
+      if constexpr (WIDE) {
+        b0 = transpose8x8(ha), b1 = transpose8x8(hb);
+        b2 = transpose8x8(la), b3 = transpose8x8(lb);
+      } else {
+        b0 = transpose8x8(lc < 2 ? ha : la), b1 = transpose8x8(lc < 2 ? hb : lb);
+      }
+
+      // ---- O[dimension][row] += V^T P
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // nibbles 4 h .. 4 h + 3 of two tokens' words, one token a half
+          const uint32_t x = __byte_perm(va[0][j], va[1][j], h ? 0x7632 : 0x5410);
+          const uint32_t y = __byte_perm(va[2][j], va[3][j], h ? 0x7632 : 0x5410);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t xs = x >> (8 * u), ys = y >> (8 * u);
+            const uint32_t a[4] = {sub_1032((xs & 0x000f000fu) | 0x64006400u),
+                                   sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u),
+                                   sub_1032((ys & 0x000f000fu) | 0x64006400u),
+                                   sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u)};
+            mma16816<false>(o[4 * j + 2 * h + u], a, b0, b1);
+            if constexpr (WIDE) mma16816<false>(o[4 * j + 2 * h + u], a, b2, b3);
+          }
+        }
+    }
+
+    // ---- the warp's state to shared memory: O is O[d = (D / 8) ln + 2 k + {0, 1}]
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      l0 += __shfl_xor_sync(kFull, l0, x);
+      l1 += __shfl_xor_sync(kFull, l1, x);
+      z0 += __shfl_xor_sync(kFull, z0, x);
+      z1 += __shfl_xor_sync(kFull, z1, x);
+    }
+    const float back = v_ref * 0x1p-7f;
+#pragma unroll
+    for (int k = 0; k < MT; ++k) {
+      float2 a = make_float2(o[k][0], o[k][2]), b = make_float2(o[k][1], o[k][3]);
+      if constexpr (!WIDE) {  // columns 4-7 hold the remainder terms of 0-3
+        a.x += __shfl_xor_sync(kFull, a.x, 2);
+        a.y += __shfl_xor_sync(kFull, a.y, 2);
+        b.x += __shfl_xor_sync(kFull, b.x, 2);
+        b.y += __shfl_xor_sync(kFull, b.y, 2);
+      }
+      if (WIDE || lc < 2) {
+        float *dst = mer_o + (warp * kTile + 2 * lc) * L::kRowStride + (D / 8) * ln + 2 * k;
+        *reinterpret_cast<float2 *>(dst) =
+            make_float2(fmaf(a.x, back, z0), fmaf(a.y, back, z0));
+        *reinterpret_cast<float2 *>(dst + L::kRowStride) =
+            make_float2(fmaf(b.x, back, z1), fmaf(b.y, back, z1));
+      }
+    }
+    if (ln == 0 && (WIDE || lc < 2)) {
+      mer_m[warp * kTile + 2 * lc] = m0;
+      mer_m[warp * kTile + 2 * lc + 1] = m1;
+      mer_l[warp * kTile + 2 * lc] = l0;
+      mer_l[warp * kTile + 2 * lc + 1] = l1;
+    }
+    __syncthreads();
+
+    // ---- the item's CTAs: the first holds its start, the last its end
+    const int64_t i0 = cur.base * heads + static_cast<int64_t>(item) * n_b, i1 = i0 + n_b;
+    const int first = static_cast<int>(i0 / run), last = static_cast<int>((i1 - 1) / run);
+    auto store = [&](int r, int d, float4 v) {  // row r of the tile, dimensions d .. d + 3
+      const size_t at = q_row(r0 + r) * D + d;
+      if constexpr (OUT16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+            make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
+      else
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = v;
+    };
+    // CTA c's state of this item: slot 0 when its part starts the CTA's run.
+    auto state = [&](int c, int r) {
+      const int slot = c > first || i0 == first * run ? 0 : 1;
+      return p.ws + ((static_cast<size_t>(c) * 2 + slot) * kTile + r) * (D + 4);
+    };
+    for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
+      const int r = e / (D / 4), d = 4 * (e % (D / 4));
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) M = fmaxf(M, mer_m[k * kTile + r]);
+      float l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float lk = mer_l[k * kTile + r];
+        const float f = M == -INFINITY ? 1.f : ex2(mer_m[k * kTile + r] - M);
+        const float4 v =
+            *reinterpret_cast<const float4 *>(mer_o + (k * kTile + r) * L::kRowStride + d);
+        l = fmaf(f, lk, l);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (first == last) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros; NaN stays NaN
+        store(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      } else {
+        float *dst = state(blockIdx.x, r);
+        *reinterpret_cast<float4 *>(dst + d) = acc;
+        if (d == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(M, l);
+      }
+    }
+    if (first != last) {
+      // The last of the item's CTAs to arrive merges their states.  One thread
+      // arrives with an acquire-release add behind the barrier, so the CTA's
+      // states are visible before its arrival counts, and every other CTA's
+      // states to the last one.
+      __syncthreads();
+      if (tid == 0) *s_last = atomic_add_acq_rel_gpu(p.ctr + first, 1) == last - first;
+      __syncthreads();
+      if (*s_last) {
+        for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
+          const int r = e / (D / 4), d = 4 * (e % (D / 4));
+          float m = -INFINITY, l = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int kBatch = 8;
+          for (int c = first; c <= last; c += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+              if (c + u <= last) {
+                const float *sp = state(c + u, r);
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(sp + D));
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(sp + d));
+              }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+              if (c + u <= last && ml[u].y != 0.f) {
+                const float mn = fmaxf(m, ml[u].x);
+                const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
+                const float f = mn == -INFINITY ? 1.f : ex2(ml[u].x - mn);
+                acc.x = fmaf(acc.x, a, v[u].x * f);
+                acc.y = fmaf(acc.y, a, v[u].y * f);
+                acc.z = fmaf(acc.z, a, v[u].z * f);
+                acc.w = fmaf(acc.w, a, v[u].w * f);
+                l = fmaf(l, a, ml[u].y * f);
+                m = mn;
+              }
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          store(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        }
+      }
+    }
+    w += n_pg;
+    __syncthreads();  // the merge area is free for the next item
+  }
+}
+
+template <int D, bool BF16, bool WIDE, bool OUT16>
+int launch_rows_t(const RowsParams &p, int ctas, cudaStream_t stream) {
+  auto kern = kv4_rows_kernel<D, BF16, WIDE, OUT16>;
+  static ContextCache<bool> smem_set;
+  if (set_smem_limit(kern, RowsSmem<D>::kBytes, smem_set) != PA_OK) return PA_ERR_CUDA;
+  return launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), RowsSmem<D>::kBytes, stream, p) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+template <int D, bool BF16>
+int launch_rows_d(const RowsParams &p, int ctas, cudaStream_t stream) {
+  const bool wide = p.tile_rows > 4;
+  if (p.n_new > 0)
+    return wide ? launch_rows_t<D, BF16, true, true>(p, ctas, stream)
+                : launch_rows_t<D, BF16, false, true>(p, ctas, stream);
+  return wide ? launch_rows_t<D, BF16, true, false>(p, ctas, stream)
+              : launch_rows_t<D, BF16, false, false>(p, ctas, stream);
+}
+
+size_t partials_bytes(int head_dim, int ctas) {
+  return static_cast<size_t>(ctas) * 2 * kTile * (head_dim + 4) * sizeof(float);
+}
+
+}  // namespace
+
+size_t kv4_rows_workspace_bytes(int head_dim, int sms) {
+  const int ctas = sms * kCtasPerSm;
+  return partials_bytes(head_dim, ctas) + static_cast<size_t>(ctas) * sizeof(int);
+}
+
+int launch_kv4_rows(const Kv4AttentionLaunch &a, cudaStream_t stream) {
+  const int ctas = sm_count() * kCtasPerSm;
+  if (ctas <= 0) return PA_ERR_CUDA;
+  RowsParams p;
+  p.q = static_cast<const uint16_t *>(a.q);
+  p.cache = a.cache;
+  p.block_table = a.block_table;
+  p.ctx_lens = a.ctx_lens;
+  p.out = a.out;
+  p.ws = static_cast<float *>(a.workspace);
+  p.ctr = reinterpret_cast<int *>(static_cast<char *>(a.workspace) +
+                                  partials_bytes(a.head_dim, ctas));
+  p.status = a.status;
+  p.qscale = a.scale * kLog2e;
+  p.n_new = a.n_new;
+  p.queries = a.n_new > 0 ? a.n_new : 1;
+  p.n_q_heads = a.n_q_heads;
+  p.n_kv_heads = a.n_kv_heads;
+  p.group = a.n_q_heads / a.n_kv_heads;
+  p.batch = a.batch;
+  p.max_blocks = a.max_blocks;
+  p.num_pages = a.num_pages;
+  p.n_rows = p.queries * p.group;
+  p.n_sub = (p.n_rows + kTile - 1) / kTile;
+  p.tile_rows = (p.n_rows + p.n_sub - 1) / p.n_sub;
+  p.n_sub = (p.n_rows + p.tile_rows - 1) / p.tile_rows;
+  if (launch_clear_counters(p.ctr, ctas, stream) != PA_OK) return PA_ERR_CUDA;
+  if (a.head_dim == 128)
+    return a.bf16 ? launch_rows_d<128, true>(p, ctas, stream)
+                  : launch_rows_d<128, false>(p, ctas, stream);
+  return a.bf16 ? launch_rows_d<64, true>(p, ctas, stream)
+                : launch_rows_d<64, false>(p, ctas, stream);
+}
+
+}  // namespace pa
