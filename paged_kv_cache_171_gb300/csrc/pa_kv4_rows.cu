@@ -26,6 +26,11 @@
 //      times 1/16 minus 72; both exact.  Uncentred, the sum of 8 p would drown
 //      a diffuse row's result in rounding.
 // The weights p scale_v enter as two fp16 terms (head and remainder, 22 bits).
+// Products of a head term and a code have 15 bits, so their sums hardly ever
+// round; a remainder added to such a sum always would, toward zero, so the two
+// are accumulated apart (4 rows or fewer) or page by page in an accumulator of
+// their own that is added to the state with a rounding add (measured on the 32k
+// rows at 8 rows a tile: error 9e-6 of the result in one accumulator).
 // They are taken relative to a power of two above the largest |scale_v| so far
 // and multiplied by 2^7, so that they stay below 2^15 and the second term
 // reaches 2^-32 of the largest.  With at most 4 rows (WIDE false) columns 4-7
@@ -64,6 +69,7 @@ struct RowsParams {
   float qscale;  // scale * log2 e
   int n_new, queries, n_q_heads, n_kv_heads, group, batch, max_blocks, num_pages;
   int n_rows, n_sub, tile_rows;  // rows a kv head, row tiles, rows a tile
+  uint32_t page_bytes;           // all kv heads' blocks of a page
 };
 
 template <int D>
@@ -75,7 +81,9 @@ struct RowsSmem {
   static constexpr int kMergeM = kMergeO + kWarps * kTile * kRowStride * 4;
   static constexpr int kMergeL = kMergeM + kWarps * kTile * 4;
   static constexpr int kBars = kMergeL + kWarps * kTile * 4;
-  static constexpr int kLast = kBars + kWarps * kStages * 8;
+  static constexpr int kParts = kBars + kWarps * kStages * 8;  // Part[2]
+  static constexpr int kWalk = kParts + 2 * 64;                // Walk
+  static constexpr int kLast = kWalk + 64;
   static constexpr int kBytes = kLast + 16;
   static_assert(kBlock % 16 == 0 && kBars % 8 == 0, "alignment");
 };
@@ -113,62 +121,141 @@ __device__ __forceinline__ int token_of(int r) {
   return (r & 1) ? 4 * a + 3 - b : 4 * a + b;
 }
 
-// One warp's ring of page blocks.  Block i of an item's run is page first +
-// kWarps i of the sequence; `issued` and `waited` number the blocks over the
-// CTA's whole run, which gives the stage and the parity.
+// One warp's ring of page blocks.  Block i of an item's part is page kWarps i of
+// bt_row; `issued` and `waited` number the blocks over the CTA's whole run, which
+// gives the stage and the parity.
 template <int D>
 struct BlockRing {
   uint32_t stage0, bar0;
-  const uint8_t *cache;
-  const int32_t *bt_row;
-  int *status;
-  int64_t head_stride, head_offset;  // bytes a page, bytes of the kv head in it
-  int first, n, num_pages, ids_cur, ids_nxt;
+  const uint8_t *cache;    // the kv head's block of page 0
+  const int32_t *bt_row;   // the warp's first page of the part
+  int n, ids_cur, ids_nxt;
   uint32_t issued, waited;  // blocks over the whole run
 
-  __device__ int fetch_id(int i) const {
-    return i < n ? __ldg(bt_row + first + kWarps * i) : 0;
-  }
+  __device__ int fetch_id(int i) const { return i < n ? __ldg(bt_row + kWarps * i) : 0; }
   __device__ void start(int lane) {
     ids_cur = fetch_id(lane);
     ids_nxt = fetch_id(32 + lane);
   }
-  // Called by the whole warp with i = 0, 1, 2, ... of the item's blocks.
-  __device__ void issue(int i, int lane) {
+  // Called by the whole warp with i = 0, 1, 2, ... of the part's blocks.
+  __device__ void issue(int i, int lane, const RowsParams &p) {
     if ((i & 31) == 0 && i > 0) {
       ids_cur = ids_nxt;
       ids_nxt = fetch_id(i + 32 + lane);
     }
     int id = __shfl_sync(kFull, ids_cur, i & 31);
     if (lane == 0) {
-      if (static_cast<unsigned>(id) >= static_cast<unsigned>(num_pages)) {
-        record_error(status, PA_ERR_BAD_BLOCK);
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
+        record_error(p.status, PA_ERR_BAD_BLOCK);
         id = 0;  // read a page that exists; the result is flagged as invalid
       }
       const uint32_t s = issued % kStages;
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(bar0 + 8 * s, kv4::block_bytes(D));
-      bulk_load(stage0 + s * kv4::block_bytes(D), cache + id * head_stride + head_offset,
+      bulk_load(stage0 + s * kv4::block_bytes(D),
+                cache + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes,
                 kv4::block_bytes(D), bar0 + 8 * s);
     }
     ++issued;
   }
   // Warp-uniform wait for the next block; its stage, or 0 when the wait ran out.
-  __device__ uint32_t wait(int lane) {
+  __device__ uint32_t wait(int lane, const RowsParams &p) {
     const uint32_t s = waited % kStages, par = (waited / kStages) & 1;
     ++waited;
     if (__all_sync(kFull, mbar_wait(bar0 + 8 * s, par))) return stage0 + s * kv4::block_bytes(D);
-    if (lane == 0) record_error(status, PA_ERR_TIMEOUT);
+    if (lane == 0) record_error(p.status, PA_ERR_TIMEOUT);
     for (uint32_t k = waited; k < issued; ++k)  // copies in flight still land
       mbar_wait(bar0 + 8 * (k % kStages), (k / kStages) & 1);
     return 0;
   }
 };
 
-// Which sequence a position of the flattened page list belongs to.
-struct Cursor {
-  int b;            // sequence
-  int64_t base;     // pages of one (kv head, row tile) of the sequences before b
+// The part of one item that a CTA's run holds.
+struct Part {
+  int b, g;           // sequence, kv head
+  int r0, n_r;        // rows of the kv head
+  int pg0, n_pg;      // pages
+  int tokens;         // keys of the sequence, the chunk's included
+  int first, last;    // CTAs that hold the item
+  int slot;           // of the first one's state: 0 when the item starts its run
+  int more;           // the run goes on behind this part
+};
+static_assert(sizeof(Part) <= 64, "room in shared memory");
+
+// The CTA's run [w, w1) of the flattened page list, walked part by part by one
+// thread, which keeps the others' registers free of it.
+struct Walk {
+  int64_t w, w1, run, base;  // base: pages of one (kv head, row tile) before sequence b
+  int b, n_b;
+
+  // Tokens of sequence b, the chunk's included (a clamped length is reported by
+  // the first CTA's scan).
+  static __device__ int tokens(const RowsParams &p, int b, bool report) {
+    const int most = p.max_blocks * kPageSize - p.n_new;
+    int t = __ldg(p.ctx_lens + b);
+    if (t < 0 || t > most) {
+      if (report) record_error(p.status, PA_ERR_BAD_CTX);
+      t = t < 0 ? 0 : most;
+    }
+    return t + p.n_new;
+  }
+  // An empty sequence counts one page, so that someone writes its zeros.
+  static __device__ int pages(int tokens) {
+    return max(1, (tokens + kPageSize - 1) / kPageSize);
+  }
+  // The whole warp: lane l sums the pages of sequences [l per, (l + 1) per), and a
+  // scan finds the sequence in which this CTA's run starts.  False: no run.
+  // Warp-uniform results; lane 0 keeps them in *out.
+  static __device__ bool start(const RowsParams &p, int lane, Walk *out) {
+    Walk x;
+    const int heads = p.n_kv_heads * p.n_sub;
+    const int per = (p.batch + 31) / 32;
+    const int b0 = min(p.batch, lane * per), b1 = min(p.batch, b0 + per);
+    int64_t sum = 0;
+#pragma unroll 4
+    for (int i = b0; i < b1; ++i) sum += pages(tokens(p, i, blockIdx.x == 0));
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t total = __shfl_sync(kFull, incl, 31) * heads;
+    x.run = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinPages));
+    x.w = blockIdx.x * x.run;
+    x.w1 = min(total, x.w + x.run);
+    if (x.w >= x.w1) return false;
+    const int src = __ffs(__ballot_sync(kFull, incl * heads > x.w)) - 1;
+    x.b = __shfl_sync(kFull, b0, src);
+    x.base = __shfl_sync(kFull, incl - sum, src);
+    x.n_b = pages(tokens(p, x.b, false));
+    if (lane == 0) *out = x;
+    return true;
+  }
+  __device__ void next(const RowsParams &p, volatile Part &s) {
+    const int heads = p.n_kv_heads * p.n_sub;
+    while ((base + n_b) * heads <= w) {
+      base += n_b;
+      n_b = pages(tokens(p, ++b, false));
+    }
+    const int64_t rel = w - base * heads;
+    const int item = static_cast<int>(rel / n_b);
+    const int pg0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
+    const int n_pg = static_cast<int>(min(static_cast<int64_t>(n_b - pg0), w1 - w));
+    const int64_t i0 = w - pg0;  // the item's first page
+    s.b = b;
+    s.g = item / p.n_sub;
+    s.r0 = (item % p.n_sub) * p.tile_rows;
+    s.n_r = min(p.tile_rows, p.n_rows - (item % p.n_sub) * p.tile_rows);
+    s.pg0 = pg0;
+    s.n_pg = n_pg;
+    s.tokens = tokens(p, b, false);
+    s.first = static_cast<int>(i0 / run);
+    s.last = static_cast<int>((i0 + n_b - 1) / run);
+    s.slot = i0 % run == 0 ? 0 : 1;
+    w += n_pg;
+    s.more = w < w1;
+  }
 };
 
 template <int D, bool BF16, bool WIDE, bool OUT16>
@@ -191,89 +278,51 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   griddep_wait();  // inputs may come from the previous kernel in the stream
   __syncthreads();
 
-  // ---- this CTA's run [w0, w1) of the flattened page list: lane l sums the
-  // pages of sequences [l per, (l + 1) per), a warp scan finds the run's start
-  const int maxT = p.max_blocks * kPageSize;
-  const int extra = p.n_new;  // tokens of the chunk, behind ctx_lens
-  auto tokens_of = [&](int b, bool report) {
-    int t = __ldg(p.ctx_lens + b);
-    if (t < 0 || t > maxT - extra) {
-      if (report) record_error(p.status, PA_ERR_BAD_CTX);
-      t = t < 0 ? 0 : maxT - extra;
+  volatile Part *parts = reinterpret_cast<volatile Part *>(smem + L::kParts);
+  volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::kLast);
+  Walk *walk = reinterpret_cast<Walk *>(smem + L::kWalk);
+  if (warp == kWarps - 1) {  // the warp with the fewest pages plans
+    const bool any = Walk::start(p, lane, walk);
+    if (lane == 0) {
+      if (any) walk->next(p, parts[0]);
+      *s_last = any;
     }
-    return t + extra;
-  };
-  auto pages_of = [](int tokens) { return max(1, (tokens + kPageSize - 1) / kPageSize); };
-  const int heads = p.n_kv_heads * p.n_sub;  // items a sequence
-  const int per = (p.batch + 31) / 32;
-  const int lb0 = min(p.batch, lane * per), lb1 = min(p.batch, lb0 + per);
-  int64_t sum = 0;
-#pragma unroll 4
-  for (int b = lb0; b < lb1; ++b) sum += pages_of(tokens_of(b, blockIdx.x == 0 && warp == 0));
-  int64_t incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += v;
   }
-  const int64_t total = __shfl_sync(kFull, incl, 31) * heads;
-  int64_t run = (total + gridDim.x - 1) / gridDim.x;
-  if (run < kMinPages) run = kMinPages;
-  const int64_t w0 = blockIdx.x * run, w1 = min(total, w0 + run);
-  if (w0 >= w1) return;
-  const int src = __ffs(__ballot_sync(kFull, incl * heads > w0)) - 1;
-  Cursor cur;
-  cur.b = __shfl_sync(kFull, lb0, src);
-  cur.base = __shfl_sync(kFull, incl - sum, src);
-  int n_b = pages_of(tokens_of(cur.b, false));
+  __syncthreads();
+  if (!*s_last) return;
 
   BlockRing<D> ring;
   ring.stage0 = sb + warp * kStages * L::kBlock;
   ring.bar0 = sb + L::kBars + warp * kStages * 8;
-  ring.cache = p.cache;
-  ring.status = p.status;
-  ring.head_stride = static_cast<int64_t>(p.n_kv_heads) * L::kBlock;
-  ring.num_pages = p.num_pages;
   ring.issued = ring.waited = 0;
   bool alive = true;  // false once a wait of this warp has run out
 
   float *mer_o = reinterpret_cast<float *>(smem + L::kMergeO);
   float *mer_m = reinterpret_cast<float *>(smem + L::kMergeM);
   float *mer_l = reinterpret_cast<float *>(smem + L::kMergeL);
-  volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::kLast);
   const int tk = token_of(ln);
 
-  for (int64_t w = w0; w < w1;) {
-    // ---- the item that w lies in, and the run's pages of it
-    while ((cur.base + n_b) * heads <= w) {
-      cur.base += n_b;
-      n_b = pages_of(tokens_of(++cur.b, false));
+  for (int turn = 0;; turn ^= 1) {
+    volatile Part &part = parts[turn];
+    const int first_page = part.pg0 + warp;
+    int key0 = first_page * kPageSize;  // of the page at hand
+    {
+      const int n_pg = part.n_pg, b = part.b;
+      ring.bt_row = p.block_table + static_cast<size_t>(b) * p.max_blocks + first_page;
+      ring.cache = p.cache + static_cast<size_t>(part.g) * L::kBlock;
+      ring.n = part.tokens > 0 && alive && warp < n_pg ? (n_pg - warp + kWarps - 1) / kWarps : 0;
     }
-    const int64_t rel = w - cur.base * heads;
-    const int item = static_cast<int>(rel / n_b);
-    const int pg0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
-    const int n_pg = static_cast<int>(min(static_cast<int64_t>(n_b - pg0), w1 - w));
-    const int g = item / p.n_sub, r0 = (item % p.n_sub) * p.tile_rows;
-    const int n_r = min(p.tile_rows, p.n_rows - r0);
-    const int T = tokens_of(cur.b, false);
-    // last key (exclusive) each of this lane's two rows sees
-    auto row_of = [&](int col) { return r0 + min(WIDE ? col : (col & 3), n_r - 1); };
-    auto limit_of = [&](int r) { return OUT16 ? T - extra + 1 + r / p.group : T; };
-    const int lim0 = limit_of(row_of(2 * lc)), lim1 = limit_of(row_of(2 * lc + 1));
-    const int lim_all = limit_of(r0);  // every row sees at least this many keys
-
-    ring.bt_row = p.block_table + static_cast<size_t>(cur.b) * p.max_blocks;
-    ring.head_offset = static_cast<int64_t>(g) * L::kBlock;
-    ring.first = pg0 + warp;
-    ring.n = T > 0 && alive && warp < n_pg ? (n_pg - warp + kWarps - 1) / kWarps : 0;
     ring.start(lane);
-    for (int i = 0; i < kStages && i < ring.n; ++i) ring.issue(i, lane);
+    for (int i = 0; i < kStages && i < ring.n; ++i) ring.issue(i, lane, p);
+    if (tid == (kWarps - 1) * 32 && part.more) walk->next(p, parts[turn ^ 1]);
 
     // ---- q of this lane's column as the first product's operand
-    const size_t q_row0 = static_cast<size_t>(cur.b) * p.queries * p.n_q_heads + g * p.group;
-    auto q_row = [&](int r) {  // row r of the kv head: query r / G, head r % G
-      return q_row0 + static_cast<size_t>(r / p.group) * p.n_q_heads + r % p.group;
+    // row r of the kv head: query r / G, head r % G
+    auto q_row = [&](int r) {
+      return (static_cast<size_t>(part.b) * p.queries + r / p.group) * p.n_q_heads +
+             part.g * p.group + r % p.group;
     };
+    const int n_r = part.n_r;
     uint32_t qb[2 * KW][2];
     float f0, f1, e0, e1;  // per column 2 lc, 2 lc + 1: score factor, scaled sum of q
     {
@@ -281,7 +330,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       float x[8 * KW];
       if (col < n_r) {
         const uint4 *src4 =
-            reinterpret_cast<const uint4 *>(p.q + q_row(r0 + col) * D + (D / 4) * lc);
+            reinterpret_cast<const uint4 *>(p.q + q_row(part.r0 + col) * D + (D / 4) * lc);
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
           const uint4 v = __ldg(src4 + k);
@@ -334,13 +383,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, z0 = 0.f, z1 = 0.f;
     float v_ref = 0.f, v_inv = 0.f;  // reference of scale_v (a power of two), 2^7 / it
 
-    for (int i = 0; i < ring.n; ++i) {
-      const uint32_t st = ring.wait(lane);
+    // the first key that some row of the tile does not see
+    const int lim_all = OUT16 ? part.tokens - p.n_new + 1 + part.r0 / p.group : part.tokens;
+    for (int i = 0; i < ring.n; ++i, key0 += kWarps * kPageSize) {
+      const uint32_t st = ring.wait(lane, p);
       if (st == 0) {
         alive = false;
         break;
       }
-      const int key0 = (pg0 + warp + kWarps * i) * kPageSize;
 
       // ---- scores: S[token][row]
       const uint32_t kmeta0 = lds32(st + kv4::meta_offset(D, 0, tk));
@@ -357,7 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
         ka[0] = a.x, ka[1] = a.y;
         kb[0] = b.x, kb[1] = b.y;
       }
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains
 #pragma unroll
       for (int k = 0; k < KW; ++k)
 #pragma unroll
@@ -365,7 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
           const uint32_t xa = ka[k] >> (8 * h), xb = kb[k] >> (8 * h);
           const uint32_t a[4] = {xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u,
                                  xb & 0x00f000f0u};
-          mma16816<false>(s, a, qb[2 * k + h][0], qb[2 * k + h][1]);
+          mma16816<false>(h ? s1 : s, a, qb[2 * k + h][0], qb[2 * k + h][1]);
         }
       // V's scales and zeros of the same two tokens, and V's codes
       uint32_t vm0 = lds32(st + kv4::meta_offset(D, 1, tk));
@@ -382,17 +432,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
         }
       }
       __syncwarp();  // the stage has been read by every lane
-      if (i + kStages < ring.n) ring.issue(i + kStages, lane);
+      if (i + kStages < ring.n) ring.issue(i + kStages, lane, p);
 
       {
         const float2 k0 = unpack2<BF16>(kmeta0), k1 = unpack2<BF16>(kmeta1);
-        s[0] = fmaf(k0.x, fmaf(f0, s[0], -8.f * e0), k0.y * e0);
-        s[1] = fmaf(k0.x, fmaf(f1, s[1], -8.f * e1), k0.y * e1);
-        s[2] = fmaf(k1.x, fmaf(f0, s[2], -8.f * e0), k1.y * e0);
-        s[3] = fmaf(k1.x, fmaf(f1, s[3], -8.f * e1), k1.y * e1);
+        s[0] = fmaf(k0.x, fmaf(f0, s[0] + s1[0], -8.f * e0), k0.y * e0);
+        s[1] = fmaf(k0.x, fmaf(f1, s[1] + s1[1], -8.f * e1), k0.y * e1);
+        s[2] = fmaf(k1.x, fmaf(f0, s[2] + s1[2], -8.f * e0), k1.y * e0);
+        s[3] = fmaf(k1.x, fmaf(f1, s[3] + s1[3], -8.f * e1), k1.y * e1);
       }
       if (key0 + kPageSize > lim_all) {
-        const int t0 = key0 + tk, t1 = t0 + 8;
+        // last key (exclusive) each of this lane's two rows sees
+        const int T = part.tokens, t0 = key0 + tk, t1 = t0 + 8;
+        auto limit = [&](int col) {
+          const int r = part.r0 + min(WIDE ? col : (col & 3), n_r - 1);
+          return OUT16 ? T - p.n_new + 1 + r / p.group : T;
+        };
+        const int lim0 = limit(2 * lc), lim1 = limit(2 * lc + 1);
         s[0] = t0 < lim0 ? s[0] : -INFINITY;
         s[1] = t0 < lim1 ? s[1] : -INFINITY;
         s[2] = t1 < lim0 ? s[2] : -INFINITY;
@@ -475,8 +531,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
                                    sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u),
                                    sub_1032((ys & 0x000f000fu) | 0x64006400u),
                                    sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u)};
-            mma16816<false>(o[4 * j + 2 * h + u], a, b0, b1);
-            if constexpr (WIDE) mma16816<false>(o[4 * j + 2 * h + u], a, b2, b3);
+            float (&ok)[4] = o[4 * j + 2 * h + u];
+            if constexpr (WIDE) {
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<false>(t, a, b2, b3);
+              mma16816<false>(t, a, b0, b1);
+              ok[0] += t[0], ok[1] += t[1], ok[2] += t[2], ok[3] += t[3];
+            } else {
+              mma16816<false>(ok, a, b0, b1);
+            }
           }
         }
     }
@@ -516,10 +579,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     __syncthreads();
 
     // ---- the item's CTAs: the first holds its start, the last its end
-    const int64_t i0 = cur.base * heads + static_cast<int64_t>(item) * n_b, i1 = i0 + n_b;
-    const int first = static_cast<int>(i0 / run), last = static_cast<int>((i1 - 1) / run);
+    const int first = part.first, last = part.last;
     auto store = [&](int r, int d, float4 v) {  // row r of the tile, dimensions d .. d + 3
-      const size_t at = q_row(r0 + r) * D + d;
+      const size_t at = q_row(part.r0 + r) * D + d;
       if constexpr (OUT16)
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
             make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
@@ -528,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     };
     // CTA c's state of this item: slot 0 when its part starts the CTA's run.
     auto state = [&](int c, int r) {
-      const int slot = c > first || i0 == first * run ? 0 : 1;
+      const int slot = c > first ? 0 : part.slot;
       return p.ws + ((static_cast<size_t>(c) * 2 + slot) * kTile + r) * (D + 4);
     };
     for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
@@ -572,7 +634,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
           const int r = e / (D / 4), d = 4 * (e % (D / 4));
           float m = -INFINITY, l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int kBatch = 8;
+          constexpr int kBatch = 4;
           for (int c = first; c <= last; c += kBatch) {
             float2 ml[kBatch];
             float4 v[kBatch];
@@ -602,8 +664,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
         }
       }
     }
-    w += n_pg;
-    __syncthreads();  // the merge area is free for the next item
+    if (!part.more) break;
+    __syncthreads();  // the merge area is free, and the next part is planned
   }
 }
 
@@ -661,6 +723,7 @@ int launch_kv4_rows(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.batch = a.batch;
   p.max_blocks = a.max_blocks;
   p.num_pages = a.num_pages;
+  p.page_bytes = static_cast<uint32_t>(a.n_kv_heads) * kv4::block_bytes(a.head_dim);
   p.n_rows = p.queries * p.group;
   p.n_sub = (p.n_rows + kTile - 1) / kTile;
   p.tile_rows = (p.n_rows + p.n_sub - 1) / p.n_sub;
