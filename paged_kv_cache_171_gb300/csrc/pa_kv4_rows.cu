@@ -54,9 +54,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleSlack = 8.0f;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 4, kStages = 4, kTile = 8;  // query rows a tile
+constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
+constexpr int kWarps = 4, kStages = 3, kTile = 8;  // query rows a tile
+constexpr int kPair = 2;         // pages a stage holds
 constexpr int kCtasPerSm = 4;
-constexpr int kMinPages = 8;     // least pages a CTA takes
+constexpr int kMinPages = kWarps * kPair;  // least pages a CTA takes
 
 struct RowsParams {
   const uint16_t *q;
@@ -75,17 +77,20 @@ struct RowsParams {
 template <int D>
 struct RowsSmem {
   static constexpr int kBlock = kv4::block_bytes(D);
-  static constexpr int kRing = kWarps * kStages * kBlock;
+  static constexpr int kStage = kPair * kBlock;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  // The warps' states at the end of a part, over the ring: no copy is in flight then.
   static constexpr int kRowStride = D + 4;  // floats a merged row
-  static constexpr int kMergeO = kRing;
+  static constexpr int kMergeO = 0;
   static constexpr int kMergeM = kMergeO + kWarps * kTile * kRowStride * 4;
   static constexpr int kMergeL = kMergeM + kWarps * kTile * 4;
-  static constexpr int kBars = kMergeL + kWarps * kTile * 4;
+  static_assert(kMergeL + kWarps * kTile * 4 <= kRing, "merge area must fit in the ring");
+  static constexpr int kBars = kRing;
   static constexpr int kParts = kBars + kWarps * kStages * 8;  // Part[2]
   static constexpr int kWalk = kParts + 2 * 64;                // Walk
   static constexpr int kLast = kWalk + 64;
   static constexpr int kBytes = kLast + 16;
-  static_assert(kBlock % 16 == 0 && kBars % 8 == 0, "alignment");
+  static_assert(kBlock % 16 == 0 && kBars % 8 == 0 && kParts % 16 == 0, "alignment");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
@@ -121,48 +126,62 @@ __device__ __forceinline__ int token_of(int r) {
   return (r & 1) ? 4 * a + 3 - b : 4 * a + b;
 }
 
-// One warp's ring of page blocks.  Block i of an item's part is page kWarps i of
-// bt_row; `issued` and `waited` number the blocks over the CTA's whole run, which
-// gives the stage and the parity.
+// One warp's ring of stages of two pages.  Chunk i of an item's part is pages
+// kWarps kPair i and the one behind it of bt_row (the last may be one page);
+// `issued` and `waited` number the chunks over the CTA's whole run, which gives
+// the stage and the parity.
 template <int D>
 struct BlockRing {
+  static constexpr int kBlock = kv4::block_bytes(D);
   uint32_t stage0, bar0;
   const uint8_t *cache;    // the kv head's block of page 0
   const int32_t *bt_row;   // the warp's first page of the part
-  int n, ids_cur, ids_nxt;
-  uint32_t issued, waited;  // blocks over the whole run
+  int n, pages;            // chunks of the warp; pages of the part from bt_row on
+  int ids_cur, ids_nxt;
+  uint32_t issued, waited;  // chunks over the whole run
 
-  __device__ int fetch_id(int i) const { return i < n ? __ldg(bt_row + kWarps * i) : 0; }
-  __device__ void start(int lane) {
-    ids_cur = fetch_id(lane);
-    ids_nxt = fetch_id(32 + lane);
+  // Lane l holds the id of page l & 1 of chunk 16 w + (l >> 1), w the window.
+  __device__ int fetch_id(int w, int lane) const {
+    const int pg = kWarps * kPair * (16 * w + (lane >> 1)) + (lane & 1);
+    return pg < pages ? __ldg(bt_row + pg) : 0;
   }
-  // Called by the whole warp with i = 0, 1, 2, ... of the part's blocks.
+  __device__ void start(int lane) {
+    ids_cur = fetch_id(0, lane);
+    ids_nxt = n > 16 ? fetch_id(1, lane) : 0;
+  }
+  // Called by the whole warp with i = 0, 1, 2, ... of the part's chunks.
   __device__ void issue(int i, int lane, const RowsParams &p) {
-    if ((i & 31) == 0 && i > 0) {
+    if ((i & 15) == 0 && i > 0) {
       ids_cur = ids_nxt;
-      ids_nxt = fetch_id(i + 32 + lane);
+      ids_nxt = fetch_id((i >> 4) + 1, lane);
     }
-    int id = __shfl_sync(kFull, ids_cur, i & 31);
+    int id0 = __shfl_sync(kFull, ids_cur, 2 * (i & 15));
+    int id1 = __shfl_sync(kFull, ids_cur, 2 * (i & 15) + 1);
     if (lane == 0) {
-      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
+      const bool two = kWarps * kPair * i + 1 < pages;
+      if (static_cast<unsigned>(id0) >= static_cast<unsigned>(p.num_pages) ||
+          static_cast<unsigned>(id1) >= static_cast<unsigned>(p.num_pages)) {
         record_error(p.status, PA_ERR_BAD_BLOCK);
-        id = 0;  // read a page that exists; the result is flagged as invalid
+        id0 = id1 = 0;  // read a page that exists; the result is flagged as invalid
       }
-      const uint32_t s = issued % kStages;
+      const uint32_t s = issued % kStages, bar = bar0 + 8 * s;
+      const uint32_t dst = stage0 + s * (kPair * kBlock);
       fence_proxy_async_smem();
-      mbar_arrive_expect_tx(bar0 + 8 * s, kv4::block_bytes(D));
-      bulk_load(stage0 + s * kv4::block_bytes(D),
-                cache + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes,
-                kv4::block_bytes(D), bar0 + 8 * s);
+      mbar_arrive_expect_tx(bar, two ? 2 * kBlock : kBlock);
+      bulk_load(dst, cache + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * p.page_bytes,
+                kBlock, bar);
+      if (two)
+        bulk_load(dst + kBlock,
+                  cache + static_cast<uint64_t>(static_cast<uint32_t>(id1)) * p.page_bytes,
+                  kBlock, bar);
     }
     ++issued;
   }
-  // Warp-uniform wait for the next block; its stage, or 0 when the wait ran out.
+  // Warp-uniform wait for the next chunk; its stage, or 0 when the wait ran out.
   __device__ uint32_t wait(int lane, const RowsParams &p) {
     const uint32_t s = waited % kStages, par = (waited / kStages) & 1;
     ++waited;
-    if (__all_sync(kFull, mbar_wait(bar0 + 8 * s, par))) return stage0 + s * kv4::block_bytes(D);
+    if (__all_sync(kFull, mbar_wait(bar0 + 8 * s, par))) return stage0 + s * (kPair * kBlock);
     if (lane == 0) record_error(p.status, PA_ERR_TIMEOUT);
     for (uint32_t k = waited; k < issued; ++k)  // copies in flight still land
       mbar_wait(bar0 + 8 * (k % kStages), (k / kStages) & 1);
@@ -292,7 +311,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   if (!*s_last) return;
 
   BlockRing<D> ring;
-  ring.stage0 = sb + warp * kStages * L::kBlock;
+  ring.stage0 = sb + warp * kStages * L::kStage;
   ring.bar0 = sb + L::kBars + warp * kStages * 8;
   ring.issued = ring.waited = 0;
   bool alive = true;  // false once a wait of this warp has run out
@@ -301,16 +320,20 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   float *mer_m = reinterpret_cast<float *>(smem + L::kMergeM);
   float *mer_l = reinterpret_cast<float *>(smem + L::kMergeL);
   const int tk = token_of(ln);
+  // V rows of the tokens that score rows 2 lc and 2 lc + 1 stand for
+  const int t0 = token_of(2 * lc) * kv4::row_bytes(D);
+  const int t1 = token_of(2 * lc + 1) * kv4::row_bytes(D);
 
   for (int turn = 0;; turn ^= 1) {
     volatile Part &part = parts[turn];
-    const int first_page = part.pg0 + warp;
-    int key0 = first_page * kPageSize;  // of the page at hand
+    const int first_page = part.pg0 + kPair * warp;
+    int key0 = first_page * kPageSize;  // of the chunk at hand
     {
-      const int n_pg = part.n_pg, b = part.b;
+      const int b = part.b;
       ring.bt_row = p.block_table + static_cast<size_t>(b) * p.max_blocks + first_page;
       ring.cache = p.cache + static_cast<size_t>(part.g) * L::kBlock;
-      ring.n = part.tokens > 0 && alive && warp < n_pg ? (n_pg - warp + kWarps - 1) / kWarps : 0;
+      ring.pages = part.tokens > 0 && alive ? part.n_pg - kPair * warp : 0;
+      ring.n = max(0, (ring.pages + kWarps * kPair - 1) / (kWarps * kPair));
     }
     ring.start(lane);
     for (int i = 0; i < kStages && i < ring.n; ++i) ring.issue(i, lane, p);
@@ -380,178 +403,202 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     float o[MT][4];
 #pragma unroll
     for (int k = 0; k < MT; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, z0 = 0.f, z1 = 0.f;
+    // per row 2 lc (x) and 2 lc + 1 (y): the running max, negated, the sums l and z
+    float2 nm = make_float2(-kNoKey, -kNoKey);
+    float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
     float v_ref = 0.f, v_inv = 0.f;  // reference of scale_v (a power of two), 2^7 / it
+    const float2 f2 = make_float2(f0, f1), e2 = make_float2(e0, e1);
+    const float2 e8 = make_float2(-8.f * e0, -8.f * e1);
+    const float rem = lc < 2 ? 0.f : -1.f;  // this lane's columns carry remainder terms
 
-    // the first key that some row of the tile does not see
-    const int lim_all = OUT16 ? part.tokens - p.n_new + 1 + part.r0 / p.group : part.tokens;
-    for (int i = 0; i < ring.n; ++i, key0 += kWarps * kPageSize) {
+    // Keys that every row of the tile sees and this part holds end here.
+    const int part_end = (part.pg0 + part.n_pg) * kPageSize;
+    const int lim_all = min(part_end, OUT16 ? part.tokens - p.n_new + 1 + part.r0 / p.group
+                                            : part.tokens);
+    for (int i = 0; i < ring.n; ++i, key0 += kWarps * kPair * kPageSize) {
       const uint32_t st = ring.wait(lane, p);
       if (st == 0) {
         alive = false;
         break;
       }
 
-      // ---- scores: S[token][row]
-      const uint32_t kmeta0 = lds32(st + kv4::meta_offset(D, 0, tk));
-      const uint32_t kmeta1 = lds32(st + kv4::meta_offset(D, 0, tk + 8));
-      uint32_t ka[KW], kb[KW];
-      if constexpr (KW == 4) {
-        const uint4 a = lds128(st + kv4::code_offset(D, 0, tk) + 16 * lc);
-        const uint4 b = lds128(st + kv4::code_offset(D, 0, tk + 8) + 16 * lc);
-        ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
-        kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
-      } else {
-        const uint2 a = lds64(st + kv4::code_offset(D, 0, tk) + 8 * lc);
-        const uint2 b = lds64(st + kv4::code_offset(D, 0, tk + 8) + 8 * lc);
-        ka[0] = a.x, ka[1] = a.y;
-        kb[0] = b.x, kb[1] = b.y;
-      }
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains
+      // ---- scores S[token][row] of the two pages; this lane: tokens tk and tk + 8 of
+      // each (index 2 page + half), rows 2 lc and 2 lc + 1
+      float2 s[2 * kPair], d[2 * kPair];
+      uint32_t vm[2 * kPair];
 #pragma unroll
-      for (int k = 0; k < KW; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t xa = ka[k] >> (8 * h), xb = kb[k] >> (8 * h);
-          const uint32_t a[4] = {xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u,
-                                 xb & 0x00f000f0u};
-          mma16816<false>(h ? s1 : s, a, qb[2 * k + h][0], qb[2 * k + h][1]);
-        }
-      // V's scales and zeros of the same two tokens, and V's codes
-      uint32_t vm0 = lds32(st + kv4::meta_offset(D, 1, tk));
-      uint32_t vm1 = lds32(st + kv4::meta_offset(D, 1, tk + 8));
-      uint32_t va[4][VW];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int t = token_of(2 * lc + (u & 1)) + 8 * (u >> 1);
-        if constexpr (VW == 2) {
-          const uint2 x = lds64(st + kv4::code_offset(D, 1, t) + 8 * ln);
-          va[u][0] = x.x, va[u][1] = x.y;
+      for (int pg = 0; pg < kPair; ++pg) {
+        const uint32_t blk = st + pg * L::kBlock;
+        const uint32_t km0 = lds32(blk + kv4::meta_offset(D, 0, 0) + 4 * tk);
+        const uint32_t km1 = lds32(blk + kv4::meta_offset(D, 0, 8) + 4 * tk);
+        vm[2 * pg] = lds32(blk + kv4::meta_offset(D, 1, 0) + 4 * tk);
+        vm[2 * pg + 1] = lds32(blk + kv4::meta_offset(D, 1, 8) + 4 * tk);
+        const uint32_t row = blk + tk * kv4::row_bytes(D) + 4 * KW * lc;
+        uint32_t ka[KW], kb[KW];
+        if constexpr (KW == 4) {
+          const uint4 a = lds128(row), b = lds128(row + 8 * kv4::row_bytes(D));
+          ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
+          kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
         } else {
-          va[u][0] = lds32(st + kv4::code_offset(D, 1, t) + 4 * ln);
+          const uint2 a = lds64(row), b = lds64(row + 8 * kv4::row_bytes(D));
+          ka[0] = a.x, ka[1] = a.y;
+          kb[0] = b.x, kb[1] = b.y;
         }
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KW; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t xa = ka[k] >> (8 * h), xb = kb[k] >> (8 * h);
+            const uint32_t a[4] = {xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u,
+                                   xb & 0x00f000f0u};
+            mma16816<false>(acc, a, qb[2 * k + h][0], qb[2 * k + h][1]);
+          }
+        const float2 k0 = unpack2<BF16>(km0), k1 = unpack2<BF16>(km1);
+        s[2 * pg] = __ffma2_rn(make_float2(k0.x, k0.x),
+                               __ffma2_rn(f2, make_float2(acc[0], acc[1]), e8),
+                               __fmul2_rn(make_float2(k0.y, k0.y), e2));
+        s[2 * pg + 1] = __ffma2_rn(make_float2(k1.x, k1.x),
+                                   __ffma2_rn(f2, make_float2(acc[2], acc[3]), e8),
+                                   __fmul2_rn(make_float2(k1.y, k1.y), e2));
       }
-      __syncwarp();  // the stage has been read by every lane
-      if (i + kStages < ring.n) ring.issue(i + kStages, lane, p);
-
-      {
-        const float2 k0 = unpack2<BF16>(kmeta0), k1 = unpack2<BF16>(kmeta1);
-        s[0] = fmaf(k0.x, fmaf(f0, s[0] + s1[0], -8.f * e0), k0.y * e0);
-        s[1] = fmaf(k0.x, fmaf(f1, s[1] + s1[1], -8.f * e1), k0.y * e1);
-        s[2] = fmaf(k1.x, fmaf(f0, s[2] + s1[2], -8.f * e0), k1.y * e0);
-        s[3] = fmaf(k1.x, fmaf(f1, s[3] + s1[3], -8.f * e1), k1.y * e1);
-      }
-      if (key0 + kPageSize > lim_all) {
+      if (key0 + kPair * kPageSize > lim_all) {
         // last key (exclusive) each of this lane's two rows sees
-        const int T = part.tokens, t0 = key0 + tk, t1 = t0 + 8;
+        const int T = min(part.tokens, part_end);
         auto limit = [&](int col) {
           const int r = part.r0 + min(WIDE ? col : (col & 3), n_r - 1);
-          return OUT16 ? T - p.n_new + 1 + r / p.group : T;
+          return OUT16 ? min(T, part.tokens - p.n_new + 1 + r / p.group) : T;
         };
         const int lim0 = limit(2 * lc), lim1 = limit(2 * lc + 1);
-        s[0] = t0 < lim0 ? s[0] : -INFINITY;
-        s[1] = t0 < lim1 ? s[1] : -INFINITY;
-        s[2] = t1 < lim0 ? s[2] : -INFINITY;
-        s[3] = t1 < lim1 ? s[3] : -INFINITY;
-        // rows past the end may hold anything: 0 * NaN must not enter
-        if (t0 >= T) vm0 = 0;
-        if (t1 >= T) vm1 = 0;
+#pragma unroll
+        for (int u = 0; u < 2 * kPair; ++u) {
+          const int t = key0 + tk + 8 * u;
+          s[u].x = t < lim0 ? s[u].x : -INFINITY;
+          s[u].y = t < lim1 ? s[u].y : -INFINITY;
+          // rows past the end may hold anything: 0 * NaN must not enter
+          if (t >= T) vm[u] = 0;
+        }
       }
-      const float2 v0 = unpack2<BF16>(vm0), v1 = unpack2<BF16>(vm1);
+      float2 v[2 * kPair];
+#pragma unroll
+      for (int u = 0; u < 2 * kPair; ++u) {
+        v[u] = unpack2<BF16>(vm[u]);
+        d[u] = __fadd2_rn(s[u], nm);
+      }
 
       // ---- move the references when a score or a scale outgrows them
-      const bool need = s[0] > m0 + kRescaleSlack || s[2] > m0 + kRescaleSlack ||
-                        s[1] > m1 + kRescaleSlack || s[3] > m1 + kRescaleSlack ||
-                        fabsf(v0.x) > v_ref || fabsf(v1.x) > v_ref;
-      if (__any_sync(kFull, need)) {
-        float a = fmaxf(s[0], s[2]), b = fmaxf(s[1], s[3]);
-        float v = fmaxf(fabsf(v0.x), fabsf(v1.x));
+      const float grow = fmaxf(fmaxf(fmaxf(d[0].x, d[0].y), fmaxf(d[1].x, d[1].y)),
+                               fmaxf(fmaxf(d[2].x, d[2].y), fmaxf(d[3].x, d[3].y)));
+      float vtop = fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[1].x)),
+                         fmaxf(fabsf(v[2].x), fabsf(v[3].x)));
+      if (__any_sync(kFull, grow > kRescaleSlack || vtop > v_ref)) {
+        float a = fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x));
+        float b = fmaxf(fmaxf(s[0].y, s[1].y), fmaxf(s[2].y, s[3].y));
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
           a = fmaxf(a, __shfl_xor_sync(kFull, a, x));
           b = fmaxf(b, __shfl_xor_sync(kFull, b, x));
-          v = fmaxf(v, __shfl_xor_sync(kFull, v, x));
+          vtop = fmaxf(vtop, __shfl_xor_sync(kFull, vtop, x));
         }
-        const float n0 = fmaxf(m0, a), n1 = fmaxf(m1, b);
-        const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
-        const float c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 *= c0, z0 *= c0, l1 *= c1, z1 *= c1;
-        float cv = 1.f;
-        if (v > v_ref) {
-          // a power of two above v, and at least 2^-100
+        const float n0 = fmaxf(-nm.x, a), n1 = fmaxf(-nm.y, b);
+        float2 c = make_float2(ex2(-nm.x - n0), ex2(-nm.y - n1));
+        nm = make_float2(-n0, -n1);
+        l2 = __fmul2_rn(l2, c);
+        z2 = __fmul2_rn(z2, c);
+        if (vtop > v_ref) {
+          // a power of two above it, and at least 2^-100
           const float up = fmaxf(
-              __uint_as_float((__float_as_uint(v) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
-          cv = v_ref / up;
+              __uint_as_float((__float_as_uint(vtop) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
+          c = __fmul2_rn(c, make_float2(v_ref / up, v_ref / up));
           v_ref = up;
           v_inv = 128.f / up;
         }
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
-          o[k][0] *= c0 * cv;
-          o[k][1] *= c1 * cv;
-          o[k][2] *= c0 * cv;
-          o[k][3] *= c1 * cv;
+          o[k][0] *= c.x;
+          o[k][1] *= c.y;
+          o[k][2] *= c.x;
+          o[k][3] *= c.y;
         }
+#pragma unroll
+        for (int u = 0; u < 2 * kPair; ++u) d[u] = __fadd2_rn(s[u], nm);
       }
-      // A row with no key so far keeps m = -inf: its weights are 0, not e^(-inf + inf).
-      const float a0 = m0 == -INFINITY ? 0.f : m0, a1 = m1 == -INFINITY ? 0.f : m1;
-      const float p0 = ex2(s[0] - a0), p1 = ex2(s[1] - a1);
-      const float p2 = ex2(s[2] - a0), p3 = ex2(s[3] - a1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      z0 = fmaf(p0, v0.y, fmaf(p2, v1.y, z0));
-      z1 = fmaf(p1, v0.y, fmaf(p3, v1.y, z1));
-      const float x0 = v0.x * v_inv, x1 = v1.x * v_inv;
-      const float w0a = p0 * x0, w1a = p1 * x0, w2a = p2 * x1, w3a = p3 * x1;
-      const uint32_t ha = pack2<false>(w0a, w1a), hb = pack2<false>(w2a, w3a);
-      const float2 ra = unpack2<false>(ha), rb = unpack2<false>(hb);
-      const uint32_t la = pack2<false>(w0a - ra.x, w1a - ra.y);
-      const uint32_t lb = pack2<false>(w2a - rb.x, w3a - rb.y);
-      uint32_t b0, b1, b2 = 0, b3 = 0;
-      if constexpr (WIDE) {
-        b0 = transpose8x8(ha), b1 = transpose8x8(hb);
-        b2 = transpose8x8(la), b3 = transpose8x8(lb);
-      } else {
-        b0 = transpose8x8(lc < 2 ? ha : la), b1 = transpose8x8(lc < 2 ? hb : lb);
+
+      // ---- weights, as the second product's operand
+      uint32_t hi[2 * kPair], lo[2 * kPair];
+#pragma unroll
+      for (int u = 0; u < 2 * kPair; ++u) {
+        const float2 pr = make_float2(ex2(d[u].x), ex2(d[u].y));
+        l2 = __fadd2_rn(l2, pr);
+        z2 = __ffma2_rn(pr, make_float2(v[u].y, v[u].y), z2);
+        const float x = v[u].x * v_inv;
+        const float2 wt = __fmul2_rn(pr, make_float2(x, x));
+        const uint32_t head = pack2<false>(wt.x, wt.y);
+        const float2 back = unpack2<false>(head);
+        if constexpr (WIDE) {
+          hi[u] = transpose8x8(head);
+          lo[u] = transpose8x8(pack2<false>(wt.x - back.x, wt.y - back.y));
+        } else {  // the head term again, or the remainder
+          const float2 mine = __ffma2_rn(make_float2(rem, rem), back, wt);
+          hi[u] = transpose8x8(pack2<false>(mine.x, mine.y));
+          lo[u] = 0;
+        }
       }
 
       // ---- O[dimension][row] += V^T P
 #pragma unroll
-      for (int j = 0; j < VW; ++j)
+      for (int pg = 0; pg < kPair; ++pg) {
+        const uint32_t col = st + pg * L::kBlock + kv4::code_offset(D, 1, 0) + 4 * VW * ln;
+        uint32_t va[4][VW];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // nibbles 4 h .. 4 h + 3 of two tokens' words, one token a half
-          const uint32_t x = __byte_perm(va[0][j], va[1][j], h ? 0x7632 : 0x5410);
-          const uint32_t y = __byte_perm(va[2][j], va[3][j], h ? 0x7632 : 0x5410);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t xs = x >> (8 * u), ys = y >> (8 * u);
-            const uint32_t a[4] = {sub_1032((xs & 0x000f000fu) | 0x64006400u),
-                                   sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u),
-                                   sub_1032((ys & 0x000f000fu) | 0x64006400u),
-                                   sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u)};
-            float (&ok)[4] = o[4 * j + 2 * h + u];
-            if constexpr (WIDE) {
-              float t[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<false>(t, a, b2, b3);
-              mma16816<false>(t, a, b0, b1);
-              ok[0] += t[0], ok[1] += t[1], ok[2] += t[2], ok[3] += t[3];
-            } else {
-              mma16816<false>(ok, a, b0, b1);
-            }
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t at = col + (u & 1 ? t1 : t0) + 8 * (u >> 1) * kv4::row_bytes(D);
+          if constexpr (VW == 2) {
+            const uint2 x = lds64(at);
+            va[u][0] = x.x, va[u][1] = x.y;
+          } else {
+            va[u][0] = lds32(at);
           }
         }
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // nibbles 4 h .. 4 h + 3 of two tokens' words, one token a half
+            const uint32_t x = __byte_perm(va[0][j], va[1][j], h ? 0x7632 : 0x5410);
+            const uint32_t y = __byte_perm(va[2][j], va[3][j], h ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t xs = x >> (8 * u), ys = y >> (8 * u);
+              const uint32_t a[4] = {sub_1032((xs & 0x000f000fu) | 0x64006400u),
+                                     sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u),
+                                     sub_1032((ys & 0x000f000fu) | 0x64006400u),
+                                     sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u)};
+              float (&ok)[4] = o[4 * j + 2 * h + u];
+              if constexpr (WIDE) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<false>(t, a, lo[2 * pg], lo[2 * pg + 1]);
+                mma16816<false>(t, a, hi[2 * pg], hi[2 * pg + 1]);
+                ok[0] += t[0], ok[1] += t[1], ok[2] += t[2], ok[3] += t[3];
+              } else {
+                mma16816<false>(ok, a, hi[2 * pg], hi[2 * pg + 1]);
+              }
+            }
+          }
+      }
+      __syncwarp();  // the stage has been read by every lane
+      if (i + kStages < ring.n) ring.issue(i + kStages, lane, p);
     }
 
     // ---- the warp's state to shared memory: O is O[d = (D / 8) ln + 2 k + {0, 1}]
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
-      l0 += __shfl_xor_sync(kFull, l0, x);
-      l1 += __shfl_xor_sync(kFull, l1, x);
-      z0 += __shfl_xor_sync(kFull, z0, x);
-      z1 += __shfl_xor_sync(kFull, z1, x);
+      l2.x += __shfl_xor_sync(kFull, l2.x, x);
+      l2.y += __shfl_xor_sync(kFull, l2.y, x);
+      z2.x += __shfl_xor_sync(kFull, z2.x, x);
+      z2.y += __shfl_xor_sync(kFull, z2.y, x);
     }
+    __syncthreads();  // every warp is done with the ring
     const float back = v_ref * 0x1p-7f;
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
@@ -565,16 +612,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       if (WIDE || lc < 2) {
         float *dst = mer_o + (warp * kTile + 2 * lc) * L::kRowStride + (D / 8) * ln + 2 * k;
         *reinterpret_cast<float2 *>(dst) =
-            make_float2(fmaf(a.x, back, z0), fmaf(a.y, back, z0));
+            make_float2(fmaf(a.x, back, z2.x), fmaf(a.y, back, z2.x));
         *reinterpret_cast<float2 *>(dst + L::kRowStride) =
-            make_float2(fmaf(b.x, back, z1), fmaf(b.y, back, z1));
+            make_float2(fmaf(b.x, back, z2.y), fmaf(b.y, back, z2.y));
       }
     }
     if (ln == 0 && (WIDE || lc < 2)) {
-      mer_m[warp * kTile + 2 * lc] = m0;
-      mer_m[warp * kTile + 2 * lc + 1] = m1;
-      mer_l[warp * kTile + 2 * lc] = l0;
-      mer_l[warp * kTile + 2 * lc + 1] = l1;
+      mer_m[warp * kTile + 2 * lc] = -nm.x;
+      mer_m[warp * kTile + 2 * lc + 1] = -nm.y;
+      mer_l[warp * kTile + 2 * lc] = l2.x;
+      mer_l[warp * kTile + 2 * lc + 1] = l2.y;
     }
     __syncthreads();
 
@@ -595,7 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     };
     for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
       const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      float M = -INFINITY;
+      float M = kNoKey;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) M = fmaxf(M, mer_m[k * kTile + r]);
       float l = 0.f;
@@ -603,7 +650,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float lk = mer_l[k * kTile + r];
-        const float f = M == -INFINITY ? 1.f : ex2(mer_m[k * kTile + r] - M);
+        const float f = ex2(mer_m[k * kTile + r] - M);
         const float4 v =
             *reinterpret_cast<const float4 *>(mer_o + (k * kTile + r) * L::kRowStride + d);
         l = fmaf(f, lk, l);
@@ -632,7 +679,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       if (*s_last) {
         for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
           const int r = e / (D / 4), d = 4 * (e % (D / 4));
-          float m = -INFINITY, l = 0.f;
+          float m = kNoKey, l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           constexpr int kBatch = 4;
           for (int c = first; c <= last; c += kBatch) {
@@ -649,8 +696,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
             for (int u = 0; u < kBatch; ++u)
               if (c + u <= last && ml[u].y != 0.f) {
                 const float mn = fmaxf(m, ml[u].x);
-                const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
-                const float f = mn == -INFINITY ? 1.f : ex2(ml[u].x - mn);
+                const float a = ex2(m - mn), f = ex2(ml[u].x - mn);
                 acc.x = fmaf(acc.x, a, v[u].x * f);
                 acc.y = fmaf(acc.y, a, v[u].y * f);
                 acc.z = fmaf(acc.z, a, v[u].z * f);
@@ -665,7 +711,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       }
     }
     if (!part.more) break;
-    __syncthreads();  // the merge area is free, and the next part is planned
+    fence_proxy_async_smem();  // the merge area's last reads, before copies over it
+    __syncthreads();           // ... and the next part is planned
   }
 }
 
