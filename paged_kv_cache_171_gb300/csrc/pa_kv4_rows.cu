@@ -39,12 +39,13 @@
 // product's operand (row, token) by movmatrix.
 //
 // Work split.  The pages of all (sequence, kv head, row tile) items, laid end to
-// end, are cut into equal runs, one a CTA, as many CTAs as fit the GPU at once:
-// a ragged batch takes the time of its pages, not of its longest sequence.  A
-// CTA's 4 warps take its run's pages in turn, each with its own ring of stages
-// filled by bulk copies, and merge their (m, l, O) states when an item ends.  An
-// item cut between CTAs leaves one state a CTA, and the last of them to arrive
-// merges them in order of position, so results do not depend on timing.
+// end, are cut into equal runs: a ragged batch takes the time of its pages, not of
+// its longest sequence.  A run belongs to a team of 4 warps, and an SM holds 4
+// teams in one CTA, so that they can keep step (below).  A team's warps take its
+// run's pages two by two in turn, each with its own ring of stages filled by bulk
+// copies, and merge their (m, l, O) states when an item ends.  An item cut between
+// teams leaves one state a team, folded in order of position by a second kernel
+// (results do not depend on timing).
 #include "pa_device.cuh"
 #include "pa_kv4.cuh"
 
@@ -55,18 +56,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleSlack = 8.0f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
-constexpr int kWarps = 4, kStages = 3, kTile = 8;  // query rows a tile
+constexpr int kWarps = 4, kStages = 2, kTile = 8;  // query rows a tile
 constexpr int kPair = 2;         // pages a stage holds
-constexpr int kCtasPerSm = 4;
-constexpr int kMinPages = kWarps * kPair;  // least pages a CTA takes
+constexpr int kTeams = 4;        // teams of kWarps warps a CTA, one CTA an SM
+constexpr int kMinPages = kWarps * kPair;  // least pages a team takes
+constexpr uint32_t kLead = 2;         // chunks a warp may be ahead of the slowest team
 
 struct RowsParams {
   const uint16_t *q;
   const uint8_t *cache;
   const int32_t *block_table, *ctx_lens;
   void *out;
-  float *ws;     // [CTA][2][kTile][D + 4] partial states
-  int *ctr;      // [CTA] arrivals of the item that starts in the CTA's run and leaves it
+  float *ws;     // [team][2][kTile][D + 4] partial states
+  int4 *cut;     // [team][2] the item that starts in the team's run and leaves it
   int *status;
   float qscale;  // scale * log2 e
   int n_new, queries, n_q_heads, n_kv_heads, group, batch, max_blocks, num_pages;
@@ -79,18 +81,21 @@ struct RowsSmem {
   static constexpr int kBlock = kv4::block_bytes(D);
   static constexpr int kStage = kPair * kBlock;
   static constexpr int kRing = kWarps * kStages * kStage;
-  // The warps' states at the end of a part, over the ring: no copy is in flight then.
   static constexpr int kRowStride = D + 4;  // floats a merged row
-  static constexpr int kMergeO = 0;
+  static constexpr int kMergeO = kRing;
   static constexpr int kMergeM = kMergeO + kWarps * kTile * kRowStride * 4;
   static constexpr int kMergeL = kMergeM + kWarps * kTile * 4;
-  static_assert(kMergeL + kWarps * kTile * 4 <= kRing, "merge area must fit in the ring");
-  static constexpr int kBars = kRing;
-  static constexpr int kParts = kBars + kWarps * kStages * 8;  // Part[2]
-  static constexpr int kWalk = kParts + 2 * 64;                // Walk
-  static constexpr int kLast = kWalk + 64;
-  static constexpr int kBytes = kLast + 16;
-  static_assert(kBlock % 16 == 0 && kBars % 8 == 0 && kParts % 16 == 0, "alignment");
+  static constexpr int kQ = kMergeL + kWarps * kTile * 4;      // [2][kTile][D], 16 bits
+  static constexpr int kBars = kQ + 2 * kTile * D * 2;
+  static constexpr int kParts = kBars + kWarps * kStages * 8;  // Part[4]
+  static constexpr int kWalk = kParts + 4 * 64;                // Walk
+  static constexpr int kFlags = kWalk + 64;
+  static constexpr int kTeam = (kFlags + 64 + 127) & ~127;     // all of the above, a team
+  static constexpr int kDone = kTeams * kTeam;  // chunks done, a team's first warp's
+  static constexpr int kBytes = kDone + kTeams * 4;
+  static_assert(kBlock % 128 == 0 && kQ % 16 == 0 && kBars % 8 == 0 && kParts % 16 == 0,
+                "alignment");
+  static_assert(kTeam % 128 == 0 && kBytes <= 232448, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
@@ -118,6 +123,16 @@ __device__ __forceinline__ uint32_t sixteenth_sub_72(uint32_t x) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// d = a b, the accumulator starting at zero.
+__device__ __forceinline__ void mma_from_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Physical token of score row r < 8 (row r + 8: 8 more).  The order makes the
 // rows that neighbouring lanes read from a stage alternate between its even and
 // odd rows, which is what shared memory's 32 banks want of 64-byte rows.
@@ -126,59 +141,175 @@ __device__ __forceinline__ int token_of(int r) {
   return (r & 1) ? 4 * a + 3 - b : 4 * a + b;
 }
 
-// One warp's ring of stages of two pages.  Chunk i of an item's part is pages
-// kWarps kPair i and the one behind it of bt_row (the last may be one page);
-// `issued` and `waited` number the chunks over the CTA's whole run, which gives
-// the stage and the parity.
+// The part of one item that a team's run holds.
+struct Part {
+  int b, g;           // sequence, kv head
+  int r0, n_r;        // rows of the kv head
+  int pg0, n_pg;      // pages
+  int tokens;         // keys of the sequence, the chunk's included
+  int first, last;    // teams that hold the item
+  int slot;           // of the first one's state: 0 when the item starts its run
+  int more;           // the run goes on behind this part
+};
+static_assert(sizeof(Part) <= 64, "room in shared memory");
+
+// The team's run [w, w1) of the flattened page list, walked part by part by one
+// thread, which keeps the others' registers free of it.
+struct Walk {
+  int64_t w, w1, run, base;  // base: pages of one (kv head, row tile) before sequence b
+  int b, n_b, tokens;        // the sequence, its pages and its tokens
+
+  // Tokens of sequence b, the chunk's included (a clamped length is reported by
+  // the first team's scan).
+  static __device__ int tokens_of(const RowsParams &p, int b, bool report) {
+    const int most = p.max_blocks * kPageSize - p.n_new;
+    int t = __ldg(p.ctx_lens + b);
+    if (t < 0 || t > most) {
+      if (report) record_error(p.status, PA_ERR_BAD_CTX);
+      t = t < 0 ? 0 : most;
+    }
+    return t + p.n_new;
+  }
+  // An empty sequence counts one page, so that someone writes its zeros.
+  static __device__ int pages_of(int tokens) {
+    return max(1, (tokens + kPageSize - 1) / kPageSize);
+  }
+  // 64-bit division only where 32 bits do not hold the operands.
+  static __device__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+  }
+  // The whole warp: lane l sums the pages of sequences [l per, (l + 1) per), and a
+  // scan finds the sequence in which the team's run starts.  False: no run.
+  // Warp-uniform results; lane 0 keeps them in *out.
+  static __device__ bool start(const RowsParams &p, int team, int n_teams, int lane, Walk *out) {
+    Walk x;
+    const int heads = p.n_kv_heads * p.n_sub;
+    const int per = (p.batch + 31) / 32;
+    const int b0 = min(p.batch, lane * per), b1 = min(p.batch, b0 + per);
+    int64_t sum = 0;
+    int tokens = 0;  // of sequence b0
+#pragma unroll 4
+    for (int i = b0; i < b1; ++i) {
+      const int t = tokens_of(p, i, team == 0);
+      sum += pages_of(t);
+      if (i == b0) tokens = t;
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t total = __shfl_sync(kFull, incl, 31) * heads;
+    x.run = max(quotient(total + n_teams - 1, n_teams), static_cast<int64_t>(kMinPages));
+    x.w = team * x.run;
+    x.w1 = min(total, x.w + x.run);
+    if (x.w >= x.w1) return false;
+    const int src = __ffs(__ballot_sync(kFull, incl * heads > x.w)) - 1;
+    x.b = __shfl_sync(kFull, b0, src);
+    x.base = __shfl_sync(kFull, incl - sum, src);
+    x.tokens = __shfl_sync(kFull, tokens, src);
+    x.n_b = pages_of(x.tokens);
+    if (lane == 0) *out = x;
+    return true;
+  }
+  __device__ void next(const RowsParams &p, volatile Part &s) {
+    const int heads = p.n_kv_heads * p.n_sub;
+    while ((base + n_b) * heads <= w) {
+      base += n_b;
+      tokens = tokens_of(p, ++b, false);
+      n_b = pages_of(tokens);
+    }
+    const int64_t rel = w - base * heads;
+    const int item = static_cast<int>(quotient(rel, n_b));
+    const int pg0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
+    const int n_pg = static_cast<int>(min(static_cast<int64_t>(n_b - pg0), w1 - w));
+    const int64_t i0 = w - pg0;  // the item's first page
+    const int g = item / p.n_sub, sub = item - g * p.n_sub;
+    const int first = static_cast<int>(quotient(i0, run));
+    s.b = b;
+    s.g = g;
+    s.r0 = sub * p.tile_rows;
+    s.n_r = min(p.tile_rows, p.n_rows - sub * p.tile_rows);
+    s.pg0 = pg0;
+    s.n_pg = n_pg;
+    s.tokens = tokens;
+    s.first = first;
+    s.last = static_cast<int>(quotient(i0 + n_b - 1, run));
+    s.slot = i0 == first * run ? 0 : 1;
+    w += n_pg;
+    s.more = w < w1;
+  }
+};
+
+// One warp's ring of stages of two pages and the cursor that feeds it, which runs
+// up to kStages chunks ahead of the page math and into the next part: the copies
+// of a part's first pages are in flight while the part before it is merged.
+// Chunk i of a part is, for warp w, pages kPair (kWarps i + w) and the one behind
+// it (the last may be one page).  `issued` and `waited` number the chunks over the
+// team's whole run, which gives the stage and the parity.
 template <int D>
-struct BlockRing {
+struct Feed {
   static constexpr int kBlock = kv4::block_bytes(D);
   uint32_t stage0, bar0;
   const uint8_t *cache;    // the kv head's block of page 0
   const int32_t *bt_row;   // the warp's first page of the part
-  int n, pages;            // chunks of the warp; pages of the part from bt_row on
+  int i, n, pages;         // next chunk, chunks, pages of the part from bt_row on
   int ids_cur, ids_nxt;
   uint32_t issued, waited;  // chunks over the whole run
 
   // Lane l holds the id of page l & 1 of chunk 16 w + (l >> 1), w the window.
-  __device__ int fetch_id(int w, int lane) const {
+  static __device__ int fetch_ids(const int32_t *row, int pages, int w, int lane) {
     const int pg = kWarps * kPair * (16 * w + (lane >> 1)) + (lane & 1);
-    return pg < pages ? __ldg(bt_row + pg) : 0;
+    return pg < pages ? __ldg(row + pg) : 0;
   }
-  __device__ void start(int lane) {
-    ids_cur = fetch_id(0, lane);
-    ids_nxt = n > 16 ? fetch_id(1, lane) : 0;
+  static __device__ const int32_t *row_of(const RowsParams &p, const volatile Part &s, int warp) {
+    return p.block_table + static_cast<size_t>(s.b) * p.max_blocks + s.pg0 + kPair * warp;
   }
-  // Called by the whole warp with i = 0, 1, 2, ... of the part's chunks.
-  __device__ void issue(int i, int lane, const RowsParams &p) {
+  // Pages from this warp's first one on; none of an empty sequence's.
+  static __device__ int pages_of(const volatile Part &s, int warp) {
+    return s.tokens > 0 ? s.n_pg - kPair * warp : 0;
+  }
+  static __device__ int chunks_of(const volatile Part &s, int warp) {
+    return max(0, (pages_of(s, warp) + kWarps * kPair - 1) / (kWarps * kPair));
+  }
+  // Turns to part s, whose first window of page ids is at hand.
+  __device__ void turn_to(const RowsParams &p, const volatile Part &s, int ids, int warp,
+                          int lane) {
+    cache = p.cache + static_cast<size_t>(s.g) * kBlock;
+    bt_row = row_of(p, s, warp);
+    pages = pages_of(s, warp);
+    n = chunks_of(s, warp);
+    i = 0;
+    ids_cur = ids;
+    ids_nxt = n > 16 ? fetch_ids(bt_row, pages, 1, lane) : 0;
+  }
+  // The whole warp: the next chunk of the part (i < n) into its stage.
+  __device__ void issue(const RowsParams &p, int lane) {
     if ((i & 15) == 0 && i > 0) {
       ids_cur = ids_nxt;
-      ids_nxt = fetch_id((i >> 4) + 1, lane);
+      ids_nxt = fetch_ids(bt_row, pages, (i >> 4) + 1, lane);
     }
-    int id0 = __shfl_sync(kFull, ids_cur, 2 * (i & 15));
-    int id1 = __shfl_sync(kFull, ids_cur, 2 * (i & 15) + 1);
-    if (lane == 0) {
-      const bool two = kWarps * kPair * i + 1 < pages;
-      if (static_cast<unsigned>(id0) >= static_cast<unsigned>(p.num_pages) ||
-          static_cast<unsigned>(id1) >= static_cast<unsigned>(p.num_pages)) {
+    // lanes 0 and 1 copy a page each
+    int id = __shfl_sync(kFull, ids_cur, 2 * (i & 15) + (lane & 1));
+    const int here = min(2, pages - kWarps * kPair * i);
+    if (lane < here) {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
         record_error(p.status, PA_ERR_BAD_BLOCK);
-        id0 = id1 = 0;  // read a page that exists; the result is flagged as invalid
+        id = 0;  // read a page that exists; the result is flagged as invalid
       }
       const uint32_t s = issued % kStages, bar = bar0 + 8 * s;
-      const uint32_t dst = stage0 + s * (kPair * kBlock);
       fence_proxy_async_smem();
-      mbar_arrive_expect_tx(bar, two ? 2 * kBlock : kBlock);
-      bulk_load(dst, cache + static_cast<uint64_t>(static_cast<uint32_t>(id0)) * p.page_bytes,
-                kBlock, bar);
-      if (two)
-        bulk_load(dst + kBlock,
-                  cache + static_cast<uint64_t>(static_cast<uint32_t>(id1)) * p.page_bytes,
-                  kBlock, bar);
+      if (lane == 0) mbar_arrive_expect_tx(bar, here * kBlock);
+      bulk_load(stage0 + s * (kPair * kBlock) + lane * kBlock,
+                cache + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes, kBlock,
+                bar);
     }
+    ++i;
     ++issued;
   }
   // Warp-uniform wait for the next chunk; its stage, or 0 when the wait ran out.
-  __device__ uint32_t wait(int lane, const RowsParams &p) {
+  __device__ uint32_t wait(const RowsParams &p, int lane) {
     const uint32_t s = waited % kStages, par = (waited / kStages) & 1;
     ++waited;
     if (__all_sync(kFull, mbar_wait(bar0 + 8 * s, par))) return stage0 + s * (kPair * kBlock);
@@ -189,132 +320,133 @@ struct BlockRing {
   }
 };
 
-// The part of one item that a CTA's run holds.
-struct Part {
-  int b, g;           // sequence, kv head
-  int r0, n_r;        // rows of the kv head
-  int pg0, n_pg;      // pages
-  int tokens;         // keys of the sequence, the chunk's included
-  int first, last;    // CTAs that hold the item
-  int slot;           // of the first one's state: 0 when the item starts its run
-  int more;           // the run goes on behind this part
-};
-static_assert(sizeof(Part) <= 64, "room in shared memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
-// The CTA's run [w, w1) of the flattened page list, walked part by part by one
-// thread, which keeps the others' registers free of it.
-struct Walk {
-  int64_t w, w1, run, base;  // base: pages of one (kv head, row tile) before sequence b
-  int b, n_b;
-
-  // Tokens of sequence b, the chunk's included (a clamped length is reported by
-  // the first CTA's scan).
-  static __device__ int tokens(const RowsParams &p, int b, bool report) {
-    const int most = p.max_blocks * kPageSize - p.n_new;
-    int t = __ldg(p.ctx_lens + b);
-    if (t < 0 || t > most) {
-      if (report) record_error(p.status, PA_ERR_BAD_CTX);
-      t = t < 0 ? 0 : most;
-    }
-    return t + p.n_new;
-  }
-  // An empty sequence counts one page, so that someone writes its zeros.
-  static __device__ int pages(int tokens) {
-    return max(1, (tokens + kPageSize - 1) / kPageSize);
-  }
-  // The whole warp: lane l sums the pages of sequences [l per, (l + 1) per), and a
-  // scan finds the sequence in which this CTA's run starts.  False: no run.
-  // Warp-uniform results; lane 0 keeps them in *out.
-  static __device__ bool start(const RowsParams &p, int lane, Walk *out) {
-    Walk x;
-    const int heads = p.n_kv_heads * p.n_sub;
-    const int per = (p.batch + 31) / 32;
-    const int b0 = min(p.batch, lane * per), b1 = min(p.batch, b0 + per);
-    int64_t sum = 0;
-#pragma unroll 4
-    for (int i = b0; i < b1; ++i) sum += pages(tokens(p, i, blockIdx.x == 0));
-    int64_t incl = sum;
+// The kWarps states of each of n_r rows in shared memory, merged by the exponent
+// law; fn(row, first of 4 dimensions, O, m, l).
+template <int D, class Fn>
+__device__ __forceinline__ void merge_rows(const float *o, const float *m, const float *l, int n_r,
+                                           int tid, Fn fn) {
+  for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
+    const int r = e / (D / 4), d = 4 * (e % (D / 4));
+    float M = kNoKey;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += v;
+    for (int k = 0; k < kWarps; ++k) M = fmaxf(M, m[k * kTile + r]);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const float f = ex2(m[k * kTile + r] - M);
+      const float4 v =
+          *reinterpret_cast<const float4 *>(o + (k * kTile + r) * RowsSmem<D>::kRowStride + d);
+      sum = fmaf(f, l[k * kTile + r], sum);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
     }
-    const int64_t total = __shfl_sync(kFull, incl, 31) * heads;
-    x.run = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinPages));
-    x.w = blockIdx.x * x.run;
-    x.w1 = min(total, x.w + x.run);
-    if (x.w >= x.w1) return false;
-    const int src = __ffs(__ballot_sync(kFull, incl * heads > x.w)) - 1;
-    x.b = __shfl_sync(kFull, b0, src);
-    x.base = __shfl_sync(kFull, incl - sum, src);
-    x.n_b = pages(tokens(p, x.b, false));
-    if (lane == 0) *out = x;
-    return true;
+    fn(r, d, acc, M, sum);
   }
-  __device__ void next(const RowsParams &p, volatile Part &s) {
-    const int heads = p.n_kv_heads * p.n_sub;
-    while ((base + n_b) * heads <= w) {
-      base += n_b;
-      n_b = pages(tokens(p, ++b, false));
-    }
-    const int64_t rel = w - base * heads;
-    const int item = static_cast<int>(rel / n_b);
-    const int pg0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
-    const int n_pg = static_cast<int>(min(static_cast<int64_t>(n_b - pg0), w1 - w));
-    const int64_t i0 = w - pg0;  // the item's first page
-    s.b = b;
-    s.g = item / p.n_sub;
-    s.r0 = (item % p.n_sub) * p.tile_rows;
-    s.n_r = min(p.tile_rows, p.n_rows - (item % p.n_sub) * p.tile_rows);
-    s.pg0 = pg0;
-    s.n_pg = n_pg;
-    s.tokens = tokens(p, b, false);
-    s.first = static_cast<int>(i0 / run);
-    s.last = static_cast<int>((i0 + n_b - 1) / run);
-    s.slot = i0 % run == 0 ? 0 : 1;
-    w += n_pg;
-    s.more = w < w1;
-  }
-};
+}
+
+// O / l to the result's row; zeros when no key was seen (NaN stays NaN).
+template <int D, bool BF16, bool OUT16>
+__device__ __forceinline__ void store_row(const RowsParams &p, size_t row, int d, float4 v,
+                                          float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if constexpr (OUT16)
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * D + d) =
+        make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
+  else
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D + d) = v;
+}
+
+// Team c's state of an item: slot 0 when its part starts the team's run.
+template <int D>
+__device__ __forceinline__ float *state_of(const RowsParams &p, const volatile Part &s, int c) {
+  const int slot = c > s.first ? 0 : s.slot;
+  return p.ws + (static_cast<size_t>(c) * 2 + slot) * kTile * (D + 4);
+}
+
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kWarps * 32) : "memory");
+}
 
 template <int D, bool BF16, bool WIDE, bool OUT16>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+__global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
     kv4_rows_kernel(const RowsParams p) {
   using L = RowsSmem<D>;
   constexpr int MT = D / 16;   // row tiles of the second product (head dimensions)
   constexpr int KW = D / 32;   // 32-bit words of K codes a thread holds per token
   constexpr int VW = D / 64;   // of V codes
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  // a team is a unit of its own from here on: own shared memory, own barrier
+  const int team = threadIdx.x / (kWarps * 32), tid = threadIdx.x % (kWarps * 32);
+  const int team_id = blockIdx.x * kTeams + team;
+  uint8_t *smem = smem_all + team * L::kTeam;
+  volatile uint32_t *done = reinterpret_cast<volatile uint32_t *>(smem_all + L::kDone);
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = tid & 31, warp = tid >> 5;
   const int ln = lane >> 2, lc = lane & 3;
 
   if (tid == 0) {
     for (int s = 0; s < kWarps * kStages; ++s) mbar_init(sb + L::kBars + 8 * s, 1);
     fence_mbar_init();
+    done[team] = 0;
   }
-  griddep_release();
   griddep_wait();  // inputs may come from the previous kernel in the stream
+  griddep_release();
   __syncthreads();
 
   volatile Part *parts = reinterpret_cast<volatile Part *>(smem + L::kParts);
-  volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::kLast);
+  volatile int *flags = reinterpret_cast<volatile int *>(smem + L::kFlags);
   Walk *walk = reinterpret_cast<Walk *>(smem + L::kWalk);
-  if (warp == kWarps - 1) {  // the warp with the fewest pages plans
-    const bool any = Walk::start(p, lane, walk);
+  if (warp == kWarps - 1) {  // the warp with the fewest pages plans, two parts ahead
+    const bool any = Walk::start(p, team_id, gridDim.x * kTeams, lane, walk);
     if (lane == 0) {
-      if (any) walk->next(p, parts[0]);
-      *s_last = any;
+      if (any) {
+        walk->next(p, parts[0]);
+        if (parts[0].more) walk->next(p, parts[1]);
+      } else {
+        done[team] = 0x7fffffff;
+        p.cut[2 * team_id] = make_int4(0, 0, 0, 0);
+      }
+      flags[0] = any;
     }
   }
-  __syncthreads();
-  if (!*s_last) return;
+  team_sync(team);
+  if (!flags[0]) return;
 
-  BlockRing<D> ring;
-  ring.stage0 = sb + warp * kStages * L::kStage;
-  ring.bar0 = sb + L::kBars + warp * kStages * 8;
-  ring.issued = ring.waited = 0;
+  // row r of a part's kv head: query r / G, head r % G
+  auto q_row = [&](const volatile Part &s, int r) {
+    return (static_cast<size_t>(s.b) * p.queries + r / p.group) * p.n_q_heads + s.g * p.group +
+           r % p.group;
+  };
+  // a part's q rows to shared memory, 16 bytes a thread
+  auto load_q = [&](const volatile Part &s, int buf) {
+    constexpr int kChunks = D / 8;
+    if (tid < s.n_r * kChunks)
+      cp_async16(sb + L::kQ + buf * (kTile * D * 2) + tid * 16,
+                 p.q + q_row(s, s.r0 + tid / kChunks) * D + (tid % kChunks) * 8);
+  };
+
+  Feed<D> feed;
+  feed.stage0 = sb + warp * kStages * L::kStage;
+  feed.bar0 = sb + L::kBars + warp * kStages * 8;
+  feed.issued = feed.waited = 0;
   bool alive = true;  // false once a wait of this warp has run out
+  feed.turn_to(p, parts[0],
+               Feed<D>::fetch_ids(Feed<D>::row_of(p, parts[0], warp),
+                                  Feed<D>::pages_of(parts[0], warp), 0, lane),
+               warp, lane);
+  load_q(parts[0], 0);
+  for (int k = 0; k < kStages && feed.i < feed.n; ++k) feed.issue(p, lane);
 
   float *mer_o = reinterpret_cast<float *>(smem + L::kMergeO);
   float *mer_m = reinterpret_cast<float *>(smem + L::kMergeM);
@@ -323,28 +455,32 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   // V rows of the tokens that score rows 2 lc and 2 lc + 1 stand for
   const int t0 = token_of(2 * lc) * kv4::row_bytes(D);
   const int t1 = token_of(2 * lc + 1) * kv4::row_bytes(D);
+  cp_async_wait();
+  team_sync(team);
+  uint32_t chunks_done = 0;
 
-  for (int turn = 0;; turn ^= 1) {
-    volatile Part &part = parts[turn];
-    const int first_page = part.pg0 + kPair * warp;
-    int key0 = first_page * kPageSize;  // of the chunk at hand
-    {
-      const int b = part.b;
-      ring.bt_row = p.block_table + static_cast<size_t>(b) * p.max_blocks + first_page;
-      ring.cache = p.cache + static_cast<size_t>(part.g) * L::kBlock;
-      ring.pages = part.tokens > 0 && alive ? part.n_pg - kPair * warp : 0;
-      ring.n = max(0, (ring.pages + kWarps * kPair - 1) / (kWarps * kPair));
+  for (int turn = 0;; ++turn) {
+    const volatile Part &part = parts[turn & 3];
+    const volatile Part &then = parts[(turn + 1) & 3];
+    int key0 = (part.pg0 + kPair * warp) * kPageSize;  // of the chunk at hand
+    const int n_chunks = Feed<D>::chunks_of(part, warp);
+    bool ahead = false;  // the feed has turned to the next part
+    int ids_then = 0;
+    if (part.more) {
+      ids_then = Feed<D>::fetch_ids(Feed<D>::row_of(p, then, warp),
+                                    Feed<D>::pages_of(then, warp), 0, lane);
+      load_q(then, (turn + 1) & 1);
+      if (tid == (kWarps - 1) * 32 && then.more) walk->next(p, parts[(turn + 2) & 3]);
     }
-    ring.start(lane);
-    for (int i = 0; i < kStages && i < ring.n; ++i) ring.issue(i, lane, p);
-    if (tid == (kWarps - 1) * 32 && part.more) walk->next(p, parts[turn ^ 1]);
+    // up to kStages chunks ahead, into the next part if need be
+    auto feed_on = [&]() {
+      if (ahead || !part.more) return;
+      feed.turn_to(p, then, ids_then, warp, lane);
+      ahead = true;
+      while (feed.i < feed.n && feed.issued - feed.waited < kStages) feed.issue(p, lane);
+    };
 
     // ---- q of this lane's column as the first product's operand
-    // row r of the kv head: query r / G, head r % G
-    auto q_row = [&](int r) {
-      return (static_cast<size_t>(part.b) * p.queries + r / p.group) * p.n_q_heads +
-             part.g * p.group + r % p.group;
-    };
     const int n_r = part.n_r;
     uint32_t qb[2 * KW][2];
     float f0, f1, e0, e1;  // per column 2 lc, 2 lc + 1: score factor, scaled sum of q
@@ -352,11 +488,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       const int col = WIDE ? ln : (ln & 3);
       float x[8 * KW];
       if (col < n_r) {
-        const uint4 *src4 =
-            reinterpret_cast<const uint4 *>(p.q + q_row(part.r0 + col) * D + (D / 4) * lc);
+        const uint32_t row =
+            sb + L::kQ + (turn & 1) * (kTile * D * 2) + col * (D * 2) + lc * (D / 2);
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
-          const uint4 v = __ldg(src4 + k);
+          const uint4 v = lds128(row + 16 * k);
           const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -407,16 +543,26 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     float2 nm = make_float2(-kNoKey, -kNoKey);
     float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
     float v_ref = 0.f, v_inv = 0.f;  // reference of scale_v (a power of two), 2^7 / it
-    const float2 f2 = make_float2(f0, f1), e2 = make_float2(e0, e1);
-    const float2 e8 = make_float2(-8.f * e0, -8.f * e1);
     const float rem = lc < 2 ? 0.f : -1.f;  // this lane's columns carry remainder terms
 
     // Keys that every row of the tile sees and this part holds end here.
     const int part_end = (part.pg0 + part.n_pg) * kPageSize;
     const int lim_all = min(part_end, OUT16 ? part.tokens - p.n_new + 1 + part.r0 / p.group
                                             : part.tokens);
-    for (int i = 0; i < ring.n; ++i, key0 += kWarps * kPair * kPageSize) {
-      const uint32_t st = ring.wait(lane, p);
+    while (alive && feed.i < feed.n && feed.issued - feed.waited < kStages) feed.issue(p, lane);
+    if (alive && feed.i == feed.n) feed_on();  // a short part: the next one's pages
+    for (int i = 0; i < n_chunks && alive; ++i, key0 += kWarps * kPair * kPageSize) {
+      // The schedulers favour older warps; without a check the first teams would
+      // finish long before the last, and leave an SM with too few warps to fill it.
+      if ((chunks_done & 1) == 0) {
+        for (int k = 0; k < 64; ++k) {
+          const uint4 all = lds128(smem_u32(smem_all + L::kDone));
+          const uint32_t slowest = min(min(all.x, all.y), min(all.z, all.w));
+          if (chunks_done <= slowest + kLead) break;
+          __nanosleep(100);
+        }
+      }
+      const uint32_t st = feed.wait(p, lane);
       if (st == 0) {
         alive = false;
         break;
@@ -444,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
           ka[0] = a.x, ka[1] = a.y;
           kb[0] = b.x, kb[1] = b.y;
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4];
 #pragma unroll
         for (int k = 0; k < KW; ++k)
 #pragma unroll
@@ -452,15 +598,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
             const uint32_t xa = ka[k] >> (8 * h), xb = kb[k] >> (8 * h);
             const uint32_t a[4] = {xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u,
                                    xb & 0x00f000f0u};
-            mma16816<false>(acc, a, qb[2 * k + h][0], qb[2 * k + h][1]);
+            if (k + h == 0)
+              mma_from_zero(acc, a, qb[0][0], qb[0][1]);
+            else
+              mma16816<false>(acc, a, qb[2 * k + h][0], qb[2 * k + h][1]);
           }
         const float2 k0 = unpack2<BF16>(km0), k1 = unpack2<BF16>(km1);
-        s[2 * pg] = __ffma2_rn(make_float2(k0.x, k0.x),
-                               __ffma2_rn(f2, make_float2(acc[0], acc[1]), e8),
-                               __fmul2_rn(make_float2(k0.y, k0.y), e2));
-        s[2 * pg + 1] = __ffma2_rn(make_float2(k1.x, k1.x),
-                                   __ffma2_rn(f2, make_float2(acc[2], acc[3]), e8),
-                                   __fmul2_rn(make_float2(k1.y, k1.y), e2));
+        s[2 * pg].x = fmaf(k0.x, fmaf(f0, acc[0], -8.f * e0), k0.y * e0);
+        s[2 * pg].y = fmaf(k0.x, fmaf(f1, acc[1], -8.f * e1), k0.y * e1);
+        s[2 * pg + 1].x = fmaf(k1.x, fmaf(f0, acc[2], -8.f * e0), k1.y * e0);
+        s[2 * pg + 1].y = fmaf(k1.x, fmaf(f1, acc[3], -8.f * e1), k1.y * e1);
       }
       if (key0 + kPair * kPageSize > lim_all) {
         // last key (exclusive) each of this lane's two rows sees
@@ -530,16 +677,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       for (int u = 0; u < 2 * kPair; ++u) {
         const float2 pr = make_float2(ex2(d[u].x), ex2(d[u].y));
         l2 = __fadd2_rn(l2, pr);
-        z2 = __ffma2_rn(pr, make_float2(v[u].y, v[u].y), z2);
+        z2 = make_float2(fmaf(pr.x, v[u].y, z2.x), fmaf(pr.y, v[u].y, z2.y));
         const float x = v[u].x * v_inv;
-        const float2 wt = __fmul2_rn(pr, make_float2(x, x));
+        const float2 wt = make_float2(pr.x * x, pr.y * x);
         const uint32_t head = pack2<false>(wt.x, wt.y);
         const float2 back = unpack2<false>(head);
         if constexpr (WIDE) {
           hi[u] = transpose8x8(head);
           lo[u] = transpose8x8(pack2<false>(wt.x - back.x, wt.y - back.y));
         } else {  // the head term again, or the remainder
-          const float2 mine = __ffma2_rn(make_float2(rem, rem), back, wt);
+          const float2 mine = make_float2(fmaf(rem, back.x, wt.x), fmaf(rem, back.y, wt.y));
           hi[u] = transpose8x8(pack2<false>(mine.x, mine.y));
           lo[u] = 0;
         }
@@ -576,8 +723,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
                                      sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u)};
               float (&ok)[4] = o[4 * j + 2 * h + u];
               if constexpr (WIDE) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816<false>(t, a, lo[2 * pg], lo[2 * pg + 1]);
+                float t[4];
+                mma_from_zero(t, a, lo[2 * pg], lo[2 * pg + 1]);
                 mma16816<false>(t, a, hi[2 * pg], hi[2 * pg + 1]);
                 ok[0] += t[0], ok[1] += t[1], ok[2] += t[2], ok[3] += t[3];
               } else {
@@ -587,7 +734,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
           }
       }
       __syncwarp();  // the stage has been read by every lane
-      if (i + kStages < ring.n) ring.issue(i + kStages, lane, p);
+      if (feed.i < feed.n)
+        feed.issue(p, lane);
+      else
+        feed_on();
+      ++chunks_done;
+      if (tid == 0) done[team] = chunks_done;
     }
 
     // ---- the warp's state to shared memory: O is O[d = (D / 8) ln + 2 k + {0, 1}]
@@ -598,7 +750,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       z2.x += __shfl_xor_sync(kFull, z2.x, x);
       z2.y += __shfl_xor_sync(kFull, z2.y, x);
     }
-    __syncthreads();  // every warp is done with the ring
+    cp_async_wait();  // the next part's q
+    team_sync(team);  // the part before this one has been merged
     const float back = v_ref * 0x1p-7f;
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
@@ -623,97 +776,78 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       mer_l[warp * kTile + 2 * lc] = l2.x;
       mer_l[warp * kTile + 2 * lc + 1] = l2.y;
     }
-    __syncthreads();
+    team_sync(team);
 
-    // ---- the item's CTAs: the first holds its start, the last its end
-    const int first = part.first, last = part.last;
-    auto store = [&](int r, int d, float4 v) {  // row r of the tile, dimensions d .. d + 3
-      const size_t at = q_row(part.r0 + r) * D + d;
-      if constexpr (OUT16)
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
-            make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
-      else
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = v;
-    };
-    // CTA c's state of this item: slot 0 when its part starts the CTA's run.
-    auto state = [&](int c, int r) {
-      const int slot = c > first ? 0 : part.slot;
-      return p.ws + ((static_cast<size_t>(c) * 2 + slot) * kTile + r) * (D + 4);
-    };
-    for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
-      const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      float M = kNoKey;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) M = fmaxf(M, mer_m[k * kTile + r]);
-      float l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float lk = mer_l[k * kTile + r];
-        const float f = ex2(mer_m[k * kTile + r] - M);
-        const float4 v =
-            *reinterpret_cast<const float4 *>(mer_o + (k * kTile + r) * L::kRowStride + d);
-        l = fmaf(f, lk, l);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-      }
-      if (first == last) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros; NaN stays NaN
-        store(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    const bool whole = part.first == part.last;
+    // the warps' states of a row merged: dimensions d .. d + 3, and (m, l)
+    merge_rows<D>(mer_o, mer_m, mer_l, n_r, tid, [&](int r, int d, float4 acc, float m, float l) {
+      if (whole) {
+        store_row<D, BF16, OUT16>(p, q_row(part, part.r0 + r), d, acc, l);
       } else {
-        float *dst = state(blockIdx.x, r);
+        float *dst = state_of<D>(p, part, team_id) + r * (D + 4);
         *reinterpret_cast<float4 *>(dst + d) = acc;
-        if (d == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(M, l);
+        if (d == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(m, l);
       }
-    }
-    if (first != last) {
-      // The last of the item's CTAs to arrive merges their states.  One thread
-      // arrives with an acquire-release add behind the barrier, so the CTA's
-      // states are visible before its arrival counts, and every other CTA's
-      // states to the last one.
-      __syncthreads();
-      if (tid == 0) *s_last = atomic_add_acq_rel_gpu(p.ctr + first, 1) == last - first;
-      __syncthreads();
-      if (*s_last) {
-        for (int e = tid; e < n_r * (D / 4); e += kWarps * 32) {
-          const int r = e / (D / 4), d = 4 * (e % (D / 4));
-          float m = kNoKey, l = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int kBatch = 4;
-          for (int c = first; c <= last; c += kBatch) {
-            float2 ml[kBatch];
-            float4 v[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-              if (c + u <= last) {
-                const float *sp = state(c + u, r);
-                ml[u] = __ldcg(reinterpret_cast<const float2 *>(sp + D));
-                v[u] = __ldcg(reinterpret_cast<const float4 *>(sp + d));
-              }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-              if (c + u <= last && ml[u].y != 0.f) {
-                const float mn = fmaxf(m, ml[u].x);
-                const float a = ex2(m - mn), f = ex2(ml[u].x - mn);
-                acc.x = fmaf(acc.x, a, v[u].x * f);
-                acc.y = fmaf(acc.y, a, v[u].y * f);
-                acc.z = fmaf(acc.z, a, v[u].z * f);
-                acc.w = fmaf(acc.w, a, v[u].w * f);
-                l = fmaf(l, a, ml[u].y * f);
-                m = mn;
-              }
-          }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          store(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        }
+    });
+    if (!part.more) {
+      // the run's last part may start an item that later teams hold more of
+      if (tid == 0) {
+        const bool cut = part.last > team_id && part.first == team_id;
+        p.cut[2 * team_id] = make_int4(cut ? part.last - team_id + 1 : 0, part.slot, part.n_r, 0);
+        p.cut[2 * team_id + 1] = make_int4(part.b, part.g, part.r0, 0);
+        done[team] = 0x7fffffff;
       }
+      break;
     }
-    if (!part.more) break;
-    fence_proxy_async_smem();  // the merge area's last reads, before copies over it
-    __syncthreads();           // ... and the next part is planned
   }
+}
+
+// ---- items cut between teams: CTA c folds the states of the one that starts in team
+// c's run (if any), a thread a (row, 4 dimensions), eight states a step
+template <int D, bool BF16, bool OUT16>
+__global__ void __launch_bounds__(kTile * D / 4) kv4_fold_kernel(const RowsParams p) {
+  griddep_release();
+  griddep_wait();  // the states
+  const int c = blockIdx.x;
+  const int4 cut = __ldcg(p.cut + 2 * c), at = __ldcg(p.cut + 2 * c + 1);
+  const int n = cut.x, r = threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
+  if (r >= cut.z) return;
+  constexpr int kBatch = 8, kState = kTile * (D + 4);
+  float m = kNoKey, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float *first = p.ws + (static_cast<size_t>(c) * 2 + cut.y) * kState + r * (D + 4);
+  const float *rest = p.ws + static_cast<size_t>(c) * 2 * kState + r * (D + 4);
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      ml[u] = make_float2(kNoKey, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int k = k0 + u;
+      if (k < n) {
+        const float *sp = k == 0 ? first : rest + static_cast<size_t>(k) * 2 * kState;
+        ml[u] = __ldcg(reinterpret_cast<const float2 *>(sp + D));
+        v[u] = __ldcg(reinterpret_cast<const float4 *>(sp + d));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float mn = fmaxf(m, ml[u].x);
+      const float a = ex2(m - mn), f = ex2(ml[u].x - mn);
+      acc.x = fmaf(acc.x, a, v[u].x * f);
+      acc.y = fmaf(acc.y, a, v[u].y * f);
+      acc.z = fmaf(acc.z, a, v[u].z * f);
+      acc.w = fmaf(acc.w, a, v[u].w * f);
+      l = fmaf(l, a, ml[u].y * f);
+      m = mn;
+    }
+  }
+  if (n == 0) return;
+  const int row = at.z + r;
+  store_row<D, BF16, OUT16>(
+      p, (static_cast<size_t>(at.x) * p.queries + row / p.group) * p.n_q_heads + at.y * p.group +
+             row % p.group, d, acc, l);
 }
 
 template <int D, bool BF16, bool WIDE, bool OUT16>
@@ -721,10 +855,12 @@ int launch_rows_t(const RowsParams &p, int ctas, cudaStream_t stream) {
   auto kern = kv4_rows_kernel<D, BF16, WIDE, OUT16>;
   static ContextCache<bool> smem_set;
   if (set_smem_limit(kern, RowsSmem<D>::kBytes, smem_set) != PA_OK) return PA_ERR_CUDA;
-  return launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), RowsSmem<D>::kBytes, stream, p) ==
-                 cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(ctas), dim3(kTeams * kWarps * 32), RowsSmem<D>::kBytes, stream, p) !=
+          cudaSuccess ||
+      launch_pdl(kv4_fold_kernel<D, BF16, OUT16>, dim3(ctas * kTeams), dim3(kTile * D / 4), 0,
+                 stream, p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
 }
 
 template <int D, bool BF16>
@@ -738,18 +874,17 @@ int launch_rows_d(const RowsParams &p, int ctas, cudaStream_t stream) {
 }
 
 size_t partials_bytes(int head_dim, int ctas) {
-  return static_cast<size_t>(ctas) * 2 * kTile * (head_dim + 4) * sizeof(float);
+  return static_cast<size_t>(ctas) * kTeams * 2 * kTile * (head_dim + 4) * sizeof(float);
 }
 
 }  // namespace
 
 size_t kv4_rows_workspace_bytes(int head_dim, int sms) {
-  const int ctas = sms * kCtasPerSm;
-  return partials_bytes(head_dim, ctas) + static_cast<size_t>(ctas) * sizeof(int);
+  return partials_bytes(head_dim, sms) + static_cast<size_t>(sms) * kTeams * 2 * sizeof(int4);
 }
 
 int launch_kv4_rows(const Kv4AttentionLaunch &a, cudaStream_t stream) {
-  const int ctas = sm_count() * kCtasPerSm;
+  const int ctas = sm_count();
   if (ctas <= 0) return PA_ERR_CUDA;
   RowsParams p;
   p.q = static_cast<const uint16_t *>(a.q);
@@ -758,8 +893,8 @@ int launch_kv4_rows(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.ctx_lens = a.ctx_lens;
   p.out = a.out;
   p.ws = static_cast<float *>(a.workspace);
-  p.ctr = reinterpret_cast<int *>(static_cast<char *>(a.workspace) +
-                                  partials_bytes(a.head_dim, ctas));
+  p.cut = reinterpret_cast<int4 *>(static_cast<char *>(a.workspace) +
+                                   partials_bytes(a.head_dim, ctas));
   p.status = a.status;
   p.qscale = a.scale * kLog2e;
   p.n_new = a.n_new;
@@ -775,7 +910,6 @@ int launch_kv4_rows(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.n_sub = (p.n_rows + kTile - 1) / kTile;
   p.tile_rows = (p.n_rows + p.n_sub - 1) / p.n_sub;
   p.n_sub = (p.n_rows + p.tile_rows - 1) / p.tile_rows;
-  if (launch_clear_counters(p.ctr, ctas, stream) != PA_OK) return PA_ERR_CUDA;
   if (a.head_dim == 128)
     return a.bf16 ? launch_rows_d<128, true>(p, ctas, stream)
                   : launch_rows_d<128, false>(p, ctas, stream);
