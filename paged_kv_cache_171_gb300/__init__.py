@@ -647,53 +647,86 @@ def topm_retain(scores, current, budget, keep=None, kept_per_head=None, workspac
 
 
 # --- rotated appends and the 4-bit cache --------------------------------------
+# A decode step makes these calls once a layer, so their checks are kept cheap: a
+# tensor that is as it should be costs four attribute reads.
 
-def _want(t, name, dtype, shape, device):
-    """t is a contiguous tensor of this type, shape (None: any extent) and device."""
-    if (t.dtype != dtype or t.dim() != len(shape) or t.device != device or
-            not t.is_contiguous() or
-            any(w is not None and n != w for n, w in zip(t.shape, shape))):
-        raise ValueError(
-            f"{name}: want a contiguous {dtype} tensor of shape "
-            f"{tuple('*' if w is None else w for w in shape)} on {device}, got {t.dtype} "
-            f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
+def _bad(t, name, dtype, shape, index):
+    return ValueError(
+        f"{name}: want a contiguous {dtype} tensor of shape "
+        f"{tuple('*' if w is None else w for w in shape)} on cuda:{index}, got {t.dtype} "
+        f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
-def _token_stride(t, name, like, heads, D):
+def _want(t, name, dtype, shape, index):
+    """t is a contiguous tensor of this type and shape on CUDA device `index`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != index:
+        raise _bad(t, name, dtype, shape, index)
+
+
+def _want_2d(t, name, dtype, rows, index):
+    """As _want, of any number of columns; returns (rows, columns)."""
+    if t.dtype is not dtype or t.dim() != 2 or not t.is_contiguous() or \
+            t.get_device() != index or (rows is not None and t.shape[0] != rows):
+        raise _bad(t, name, dtype, (rows, None), index)
+    return t.shape
+
+
+def _token_stride(t, name, dtype, index, n_tok, heads, D):
     """Elements from one token's rows [heads, D] to the next one's."""
-    if t.dtype != like.dtype or t.device != like.device or t.dim() != 3 or \
-            t.shape[0] != like.shape[0] or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name}: want {like.dtype} [{like.shape[0]}, {heads}, {D}] on "
-                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (n_tok, heads, D):
+        raise ValueError(f"{name}: want {dtype} [{n_tok}, {heads}, {D}] on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    token, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous rows (strides "
-                         f"{tuple(t.stride())}); call .contiguous()")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+                         f"{(token, head, one)}); call .contiguous()")
+    return token if n_tok > 1 else heads * D
 
 
-class _Launch:
-    """The device and stream of one call: the device of its tensors is made
-    current, and what the call allocates belongs to the stream it runs on."""
+def _device_index(t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    return index
 
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {device}")
-        self._guards = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self._guards.append(torch.cuda.stream(stream))
+
+class _On:
+    """Makes device `index` current, and `stream` (a torch stream or a handle, if
+    given) the current stream there, so that what a call allocates belongs to the
+    stream it runs on.  Yields the stream's handle."""
+
+    def __init__(self, index, stream):
+        self.index, self.stream, self.guards = index, stream, []
 
     def __enter__(self):
-        for g in self._guards:
+        import torch
+        stream = self.stream
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(stream, device=self.index)
+        if stream is not None and stream.device_index != self.index:
+            raise ValueError(f"stream of cuda:{stream.device_index} for tensors on "
+                             f"cuda:{self.index}")
+        self.guards.append(torch.cuda.device(self.index))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+        for g in self.guards:
             g.__enter__()
+        return (stream or torch.cuda.current_stream()).cuda_stream
 
     def __exit__(self, *exc):
-        for g in reversed(self._guards):
+        for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+def _run(index, stream, call):
+    """call(handle) on device `index`: directly when it is the current one and no
+    stream is named (the usual case), else under _On."""
+    import torch
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with _On(index, stream) as handle:
+        return call(handle)
 
 
 def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
@@ -706,6 +739,9 @@ def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
     return torch.cat((ang.cos(), ang.sin()), -1).float()
 
 
+_KV4_HEAD_DIM = {16 * d + 128: d for d in (64, 128)}  # block bytes -> head_dim
+
+
 def kv4_cache(num_pages, n_kv_heads, head_dim, device="cuda"):
     """An empty 4-bit cache: uint8 [num_pages, n_kv_heads, block bytes]."""
     import torch
@@ -715,39 +751,63 @@ def kv4_cache(num_pages, n_kv_heads, head_dim, device="cuda"):
     return torch.zeros((num_pages, n_kv_heads, block), dtype=torch.uint8, device=device)
 
 
-def _kv4_dims(kv_cache, hkv=None):
-    """num_pages, n_kv_heads and head_dim of a 4-bit cache tensor."""
+def _kv4_dims(kv_cache, index):
+    """num_pages, n_kv_heads and head_dim of a 4-bit cache tensor on device `index`."""
     import torch
-    if kv_cache.dim() != 3 or kv_cache.dtype != torch.uint8 or not kv_cache.is_contiguous() or \
-            kv_cache.shape[2] not in (1152, 2176) or (hkv is not None and
-                                                      kv_cache.shape[1] != hkv):
+    shape = kv_cache.shape
+    D = _KV4_HEAD_DIM.get(shape[2]) if len(shape) == 3 else None
+    if D is None or kv_cache.dtype is not torch.uint8 or not kv_cache.is_contiguous() or \
+            kv_cache.get_device() != index:
         raise ValueError("kv_cache: want contiguous uint8 [num_pages, n_kv_heads, "
-                         f"pa_kv4_block_bytes(head_dim)], got {kv_cache.dtype} "
-                         f"{tuple(kv_cache.shape)}")
-    pages, heads, block = kv_cache.shape
-    return pages, heads, (block - 128) // 16
+                         f"pa_kv4_block_bytes(head_dim)] on cuda:{index}, got {kv_cache.dtype} "
+                         f"{tuple(shape)} on {kv_cache.device}")
+    return shape[0], shape[1], D
 
 
-def _append_args(k_new, v_new, q, q_out, block_table, seq_idx, pos, cos_sin):
+def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, hkv_cache, D_cache,
+            block_table, seq_idx, pos, cos_sin, interleaved, stream):
+    """The common part of the two rotated appends: `entry` with `caches` (pointers)."""
     import torch
+    if k_new.dim() != 3:
+        raise ValueError(f"k_new: want [n_tok, n_kv_heads, head_dim], got {tuple(k_new.shape)}")
     n_tok, hkv, D = k_new.shape
-    dev = k_new.device
-    ks = _token_stride(k_new, "k_new", k_new, hkv, D)
-    vs = _token_stride(v_new, "v_new", k_new, hkv, D)
-    _want(block_table, "block_table", torch.int32, (None, None), dev)
-    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), dev)
-    _want(pos, "pos", torch.int32, (n_tok,), dev)
+    if hkv != hkv_cache or D != D_cache:
+        raise ValueError(f"the cache holds {hkv_cache} heads of head_dim {D_cache}, k_new has "
+                         f"{hkv} of {D}")
+    dtype, index = k_new.dtype, k_new.get_device()
+    code = dtype_code(k_new)
+    ks = _token_stride(k_new, "k_new", dtype, index, n_tok, hkv, D)
+    vs = _token_stride(v_new, "v_new", dtype, index, n_tok, hkv, D)
+    batch, max_blocks = _want_2d(block_table, "block_table", torch.int32, None, index)
+    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), index)
+    _want(pos, "pos", torch.int32, (n_tok,), index)
+    max_pos = rot = hq = qs = 0
     if cos_sin is not None:
-        _want(cos_sin, "cos_sin", torch.float32, (None, None), dev)
-    hq = qs = 0
+        max_pos, rot = _want_2d(cos_sin, "cos_sin", torch.float32, None, index)
     if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q: want [n_tok, n_q_heads, head_dim], got {tuple(q.shape)}")
         hq = q.shape[1]
-        qs = _token_stride(q, "q", k_new, hq, D)
+        qs = _token_stride(q, "q", dtype, index, n_tok, hq, D)
         if q_out is not None:
-            _want(q_out, "q_out", k_new.dtype, (n_tok, hq, D), dev)
+            _want(q_out, "q_out", dtype, (n_tok, hq, D), index)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    return n_tok, hq, hkv, D, ks, vs, qs
+    index = _device_index(k_new)
+
+    def call(handle):
+        to = q_out
+        if q is not None and to is None:
+            to = torch.empty((n_tok, hq, D), dtype=dtype, device=q.device)
+        _check(entry(k_new.data_ptr(), v_new.data_ptr(), None if q is None else q.data_ptr(),
+                     *caches, None if to is None else to.data_ptr(), block_table.data_ptr(),
+                     seq_idx.data_ptr(), pos.data_ptr(),
+                     None if cos_sin is None else cos_sin.data_ptr(), n_tok, ks, vs, qs, hq, hkv,
+                     D, page_size, batch, max_blocks, num_pages, max_pos, rot, int(interleaved),
+                     code, handle), where)
+        return to
+
+    return _run(index, stream, call)
 
 
 def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, cos_sin, q=None,
@@ -757,19 +817,15 @@ def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, co
     output); cos_sin float32 [max_pos, rot_dim] (rope_table).  Writes the caches
     [pages, h_kv, 16, D]; returns the rotated q ([n_tok, h_q, D], q_out if
     given), or None without q."""
-    import torch
-    n_tok, hq, hkv, D, ks, vs, qs = _append_args(k_new, v_new, q, q_out, block_table, seq_idx,
-                                                 pos, cos_sin)
-    _want(k_cache, "k_cache", k_new.dtype, (None, hkv, None, D), k_new.device)
-    _want(v_cache, "v_cache", k_new.dtype, tuple(k_cache.shape), k_new.device)
-    with _Launch(k_new.device, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty((n_tok, hq, D), dtype=q.dtype, device=q.device)
-        pa_append_kv_rope(k_new, v_new, q, k_cache, v_cache, q_out, block_table, seq_idx, pos,
-                          cos_sin, n_tok, ks, vs, qs, hq, hkv, D, k_cache.shape[2],
-                          block_table.shape[0], block_table.shape[1], k_cache.shape[0],
-                          cos_sin.shape[0], cos_sin.shape[1], interleaved, dtype_code(k_new))
-    return q_out
+    if cos_sin is None or k_cache.dim() != 4:
+        raise ValueError("append_kv_rope wants cos_sin and caches [pages, h_kv, 16, D]")
+    pages, hkv, P, D = shape = k_cache.shape
+    index = k_new.get_device()
+    _want(k_cache, "k_cache", k_new.dtype, shape, index)
+    _want(v_cache, "v_cache", k_new.dtype, shape, index)
+    return _append(lib().pa_append_kv_rope, "pa_append_kv_rope", k_new, v_new, q, q_out,
+                   (k_cache.data_ptr(), v_cache.data_ptr()), pages, P, hkv, D, block_table,
+                   seq_idx, pos, cos_sin, interleaved, stream)
 
 
 def append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin=None, q=None,
@@ -777,21 +833,10 @@ def append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin=None, 
     """pa_append_kv4 on tensors: as append_kv_rope, into a 4-bit cache (kv4_cache);
     without cos_sin nothing is rotated.  The dtype of k_new is that of the cache's
     scales and zeros: keep to one for a cache.  Returns the rotated q, or None."""
-    import torch
-    n_tok, hq, hkv, D, ks, vs, qs = _append_args(k_new, v_new, q, q_out, block_table, seq_idx,
-                                                 pos, cos_sin)
-    pages, _, D4 = _kv4_dims(kv_cache, hkv)
-    if D4 != D or kv_cache.device != k_new.device:
-        raise ValueError(f"kv_cache holds head_dim {D4} on {kv_cache.device}, k_new has {D} on "
-                         f"{k_new.device}")
-    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-    with _Launch(k_new.device, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty((n_tok, hq, D), dtype=q.dtype, device=q.device)
-        pa_append_kv4(k_new, v_new, q, kv_cache, q_out, block_table, seq_idx, pos, cos_sin, n_tok,
-                      ks, vs, qs, hq, hkv, D, 16, block_table.shape[0], block_table.shape[1],
-                      pages, max_pos, rot, interleaved, dtype_code(k_new))
-    return q_out
+    pages, hkv, D = _kv4_dims(kv_cache, k_new.get_device())
+    return _append(lib().pa_append_kv4, "pa_append_kv4", k_new, v_new, q, q_out,
+                   (kv_cache.data_ptr(),), pages, 16, hkv, D, block_table, seq_idx, pos, cos_sin,
+                   interleaved, stream)
 
 
 def read_kv4(kv_cache, block_table, seq_idx, pos, dtype=None, k_out=None, v_out=None,
@@ -800,44 +845,87 @@ def read_kv4(kv_cache, block_table, seq_idx, pos, dtype=None, k_out=None, v_out=
     values, each [n_tok, h_kv, D] of dtype (torch.bfloat16 or torch.float16, the
     type the cache was written with; k_out's if given)."""
     import torch
-    pages, hkv, D = _kv4_dims(kv_cache)
-    dev, n_tok = kv_cache.device, seq_idx.shape[0]
-    _want(block_table, "block_table", torch.int32, (None, None), dev)
-    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), dev)
-    _want(pos, "pos", torch.int32, (n_tok,), dev)
+    index = kv_cache.get_device()
+    pages, hkv, D = _kv4_dims(kv_cache, index)
+    batch, max_blocks = _want_2d(block_table, "block_table", torch.int32, None, index)
+    if seq_idx.dim() != 1:
+        raise ValueError(f"seq_idx: want [n_tok], got {tuple(seq_idx.shape)}")
+    n_tok = seq_idx.shape[0]
+    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), index)
+    _want(pos, "pos", torch.int32, (n_tok,), index)
     if dtype is None:
         if k_out is None and v_out is None:
             raise ValueError("read_kv4 wants dtype, k_out or v_out")
         dtype = (k_out if k_out is not None else v_out).dtype
-    with _Launch(dev, stream):
-        if k_out is None:
-            k_out = torch.empty((n_tok, hkv, D), dtype=dtype, device=dev)
-        if v_out is None:
-            v_out = torch.empty((n_tok, hkv, D), dtype=dtype, device=dev)
-        _want(k_out, "k_out", dtype, (n_tok, hkv, D), dev)
-        _want(v_out, "v_out", dtype, (n_tok, hkv, D), dev)
-        pa_read_kv4(kv_cache, block_table, seq_idx, pos, k_out, v_out, n_tok, hkv, D, 16,
-                    block_table.shape[0], block_table.shape[1], pages, dtype_code(k_out))
-    return k_out, v_out
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"unsupported dtype {dtype}")
+    shape = (n_tok, hkv, D)
+    if k_out is not None:
+        _want(k_out, "k_out", dtype, shape, index)
+    if v_out is not None:
+        _want(v_out, "v_out", dtype, shape, index)
+    _device_index(kv_cache)
+
+    def call(handle):
+        k = k_out if k_out is not None else torch.empty(shape, dtype=dtype, device=kv_cache.device)
+        v = v_out if v_out is not None else torch.empty(shape, dtype=dtype, device=kv_cache.device)
+        _check(lib().pa_read_kv4(kv_cache.data_ptr(), block_table.data_ptr(), seq_idx.data_ptr(),
+                                 pos.data_ptr(), k.data_ptr(), v.data_ptr(), n_tok, hkv, D, 16,
+                                 batch, max_blocks, pages, dtype_code(k), handle), "pa_read_kv4")
+        return k, v
+
+    return _run(index, stream, call)
 
 
 def copy_pages_kv4(kv_cache, src, dst, stream=None):
     """pa_copy_pages_kv4 on tensors: page src[i] to page dst[i] (int32, on the device)."""
     import torch
-    pages, hkv, D = _kv4_dims(kv_cache)
-    _want(src, "src", torch.int32, (None,), kv_cache.device)
-    _want(dst, "dst", torch.int32, tuple(src.shape), kv_cache.device)
-    with _Launch(kv_cache.device, stream):
-        pa_copy_pages_kv4(kv_cache, src, dst, src.shape[0], hkv, D, 16, pages)
+    index = _device_index(kv_cache)
+    pages, hkv, D = _kv4_dims(kv_cache, index)
+    n = src.numel()
+    _want(src, "src", torch.int32, (n,), index)
+    _want(dst, "dst", torch.int32, (n,), index)
+    _run(index, stream, lambda handle: _check(lib().pa_copy_pages_kv4(
+        kv_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, hkv, D, 16, pages, handle),
+        "pa_copy_pages_kv4"))
 
 
-def _workspace(workspace, need, device):
+def _attend(entry, where, need, q, n_new, kv_cache, block_table, ctx_lens, scale, out, out_dtype,
+            workspace, stream):
+    """The common part of decode_kv4 (n_new None) and prefill_kv4."""
     import torch
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: want a contiguous tensor on {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    index = q.get_device()
+    shape = q.shape
+    B, hq, D = shape[0], shape[-2], shape[-1]
+    pages, hkv, D4 = _kv4_dims(kv_cache, index)
+    if D4 != D:
+        raise ValueError(f"kv_cache holds head_dim {D4}, q has {D}")
+    code = dtype_code(q)
+    if not q.is_contiguous():
+        raise ValueError(f"q: want a contiguous tensor, got strides {tuple(q.stride())}")
+    _, mb = _want_2d(block_table, "block_table", torch.int32, B, index)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    if out is not None:
+        _want(out, "out", out_dtype, shape, index)
+    if workspace is not None and (workspace.get_device() != index or
+                                  not workspace.is_contiguous()):
+        raise ValueError(f"workspace: want a contiguous tensor on cuda:{index}")
+    _device_index(q)
+
+    def call(handle):
+        o = out if out is not None else torch.empty(shape, dtype=out_dtype, device=q.device)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(need(B, hq, hkv, D, mb), dtype=torch.uint8, device=q.device)
+        args = (o.data_ptr(), scale, hq, hkv, D, 16, B, mb, pages, code, ws.data_ptr(), ws.nbytes,
+                handle)
+        if n_new is not None:
+            args = (n_new,) + args
+        _check(entry(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+                     ctx_lens.data_ptr(), *args), where)
+        return o
+
+    return _run(index, stream, call)
 
 
 def decode_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=None, stream=None):
@@ -847,43 +935,24 @@ def decode_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=No
     any tensor of pa_decode_kv4_workspace_size(D) bytes, not shared with a call
     that may run at the same time."""
     import torch
-    B, hq, D = q.shape
-    dev = q.device
-    pages, hkv, D4 = _kv4_dims(kv_cache)
-    _want(q, "q", q.dtype, (B, hq, D4), dev)
-    _want(kv_cache, "kv_cache", torch.uint8, (pages, hkv, None), dev)
-    _want(block_table, "block_table", torch.int32, (B, None), dev)
-    _want(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
-    with _Launch(dev, stream):
-        if out is None:
-            out = torch.empty((B, hq, D), dtype=torch.float32, device=dev)
-        _want(out, "out", torch.float32, (B, hq, D), dev)
-        workspace, size = _workspace(workspace, pa_decode_kv4_workspace_size(D), dev)
-        pa_decode_kv4(q, kv_cache, block_table, ctx_lens, out, scale, hq, hkv, D, 16, B,
-                      block_table.shape[1], pages, dtype_code(q), workspace, size)
-    return out
+    if q.dim() != 3:
+        raise ValueError(f"q: want [B, h_q, D], got {tuple(q.shape)}")
+    return _attend(lib().pa_decode_kv4, "pa_decode_kv4",
+                   lambda B, hq, hkv, D, mb: pa_decode_kv4_workspace_size(D), q, None, kv_cache,
+                   block_table, ctx_lens, scale, out, torch.float32, workspace, stream)
 
 
 def prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=None,
                 stream=None):
     """pa_prefill_kv4 on tensors: q [B, n_new, h_q, D], the chunk's queries, whose
     K/V rows append_kv4 has stored at positions ctx_lens[b] ..; ctx_lens = tokens
-    cached before the chunk.  Returns [B, n_new, h_q, D] in q's dtype."""
-    import torch
-    B, n_new, hq, D = q.shape
-    dev = q.device
-    pages, hkv, D4 = _kv4_dims(kv_cache)
-    _want(q, "q", q.dtype, (B, n_new, hq, D4), dev)
-    _want(kv_cache, "kv_cache", torch.uint8, (pages, hkv, None), dev)
-    _want(block_table, "block_table", torch.int32, (B, None), dev)
-    _want(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
-    mb = block_table.shape[1]
-    with _Launch(dev, stream):
-        if out is None:
-            out = torch.empty((B, n_new, hq, D), dtype=q.dtype, device=dev)
-        _want(out, "out", q.dtype, (B, n_new, hq, D), dev)
-        workspace, size = _workspace(
-            workspace, pa_prefill_kv4_workspace_size(B, n_new, hq, hkv, D, 16, mb), dev)
-        pa_prefill_kv4(q, kv_cache, block_table, ctx_lens, n_new, out, scale, hq, hkv, D, 16, B,
-                       mb, pages, dtype_code(q), workspace, size)
-    return out
+    cached before the chunk.  Returns [B, n_new, h_q, D] in q's dtype.  workspace:
+    any tensor of pa_prefill_kv4_workspace_size(...) bytes, as in decode_kv4."""
+    if q.dim() != 4:
+        raise ValueError(f"q: want [B, n_new, h_q, D], got {tuple(q.shape)}")
+    n_new = q.shape[1]
+    return _attend(lib().pa_prefill_kv4, "pa_prefill_kv4",
+                   lambda B, hq, hkv, D, mb: pa_prefill_kv4_workspace_size(B, n_new, hq, hkv, D,
+                                                                           16, mb),
+                   q, n_new, kv_cache, block_table, ctx_lens, scale, out, q.dtype, workspace,
+                   stream)
