@@ -80,5 +80,8 @@ struct Kv4AttentionLaunch {
 // Workspace of the row kernel on a device of `sms` SMs.
 size_t kv4_rows_workspace_bytes(int head_dim, int sms);
 int launch_kv4_rows(const Kv4AttentionLaunch &a, cudaStream_t stream);
+// The tile kernel (tcgen05): chunks of many rows.
+size_t kv4_tiles_workspace_bytes(int head_dim, int sms);
+int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream);
 
 }  // namespace pa

@@ -33,6 +33,14 @@ int append(AppendRopeLaunch &a, int page_size, int dtype, pa_stream_t stream) {
   return launch_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Chunks of more than this many rows (queries x group) a kv head go to the tile
+// kernel.
+constexpr int kMostRows = 64;
+
+bool wants_tiles(int n_new, int n_q_heads, int n_kv_heads) {
+  return n_new > 0 && static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > kMostRows;
+}
+
 int sms_or_default() { return sm_count() > 0 ? sm_count() : 152; }
 
 int attention(Kv4AttentionLaunch &a, int page_size, int dtype, size_t workspace_bytes,
@@ -42,12 +50,15 @@ int attention(Kv4AttentionLaunch &a, int page_size, int dtype, size_t workspace_
                         a.num_pages, dtype);
   if (rc) return rc;
   if (!aligned16(a.q) || !aligned16(a.cache) || !aligned16(a.out)) return PA_ERR_ALIGN;
-  if (!a.workspace || workspace_bytes < kv4_rows_workspace_bytes(a.head_dim, sms_or_default()))
-    return PA_ERR_WORKSPACE;
+  const bool tiles = wants_tiles(a.n_new, a.n_q_heads, a.n_kv_heads);
+  const size_t need = tiles ? kv4_tiles_workspace_bytes(a.head_dim, sms_or_default())
+                            : kv4_rows_workspace_bytes(a.head_dim, sms_or_default());
+  if (!a.workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
   if (!aligned16(a.workspace)) return PA_ERR_ALIGN;
   if ((rc = current_status_ptr(&a.status))) return rc;
   a.bf16 = dtype == PA_BF16;
-  return launch_kv4_rows(a, reinterpret_cast<cudaStream_t>(stream));
+  return tiles ? launch_kv4_tiles(a, reinterpret_cast<cudaStream_t>(stream))
+               : launch_kv4_rows(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -147,7 +158,9 @@ size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_
                    PA_BF16) ||
       n_new <= 0 || n_new > static_cast<int64_t>(max_blocks_per_seq) * page_size)
     return 0;
-  return kv4_rows_workspace_bytes(head_dim, sms_or_default());
+  return wants_tiles(n_new, n_q_heads, n_kv_heads)
+             ? kv4_tiles_workspace_bytes(head_dim, sms_or_default())
+             : kv4_rows_workspace_bytes(head_dim, sms_or_default());
 }
 
 int pa_prefill_kv4(const void *q, const void *kv_cache, const int32_t *block_table,

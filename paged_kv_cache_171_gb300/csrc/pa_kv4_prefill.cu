@@ -1,0 +1,855 @@
+// pa_kv4_prefill.cu -- chunked-prefill attention over the 4-bit paged cache on the
+// 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+// Query i of sequence b (0 <= i < n_new) attends keys 0 .. ctx_lens[b] + i of the
+// values K = zero_k + scale_k (c - 8), V alike.  As in the row kernel only the
+// codes enter the matrix products, as exact 16-bit c - 8, and the scales and zeros
+// are applied to the scores and weights,
+//   S   = Q (c_k - 8)^T                       tcgen05, 128 x 128 x head_dim
+//   s_t = scale_k[t] S_t + zero_k[t] sum q,    p_t = 2^(s_t - m)
+//   O  += (p_t scale_v[t] / v_ref) (c_v - 8)   tcgen05, A in tensor memory
+//   z  += p_t zero_v[t],                       out = (O v_ref + z) / l
+// so a key tile is turned into 16-bit operand tiles once for 256 query rows, at no
+// rounding.  The weights are rounded once to the cache's type, as the result is.
+// v_ref is a power of two above the largest |scale_v| of the tiles so far (fp16
+// weights stay in range); when it grows, O is rescaled like at a move of m.
+//
+// Tiles.  An item is 256 consecutive rows (query, head) of one kv head, whatever
+// the group size: row r is query r / G, head r % G.  It is two row tiles A and B of
+// 128 rows that share every key tile of 128 keys (8 pages).  The tensor pipe
+// alternates between them: B's softmax of key tile j starts once A has handed over
+// its weights of j, A's of j + 1 once B has handed over those of j.
+//
+// Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B,
+// warps 2 and 3 turn codes into the K and V operand tiles (two stages each, the
+// next tile's codes in registers), warps 4-7 and 8-11 are the softmax of A and B, a
+// thread a row.  Every hand-off is an mbarrier and every wait is bounded.
+//
+// Nibbles.  (x & 0x000f000f) | 0x43004300 is the bf16 pair 128 + c of nibbles 0 and
+// 4 of a word, minus 136 is c - 8 (fp16: | 0x6400 is 1024 + c, minus 1032); the
+// other nibbles follow by shifts.  The operand tiles keep that order of dimensions
+// (0 4 1 5 2 6 3 7 of each eight): Q is stored in it, and the result is put back
+// into the natural one on its way out.
+//
+// Work split.  The key tiles of all items, laid end to end, are cut into equal runs,
+// one an SM: 256 items on 152 SMs take 1.7 items' time, not two, and a single
+// sequence's chunk over a long context fills the GPU.  An item cut between CTAs
+// leaves an fp32 state (O, m, l) a row and CTA, folded by a second kernel.
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "pa_kv4.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;
+constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRows = 128, kKeys = 128;     // a row tile, a key tile
+constexpr int kItemRows = 2 * kRows;
+constexpr int kStages = 2;                  // of K and of V
+constexpr int kKWarp = 2, kVWarp = 3, kSoftmaxWarp0 = 4;
+constexpr int kThreads = 12 * 32;
+
+struct PrefillParams {
+  const uint16_t *q;
+  const uint8_t *cache;
+  const int32_t *block_table, *ctx_lens;
+  uint16_t *out;
+  float *ws;    // [CTA][2][kItemRows][D + 4] partial states
+  int4 *cut;    // [CTA][2] the item that starts in the CTA's run and leaves it
+  int *status;
+  float qscale;  // scale * log2 e
+  int n_new, n_q_heads, n_kv_heads, group, batch, max_blocks, num_pages;
+  int n_rows, n_items;  // rows a kv head, items a kv head
+  uint32_t page_bytes;
+};
+
+template <int D>
+struct PrefillSmem {
+  static constexpr int kColBlk = kRows * 128;         // one 64-column block, 128 rows
+  static constexpr int kTile = (D / 64) * kColBlk;    // 128 rows x D, 16 bits
+  static constexpr int kQ = 0;                        // Q_A, Q_B
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  // per stage and pair of keys: scale_k x2, zero_k x2 (both times qscale),
+  // scale_v / v_ref x2, zero_v x2; then (v_ref before / now, v_ref) per stage
+  static constexpr int kMeta = kV + kStages * kTile;
+  static constexpr int kRef = kMeta + kStages * (kKeys / 2) * 32;
+  static constexpr int kBars = kRef + kStages * 8;
+  static constexpr int kSlot = kBars + 24 * 8;        // TMEM address, abort flag
+  static constexpr int kPart = kSlot + 16;
+  static constexpr int kWalk = kPart + 64;
+  static constexpr int kBytes = kWalk + 64;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 232448, "exceeds the per-CTA shared memory limit");
+};
+
+enum {
+  kBarK = 0,       // K stage s converted, at + s (one arrival)
+  kBarV = 2,       // V stage s and its metas
+  kBarKFree = 4,   // K stage s read by row tile x's S MMA (commit), at + 2 x + s
+  kBarVFree = 8,   // V stage s read by row tile x's P V MMAs, at + 2 x + s
+  kBarS = 12,      // S_x in TMEM (commit), at + x
+  kBarP = 14,      // keys 64 h .. 64 h + 63 of P_x in TMEM, at + 2 x + h (4 arrivals)
+  kBarO = 18,      // the last P_x V done (commit), at + x
+  kBarDrain = 20,  // an MMA warp's own drain on its failure path, at + x
+  kNumBars = 22
+};
+
+// The part of one item that a CTA's run holds.
+struct TilePart {
+  int b, g, row0;      // sequence, kv head, first row of the item
+  int ctx;             // cached tokens of the sequence
+  int t0, nt;          // key tiles
+  int first, last;     // CTAs that hold the item
+  int slot;            // of the first one's state: 0 when the item starts its run
+  int more;            // the run goes on behind this part
+};
+static_assert(sizeof(TilePart) <= 64, "room in shared memory");
+
+// The CTA's run [w, w1) of the flattened list of key tiles.
+struct TileWalk {
+  int64_t w, w1, run, base;  // base: key tiles of the sequences before b
+  int b, ctx, per_head;      // the sequence; key tiles of one of its kv heads
+
+  static __device__ int ctx_of(const PrefillParams &p, int b, bool report) {
+    const int most = p.max_blocks * kPageSize - p.n_new;
+    int t = __ldg(p.ctx_lens + b);
+    if (t < 0 || t > most) {
+      if (report) record_error(p.status, PA_ERR_BAD_CTX);
+      t = t < 0 ? 0 : most;
+    }
+    return t;
+  }
+  // Key tiles that item k (of a kv head) of a sequence with ctx cached tokens sees.
+  static __device__ int tiles_of(const PrefillParams &p, int ctx, int k) {
+    const int last_row = min(p.n_rows, (k + 1) * kItemRows) - 1;
+    return (ctx + last_row / p.group) / kKeys + 1;
+  }
+  static __device__ int head_tiles(const PrefillParams &p, int ctx) {
+    int n = 0;
+    for (int k = 0; k < p.n_items; ++k) n += tiles_of(p, ctx, k);
+    return n;
+  }
+  static __device__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+  }
+  // The whole warp; lane 0 keeps the result in *out.  False: no run.
+  static __device__ bool start(const PrefillParams &p, int lane, TileWalk *out) {
+    TileWalk x;
+    const int per = (p.batch + 31) / 32;
+    const int b0 = min(p.batch, lane * per), b1 = min(p.batch, b0 + per);
+    int64_t sum = 0;
+    for (int i = b0; i < b1; ++i) sum += head_tiles(p, ctx_of(p, i, blockIdx.x == 0));
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t total = __shfl_sync(kFull, incl, 31) * p.n_kv_heads;
+    x.run = quotient(total + gridDim.x - 1, gridDim.x);
+    x.w = blockIdx.x * x.run;
+    x.w1 = min(total, x.w + x.run);
+    if (x.w >= x.w1) return false;
+    const int src = __ffs(__ballot_sync(kFull, incl * p.n_kv_heads > x.w)) - 1;
+    x.b = __shfl_sync(kFull, b0, src);
+    x.base = __shfl_sync(kFull, incl - sum, src) * p.n_kv_heads;
+    x.ctx = ctx_of(p, x.b, false);
+    x.per_head = head_tiles(p, x.ctx);
+    if (lane == 0) *out = x;
+    return true;
+  }
+  __device__ void next(const PrefillParams &p, TilePart &s) {
+    while (base + static_cast<int64_t>(per_head) * p.n_kv_heads <= w) {
+      base += static_cast<int64_t>(per_head) * p.n_kv_heads;
+      ctx = ctx_of(p, ++b, false);
+      per_head = head_tiles(p, ctx);
+    }
+    const int64_t rel = w - base;
+    const int g = static_cast<int>(quotient(rel, per_head));
+    int t = static_cast<int>(rel - static_cast<int64_t>(g) * per_head), k = 0, n;
+    while (t >= (n = tiles_of(p, ctx, k))) {
+      t -= n;
+      ++k;
+    }
+    const int64_t i0 = w - t;  // the item's first key tile
+    s.b = b;
+    s.g = g;
+    s.row0 = k * kItemRows;
+    s.ctx = ctx;
+    s.t0 = t;
+    s.nt = static_cast<int>(min(static_cast<int64_t>(n - t), w1 - w));
+    s.first = static_cast<int>(quotient(i0, run));
+    s.last = static_cast<int>(quotient(i0 + n - 1, run));
+    s.slot = i0 == s.first * run ? 0 : 1;
+    w += s.nt;
+    s.more = w < w1;
+  }
+};
+
+// Row r of a kv head in the [batch][n_new][n_q_heads] order of q and out.
+__device__ __forceinline__ size_t row_at(const PrefillParams &p, int b, int g, int r) {
+  return (static_cast<size_t>(b) * p.n_new + r / p.group) * p.n_q_heads + g * p.group +
+         r % p.group;
+}
+
+// The eight codes of a word as c - 8, in the order 0 4 1 5 2 6 3 7.
+template <bool BF16>
+__device__ __forceinline__ uint4 centred(uint32_t x) {
+  uint32_t o[4];
+  if constexpr (BF16) {
+    const __nv_bfloat162 mid = __float2bfloat162_rn(136.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = ((x >> (4 * k)) & 0x000f000fu) | 0x43004300u;
+      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&w), mid);
+      o[k] = *reinterpret_cast<const uint32_t *>(&r);
+    }
+  } else {
+    const __half2 mid = __float2half2_rn(1032.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
+      const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&w), mid);
+      o[k] = *reinterpret_cast<const uint32_t *>(&r);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Converter warps: codes -> operand tiles of K (which = 0) or V (1), and for V the
+// tile's scales and zeros.  Lane l takes 16-byte pieces l, l + 32, ... of the tile's
+// codes in row order, a batch of loads ahead of their conversion.
+template <int D, bool BF16>
+__device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
+                                              const TilePart &part, uint32_t sb, uint8_t *smem,
+                                              int n_active, volatile int *abort_flag, int lane) {
+  using L = PrefillSmem<D>;
+  constexpr int kPieces = D / 32;                  // 16-byte pieces of a row's codes
+  constexpr int kIters = kKeys * kPieces / 32;     // pieces a lane
+  constexpr int kRowsIter = 32 / kPieces;          // rows an iteration
+  constexpr int kBatch = 4;
+  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  const uint32_t ring = sb + (which ? L::kV : L::kK);
+  const int full = which ? kBarV : kBarK, free = which ? kBarVFree : kBarKFree;
+  const int tokens = part.ctx + p.n_new;
+  const int n_pages = (tokens + kPageSize - 1) / kPageSize;
+  const int32_t *bt_row = p.block_table + static_cast<size_t>(part.b) * p.max_blocks;
+  const uint8_t *head = p.cache + static_cast<size_t>(part.g) * kv4::block_bytes(D);
+  // lane l < 8: the id of page l of a tile (page 0 past the sequence's end: masked)
+  auto page_id = [&](int t) {
+    const int pg = (part.t0 + t) * (kKeys / kPageSize) + (lane & 7);
+    return t < part.nt && pg < n_pages ? __ldg(bt_row + pg) : 0;
+  };
+  float v_ref = 0.f;
+  int raw = page_id(0);
+  bool ok = true;
+  int t = 0;
+  for (; t < part.nt; ++t) {
+    int id = raw;
+    raw = page_id(t + 1);
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
+      if (lane < 8) record_error(p.status, PA_ERR_BAD_BLOCK);
+      id = 0;
+    }
+    auto block = [&](int row) {  // of the tile's row (all lanes take part)
+      const int pg = __shfl_sync(kFull, id, row / kPageSize);
+      return head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * p.page_bytes;
+    };
+    uint4 buf[2][kBatch];
+    auto load = [&](int it0, uint4 (&to)[kBatch]) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int row = (it0 + u) * kRowsIter + lane / kPieces;
+        to[u] = __ldg(reinterpret_cast<const uint4 *>(
+            block(row) + kv4::code_offset(D, which, row % kPageSize) + 16 * (lane % kPieces)));
+      }
+    };
+    load(0, buf[0]);
+    uint32_t km[kKeys / 32], vm[kKeys / 32];
+    if (which) {
+#pragma unroll
+      for (int u = 0; u < kKeys / 32; ++u) {
+        const int row = 32 * u + lane;
+        const uint8_t *blk = block(row);
+        const bool live = (part.t0 + t) * kKeys + row < tokens;
+        km[u] = vm[u] = 0;  // rows past the end may hold anything: 0 * NaN is NaN
+        if (live) {
+          km[u] = __ldg(reinterpret_cast<const uint32_t *>(
+              blk + kv4::meta_offset(D, 0, row % kPageSize)));
+          vm[u] = __ldg(reinterpret_cast<const uint32_t *>(
+              blk + kv4::meta_offset(D, 1, row % kPageSize)));
+        }
+      }
+    }
+    const int s = t % kStages;
+    for (int x = 0; x < n_active && ok && t >= kStages; ++x)
+      ok = warp_wait(bar(free + 2 * x + s), (t / kStages - 1) & 1, abort_flag);
+    if (!ok) break;
+    if (which) {
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < kKeys / 32; ++u) top = fmaxf(top, fabsf(unpack2<BF16>(vm[u]).x));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      float ratio = 1.f;
+      if (top > v_ref) {
+        const float up = fmaxf(
+            __uint_as_float((__float_as_uint(top) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
+        ratio = v_ref / up;
+        v_ref = up;
+      }
+      const float inv = v_ref > 0.f ? 1.f / v_ref : 0.f;
+      float *meta = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8;
+#pragma unroll
+      for (int u = 0; u < kKeys / 32; ++u) {
+        const int row = 32 * u + lane;
+        const float2 k = unpack2<BF16>(km[u]), v = unpack2<BF16>(vm[u]);
+        float *m = meta + (row >> 1) * 8 + (row & 1);
+        m[0] = k.x * p.qscale;
+        m[2] = k.y * p.qscale;
+        m[4] = v.x * inv;
+        m[6] = v.y;
+      }
+      if (lane == 0)
+        *reinterpret_cast<float2 *>(smem + L::kRef + 8 * s) = make_float2(ratio, v_ref);
+    }
+    const uint32_t dst = ring + s * L::kTile;
+#pragma unroll
+    for (int it0 = 0; it0 < kIters; it0 += kBatch) {
+      uint4 (&now)[kBatch] = buf[(it0 / kBatch) & 1];
+      if (it0 + kBatch < kIters) load(it0 + kBatch, buf[(it0 / kBatch + 1) & 1]);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int row = (it0 + u) * kRowsIter + lane / kPieces;
+        const int c0 = 4 * (lane % kPieces);
+        const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 o = centred<BF16>(w[k]);
+          const int c = c0 + k;
+          st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(row, c), o.x, o.y, o.z, o.w);
+        }
+      }
+    }
+    fence_proxy_async_smem();  // generic stores -> read by the tensor cores
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(full + s));
+  }
+  // every MMA that reads a stage has committed before the part ends
+  for (int k = max(0, t - kStages); k < t && ok; ++k)
+    for (int x = 0; x < n_active && ok; ++x)
+      ok = warp_wait(bar(free + 2 * x + k % kStages), (k / kStages) & 1, abort_flag);
+  if (!ok && lane == 0) raise_abort(p.status, abort_flag);
+}
+
+// MMA warp x (lane 0): S_x(0), then per key tile t: P_x(t) V_t in two key halves,
+// S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.
+template <int D, bool BF16>
+__device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t tmem, int *status,
+                                          volatile int *abort_flag, int lane) {
+  using L = PrefillSmem<D>;
+  constexpr uint32_t kIdS = tc::idesc_f16(BF16, kRows, kKeys, false, false);
+  constexpr uint32_t kIdO = tc::idesc_f16(BF16, kRows, D, false, true);
+  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  const uint64_t dq = tc::smem_desc_sw128(sb + L::kQ + x * L::kTile, 16, 1024);
+  const uint64_t dk0 = tc::smem_desc_sw128(sb + L::kK, 16, 1024);
+  const uint64_t dv0 = tc::smem_desc_sw128(sb + L::kV, L::kColBlk, 1024);
+  const uint32_t tS = tmem + x * kKeys, tO = tmem + 2 * kKeys + x * D;
+  auto s_mma = [&](int t) {
+    if (lane == 0) {
+      const uint64_t dk = dk0 + static_cast<uint64_t>(((t % kStages) * L::kTile) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * L::kColBlk + (kk & 3) * 32) >> 4);
+        tc::mma_f16(tS, dq + off, dk + off, kIdS, kk > 0);
+      }
+      tc::commit(bar(kBarS + x));
+      tc::commit(bar(kBarKFree + 2 * x + t % kStages));
+    }
+    __syncwarp();
+  };
+  auto pv_mma = [&](int t, int h) {
+    if (lane == 0) {
+      const uint64_t dv = dv0 + static_cast<uint64_t>(((t % kStages) * L::kTile) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        tc::mma_f16_tmem_a(tO, tS + 32 * h + 8 * kk,
+                           dv + static_cast<uint64_t>(((4 * h + kk) * 2048) >> 4), kIdO,
+                           (t > 0 || h > 0 || kk > 0) ? 1u : 0u);
+      if (h == 1) {
+        tc::commit(bar(kBarVFree + 2 * x + t % kStages));
+        if (t == nt - 1) tc::commit(bar(kBarO + x));
+      }
+    }
+    __syncwarp();
+  };
+  bool ok = warp_wait(bar(kBarK), 0, abort_flag);
+  if (ok) {
+    tc::fence_after_sync();
+    s_mma(0);
+  }
+  for (int t = 0; t < nt && ok; ++t) {
+    for (int h = 0; h < 2 && ok; ++h) {
+      ok = warp_wait(bar(kBarP + 2 * x + h), t & 1, abort_flag) &&
+           (h || warp_wait(bar(kBarV + t % kStages), (t / kStages) & 1, abort_flag));
+      if (!ok) break;
+      tc::fence_after_sync();
+      pv_mma(t, h);
+    }
+    if (ok && t + 1 < nt &&
+        (ok = warp_wait(bar(kBarK + (t + 1) % kStages), ((t + 1) / kStages) & 1, abort_flag))) {
+      tc::fence_after_sync();
+      s_mma(t + 1);
+    }
+  }
+  if (!ok) {
+    if (lane == 0) {
+      raise_abort(status, abort_flag);
+      tc::commit(bar(kBarDrain + x));  // arrives once every MMA issued so far is done
+    }
+    __syncwarp();
+    mbar_wait(bar(kBarDrain + x), 0);
+  }
+}
+
+// Softmax warpgroup x: lane l of warp w owns row 32 (w mod 4) + l of row tile x.
+template <int D, bool BF16>
+__device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const TilePart &part, int x,
+                                              int n_active, uint32_t sb, uint32_t tmem,
+                                              const uint8_t *smem, volatile int *abort_flag,
+                                              int warp, int lane) {
+  using L = PrefillSmem<D>;
+  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  const int r = ((warp & 3) << 5) + lane, row = part.row0 + x * kRows + r;
+  const bool real = row < p.n_rows;
+  const int lim = part.ctx + min(row, p.n_rows - 1) / p.group;  // last key the row sees
+  const int lim_all = part.ctx + (part.row0 + x * kRows) / p.group;
+  const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t tS = tmem + x * kKeys + lane_base;
+  const uint32_t tO = tmem + 2 * kKeys + x * D + lane_base;
+
+  float qsum = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = lds128(sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack2<BF16>(w[k]);
+      qsum += f.x + f.y;
+    }
+  }
+  const float2 q2 = make_float2(qsum, qsum);
+
+  float m = kNoKey, v_ref = 0.f;
+  float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
+  bool bad = false;
+  for (int t = 0; t < part.nt; ++t) {
+    // the other row tile's turn first
+    const int to = t - 1 + x;
+    if (n_active == 2 && to >= 0)
+      bad = !warp_wait(bar(kBarP + 2 * (x ^ 1)), to & 1, abort_flag) ||
+            !warp_wait(bar(kBarP + 2 * (x ^ 1) + 1), to & 1, abort_flag);
+    if (bad || !warp_wait(bar(kBarV + t % kStages), (t / kStages) & 1, abort_flag) ||
+        !warp_wait(bar(kBarS + x), t & 1, abort_flag)) {
+      bad = true;
+      break;
+    }
+    tc::fence_after_sync();
+    uint32_t s[kKeys];
+#pragma unroll
+    for (int cb = 0; cb < kKeys / 32; ++cb)
+      tc::ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(s + cb * 32));
+    const uint32_t meta = sb + L::kMeta + (t % kStages) * (kKeys / 2) * 32;
+    const float2 ref = *reinterpret_cast<const float2 *>(smem + L::kRef + 8 * (t % kStages));
+    v_ref = ref.y;
+    tc::wait_ld();
+
+    // ---- scores from the raw sums, two keys an instruction
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 2) {
+      const uint4 u = lds128(meta + c * 16);
+      const float2 e = __ffma2_rn(
+          make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+          make_float2(__uint_as_float(u.x), __uint_as_float(u.y)),
+          __fmul2_rn(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), q2));
+      s[c] = __float_as_uint(e.x);
+      s[c + 1] = __float_as_uint(e.y);
+    }
+    const int key0 = (part.t0 + t) * kKeys;
+    const bool edge = key0 + kKeys - 1 > lim_all;
+    if (edge) {
+      const int last = lim - key0;  // keys past this one are masked for the row
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c)
+        if (c > last) s[c] = __float_as_uint(-INFINITY);
+    }
+    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 8) {
+      t0 = max3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      t1 = max3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+      t2 = max3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+      t3 = max3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+    }
+    const float cand = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+    float corr = 1.f;
+    if (cand - m > kSlack) {
+      corr = ex2(m - cand);  // 0 while m was no key's
+      m = cand;
+      l2 = __fmul2_rn(l2, make_float2(corr, corr));
+      z2 = __fmul2_rn(z2, make_float2(corr, corr));
+    }
+    const bool need = corr != 1.f || ref.x != 1.f;
+    corr *= ref.x;
+    const float2 nm = make_float2(-m, -m);
+
+    // ---- weights over the S columns, two keys a column; each 64-key half is handed
+    // to the MMA warp as soon as it is written
+    auto chunk = [&](int ch, auto masked) {
+      uint32_t ph[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int c = 32 * ch + 2 * k;
+        const float2 sc = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        const float2 e = __fadd2_rn(sc, nm);
+        const float2 pr = make_float2(ex2(e.x), ex2(e.y));
+        l2 = __fadd2_rn(l2, pr);
+        const uint4 u = lds128(meta + c * 16 + 16);
+        float2 vs = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        float2 vz = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        if constexpr (decltype(masked)::value) {  // a masked row may not be finite
+          if (sc.x == -INFINITY) vs.x = vz.x = 0.f;
+          if (sc.y == -INFINITY) vs.y = vz.y = 0.f;
+        }
+        z2 = __ffma2_rn(pr, vz, z2);
+        const float2 w = __fmul2_rn(pr, vs);
+        ph[k] = pack2<BF16>(w.x, w.y);
+      }
+      tc::st16(tS + 16 * ch, ph);
+      if (ch == 1 && t > 0 && __any_sync(kFull, need)) {
+        // P_x V of the tile before has completed: S_x was issued behind it
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          tc::ld32(tO + cb * 32, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+          tc::st32(tO + cb * 32, o);
+        }
+      }
+      if (ch & 1) {
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + 2 * x + (ch >> 1)));
+      }
+    };
+    if (edge) {
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) chunk(ch, std::true_type{});
+    } else {
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) chunk(ch, std::false_type{});
+    }
+  }
+  if (!bad) bad = !warp_wait(bar(kBarO + x), 0, abort_flag);
+  if (bad) {
+    if (lane == 0) raise_abort(p.status, abort_flag);
+    return;
+  }
+  tc::fence_after_sync();
+
+  // ---- (O v_ref + z) / l in the natural order of dimensions, or the row's state
+  const bool whole = part.first == part.last;
+  const float l = l2.x + l2.y, z = z2.x + z2.y;
+  const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+  const int slot = static_cast<int>(blockIdx.x) > part.first ? 0 : part.slot;
+  float *state = p.ws + ((static_cast<size_t>(blockIdx.x) * 2 + slot) * kItemRows + x * kRows + r) *
+                            (D + 4);
+  uint16_t *dst = p.out + row_at(p, part.b, part.g, row) * D;
+#pragma unroll
+  for (int cb = 0; cb < D / 32; ++cb) {
+    uint32_t o[32];
+    tc::ld32(tO + cb * 32, o);
+    tc::wait_ld();
+    if (!real) continue;
+    float f[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // where dimension k of eight is
+      f[k] = fmaf(__uint_as_float(o[(k & ~7) + kAt[k & 7]]), v_ref, z) * inv;
+    }
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        *reinterpret_cast<uint4 *>(dst + cb * 32 + k) =
+            make_uint4(pack2<BF16>(f[k], f[k + 1]), pack2<BF16>(f[k + 2], f[k + 3]),
+                       pack2<BF16>(f[k + 4], f[k + 5]), pack2<BF16>(f[k + 6], f[k + 7]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        *reinterpret_cast<float4 *>(state + cb * 32 + k) =
+            make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    }
+  }
+  if (real && !whole) *reinterpret_cast<float2 *>(state + D) = make_float2(m, l);
+}
+
+// Row tile x of Q in the operand's order of dimensions, zeros past the rows; 128
+// threads, whose loads all go out before their first store.
+template <int D>
+__device__ __forceinline__ void load_q(const PrefillParams &p, const TilePart &part, int x,
+                                       uint32_t sb, int th) {
+  using L = PrefillSmem<D>;
+  constexpr int kPer = kRows * (D / 8) / 128;  // 16-byte chunks a thread
+  uint4 v[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int e = th + 128 * k, r = e / (D / 8), c = e % (D / 8);
+    const int row = part.row0 + x * kRows + r;
+    v[k] = make_uint4(0, 0, 0, 0);
+    if (row < p.n_rows)
+      v[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(p, part.b, part.g, row) * D +
+                                                   c * 8));
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int e = th + 128 * k, r = e / (D / 8), c = e % (D / 8);
+    st_shared_v4(sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c),
+                 __byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].x, v[k].z, 0x7632),
+                 __byte_perm(v[k].y, v[k].w, 0x5410), __byte_perm(v[k].y, v[k].w, 0x7632));
+  }
+  fence_proxy_async_smem();  // generic stores -> read by the tensor cores
+}
+
+// All threads of the CTA, at named barrier N.
+template <int N>
+__device__ __forceinline__ void cta_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(N), "n"(kThreads) : "memory");
+}
+
+// Registers a thread after the split: the softmax holds a whole row of scores.  The
+// launch's 384 x 168 cover 128 x 88 + 256 x 208.
+constexpr int kRegsLow = 88, kRegsHigh = 208;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split");
+template <int N, bool UP>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (UP)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillParams p) {
+  using L = PrefillSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kSlot + 4);
+  volatile int *any = reinterpret_cast<volatile int *>(smem + L::kSlot + 8);
+  TilePart *part_s = reinterpret_cast<TilePart *>(smem + L::kPart);
+  TileWalk *walk = reinterpret_cast<TileWalk *>(smem + L::kWalk);
+  auto init_bars = [&] {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= kBarP && i < kBarP + 4 ? 4 : 1);
+    fence_mbar_init();
+  };
+
+  griddep_wait();  // inputs may come from the previous kernel in the stream
+  griddep_release();
+  if (warp == 0) {
+    const bool have = TileWalk::start(p, lane, walk);
+    if (lane == 0) {
+      if (have) walk->next(p, *part_s);
+      else p.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      *any = have;
+      *abort_flag = 0;
+      init_bars();
+    }
+  }
+  __syncthreads();
+  if (!*any) return;
+  if (warp == 0) {
+    // S_A: columns 0-127, S_B: 128-255, O_A: 256 .. 256+D-1, O_B: 256+D .. 256+2D-1
+    tc::alloc(sb + L::kSlot, 512);
+    tc::relinquish();
+  }
+
+  // Both sides walk the parts in step: barrier 1 when Q and the part are in place,
+  // barrier 2 at its end, barrier 3 once thread 0 has planned the next one.
+  if (warp < kSoftmaxWarp0) {
+    set_registers<kRegsLow, false>();
+    for (;;) {
+      const TilePart part = *part_s;
+      const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
+      tc::fence_before_sync();
+      cta_sync<1>();
+      tc::fence_after_sync();
+      const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
+      if (warp >= kKWarp)
+        convert_tiles<D, BF16>(warp == kVWarp, p, part, sb, smem, n_active, abort_flag, lane);
+      else if (warp < n_active)
+        mma_tiles<D, BF16>(warp, part.nt, sb, tmem, p.status, abort_flag, lane);
+      tc::fence_before_sync();
+      cta_sync<2>();
+      tc::fence_after_sync();
+      const bool end = !part.more || *abort_flag;
+      if (tid == 0) {
+        if (end) {
+          // the run's last part may start an item that later CTAs hold more of
+          const int c = blockIdx.x;
+          const bool cut = part.last > c && part.first == c;
+          p.cut[2 * c] = make_int4(cut ? part.last - c + 1 : 0, part.slot, part.row0, 0);
+          p.cut[2 * c + 1] = make_int4(part.b, part.g, 0, 0);
+        } else {  // every phase of the part has been waited for: start afresh
+          for (int i = 0; i < kNumBars; ++i)
+            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(i)) : "memory");
+          init_bars();
+          walk->next(p, *part_s);
+        }
+      }
+      if (end) break;
+      cta_sync<3>();
+    }
+  } else {
+    set_registers<kRegsHigh, true>();
+    const int x = (warp - kSoftmaxWarp0) >> 2;
+    for (;;) {
+      const TilePart part = *part_s;
+      const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
+      load_q<D>(p, part, x, sb, tid & 127);
+      tc::fence_before_sync();
+      cta_sync<1>();
+      tc::fence_after_sync();
+      const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
+      if (x < n_active)
+        softmax_tiles<D, BF16>(p, part, x, n_active, sb, tmem, smem, abort_flag, warp, lane);
+      tc::fence_before_sync();
+      cta_sync<2>();
+      tc::fence_after_sync();
+      if (!part.more || *abort_flag) break;
+      cta_sync<3>();
+    }
+  }
+  __syncthreads();
+  if (warp == 0) tc::dealloc(*reinterpret_cast<volatile uint32_t *>(smem + L::kSlot), 512);
+}
+
+// ---- items cut between CTAs: block (c, y) folds the states of rows kFoldRows y .. of
+// the item that starts in CTA c's run (if any), a thread a (row, 4 dimensions)
+constexpr int kFoldRows = 16;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kFoldRows * D / 4) kv4_prefill_fold_kernel(
+    const PrefillParams p) {
+  griddep_release();
+  griddep_wait();  // the states
+  const int c = blockIdx.x;
+  const int4 cut = __ldcg(p.cut + 2 * c);
+  const int n = cut.x;
+  if (n == 0) return;
+  const int4 at = __ldcg(p.cut + 2 * c + 1);
+  const int r = blockIdx.y * kFoldRows + threadIdx.x / (D / 4);
+  const int d = 4 * (threadIdx.x % (D / 4)), row = cut.z + r;
+  if (row >= p.n_rows) return;
+  constexpr int kBatch = 4;
+  constexpr size_t kState = static_cast<size_t>(kItemRows) * (D + 4);
+  float m = kNoKey, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float *first = p.ws + (static_cast<size_t>(c) * 2 + cut.y) * kState + r * (D + 4);
+  const float *rest = p.ws + static_cast<size_t>(c) * 2 * kState + r * (D + 4);
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      ml[u] = make_float2(kNoKey, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int k = k0 + u;
+      if (k < n) {
+        const float *sp = k == 0 ? first : rest + static_cast<size_t>(k) * 2 * kState;
+        ml[u] = __ldcg(reinterpret_cast<const float2 *>(sp + D));
+        v[u] = __ldcg(reinterpret_cast<const float4 *>(sp + d));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float mn = fmaxf(m, ml[u].x);
+      const float a = ex2(m - mn), f = ex2(ml[u].x - mn);
+      acc.x = fmaf(acc.x, a, v[u].x * f);
+      acc.y = fmaf(acc.y, a, v[u].y * f);
+      acc.z = fmaf(acc.z, a, v[u].z * f);
+      acc.w = fmaf(acc.w, a, v[u].w * f);
+      l = fmaf(l, a, ml[u].y * f);
+      m = mn;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2 *>(p.out + row_at(p, at.x, at.y, row) * D + d) =
+      make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+}
+
+size_t states_bytes(int head_dim, int ctas) {
+  return static_cast<size_t>(ctas) * 2 * kItemRows * (head_dim + 4) * sizeof(float);
+}
+
+template <int D, bool BF16>
+int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
+  auto kern = kv4_prefill_kernel<D, BF16>;
+  static ContextCache<bool> smem_set;
+  if (set_smem_limit(kern, PrefillSmem<D>::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(ctas), dim3(kThreads), PrefillSmem<D>::kAlloc, stream, p) !=
+          cudaSuccess ||
+      launch_pdl(kv4_prefill_fold_kernel<D, BF16>, dim3(ctas, kItemRows / kFoldRows),
+                 dim3(kFoldRows * D / 4), 0, stream, p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
+}
+
+}  // namespace
+
+size_t kv4_tiles_workspace_bytes(int head_dim, int sms) {
+  return states_bytes(head_dim, sms) + static_cast<size_t>(sms) * 2 * sizeof(int4);
+}
+
+int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream) {
+  const int ctas = sm_count();
+  if (ctas <= 0) return PA_ERR_CUDA;
+  PrefillParams p;
+  p.q = static_cast<const uint16_t *>(a.q);
+  p.cache = a.cache;
+  p.block_table = a.block_table;
+  p.ctx_lens = a.ctx_lens;
+  p.out = static_cast<uint16_t *>(a.out);
+  p.ws = static_cast<float *>(a.workspace);
+  p.cut = reinterpret_cast<int4 *>(static_cast<char *>(a.workspace) +
+                                   states_bytes(a.head_dim, ctas));
+  p.status = a.status;
+  p.qscale = a.scale * kLog2e;
+  p.n_new = a.n_new;
+  p.n_q_heads = a.n_q_heads;
+  p.n_kv_heads = a.n_kv_heads;
+  p.group = a.n_q_heads / a.n_kv_heads;
+  p.batch = a.batch;
+  p.max_blocks = a.max_blocks;
+  p.num_pages = a.num_pages;
+  p.n_rows = a.n_new * p.group;
+  p.n_items = (p.n_rows + kItemRows - 1) / kItemRows;
+  p.page_bytes = static_cast<uint32_t>(a.n_kv_heads) * kv4::block_bytes(a.head_dim);
+  if (a.head_dim == 128)
+    return a.bf16 ? launch_t<128, true>(p, ctas, stream) : launch_t<128, false>(p, ctas, stream);
+  return a.bf16 ? launch_t<64, true>(p, ctas, stream) : launch_t<64, false>(p, ctas, stream);
+}
+
+}  // namespace pa

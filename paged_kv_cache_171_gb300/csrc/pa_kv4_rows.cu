@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         s[2 * pg + 1].x = fmaf(k1.x, fmaf(f0, acc[2], -8.f * e0), k1.y * e0);
         s[2 * pg + 1].y = fmaf(k1.x, fmaf(f1, acc[3], -8.f * e1), k1.y * e1);
       }
-      if (key0 + kPair * kPageSize > lim_all) {
+      const bool edge = key0 + kPair * kPageSize > lim_all;
+      if (edge) {
         // last key (exclusive) each of this lane's two rows sees
         const int T = min(part.tokens, part_end);
         auto limit = [&](int col) {
@@ -677,9 +678,14 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
       for (int u = 0; u < 2 * kPair; ++u) {
         const float2 pr = make_float2(ex2(d[u].x), ex2(d[u].y));
         l2 = __fadd2_rn(l2, pr);
-        z2 = make_float2(fmaf(pr.x, v[u].y, z2.x), fmaf(pr.y, v[u].y, z2.y));
         const float x = v[u].x * v_inv;
-        const float2 wt = make_float2(pr.x * x, pr.y * x);
+        float2 wt = make_float2(pr.x * x, pr.y * x);
+        float2 zt = make_float2(v[u].y, v[u].y);
+        if (OUT16 && edge) {  // a key that this row does not see may not be finite
+          if (s[u].x == -INFINITY) wt.x = zt.x = 0.f;
+          if (s[u].y == -INFINITY) wt.y = zt.y = 0.f;
+        }
+        z2 = make_float2(fmaf(pr.x, zt.x, z2.x), fmaf(pr.y, zt.y, z2.y));
         const uint32_t head = pack2<false>(wt.x, wt.y);
         const float2 back = unpack2<false>(head);
         if constexpr (WIDE) {

@@ -180,6 +180,24 @@ def test_prefill_magnitudes(n_new, dtype, q_mul, spread, scale):
     check_prefill(8, 2, n_new, [0, 333], 128, dtype, q_mul, spread, scale)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new", [5, 40, 200])
+def test_prefill_rows_that_are_not_finite_reach_only_their_queries(n_new, dtype):
+    """A key or value row that is not finite makes the queries that see it NaN, and
+    leaves the ones before it as they are."""
+    dt, gen, ctx, at = DT[dtype], torch.Generator().manual_seed(6), 30, 3
+    pool, bt = make_pool([ctx + n_new], 1, 128, dt, gen)
+    q = torch.randn((1, n_new, 4, 128), generator=gen).to(dt).cuda()
+    clean = pa.prefill_kv4(q, pool.cuda(), bt.cuda(), i32(ctx), 0.09)
+    page, slot = int(bt[0, (ctx + at) // 16]), (ctx + at) % 16
+    for which in (0, 1):
+        bad = pool.clone()
+        bad[page, 0, 16 * 128 + (which * 16 + slot) * 4:][:4] = 255  # NaN scale and zero
+        got = pa.prefill_kv4(q, bad.cuda(), bt.cuda(), i32(ctx), 0.09)
+        assert torch.equal(got[:, :at], clean[:, :at])
+        assert torch.isnan(got[:, at:]).all()
+
+
 @pytest.mark.parametrize("rot,inter", [(None, False), (1, False), (1, True), (2, False), (2, True),
                                        (16, False), (48, True)])
 @pytest.mark.parametrize("hq,hkv,d,dtype,lens", [
