@@ -2,17 +2,22 @@
 // 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
 //
 // Query i of sequence b (0 <= i < n_new) attends keys 0 .. ctx_lens[b] + i of the
-// values K = zero_k + scale_k (c - 8), V alike.  As in the row kernel only the
-// codes enter the matrix products, as exact 16-bit c - 8, and the scales and zeros
-// are applied to the scores and weights,
-//   S   = Q (c_k - 8)^T                       tcgen05, 128 x 128 x head_dim
-//   s_t = scale_k[t] S_t + zero_k[t] sum q,    p_t = 2^(s_t - m)
-//   O  += (p_t scale_v[t] / v_ref) (c_v - 8)   tcgen05, A in tensor memory
-//   z  += p_t zero_v[t],                       out = (O v_ref + z) / l
-// so a key tile is turned into 16-bit operand tiles once for 256 query rows, at no
-// rounding.  The weights are rounded once to the cache's type, as the result is.
-// v_ref is a power of two above the largest |scale_v| of the tiles so far (fp16
-// weights stay in range); when it grows, O is rescaled like at a move of m.
+// values K = zero_k + scale_k (c - 8), V alike, c the 4-bit codes.  Per row tile and
+// key tile: S = Q K^T (tcgen05, 128 x 128 x head_dim), an online softmax, and O +=
+// P V with P in tensor memory.  All operands are fp16, 11 significant bits; a key
+// tile is turned into operand tiles once for 256 query rows.
+//
+// Two forms, by the cache's type (EXACT below):
+//  * bf16: the converters store zero + scale (c - 8) rounded once to fp16, over a power
+//    of two above the tile's largest magnitude (k_ref, v_ref).  K, V and P are then
+//    off by 2^-12 each at most, an eighth of the bf16 result's own rounding, and the
+//    softmax works on S as it comes.
+//  * fp16: that would be as much as the result's rounding, so the codes enter the
+//    products exactly, as c - 8, and the softmax threads apply the rest,
+//      s_t = scale_k[t] S_t + zero_k[t] sum q,   P = p_t scale_v[t] / v_ref,
+//      z += p_t zero_v[t],                       out = (O v_ref + z) / l,
+//    reading each key's scales and zeros from shared memory.
+// When v_ref grows, O is rescaled like at a move of the running maximum.
 //
 // Tiles.  An item is 256 consecutive rows (query, head) of one kv head, whatever
 // the group size: row r is query r / G, head r % G.  It is two row tiles A and B of
@@ -25,19 +30,16 @@
 // next tile's codes in registers), warps 4-7 and 8-11 are the softmax of A and B, a
 // thread a row.  Every hand-off is an mbarrier and every wait is bounded.
 //
-// Nibbles.  (x & 0x000f000f) | 0x43004300 is the bf16 pair 128 + c of nibbles 0 and
-// 4 of a word, minus 136 is c - 8 (fp16: | 0x6400 is 1024 + c, minus 1032); the
-// other nibbles follow by shifts.  The operand tiles keep that order of dimensions
-// (0 4 1 5 2 6 3 7 of each eight): Q is stored in it, and the result is put back
-// into the natural one on its way out.
+// Nibbles.  (x & 0x000f000f) | 0x64006400 is the fp16 pair 1024 + c of nibbles 0 and
+// 4 of a word, minus 1032 is c - 8; the other nibbles follow by shifts.  The operand
+// tiles keep that order of dimensions (0 4 1 5 2 6 3 7 of each eight): Q is stored
+// in it, and the result is put back into the natural one on its way out.
 //
 // Work split.  The key tiles of all items, laid end to end, are cut into equal runs,
 // one an SM: 256 items on 152 SMs take 1.7 items' time, not two, and a single
 // sequence's chunk over a long context fills the GPU.  An item cut between CTAs
 // leaves an fp32 state (O, m, l) a row and CTA, folded by a second kernel.
-#include <cuda_bf16.h>
-
-#include <type_traits>
+#include <float.h>
 
 #include "pa_kv4.cuh"
 #include "pa_tcgen05.cuh"
@@ -63,7 +65,8 @@ struct PrefillParams {
   float *ws;    // [CTA][2][kItemRows][D + 4] partial states
   int4 *cut;    // [CTA][2] the item that starts in the CTA's run and leaves it
   int *status;
-  float qscale;  // scale * log2 e
+  float qscale;     // |scale| * log2 e, at least 1e-30
+  uint32_t qsign;   // 0x80008000 when scale < 0 (folded into Q), else 0
   int n_new, n_q_heads, n_kv_heads, group, batch, max_blocks, num_pages;
   int n_rows, n_items;  // rows a kv head, items a kv head
   uint32_t page_bytes;
@@ -76,11 +79,13 @@ struct PrefillSmem {
   static constexpr int kQ = 0;                        // Q_A, Q_B
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
-  // per stage and pair of keys: scale_k x2, zero_k x2 (both times qscale),
-  // scale_v / v_ref x2, zero_v x2; then (v_ref before / now, v_ref) per stage
+  // EXACT: per stage and pair of keys scale_k x2, zero_k x2 (both times qscale),
+  // scale_v / v_ref x2, zero_v x2.  Else kRowF: the factor of each row's S.
   static constexpr int kMeta = kV + kStages * kTile;
+  static constexpr int kRowF = kMeta;
+  // per stage: k_ref of the tile, v_ref before / now, v_ref
   static constexpr int kRef = kMeta + kStages * (kKeys / 2) * 32;
-  static constexpr int kBars = kRef + kStages * 8;
+  static constexpr int kBars = kRef + kStages * 16;
   static constexpr int kSlot = kBars + 24 * 8;        // TMEM address, abort flag
   static constexpr int kPart = kSlot + 16;
   static constexpr int kWalk = kPart + 64;
@@ -199,34 +204,35 @@ __device__ __forceinline__ size_t row_at(const PrefillParams &p, int b, int g, i
          r % p.group;
 }
 
-// The eight codes of a word as c - 8, in the order 0 4 1 5 2 6 3 7.
-template <bool BF16>
-__device__ __forceinline__ uint4 centred(uint32_t x) {
+// The eight codes of a word as c - 8 (fp16), in the order 0 4 1 5 2 6 3 7; with
+// EXACT false, zero + scale (c - 8).
+template <bool EXACT>
+__device__ __forceinline__ uint4 operand(uint32_t x, __half2 scale, __half2 zero) {
   uint32_t o[4];
-  if constexpr (BF16) {
-    const __nv_bfloat162 mid = __float2bfloat162_rn(136.f);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = ((x >> (4 * k)) & 0x000f000fu) | 0x43004300u;
-      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&w), mid);
-      o[k] = *reinterpret_cast<const uint32_t *>(&r);
-    }
-  } else {
-    const __half2 mid = __float2half2_rn(1032.f);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
-      const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&w), mid);
-      o[k] = *reinterpret_cast<const uint32_t *>(&r);
-    }
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
+    __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1032.f));
+    if constexpr (!EXACT) r = __hfma2(scale, r, zero);
+    o[k] = *reinterpret_cast<const uint32_t *>(&r);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Converter warps: codes -> operand tiles of K (which = 0) or V (1), and for V the
-// tile's scales and zeros.  Lane l takes 16-byte pieces l, l + 32, ... of the tile's
-// codes in row order, a batch of loads ahead of their conversion.
-template <int D, bool BF16>
+// A power of two above x >= 0, and at least 2^-100.
+__device__ __forceinline__ float above(float x) {
+  return fmaxf(__uint_as_float((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
+}
+
+// Converter warps: codes -> operand tiles of K (which = 0) or V (1), with the tile's
+// references (K: k_ref; V: v_ref) and, in the exact form, its scales and zeros (V).
+// Lane l takes 16-byte pieces l, l + 32, ... of the tile's codes in row order, four at
+// a time, the next four on their way meanwhile.
+//
+// A row past the sequence's end stands for zeros (it may hold anything, and 0 * NaN is
+// NaN).  A key or value row that is not finite makes its key's score NaN, which
+// masking removes for the queries that do not see it, and its values zero.
+template <int D, bool BF16, bool EXACT>
 __device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
                                               const TilePart &part, uint32_t sb, uint8_t *smem,
                                               int n_active, volatile int *abort_flag, int lane) {
@@ -234,7 +240,7 @@ __device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
   constexpr int kPieces = D / 32;                  // 16-byte pieces of a row's codes
   constexpr int kIters = kKeys * kPieces / 32;     // pieces a lane
   constexpr int kRowsIter = 32 / kPieces;          // rows an iteration
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 4, kSlots = kKeys / 32;
   auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
   const uint32_t ring = sb + (which ? L::kV : L::kK);
   const int full = which ? kBarV : kBarK, free = which ? kBarVFree : kBarKFree;
@@ -242,6 +248,7 @@ __device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
   const int n_pages = (tokens + kPageSize - 1) / kPageSize;
   const int32_t *bt_row = p.block_table + static_cast<size_t>(part.b) * p.max_blocks;
   const uint8_t *head = p.cache + static_cast<size_t>(part.g) * kv4::block_bytes(D);
+  const int piece = lane % kPieces, row_l = lane / kPieces;
   // lane l < 8: the id of page l of a tile (page 0 past the sequence's end: masked)
   auto page_id = [&](int t) {
     const int pg = (part.t0 + t) * (kKeys / kPageSize) + (lane & 7);
@@ -262,81 +269,133 @@ __device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
       const int pg = __shfl_sync(kFull, id, row / kPageSize);
       return head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * p.page_bytes;
     };
-    uint4 buf[2][kBatch];
     auto load = [&](int it0, uint4 (&to)[kBatch]) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int row = (it0 + u) * kRowsIter + lane / kPieces;
+        const int row = (it0 + u) * kRowsIter + row_l;
         to[u] = __ldg(reinterpret_cast<const uint4 *>(
-            block(row) + kv4::code_offset(D, which, row % kPageSize) + 16 * (lane % kPieces)));
+            block(row) + kv4::code_offset(D, which, row % kPageSize) + 16 * piece));
       }
     };
-    load(0, buf[0]);
-    uint32_t km[kKeys / 32], vm[kKeys / 32];
-    if (which) {
+    // scales and zeros of rows lane, lane + 32, ..
+    uint32_t km[kSlots], vm[kSlots];
 #pragma unroll
-      for (int u = 0; u < kKeys / 32; ++u) {
-        const int row = 32 * u + lane;
-        const uint8_t *blk = block(row);
-        const bool live = (part.t0 + t) * kKeys + row < tokens;
-        km[u] = vm[u] = 0;  // rows past the end may hold anything: 0 * NaN is NaN
-        if (live) {
-          km[u] = __ldg(reinterpret_cast<const uint32_t *>(
-              blk + kv4::meta_offset(D, 0, row % kPageSize)));
-          vm[u] = __ldg(reinterpret_cast<const uint32_t *>(
-              blk + kv4::meta_offset(D, 1, row % kPageSize)));
-        }
+    for (int u = 0; u < kSlots; ++u) {
+      const int row = 32 * u + lane;
+      const uint8_t *blk = block(row);
+      km[u] = vm[u] = 0;
+      if ((part.t0 + t) * kKeys + row < tokens) {
+        km[u] = __ldg(reinterpret_cast<const uint32_t *>(
+            blk + kv4::meta_offset(D, 0, row % kPageSize)));
+        vm[u] = __ldg(reinterpret_cast<const uint32_t *>(
+            blk + kv4::meta_offset(D, 1, row % kPageSize)));
       }
     }
+    uint4 now[kBatch];
+    load(0, now);
     const int s = t % kStages;
     for (int x = 0; x < n_active && ok && t >= kStages; ++x)
       ok = warp_wait(bar(free + 2 * x + s), (t / kStages - 1) & 1, abort_flag);
     if (!ok) break;
-    if (which) {
-      float top = 0.f;
+
+    // ---- references, and what the rows are converted with
+    uint32_t with[kSlots];  // half2 (scale, zero) over the reference, of this operand
+    {
+      float2 k[kSlots], v[kSlots];
+      float k_top = 0.f, v_top = 0.f;
 #pragma unroll
-      for (int u = 0; u < kKeys / 32; ++u) top = fmaxf(top, fabsf(unpack2<BF16>(vm[u]).x));
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      float ratio = 1.f;
-      if (top > v_ref) {
-        const float up = fmaxf(
-            __uint_as_float((__float_as_uint(top) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
-        ratio = v_ref / up;
-        v_ref = up;
+      for (int u = 0; u < kSlots; ++u) {
+        k[u] = unpack2<BF16>(km[u]);
+        v[u] = unpack2<BF16>(vm[u]);
+        if (!(fabsf(k[u].x) <= FLT_MAX && fabsf(k[u].y) <= FLT_MAX &&
+              fabsf(v[u].x) <= FLT_MAX && fabsf(v[u].y) <= FLT_MAX)) {
+          k[u] = make_float2(0.f, __int_as_float(0x7fc00000));
+          v[u] = make_float2(0.f, 0.f);
+        }
+        // a NaN does not count
+        k_top = fmaxf(k_top, fmaf(8.f, fabsf(k[u].x), fabsf(k[u].y)));
+        v_top = fmaxf(v_top, EXACT ? fabsf(v[u].x) : fmaf(8.f, fabsf(v[u].x), fabsf(v[u].y)));
       }
-      const float inv = v_ref > 0.f ? 1.f / v_ref : 0.f;
-      float *meta = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8;
 #pragma unroll
-      for (int u = 0; u < kKeys / 32; ++u) {
-        const int row = 32 * u + lane;
-        const float2 k = unpack2<BF16>(km[u]), v = unpack2<BF16>(vm[u]);
-        float *m = meta + (row >> 1) * 8 + (row & 1);
-        m[0] = k.x * p.qscale;
-        m[2] = k.y * p.qscale;
-        m[4] = v.x * inv;
-        m[6] = v.y;
+      for (int o = 1; o < 32; o <<= 1) {
+        k_top = fmaxf(k_top, __shfl_xor_sync(kFull, k_top, o));
+        v_top = fmaxf(v_top, __shfl_xor_sync(kFull, v_top, o));
       }
-      if (lane == 0)
-        *reinterpret_cast<float2 *>(smem + L::kRef + 8 * s) = make_float2(ratio, v_ref);
+      const float k_ref = above(k_top);
+      float ref = k_ref;
+      if (which) {
+        float ratio = 1.f;
+        if (v_top > v_ref) {
+          ratio = v_ref / above(v_top);
+          v_ref = above(v_top);
+        }
+        ref = v_ref > 0.f ? v_ref : 1.f;
+        // V's stage is free once the softmax has read these for the tile before in it
+        if (lane == 0)
+          *reinterpret_cast<float4 *>(smem + L::kRef + 16 * s) =
+              make_float4(k_ref, ratio, v_ref, 0.f);
+      }
+      const float inv = 1.f / ref;
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) {
+        if constexpr (EXACT) {
+          if (which) {
+            const int row = 32 * u + lane;
+            float *m = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8 +
+                       (row >> 1) * 8 + (row & 1);
+            m[0] = k[u].x * p.qscale;
+            m[2] = k[u].y * p.qscale;
+            m[4] = v[u].x * inv;
+            m[6] = v[u].y;
+          }
+          with[u] = 0;
+        } else {
+          const float2 a = which ? v[u] : k[u];
+          with[u] = pack2<false>(a.x * inv, a.y * inv);
+        }
+      }
     }
+
     const uint32_t dst = ring + s * L::kTile;
-#pragma unroll
+#pragma unroll 1
     for (int it0 = 0; it0 < kIters; it0 += kBatch) {
-      uint4 (&now)[kBatch] = buf[(it0 / kBatch) & 1];
-      if (it0 + kBatch < kIters) load(it0 + kBatch, buf[(it0 / kBatch + 1) & 1]);
+      uint4 next[kBatch];
+      if (it0 + kBatch < kIters) load(it0 + kBatch, next);
+      // a batch is kBatch kRowsIter rows: 32 (head_dim 128, one slot) or 64 (two)
+      constexpr int kPer = kBatch * kRowsIter / 32;
+      uint32_t mine[kPer];
+#pragma unroll
+      for (int h = 0; h < kPer; ++h) {
+        mine[h] = with[h];
+#pragma unroll
+        for (int u = kPer; u < kSlots; u += kPer)
+          if (it0 / kBatch * kPer == u) mine[h] = with[u + h];
+      }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int row = (it0 + u) * kRowsIter + lane / kPieces;
-        const int c0 = 4 * (lane % kPieces);
-        const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+        const int row = (it0 + u) * kRowsIter + row_l;
+        __half2 scale = __float2half2_rn(0.f), zero = scale;
+        if constexpr (!EXACT) {
+          const uint32_t sz = __shfl_sync(kFull, mine[u * kPer / kBatch], row % 32);
+          const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
+          scale = *reinterpret_cast<const __half2 *>(&s2);
+          zero = *reinterpret_cast<const __half2 *>(&z2);
+        }
+        // the upper column block's pieces go in another order: no two lanes of a
+        // store meet in a bank
+        const bool upper = piece >= 2;
+        const uint32_t w[4] = {upper ? now[u].z : now[u].x, upper ? now[u].w : now[u].y,
+                               upper ? now[u].x : now[u].z, upper ? now[u].y : now[u].w};
+        const int flip = upper ? 2 : 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 o = centred<BF16>(w[k]);
-          const int c = c0 + k;
+          const uint4 o = operand<EXACT>(w[k], scale, zero);
+          const int c = 4 * piece + (k ^ flip);
           st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(row, c), o.x, o.y, o.z, o.w);
         }
       }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) now[u] = next[u];
     }
     fence_proxy_async_smem();  // generic stores -> read by the tensor cores
     __syncwarp();
@@ -351,12 +410,12 @@ __device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
 
 // MMA warp x (lane 0): S_x(0), then per key tile t: P_x(t) V_t in two key halves,
 // S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.
-template <int D, bool BF16>
+template <int D>
 __device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t tmem, int *status,
                                           volatile int *abort_flag, int lane) {
   using L = PrefillSmem<D>;
-  constexpr uint32_t kIdS = tc::idesc_f16(BF16, kRows, kKeys, false, false);
-  constexpr uint32_t kIdO = tc::idesc_f16(BF16, kRows, D, false, true);
+  constexpr uint32_t kIdS = tc::idesc_f16(false, kRows, kKeys, false, false);
+  constexpr uint32_t kIdO = tc::idesc_f16(false, kRows, D, false, true);
   auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
   const uint64_t dq = tc::smem_desc_sw128(sb + L::kQ + x * L::kTile, 16, 1024);
   const uint64_t dk0 = tc::smem_desc_sw128(sb + L::kK, 16, 1024);
@@ -420,38 +479,44 @@ __device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t t
 }
 
 // Softmax warpgroup x: lane l of warp w owns row 32 (w mod 4) + l of row tile x.
-template <int D, bool BF16>
-__device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const TilePart &part, int x,
+template <int D, bool BF16, bool EXACT>
+__device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const volatile TilePart &part, int x,
                                               int n_active, uint32_t sb, uint32_t tmem,
                                               const uint8_t *smem, volatile int *abort_flag,
                                               int warp, int lane) {
   using L = PrefillSmem<D>;
   auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
-  const int r = ((warp & 3) << 5) + lane, row = part.row0 + x * kRows + r;
-  const bool real = row < p.n_rows;
-  const int lim = part.ctx + min(row, p.n_rows - 1) / p.group;  // last key the row sees
+  const int r = ((warp & 3) << 5) + lane;
+  // last key that the row sees, and that every row of the tile sees
+  const int lim = part.ctx + min(part.row0 + x * kRows + r, p.n_rows - 1) / p.group;
   const int lim_all = part.ctx + (part.row0 + x * kRows) / p.group;
+  const int nt = part.nt;
+  int key0 = part.t0 * kKeys;
   const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t tS = tmem + x * kKeys + lane_base;
   const uint32_t tO = tmem + 2 * kKeys + x * D + lane_base;
 
-  float qsum = 0.f;
+  float qsum = 0.f, row_f = 0.f;
+  if constexpr (EXACT) {
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    const uint4 v = lds128(sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 v = lds128(sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack2<BF16>(w[k]);
-      qsum += f.x + f.y;
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<false>(w[k]);
+        qsum += f.x + f.y;
+      }
     }
+  } else {
+    row_f = reinterpret_cast<const float *>(smem + L::kRowF)[x * kRows + r];
   }
   const float2 q2 = make_float2(qsum, qsum);
 
   float m = kNoKey, v_ref = 0.f;
   float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
   bool bad = false;
-  for (int t = 0; t < part.nt; ++t) {
+  for (int t = 0; t < nt; ++t, key0 += kKeys) {
     // the other row tile's turn first
     const int to = t - 1 + x;
     if (n_active == 2 && to >= 0)
@@ -468,24 +533,24 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const Tile
     for (int cb = 0; cb < kKeys / 32; ++cb)
       tc::ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(s + cb * 32));
     const uint32_t meta = sb + L::kMeta + (t % kStages) * (kKeys / 2) * 32;
-    const float2 ref = *reinterpret_cast<const float2 *>(smem + L::kRef + 8 * (t % kStages));
-    v_ref = ref.y;
+    const float4 ref = *reinterpret_cast<const float4 *>(smem + L::kRef + 16 * (t % kStages));
+    v_ref = ref.z;
+    const float f = EXACT ? 1.f : row_f * ref.x;  // scores = f S
     tc::wait_ld();
 
-    // ---- scores from the raw sums, two keys an instruction
+    if constexpr (EXACT) {  // scores from the raw sums, two keys an instruction
 #pragma unroll
-    for (int c = 0; c < kKeys; c += 2) {
-      const uint4 u = lds128(meta + c * 16);
-      const float2 e = __ffma2_rn(
-          make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-          make_float2(__uint_as_float(u.x), __uint_as_float(u.y)),
-          __fmul2_rn(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), q2));
-      s[c] = __float_as_uint(e.x);
-      s[c + 1] = __float_as_uint(e.y);
+      for (int c = 0; c < kKeys; c += 2) {
+        const uint4 u = lds128(meta + c * 16);
+        const float2 e = __ffma2_rn(
+            make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+            make_float2(__uint_as_float(u.x), __uint_as_float(u.y)),
+            __fmul2_rn(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), q2));
+        s[c] = __float_as_uint(e.x);
+        s[c + 1] = __float_as_uint(e.y);
+      }
     }
-    const int key0 = (part.t0 + t) * kKeys;
-    const bool edge = key0 + kKeys - 1 > lim_all;
-    if (edge) {
+    if (key0 + kKeys - 1 > lim_all) {
       const int last = lim - key0;  // keys past this one are masked for the row
 #pragma unroll
       for (int c = 0; c < kKeys; ++c)
@@ -499,7 +564,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const Tile
       t2 = max3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
       t3 = max3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
     }
-    const float cand = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+    const float cand = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * f;
     float corr = 1.f;
     if (cand - m > kSlack) {
       corr = ex2(m - cand);  // 0 while m was no key's
@@ -507,31 +572,30 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const Tile
       l2 = __fmul2_rn(l2, make_float2(corr, corr));
       z2 = __fmul2_rn(z2, make_float2(corr, corr));
     }
-    const bool need = corr != 1.f || ref.x != 1.f;
-    corr *= ref.x;
-    const float2 nm = make_float2(-m, -m);
+    const bool need = corr != 1.f || ref.y != 1.f;
+    corr *= ref.y;
+    const float2 nm = make_float2(-m, -m), f2 = make_float2(f, f);
 
     // ---- weights over the S columns, two keys a column; each 64-key half is handed
     // to the MMA warp as soon as it is written
-    auto chunk = [&](int ch, auto masked) {
+    auto chunk = [&](int ch) {
       uint32_t ph[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int c = 32 * ch + 2 * k;
         const float2 sc = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        const float2 e = __fadd2_rn(sc, nm);
+        const float2 e = EXACT ? __fadd2_rn(sc, nm) : __ffma2_rn(sc, f2, nm);
         const float2 pr = make_float2(ex2(e.x), ex2(e.y));
         l2 = __fadd2_rn(l2, pr);
-        const uint4 u = lds128(meta + c * 16 + 16);
-        float2 vs = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-        float2 vz = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-        if constexpr (decltype(masked)::value) {  // a masked row may not be finite
-          if (sc.x == -INFINITY) vs.x = vz.x = 0.f;
-          if (sc.y == -INFINITY) vs.y = vz.y = 0.f;
+        if constexpr (EXACT) {
+          const uint4 u = lds128(meta + c * 16 + 16);
+          z2 = __ffma2_rn(pr, make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), z2);
+          const float2 w =
+              __fmul2_rn(pr, make_float2(__uint_as_float(u.x), __uint_as_float(u.y)));
+          ph[k] = pack2<false>(w.x, w.y);
+        } else {
+          ph[k] = pack2<false>(pr.x, pr.y);
         }
-        z2 = __ffma2_rn(pr, vz, z2);
-        const float2 w = __fmul2_rn(pr, vs);
-        ph[k] = pack2<BF16>(w.x, w.y);
       }
       tc::st16(tS + 16 * ch, ph);
       if (ch == 1 && t > 0 && __any_sync(kFull, need)) {
@@ -553,13 +617,8 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const Tile
         if (lane == 0) mbar_arrive(bar(kBarP + 2 * x + (ch >> 1)));
       }
     };
-    if (edge) {
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) chunk(ch, std::true_type{});
-    } else {
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) chunk(ch, std::false_type{});
-    }
+    for (int ch = 0; ch < 4; ++ch) chunk(ch);
   }
   if (!bad) bad = !warp_wait(bar(kBarO + x), 0, abort_flag);
   if (bad) {
@@ -569,7 +628,8 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const Tile
   tc::fence_after_sync();
 
   // ---- (O v_ref + z) / l in the natural order of dimensions, or the row's state
-  const bool whole = part.first == part.last;
+  const int row = part.row0 + x * kRows + r;
+  const bool real = row < p.n_rows, whole = part.first == part.last;
   const float l = l2.x + l2.y, z = z2.x + z2.y;
   const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
   const int slot = static_cast<int>(blockIdx.x) > part.first ? 0 : part.slot;
@@ -604,17 +664,18 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const Tile
   if (real && !whole) *reinterpret_cast<float2 *>(state + D) = make_float2(m, l);
 }
 
-// Row tile x of Q in the operand's order of dimensions, zeros past the rows; 128
-// threads, whose loads all go out before their first store.
-template <int D>
-__device__ __forceinline__ void load_q(const PrefillParams &p, const TilePart &part, int x,
-                                       uint32_t sb, int th) {
+// Row tile x of Q in the operand's order of dimensions, zeros past the rows, by 128
+// threads; not exact: as fp16 over a power of two a row, whose product with the score
+// factor goes to kRowF.  A thread's loads all go out before its first store.
+template <int D, bool BF16, bool EXACT>
+__device__ __forceinline__ void load_q(const PrefillParams &p, const volatile TilePart &part,
+                                       int x, uint32_t sb, uint8_t *smem, int th) {
   using L = PrefillSmem<D>;
-  constexpr int kPer = kRows * (D / 8) / 128;  // 16-byte chunks a thread
+  constexpr int kChunks = D / 8, kPer = kRows * kChunks / 128;  // 16-byte chunks: a row, a thread
   uint4 v[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int e = th + 128 * k, r = e / (D / 8), c = e % (D / 8);
+    const int e = th + 128 * k, r = e / kChunks, c = e % kChunks;
     const int row = part.row0 + x * kRows + r;
     v[k] = make_uint4(0, 0, 0, 0);
     if (row < p.n_rows)
@@ -623,10 +684,30 @@ __device__ __forceinline__ void load_q(const PrefillParams &p, const TilePart &p
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int e = th + 128 * k, r = e / (D / 8), c = e % (D / 8);
+    const int e = th + 128 * k, r = e / kChunks, c = e % kChunks;
+    uint32_t w[4] = {v[k].x ^ p.qsign, v[k].y ^ p.qsign, v[k].z ^ p.qsign, v[k].w ^ p.qsign};
+    if constexpr (!EXACT) {
+      float2 f[4];
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        f[u] = unpack2<BF16>(w[u]);
+        top = fmaxf(top, fmaxf(fabsf(f[u].x), fabsf(f[u].y)));
+      }
+#pragma unroll
+      for (int o = 1; o < kChunks; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      // 2^ex brings the row's largest magnitude into [2^14, 2^15)
+      const int ex = min(90, max(-90, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = pack2<false>(f[u].x * up, f[u].y * up);
+      if (c == 0)
+        reinterpret_cast<float *>(smem + L::kRowF)[x * kRows + r] =
+            p.qscale * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+    }
     st_shared_v4(sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c),
-                 __byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].x, v[k].z, 0x7632),
-                 __byte_perm(v[k].y, v[k].w, 0x5410), __byte_perm(v[k].y, v[k].w, 0x7632));
+                 __byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
+                 __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
   }
   fence_proxy_async_smem();  // generic stores -> read by the tensor cores
 }
@@ -652,6 +733,7 @@ __device__ __forceinline__ void set_registers() {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillParams p) {
   using L = PrefillSmem<D>;
+  constexpr bool EXACT = !BF16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -699,9 +781,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
       tc::fence_after_sync();
       const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
       if (warp >= kKWarp)
-        convert_tiles<D, BF16>(warp == kVWarp, p, part, sb, smem, n_active, abort_flag, lane);
+        convert_tiles<D, BF16, EXACT>(warp == kVWarp, p, part, sb, smem, n_active, abort_flag, lane);
       else if (warp < n_active)
-        mma_tiles<D, BF16>(warp, part.nt, sb, tmem, p.status, abort_flag, lane);
+        mma_tiles<D>(warp, part.nt, sb, tmem, p.status, abort_flag, lane);
       tc::fence_before_sync();
       cta_sync<2>();
       tc::fence_after_sync();
@@ -727,19 +809,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     set_registers<kRegsHigh, true>();
     const int x = (warp - kSoftmaxWarp0) >> 2;
     for (;;) {
-      const TilePart part = *part_s;
-      const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
-      load_q<D>(p, part, x, sb, tid & 127);
+      const int n_active = part_s->row0 + kRows < p.n_rows ? 2 : 1;
+      const bool more = part_s->more;
+      load_q<D, BF16, EXACT>(p, *part_s, x, sb, smem, tid & 127);
       tc::fence_before_sync();
       cta_sync<1>();
       tc::fence_after_sync();
       const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
       if (x < n_active)
-        softmax_tiles<D, BF16>(p, part, x, n_active, sb, tmem, smem, abort_flag, warp, lane);
+        softmax_tiles<D, BF16, EXACT>(p, *part_s, x, n_active, sb, tmem, smem, abort_flag, warp, lane);
       tc::fence_before_sync();
       cta_sync<2>();
       tc::fence_after_sync();
-      if (!part.more || *abort_flag) break;
+      if (!more || *abort_flag) break;
       cta_sync<3>();
     }
   }
@@ -836,7 +918,10 @@ int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.cut = reinterpret_cast<int4 *>(static_cast<char *>(a.workspace) +
                                    states_bytes(a.head_dim, ctas));
   p.status = a.status;
-  p.qscale = a.scale * kLog2e;
+  // The maximum is taken over raw sums, so their factor has to be positive: a negative
+  // scale flips the sign of Q instead, a zero scale becomes one that makes every weight 1.
+  p.qscale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+  p.qsign = a.scale < 0.f ? 0x80008000u : 0u;
   p.n_new = a.n_new;
   p.n_q_heads = a.n_q_heads;
   p.n_kv_heads = a.n_kv_heads;

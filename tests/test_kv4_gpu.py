@@ -181,6 +181,27 @@ def test_prefill_magnitudes(n_new, dtype, q_mul, spread, scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("n_new,ctx", [(6, 5000), (300, 4000)])
+def test_prefill_magnitudes_along_the_context(n_new, ctx, order, dtype):
+    """K and V whose magnitude grows, or shrinks, along a long context: each tile of
+    keys with scales of its own."""
+    dt, gen, n = DT[dtype], torch.Generator().manual_seed(8), n_new + ctx
+    pool, bt = make_pool([n], 1, 128, dt, gen, junk=False)
+    by = 4.0 ** (order * torch.linspace(-2, 2, n))[:, None, None]
+    k = torch.randn((n, 1, 128), generator=gen) * by
+    v = torch.randn((n, 1, 128), generator=gen) * by
+    ref.store(pool, bt, *tokens_of([n]), k, v, dt)
+    q = (torch.randn((1, n_new, 4, 128), generator=gen) * 0.1).to(dt)
+    seen = [[ctx + i + 1 for i in range(n_new)]]
+    want, _ = ref.attention(q.cuda(), pool.cuda(), bt, seen, 0.09, dt)
+    got = pa.prefill_kv4(q.cuda(), pool.cuda(), bt.cuda(), i32(ctx), 0.09)
+    rel = float((got.double() - want).norm() / want.norm())
+    # four roundings of half a step each at most: K, V, the weights and the result
+    assert rel < 4 * torch.finfo(dt).eps / 2, rel
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("n_new", [5, 40, 200])
 def test_prefill_rows_that_are_not_finite_reach_only_their_queries(n_new, dtype):
     """A key or value row that is not finite makes the queries that see it NaN, and
