@@ -9,15 +9,16 @@
 //
 // Two forms, by the cache's type (EXACT below):
 //  * bf16: the converters store zero + scale (c - 8) rounded once to fp16, over a power
-//    of two above the tile's largest magnitude (k_ref, v_ref).  K, V and P are then
+//    of two above the largest magnitude of 32 keys (k_ref, v_ref).  K, V and P are then
 //    off by 2^-12 each at most, an eighth of the bf16 result's own rounding, and the
-//    softmax works on S as it comes.
+//    softmax works on S as it comes: a factor for each 32 keys in its exponent.
 //  * fp16: that would be as much as the result's rounding, so the codes enter the
 //    products exactly, as c - 8, and the softmax threads apply the rest,
 //      s_t = scale_k[t] S_t + zero_k[t] sum q,   P = p_t scale_v[t] / v_ref,
 //      z += p_t zero_v[t],                       out = (O v_ref + z) / l,
 //    reading each key's scales and zeros from shared memory.
-// When v_ref grows, O is rescaled like at a move of the running maximum.
+// P carries v_ref over the largest v_ref so far; when that grows, O is rescaled like
+// at a move of the running maximum.
 //
 // Tiles.  An item is 256 consecutive rows (query, head) of one kv head, whatever
 // the group size: row r is query r / G, head r % G.  It is two row tiles A and B of
@@ -25,10 +26,11 @@
 // alternates between them: B's softmax of key tile j starts once A has handed over
 // its weights of j, A's of j + 1 once B has handed over those of j.
 //
-// Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B,
-// warps 2 and 3 turn codes into the K and V operand tiles (two stages each, the
-// next tile's codes in registers), warps 4-7 and 8-11 are the softmax of A and B, a
-// thread a row.  Every hand-off is an mbarrier and every wait is bounded.
+// Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B, warps
+// 4-7 turn codes into the K and V operand tiles (two stages each): a warp 32 keys of
+// each tile, from a ring of pages that it fills for itself by bulk copies.  Warps 8-11
+// and 12-15 are the softmax of A and B, a thread a row.  Every hand-off is an mbarrier
+// and every wait is bounded.
 //
 // Nibbles.  (x & 0x000f000f) | 0x64006400 is the fp16 pair 1024 + c of nibbles 0 and
 // 4 of a word, minus 1032 is c - 8; the other nibbles follow by shifts.  The operand
@@ -54,8 +56,9 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 128, kKeys = 128;     // a row tile, a key tile
 constexpr int kItemRows = 2 * kRows;
 constexpr int kStages = 2;                  // of K and of V
-constexpr int kKWarp = 2, kVWarp = 3, kSoftmaxWarp0 = 4;
-constexpr int kThreads = 12 * 32;
+constexpr int kConvertWarp0 = 4, kConverters = 4, kSoftmaxWarp0 = 8;
+constexpr int kThreads = 16 * 32;
+constexpr int kRawPages = 3;                // a converter warp's ring
 
 struct PrefillParams {
   const uint16_t *q;
@@ -83,10 +86,11 @@ struct PrefillSmem {
   // scale_v / v_ref x2, zero_v x2.  Else kRowF: the factor of each row's S.
   static constexpr int kMeta = kV + kStages * kTile;
   static constexpr int kRowF = kMeta;
-  // per stage: k_ref of the tile, v_ref before / now, v_ref
-  static constexpr int kRef = kMeta + kStages * (kKeys / 2) * 32;
-  static constexpr int kBars = kRef + kStages * 16;
-  static constexpr int kSlot = kBars + 24 * 8;        // TMEM address, abort flag
+  static constexpr int kRaw = kMeta + kStages * (kKeys / 2) * 32;  // the converters' pages
+  // per stage: k_ref of each 32 keys, then v_ref
+  static constexpr int kRef = kRaw + kConverters * kRawPages * kv4::block_bytes(D);
+  static constexpr int kBars = kRef + kStages * 32;
+  static constexpr int kSlot = kBars + 34 * 8;        // TMEM address, abort flag
   static constexpr int kPart = kSlot + 16;
   static constexpr int kWalk = kPart + 64;
   static constexpr int kBytes = kWalk + 64;
@@ -95,15 +99,16 @@ struct PrefillSmem {
 };
 
 enum {
-  kBarK = 0,       // K stage s converted, at + s (one arrival)
-  kBarV = 2,       // V stage s and its metas
+  kBarK = 0,       // K stage s converted, at + s (4 arrivals)
+  kBarV = 2,       // V stage s and its references (4 arrivals)
   kBarKFree = 4,   // K stage s read by row tile x's S MMA (commit), at + 2 x + s
   kBarVFree = 8,   // V stage s read by row tile x's P V MMAs, at + 2 x + s
   kBarS = 12,      // S_x in TMEM (commit), at + x
   kBarP = 14,      // keys 64 h .. 64 h + 63 of P_x in TMEM, at + 2 x + h (4 arrivals)
   kBarO = 18,      // the last P_x V done (commit), at + x
   kBarDrain = 20,  // an MMA warp's own drain on its failure path, at + x
-  kNumBars = 22
+  kBarRaw = 22,    // page s of converter w's ring (bulk copy), at + 3 w + s
+  kNumBars = 34
 };
 
 // The part of one item that a CTA's run holds.
@@ -224,187 +229,181 @@ __device__ __forceinline__ float above(float x) {
   return fmaxf(__uint_as_float((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
 }
 
-// Converter warps: codes -> operand tiles of K (which = 0) or V (1), with the tile's
-// references (K: k_ref; V: v_ref) and, in the exact form, its scales and zeros (V).
-// Lane l takes 16-byte pieces l, l + 32, ... of the tile's codes in row order, four at
-// a time, the next four on their way meanwhile.
+// The exponent of a power of two, and 2^k for -126 <= k <= 127.
+__device__ __forceinline__ int exponent(float x) {
+  return static_cast<int>(__float_as_uint(x) >> 23) - 127;
+}
+__device__ __forceinline__ float exp2i(int k) {
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Converter warp w: keys 32 w .. 32 w + 31 (two pages) of every key tile, K then V,
+// and their references and, in the exact form, scales and zeros.
 //
 // A row past the sequence's end stands for zeros (it may hold anything, and 0 * NaN is
 // NaN).  A key or value row that is not finite makes its key's score NaN, which
 // masking removes for the queries that do not see it, and its values zero.
 template <int D, bool BF16, bool EXACT>
-__device__ __forceinline__ void convert_tiles(int which, const PrefillParams &p,
+__device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
                                               const TilePart &part, uint32_t sb, uint8_t *smem,
                                               int n_active, volatile int *abort_flag, int lane) {
   using L = PrefillSmem<D>;
-  constexpr int kPieces = D / 32;                  // 16-byte pieces of a row's codes
-  constexpr int kIters = kKeys * kPieces / 32;     // pieces a lane
-  constexpr int kRowsIter = 32 / kPieces;          // rows an iteration
-  constexpr int kBatch = 4, kSlots = kKeys / 32;
+  constexpr int kBlock = kv4::block_bytes(D);
+  constexpr int kPieces = D / 32;                // 16-byte pieces of a row's codes
+  constexpr int kIters = kPageSize * kPieces / 32;  // pieces a lane and page
+  constexpr int kPagesTile = kKeys / kPageSize;
   auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
-  const uint32_t ring = sb + (which ? L::kV : L::kK);
-  const int full = which ? kBarV : kBarK, free = which ? kBarVFree : kBarKFree;
   const int tokens = part.ctx + p.n_new;
   const int n_pages = (tokens + kPageSize - 1) / kPageSize;
   const int32_t *bt_row = p.block_table + static_cast<size_t>(part.b) * p.max_blocks;
-  const uint8_t *head = p.cache + static_cast<size_t>(part.g) * kv4::block_bytes(D);
+  const uint8_t *head = p.cache + static_cast<size_t>(part.g) * kBlock;
   const int piece = lane % kPieces, row_l = lane / kPieces;
-  // lane l < 8: the id of page l of a tile (page 0 past the sequence's end: masked)
-  auto page_id = [&](int t) {
-    const int pg = (part.t0 + t) * (kKeys / kPageSize) + (lane & 7);
+  const uint32_t raw0 = sb + L::kRaw + w * kRawPages * kBlock;
+
+  // Page ids: lane l holds page l & 1 of the warp's two in tile 16 v + (l >> 1), v the
+  // window; past the sequence's end page 0, which is masked.
+  auto ids_of = [&](int v) {
+    const int t = 16 * v + (lane >> 1);
+    const int pg = (part.t0 + t) * kPagesTile + 2 * w + (lane & 1);
     return t < part.nt && pg < n_pages ? __ldg(bt_row + pg) : 0;
   };
-  float v_ref = 0.f;
-  int raw = page_id(0);
+  int ids = ids_of(0), ids_next = ids_of(1);
+  int issued = 0;  // the warp's pages, 2 a tile; page i sits in ring slot i % kRawPages
+  auto issue = [&]() {
+    if ((issued & 31) == 0 && issued > 0) {
+      ids = ids_next;
+      ids_next = ids_of((issued >> 5) + 1);
+    }
+    int id = __shfl_sync(kFull, ids, issued & 31);
+    if (lane == 0) {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
+        record_error(p.status, PA_ERR_BAD_BLOCK);
+        id = 0;
+      }
+      const int s = issued % kRawPages;
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(bar(kBarRaw + kRawPages * w + s), kBlock);
+      bulk_load(raw0 + s * kBlock,
+                head + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes, kBlock,
+                bar(kBarRaw + kRawPages * w + s));
+    }
+    ++issued;
+  };
+  const int total = 2 * part.nt;
+  while (issued < kRawPages && issued < total) issue();
+
   bool ok = true;
   int t = 0;
   for (; t < part.nt; ++t) {
-    int id = raw;
-    raw = page_id(t + 1);
-    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
-      if (lane < 8) record_error(p.status, PA_ERR_BAD_BLOCK);
-      id = 0;
-    }
-    auto block = [&](int row) {  // of the tile's row (all lanes take part)
-      const int pg = __shfl_sync(kFull, id, row / kPageSize);
-      return head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * p.page_bytes;
-    };
-    auto load = [&](int it0, uint4 (&to)[kBatch]) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int row = (it0 + u) * kRowsIter + row_l;
-        to[u] = __ldg(reinterpret_cast<const uint4 *>(
-            block(row) + kv4::code_offset(D, which, row % kPageSize) + 16 * piece));
-      }
-    };
-    // scales and zeros of rows lane, lane + 32, ..
-    uint32_t km[kSlots], vm[kSlots];
-#pragma unroll
-    for (int u = 0; u < kSlots; ++u) {
-      const int row = 32 * u + lane;
-      const uint8_t *blk = block(row);
-      km[u] = vm[u] = 0;
-      if ((part.t0 + t) * kKeys + row < tokens) {
-        km[u] = __ldg(reinterpret_cast<const uint32_t *>(
-            blk + kv4::meta_offset(D, 0, row % kPageSize)));
-        vm[u] = __ldg(reinterpret_cast<const uint32_t *>(
-            blk + kv4::meta_offset(D, 1, row % kPageSize)));
-      }
-    }
-    uint4 now[kBatch];
-    load(0, now);
-    const int s = t % kStages;
-    for (int x = 0; x < n_active && ok && t >= kStages; ++x)
-      ok = warp_wait(bar(free + 2 * x + s), (t / kStages - 1) & 1, abort_flag);
+    for (int i = 2 * t; i < 2 * t + 2 && ok; ++i)
+      ok = warp_wait(bar(kBarRaw + kRawPages * w + i % kRawPages), (i / kRawPages) & 1,
+                     abort_flag);
     if (!ok) break;
-
-    // ---- references, and what the rows are converted with
-    uint32_t with[kSlots];  // half2 (scale, zero) over the reference, of this operand
+    const uint32_t raw[2] = {raw0 + ((2 * t) % kRawPages) * kBlock,
+                             raw0 + ((2 * t + 1) % kRawPages) * kBlock};
+    // ---- scales and zeros of row `lane` of the warp's 32
+    float2 k, v;
     {
-      float2 k[kSlots], v[kSlots];
-      float k_top = 0.f, v_top = 0.f;
-#pragma unroll
-      for (int u = 0; u < kSlots; ++u) {
-        k[u] = unpack2<BF16>(km[u]);
-        v[u] = unpack2<BF16>(vm[u]);
-        if (!(fabsf(k[u].x) <= FLT_MAX && fabsf(k[u].y) <= FLT_MAX &&
-              fabsf(v[u].x) <= FLT_MAX && fabsf(v[u].y) <= FLT_MAX)) {
-          k[u] = make_float2(0.f, __int_as_float(0x7fc00000));
-          v[u] = make_float2(0.f, 0.f);
-        }
-        // a NaN does not count
-        k_top = fmaxf(k_top, fmaf(8.f, fabsf(k[u].x), fabsf(k[u].y)));
-        v_top = fmaxf(v_top, EXACT ? fabsf(v[u].x) : fmaf(8.f, fabsf(v[u].x), fabsf(v[u].y)));
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        k_top = fmaxf(k_top, __shfl_xor_sync(kFull, k_top, o));
-        v_top = fmaxf(v_top, __shfl_xor_sync(kFull, v_top, o));
-      }
-      const float k_ref = above(k_top);
-      float ref = k_ref;
-      if (which) {
-        float ratio = 1.f;
-        if (v_top > v_ref) {
-          ratio = v_ref / above(v_top);
-          v_ref = above(v_top);
-        }
-        ref = v_ref > 0.f ? v_ref : 1.f;
-        // V's stage is free once the softmax has read these for the tile before in it
-        if (lane == 0)
-          *reinterpret_cast<float4 *>(smem + L::kRef + 16 * s) =
-              make_float4(k_ref, ratio, v_ref, 0.f);
-      }
-      const float inv = 1.f / ref;
-#pragma unroll
-      for (int u = 0; u < kSlots; ++u) {
-        if constexpr (EXACT) {
-          if (which) {
-            const int row = 32 * u + lane;
-            float *m = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8 +
-                       (row >> 1) * 8 + (row & 1);
-            m[0] = k[u].x * p.qscale;
-            m[2] = k[u].y * p.qscale;
-            m[4] = v[u].x * inv;
-            m[6] = v[u].y;
-          }
-          with[u] = 0;
-        } else {
-          const float2 a = which ? v[u] : k[u];
-          with[u] = pack2<false>(a.x * inv, a.y * inv);
-        }
-      }
+      const uint32_t blk = lane < kPageSize ? raw[0] : raw[1];
+      k = unpack2<BF16>(lds32(blk + kv4::meta_offset(D, 0, 0) + 4 * (lane % kPageSize)));
+      v = unpack2<BF16>(lds32(blk + kv4::meta_offset(D, 1, 0) + 4 * (lane % kPageSize)));
     }
+    if ((part.t0 + t) * kKeys + 32 * w + lane >= tokens) {
+      k = v = make_float2(0.f, 0.f);
+    } else if (!(fabsf(k.x) <= FLT_MAX && fabsf(k.y) <= FLT_MAX && fabsf(v.x) <= FLT_MAX &&
+                 fabsf(v.y) <= FLT_MAX)) {
+      k = make_float2(0.f, __int_as_float(0x7fc00000));
+      v = make_float2(0.f, 0.f);
+    }
+    float k_top = EXACT ? 0.f : fmaf(8.f, fabsf(k.x), fabsf(k.y));  // a NaN does not count
+    float v_top = EXACT ? fabsf(v.x) : fmaf(8.f, fabsf(v.x), fabsf(v.y));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      if (!EXACT) k_top = fmaxf(k_top, __shfl_xor_sync(kFull, k_top, o));
+      v_top = fmaxf(v_top, __shfl_xor_sync(kFull, v_top, o));
+    }
+    const float k_ref = EXACT ? 1.f : above(k_top), v_ref = above(v_top);
 
-    const uint32_t dst = ring + s * L::kTile;
+    const int s = t % kStages;
 #pragma unroll 1
-    for (int it0 = 0; it0 < kIters; it0 += kBatch) {
-      uint4 next[kBatch];
-      if (it0 + kBatch < kIters) load(it0 + kBatch, next);
-      // a batch is kBatch kRowsIter rows: 32 (head_dim 128, one slot) or 64 (two)
-      constexpr int kPer = kBatch * kRowsIter / 32;
-      uint32_t mine[kPer];
-#pragma unroll
-      for (int h = 0; h < kPer; ++h) {
-        mine[h] = with[h];
-#pragma unroll
-        for (int u = kPer; u < kSlots; u += kPer)
-          if (it0 / kBatch * kPer == u) mine[h] = with[u + h];
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int row = (it0 + u) * kRowsIter + row_l;
-        __half2 scale = __float2half2_rn(0.f), zero = scale;
-        if constexpr (!EXACT) {
-          const uint32_t sz = __shfl_sync(kFull, mine[u * kPer / kBatch], row % 32);
-          const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
-          scale = *reinterpret_cast<const __half2 *>(&s2);
-          zero = *reinterpret_cast<const __half2 *>(&z2);
-        }
-        // the upper column block's pieces go in another order: no two lanes of a
-        // store meet in a bank
-        const bool upper = piece >= 2;
-        const uint32_t w[4] = {upper ? now[u].z : now[u].x, upper ? now[u].w : now[u].y,
-                               upper ? now[u].x : now[u].z, upper ? now[u].y : now[u].w};
-        const int flip = upper ? 2 : 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 o = operand<EXACT>(w[k], scale, zero);
-          const int c = 4 * piece + (k ^ flip);
-          st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(row, c), o.x, o.y, o.z, o.w);
+    for (int which = 0; which < 2; ++which) {
+      const int free = which ? kBarVFree : kBarKFree;
+      for (int x = 0; x < n_active && ok && t >= kStages; ++x)
+        ok = warp_wait(bar(free + 2 * x + s), (t / kStages - 1) & 1, abort_flag);
+      if (!ok) break;
+      const float inv = 1.f / (which ? v_ref : k_ref);
+      const float2 own = which ? v : k;
+      const uint32_t with = pack2<false>(own.x * inv, own.y * inv);
+      if (which) {
+        // V's stage is free once the softmax has read these for the tile before in it
+        float *refs = reinterpret_cast<float *>(smem + L::kRef) + 8 * s;
+        if (lane == 0) refs[w] = k_ref, refs[4 + w] = v_ref;
+        if constexpr (EXACT) {
+          const int row = 32 * w + lane;
+          float *m = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8 +
+                     (row >> 1) * 8 + (row & 1);
+          m[0] = k.x * p.qscale;
+          m[2] = k.y * p.qscale;
+          m[4] = v.x * inv;
+          m[6] = v.y;
         }
       }
+      const uint32_t dst = sb + (which ? L::kV : L::kK) + s * L::kTile;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) now[u] = next[u];
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          const int row = it * (32 / kPieces) + row_l;  // of the page
+          const uint4 x = lds128(raw[h] + which * kPageSize * kv4::row_bytes(D) +
+                                 row * kv4::row_bytes(D) + 16 * piece);
+          __half2 scale = __float2half2_rn(0.f), zero = scale;
+          if constexpr (!EXACT) {
+            const uint32_t sz = __shfl_sync(kFull, with, h * kPageSize + row);
+            const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
+            scale = *reinterpret_cast<const __half2 *>(&s2);
+            zero = *reinterpret_cast<const __half2 *>(&z2);
+          }
+          // the upper column block's pieces go in another order: no two lanes of a
+          // store meet in a bank
+          const bool upper = piece >= 2;
+          const uint32_t wd[4] = {upper ? x.z : x.x, upper ? x.w : x.y, upper ? x.x : x.z,
+                                  upper ? x.y : x.w};
+          const int flip = upper ? 2 : 0, at = 32 * w + h * kPageSize + row;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4 o = operand<EXACT>(wd[u], scale, zero);
+            const int c = 4 * piece + (u ^ flip);
+            st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(at, c), o.x, o.y, o.z, o.w);
+          }
+        }
+      fence_proxy_async_smem();  // generic stores -> read by the tensor cores
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar((which ? kBarV : kBarK) + s));
     }
-    fence_proxy_async_smem();  // generic stores -> read by the tensor cores
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(full + s));
+    if (!ok) break;
+    // both pages have been read
+    for (int i = 0; i < 2 && issued < total; ++i) issue();
+  }
+  if (!ok) {
+    if (lane == 0) raise_abort(p.status, abort_flag);
+    for (int i = max(2 * t, issued - kRawPages); i < issued; ++i)  // copies in flight still land
+      mbar_wait(bar(kBarRaw + kRawPages * w + i % kRawPages), (i / kRawPages) & 1);
+    return;
   }
   // every MMA that reads a stage has committed before the part ends
-  for (int k = max(0, t - kStages); k < t && ok; ++k)
+  for (int i = max(0, t - kStages); i < t && ok; ++i)
     for (int x = 0; x < n_active && ok; ++x)
-      ok = warp_wait(bar(free + 2 * x + k % kStages), (k / kStages) & 1, abort_flag);
+      ok = warp_wait(bar(kBarKFree + 2 * x + i % kStages), (i / kStages) & 1, abort_flag) &&
+           warp_wait(bar(kBarVFree + 2 * x + i % kStages), (i / kStages) & 1, abort_flag);
   if (!ok && lane == 0) raise_abort(p.status, abort_flag);
 }
 
@@ -533,9 +532,18 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     for (int cb = 0; cb < kKeys / 32; ++cb)
       tc::ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(s + cb * 32));
     const uint32_t meta = sb + L::kMeta + (t % kStages) * (kKeys / 2) * 32;
-    const float4 ref = *reinterpret_cast<const float4 *>(smem + L::kRef + 16 * (t % kStages));
-    v_ref = ref.z;
-    const float f = EXACT ? 1.f : row_f * ref.x;  // scores = f S
+    const float4 k_ref = *reinterpret_cast<const float4 *>(smem + L::kRef + 32 * (t % kStages));
+    const float4 vr = *reinterpret_cast<const float4 *>(smem + L::kRef + 32 * (t % kStages) + 16);
+    // scores = f[ch] S, of 32 keys each; P = 2^(score - m) v_ref[ch] / the largest so far
+    const float kr[4] = {k_ref.x, k_ref.y, k_ref.z, k_ref.w};
+    float f[4];
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)  // never 0: a masked -inf stays -inf
+      f[ch] = EXACT ? 1.f : fmaxf(row_f * kr[ch], FLT_MIN);
+    const float v_top = fmaxf(fmaxf(fmaxf(vr.x, vr.y), fmaxf(vr.z, vr.w)), v_ref);
+    const float grown =
+        v_ref > 0.f ? exp2i(max(-126, exponent(v_ref) - exponent(v_top))) : 0.f;
+    v_ref = v_top;
     tc::wait_ld();
 
     if constexpr (EXACT) {  // scores from the raw sums, two keys an instruction
@@ -556,15 +564,17 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
       for (int c = 0; c < kKeys; ++c)
         if (c > last) s[c] = __float_as_uint(-INFINITY);
     }
-    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+    float cand = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kKeys; c += 8) {
-      t0 = max3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      t1 = max3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-      t2 = max3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-      t3 = max3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+    for (int ch = 0; ch < 4; ++ch) {
+      float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+      for (int c = 32 * ch; c < 32 * ch + 32; c += 4) {
+        t0 = max3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        t1 = max3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+      }
+      cand = fmaxf(cand, fmaxf(t0, t1) * f[ch]);
     }
-    const float cand = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * f;
     float corr = 1.f;
     if (cand - m > kSlack) {
       corr = ex2(m - cand);  // 0 while m was no key's
@@ -572,24 +582,30 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
       l2 = __fmul2_rn(l2, make_float2(corr, corr));
       z2 = __fmul2_rn(z2, make_float2(corr, corr));
     }
-    const bool need = corr != 1.f || ref.y != 1.f;
-    corr *= ref.y;
-    const float2 nm = make_float2(-m, -m), f2 = make_float2(f, f);
+    const bool need = corr != 1.f || grown != 1.f;
+    corr *= grown;
 
     // ---- weights over the S columns, two keys a column; each 64-key half is handed
     // to the MMA warp as soon as it is written
     auto chunk = [&](int ch) {
       uint32_t ph[16];
+      // v_ref[ch] over the largest, 2^by: into the exponent, out of the sum.  Below
+      // 2^-60 these values no longer count, but their weights still do.
+      const int by = max(-60, exponent(ch == 0 ? vr.x : ch == 1 ? vr.y : ch == 2 ? vr.z : vr.w) -
+                                  exponent(v_ref));
+      const float nb = static_cast<float>(by) - m, back = exp2i(-by);
+      const float2 nm = make_float2(nb, nb), f2 = make_float2(f[ch], f[ch]);
+      float2 sum = make_float2(0.f, 0.f), zs = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int c = 32 * ch + 2 * k;
         const float2 sc = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         const float2 e = EXACT ? __fadd2_rn(sc, nm) : __ffma2_rn(sc, f2, nm);
         const float2 pr = make_float2(ex2(e.x), ex2(e.y));
-        l2 = __fadd2_rn(l2, pr);
+        sum = __fadd2_rn(sum, pr);
         if constexpr (EXACT) {
           const uint4 u = lds128(meta + c * 16 + 16);
-          z2 = __ffma2_rn(pr, make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), z2);
+          zs = __ffma2_rn(pr, make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), zs);
           const float2 w =
               __fmul2_rn(pr, make_float2(__uint_as_float(u.x), __uint_as_float(u.y)));
           ph[k] = pack2<false>(w.x, w.y);
@@ -597,6 +613,9 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
           ph[k] = pack2<false>(pr.x, pr.y);
         }
       }
+      const float2 undo = make_float2(back, back);
+      l2 = __ffma2_rn(sum, undo, l2);
+      if constexpr (EXACT) z2 = __ffma2_rn(zs, undo, z2);
       tc::st16(tS + 16 * ch, ph);
       if (ch == 1 && t > 0 && __any_sync(kFull, need)) {
         // P_x V of the tile before has completed: S_x was issued behind it
@@ -718,10 +737,10 @@ __device__ __forceinline__ void cta_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(N), "n"(kThreads) : "memory");
 }
 
-// Registers a thread after the split: the softmax holds a whole row of scores.  The
-// launch's 384 x 168 cover 128 x 88 + 256 x 208.
-constexpr int kRegsLow = 88, kRegsHigh = 208;
-static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split");
+// Registers a thread after the split: the softmax holds a whole row of scores.
+constexpr int kRegsMma = 56, kRegsConvert = 88, kRegsSoftmax = 184;
+static_assert(128 * (kRegsMma + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * 128,
+              "register split");
 template <int N, bool UP>
 __device__ __forceinline__ void set_registers() {
   if constexpr (UP)
@@ -745,7 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
   TilePart *part_s = reinterpret_cast<TilePart *>(smem + L::kPart);
   TileWalk *walk = reinterpret_cast<TileWalk *>(smem + L::kWalk);
   auto init_bars = [&] {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= kBarP && i < kBarP + 4 ? 4 : 1);
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bar(i), i < kBarKFree || (i >= kBarP && i < kBarP + 4) ? 4 : 1);
     fence_mbar_init();
   };
 
@@ -769,24 +789,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     tc::relinquish();
   }
 
-  // Both sides walk the parts in step: barrier 1 when Q and the part are in place,
-  // barrier 2 at its end, barrier 3 once thread 0 has planned the next one.
-  if (warp < kSoftmaxWarp0) {
-    set_registers<kRegsLow, false>();
+  // All walk the parts in step: barrier 1 when Q and the part are in place, barrier 2
+  // at its end, barrier 3 once thread 0 has planned the next one.
+  auto begin = [&] {
+    tc::fence_before_sync();
+    cta_sync<1>();
+    tc::fence_after_sync();
+    return *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
+  };
+  auto finish = [&] {
+    tc::fence_before_sync();
+    cta_sync<2>();
+    tc::fence_after_sync();
+  };
+  if (warp < kConvertWarp0) {
+    set_registers<kRegsMma, false>();
     for (;;) {
       const TilePart part = *part_s;
       const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
-      tc::fence_before_sync();
-      cta_sync<1>();
-      tc::fence_after_sync();
-      const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
-      if (warp >= kKWarp)
-        convert_tiles<D, BF16, EXACT>(warp == kVWarp, p, part, sb, smem, n_active, abort_flag, lane);
-      else if (warp < n_active)
-        mma_tiles<D>(warp, part.nt, sb, tmem, p.status, abort_flag, lane);
-      tc::fence_before_sync();
-      cta_sync<2>();
-      tc::fence_after_sync();
+      const uint32_t tmem = begin();
+      if (warp < n_active) mma_tiles<D>(warp, part.nt, sb, tmem, p.status, abort_flag, lane);
+      finish();
       const bool end = !part.more || *abort_flag;
       if (tid == 0) {
         if (end) {
@@ -805,22 +828,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
       if (end) break;
       cta_sync<3>();
     }
+  } else if (warp < kSoftmaxWarp0) {
+    set_registers<kRegsConvert, false>();
+    for (;;) {
+      const TilePart part = *part_s;
+      const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
+      begin();
+      convert_tiles<D, BF16, EXACT>(warp - kConvertWarp0, p, part, sb, smem, n_active, abort_flag,
+                                    lane);
+      finish();
+      if (!part.more || *abort_flag) break;
+      cta_sync<3>();
+    }
   } else {
-    set_registers<kRegsHigh, true>();
+    set_registers<kRegsSoftmax, true>();
     const int x = (warp - kSoftmaxWarp0) >> 2;
     for (;;) {
       const int n_active = part_s->row0 + kRows < p.n_rows ? 2 : 1;
       const bool more = part_s->more;
       load_q<D, BF16, EXACT>(p, *part_s, x, sb, smem, tid & 127);
-      tc::fence_before_sync();
-      cta_sync<1>();
-      tc::fence_after_sync();
-      const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
+      const uint32_t tmem = begin();
       if (x < n_active)
-        softmax_tiles<D, BF16, EXACT>(p, *part_s, x, n_active, sb, tmem, smem, abort_flag, warp, lane);
-      tc::fence_before_sync();
-      cta_sync<2>();
-      tc::fence_after_sync();
+        softmax_tiles<D, BF16, EXACT>(p, *part_s, x, n_active, sb, tmem, smem, abort_flag, warp,
+                                      lane);
+      finish();
       if (!more || *abort_flag) break;
       cta_sync<3>();
     }
