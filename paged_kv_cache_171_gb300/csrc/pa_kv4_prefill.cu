@@ -224,9 +224,10 @@ __device__ __forceinline__ uint4 operand(uint32_t x, __half2 scale, __half2 zero
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A power of two above x >= 0, and at least 2^-100.
+// A power of two of at least x >= 0, kept to 2^-100 .. 2^126 (x / 2^126 is below 4).
 __device__ __forceinline__ float above(float x) {
-  return fmaxf(__uint_as_float((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u), 0x1p-100f);
+  const float up = __uint_as_float((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u);
+  return fminf(fmaxf(up, 0x1p-100f), 0x1p126f);
 }
 
 // The exponent of a power of two, and 2^k for -126 <= k <= 127.
@@ -278,28 +279,39 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
   };
   int ids = ids_of(0), ids_next = ids_of(1);
   int issued = 0;  // the warp's pages, 2 a tile; page i sits in ring slot i % kRawPages
-  auto issue = [&]() {
+  const int total = 2 * part.nt;
+  // the next pages, as many as `most` (1 or 2), a lane each
+  auto issue = [&](int most) {
+    const int n = min(most, total - issued);
     if ((issued & 31) == 0 && issued > 0) {
       ids = ids_next;
       ids_next = ids_of((issued >> 5) + 1);
     }
-    int id = __shfl_sync(kFull, ids, issued & 31);
-    if (lane == 0) {
+    // the second page may be the next window's first
+    const int from = (issued + (lane & 1)) & 31;
+    int id = __shfl_sync(kFull, ids, from);
+    const int id_next = __shfl_sync(kFull, ids_next, from);
+    if ((issued & 31) == 31 && (lane & 1)) id = id_next;
+    if (lane < n) {
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
         record_error(p.status, PA_ERR_BAD_BLOCK);
         id = 0;
       }
-      const int s = issued % kRawPages;
+      const int s = (issued + lane) % kRawPages;
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(bar(kBarRaw + kRawPages * w + s), kBlock);
       bulk_load(raw0 + s * kBlock,
                 head + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes, kBlock,
                 bar(kBarRaw + kRawPages * w + s));
     }
-    ++issued;
+    if (n == 2 && (issued & 31) == 31) {
+      ids = ids_next;
+      ids_next = ids_of(((issued + 1) >> 5) + 1);
+    }
+    issued += max(0, n);
   };
-  const int total = 2 * part.nt;
-  while (issued < kRawPages && issued < total) issue();
+  issue(2);
+  issue(1);
 
   bool ok = true;
   int t = 0;
@@ -317,6 +329,17 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       k = unpack2<BF16>(lds32(blk + kv4::meta_offset(D, 0, 0) + 4 * (lane % kPageSize)));
       v = unpack2<BF16>(lds32(blk + kv4::meta_offset(D, 1, 0) + 4 * (lane % kPageSize)));
     }
+    // the codes into registers, the next pages into their slots
+    uint4 codes[2 * kIters], v_codes[2 * kIters];
+#pragma unroll
+    for (int i = 0; i < 2 * kIters; ++i) {
+      const uint32_t at = raw[i / kIters] +
+                          ((i % kIters) * (32 / kPieces) + row_l) * kv4::row_bytes(D) + 16 * piece;
+      codes[i] = lds128(at);
+      v_codes[i] = lds128(at + kPageSize * kv4::row_bytes(D));
+    }
+    __syncwarp();
+    issue(2);
     if ((part.t0 + t) * kKeys + 32 * w + lane >= tokens) {
       k = v = make_float2(0.f, 0.f);
     } else if (!(fabsf(k.x) <= FLT_MAX && fabsf(k.y) <= FLT_MAX && fabsf(v.x) <= FLT_MAX &&
@@ -326,11 +349,9 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
     }
     float k_top = EXACT ? 0.f : fmaf(8.f, fabsf(k.x), fabsf(k.y));  // a NaN does not count
     float v_top = EXACT ? fabsf(v.x) : fmaf(8.f, fabsf(v.x), fabsf(v.y));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      if (!EXACT) k_top = fmaxf(k_top, __shfl_xor_sync(kFull, k_top, o));
-      v_top = fmaxf(v_top, __shfl_xor_sync(kFull, v_top, o));
-    }
+    // no float is negative here, so their bits are in their order
+    if (!EXACT) k_top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(k_top, 0.f))));
+    v_top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(v_top, 0.f))));
     const float k_ref = EXACT ? 1.f : above(k_top), v_ref = above(v_top);
 
     const int s = t % kStages;
@@ -340,7 +361,7 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       for (int x = 0; x < n_active && ok && t >= kStages; ++x)
         ok = warp_wait(bar(free + 2 * x + s), (t / kStages - 1) & 1, abort_flag);
       if (!ok) break;
-      const float inv = 1.f / (which ? v_ref : k_ref);
+      const float inv = exp2i(-exponent(which ? v_ref : k_ref));
       const float2 own = which ? v : k;
       const uint32_t with = pack2<false>(own.x * inv, own.y * inv);
       if (which) {
@@ -359,43 +380,40 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       }
       const uint32_t dst = sb + (which ? L::kV : L::kK) + s * L::kTile;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int it = 0; it < kIters; ++it) {
-          const int row = it * (32 / kPieces) + row_l;  // of the page
-          const uint4 x = lds128(raw[h] + which * kPageSize * kv4::row_bytes(D) +
-                                 row * kv4::row_bytes(D) + 16 * piece);
-          __half2 scale = __float2half2_rn(0.f), zero = scale;
-          if constexpr (!EXACT) {
-            const uint32_t sz = __shfl_sync(kFull, with, h * kPageSize + row);
-            const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
-            scale = *reinterpret_cast<const __half2 *>(&s2);
-            zero = *reinterpret_cast<const __half2 *>(&z2);
-          }
-          // the upper column block's pieces go in another order: no two lanes of a
-          // store meet in a bank
-          const bool upper = piece >= 2;
-          const uint32_t wd[4] = {upper ? x.z : x.x, upper ? x.w : x.y, upper ? x.x : x.z,
-                                  upper ? x.y : x.w};
-          const int flip = upper ? 2 : 0, at = 32 * w + h * kPageSize + row;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint4 o = operand<EXACT>(wd[u], scale, zero);
-            const int c = 4 * piece + (u ^ flip);
-            st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(at, c), o.x, o.y, o.z, o.w);
-          }
+      for (int i = 0; i < 2 * kIters; ++i) {
+        // row of the warp's 32
+        const int row = (i / kIters) * kPageSize + (i % kIters) * (32 / kPieces) + row_l;
+        const uint4 x = codes[i];
+        __half2 scale = __float2half2_rn(0.f), zero = scale;
+        if constexpr (!EXACT) {
+          const uint32_t sz = __shfl_sync(kFull, with, row);
+          const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
+          scale = *reinterpret_cast<const __half2 *>(&s2);
+          zero = *reinterpret_cast<const __half2 *>(&z2);
         }
+        // the upper column block's pieces go in another order: no two lanes of a store
+        // meet in a bank
+        const bool upper = piece >= 2;
+        const uint32_t wd[4] = {upper ? x.z : x.x, upper ? x.w : x.y, upper ? x.x : x.z,
+                                upper ? x.y : x.w};
+        const int flip = upper ? 2 : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 o = operand<EXACT>(wd[u], scale, zero);
+          const int c = 4 * piece + (u ^ flip);
+          st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(32 * w + row, c), o.x, o.y, o.z, o.w);
+        }
+        codes[i] = v_codes[i];  // for the second round
+      }
       fence_proxy_async_smem();  // generic stores -> read by the tensor cores
       __syncwarp();
       if (lane == 0) mbar_arrive(bar((which ? kBarV : kBarK) + s));
     }
     if (!ok) break;
-    // both pages have been read
-    for (int i = 0; i < 2 && issued < total; ++i) issue();
   }
   if (!ok) {
     if (lane == 0) raise_abort(p.status, abort_flag);
-    for (int i = max(2 * t, issued - kRawPages); i < issued; ++i)  // copies in flight still land
+    for (int i = max(0, issued - kRawPages); i < issued; ++i)  // copies in flight still land
       mbar_wait(bar(kBarRaw + kRawPages * w + i % kRawPages), (i / kRawPages) & 1);
     return;
   }
