@@ -8,12 +8,13 @@
 // tile is turned into operand tiles once for 256 query rows.
 //
 // Two forms, by the cache's type (EXACT below):
-//  * bf16: the converters store zero + scale (c - 8) rounded once to fp16, over a power
-//    of two above the largest magnitude of 32 keys (k_ref, v_ref).  K, V and P are then
-//    off by 2^-12 each at most, an eighth of the bf16 result's own rounding, and the
-//    softmax works on S as it comes: a factor for each 32 keys in its exponent.
+//  * bf16: the converters store zero + scale (c - 8) as fp16, over a power of two above
+//    the largest magnitude of 32 keys (k_ref, v_ref).  K and V are then off by two half
+//    steps of 2^-11 and P by one, well below the bf16 result's own rounding of 2^-8, and
+//    the softmax works on S as it comes: a factor for each 32 keys in its exponent.
 //  * fp16: that would be as much as the result's rounding, so the codes enter the
-//    products exactly, as c - 8, and the softmax threads apply the rest,
+//    products exactly, as c - 8 ((x & 0x000f000f) | 0x64006400 is 1024 + c), and the
+//    softmax threads apply the rest,
 //      s_t = scale_k[t] S_t + zero_k[t] sum q,   P = p_t scale_v[t] / v_ref,
 //      z += p_t zero_v[t],                       out = (O v_ref + z) / l,
 //    reading each key's scales and zeros from shared memory.
@@ -32,10 +33,10 @@
 // and 12-15 are the softmax of A and B, a thread a row.  Every hand-off is an mbarrier
 // and every wait is bounded.
 //
-// Nibbles.  (x & 0x000f000f) | 0x64006400 is the fp16 pair 1024 + c of nibbles 0 and
-// 4 of a word, minus 1032 is c - 8; the other nibbles follow by shifts.  The operand
-// tiles keep that order of dimensions (0 4 1 5 2 6 3 7 of each eight): Q is stored
-// in it, and the result is put back into the natural one on its way out.
+// Nibbles.  x & 0x000f000f holds nibbles 0 and 4 of a word in two 16-bit halves, and so
+// on: a fp16 pair is made of nibbles four apart.  The operand tiles keep that order of
+// dimensions (0 4 1 5 2 6 3 7 of each eight): Q is stored in it, and the result is put
+// back into the natural one on its way out.
 //
 // Work split.  The key tiles of all items, laid end to end, are cut into equal runs,
 // one an SM: 256 items on 152 SMs take 1.7 items' time, not two, and a single
@@ -209,16 +210,24 @@ __device__ __forceinline__ size_t row_at(const PrefillParams &p, int b, int g, i
          r % p.group;
 }
 
-// The eight codes of a word as c - 8 (fp16), in the order 0 4 1 5 2 6 3 7; with
-// EXACT false, zero + scale (c - 8).
+// The eight codes of a word, in the order 0 4 1 5 2 6 3 7.  EXACT: as c - 8.  Else as
+// zero + scale (c - 8) over 2^7 ref: (x & 0x000f000f) is the fp16 subnormal pair
+// c 2^-24 and (x & 0x00f000f0) is c 2^-20, so with s24 = scale 2^24, s20 = scale 2^20
+// and z = zero - 8 scale a pair is one AND and one FMA.
 template <bool EXACT>
-__device__ __forceinline__ uint4 operand(uint32_t x, __half2 scale, __half2 zero) {
+__device__ __forceinline__ uint4 operand(uint32_t x, __half2 s24, __half2 s20, __half2 z) {
   uint32_t o[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t w = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
-    __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1032.f));
-    if constexpr (!EXACT) r = __hfma2(scale, r, zero);
+    uint32_t w;
+    __half2 r;
+    if constexpr (EXACT) {
+      w = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
+      r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1032.f));
+    } else {
+      w = (x >> (8 * (k >> 1))) & ((k & 1) ? 0x00f000f0u : 0x000f000fu);
+      r = __hfma2((k & 1) ? s20 : s24, *reinterpret_cast<const __half2 *>(&w), z);
+    }
     o[k] = *reinterpret_cast<const uint32_t *>(&r);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
@@ -267,7 +276,9 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
   const int n_pages = (tokens + kPageSize - 1) / kPageSize;
   const int32_t *bt_row = p.block_table + static_cast<size_t>(part.b) * p.max_blocks;
   const uint8_t *head = p.cache + static_cast<size_t>(part.g) * kBlock;
-  const int piece = lane % kPieces, row_l = lane / kPieces;
+  // the upper column block's pieces (head_dim 128) take another row than the lower's, so
+  // that no two lanes of a store meet in a bank
+  const int piece = lane % kPieces, row_l = (lane / kPieces) ^ (piece >= 2 ? 4 : 0);
   const uint32_t raw0 = sb + L::kRaw + w * kRawPages * kBlock;
 
   // Page ids: lane l holds page l & 1 of the warp's two in tile 16 v + (l >> 1), v the
@@ -363,7 +374,9 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       if (!ok) break;
       const float inv = exp2i(-exponent(which ? v_ref : k_ref));
       const float2 own = which ? v : k;
-      const uint32_t with = pack2<false>(own.x * inv, own.y * inv);
+      // over 2^7 ref: |scale| 2^24 is at most 2^14
+      const uint32_t scales = pack2<false>(own.x * inv * 0x1p17f, own.x * inv * 0x1p13f);
+      const uint32_t zeros = pack2<false>(fmaf(-8.f, own.x, own.y) * inv * 0x1p-7f, 0.f);
       if (which) {
         // V's stage is free once the softmax has read these for the tile before in it
         float *refs = reinterpret_cast<float *>(smem + L::kRef) + 8 * s;
@@ -383,25 +396,24 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       for (int i = 0; i < 2 * kIters; ++i) {
         // row of the warp's 32
         const int row = (i / kIters) * kPageSize + (i % kIters) * (32 / kPieces) + row_l;
-        const uint4 x = codes[i];
-        __half2 scale = __float2half2_rn(0.f), zero = scale;
+        __half2 s24 = __float2half2_rn(0.f), s20 = s24, z = s24;
         if constexpr (!EXACT) {
-          const uint32_t sz = __shfl_sync(kFull, with, row);
-          const uint32_t s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
-          scale = *reinterpret_cast<const __half2 *>(&s2);
-          zero = *reinterpret_cast<const __half2 *>(&z2);
+          const uint32_t sc = __shfl_sync(kFull, scales, row);
+          const uint32_t zr = __shfl_sync(kFull, zeros, row);
+          const uint32_t a = __byte_perm(sc, sc, 0x1010), b = __byte_perm(sc, sc, 0x3232);
+          const uint32_t c = __byte_perm(zr, zr, 0x1010);
+          s24 = *reinterpret_cast<const __half2 *>(&a);
+          s20 = *reinterpret_cast<const __half2 *>(&b);
+          z = *reinterpret_cast<const __half2 *>(&c);
         }
-        // the upper column block's pieces go in another order: no two lanes of a store
-        // meet in a bank
-        const bool upper = piece >= 2;
-        const uint32_t wd[4] = {upper ? x.z : x.x, upper ? x.w : x.y, upper ? x.x : x.z,
-                                upper ? x.y : x.w};
-        const int flip = upper ? 2 : 0;
+        const uint32_t wd[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+        // 16-byte chunks 4 piece .. 4 piece + 3 of the row, swizzled
+        const int at = 32 * w + row, c0 = 4 * piece;
+        const uint32_t to = dst + (c0 >> 3) * L::kColBlk + swz128(at, c0);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint4 o = operand<EXACT>(wd[u], scale, zero);
-          const int c = 4 * piece + (u ^ flip);
-          st_shared_v4(dst + (c >> 3) * L::kColBlk + swz128(32 * w + row, c), o.x, o.y, o.z, o.w);
+          const uint4 o = operand<EXACT>(wd[u], s24, s20, z);
+          st_shared_v4(to ^ (u << 4), o.x, o.y, o.z, o.w);
         }
         codes[i] = v_codes[i];  // for the second round
       }
@@ -557,7 +569,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     float f[4];
 #pragma unroll
     for (int ch = 0; ch < 4; ++ch)  // never 0: a masked -inf stays -inf
-      f[ch] = EXACT ? 1.f : fmaxf(row_f * kr[ch], FLT_MIN);
+      f[ch] = EXACT ? 1.f : fmaxf(row_f * kr[ch] * 128.f, FLT_MIN);
     const float v_top = fmaxf(fmaxf(fmaxf(vr.x, vr.y), fmaxf(vr.z, vr.w)), v_ref);
     const float grown =
         v_ref > 0.f ? exp2i(max(-126, exponent(v_ref) - exponent(v_top))) : 0.f;
@@ -668,6 +680,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
   const int row = part.row0 + x * kRows + r;
   const bool real = row < p.n_rows, whole = part.first == part.last;
   const float l = l2.x + l2.y, z = z2.x + z2.y;
+  const float out_ref = EXACT ? v_ref : v_ref * 128.f;  // the operands are over 2^7 v_ref
   const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
   const int slot = static_cast<int>(blockIdx.x) > part.first ? 0 : part.slot;
   float *state = p.ws + ((static_cast<size_t>(blockIdx.x) * 2 + slot) * kItemRows + x * kRows + r) *
@@ -683,7 +696,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // where dimension k of eight is
-      f[k] = fmaf(__uint_as_float(o[(k & ~7) + kAt[k & 7]]), v_ref, z) * inv;
+      f[k] = fmaf(__uint_as_float(o[(k & ~7) + kAt[k & 7]]), out_ref, z) * inv;
     }
     if (whole) {
 #pragma unroll
