@@ -303,13 +303,12 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
     int id = __shfl_sync(kFull, ids, from);
     const int id_next = __shfl_sync(kFull, ids_next, from);
     if ((issued & 31) == 31 && (lane & 1)) id = id_next;
-    if (lane < n) {
+    if (lane < n) {  // (behind a proxy fence, where a slot has been read)
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
         record_error(p.status, PA_ERR_BAD_BLOCK);
         id = 0;
       }
       const int s = (issued + lane) % kRawPages;
-      fence_proxy_async_smem();
       mbar_arrive_expect_tx(bar(kBarRaw + kRawPages * w + s), kBlock);
       bulk_load(raw0 + s * kBlock,
                 head + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes, kBlock,
@@ -327,9 +326,9 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
   bool ok = true;
   int t = 0;
   for (; t < part.nt; ++t) {
-    for (int i = 2 * t; i < 2 * t + 2 && ok; ++i)
-      ok = warp_wait(bar(kBarRaw + kRawPages * w + i % kRawPages), (i / kRawPages) & 1,
-                     abort_flag);
+    ok = warp_wait2(bar(kBarRaw + kRawPages * w + 2 * t % kRawPages), (2 * t / kRawPages) & 1,
+                    bar(kBarRaw + kRawPages * w + (2 * t + 1) % kRawPages),
+                    ((2 * t + 1) / kRawPages) & 1, abort_flag);
     if (!ok) break;
     const uint32_t raw[2] = {raw0 + ((2 * t) % kRawPages) * kBlock,
                              raw0 + ((2 * t + 1) % kRawPages) * kBlock};
@@ -349,8 +348,6 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       codes[i] = lds128(at);
       v_codes[i] = lds128(at + kPageSize * kv4::row_bytes(D));
     }
-    __syncwarp();
-    issue(2);
     if ((part.t0 + t) * kKeys + 32 * w + lane >= tokens) {
       k = v = make_float2(0.f, 0.f);
     } else if (!(fabsf(k.x) <= FLT_MAX && fabsf(k.y) <= FLT_MAX && fabsf(v.x) <= FLT_MAX &&
@@ -369,8 +366,9 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const int free = which ? kBarVFree : kBarKFree;
-      for (int x = 0; x < n_active && ok && t >= kStages; ++x)
-        ok = warp_wait(bar(free + 2 * x + s), (t / kStages - 1) & 1, abort_flag);
+      if (t >= kStages)  // with one row tile, its barrier twice
+        ok = warp_wait2(bar(free + s), (t / kStages - 1) & 1,
+                        bar(free + 2 * (n_active - 1) + s), (t / kStages - 1) & 1, abort_flag);
       if (!ok) break;
       const float inv = exp2i(-exponent(which ? v_ref : k_ref));
       const float2 own = which ? v : k;
@@ -420,6 +418,7 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
       fence_proxy_async_smem();  // generic stores -> read by the tensor cores
       __syncwarp();
       if (lane == 0) mbar_arrive(bar((which ? kBarV : kBarK) + s));
+      if (!which) issue(2);  // the pages' codes are in registers, and the fence covers it
     }
     if (!ok) break;
   }
@@ -485,8 +484,9 @@ __device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t t
   }
   for (int t = 0; t < nt && ok; ++t) {
     for (int h = 0; h < 2 && ok; ++h) {
-      ok = warp_wait(bar(kBarP + 2 * x + h), t & 1, abort_flag) &&
-           (h || warp_wait(bar(kBarV + t % kStages), (t / kStages) & 1, abort_flag));
+      ok = h ? warp_wait(bar(kBarP + 2 * x + 1), t & 1, abort_flag)
+             : warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarP + 2 * x), t & 1,
+                          abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
       pv_mma(t, h);
@@ -549,10 +549,9 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     // the other row tile's turn first
     const int to = t - 1 + x;
     if (n_active == 2 && to >= 0)
-      bad = !warp_wait(bar(kBarP + 2 * (x ^ 1)), to & 1, abort_flag) ||
-            !warp_wait(bar(kBarP + 2 * (x ^ 1) + 1), to & 1, abort_flag);
-    if (bad || !warp_wait(bar(kBarV + t % kStages), (t / kStages) & 1, abort_flag) ||
-        !warp_wait(bar(kBarS + x), t & 1, abort_flag)) {
+      bad = !warp_wait(bar(kBarP + 2 * (x ^ 1) + 1), to & 1, abort_flag);
+    if (bad || !warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarS + x), t & 1,
+                           abort_flag)) {
       bad = true;
       break;
     }

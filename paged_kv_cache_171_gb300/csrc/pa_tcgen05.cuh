@@ -55,6 +55,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
 }
 
+// Two phases at once: their tests overlap.
+__device__ __forceinline__ bool warp_wait2(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                           uint32_t parity1, volatile int *abort_flag) {
+  const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return warp_wait(bar0, parity0, abort_flag) && warp_wait(bar1, parity1, abort_flag);
+}
+
 __device__ __forceinline__ void raise_abort(int *status, volatile int *abort_flag) {
   record_error(status, PA_ERR_TIMEOUT);
   *abort_flag = 1;
