@@ -549,7 +549,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     // the other row tile's turn first
     const int to = t - 1 + x;
     if (n_active == 2 && to >= 0)
-      bad = !warp_wait(bar(kBarP + 2 * (x ^ 1) + 1), to & 1, abort_flag);
+      bad = !warp_wait(bar(kBarP + 2 * (x ^ 1)), to & 1, abort_flag);
     if (bad || !warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarS + x), t & 1,
                            abort_flag)) {
       bad = true;
