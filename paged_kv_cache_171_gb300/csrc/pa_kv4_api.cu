@@ -35,7 +35,7 @@ int append(AppendRopeLaunch &a, int page_size, int dtype, pa_stream_t stream) {
 
 // Chunks of more than this many rows (queries x group) a kv head go to the tile
 // kernel.
-constexpr int kMostRows = 64;
+constexpr int kMostRows = 8;
 
 bool wants_tiles(int n_new, int n_q_heads, int n_kv_heads) {
   return n_new > 0 && static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > kMostRows;

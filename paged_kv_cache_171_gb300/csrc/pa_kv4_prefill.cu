@@ -27,6 +27,11 @@
 // alternates between them: B's softmax of key tile j starts once A has handed over
 // its weights of j, A's of j + 1 once B has handed over those of j.
 //
+// An item of at most 128 rows (a short chunk) has its rows in both tiles, which split
+// the key tiles instead: A the even ones, B the odd ones, so that one's softmax still
+// overlaps the other's products.  At the end A reads both O's (the lanes hold the same
+// rows) and merges the two states.
+//
 // Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B, warps
 // 4-7 turn codes into the K and V operand tiles (two stages each): a warp 32 keys of
 // each tile, from a ring of pages that it fills for itself by bulk copies.  Warps 8-11
@@ -122,6 +127,21 @@ struct TilePart {
   int more;            // the run goes on behind this part
 };
 static_assert(sizeof(TilePart) <= 64, "room in shared memory");
+
+// How a part uses the two row tiles.
+struct Tiling {
+  int n_active;  // row tiles at work
+  bool split;    // they hold the same rows and split the key tiles
+  __device__ Tiling(int row0, int nt, int n_rows) {
+    const bool one = row0 + kRows >= n_rows;
+    split = one && nt >= 2;
+    n_active = one && !split ? 1 : 2;
+  }
+  // The row tiles that read stage s (of tile t = s mod 2 when split): first and last.
+  __device__ int first(int s) const { return split ? s : 0; }
+  __device__ int last(int s) const { return split ? s : n_active - 1; }
+};
+static_assert(kStages == 2, "split key tiles: a stage belongs to one row tile");
 
 // The CTA's run [w, w1) of the flattened list of key tiles.
 struct TileWalk {
@@ -265,7 +285,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 template <int D, bool BF16, bool EXACT>
 __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
                                               const TilePart &part, uint32_t sb, uint8_t *smem,
-                                              int n_active, volatile int *abort_flag, int lane) {
+                                              const Tiling &tl, volatile int *abort_flag,
+                                              int lane) {
   using L = PrefillSmem<D>;
   constexpr int kBlock = kv4::block_bytes(D);
   constexpr int kPieces = D / 32;                // 16-byte pieces of a row's codes
@@ -366,9 +387,9 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const int free = which ? kBarVFree : kBarKFree;
-      if (t >= kStages)  // with one row tile, its barrier twice
-        ok = warp_wait2(bar(free + s), (t / kStages - 1) & 1,
-                        bar(free + 2 * (n_active - 1) + s), (t / kStages - 1) & 1, abort_flag);
+      if (t >= kStages)  // with one reader, its barrier twice
+        ok = warp_wait2(bar(free + 2 * tl.first(s) + s), (t / kStages - 1) & 1,
+                        bar(free + 2 * tl.last(s) + s), (t / kStages - 1) & 1, abort_flag);
       if (!ok) break;
       const float inv = exp2i(-exponent(which ? v_ref : k_ref));
       const float2 own = which ? v : k;
@@ -430,17 +451,18 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
   }
   // every MMA that reads a stage has committed before the part ends
   for (int i = max(0, t - kStages); i < t && ok; ++i)
-    for (int x = 0; x < n_active && ok; ++x)
-      ok = warp_wait(bar(kBarKFree + 2 * x + i % kStages), (i / kStages) & 1, abort_flag) &&
-           warp_wait(bar(kBarVFree + 2 * x + i % kStages), (i / kStages) & 1, abort_flag);
+    for (int x = tl.first(i % kStages); x <= tl.last(i % kStages) && ok; ++x)
+      ok = warp_wait2(bar(kBarKFree + 2 * x + i % kStages), (i / kStages) & 1,
+                      bar(kBarVFree + 2 * x + i % kStages), (i / kStages) & 1, abort_flag);
   if (!ok && lane == 0) raise_abort(p.status, abort_flag);
 }
 
 // MMA warp x (lane 0): S_x(0), then per key tile t: P_x(t) V_t in two key halves,
-// S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.
+// S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.  (Split key
+// tiles: t = x, x + 2, ..)
 template <int D>
-__device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t tmem, int *status,
-                                          volatile int *abort_flag, int lane) {
+__device__ __forceinline__ void mma_tiles(int x, bool split, int nt, uint32_t sb, uint32_t tmem,
+                                          int *status, volatile int *abort_flag, int lane) {
   using L = PrefillSmem<D>;
   constexpr uint32_t kIdS = tc::idesc_f16(false, kRows, kKeys, false, false);
   constexpr uint32_t kIdO = tc::idesc_f16(false, kRows, D, false, true);
@@ -449,6 +471,7 @@ __device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t t
   const uint64_t dk0 = tc::smem_desc_sw128(sb + L::kK, 16, 1024);
   const uint64_t dv0 = tc::smem_desc_sw128(sb + L::kV, L::kColBlk, 1024);
   const uint32_t tS = tmem + x * kKeys, tO = tmem + 2 * kKeys + x * D;
+  const int step = split ? 2 : 1, t_first = split ? x : 0;
   auto s_mma = [&](int t) {
     if (lane == 0) {
       const uint64_t dk = dk0 + static_cast<uint64_t>(((t % kStages) * L::kTile) >> 4);
@@ -469,32 +492,33 @@ __device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t t
       for (int kk = 0; kk < 4; ++kk)
         tc::mma_f16_tmem_a(tO, tS + 32 * h + 8 * kk,
                            dv + static_cast<uint64_t>(((4 * h + kk) * 2048) >> 4), kIdO,
-                           (t > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                           (t > t_first || h > 0 || kk > 0) ? 1u : 0u);
       if (h == 1) {
         tc::commit(bar(kBarVFree + 2 * x + t % kStages));
-        if (t == nt - 1) tc::commit(bar(kBarO + x));
+        if (t + step >= nt) tc::commit(bar(kBarO + x));
       }
     }
     __syncwarp();
   };
-  bool ok = warp_wait(bar(kBarK), 0, abort_flag);
+  bool ok = warp_wait(bar(kBarK + t_first), 0, abort_flag);
   if (ok) {
     tc::fence_after_sync();
-    s_mma(0);
+    s_mma(t_first);
   }
-  for (int t = 0; t < nt && ok; ++t) {
+  for (int t = t_first, j = 0; t < nt && ok; t += step, ++j) {  // the j-th tile of x
     for (int h = 0; h < 2 && ok; ++h) {
-      ok = h ? warp_wait(bar(kBarP + 2 * x + 1), t & 1, abort_flag)
-             : warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarP + 2 * x), t & 1,
+      ok = h ? warp_wait(bar(kBarP + 2 * x + 1), j & 1, abort_flag)
+             : warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarP + 2 * x), j & 1,
                           abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
       pv_mma(t, h);
     }
-    if (ok && t + 1 < nt &&
-        (ok = warp_wait(bar(kBarK + (t + 1) % kStages), ((t + 1) / kStages) & 1, abort_flag))) {
+    const int tn = t + step;
+    if (ok && tn < nt &&
+        (ok = warp_wait(bar(kBarK + tn % kStages), (tn / kStages) & 1, abort_flag))) {
       tc::fence_after_sync();
-      s_mma(t + 1);
+      s_mma(tn);
     }
   }
   if (!ok) {
@@ -510,17 +534,19 @@ __device__ __forceinline__ void mma_tiles(int x, int nt, uint32_t sb, uint32_t t
 // Softmax warpgroup x: lane l of warp w owns row 32 (w mod 4) + l of row tile x.
 template <int D, bool BF16, bool EXACT>
 __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const volatile TilePart &part, int x,
-                                              int n_active, uint32_t sb, uint32_t tmem,
-                                              const uint8_t *smem, volatile int *abort_flag,
+                                              const Tiling &tl, uint32_t sb, uint32_t tmem,
+                                              uint8_t *smem, volatile int *abort_flag,
                                               int warp, int lane) {
   using L = PrefillSmem<D>;
   auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
   const int r = ((warp & 3) << 5) + lane;
   // last key that the row sees, and that every row of the tile sees
-  const int lim = part.ctx + min(part.row0 + x * kRows + r, p.n_rows - 1) / p.group;
-  const int lim_all = part.ctx + (part.row0 + x * kRows) / p.group;
+  const int row0 = part.row0 + (tl.split ? 0 : x * kRows);
+  const int lim = part.ctx + min(row0 + r, p.n_rows - 1) / p.group;
+  const int lim_all = part.ctx + row0 / p.group;
+  const int step = tl.split ? 2 : 1, t_first = tl.split ? x : 0;
   const int nt = part.nt;
-  int key0 = part.t0 * kKeys;
+  int key0 = (part.t0 + t_first) * kKeys;
   const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t tS = tmem + x * kKeys + lane_base;
   const uint32_t tO = tmem + 2 * kKeys + x * D + lane_base;
@@ -545,12 +571,12 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
   float m = kNoKey, v_ref = 0.f;
   float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
   bool bad = false;
-  for (int t = 0; t < nt; ++t, key0 += kKeys) {
+  for (int t = t_first, j = 0; t < nt; t += step, ++j, key0 += step * kKeys) {
     // the other row tile's turn first
     const int to = t - 1 + x;
-    if (n_active == 2 && to >= 0)
+    if (tl.n_active == 2 && !tl.split && to >= 0)
       bad = !warp_wait(bar(kBarP + 2 * (x ^ 1)), to & 1, abort_flag);
-    if (bad || !warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarS + x), t & 1,
+    if (bad || !warp_wait2(bar(kBarV + t % kStages), (t / kStages) & 1, bar(kBarS + x), j & 1,
                            abort_flag)) {
       bad = true;
       break;
@@ -646,7 +672,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
       l2 = __ffma2_rn(sum, undo, l2);
       if constexpr (EXACT) z2 = __ffma2_rn(zs, undo, z2);
       tc::st16(tS + 16 * ch, ph);
-      if (ch == 1 && t > 0 && __any_sync(kFull, need)) {
+      if (ch == 1 && j > 0 && __any_sync(kFull, need)) {
         // P_x V of the tile before has completed: S_x was issued behind it
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -669,45 +695,66 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     for (int ch = 0; ch < 4; ++ch) chunk(ch);
   }
   if (!bad) bad = !warp_wait(bar(kBarO + x), 0, abort_flag);
-  if (bad) {
-    if (lane == 0) raise_abort(p.status, abort_flag);
-    return;
+  if (bad && lane == 0) raise_abort(p.status, abort_flag);
+  float l = l2.x + l2.y, z = z2.x + z2.y;
+  // out = o_a O + o_b O_B + z, over l
+  float o_a = EXACT ? v_ref : v_ref * 128.f, o_b = 0.f;  // the operands are over 2^7 v_ref
+  if (tl.split) {
+    // B leaves its (m, l, z, reference) in Q_B, whose products are done; both
+    // warpgroups always meet here, failed or not
+    float4 *other = reinterpret_cast<float4 *>(smem + L::kQ + L::kTile) + r;
+    if (x == 1 && !bad) *other = make_float4(m, l, z, o_a);
+    tc::fence_before_sync();
+    asm volatile("bar.sync 4, 256;" ::: "memory");
+    bad = __any_sync(kFull, *abort_flag);
+    if (x == 1) return;
+    const float4 b = *other;
+    const float mn = fmaxf(m, b.x), ca = ex2(m - mn), cb = ex2(b.x - mn);
+    m = mn;
+    l = ca * l + cb * b.y;
+    z = ca * z + cb * b.z;
+    o_a *= ca;
+    o_b = cb * b.w;
   }
+  if (bad) return;
   tc::fence_after_sync();
 
-  // ---- (O v_ref + z) / l in the natural order of dimensions, or the row's state
-  const int row = part.row0 + x * kRows + r;
+  // ---- the row's result in the natural order of dimensions, or its state
+  const int row = row0 + r;
   const bool real = row < p.n_rows, whole = part.first == part.last;
-  const float l = l2.x + l2.y, z = z2.x + z2.y;
-  const float out_ref = EXACT ? v_ref : v_ref * 128.f;  // the operands are over 2^7 v_ref
   const float inv = !whole ? 1.f : (l == 0.f ? 0.f : 1.f / l);
   const int slot = static_cast<int>(blockIdx.x) > part.first ? 0 : part.slot;
-  float *state = p.ws + ((static_cast<size_t>(blockIdx.x) * 2 + slot) * kItemRows + x * kRows + r) *
-                            (D + 4);
+  float *state = p.ws + ((static_cast<size_t>(blockIdx.x) * 2 + slot) * kItemRows +
+                         (row - part.row0)) * (D + 4);
   uint16_t *dst = p.out + row_at(p, part.b, part.g, row) * D;
 #pragma unroll
   for (int cb = 0; cb < D / 32; ++cb) {
     uint32_t o[32];
     tc::ld32(tO + cb * 32, o);
     tc::wait_ld();
-    if (!real) continue;
     float f[32];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // where dimension k of eight is
-      f[k] = fmaf(__uint_as_float(o[(k & ~7) + kAt[k & 7]]), out_ref, z) * inv;
+    for (int k = 0; k < 32; ++k) f[k] = fmaf(__uint_as_float(o[k]), o_a, z);
+    if (tl.split) {
+      tc::ld32(tO + D + cb * 32, o);  // O_B is D columns to the right
+      tc::wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) f[k] = fmaf(__uint_as_float(o[k]), o_b, f[k]);
     }
+    if (!real) continue;
+    constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // where dimension k of eight is
+    auto at = [&](int k) { return f[(k & ~7) + kAt[k & 7]] * inv; };
     if (whole) {
 #pragma unroll
       for (int k = 0; k < 32; k += 8)
         *reinterpret_cast<uint4 *>(dst + cb * 32 + k) =
-            make_uint4(pack2<BF16>(f[k], f[k + 1]), pack2<BF16>(f[k + 2], f[k + 3]),
-                       pack2<BF16>(f[k + 4], f[k + 5]), pack2<BF16>(f[k + 6], f[k + 7]));
+            make_uint4(pack2<BF16>(at(k), at(k + 1)), pack2<BF16>(at(k + 2), at(k + 3)),
+                       pack2<BF16>(at(k + 4), at(k + 5)), pack2<BF16>(at(k + 6), at(k + 7)));
     } else {
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
         *reinterpret_cast<float4 *>(state + cb * 32 + k) =
-            make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+            make_float4(at(k), at(k + 1), at(k + 2), at(k + 3));
     }
   }
   if (real && !whole) *reinterpret_cast<float2 *>(state + D) = make_float2(m, l);
@@ -718,14 +765,14 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
 // factor goes to kRowF.  A thread's loads all go out before its first store.
 template <int D, bool BF16, bool EXACT>
 __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile TilePart &part,
-                                       int x, uint32_t sb, uint8_t *smem, int th) {
+                                       bool split, int x, uint32_t sb, uint8_t *smem, int th) {
   using L = PrefillSmem<D>;
   constexpr int kChunks = D / 8, kPer = kRows * kChunks / 128;  // 16-byte chunks: a row, a thread
   uint4 v[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int e = th + 128 * k, r = e / kChunks, c = e % kChunks;
-    const int row = part.row0 + x * kRows + r;
+    const int row = part.row0 + (split ? 0 : x * kRows) + r;
     v[k] = make_uint4(0, 0, 0, 0);
     if (row < p.n_rows)
       v[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + row_at(p, part.b, part.g, row) * D +
@@ -836,9 +883,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     set_registers<kRegsMma, false>();
     for (;;) {
       const TilePart part = *part_s;
-      const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
+      const Tiling tl(part.row0, part.nt, p.n_rows);
       const uint32_t tmem = begin();
-      if (warp < n_active) mma_tiles<D>(warp, part.nt, sb, tmem, p.status, abort_flag, lane);
+      if (warp < tl.n_active)
+        mma_tiles<D>(warp, tl.split, part.nt, sb, tmem, p.status, abort_flag, lane);
       finish();
       const bool end = !part.more || *abort_flag;
       if (tid == 0) {
@@ -862,10 +910,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     set_registers<kRegsConvert, false>();
     for (;;) {
       const TilePart part = *part_s;
-      const int n_active = part.row0 + kRows < p.n_rows ? 2 : 1;
+      const Tiling tl(part.row0, part.nt, p.n_rows);
       begin();
-      convert_tiles<D, BF16, EXACT>(warp - kConvertWarp0, p, part, sb, smem, n_active, abort_flag,
-                                    lane);
+      convert_tiles<D, BF16, EXACT>(warp - kConvertWarp0, p, part, sb, smem, tl, abort_flag, lane);
       finish();
       if (!part.more || *abort_flag) break;
       cta_sync<3>();
@@ -874,12 +921,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     set_registers<kRegsSoftmax, true>();
     const int x = (warp - kSoftmaxWarp0) >> 2;
     for (;;) {
-      const int n_active = part_s->row0 + kRows < p.n_rows ? 2 : 1;
+      const Tiling tl(part_s->row0, part_s->nt, p.n_rows);
       const bool more = part_s->more;
-      load_q<D, BF16, EXACT>(p, *part_s, x, sb, smem, tid & 127);
+      load_q<D, BF16, EXACT>(p, *part_s, tl.split, x, sb, smem, tid & 127);
       const uint32_t tmem = begin();
-      if (x < n_active)
-        softmax_tiles<D, BF16, EXACT>(p, *part_s, x, n_active, sb, tmem, smem, abort_flag, warp,
+      if (x < tl.n_active)
+        softmax_tiles<D, BF16, EXACT>(p, *part_s, x, tl, sb, tmem, smem, abort_flag, warp,
                                       lane);
       finish();
       if (!more || *abort_flag) break;
