@@ -33,12 +33,22 @@ int append(AppendRopeLaunch &a, int page_size, int dtype, pa_stream_t stream) {
   return launch_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-// Chunks of more than this many rows (queries x group) a kv head go to the tile
-// kernel.
-constexpr int kMostRows = 8;
+// Whether a chunk goes to the tile kernel: by its rows (queries x group) a kv head.
+// The row kernel reads the cache once for 8 of them, the tile kernel once for 256 at
+// the price of turning it into operand tiles.  Measured over 4 x 32768 tokens of 8 kv
+// heads at head_dim 128, rows against tiles: bf16 16 rows 84 / 120 us, 32 rows 144 /
+// 121 us; fp16, whose tile form is the slower one, 32 rows 144 / 157 us, 64 rows 269 /
+// 162 us.
+bool wants_tiles(int n_new, int n_q_heads, int n_kv_heads, bool bf16) {
+  return n_new > 0 &&
+         static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > (bf16 ? 24 : 40);
+}
 
-bool wants_tiles(int n_new, int n_q_heads, int n_kv_heads) {
-  return n_new > 0 && static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > kMostRows;
+// The larger of the two kernels' workspaces where the type decides between them.
+size_t chunk_workspace(int n_new, int n_q_heads, int n_kv_heads, int head_dim, int sms) {
+  return wants_tiles(n_new, n_q_heads, n_kv_heads, true)
+             ? kv4_tiles_workspace_bytes(head_dim, sms)
+             : kv4_rows_workspace_bytes(head_dim, sms);
 }
 
 int sms_or_default() { return sm_count() > 0 ? sm_count() : 152; }
@@ -50,9 +60,9 @@ int attention(Kv4AttentionLaunch &a, int page_size, int dtype, size_t workspace_
                         a.num_pages, dtype);
   if (rc) return rc;
   if (!aligned16(a.q) || !aligned16(a.cache) || !aligned16(a.out)) return PA_ERR_ALIGN;
-  const bool tiles = wants_tiles(a.n_new, a.n_q_heads, a.n_kv_heads);
-  const size_t need = tiles ? kv4_tiles_workspace_bytes(a.head_dim, sms_or_default())
-                            : kv4_rows_workspace_bytes(a.head_dim, sms_or_default());
+  const bool tiles = wants_tiles(a.n_new, a.n_q_heads, a.n_kv_heads, dtype == PA_BF16);
+  const size_t need = chunk_workspace(a.n_new, a.n_q_heads, a.n_kv_heads, a.head_dim,
+                                      sms_or_default());
   if (!a.workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
   if (!aligned16(a.workspace)) return PA_ERR_ALIGN;
   if ((rc = current_status_ptr(&a.status))) return rc;
@@ -158,9 +168,7 @@ size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_
                    PA_BF16) ||
       n_new <= 0 || n_new > static_cast<int64_t>(max_blocks_per_seq) * page_size)
     return 0;
-  return wants_tiles(n_new, n_q_heads, n_kv_heads)
-             ? kv4_tiles_workspace_bytes(head_dim, sms_or_default())
-             : kv4_rows_workspace_bytes(head_dim, sms_or_default());
+  return chunk_workspace(n_new, n_q_heads, n_kv_heads, head_dim, sms_or_default());
 }
 
 int pa_prefill_kv4(const void *q, const void *kv_cache, const int32_t *block_table,
