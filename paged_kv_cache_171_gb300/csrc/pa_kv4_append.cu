@@ -11,8 +11,8 @@
 //
 // Quantisation of a row x (fp32 after the rotation): scale = r16((max - min) /
 // 15), zero = r16(min + 8 scale), code = rint((x - zero) / scale) + 8 clamped
-// to 0 .. 15; the division is IEEE, so the codes are those of the formula
-// evaluated step by step in fp32.  A scale of 0 gives code 8 (x = zero); a row
+// to 0 .. 15, the codes of the formula evaluated step by step in fp32 (a product
+// with the reciprocal decides where it is clear, an IEEE division where it is not).  A scale of 0 gives code 8 (x = zero); a row
 // whose range, scale or zero is not finite gives scale = zero = NaN.
 //
 // Bound: memory.  A row is head_dim / 16 threads of 16 dimensions; thread t
@@ -72,40 +72,17 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const AppendParams p) 
   if (idx >= p.total) return;
   const int t = static_cast<int>(idx % TPR);
   const int64_t unit = idx / TPR;
-  const int64_t j = unit / p.row_lanes;
+  const int64_t j = p.total >> 32 ? unit / p.row_lanes
+                                  : static_cast<uint32_t>(unit) / static_cast<uint32_t>(p.row_lanes);
   const int r0 = static_cast<int>(unit - j * p.row_lanes);
 
   const int b = p.seq_idx[j], pos = p.pos[j];
-  const bool reporter = t == 0 && r0 == 0;
   const bool turn = p.cos_sin != nullptr;
-  if (b < 0 || b >= p.batch || pos < 0 || pos >= p.max_blocks * kPageSize ||
-      (turn && pos >= p.max_pos)) {
-    if (reporter) record_error(p.status, PA_ERR_BAD_INDEX);
-    return;
-  }
-  const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPageSize];
-  if (page < 0 || page >= p.num_pages) {
-    if (reporter) record_error(p.status, PA_ERR_BAD_BLOCK);
-    return;
-  }
-  const int slot = pos % kPageSize;
   const int half_chunks = p.rot_dim / 16;         // chunks of rotated first elements
   const bool mine = turn && t < half_chunks;      // this thread's chunks are rotated
   const bool split = mine && !p.interleaved;      // pairs (i, i + rot / 2)
   const int rc0 = split ? t : 2 * t, rc1 = split ? t + half_chunks : 2 * t + 1;
-
-  float cs[8], sn[8];
-  if (mine) {
-    const float4 *row = reinterpret_cast<const float4 *>(
-        p.cos_sin + static_cast<size_t>(pos) * p.rot_dim);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 c = __ldg(row + 2 * t + k), s = __ldg(row + p.rot_dim / 8 + 2 * t + k);
-      cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
-      sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
-    }
-  }
-
+  // the rows, on their way while the place is looked up
   uint4 in[NR][2];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
@@ -120,6 +97,31 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const AppendParams p) 
     in[i][0] = s4[is_v ? 2 * t : rc0];
     in[i][1] = s4[is_v ? 2 * t + 1 : rc1];
   }
+
+  const bool reporter = t == 0 && r0 == 0;
+  if (b < 0 || b >= p.batch || pos < 0 || pos >= p.max_blocks * kPageSize ||
+      (turn && pos >= p.max_pos)) {
+    if (reporter) record_error(p.status, PA_ERR_BAD_INDEX);
+    return;
+  }
+  const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPageSize];
+  float cs[8], sn[8];
+  if (mine) {
+    const float4 *row = reinterpret_cast<const float4 *>(
+        p.cos_sin + static_cast<size_t>(pos) * p.rot_dim);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 c = __ldg(row + 2 * t + k), s = __ldg(row + p.rot_dim / 8 + 2 * t + k);
+      cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
+      sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
+    }
+  }
+  if (page < 0 || page >= p.num_pages) {
+    if (reporter) record_error(p.status, PA_ERR_BAD_BLOCK);
+    return;
+  }
+  const int slot = pos % kPageSize;
+
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int r = r0 + i * p.row_lanes;
@@ -188,14 +190,27 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const AppendParams p) 
       uint32_t zb = round16<BF16>(__fmaf_rn(8.f, s, mn), z);
       const bool fine = fabsf(range) <= FLT_MAX && fabsf(s) <= FLT_MAX && fabsf(z) <= FLT_MAX;
       if (!fine) sb = zb = BF16 ? 0x7fc0u : 0x7e00u;
+      // (x - z) / s by the reciprocal, within 2^-21 of the quotient; a row with an
+      // element that near the border between two codes is divided out
       const bool step = fine && s > 0.f;
-      uint32_t code[2] = {0u, 0u};
+      const float inv = step ? __fdiv_rn(1.f, s) : 0.f;
+      float c[16];
+      bool near = false;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        float c = 8.f;
-        if (step) c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], z), s)) + 8.f, 0.f), 15.f);
-        code[k >> 3] |= static_cast<uint32_t>(c) << (4 * (k & 7));
+        const float y = __fsub_rn(x[k], z) * inv;
+        c[k] = rintf(y);
+        near |= !(fabsf(y - c[k]) < 0.4999f);
       }
+      if (near && step) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) c[k] = rintf(__fdiv_rn(__fsub_rn(x[k], z), s));
+      }
+      uint32_t code[2] = {0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        code[k >> 3] |= static_cast<uint32_t>(step ? fminf(fmaxf(c[k] + 8.f, 0.f), 15.f) : 8.f)
+                        << (4 * (k & 7));
       uint8_t *blk = p.kv4 + (static_cast<size_t>(page) * p.n_kv_heads + g) *
                                  kv4::block_bytes(D);
       uint32_t *row = reinterpret_cast<uint32_t *>(blk + kv4::code_offset(D, is_v, slot));
@@ -249,61 +264,80 @@ int launch_append_t(const AppendRopeLaunch &a, cudaStream_t stream) {
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// ---- read: thread = 16 dimensions of one (token, kv head, K or V) row
+// ---- read: a CTA takes `per_cta` tokens, whose places its first threads look up for
+// all; a thread 8 dimensions (16 bytes out) of four rows at a time
 struct ReadParams {
   const uint8_t *cache;
   const int32_t *block_table, *seq_idx, *pos;
   uint16_t *k_out, *v_out;
   int *status;
-  int64_t total;
-  int n_kv_heads, batch, max_blocks, num_pages;
+  int n_tok, per_cta, n_kv_heads, batch, max_blocks, num_pages;
 };
+constexpr int kReadThreads = 256, kReadTokens = 64;  // tokens a CTA at most
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) read_kv4_kernel(const ReadParams p) {
-  constexpr int TPR = D / 16;
+__global__ void __launch_bounds__(kReadThreads) read_kv4_kernel(const ReadParams p) {
+  constexpr int TPR = D / 8, kUnroll = 4;
+  __shared__ const uint8_t *place[kReadTokens];  // the token's page, or null
+  __shared__ int slots[kReadTokens];
   griddep_release();
   griddep_wait();
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (idx >= p.total) return;
-  const int t = static_cast<int>(idx % TPR);
-  int64_t u = idx / TPR;
-  const int g = static_cast<int>(u % p.n_kv_heads);
-  u /= p.n_kv_heads;
-  const int which = static_cast<int>(u & 1);
-  const int64_t j = u >> 1;
-  const int b = p.seq_idx[j], pos = p.pos[j];
-  const bool reporter = t == 0 && g == 0 && which == 0;
-  if (b < 0 || b >= p.batch || pos < 0 || pos >= p.max_blocks * kPageSize) {
-    if (reporter) record_error(p.status, PA_ERR_BAD_INDEX);
-    return;
+  const int j0 = blockIdx.x * p.per_cta, n = min(p.per_cta, p.n_tok - j0);
+  const int64_t page_bytes = static_cast<int64_t>(p.n_kv_heads) * kv4::block_bytes(D);
+  if (threadIdx.x < n) {
+    const int b = p.seq_idx[j0 + threadIdx.x], pos = p.pos[j0 + threadIdx.x];
+    const uint8_t *at = nullptr;
+    if (b < 0 || b >= p.batch || pos < 0 || pos >= p.max_blocks * kPageSize) {
+      record_error(p.status, PA_ERR_BAD_INDEX);
+    } else {
+      const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPageSize];
+      if (page < 0 || page >= p.num_pages)
+        record_error(p.status, PA_ERR_BAD_BLOCK);
+      else
+        at = p.cache + page * page_bytes;
+    }
+    place[threadIdx.x] = at;
+    slots[threadIdx.x] = pos & (kPageSize - 1);
   }
-  const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPageSize];
-  if (page < 0 || page >= p.num_pages) {
-    if (reporter) record_error(p.status, PA_ERR_BAD_BLOCK);
-    return;
-  }
-  const int slot = pos % kPageSize;
-  const uint8_t *blk =
-      p.cache + (static_cast<size_t>(page) * p.n_kv_heads + g) * kv4::block_bytes(D);
-  const uint2 codes =
-      *reinterpret_cast<const uint2 *>(blk + kv4::code_offset(D, which, slot) + 8 * t);
-  const float2 sz = unpack2<BF16>(
-      *reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, which, slot)));
-  uint32_t o[8];
+  __syncthreads();
+  // unit (token, K or V, kv head, 8 dimensions), the last fastest
+  const uint32_t heads = p.n_kv_heads, total = n * 2u * heads * TPR;
+  for (uint32_t u0 = threadIdx.x; u0 < total; u0 += kUnroll * kReadThreads) {
+    uint32_t code[kUnroll], meta[kUnroll];
+    uint4 *dst[kUnroll];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t w = (k < 4 ? codes.x : codes.y) >> (8 * (k & 3));
-    // the product of a 16-bit scale and a code is exact: one rounding to fp32
-    const float lo = __fmaf_rn(sz.x, static_cast<float>(static_cast<int>(w & 15) - 8), sz.y);
-    const float hi =
-        __fmaf_rn(sz.x, static_cast<float>(static_cast<int>((w >> 4) & 15) - 8), sz.y);
-    o[k] = pack2<BF16>(lo, hi);
+    for (int i = 0; i < kUnroll; ++i) {
+      const uint32_t u = u0 + i * kReadThreads;
+      dst[i] = nullptr;
+      if (u >= total) continue;
+      const uint32_t t = u % TPR, row = u / TPR, kv = row / heads, g = row - kv * heads;
+      const uint32_t which = kv & 1, j = kv >> 1;
+      const uint8_t *blk = place[j];
+      if (!blk) continue;
+      blk += static_cast<size_t>(g) * kv4::block_bytes(D);
+      const int slot = slots[j];
+      code[i] = __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::code_offset(D, which, slot)) + t);
+      meta[i] = __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, which, slot)));
+      dst[i] = reinterpret_cast<uint4 *>(which ? p.v_out : p.k_out) +
+               (static_cast<size_t>(j0 + j) * heads + g) * TPR + t;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      if (!dst[i]) continue;
+      const float2 sz = unpack2<BF16>(meta[i]);
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = code[i] >> (8 * k);
+        // the product of a 16-bit scale and a code is exact: one rounding to fp32
+        const float lo = __fmaf_rn(sz.x, static_cast<float>(static_cast<int>(w & 15) - 8), sz.y);
+        const float hi =
+            __fmaf_rn(sz.x, static_cast<float>(static_cast<int>((w >> 4) & 15) - 8), sz.y);
+        o[k] = pack2<BF16>(lo, hi);
+      }
+      *dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
-  uint4 *dst = reinterpret_cast<uint4 *>((which ? p.v_out : p.k_out) +
-                                         (j * p.n_kv_heads + g) * D + 16 * t);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <int D, bool BF16>
@@ -316,15 +350,21 @@ int launch_read_t(const ReadKv4Launch &a, cudaStream_t stream) {
   p.k_out = static_cast<uint16_t *>(a.k_out);
   p.v_out = static_cast<uint16_t *>(a.v_out);
   p.status = a.status;
+  p.n_tok = a.n_tok;
   p.n_kv_heads = a.n_kv_heads;
   p.batch = a.batch;
   p.max_blocks = a.max_blocks;
   p.num_pages = a.num_pages;
-  p.total = static_cast<int64_t>(a.n_tok) * a.n_kv_heads * 2 * (D / 16);
-  const int64_t blocks = (p.total + 255) / 256;
-  if (blocks > 0x7fffffff) return PA_ERR_SHAPE;
-  return launch_pdl(read_kv4_kernel<D, BF16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                    stream, p) == cudaSuccess
+  // Four rows a thread once that fills the GPU twice; one token a CTA before.
+  const int per_token = 2 * a.n_kv_heads * (D / 8);
+  int tokens = 4 * kReadThreads / per_token;
+  if (tokens < 1) tokens = 1;
+  if (tokens > kReadTokens) tokens = kReadTokens;
+  if (static_cast<int64_t>(a.n_tok) < static_cast<int64_t>(tokens) * 152 * 8) tokens = 1;
+  p.per_cta = tokens;
+  const int blocks = (a.n_tok - 1) / tokens + 1;
+  return launch_pdl(read_kv4_kernel<D, BF16>, dim3(blocks), dim3(kReadThreads), 0, stream, p) ==
+                 cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }
