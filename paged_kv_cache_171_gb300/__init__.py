@@ -719,14 +719,11 @@ class _On:
             g.__exit__(*exc)
 
 
-def _run(index, stream, call):
-    """call(handle) on device `index`: directly when it is the current one and no
-    stream is named (the usual case), else under _On."""
+def _elsewhere(index, stream):
+    """True unless the call is for the current device and its current stream (the
+    usual case, found out cheaply); then it is made again under _On."""
     import torch
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return call(torch._C._cuda_getCurrentRawStream(index))
-    with _On(index, stream) as handle:
-        return call(handle)
+    return stream is not None or torch._C._cuda_getDevice() != index
 
 
 def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
@@ -765,8 +762,9 @@ def _kv4_dims(kv_cache, index):
 
 
 def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, hkv_cache, D_cache,
-            block_table, seq_idx, pos, cos_sin, interleaved, stream):
-    """The common part of the two rotated appends: `entry` with `caches` (pointers)."""
+            block_table, seq_idx, pos, cos_sin, interleaved, index):
+    """The common part of the two rotated appends, on the current stream of device
+    `index`: `entry` with `caches` (pointers)."""
     import torch
     if k_new.dim() != 3:
         raise ValueError(f"k_new: want [n_tok, n_kv_heads, head_dim], got {tuple(k_new.shape)}")
@@ -774,40 +772,36 @@ def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, 
     if hkv != hkv_cache or D != D_cache:
         raise ValueError(f"the cache holds {hkv_cache} heads of head_dim {D_cache}, k_new has "
                          f"{hkv} of {D}")
-    dtype, index = k_new.dtype, k_new.get_device()
-    code = dtype_code(k_new)
+    dtype, i32 = k_new.dtype, torch.int32
     ks = _token_stride(k_new, "k_new", dtype, index, n_tok, hkv, D)
     vs = _token_stride(v_new, "v_new", dtype, index, n_tok, hkv, D)
-    batch, max_blocks = _want_2d(block_table, "block_table", torch.int32, None, index)
-    _want(seq_idx, "seq_idx", torch.int32, (n_tok,), index)
-    _want(pos, "pos", torch.int32, (n_tok,), index)
+    batch, max_blocks = _want_2d(block_table, "block_table", i32, None, index)
+    _want(seq_idx, "seq_idx", i32, (n_tok,), index)
+    _want(pos, "pos", i32, (n_tok,), index)
     max_pos = rot = hq = qs = 0
+    table = q_in = q_to = None
     if cos_sin is not None:
         max_pos, rot = _want_2d(cos_sin, "cos_sin", torch.float32, None, index)
+        table = cos_sin.data_ptr()
     if q is not None:
         if q.dim() != 3:
             raise ValueError(f"q: want [n_tok, n_q_heads, head_dim], got {tuple(q.shape)}")
         hq = q.shape[1]
         qs = _token_stride(q, "q", dtype, index, n_tok, hq, D)
-        if q_out is not None:
+        if q_out is None:
+            q_out = torch.empty((n_tok, hq, D), dtype=dtype, device=q.device)
+        else:
             _want(q_out, "q_out", dtype, (n_tok, hq, D), index)
+        q_in, q_to = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    index = _device_index(k_new)
-
-    def call(handle):
-        to = q_out
-        if q is not None and to is None:
-            to = torch.empty((n_tok, hq, D), dtype=dtype, device=q.device)
-        _check(entry(k_new.data_ptr(), v_new.data_ptr(), None if q is None else q.data_ptr(),
-                     *caches, None if to is None else to.data_ptr(), block_table.data_ptr(),
-                     seq_idx.data_ptr(), pos.data_ptr(),
-                     None if cos_sin is None else cos_sin.data_ptr(), n_tok, ks, vs, qs, hq, hkv,
-                     D, page_size, batch, max_blocks, num_pages, max_pos, rot, int(interleaved),
-                     code, handle), where)
-        return to
-
-    return _run(index, stream, call)
+    rc = entry(k_new.data_ptr(), v_new.data_ptr(), q_in, *caches, q_to, block_table.data_ptr(),
+               seq_idx.data_ptr(), pos.data_ptr(), table, n_tok, ks, vs, qs, hq, hkv, D,
+               page_size, batch, max_blocks, num_pages, max_pos, rot, bool(interleaved),
+               dtype_code(k_new), torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, where)
+    return q_out
 
 
 def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, cos_sin, q=None,
@@ -817,15 +811,19 @@ def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, co
     output); cos_sin float32 [max_pos, rot_dim] (rope_table).  Writes the caches
     [pages, h_kv, 16, D]; returns the rotated q ([n_tok, h_q, D], q_out if
     given), or None without q."""
+    index = _device_index(k_new)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos,
+                                  cos_sin, q, q_out, interleaved)
     if cos_sin is None or k_cache.dim() != 4:
         raise ValueError("append_kv_rope wants cos_sin and caches [pages, h_kv, 16, D]")
     pages, hkv, P, D = shape = k_cache.shape
-    index = k_new.get_device()
     _want(k_cache, "k_cache", k_new.dtype, shape, index)
     _want(v_cache, "v_cache", k_new.dtype, shape, index)
     return _append(lib().pa_append_kv_rope, "pa_append_kv_rope", k_new, v_new, q, q_out,
                    (k_cache.data_ptr(), v_cache.data_ptr()), pages, P, hkv, D, block_table,
-                   seq_idx, pos, cos_sin, interleaved, stream)
+                   seq_idx, pos, cos_sin, interleaved, index)
 
 
 def append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin=None, q=None,
@@ -833,10 +831,15 @@ def append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin=None, 
     """pa_append_kv4 on tensors: as append_kv_rope, into a 4-bit cache (kv4_cache);
     without cos_sin nothing is rotated.  The dtype of k_new is that of the cache's
     scales and zeros: keep to one for a cache.  Returns the rotated q, or None."""
-    pages, hkv, D = _kv4_dims(kv_cache, k_new.get_device())
+    index = _device_index(k_new)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin, q,
+                              q_out, interleaved)
+    pages, hkv, D = _kv4_dims(kv_cache, index)
     return _append(lib().pa_append_kv4, "pa_append_kv4", k_new, v_new, q, q_out,
                    (kv_cache.data_ptr(),), pages, 16, hkv, D, block_table, seq_idx, pos, cos_sin,
-                   interleaved, stream)
+                   interleaved, index)
 
 
 def read_kv4(kv_cache, block_table, seq_idx, pos, dtype=None, k_out=None, v_out=None,
@@ -845,87 +848,72 @@ def read_kv4(kv_cache, block_table, seq_idx, pos, dtype=None, k_out=None, v_out=
     values, each [n_tok, h_kv, D] of dtype (torch.bfloat16 or torch.float16, the
     type the cache was written with; k_out's if given)."""
     import torch
-    index = kv_cache.get_device()
+    index = _device_index(kv_cache)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return read_kv4(kv_cache, block_table, seq_idx, pos, dtype, k_out, v_out)
     pages, hkv, D = _kv4_dims(kv_cache, index)
     batch, max_blocks = _want_2d(block_table, "block_table", torch.int32, None, index)
-    if seq_idx.dim() != 1:
-        raise ValueError(f"seq_idx: want [n_tok], got {tuple(seq_idx.shape)}")
-    n_tok = seq_idx.shape[0]
+    n_tok = seq_idx.numel()
     _want(seq_idx, "seq_idx", torch.int32, (n_tok,), index)
     _want(pos, "pos", torch.int32, (n_tok,), index)
     if dtype is None:
         if k_out is None and v_out is None:
             raise ValueError("read_kv4 wants dtype, k_out or v_out")
         dtype = (k_out if k_out is not None else v_out).dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise TypeError(f"unsupported dtype {dtype}")
     shape = (n_tok, hkv, D)
-    if k_out is not None:
-        _want(k_out, "k_out", dtype, shape, index)
-    if v_out is not None:
-        _want(v_out, "v_out", dtype, shape, index)
-    _device_index(kv_cache)
-
-    def call(handle):
-        k = k_out if k_out is not None else torch.empty(shape, dtype=dtype, device=kv_cache.device)
-        v = v_out if v_out is not None else torch.empty(shape, dtype=dtype, device=kv_cache.device)
-        _check(lib().pa_read_kv4(kv_cache.data_ptr(), block_table.data_ptr(), seq_idx.data_ptr(),
-                                 pos.data_ptr(), k.data_ptr(), v.data_ptr(), n_tok, hkv, D, 16,
-                                 batch, max_blocks, pages, dtype_code(k), handle), "pa_read_kv4")
-        return k, v
-
-    return _run(index, stream, call)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=kv_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=kv_cache.device)
+    _want(k_out, "k_out", dtype, shape, index)
+    _want(v_out, "v_out", dtype, shape, index)
+    rc = lib().pa_read_kv4(kv_cache.data_ptr(), block_table.data_ptr(), seq_idx.data_ptr(),
+                           pos.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), n_tok, hkv, D, 16,
+                           batch, max_blocks, pages, dtype_code(k_out),
+                           torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_read_kv4")
+    return k_out, v_out
 
 
 def copy_pages_kv4(kv_cache, src, dst, stream=None):
     """pa_copy_pages_kv4 on tensors: page src[i] to page dst[i] (int32, on the device)."""
     import torch
     index = _device_index(kv_cache)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return copy_pages_kv4(kv_cache, src, dst)
     pages, hkv, D = _kv4_dims(kv_cache, index)
     n = src.numel()
     _want(src, "src", torch.int32, (n,), index)
     _want(dst, "dst", torch.int32, (n,), index)
-    _run(index, stream, lambda handle: _check(lib().pa_copy_pages_kv4(
-        kv_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, hkv, D, 16, pages, handle),
-        "pa_copy_pages_kv4"))
+    _check(lib().pa_copy_pages_kv4(kv_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, hkv, D,
+                                   16, pages, torch._C._cuda_getCurrentRawStream(index)),
+           "pa_copy_pages_kv4")
 
 
-def _attend(entry, where, need, q, n_new, kv_cache, block_table, ctx_lens, scale, out, out_dtype,
-            workspace, stream):
-    """The common part of decode_kv4 (n_new None) and prefill_kv4."""
+def _attention_args(q, kv_cache, block_table, ctx_lens, out, out_dtype, workspace, index):
+    """What decode_kv4 and prefill_kv4 have in common: the checks, and (B, h_q, D,
+    pages, h_kv, max_blocks, out)."""
     import torch
-    index = q.get_device()
     shape = q.shape
     B, hq, D = shape[0], shape[-2], shape[-1]
     pages, hkv, D4 = _kv4_dims(kv_cache, index)
     if D4 != D:
         raise ValueError(f"kv_cache holds head_dim {D4}, q has {D}")
-    code = dtype_code(q)
     if not q.is_contiguous():
         raise ValueError(f"q: want a contiguous tensor, got strides {tuple(q.stride())}")
     _, mb = _want_2d(block_table, "block_table", torch.int32, B, index)
     _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
-    if out is not None:
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    else:
         _want(out, "out", out_dtype, shape, index)
     if workspace is not None and (workspace.get_device() != index or
                                   not workspace.is_contiguous()):
         raise ValueError(f"workspace: want a contiguous tensor on cuda:{index}")
-    _device_index(q)
-
-    def call(handle):
-        o = out if out is not None else torch.empty(shape, dtype=out_dtype, device=q.device)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(need(B, hq, hkv, D, mb), dtype=torch.uint8, device=q.device)
-        args = (o.data_ptr(), scale, hq, hkv, D, 16, B, mb, pages, code, ws.data_ptr(), ws.nbytes,
-                handle)
-        if n_new is not None:
-            args = (n_new,) + args
-        _check(entry(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-                     ctx_lens.data_ptr(), *args), where)
-        return o
-
-    return _run(index, stream, call)
+    return B, hq, D, pages, hkv, mb, out
 
 
 def decode_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=None, stream=None):
@@ -935,11 +923,24 @@ def decode_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=No
     any tensor of pa_decode_kv4_workspace_size(D) bytes, not shared with a call
     that may run at the same time."""
     import torch
+    index = _device_index(q)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return decode_kv4(q, kv_cache, block_table, ctx_lens, scale, out, workspace)
     if q.dim() != 3:
         raise ValueError(f"q: want [B, h_q, D], got {tuple(q.shape)}")
-    return _attend(lib().pa_decode_kv4, "pa_decode_kv4",
-                   lambda B, hq, hkv, D, mb: pa_decode_kv4_workspace_size(D), q, None, kv_cache,
-                   block_table, ctx_lens, scale, out, torch.float32, workspace, stream)
+    B, hq, D, pages, hkv, mb, out = _attention_args(q, kv_cache, block_table, ctx_lens, out,
+                                                    torch.float32, workspace, index)
+    if workspace is None:
+        workspace = torch.empty(pa_decode_kv4_workspace_size(D), dtype=torch.uint8,
+                                device=q.device)
+    rc = lib().pa_decode_kv4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+                             ctx_lens.data_ptr(), out.data_ptr(), scale, hq, hkv, D, 16, B, mb,
+                             pages, dtype_code(q), workspace.data_ptr(), workspace.nbytes,
+                             torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_decode_kv4")
+    return out
 
 
 def prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=None,
@@ -948,11 +949,23 @@ def prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=N
     K/V rows append_kv4 has stored at positions ctx_lens[b] ..; ctx_lens = tokens
     cached before the chunk.  Returns [B, n_new, h_q, D] in q's dtype.  workspace:
     any tensor of pa_prefill_kv4_workspace_size(...) bytes, as in decode_kv4."""
+    import torch
+    index = _device_index(q)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out, workspace)
     if q.dim() != 4:
         raise ValueError(f"q: want [B, n_new, h_q, D], got {tuple(q.shape)}")
     n_new = q.shape[1]
-    return _attend(lib().pa_prefill_kv4, "pa_prefill_kv4",
-                   lambda B, hq, hkv, D, mb: pa_prefill_kv4_workspace_size(B, n_new, hq, hkv, D,
-                                                                           16, mb),
-                   q, n_new, kv_cache, block_table, ctx_lens, scale, out, q.dtype, workspace,
-                   stream)
+    B, hq, D, pages, hkv, mb, out = _attention_args(q, kv_cache, block_table, ctx_lens, out,
+                                                    q.dtype, workspace, index)
+    if workspace is None:
+        workspace = torch.empty(pa_prefill_kv4_workspace_size(B, n_new, hq, hkv, D, 16, mb),
+                                dtype=torch.uint8, device=q.device)
+    rc = lib().pa_prefill_kv4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+                              ctx_lens.data_ptr(), n_new, out.data_ptr(), scale, hq, hkv, D, 16,
+                              B, mb, pages, dtype_code(q), workspace.data_ptr(), workspace.nbytes,
+                              torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_prefill_kv4")
+    return out
