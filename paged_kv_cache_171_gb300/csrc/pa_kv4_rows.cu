@@ -5,7 +5,7 @@
 // K = zero_k + scale_k (c - 8) and V alike, c the 4-bit codes.  The codes go
 // into the tensor cores as they are (exact in 16 bits) and the scales and
 // zeros are applied outside,
-//   s_t = scale_k[t] (q . c_t - 8 sum q) + zero_k[t] sum q
+//   s_t = scale_k[t] (q . (c_t - 8)) + zero_k[t] sum q
 //   O   = sum_t (p_t scale_v[t]) (c_t - 8),   z = sum_t p_t zero_v[t]
 // so a page costs no dequantisation beyond turning nibbles into 16-bit floats.
 //
@@ -16,27 +16,23 @@
 // of codes, and because the contraction index may be permuted freely (q, or the
 // order of tokens, is permuted alike) two nibbles four places apart in one
 // word, or the same nibble of two tokens' words, form an operand register.
-//   K: x & 0x000f000f as fp16 is the subnormal c 2^-24, x & 0x00f000f0 is
-//      c 2^-20: one AND gives two elements.  q is scaled by a power of two a
-//      row (its largest magnitude near 2^15, exact in fp16 down to 2^-39 of the
-//      row's largest) with the slots of the second kind divided by 16.
-//   V: the accumulation over tokens is long, and tensor-core sums round toward
-//      zero, so the codes are centred first: (x & 0x000f000f) | 0x64006400 is
-//      1024 + c, minus 1032; (x & 0x00f000f0) | 0x64006400 is 1024 + 16 c,
-//      times 1/16 minus 72; both exact.  Uncentred, the sum of 8 p would drown
-//      a diffuse row's result in rounding.
-// The weights p scale_v enter as two fp16 terms (head and remainder, 22 bits).
-// Products of a head term and a code have 15 bits, so their sums hardly ever
-// round; a remainder added to such a sum always would, toward zero, so the two
-// are accumulated apart (4 rows or fewer) or page by page in an accumulator of
-// their own that is added to the state with a rounding add (measured on the 32k
-// rows at 8 rows a tile: error 9e-6 of the result in one accumulator).
-// They are taken relative to a power of two above the largest |scale_v| so far
-// and multiplied by 2^7, so that they stay below 2^15 and the second term
-// reaches 2^-32 of the largest.  With at most 4 rows (WIDE false) columns 4-7
-// repeat columns 0-3 and carry the second terms: one MMA does both.  The
-// weights, in the accumulator's layout (token, row), become the second
-// product's operand (row, token) by movmatrix.
+// The tensor cores align the addends of a sum to the largest and round toward zero, so
+// operands are centred first: (x & 0x000f000f) | 0x64006400 is 1024 + c, minus 1032;
+// (x & 0x00f000f0) | 0x64006400 is 1024 + 16 c, times 1/16 minus 72; both exact.
+// Codes as they are (one AND, as fp16 subnormals) would save the 64 subtractions a page,
+// but sums that carry 8 sum q or 8 sum p lose the last bits of the result: for K
+// measured 1.3e-6 of the result's norm against 2e-7 (8% faster), for V 1e-4.  q is
+// scaled by a power of two a row (its largest magnitude near 2^15; exact in fp16 down
+// to 2^-39 of that).
+// The weights p scale_v enter as two fp16 terms (head and remainder, 22 bits), relative
+// to a power of two above the largest |scale_v| so far and multiplied by 2^7: they stay
+// below 2^15 and the second term reaches 2^-32 of the largest.  With at most 4 rows
+// (WIDE false) columns 4-7 repeat columns 0-3 and carry the second terms: one MMA does
+// both.  The weights, in the accumulator's layout (token, row), become the second
+// product's operand (row, token) by movmatrix.  The sums of each two pages are taken in
+// an accumulator of their own and added to the state with a rounding add, because the
+// tensor cores' roundings toward zero add up along a long context (measured on 32k
+// tokens, 8 rows: error 9e-6 of the result in one accumulator, 8e-7 so).
 //
 // Work split.  The pages of all (sequence, kv head, row tile) items, laid end to
 // end, are cut into equal runs: a ragged batch takes the time of its pages, not of
@@ -45,7 +41,8 @@
 // run's pages two by two in turn, each with its own ring of stages filled by bulk
 // copies, and merge their (m, l, O) states when an item ends.  An item cut between
 // teams leaves one state a team, folded in order of position by a second kernel
-// (results do not depend on timing).
+// (results do not depend on timing).  Runs go round the SMs, so that a call with few
+// of them has one an SM (1 x 512 tokens of 16 heads: 21.0 -> 14.8 us of device time).
 #include "pa_device.cuh"
 #include "pa_kv4.cuh"
 
@@ -388,7 +385,7 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
   extern __shared__ __align__(128) uint8_t smem_all[];
   // a team is a unit of its own from here on: own shared memory, own barrier
   const int team = threadIdx.x / (kWarps * 32), tid = threadIdx.x % (kWarps * 32);
-  const int team_id = blockIdx.x * kTeams + team;
+  const int team_id = team * gridDim.x + blockIdx.x;
   uint8_t *smem = smem_all + team * L::kTeam;
   volatile uint32_t *done = reinterpret_cast<volatile uint32_t *>(smem_all + L::kDone);
   const uint32_t sb = smem_u32(smem);
@@ -519,16 +516,15 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
       // 2^ex brings the row's largest magnitude into [2^14, 2^15)
       const int ex = min(90, max(-90, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
       const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-      const float up16 = up * 0.0625f;
 #pragma unroll
       for (int k = 0; k < KW; ++k)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int d0 = 8 * k + 2 * s;
           qb[2 * k + s][0] = pack2<false>(x[d0] * up, x[d0 + 4] * up);
-          qb[2 * k + s][1] = pack2<false>(x[d0 + 1] * up16, x[d0 + 5] * up16);
+          qb[2 * k + s][1] = pack2<false>(x[d0 + 1] * up, x[d0 + 5] * up);
         }
-      const float f = p.qscale * __uint_as_float(static_cast<uint32_t>(127 + 24 - ex) << 23);
+      const float f = p.qscale * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
       const float e = p.qscale * total_q;
       f0 = __shfl_sync(kFull, f, 8 * lc);
       f1 = __shfl_sync(kFull, f, 8 * lc + 4);
@@ -536,9 +532,9 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
       e1 = __shfl_sync(kFull, e, 8 * lc + 4);
     }
 
-    float o[MT][4];
+    float2 o[MT][2];  // rows ln and ln + 8 of a row tile, columns 2 lc and 2 lc + 1
 #pragma unroll
-    for (int k = 0; k < MT; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+    for (int k = 0; k < MT; ++k) o[k][0] = o[k][1] = make_float2(0.f, 0.f);
     // per row 2 lc (x) and 2 lc + 1 (y): the running max, negated, the sums l and z
     float2 nm = make_float2(-kNoKey, -kNoKey);
     float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
@@ -596,18 +592,20 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t xa = ka[k] >> (8 * h), xb = kb[k] >> (8 * h);
-            const uint32_t a[4] = {xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u,
-                                   xb & 0x00f000f0u};
+            const uint32_t a[4] = {sub_1032((xa & 0x000f000fu) | 0x64006400u),
+                                   sub_1032((xb & 0x000f000fu) | 0x64006400u),
+                                   sixteenth_sub_72((xa & 0x00f000f0u) | 0x64006400u),
+                                   sixteenth_sub_72((xb & 0x00f000f0u) | 0x64006400u)};
             if (k + h == 0)
               mma_from_zero(acc, a, qb[0][0], qb[0][1]);
             else
               mma16816<false>(acc, a, qb[2 * k + h][0], qb[2 * k + h][1]);
           }
         const float2 k0 = unpack2<BF16>(km0), k1 = unpack2<BF16>(km1);
-        s[2 * pg].x = fmaf(k0.x, fmaf(f0, acc[0], -8.f * e0), k0.y * e0);
-        s[2 * pg].y = fmaf(k0.x, fmaf(f1, acc[1], -8.f * e1), k0.y * e1);
-        s[2 * pg + 1].x = fmaf(k1.x, fmaf(f0, acc[2], -8.f * e0), k1.y * e0);
-        s[2 * pg + 1].y = fmaf(k1.x, fmaf(f1, acc[3], -8.f * e1), k1.y * e1);
+        s[2 * pg].x = fmaf(k0.x, f0 * acc[0], k0.y * e0);
+        s[2 * pg].y = fmaf(k0.x, f1 * acc[1], k0.y * e1);
+        s[2 * pg + 1].x = fmaf(k1.x, f0 * acc[2], k1.y * e0);
+        s[2 * pg + 1].y = fmaf(k1.x, f1 * acc[3], k1.y * e1);
       }
       const bool edge = key0 + kPair * kPageSize > lim_all;
       if (edge) {
@@ -663,10 +661,8 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         }
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
-          o[k][0] *= c.x;
-          o[k][1] *= c.y;
-          o[k][2] *= c.x;
-          o[k][3] *= c.y;
+          o[k][0] = __fmul2_rn(o[k][0], c);
+          o[k][1] = __fmul2_rn(o[k][1], c);
         }
 #pragma unroll
         for (int u = 0; u < 2 * kPair; ++u) d[u] = __fadd2_rn(s[u], nm);
@@ -698,47 +694,58 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         }
       }
 
-      // ---- O[dimension][row] += V^T P
+      // ---- O[dimension][row] += V^T P, the chunk's sum in an accumulator of its own
+      uint32_t va[kPair][4][VW];
 #pragma unroll
       for (int pg = 0; pg < kPair; ++pg) {
         const uint32_t col = st + pg * L::kBlock + kv4::code_offset(D, 1, 0) + 4 * VW * ln;
-        uint32_t va[4][VW];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t at = col + (u & 1 ? t1 : t0) + 8 * (u >> 1) * kv4::row_bytes(D);
           if constexpr (VW == 2) {
             const uint2 x = lds64(at);
-            va[u][0] = x.x, va[u][1] = x.y;
+            va[pg][u][0] = x.x, va[pg][u][1] = x.y;
           } else {
-            va[u][0] = lds32(at);
+            va[pg][u][0] = lds32(at);
           }
         }
-#pragma unroll
-        for (int j = 0; j < VW; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // nibbles 4 h .. 4 h + 3 of two tokens' words, one token a half
-            const uint32_t x = __byte_perm(va[0][j], va[1][j], h ? 0x7632 : 0x5410);
-            const uint32_t y = __byte_perm(va[2][j], va[3][j], h ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t xs = x >> (8 * u), ys = y >> (8 * u);
-              const uint32_t a[4] = {sub_1032((xs & 0x000f000fu) | 0x64006400u),
-                                     sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u),
-                                     sub_1032((ys & 0x000f000fu) | 0x64006400u),
-                                     sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u)};
-              float (&ok)[4] = o[4 * j + 2 * h + u];
-              if constexpr (WIDE) {
-                float t[4];
-                mma_from_zero(t, a, lo[2 * pg], lo[2 * pg + 1]);
-                mma16816<false>(t, a, hi[2 * pg], hi[2 * pg + 1]);
-                ok[0] += t[0], ok[1] += t[1], ok[2] += t[2], ok[3] += t[3];
-              } else {
-                mma16816<false>(ok, a, hi[2 * pg], hi[2 * pg + 1]);
-              }
-            }
-          }
       }
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // nibbles 4 h .. 4 h + 3 of two tokens' words, one token a half
+          uint32_t x[kPair], y[kPair];
+#pragma unroll
+          for (int pg = 0; pg < kPair; ++pg) {
+            x[pg] = __byte_perm(va[pg][0][j], va[pg][1][j], h ? 0x7632 : 0x5410);
+            y[pg] = __byte_perm(va[pg][2][j], va[pg][3][j], h ? 0x7632 : 0x5410);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t a[kPair][4];
+#pragma unroll
+            for (int pg = 0; pg < kPair; ++pg) {
+              const uint32_t xs = x[pg] >> (8 * u), ys = y[pg] >> (8 * u);
+              a[pg][0] = sub_1032((xs & 0x000f000fu) | 0x64006400u);
+              a[pg][1] = sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u);
+              a[pg][2] = sub_1032((ys & 0x000f000fu) | 0x64006400u);
+              a[pg][3] = sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u);
+            }
+            float t[4];
+            if constexpr (WIDE) {
+              mma_from_zero(t, a[0], lo[0], lo[1]);
+              mma16816<false>(t, a[1], lo[2], lo[3]);
+              mma16816<false>(t, a[0], hi[0], hi[1]);
+            } else {
+              mma_from_zero(t, a[0], hi[0], hi[1]);
+            }
+            mma16816<false>(t, a[1], hi[2], hi[3]);
+            float2 (&ok)[2] = o[4 * j + 2 * h + u];
+            ok[0] = __fadd2_rn(ok[0], make_float2(t[0], t[1]));
+            ok[1] = __fadd2_rn(ok[1], make_float2(t[2], t[3]));
+          }
+        }
       __syncwarp();  // the stage has been read by every lane
       if (feed.i < feed.n)
         feed.issue(p, lane);
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
     const float back = v_ref * 0x1p-7f;
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
-      float2 a = make_float2(o[k][0], o[k][2]), b = make_float2(o[k][1], o[k][3]);
+      float2 a = make_float2(o[k][0].x, o[k][1].x), b = make_float2(o[k][0].y, o[k][1].y);
       if constexpr (!WIDE) {  // columns 4-7 hold the remainder terms of 0-3
         a.x += __shfl_xor_sync(kFull, a.x, 2);
         a.y += __shfl_xor_sync(kFull, a.y, 2);
