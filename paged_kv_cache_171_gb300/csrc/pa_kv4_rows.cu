@@ -317,13 +317,6 @@ struct Feed {
   }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 // The kWarps states of each of n_r rows in shared memory, merged by the exponent
 // law; fn(row, first of 4 dimensions, O, m, l).
 template <int D, class Fn>
