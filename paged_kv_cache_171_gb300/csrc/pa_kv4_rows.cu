@@ -36,7 +36,9 @@
 //
 // Work split.  The pages of all (sequence, kv head, row tile) items, laid end to
 // end, are cut into equal runs: a ragged batch takes the time of its pages, not of
-// its longest sequence.  A run belongs to a team of 4 warps, and an SM holds 4
+// its longest sequence.  An item counts 12 pages more than it has, for what starting
+// and merging it costs (64 sequences of 128 to 8192 tokens: 97 -> 86 us; 3, 6, 10 and 16
+// pages took 89, 88, 89 and 85).  A run belongs to a team of 4 warps, and an SM holds 4
 // teams in one CTA, so that they can keep step (below).  A team's warps take its
 // run's pages two by two in turn, each with its own ring of stages filled by bulk
 // copies, and merge their (m, l, O) states when an item ends.  An item cut between
@@ -57,6 +59,7 @@ constexpr int kWarps = 4, kStages = 2, kTile = 8;  // query rows a tile
 constexpr int kPair = 2;         // pages a stage holds
 constexpr int kTeams = 4;        // teams of kWarps warps a CTA, one CTA an SM
 constexpr int kMinPages = kWarps * kPair;  // least pages a team takes
+constexpr int kPartPages = 12;   // what a part's start and merge cost, in pages
 constexpr uint32_t kLead = 2;         // chunks a warp may be ahead of the slowest team
 
 struct RowsParams {
@@ -150,11 +153,13 @@ struct Part {
 };
 static_assert(sizeof(Part) <= 64, "room in shared memory");
 
-// The team's run [w, w1) of the flattened page list, walked part by part by one
-// thread, which keeps the others' registers free of it.
+// The team's run [w, w1) of the flattened list of units, walked part by part by one
+// thread, which keeps the others' registers free of it.  A boundary between runs in or
+// right behind an item's kPartPages units counts as lying before the item, so that
+// every part has a page.
 struct Walk {
-  int64_t w, w1, run, base;  // base: pages of one (kv head, row tile) before sequence b
-  int b, n_b, tokens;        // the sequence, its pages and its tokens
+  int64_t w, w1, run, base;  // base: units of one (kv head, row tile) before sequence b
+  int b, n_b, tokens;        // the sequence, its units and its tokens
 
   // Tokens of sequence b, the chunk's included (a clamped length is reported by
   // the first team's scan).
@@ -171,6 +176,8 @@ struct Walk {
   static __device__ int pages_of(int tokens) {
     return max(1, (tokens + kPageSize - 1) / kPageSize);
   }
+  // Units of an item in the list: its pages behind kPartPages of its own.
+  static __device__ int units_of(int tokens) { return pages_of(tokens) + kPartPages; }
   // 64-bit division only where 32 bits do not hold the operands.
   static __device__ int64_t quotient(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
@@ -188,7 +195,7 @@ struct Walk {
 #pragma unroll 4
     for (int i = b0; i < b1; ++i) {
       const int t = tokens_of(p, i, team == 0);
-      sum += pages_of(t);
+      sum += units_of(t);
       if (i == b0) tokens = t;
     }
     int64_t incl = sum;
@@ -206,36 +213,39 @@ struct Walk {
     x.b = __shfl_sync(kFull, b0, src);
     x.base = __shfl_sync(kFull, incl - sum, src);
     x.tokens = __shfl_sync(kFull, tokens, src);
-    x.n_b = pages_of(x.tokens);
+    x.n_b = units_of(x.tokens);
     if (lane == 0) *out = x;
     return true;
   }
+  // (A run that ends before its first item's pages begin: n_pg < 1.)
   __device__ void next(const RowsParams &p, volatile Part &s) {
     const int heads = p.n_kv_heads * p.n_sub;
     while ((base + n_b) * heads <= w) {
       base += n_b;
       tokens = tokens_of(p, ++b, false);
-      n_b = pages_of(tokens);
+      n_b = units_of(tokens);
     }
     const int64_t rel = w - base * heads;
     const int item = static_cast<int>(quotient(rel, n_b));
-    const int pg0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
-    const int n_pg = static_cast<int>(min(static_cast<int64_t>(n_b - pg0), w1 - w));
-    const int64_t i0 = w - pg0;  // the item's first page
+    int u0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
+    const int64_t i0 = w - u0;  // the item's first unit
+    if (u0 <= kPartPages) u0 = 0;  // a boundary in an item's own units lies before it
+    const int pg0 = max(0, u0 - kPartPages);
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(n_b), w1 - i0));
     const int g = item / p.n_sub, sub = item - g * p.n_sub;
-    const int first = static_cast<int>(quotient(i0, run));
+    const int first = static_cast<int>(quotient(i0 + kPartPages, run));
     s.b = b;
     s.g = g;
     s.r0 = sub * p.tile_rows;
     s.n_r = min(p.tile_rows, p.n_rows - sub * p.tile_rows);
     s.pg0 = pg0;
-    s.n_pg = n_pg;
+    s.n_pg = u1 - kPartPages - pg0;
     s.tokens = tokens;
     s.first = first;
     s.last = static_cast<int>(quotient(i0 + n_b - 1, run));
-    s.slot = i0 == first * run ? 0 : 1;
-    w += n_pg;
-    s.more = w < w1;
+    s.slot = i0 <= first * run ? 0 : 1;
+    w = i0 + u1;
+    s.more = w + kPartPages < w1;
   }
 };
 
@@ -398,10 +408,11 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
   volatile int *flags = reinterpret_cast<volatile int *>(smem + L::kFlags);
   Walk *walk = reinterpret_cast<Walk *>(smem + L::kWalk);
   if (warp == kWarps - 1) {  // the warp with the fewest pages plans, two parts ahead
-    const bool any = Walk::start(p, team_id, gridDim.x * kTeams, lane, walk);
+    bool any = Walk::start(p, team_id, gridDim.x * kTeams, lane, walk);
     if (lane == 0) {
+      if (any) walk->next(p, parts[0]);
+      any = any && parts[0].n_pg > 0;
       if (any) {
-        walk->next(p, parts[0]);
         if (parts[0].more) walk->next(p, parts[1]);
       } else {
         done[team] = 0x7fffffff;
