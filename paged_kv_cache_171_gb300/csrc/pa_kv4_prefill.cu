@@ -30,7 +30,9 @@
 // An item of at most 128 rows (a short chunk) has its rows in both tiles, which split
 // the key tiles instead: A the even ones, B the odd ones, so that one's softmax still
 // overlaps the other's products.  At the end A reads both O's (the lanes hold the same
-// rows) and merges the two states.
+// rows) and merges the two states.  Of at most 64 rows, the softmax warps of the upper
+// rows have none: these four turn the odd key tiles' codes, the converters the even ones'
+// (4 queries x 8 heads over 32k keys: 114 -> XX us).
 //
 // Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B, warps
 // 4-7 turn codes into the K and V operand tiles (two stages each), a warp 32 keys of
@@ -64,6 +66,7 @@ constexpr int kItemRows = 2 * kRows;
 constexpr int kStages = 2;                  // of K and of V
 constexpr int kConvertWarp0 = 4, kSoftmaxWarp0 = 8;
 constexpr int kThreads = 16 * 32;
+constexpr int kRawPages = 3;                // a converter warp's ring
 
 struct PrefillParams {
   const uint16_t *q;
@@ -91,10 +94,15 @@ struct PrefillSmem {
   // scale_v / v_ref x2, zero_v x2.  Else kRowF: the factor of each row's S.
   static constexpr int kMeta = kV + kStages * kTile;
   static constexpr int kRowF = kMeta;
+  // the converters' rings of pages: the first group's, and, where the two row tiles are
+  // one and Q_B not needed, the second group's
+  static constexpr int kRing = 4 * kRawPages * kv4::block_bytes(D);
+  static constexpr int kRaw = kMeta + kStages * (kKeys / 2) * 32, kRaw1 = kQ + kTile;
+  static_assert(kRing <= kTile, "room in Q_B");
   // per stage: k_ref of each 32 keys, then v_ref
-  static constexpr int kRef = kMeta + kStages * (kKeys / 2) * 32;
+  static constexpr int kRef = kRaw + kRing;
   static constexpr int kBars = kRef + kStages * 32;
-  static constexpr int kSlot = kBars + 22 * 8;        // TMEM address, abort flag
+  static constexpr int kSlot = kBars + 46 * 8;        // TMEM address, abort flag
   static constexpr int kPart = kSlot + 16;
   static constexpr int kWalk = kPart + 64;
   static constexpr int kBytes = kWalk + 64;
@@ -111,7 +119,8 @@ enum {
   kBarP = 14,      // keys 64 h .. 64 h + 63 of P_x in TMEM, at + 2 x + h (4 arrivals)
   kBarO = 18,      // the last P_x V done (commit), at + x
   kBarDrain = 20,  // an MMA warp's own drain on its failure path, at + x
-  kNumBars = 22
+  kBarRaw = 22,    // page s of the ring of converter w of group c, at + 3 (4 c + w) + s
+  kNumBars = 46
 };
 
 // The part of one item that a CTA's run holds.
@@ -264,16 +273,24 @@ __device__ __forceinline__ float exp2i(int k) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
-// Converter warp w: keys 32 w .. 32 w + 31 (two pages) of every key tile, K then V,
-// and their references and, in the exact form, scales and zeros.  A tile's codes come
-// straight into registers, K's once the K tile before is done and V's alike; the pages
-// are asked into L2 three tiles ahead, so that these loads have only its latency.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Converter warp w of group c: keys 32 w .. 32 w + 31 (two pages) of the key tiles c,
+// c + step, .., K then V, and their references and, in the exact form, scales and zeros.
+// The pages come through a ring of the warp's own, by bulk copies 1.5 tiles ahead.
 //
 // A row past the sequence's end stands for zeros (it may hold anything, and 0 * NaN is
 // NaN).  A key or value row that is not finite makes its key's score NaN, which
 // masking removes for the queries that do not see it, and its values zero.
 template <int D, bool BF16, bool EXACT>
-__device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
+__device__ __forceinline__ void convert_tiles(int c, int step, int w, const PrefillParams &p,
                                               const TilePart &part, uint32_t sb, uint8_t *smem,
                                               const Tiling &tl, volatile int *abort_flag,
                                               int lane) {
@@ -290,58 +307,75 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
   // the upper column block's pieces (head_dim 128) take another row than the lower's, so
   // that no two lanes of a store meet in a bank
   const int piece = lane % kPieces, row_l = (lane / kPieces) ^ (piece >= 2 ? 4 : 0);
+  const uint32_t raw0 = sb + (c == 0 ? L::kRaw : L::kRaw1) + w * kRawPages * kBlock;
+  const uint32_t raw_bar = bar(kBarRaw + kRawPages * (4 * c + w));
 
-  // The page id of tile t that this lane's parity names; past the end page 0 (masked).
-  auto id_of = [&](int t) {
+  // Page ids: lane l holds page l & 1 of the warp's two in its tile 16 v + (l >> 1), v
+  // the window; past the sequence's end page 0, which is masked.
+  auto ids_of = [&](int v) {
+    const int t = c + (16 * v + (lane >> 1)) * step;
     const int pg = (part.t0 + t) * kPagesTile + 2 * w + (lane & 1);
     return t < part.nt && pg < n_pages ? __ldg(bt_row + pg) : 0;
   };
-  const uint8_t *pages[2];  // of the tile whose codes are asked for
-  auto turn_to = [&](int id) {
-    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
-      record_error(p.status, PA_ERR_BAD_BLOCK);
-      id = 0;
+  int ids = ids_of(0), ids_next = ids_of(1);
+  int issued = 0;  // the warp's pages, 2 a tile; page i sits in ring slot i % kRawPages
+  const int total = c < part.nt ? 2 * ((part.nt - c + step - 1) / step) : 0;
+  // the next pages, as many as `most` (1 or 2), a lane each
+  auto issue = [&](int most) {
+    const int n = min(most, total - issued);
+    if ((issued & 31) == 0 && issued > 0) {
+      ids = ids_next;
+      ids_next = ids_of((issued >> 5) + 1);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      pages[u] = head + static_cast<uint64_t>(static_cast<uint32_t>(
-                            __shfl_sync(kFull, id, u))) * p.page_bytes;
+    // the second page may be the next window's first
+    const int from = (issued + (lane & 1)) & 31;
+    int id = __shfl_sync(kFull, ids, from);
+    const int id_next = __shfl_sync(kFull, ids_next, from);
+    if ((issued & 31) == 31 && (lane & 1)) id = id_next;
+    if (lane < n) {  // (behind a proxy fence, where a slot has been read)
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
+        record_error(p.status, PA_ERR_BAD_BLOCK);
+        id = 0;
+      }
+      const int s = (issued + lane) % kRawPages;
+      mbar_arrive_expect_tx(raw_bar + 8 * s, kBlock);
+      bulk_load(raw0 + s * kBlock,
+                head + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes, kBlock,
+                raw_bar + 8 * s);
+    }
+    if (n == 2 && (issued & 31) == 31) {
+      ids = ids_next;
+      ids_next = ids_of(((issued + 1) >> 5) + 1);
+    }
+    issued += max(0, n);
   };
-  uint4 codes[2][2 * kIters];
-  uint32_t meta_k = 0, meta_v = 0;  // of row `lane` of the warp's 32
-  auto load = [&](int which) {
-#pragma unroll
-    for (int i = 0; i < 2 * kIters; ++i)
-      codes[which][i] = __ldcg(reinterpret_cast<const uint4 *>(
-          pages[i / kIters] + kv4::code_offset(D, which, 0) +
-          ((i % kIters) * (32 / kPieces) + row_l) * kv4::row_bytes(D) + 16 * piece));
-  };
-  auto load_meta = [&] {
-    const uint8_t *blk = (lane < kPageSize ? pages[0] : pages[1]) + 4 * (lane % kPageSize);
-    meta_k = __ldcg(reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, 0, 0)));
-    meta_v = __ldcg(reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, 1, 0)));
-  };
-  auto prefetch = [&](int id, int t) {
-    if (lane < 2 && t < part.nt && static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages))
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                       head + static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.page_bytes),
-                   "n"(kBlock)
-                   : "memory");
-  };
-  turn_to(id_of(0));
-  int id1 = id_of(1), id2 = id_of(2), id3 = id_of(3);  // of the tiles that follow
-  load_meta();
-  load(0);
-  load(1);
-  prefetch(id1, 1);
-  prefetch(id2, 2);
+  issue(2);
+  issue(1);
 
   bool ok = true;
-  int t = 0;
-  for (; t < part.nt; ++t) {
-    const int s = t % kStages;
-    prefetch(id3, t + 3);
-    float2 k = unpack2<BF16>(meta_k), v = unpack2<BF16>(meta_v);  // scale, zero
+  int t = c;
+  for (int i = 0; t < part.nt; t += step, i += 2) {
+    const int s0 = i % kRawPages, s1 = (i + 1) % kRawPages;
+    ok = warp_wait2(raw_bar + 8 * s0, (i / kRawPages) & 1, raw_bar + 8 * s1,
+                    ((i + 1) / kRawPages) & 1, abort_flag);
+    if (!ok) break;
+    const uint32_t raw[2] = {raw0 + s0 * kBlock, raw0 + s1 * kBlock};
+    // ---- scales and zeros of row `lane` of the warp's 32
+    float2 k, v;
+    {
+      const uint32_t blk = lane < kPageSize ? raw[0] : raw[1];
+      k = unpack2<BF16>(lds32(blk + kv4::meta_offset(D, 0, 0) + 4 * (lane % kPageSize)));
+      v = unpack2<BF16>(lds32(blk + kv4::meta_offset(D, 1, 0) + 4 * (lane % kPageSize)));
+    }
+    // the codes into registers, the next pages into their slots
+    uint4 codes[2 * kIters], v_codes[2 * kIters];
+#pragma unroll
+    for (int i = 0; i < 2 * kIters; ++i) {
+      const uint32_t at = raw[i / kIters] +
+                          ((i % kIters) * (32 / kPieces) + row_l) * kv4::row_bytes(D) + 16 * piece;
+      codes[i] = lds128(at);
+      v_codes[i] = lds128(at + kPageSize * kv4::row_bytes(D));
+    }
     if ((part.t0 + t) * kKeys + 32 * w + lane >= tokens) {
       k = v = make_float2(0.f, 0.f);
     } else if (!(fabsf(k.x) <= FLT_MAX && fabsf(k.y) <= FLT_MAX && fabsf(v.x) <= FLT_MAX &&
@@ -355,15 +389,17 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
     if (!EXACT) k_top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(k_top, 0.f))));
     v_top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(v_top, 0.f))));
     const float k_ref = EXACT ? 1.f : above(k_top), v_ref = above(v_top);
-    const bool more = t + 1 < part.nt;
 
-    auto convert = [&](int which, float2 own, float ref) {
+    const int s = t % kStages;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
       const int free = which ? kBarVFree : kBarKFree;
       if (t >= kStages)  // with one reader, its barrier twice
         ok = warp_wait2(bar(free + 2 * tl.first(s) + s), (t / kStages - 1) & 1,
                         bar(free + 2 * tl.last(s) + s), (t / kStages - 1) & 1, abort_flag);
-      if (!ok) return;
-      const float inv = exp2i(-exponent(ref));
+      if (!ok) break;
+      const float inv = exp2i(-exponent(which ? v_ref : k_ref));
+      const float2 own = which ? v : k;
       // over 2^7 ref: |scale| 2^24 is at most 2^14
       const uint32_t scales = pack2<false>(own.x * inv * 0x1p17f, own.x * inv * 0x1p13f);
       const uint32_t zeros = pack2<false>(fmaf(-8.f, own.x, own.y) * inv * 0x1p-7f, 0.f);
@@ -391,13 +427,12 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
           const uint32_t sc = __shfl_sync(kFull, scales, row);
           const uint32_t zr = __shfl_sync(kFull, zeros, row);
           const uint32_t a = __byte_perm(sc, sc, 0x1010), b = __byte_perm(sc, sc, 0x3232);
-          const uint32_t e = __byte_perm(zr, zr, 0x1010);
+          const uint32_t c = __byte_perm(zr, zr, 0x1010);
           s24 = *reinterpret_cast<const __half2 *>(&a);
           s20 = *reinterpret_cast<const __half2 *>(&b);
-          z = *reinterpret_cast<const __half2 *>(&e);
+          z = *reinterpret_cast<const __half2 *>(&c);
         }
-        const uint4 x = codes[which][i];
-        const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t wd[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
         // 16-byte chunks 4 piece .. 4 piece + 3 of the row, swizzled
         const int at = 32 * w + row, c0 = 4 * piece;
         const uint32_t to = dst + (c0 >> 3) * L::kColBlk + swz128(at, c0);
@@ -406,30 +441,23 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
           const uint4 o = operand<EXACT>(wd[u], s24, s20, z);
           st_shared_v4(to ^ (u << 4), o.x, o.y, o.z, o.w);
         }
+        codes[i] = v_codes[i];  // for the second round
       }
       fence_proxy_async_smem();  // generic stores -> read by the tensor cores
       __syncwarp();
       if (lane == 0) mbar_arrive(bar((which ? kBarV : kBarK) + s));
-    };
-    convert(0, k, k_ref);
-    if (!ok) break;
-    if (more) {
-      turn_to(id1);
-      load_meta();
-      load(0);
-      id1 = id2, id2 = id3;
-      id3 = id_of(t + 4);
+      if (!which) issue(2);  // the pages' codes are in registers, and the fence covers it
     }
-    convert(1, v, v_ref);
     if (!ok) break;
-    if (more) load(1);
   }
   if (!ok) {
     if (lane == 0) raise_abort(p.status, abort_flag);
+    for (int i = max(0, issued - kRawPages); i < issued; ++i)  // copies in flight still land
+      mbar_wait(raw_bar + 8 * (i % kRawPages), (i / kRawPages) & 1);
     return;
   }
   // every MMA that reads a stage has committed before the part ends
-  for (int i = max(0, t - kStages); i < t && ok; ++i)
+  for (int i = max(c, t - kStages); i < t && ok; i += step)
     for (int x = tl.first(i % kStages); x <= tl.last(i % kStages) && ok; ++x)
       ok = warp_wait2(bar(kBarKFree + 2 * x + i % kStages), (i / kStages) & 1,
                       bar(kBarVFree + 2 * x + i % kStages), (i / kStages) & 1, abort_flag);
@@ -439,14 +467,14 @@ __device__ __forceinline__ void convert_tiles(int w, const PrefillParams &p,
 // MMA warp x (lane 0): S_x(0), then per key tile t: P_x(t) V_t in two key halves,
 // S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.  (Split key
 // tiles: t = x, x + 2, ..)
-template <int D>
+template <int D, bool FEW>
 __device__ __forceinline__ void mma_tiles(int x, bool split, int nt, uint32_t sb, uint32_t tmem,
                                           int *status, volatile int *abort_flag, int lane) {
   using L = PrefillSmem<D>;
   constexpr uint32_t kIdS = tc::idesc_f16(false, kRows, kKeys, false, false);
   constexpr uint32_t kIdO = tc::idesc_f16(false, kRows, D, false, true);
   auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
-  const uint64_t dq = tc::smem_desc_sw128(sb + L::kQ + x * L::kTile, 16, 1024);
+  const uint64_t dq = tc::smem_desc_sw128(sb + L::kQ + (FEW ? 0 : x) * L::kTile, 16, 1024);
   const uint64_t dk0 = tc::smem_desc_sw128(sb + L::kK, 16, 1024);
   const uint64_t dv0 = tc::smem_desc_sw128(sb + L::kV, L::kColBlk, 1024);
   const uint32_t tS = tmem + x * kKeys, tO = tmem + 2 * kKeys + x * D;
@@ -510,8 +538,12 @@ __device__ __forceinline__ void mma_tiles(int x, bool split, int nt, uint32_t sb
   }
 }
 
+__device__ __forceinline__ void row_tiles_sync() {  // both softmax warpgroups
+  asm volatile("bar.sync 4, 256;" ::: "memory");
+}
+
 // Softmax warpgroup x: lane l of warp w owns row 32 (w mod 4) + l of row tile x.
-template <int D, bool BF16, bool EXACT>
+template <int D, bool BF16, bool EXACT, bool FEW>
 __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const volatile TilePart &part, int x,
                                               const Tiling &tl, uint32_t sb, uint32_t tmem,
                                               uint8_t *smem, volatile int *abort_flag,
@@ -530,11 +562,12 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
   const uint32_t tS = tmem + x * kKeys + lane_base;
   const uint32_t tO = tmem + 2 * kKeys + x * D + lane_base;
 
+  const int xq = FEW ? 0 : x;  // whose Q
   float qsum = 0.f, row_f = 0.f;
   if constexpr (EXACT) {
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {
-      const uint4 v = lds128(sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c));
+      const uint4 v = lds128(sb + L::kQ + xq * L::kTile + (c >> 3) * L::kColBlk + swz128(r, c));
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -543,7 +576,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
       }
     }
   } else {
-    row_f = reinterpret_cast<const float *>(smem + L::kRowF)[x * kRows + r];
+    row_f = reinterpret_cast<const float *>(smem + L::kRowF)[xq * kRows + r];
   }
   const float2 q2 = make_float2(qsum, qsum);
 
@@ -578,7 +611,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     // The scores of kHold keys at a time, the last ones first; the first ones stay, the
     // others are read again.  (Exact: with a whole row of them and the scales on their
     // way the registers do not suffice.)
-    constexpr int kHold = EXACT ? 64 : kKeys;
+    constexpr int kHold = EXACT || FEW ? 64 : kKeys;
     uint32_t s[kHold];
     auto scores = [&](int h, bool raw) {
 #pragma unroll
@@ -684,6 +717,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarP + 2 * x + (ch >> 1)));
+        if (FEW && lane == 0) mbar_arrive(bar(kBarP + 2 * x + (ch >> 1)));  // two warps' worth
       }
     };
 #pragma unroll
@@ -703,7 +737,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
     float4 *other = reinterpret_cast<float4 *>(smem + L::kQ + L::kTile) + r;
     if (x == 1 && !bad) *other = make_float4(m, l, z, o_a);
     tc::fence_before_sync();
-    asm volatile("bar.sync 4, 256;" ::: "memory");
+    row_tiles_sync();
     bad = __any_sync(kFull, *abort_flag);
     if (x == 1) return;
     const float4 b = *other;
@@ -828,7 +862,10 @@ __device__ __forceinline__ void set_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D, bool BF16>
+// FEW: calls with at most 64 rows a kv head.  Both row tiles are the same rows (one Q),
+// and warps 2 and 3 of the softmax warpgroups, whose rows are none, turn the odd key
+// tiles' codes, through rings in Q_B's place.
+template <int D, bool BF16, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillParams p) {
   using L = PrefillSmem<D>;
   constexpr bool EXACT = !BF16;
@@ -888,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
       const Tiling tl(part.row0, part.nt, p.n_rows);
       const uint32_t tmem = begin();
       if (warp < tl.n_active)
-        mma_tiles<D>(warp, tl.split, part.nt, sb, tmem, p.status, abort_flag, lane);
+        mma_tiles<D, FEW>(warp, tl.split, part.nt, sb, tmem, p.status, abort_flag, lane);
       finish();
       const bool end = !part.more || *abort_flag;
       if (tid == 0) {
@@ -914,7 +951,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
       const TilePart part = *part_s;
       const Tiling tl(part.row0, part.nt, p.n_rows);
       begin();
-      convert_tiles<D, BF16, EXACT>(warp - kConvertWarp0, p, part, sb, smem, tl, abort_flag, lane);
+      convert_tiles<D, BF16, EXACT>(0, FEW && tl.split ? 2 : 1, warp - kConvertWarp0, p, part, sb, smem,
+                                    tl, abort_flag, lane);
       finish();
       if (!part.more || *abort_flag) break;
       cta_sync<3>();
@@ -922,17 +960,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
   } else {
     set_registers<kRegsSoftmax, true>();
     const int x = (warp - kSoftmaxWarp0) >> 2;
-    for (;;) {
-      const Tiling tl(part_s->row0, part_s->nt, p.n_rows);
-      const bool more = part_s->more;
-      load_q<D, BF16, EXACT>(p, *part_s, tl.split, x, sb, smem, tid & 127);
-      const uint32_t tmem = begin();
-      if (x < tl.n_active)
-        softmax_tiles<D, BF16, EXACT>(p, *part_s, x, tl, sb, tmem, smem, abort_flag, warp,
-                                      lane);
-      finish();
-      if (!more || *abort_flag) break;
-      cta_sync<3>();
+    auto own_q = [&](const volatile TilePart &part, const Tiling &tl) {
+      if (!FEW || x == 0) load_q<D, BF16, EXACT>(p, part, tl.split, x, sb, smem, tid & 127);
+      // what this thread left in Q_B, before copies into it
+      if (FEW) fence_proxy_async_smem();
+    };
+    if (FEW && (warp & 2)) {
+      for (;;) {
+        const TilePart part = *part_s;
+        const Tiling tl(part.row0, part.nt, p.n_rows);
+        own_q(part, tl);
+        begin();
+        if (tl.split) {
+          convert_tiles<D, BF16, EXACT>(1, 2, 2 * x + (warp & 1), p, part, sb, smem, tl,
+                                        abort_flag, lane);
+          row_tiles_sync();
+        }
+        finish();
+        if (!part.more || *abort_flag) break;
+        cta_sync<3>();
+      }
+    } else {
+      for (;;) {
+        const Tiling tl(part_s->row0, part_s->nt, p.n_rows);
+        const bool more = part_s->more;
+        own_q(*part_s, tl);
+        const uint32_t tmem = begin();
+        if (x < tl.n_active)
+          softmax_tiles<D, BF16, EXACT, FEW>(p, *part_s, x, tl, sb, tmem, smem, abort_flag, warp,
+                                             lane);
+        finish();
+        if (!more || *abort_flag) break;
+        cta_sync<3>();
+      }
     }
   }
   __syncthreads();
@@ -996,9 +1056,9 @@ size_t states_bytes(int head_dim, int ctas) {
   return static_cast<size_t>(ctas) * 2 * kItemRows * (head_dim + 4) * sizeof(float);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool FEW>
 int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
-  auto kern = kv4_prefill_kernel<D, BF16>;
+  auto kern = kv4_prefill_kernel<D, BF16, FEW>;
   static ContextCache<bool> smem_set;
   if (set_smem_limit(kern, PrefillSmem<D>::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
   if (launch_pdl(kern, dim3(ctas), dim3(kThreads), PrefillSmem<D>::kAlloc, stream, p) !=
@@ -1007,6 +1067,12 @@ int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
                  dim3(kFoldRows * D / 4), 0, stream, p) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
+}
+
+template <int D, bool BF16>
+int launch_d(const PrefillParams &p, int ctas, cudaStream_t stream) {
+  return p.n_rows <= kRows / 2 ? launch_t<D, BF16, true>(p, ctas, stream)
+                               : launch_t<D, BF16, false>(p, ctas, stream);
 }
 
 }  // namespace
@@ -1043,8 +1109,8 @@ int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.n_items = (p.n_rows + kItemRows - 1) / kItemRows;
   p.page_bytes = static_cast<uint32_t>(a.n_kv_heads) * kv4::block_bytes(a.head_dim);
   if (a.head_dim == 128)
-    return a.bf16 ? launch_t<128, true>(p, ctas, stream) : launch_t<128, false>(p, ctas, stream);
-  return a.bf16 ? launch_t<64, true>(p, ctas, stream) : launch_t<64, false>(p, ctas, stream);
+    return a.bf16 ? launch_d<128, true>(p, ctas, stream) : launch_d<128, false>(p, ctas, stream);
+  return a.bf16 ? launch_d<64, true>(p, ctas, stream) : launch_d<64, false>(p, ctas, stream);
 }
 
 }  // namespace pa
