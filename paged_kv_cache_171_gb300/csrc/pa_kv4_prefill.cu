@@ -80,6 +80,7 @@ struct PrefillParams {
   uint32_t qsign;   // 0x80008000 when scale < 0 (folded into Q), else 0
   int n_new, n_q_heads, n_kv_heads, group, batch, max_blocks, num_pages;
   int n_rows, n_items;  // rows a kv head, items a kv head
+  int part_tiles;       // what a part's start and end cost, in key tiles
   uint32_t page_bytes;
 };
 
@@ -102,9 +103,9 @@ struct PrefillSmem {
   // per stage: k_ref of each 32 keys, then v_ref
   static constexpr int kRef = kRaw + kRing;
   static constexpr int kBars = kRef + kStages * 32;
-  static constexpr int kSlot = kBars + 46 * 8;        // TMEM address, abort flag
-  static constexpr int kPart = kSlot + 16;
-  static constexpr int kWalk = kPart + 64;
+  static constexpr int kSlot = kBars + 2 * 46 * 8;        // TMEM address, abort flag
+  static constexpr int kPart = kSlot + 16;            // this part and the next
+  static constexpr int kWalk = kPart + 2 * 64;
   static constexpr int kBytes = kWalk + 64;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "exceeds the per-CTA shared memory limit");
@@ -149,10 +150,12 @@ struct Tiling {
 };
 static_assert(kStages == 2, "split key tiles: a stage belongs to one row tile");
 
-// The CTA's run [w, w1) of the flattened list of key tiles.
+// The CTA's run [w, w1) of the flattened list of units.  A boundary between runs in or
+// right behind an item's part_tiles units counts as lying before the item, so that every
+// part has a key tile.
 struct TileWalk {
-  int64_t w, w1, run, base;  // base: key tiles of the sequences before b
-  int b, ctx, per_head;      // the sequence; key tiles of one of its kv heads
+  int64_t w, w1, run, base;  // base: units of the sequences before b
+  int b, ctx, per_head;      // the sequence; units of one of its kv heads
 
   static __device__ int ctx_of(const PrefillParams &p, int b, bool report) {
     const int most = p.max_blocks * kPageSize - p.n_new;
@@ -163,14 +166,15 @@ struct TileWalk {
     }
     return t;
   }
-  // Key tiles that item k (of a kv head) of a sequence with ctx cached tokens sees.
-  static __device__ int tiles_of(const PrefillParams &p, int ctx, int k) {
+  // Units of item k (of a kv head) of a sequence with ctx cached tokens: the key tiles
+  // that it sees behind part_tiles of its own.
+  static __device__ int units_of(const PrefillParams &p, int ctx, int k) {
     const int last_row = min(p.n_rows, (k + 1) * kItemRows) - 1;
-    return (ctx + last_row / p.group) / kKeys + 1;
+    return (ctx + last_row / p.group) / kKeys + 1 + p.part_tiles;
   }
-  static __device__ int head_tiles(const PrefillParams &p, int ctx) {
+  static __device__ int head_units(const PrefillParams &p, int ctx) {
     int n = 0;
-    for (int k = 0; k < p.n_items; ++k) n += tiles_of(p, ctx, k);
+    for (int k = 0; k < p.n_items; ++k) n += units_of(p, ctx, k);
     return n;
   }
   static __device__ int64_t quotient(int64_t a, int64_t b) {
@@ -182,7 +186,7 @@ struct TileWalk {
     const int per = (p.batch + 31) / 32;
     const int b0 = min(p.batch, lane * per), b1 = min(p.batch, b0 + per);
     int64_t sum = 0;
-    for (int i = b0; i < b1; ++i) sum += head_tiles(p, ctx_of(p, i, blockIdx.x == 0));
+    for (int i = b0; i < b1; ++i) sum += head_units(p, ctx_of(p, i, blockIdx.x == 0));
     int64_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -198,7 +202,7 @@ struct TileWalk {
     x.b = __shfl_sync(kFull, b0, src);
     x.base = __shfl_sync(kFull, incl - sum, src) * p.n_kv_heads;
     x.ctx = ctx_of(p, x.b, false);
-    x.per_head = head_tiles(p, x.ctx);
+    x.per_head = head_units(p, x.ctx);
     if (lane == 0) *out = x;
     return true;
   }
@@ -206,27 +210,29 @@ struct TileWalk {
     while (base + static_cast<int64_t>(per_head) * p.n_kv_heads <= w) {
       base += static_cast<int64_t>(per_head) * p.n_kv_heads;
       ctx = ctx_of(p, ++b, false);
-      per_head = head_tiles(p, ctx);
+      per_head = head_units(p, ctx);
     }
     const int64_t rel = w - base;
     const int g = static_cast<int>(quotient(rel, per_head));
-    int t = static_cast<int>(rel - static_cast<int64_t>(g) * per_head), k = 0, n;
-    while (t >= (n = tiles_of(p, ctx, k))) {
-      t -= n;
+    int u0 = static_cast<int>(rel - static_cast<int64_t>(g) * per_head), k = 0, n;
+    while (u0 >= (n = units_of(p, ctx, k))) {
+      u0 -= n;
       ++k;
     }
-    const int64_t i0 = w - t;  // the item's first key tile
+    const int64_t i0 = w - u0;  // the item's first unit
+    if (u0 <= p.part_tiles) u0 = 0;  // a boundary in an item's own units lies before it
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(n), w1 - i0));
     s.b = b;
     s.g = g;
     s.row0 = k * kItemRows;
     s.ctx = ctx;
-    s.t0 = t;
-    s.nt = static_cast<int>(min(static_cast<int64_t>(n - t), w1 - w));
-    s.first = static_cast<int>(quotient(i0, run));
+    s.t0 = max(0, u0 - p.part_tiles);
+    s.nt = u1 - p.part_tiles - s.t0;  // (below 1: the run ends before the item's tiles begin)
+    s.first = static_cast<int>(quotient(i0 + p.part_tiles, run));
     s.last = static_cast<int>(quotient(i0 + n - 1, run));
-    s.slot = i0 == s.first * run ? 0 : 1;
-    w += s.nt;
-    s.more = w < w1;
+    s.slot = i0 <= s.first * run ? 0 : 1;
+    w = i0 + u1;
+    s.more = w + p.part_tiles < w1;
   }
 };
 
@@ -291,15 +297,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // masking removes for the queries that do not see it, and its values zero.
 template <int D, bool BF16, bool EXACT>
 __device__ __forceinline__ void convert_tiles(int c, int step, int w, const PrefillParams &p,
-                                              const TilePart &part, uint32_t sb, uint8_t *smem,
-                                              const Tiling &tl, volatile int *abort_flag,
+                                              const TilePart &part, uint32_t sb, uint32_t bars,
+                                              uint8_t *smem, const Tiling &tl, volatile int *abort_flag,
                                               int lane) {
   using L = PrefillSmem<D>;
   constexpr int kBlock = kv4::block_bytes(D);
   constexpr int kPieces = D / 32;                // 16-byte pieces of a row's codes
   constexpr int kIters = kPageSize * kPieces / 32;  // pieces a lane and page
   constexpr int kPagesTile = kKeys / kPageSize;
-  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  auto bar = [&](int i) { return bars + 8 * i; };
   const int tokens = part.ctx + p.n_new;
   const int n_pages = (tokens + kPageSize - 1) / kPageSize;
   const int32_t *bt_row = p.block_table + static_cast<size_t>(part.b) * p.max_blocks;
@@ -468,12 +474,13 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
 // S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.  (Split key
 // tiles: t = x, x + 2, ..)
 template <int D, bool FEW>
-__device__ __forceinline__ void mma_tiles(int x, bool split, int nt, uint32_t sb, uint32_t tmem,
-                                          int *status, volatile int *abort_flag, int lane) {
+__device__ __forceinline__ void mma_tiles(int x, bool split, int nt, uint32_t sb, uint32_t bars,
+                                          uint32_t tmem, int *status, volatile int *abort_flag,
+                                          int lane) {
   using L = PrefillSmem<D>;
   constexpr uint32_t kIdS = tc::idesc_f16(false, kRows, kKeys, false, false);
   constexpr uint32_t kIdO = tc::idesc_f16(false, kRows, D, false, true);
-  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  auto bar = [&](int i) { return bars + 8 * i; };
   const uint64_t dq = tc::smem_desc_sw128(sb + L::kQ + (FEW ? 0 : x) * L::kTile, 16, 1024);
   const uint64_t dk0 = tc::smem_desc_sw128(sb + L::kK, 16, 1024);
   const uint64_t dv0 = tc::smem_desc_sw128(sb + L::kV, L::kColBlk, 1024);
@@ -545,11 +552,11 @@ __device__ __forceinline__ void row_tiles_sync() {  // both softmax warpgroups
 // Softmax warpgroup x: lane l of warp w owns row 32 (w mod 4) + l of row tile x.
 template <int D, bool BF16, bool EXACT, bool FEW>
 __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const volatile TilePart &part, int x,
-                                              const Tiling &tl, uint32_t sb, uint32_t tmem,
+                                              const Tiling &tl, uint32_t sb, uint32_t bars, uint32_t tmem,
                                               uint8_t *smem, volatile int *abort_flag,
                                               int warp, int lane) {
   using L = PrefillSmem<D>;
-  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
+  auto bar = [&](int i) { return bars + 8 * i; };
   const int r = ((warp & 3) << 5) + lane;
   // last key that the row sees, and that every row of the tile sees
   const int row0 = part.row0 + (tl.split ? 0 : x * kRows);
@@ -792,12 +799,13 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
   if (real && !whole) *reinterpret_cast<float2 *>(state + D) = make_float2(m, l);
 }
 
-// Row tile x of Q in the operand's order of dimensions, zeros past the rows, by 128
-// threads; not exact: as fp16 over a power of two a row, whose product with the score
+// Row tile x of Q in the operand's order of dimensions, zeros past the rows (FEW: in
+// the warps that have some; the others' S is not looked at), by 128 threads; not exact: as fp16 over a power of two a row, whose product with the score
 // factor goes to kRowF.  A thread copies chunks to where they belong and then turns its
-// own in place.  The loops are not unrolled: this runs once a part, and straight-line
-// code would wait for its own instructions (measured 10 us a part, 16 chunks unrolled).
-template <int D, bool BF16, bool EXACT>
+// own in place.  The loops are hardly unrolled: this runs once a part, and
+// straight-line code waits for its own instructions (measured 10 us a part with all 16
+// chunks unrolled, 4 so).
+template <int D, bool BF16, bool EXACT, bool FEW>
 __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile TilePart &part,
                                        bool split, int x, uint32_t sb, uint8_t *smem, int th) {
   using L = PrefillSmem<D>;
@@ -805,8 +813,9 @@ __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile Ti
   constexpr int kStep = 128 / kChunks;
   const int c = th % kChunks, row0 = part.row0 + (split ? 0 : x * kRows), b = part.b, g = part.g;
   const uint32_t dst = sb + L::kQ + x * L::kTile + (c >> 3) * L::kColBlk;
+  const int rows = FEW ? kRows / 4 * ((p.n_rows + kRows / 4 - 1) / (kRows / 4)) : kRows;
 #pragma unroll 1
-  for (int r = th / kChunks; r < kRows; r += kStep) {
+  for (int r = th / kChunks; r < rows; r += kStep) {
     const uint32_t to = dst + swz128(r, c);
     if (row0 + r < p.n_rows)
       cp_async16(to, p.q + row_at(p, b, g, row0 + r) * D + c * 8);
@@ -814,8 +823,8 @@ __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile Ti
       st_shared_v4(to, 0, 0, 0, 0);
   }
   cp_async_wait();
-#pragma unroll 2
-  for (int r = th / kChunks; r < kRows; r += kStep) {
+#pragma unroll 4
+  for (int r = th / kChunks; r < rows; r += kStep) {
     const uint32_t at = dst + swz128(r, c);
     const uint4 v = lds128(at);
     uint32_t w[4] = {v.x ^ p.qsign, v.y ^ p.qsign, v.z ^ p.qsign, v.w ^ p.qsign};
@@ -873,28 +882,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  auto bar = [&](int i) { return sb + L::kBars + 8 * i; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kSlot + 4);
   volatile int *any = reinterpret_cast<volatile int *>(smem + L::kSlot + 8);
-  TilePart *part_s = reinterpret_cast<TilePart *>(smem + L::kPart);
+  TilePart *parts = reinterpret_cast<TilePart *>(smem + L::kPart);
   TileWalk *walk = reinterpret_cast<TileWalk *>(smem + L::kWalk);
-  auto init_bars = [&] {
+  auto bars_of = [&](int turn) { return sb + L::kBars + (turn & 1) * (8 * kNumBars); };
+  auto init_bars = [&](int turn) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i < kBarKFree || (i >= kBarP && i < kBarP + 4) ? 4 : 1);
+      mbar_init(bars_of(turn) + 8 * i, i < kBarKFree || (i >= kBarP && i < kBarP + 4) ? 4 : 1);
     fence_mbar_init();
   };
 
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_release();
   if (warp == 0) {
-    const bool have = TileWalk::start(p, lane, walk);
+    bool have = TileWalk::start(p, lane, walk);
     if (lane == 0) {
-      if (have) walk->next(p, *part_s);
-      else p.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (have) walk->next(p, parts[0]);
+      have = have && parts[0].nt > 0;
+      if (!have) p.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
       *any = have;
       *abort_flag = 0;
-      init_bars();
+      init_bars(0);
     }
   }
   __syncthreads();
@@ -905,8 +915,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     tc::relinquish();
   }
 
-  // All walk the parts in step: barrier 1 when Q and the part are in place, barrier 2
-  // at its end, barrier 3 once thread 0 has planned the next one.
+  // All walk the parts in step: barrier 1 when Q is in place, barrier 2 at the part's
+  // end.  In between warp 2 plans the next one and readies its barriers.
   auto begin = [&] {
     tc::fence_before_sync();
     cta_sync<1>();
@@ -920,78 +930,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
   };
   if (warp < kConvertWarp0) {
     set_registers<kRegsMma, false>();
-    for (;;) {
-      const TilePart part = *part_s;
+    for (int turn = 0;; ++turn) {
+      const TilePart part = parts[turn & 1];
       const Tiling tl(part.row0, part.nt, p.n_rows);
       const uint32_t tmem = begin();
       if (warp < tl.n_active)
-        mma_tiles<D, FEW>(warp, tl.split, part.nt, sb, tmem, p.status, abort_flag, lane);
+        mma_tiles<D, FEW>(warp, tl.split, part.nt, sb, bars_of(turn), tmem, p.status, abort_flag,
+                          lane);
+      if (warp == 2 && lane == 0 && part.more) {
+        if (turn > 0)
+          for (int i = 0; i < kNumBars; ++i)
+            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bars_of(turn + 1) + 8 * i)
+                         : "memory");
+        init_bars(turn + 1);
+        walk->next(p, parts[(turn + 1) & 1]);
+      }
       finish();
-      const bool end = !part.more || *abort_flag;
-      if (tid == 0) {
-        if (end) {
+      if (!part.more || *abort_flag) {
+        if (tid == 0) {
           // the run's last part may start an item that later CTAs hold more of
           const int c = blockIdx.x;
           const bool cut = part.last > c && part.first == c;
           p.cut[2 * c] = make_int4(cut ? part.last - c + 1 : 0, part.slot, part.row0, 0);
           p.cut[2 * c + 1] = make_int4(part.b, part.g, 0, 0);
-        } else {  // every phase of the part has been waited for: start afresh
-          for (int i = 0; i < kNumBars; ++i)
-            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(i)) : "memory");
-          init_bars();
-          walk->next(p, *part_s);
         }
+        break;
       }
-      if (end) break;
-      cta_sync<3>();
     }
   } else if (warp < kSoftmaxWarp0) {
     set_registers<kRegsConvert, false>();
-    for (;;) {
-      const TilePart part = *part_s;
+    for (int turn = 0;; ++turn) {
+      const TilePart part = parts[turn & 1];
       const Tiling tl(part.row0, part.nt, p.n_rows);
       begin();
-      convert_tiles<D, BF16, EXACT>(0, FEW && tl.split ? 2 : 1, warp - kConvertWarp0, p, part, sb, smem,
-                                    tl, abort_flag, lane);
+      convert_tiles<D, BF16, EXACT>(0, FEW && tl.split ? 2 : 1, warp - kConvertWarp0, p, part, sb,
+                                    bars_of(turn), smem, tl, abort_flag, lane);
       finish();
       if (!part.more || *abort_flag) break;
-      cta_sync<3>();
     }
   } else {
     set_registers<kRegsSoftmax, true>();
     const int x = (warp - kSoftmaxWarp0) >> 2;
     auto own_q = [&](const volatile TilePart &part, const Tiling &tl) {
-      if (!FEW || x == 0) load_q<D, BF16, EXACT>(p, part, tl.split, x, sb, smem, tid & 127);
+      if (!FEW || x == 0) load_q<D, BF16, EXACT, FEW>(p, part, tl.split, x, sb, smem, tid & 127);
       // what this thread left in Q_B, before copies into it
       if (FEW) fence_proxy_async_smem();
     };
     if (FEW && (warp & 2)) {
-      for (;;) {
-        const TilePart part = *part_s;
+      for (int turn = 0;; ++turn) {
+        const TilePart part = parts[turn & 1];
         const Tiling tl(part.row0, part.nt, p.n_rows);
         own_q(part, tl);
         begin();
         if (tl.split) {
-          convert_tiles<D, BF16, EXACT>(1, 2, 2 * x + (warp & 1), p, part, sb, smem, tl,
-                                        abort_flag, lane);
+          convert_tiles<D, BF16, EXACT>(1, 2, 2 * x + (warp & 1), p, part, sb, bars_of(turn), smem,
+                                        tl, abort_flag, lane);
           row_tiles_sync();
         }
         finish();
         if (!part.more || *abort_flag) break;
-        cta_sync<3>();
       }
     } else {
-      for (;;) {
-        const Tiling tl(part_s->row0, part_s->nt, p.n_rows);
-        const bool more = part_s->more;
-        own_q(*part_s, tl);
+      for (int turn = 0;; ++turn) {
+        const volatile TilePart &part = parts[turn & 1];
+        const Tiling tl(part.row0, part.nt, p.n_rows);
+        own_q(part, tl);
         const uint32_t tmem = begin();
         if (x < tl.n_active)
-          softmax_tiles<D, BF16, EXACT, FEW>(p, *part_s, x, tl, sb, tmem, smem, abort_flag, warp,
-                                             lane);
+          softmax_tiles<D, BF16, EXACT, FEW>(p, part, x, tl, sb, bars_of(turn), tmem, smem,
+                                             abort_flag, warp, lane);
+        const bool more = part.more;
         finish();
         if (!more || *abort_flag) break;
-        cta_sync<3>();
       }
     }
   }
@@ -1107,6 +1117,7 @@ int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.num_pages = a.num_pages;
   p.n_rows = a.n_new * p.group;
   p.n_items = (p.n_rows + kItemRows - 1) / kItemRows;
+  p.part_tiles = p.n_rows <= kRows / 2 ? 6 : 3;
   p.page_bytes = static_cast<uint32_t>(a.n_kv_heads) * kv4::block_bytes(a.head_dim);
   if (a.head_dim == 128)
     return a.bf16 ? launch_d<128, true>(p, ctas, stream) : launch_d<128, false>(p, ctas, stream);
