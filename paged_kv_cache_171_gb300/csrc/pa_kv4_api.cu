@@ -34,14 +34,17 @@ int append(AppendRopeLaunch &a, int page_size, int dtype, pa_stream_t stream) {
 }
 
 // Whether a chunk goes to the tile kernel: by its rows (queries x group) a kv head.
-// The row kernel reads the cache once for 8 of them, the tile kernel once for 256 at
-// the price of turning it into operand tiles.  Measured over 4 x 32768 tokens of 8 kv
-// heads at head_dim 128, rows against tiles: bf16 16 rows 84 / 120 us, 32 rows 144 /
-// 121 us; fp16, whose tile form is the slower one, 32 rows 144 / 157 us, 64 rows 269 /
-// 162 us.
+// The row kernel turns the codes once for 8 of them, the tile kernel once for 256, at
+// the price of whole operand tiles; fp16's tile form is the slower one.  Rows against
+// tiles in us, head_dim 128, rows a kv head across:
+//                                     16         24         32         64
+//   bf16  4 x 32768, 8 kv heads    97 /  95  132 /  96  168 /  95  304 /  97
+//         16 x 2000, 8 kv heads    34 /  44   43 /  45   52 /  45   90 /  45
+//   fp16  4 x 32768, 8 kv heads    97 / 132  133 / 132  168 / 134  303 / 135
+//         16 x 2000, 8 kv heads    34 /  54   43 /  54   52 /  53   90 /  54
 bool wants_tiles(int n_new, int n_q_heads, int n_kv_heads, bool bf16) {
   return n_new > 0 &&
-         static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > (bf16 ? 24 : 40);
+         static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > (bf16 ? 16 : 24);
 }
 
 // The larger of the two kernels' workspaces where the type decides between them.
