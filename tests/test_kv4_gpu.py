@@ -171,6 +171,24 @@ def test_prefill_matches_definition(hq, hkv, n_new, ctx, d, dtype):
     check_prefill(hq, hkv, n_new, ctx, d, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new,ctx", [
+    (6, [5000, 0, 130, 9000, 64, 2, 127, 128] + [40] * 60), (8, [100] * 90), (16, [20000, 3]),
+    (20, [5000, 0, 130, 9000, 64]), (70, [3000, 0, 130, 1, 6000]), (6, [7] * 3 + [4000])])
+def test_prefill_items_cut_between_runs(n_new, ctx, dtype):
+    """Many short items a run, long ones over many runs, both in one call: chunks of 24
+    to 280 rows a kv head."""
+    check_prefill(16, 4, n_new, ctx, 128, dtype, seed=3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_items_cut_between_runs(d):
+    """More items than teams of warps, short and long ones mixed."""
+    gen = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 400, (150,), generator=gen).tolist() + [9000, 1, 3000]
+    check_decode(lens, 32, 8, d, "bf16", seed=6)
+
+
 @pytest.mark.parametrize("dtype,q_mul,spread,scale", [
     ("bf16", 1.0, 1e15, 1e-16), ("bf16", 1.0, 1e-20, None), ("fp16", 100.0, 0.01, None),
     ("fp16", 0.001, 100.0, None), ("bf16", 1.0, 1.0, 0.0), ("bf16", 1.0, 1.0, -0.1),
@@ -471,3 +489,8 @@ def test_repeated_calls_are_bit_identical():
     first = pa.decode_kv4(q, pool, bt, ctx, 0.1)
     for _ in range(20):
         assert torch.equal(pa.decode_kv4(q, pool, bt, ctx, 0.1), first)
+    for n_new in (3, 10, 30, 80):  # of 4 rows a query
+        qc = torch.randn((3, n_new, 16, 128), generator=gen).bfloat16().cuda()
+        first = pa.prefill_kv4(qc, pool, bt, ctx - n_new, 0.1)
+        for _ in range(10):
+            assert torch.equal(pa.prefill_kv4(qc, pool, bt, ctx - n_new, 0.1), first)
