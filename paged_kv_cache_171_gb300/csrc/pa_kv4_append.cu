@@ -21,7 +21,10 @@
 // the thread's 8 cosines and 8 sines serve each of the NR rows of one token
 // that it handles.  NR = 1 while the call is small (more threads: the latency
 // of one dependent chain), 4 once there are enough rows to fill the GPU.
+#include <cuda_bf16.h>
 #include <float.h>
+
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_kv4.cuh"
@@ -275,6 +278,26 @@ struct ReadParams {
 };
 constexpr int kReadThreads = 256, kReadTokens = 64;  // tokens a CTA at most
 
+// zero + scale (code - 8) of a word's eight codes, rounded once: nibbles k and k + 4 as
+// the two halves of a 16-bit pair (its bits under those of 2^10 or 2^7 are 1024 + code or
+// 128 + code), whose difference from 1032 or 136 is exact, and one FMA.
+template <bool BF16>
+__device__ __forceinline__ uint4 values_of(uint32_t code, uint32_t meta) {
+  using H = std::conditional_t<BF16, __nv_bfloat162, __half2>;
+  const uint32_t ss = __byte_perm(meta, meta, 0x1010), zz = __byte_perm(meta, meta, 0x3232);
+  const uint32_t eight = BF16 ? 0x43084308u : 0x64086408u;  // 128 + 8, 1024 + 8
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = ((code >> (4 * k)) & 0x000f000fu) | (BF16 ? 0x43004300u : 0x64006400u);
+    const H c = __hsub2(*reinterpret_cast<const H *>(&w), *reinterpret_cast<const H *>(&eight));
+    const H x = __hfma2(*reinterpret_cast<const H *>(&ss), c, *reinterpret_cast<const H *>(&zz));
+    o[k] = *reinterpret_cast<const uint32_t *>(&x);
+  }
+  return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                    __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kReadThreads) read_kv4_kernel(const ReadParams p) {
   constexpr int TPR = D / 8, kUnroll = 4;
@@ -300,43 +323,36 @@ __global__ void __launch_bounds__(kReadThreads) read_kv4_kernel(const ReadParams
     slots[threadIdx.x] = pos & (kPageSize - 1);
   }
   __syncthreads();
-  // unit (token, K or V, kv head, 8 dimensions), the last fastest
-  const uint32_t heads = p.n_kv_heads, total = n * 2u * heads * TPR;
-  for (uint32_t u0 = threadIdx.x; u0 < total; u0 += kUnroll * kReadThreads) {
+  // unit (token, K or V, kv head, 8 dimensions), the last fastest: a thread's next one is
+  // kReadThreads / TPR rows on
+  const uint32_t heads = p.n_kv_heads, per_token = 2 * heads, t = threadIdx.x % TPR;
+  constexpr uint32_t kStep = kReadThreads / TPR;
+  const uint32_t step_j = kStep / per_token, step_r = kStep % per_token;
+  uint32_t j = threadIdx.x / TPR / per_token, r = threadIdx.x / TPR % per_token;
+  while (j < n) {
     uint32_t code[kUnroll], meta[kUnroll];
     uint4 *dst[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const uint32_t u = u0 + i * kReadThreads;
       dst[i] = nullptr;
-      if (u >= total) continue;
-      const uint32_t t = u % TPR, row = u / TPR, kv = row / heads, g = row - kv * heads;
-      const uint32_t which = kv & 1, j = kv >> 1;
-      const uint8_t *blk = place[j];
-      if (!blk) continue;
-      blk += static_cast<size_t>(g) * kv4::block_bytes(D);
-      const int slot = slots[j];
-      code[i] = __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::code_offset(D, which, slot)) + t);
-      meta[i] = __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, which, slot)));
-      dst[i] = reinterpret_cast<uint4 *>(which ? p.v_out : p.k_out) +
-               (static_cast<size_t>(j0 + j) * heads + g) * TPR + t;
-    }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (!dst[i]) continue;
-      const float2 sz = unpack2<BF16>(meta[i]);
-      uint32_t o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t w = code[i] >> (8 * k);
-        // the product of a 16-bit scale and a code is exact: one rounding to fp32
-        const float lo = __fmaf_rn(sz.x, static_cast<float>(static_cast<int>(w & 15) - 8), sz.y);
-        const float hi =
-            __fmaf_rn(sz.x, static_cast<float>(static_cast<int>((w >> 4) & 15) - 8), sz.y);
-        o[k] = pack2<BF16>(lo, hi);
+      const uint8_t *blk = j < n ? place[j] : nullptr;
+      if (blk) {
+        const uint32_t which = r >= heads, g = r - (which ? heads : 0);
+        const int slot = slots[j];
+        blk += g * static_cast<uint32_t>(kv4::block_bytes(D));
+        code[i] =
+            __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::code_offset(D, which, slot)) + t);
+        meta[i] = __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, which, slot)));
+        dst[i] = reinterpret_cast<uint4 *>(which ? p.v_out : p.k_out) +
+                 (static_cast<size_t>(j0 + j) * heads + g) * TPR + t;
       }
-      *dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      j += step_j;
+      r += step_r;
+      if (r >= per_token) r -= per_token, ++j;
     }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+      if (dst[i]) *dst[i] = values_of<BF16>(code[i], meta[i]);
   }
 }
 
@@ -355,12 +371,8 @@ int launch_read_t(const ReadKv4Launch &a, cudaStream_t stream) {
   p.batch = a.batch;
   p.max_blocks = a.max_blocks;
   p.num_pages = a.num_pages;
-  // Four rows a thread once that fills the GPU twice; one token a CTA before.
-  const int per_token = 2 * a.n_kv_heads * (D / 8);
-  int tokens = 4 * kReadThreads / per_token;
-  if (tokens < 1) tokens = 1;
-  if (tokens > kReadTokens) tokens = kReadTokens;
-  if (static_cast<int64_t>(a.n_tok) < static_cast<int64_t>(tokens) * 152 * 8) tokens = 1;
+  // As few tokens a CTA as leave about one wave of CTAs, eight an SM.
+  const int tokens = min(kReadTokens, (a.n_tok - 1) / (152 * 8) + 1);
   p.per_cta = tokens;
   const int blocks = (a.n_tok - 1) / tokens + 1;
   return launch_pdl(read_kv4_kernel<D, BF16>, dim3(blocks), dim3(kReadThreads), 0, stream, p) ==
