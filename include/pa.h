@@ -576,8 +576,8 @@ int pa_copy_pages_kv4(void *kv_cache, const int32_t *src, const int32_t *dst, in
 /*
  * pa_decode_kv4 -- pa_decode over a 4-bit cache: out = softmax(q K^T scale) V of
  * the values the cache stands for, fp32 accumulation, fp32 out.  T = 0 writes
- * zeros.  The pages of all sequences are cut into equal runs, one a CTA, whatever
- * the sequences' lengths, so there is no partition size to choose.
+ * zeros.  The pages of all sequences are cut into equal runs, whatever the
+ * sequences' lengths, so there is no partition size to choose.
  *   workspace  device, >= pa_decode_kv4_workspace_size(head_dim) bytes on the
  *              current device, 16-byte aligned; contents on entry do not matter.
  *              Two calls that overlap on the GPU must not share one.

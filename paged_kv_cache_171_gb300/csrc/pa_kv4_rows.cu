@@ -45,6 +45,13 @@
 // teams leaves one state a team, folded in order of position by a second kernel
 // (results do not depend on timing).  Runs go round the SMs, so that a call with few
 // of them has one an SM (1 x 512 tokens of 16 heads: 21.0 -> 14.8 us of device time).
+//
+// Bound: issue.  Turning a page's codes is some 150 of about 300 warp instructions;
+// 61% of the issue slots and 58% of the ALU's are taken, DRAM 41%.  Decode at head_dim
+// 128, a call: 8 x 4096 tokens of 32 / 32 heads 44.5 us (143 MB, 3.2 TB/s), 64
+// sequences of 128 to 8192 of 32 / 8 heads 83 us (287 MB, 3.4 TB/s), 4 x 32768 of 64 /
+// 8 heads 51 us (143 MB, 2.8 TB/s); the 16-bit cache's bytes alone would take 79, 159
+// and 79 us at the copy's bandwidth.
 #include "pa_device.cuh"
 #include "pa_kv4.cuh"
 
