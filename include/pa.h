@@ -509,7 +509,8 @@ int pa_decode_static_workspace(const void *q, const void *k_cache,
  * is pa_append_kv's, its rule on two tokens with one place included.  A token
  * whose seq_idx, pos (pos >= max_pos too) or page is bad is skipped, its row of
  * q_out left as it was, and PA_ERR_BAD_INDEX / PA_ERR_BAD_BLOCK recorded.
- * n_q_heads is not used when q is NULL.  Asynchronous on `stream`.
+ * n_q_heads is not used when q is NULL; at most 65535 heads (PA_ERR_HEADS).
+ * Asynchronous on `stream`.
  */
 int pa_append_kv_rope(const void *k_new, const void *v_new, const void *q, void *k_cache,
                       void *v_cache, void *q_out, const int32_t *block_table,
@@ -529,6 +530,9 @@ int pa_append_kv_rope(const void *k_new, const void *v_new, const void *q, void 
  *   which stands for x = zero + scale * (code - 8).
  * Block tables, page ids and the page pool are those of the 16-bit caches.  The
  * pool must be 16-byte aligned.  Rows past a sequence's end may hold anything.
+ * At most 65535 heads (PA_ERR_HEADS), and a chunk's n_new * n_q_heads / n_kv_heads
+ * rows below 2^30, their 256 x 128 tiles over the table's tokens below 2^31
+ * (PA_ERR_SHAPE).
  * pa_kv4_block_bytes is 16 * head_dim + 128, or 0 for an unsupported head_dim.
  */
 size_t pa_kv4_block_bytes(int head_dim);

@@ -6,9 +6,27 @@ using namespace pa;
 
 namespace {
 
+// check_common, and heads whose blocks and rows keep within 32 bits.
+int check_heads(int n_q_heads, int n_kv_heads, int head_dim, int page_size, int batch,
+                int max_blocks, int num_pages, int dtype) {
+  const int rc = check_common(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks,
+                              num_pages, dtype);
+  return rc ? rc : n_q_heads > 65535 ? PA_ERR_HEADS : PA_OK;
+}
+
+// A chunk's rows a kv head, and the (256 rows, 128 keys) tiles of one, in 32 bits.
+int check_chunk(int n_new, int n_q_heads, int n_kv_heads, int max_blocks, int page_size) {
+  const int64_t tokens = static_cast<int64_t>(max_blocks) * page_size;
+  if (n_new > tokens) return PA_ERR_SHAPE;
+  const int64_t rows = static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads);
+  return rows >= (int64_t(1) << 30) || (rows / 256 + 1) * (tokens / 128 + 16) >= (int64_t(1) << 31)
+             ? PA_ERR_SHAPE
+             : PA_OK;
+}
+
 int check_append(const AppendRopeLaunch &a, int page_size, int dtype) {
-  const int rc = check_common(a.q ? a.n_q_heads : a.n_kv_heads, a.n_kv_heads, a.head_dim,
-                              page_size, a.batch, a.max_blocks, a.num_pages, dtype);
+  const int rc = check_heads(a.q ? a.n_q_heads : a.n_kv_heads, a.n_kv_heads, a.head_dim,
+                             page_size, a.batch, a.max_blocks, a.num_pages, dtype);
   if (rc) return rc;
   if (a.n_tok < 0) return PA_ERR_SHAPE;
   if (a.cos_sin && (a.rot_dim < 16 || a.rot_dim > a.head_dim || a.rot_dim % 16 || a.max_pos <= 0))
@@ -59,8 +77,9 @@ int sms_or_default() { return sm_count() > 0 ? sm_count() : 152; }
 int attention(Kv4AttentionLaunch &a, int page_size, int dtype, size_t workspace_bytes,
               pa_stream_t stream) {
   if (!a.q || !a.cache || !a.block_table || !a.ctx_lens || !a.out) return PA_ERR_NULL;
-  int rc = check_common(a.n_q_heads, a.n_kv_heads, a.head_dim, page_size, a.batch, a.max_blocks,
-                        a.num_pages, dtype);
+  int rc = check_heads(a.n_q_heads, a.n_kv_heads, a.head_dim, page_size, a.batch, a.max_blocks,
+                       a.num_pages, dtype);
+  if (!rc) rc = check_chunk(a.n_new, a.n_q_heads, a.n_kv_heads, a.max_blocks, page_size);
   if (rc) return rc;
   if (!aligned16(a.q) || !aligned16(a.cache) || !aligned16(a.out)) return PA_ERR_ALIGN;
   const bool tiles = wants_tiles(a.n_new, a.n_q_heads, a.n_kv_heads, dtype == PA_BF16);
@@ -121,8 +140,8 @@ int pa_read_kv4(const void *kv_cache, const int32_t *block_table, const int32_t 
                 int head_dim, int page_size, int batch, int max_blocks_per_seq, int num_pages,
                 pa_dtype dtype, pa_stream_t stream) {
   if (!kv_cache || !block_table || !seq_idx || !pos || !k_out || !v_out) return PA_ERR_NULL;
-  int rc = check_common(n_kv_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
-                        num_pages, dtype);
+  int rc = check_heads(n_kv_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+                       num_pages, dtype);
   if (rc) return rc;
   if (n_tok < 0) return PA_ERR_SHAPE;
   if (!aligned16(kv_cache) || !aligned16(k_out) || !aligned16(v_out)) return PA_ERR_ALIGN;
@@ -138,7 +157,7 @@ int pa_copy_pages_kv4(void *kv_cache, const int32_t *src, const int32_t *dst, in
                       int n_kv_heads, int head_dim, int page_size, int num_pages,
                       pa_stream_t stream) {
   if (!kv_cache || !src || !dst) return PA_ERR_NULL;
-  int rc = check_common(n_kv_heads, n_kv_heads, head_dim, page_size, 1, 1, num_pages, PA_BF16);
+  int rc = check_heads(n_kv_heads, n_kv_heads, head_dim, page_size, 1, 1, num_pages, PA_BF16);
   if (rc) return rc;
   if (n < 0) return PA_ERR_SHAPE;
   if (!aligned16(kv_cache)) return PA_ERR_ALIGN;
@@ -167,9 +186,9 @@ int pa_decode_kv4(const void *q, const void *kv_cache, const int32_t *block_tabl
 
 size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_kv_heads,
                                      int head_dim, int page_size, int max_blocks_per_seq) {
-  if (check_common(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, 1,
-                   PA_BF16) ||
-      n_new <= 0 || n_new > static_cast<int64_t>(max_blocks_per_seq) * page_size)
+  if (check_heads(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, 1,
+                  PA_BF16) ||
+      n_new <= 0 || check_chunk(n_new, n_q_heads, n_kv_heads, max_blocks_per_seq, page_size))
     return 0;
   return chunk_workspace(n_new, n_q_heads, n_kv_heads, head_dim, sms_or_default());
 }
@@ -181,15 +200,12 @@ int pa_prefill_kv4(const void *q, const void *kv_cache, const int32_t *block_tab
                    size_t workspace_bytes, pa_stream_t stream) {
   if (!q || !kv_cache || !block_table || !ctx_lens || !out) return PA_ERR_NULL;
   if (n_new < 0) return PA_ERR_SHAPE;
-  if (max_blocks_per_seq > 0 && page_size == kPageSize &&
-      n_new > static_cast<int64_t>(max_blocks_per_seq) * page_size)
-    return PA_ERR_SHAPE;
   Kv4AttentionLaunch a = {q, static_cast<const uint8_t *>(kv_cache), block_table, ctx_lens, out,
                           workspace, nullptr, scale, n_new, n_q_heads, n_kv_heads, head_dim,
                           batch, max_blocks_per_seq, num_pages, false};
   if (n_new == 0)  // nothing to compute; the other arguments are still checked
-    return check_common(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
-                        num_pages, dtype);
+    return check_heads(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+                       num_pages, dtype);
   return attention(a, page_size, dtype, workspace_bytes, stream);
 }
 

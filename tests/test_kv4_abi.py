@@ -108,6 +108,20 @@ def test_attention_refuses(L):
     assert L.pa_prefill_kv4(*ok) == -3
 
 
+def test_sizes_past_32_bits_are_refused(L):
+    P, f, big = FAKE, ctypes.c_float(0.1), 1 << 40
+    chunk = lambda n, hq, hkv, blocks: L.pa_prefill_kv4(
+        P, P, P, P, n, P, f, hq, hkv, 128, 16, 2, blocks, 16, 0, P, big, None)
+    assert chunk(1, 65536, 65536, 8) == -2 and chunk(1, 131072, 8, 8) == -2
+    assert chunk(1 << 20, 32768, 1, 1 << 20) == -5    # 2^35 rows
+    assert chunk(1 << 24, 32, 8, 1 << 22) == -5       # 2^18 x 2^19 tiles
+    assert L.pa_prefill_kv4_workspace_size(2, 1 << 24, 32, 8, 128, 16, 1 << 22) == 0
+    assert L.pa_prefill_kv4_workspace_size(2, 1 << 17, 64, 8, 128, 16, 1 << 13) > 0
+    assert L.pa_decode_kv4(P, P, P, P, P, f, 65536, 8, 128, 16, 2, 8, 16, 0, P, big, None) == -2
+    assert L.pa_read_kv4(P, P, P, P, P, P, 4, 65536, 128, 16, 2, 8, 16, 0, None) == -2
+    assert L.pa_copy_pages_kv4(P, P, P, 4, 65536, 128, 16, 16, None) == -2
+
+
 def test_sizes(L):
     assert [L.pa_kv4_block_bytes(d) for d in (64, 128, 96, 0)] == [1152, 2176, 0, 0]
     assert ref.block_bytes(64) == 1152 and ref.block_bytes(128) == 2176
