@@ -57,6 +57,8 @@
 // queries of 64 / 8 heads over 32k tokens 89 us, 1.6 TB/s of codes).
 #include <float.h>
 
+#include <atomic>
+
 #include "pa_kv4.cuh"
 #include "pa_tcgen05.cuh"
 
@@ -866,8 +868,8 @@ __device__ __forceinline__ void cta_sync() {
 }
 
 // Registers a thread after the split: the softmax holds a whole row of scores.
-constexpr int kRegsMma = 64, kRegsConvert = 96, kRegsSoftmax = 176;
-static_assert(128 * (kRegsMma + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * 128,
+constexpr int kRegsLaunch = 128, kRegsMma = 64, kRegsConvert = 96, kRegsSoftmax = 176;
+static_assert(128 * (kRegsMma + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
               "register split");
 template <int N, bool UP>
 __device__ __forceinline__ void set_registers() {
@@ -1074,6 +1076,14 @@ int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
   auto kern = kv4_prefill_kernel<D, BF16, FEW>;
   static ContextCache<bool> smem_set;
   if (set_smem_limit(kern, PrefillSmem<D>::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
+  // the split draws on what the block was launched with; less of it would never come free
+  static std::atomic<bool> enough{false};
+  if (!enough) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs < kRegsLaunch)
+      return PA_ERR_CUDA;
+    enough = true;
+  }
   if (launch_pdl(kern, dim3(ctas), dim3(kThreads), PrefillSmem<D>::kAlloc, stream, p) !=
           cudaSuccess ||
       launch_pdl(kv4_prefill_fold_kernel<D, BF16>, dim3(ctas, (min(p.n_rows, kItemRows) + kFoldRows - 1) / kFoldRows),

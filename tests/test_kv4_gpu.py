@@ -181,6 +181,13 @@ def test_prefill_items_cut_between_runs(n_new, ctx, dtype):
     check_prefill(16, 4, n_new, ctx, 128, dtype, seed=3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new", [8, 9, 16, 17, 24, 25, 32, 33, 64, 65, 128, 129, 256, 257])
+def test_prefill_rows_at_every_border(n_new, dtype):
+    """One row a query: the kernels' row counts, one on either side."""
+    check_prefill(2, 2, n_new, [300, 0, 1000], 128, dtype, seed=1)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_items_cut_between_runs(d):
     """More items than teams of warps, short and long ones mixed."""
