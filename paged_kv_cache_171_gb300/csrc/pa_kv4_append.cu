@@ -22,10 +22,13 @@
 // the thread's 8 cosines and 8 sines serve each of the NR rows of one token
 // that it handles.  NR = 1 while the call is small (more threads: the latency
 // of one dependent chain), 4 once there are enough rows to fill the GPU.
-// Measured: rotation alone, 4 x 512 tokens of 32 / 8 heads of 128: 12.4 us a call
-// (51.4 MB, 4.1 TB/s); 8191 tokens of 16 / 16 heads of 64: 21.2 us (101.7 MB, 4.8
-// TB/s).  Quantising 4 x 2048 tokens (32 / 8 heads of 128): 45 us for 169 MB, where
-// the codes' arithmetic (50% of the issue slots) and the loads take turns.
+// Small CTAs at 80 registers keep 24 warps an SM and the last wave short: 4 x 512 tokens
+// 12.4 -> 11.0 us against CTAs of 256 at the compiler's 95, 4 x 2048 quantised and read
+// back 55.6 -> 48.3; at 64 registers the rows spill (17.4, 51.5).
+// Measured: rotation alone, 4 x 512 tokens of 32 / 8 heads of 128: 11.0 us a call
+// (51.4 MB, 4.7 TB/s); 8191 tokens of 16 / 16 heads of 64: 19.9 us (101.7 MB, 5.1
+// TB/s).  Quantising 4 x 2048 tokens (32 / 8 heads of 128): 37 us for 169 MB, where
+// the codes' arithmetic and the loads take turns.
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -36,6 +39,8 @@
 
 namespace pa {
 namespace {
+
+constexpr int kAppendThreads = 128;
 
 struct AppendParams {
   const uint16_t *k_new, *v_new, *q;
@@ -72,7 +77,7 @@ __device__ __forceinline__ uint32_t round16(float x, float &back) {
 // Row r of a token: K of kv head r, then V of kv head r - Hkv, then q.
 // Thread t of the row holds chunks c0 and c1 (8 elements each).
 template <int D, bool BF16, bool KV4, int NR>
-__global__ void __launch_bounds__(256) append_rope_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 6) append_rope_kernel(const AppendParams p) {
   constexpr int TPR = D / 16;  // threads per row
   griddep_release();
   griddep_wait();  // the rows may come from the previous kernel in the stream
@@ -257,7 +262,7 @@ int launch_append_t(const AppendRopeLaunch &a, cudaStream_t stream) {
   p.rot_dim = a.rot_dim;
   p.interleaved = a.interleaved;
   p.rows = 2 * a.n_kv_heads + (a.q ? a.n_q_heads : 0);
-  constexpr int TPR = D / 16, kThreads = 256;
+  constexpr int TPR = D / 16, kThreads = kAppendThreads;
   // One row a thread until the threads would fill about two waves of the GPU.
   const bool many = static_cast<int64_t>(a.n_tok) * p.rows * TPR > 2 * 152 * 2048;
   const int nr = many ? 4 : 1;
