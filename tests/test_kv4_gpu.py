@@ -501,3 +501,36 @@ def test_repeated_calls_are_bit_identical():
         first = pa.prefill_kv4(qc, pool, bt, ctx - n_new, 0.1)
         for _ in range(10):
             assert torch.equal(pa.prefill_kv4(qc, pool, bt, ctx - n_new, 0.1), first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_chunk_graphs_share_a_workspace(dtype):
+    """Chunks of 6, 40 and 160 rows a kv head captured in graphs that share one
+    workspace, replayed in turn on new queries: like the eager calls."""
+    dt, gen = DT[dtype], torch.Generator().manual_seed(12)
+    lens = [1500, 90, 200]
+    pool, bt = make_pool(lens, 2, 128, dt, gen)
+    pool, bt = pool.cuda(), bt.cuda()
+    sizes = [3, 20, 80]
+    ws = torch.empty(max(pa.pa_prefill_kv4_workspace_size(3, n, 4, 2, 128, 16, bt.shape[1])
+                         for n in sizes), dtype=torch.uint8, device="cuda")
+    qs = [torch.randn((3, n, 4, 128), generator=gen).to(dt).cuda() for n in sizes]
+    ctx = [i32(*[t - n for t in lens]) for n in sizes]
+    outs = [torch.empty_like(q) for q in qs]
+    graphs = [torch.cuda.CUDAGraph() for _ in sizes]
+    for q, c in zip(qs, ctx):
+        pa.prefill_kv4(q, pool, bt, c, 0.1)
+    torch.cuda.synchronize()
+    for g, q, c, o in zip(graphs, qs, ctx, outs):
+        with torch.cuda.graph(g):
+            pa.prefill_kv4(q, pool, bt, c, 0.1, out=o, workspace=ws)
+    for k in range(3):
+        for q in qs:
+            q.mul_(1.5)
+        for g in graphs[k:] + graphs[:k]:
+            g.replay()
+        torch.cuda.synchronize()
+        for q, c, o in zip(qs, ctx, outs):
+            assert torch.isfinite(o).all()
+            assert torch.equal(o, pa.prefill_kv4(q, pool, bt, c, 0.1))
+    assert pa.pa_last_device_error() == 0
