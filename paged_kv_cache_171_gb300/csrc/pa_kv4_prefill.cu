@@ -35,10 +35,10 @@
 // (4 x 4 queries, 64 / 8 heads, over 32k keys: 114 -> 102 us).
 //
 // Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B, warps
-// 4-7 turn codes into the K and V operand tiles (two stages each), a warp 32 keys of
-// each tile, from registers that it fills one tile ahead.  Warps 8-11
-// and 12-15 are the softmax of A and B, a thread a row.  Every hand-off is an mbarrier
-// and every wait is bounded.
+// 4-7 turn codes into the K and V operand tiles (two stages each): a warp 32 keys of
+// each tile, from a ring of pages that it fills for itself by bulk copies.  Warps 8-11
+// and 12-15 are the softmax of A and B, a thread a row.  Warp 2 plans the run's next
+// part during this one.  Every hand-off is an mbarrier and every wait is bounded.
 //
 // Nibbles.  x & 0x000f000f holds nibbles 0 and 4 of a word in two 16-bit halves, and so
 // on: a fp16 pair is made of nibbles four apart.  The operand tiles keep that order of
@@ -47,8 +47,9 @@
 //
 // Work split.  The key tiles of all items, laid end to end, are cut into equal runs,
 // one an SM: 256 items on 152 SMs take 1.7 items' time, not two, and a single
-// sequence's chunk over a long context fills the GPU.  An item cut between CTAs
-// leaves an fp32 state (O, m, l) a row and CTA, folded by a second kernel.
+// sequence's chunk over a long context fills the GPU.  An item counts a few key tiles
+// more than it has (part_tiles), for what starting and ending it costs.  An item cut
+// between CTAs leaves an fp32 state (O, m, l) a row and CTA, folded by a second kernel.
 //
 // Bound.  A long chunk: the chain of a key tile, from the codes over S and the softmax
 // to P V (tensor pipe 43% busy, issue 47%): 4 x 512 queries of 32 / 8 heads over 8192
@@ -1130,6 +1131,9 @@ int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.num_pages = a.num_pages;
   p.n_rows = a.n_new * p.group;
   p.n_items = (p.n_rows + kItemRows - 1) / kItemRows;
+  // Us for 0, 1, 2, 4 tiles more: 4 x 32 queries of 64 / 8 heads over 32k tokens 162, 161,
+  // 157, 153, 4 x 512 of 32 / 8 heads over 8192 within 1%; up to 64 rows, whose tiles are
+  // the shorter ones, for 3, 6, 10, 14: 96, 93, 97, 98.
   p.part_tiles = p.n_rows <= kRows / 2 ? 6 : 4;
   p.page_bytes = static_cast<uint32_t>(a.n_kv_heads) * kv4::block_bytes(a.head_dim);
   if (a.head_dim == 128)
