@@ -13,11 +13,15 @@
 //    steps of 2^-11 and P by one, well below the bf16 result's own rounding of 2^-8, and
 //    the softmax works on S as it comes: a factor for each 32 keys in its exponent.
 //  * fp16: that would be as much as the result's rounding, so the codes enter the
-//    products exactly, as c - 8 ((x & 0x000f000f) | 0x64006400 is 1024 + c), and the
-//    softmax threads apply the rest,
-//      s_t = scale_k[t] S_t + zero_k[t] sum q,   P = p_t scale_v[t] / v_ref,
-//      z += p_t zero_v[t],                       out = (O v_ref + z) / l,
-//    reading each key's scales and zeros from shared memory.
+//    products exactly, as 2 c - 15 ((x & 0x001e001e) | 0x64006400 is 1024 + 2 c, x the
+//    word shifted left by one), and the softmax threads apply the rest: with the row's
+//    middle mid = zero - scale / 2,
+//      s_t = scale_k[t] / 2 S_t + mid_k[t] sum q,   P = p_t scale_v[t] / v_ref,
+//      z += p_t mid_v[t],                           out = (O v_ref / 2 + z) / l,
+//    reading each key's scales and middles from shared memory.  The operand is centred
+//    because the tensor cores round O toward zero at every 16 keys: with c - 8, whose
+//    mean over a row is near -1/2, O grew with the number of keys where the result's
+//    terms cancel, and rows over 131072 keys were off by 0.28%; so by 0.03%.
 // P carries v_ref over the largest v_ref so far; when that grows, O is rescaled like
 // at a move of the running maximum.
 //
@@ -100,8 +104,8 @@ struct PrefillSmem {
   static constexpr int kQ = 0;                        // Q_A, Q_B
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
-  // EXACT: per stage and pair of keys scale_k x2, zero_k x2 (both times qscale),
-  // scale_v / v_ref x2, zero_v x2.  Else kRowF: the factor of each row's S.
+  // EXACT: per stage and pair of keys scale_k / 2 x2, mid_k x2 (both times qscale),
+  // scale_v / v_ref x2, mid_v x2.  Else kRowF: the factor of each row's S.
   static constexpr int kMeta = kV + kStages * kTile;
   static constexpr int kRowF = kMeta;
   // the converters' rings of pages: the first group's, and, where the two row tiles are
@@ -251,7 +255,7 @@ __device__ __forceinline__ size_t row_at(const PrefillParams &p, int b, int g, i
          r % p.group;
 }
 
-// The eight codes of a word, in the order 0 4 1 5 2 6 3 7.  EXACT: as c - 8.  Else as
+// The eight codes of a word, in the order 0 4 1 5 2 6 3 7.  EXACT: as 2 c - 15.  Else as
 // zero + scale (c - 8) over 2^7 ref: (x & 0x000f000f) is the fp16 subnormal pair
 // c 2^-24 and (x & 0x00f000f0) is c 2^-20, so with s24 = scale 2^24, s20 = scale 2^20
 // and z = zero - 8 scale a pair is one AND and one FMA.
@@ -263,8 +267,8 @@ __device__ __forceinline__ uint4 operand(uint32_t x, __half2 s24, __half2 s20, _
     uint32_t w;
     __half2 r;
     if constexpr (EXACT) {
-      w = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
-      r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1032.f));
+      w = ((k == 0 ? x << 1 : x >> (4 * k - 1)) & 0x001e001eu) | 0x64006400u;
+      r = __hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1039.f));
     } else {
       w = (x >> (8 * (k >> 1))) & ((k & 1) ? 0x00f000f0u : 0x000f000fu);
       r = __hfma2((k & 1) ? s20 : s24, *reinterpret_cast<const __half2 *>(&w), z);
@@ -426,10 +430,10 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
           const int row = 32 * w + lane;
           float *m = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8 +
                      (row >> 1) * 8 + (row & 1);
-          m[0] = k.x * p.qscale;
-          m[2] = k.y * p.qscale;
+          m[0] = k.x * (0.5f * p.qscale);
+          m[2] = fmaf(-0.5f, k.x, k.y) * p.qscale;
           m[4] = v.x * inv;
-          m[6] = v.y;
+          m[6] = fmaf(-0.5f, v.x, v.y);
         }
       }
       const uint32_t dst = sb + (which ? L::kV : L::kK) + s * L::kTile;
@@ -746,7 +750,8 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
   if (bad && lane == 0) raise_abort(p.status, abort_flag);
   float l = l2.x + l2.y, z = z2.x + z2.y;
   // out = o_a O + o_b O_B + z, over l
-  float o_a = EXACT ? v_ref : v_ref * 128.f, o_b = 0.f;  // the operands are over 2^7 v_ref
+  // (V's operands are twice the centred codes, or values over 2^7 v_ref)
+  float o_a = EXACT ? v_ref * 0.5f : v_ref * 128.f, o_b = 0.f;
   if (tl.split) {
     // B leaves its (m, l, z, reference) in Q_B, whose products are done; both
     // warpgroups always meet here, failed or not

@@ -1,0 +1,96 @@
+"""The 4-bit cache's attention where weights, rows and queries span a wide range: a key
+that takes nearly all of the weight, rows far larger than their neighbours, very large
+and very small queries, runs that a worker walks over many windows of page ids.  Every
+row is checked by itself against the definition in 64 bits.
+
+The sequences of a call share one set of pages, so that each has a long run of its own
+on the GPU without a large cache."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_171_gb300 as pa
+from tests import kv4_reference as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+U = 2.0 ** -11  # half a step of fp16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_171_gb300 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    assert pa.pa_last_device_error() == 0
+
+
+def randn(*shape, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=gen, device="cuda")
+
+
+def stored(k, v, dt):
+    """One sequence's rows k, v [n, Hkv, D] in a cache of shuffled pages: the cache and
+    the block table [1, blocks]."""
+    n, hkv, d = k.shape
+    blocks = -(-n // 16)
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    bt = torch.randperm(blocks + 1, generator=gen, device="cuda")[:blocks].to(torch.int32)[None]
+    pool = torch.zeros((blocks + 1, hkv, ref.block_bytes(d)), dtype=torch.uint8, device="cuda")
+    pos = torch.arange(n, device="cuda")
+    ref.store(pool, bt, torch.zeros_like(pos), pos, k, v, dt)
+    return pool, bt.contiguous()
+
+
+def attend(q, pool, bt, seen, scale, dt):
+    """softmax(q K^T scale) V in 64 bits, q [nq, Hq, D], query i over seen[i] keys; and
+    R = sqrt(sum p^2 |v|^2) a row: what independent relative errors of the terms p v add
+    up to, a unit of error each."""
+    nq, hq, d = q.shape
+    k, v, _ = ref.values(pool[bt[0].long()], dt)
+    k = k.transpose(0, 1).reshape(pool.shape[1], -1, d)[:, :max(seen)]
+    v = v.transpose(0, 1).reshape(pool.shape[1], -1, d)[:, :max(seen)]
+    out, r = torch.empty(q.shape, dtype=torch.float64, device="cuda"), torch.empty(nq, hq, device="cuda")
+    group = hq // pool.shape[1]
+    late = torch.arange(max(seen), device="cuda")[None, :] >= torch.tensor(seen, device="cuda")[:, None]
+    for h in range(hq):
+        s = (q[:, h].double() @ k[h // group].T * scale).masked_fill_(late, -math.inf)
+        p = s.softmax(-1)
+        out[:, h] = p @ v[h // group]
+        r[:, h] = (p.square() @ v[h // group].square().sum(-1)).sqrt()
+    return out, r
+
+
+def check_chunk(q, pool, bt, ctx, scale, dt, look):
+    """q [B, n_new, Hq, D] over the one sequence of `bt`, in B sequences; those of `look`
+    are compared.  A row's error, in the norm: half a step of the result's type of the row;
+    and, a key, the roundings of its terms, each at most U = 2^-11 relatively: of the weight,
+    and in bf16 of V (twice, the second time of its row's least value, up to 3 times a typical
+    one) and of K (alike, where a score of N(0, 1) products moves by as much as a product).
+    Independent ones add up to sqrt(1 + 10 + 10) U R / sqrt(3) < 3 U R, for fp16 U R / sqrt(3);
+    2.5 times that are allowed."""
+    B, n_new, hq, d = q.shape
+    tokens = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
+    got = pa.prefill_kv4(q, pool, bt.expand(B, -1).contiguous(), tokens, scale)
+    assert pa.pa_last_device_error() == 0
+    half, most = torch.finfo(dt).eps / 2, (8 if dt is torch.bfloat16 else 1.5) * U
+    for b in look:
+        want, r = attend(q[b], pool, bt, [ctx + i + 1 for i in range(n_new)], scale, dt)
+        err = (got[b].double() - want).norm(dim=-1)
+        tol = half * want.norm(dim=-1) + most * r
+        assert (err <= tol).all(), (b, float((err / want.norm(dim=-1)).max()), float((err / tol).max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new,hq,d,keys", [
+    (7, 4, 128, 131072), (40, 4, 128, 32768), (14, 4, 64, 32768), (300, 1, 64, 16384)])
+def test_chunk_over_a_long_run(n_new, hq, d, keys, dtype):
+    """One item a CTA: the sums of a whole context in one accumulator.  28, 56, 160 and 300
+    rows a kv head."""
+    dt = DT[dtype]
+    pool, bt = stored(randn(keys, 1, d, seed=1), randn(keys, 1, d, seed=2), dt)
+    q = randn(152, n_new, hq, d, seed=3).to(dt)
+    check_chunk(q, pool, bt, keys - n_new, 1 / math.sqrt(d), dt, (0, 77, 151))
