@@ -71,7 +71,12 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;
+// A row's running maximum moves once a score passes it by kSlack (powers of two); the
+// weights enter the tensor cores times 2^kLift, 2^15 at most.  What fp16 has left below is
+// for the keys beside one that takes nearly all of the weight (32k of them beside one of
+// 0.999 weigh 2^-25 each): 11 bits down to 2^-25 of the reference, steps of 2^-35 below.
+constexpr float kSlack = 4.0f, kLift = 11.0f;
+static_assert(kSlack + kLift <= 15.0f, "a weight stays below fp16's largest value");
 constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 128, kKeys = 128;     // a row tile, a key tile
@@ -696,7 +701,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
       // 2^-60 these values no longer count, but their weights still do.
       const int by = max(-60, exponent(ch == 0 ? vr.x : ch == 1 ? vr.y : ch == 2 ? vr.z : vr.w) -
                                   exponent(v_ref));
-      const float nb = static_cast<float>(by) - m, back = exp2i(-by);
+      const float nb = static_cast<float>(by) + kLift - m, back = exp2i(-by);
       const float2 nm = make_float2(nb, nb), f2 = make_float2(f[ch], f[ch]);
       float2 sum = make_float2(0.f, 0.f), zs = make_float2(0.f, 0.f);
 #pragma unroll
@@ -748,10 +753,11 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
   }
   if (!bad) bad = !warp_wait(bar(kBarO + x), 0, abort_flag);
   if (bad && lane == 0) raise_abort(p.status, abort_flag);
-  float l = l2.x + l2.y, z = z2.x + z2.y;
-  // out = o_a O + o_b O_B + z, over l
-  // (V's operands are twice the centred codes, or values over 2^7 v_ref)
-  float o_a = EXACT ? v_ref * 0.5f : v_ref * 128.f, o_b = 0.f;
+  // out = o_a O + o_b O_B + z, over l, all of lifted weights (V's operands are twice the
+  // centred codes, or values over 2^7 v_ref)
+  constexpr float kDown = 1.f / (1 << static_cast<int>(kLift));
+  float l = (l2.x + l2.y) * kDown, z = (z2.x + z2.y) * kDown;
+  float o_a = v_ref * (EXACT ? 0.5f * kDown : 128.f * kDown), o_b = 0.f;
   if (tl.split) {
     // B leaves its (m, l, z, reference) in Q_B, whose products are done; both
     // warpgroups always meet here, failed or not

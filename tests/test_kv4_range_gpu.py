@@ -71,7 +71,8 @@ def check_chunk(q, pool, bt, ctx, scale, dt, look):
     and in bf16 of V (twice, the second time of its row's least value, up to 3 times a typical
     one) and of K (alike, where a score of N(0, 1) products moves by as much as a product).
     Independent ones add up to sqrt(1 + 10 + 10) U R / sqrt(3) < 3 U R, for fp16 U R / sqrt(3);
-    2.5 times that are allowed."""
+    2.5 times that are allowed.  An element below the type's normal range is off by up to half
+    a step there, smallest_normal eps / 2, whatever its size: sqrt(D) of them."""
     B, n_new, hq, d = q.shape
     tokens = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
     got = pa.prefill_kv4(q, pool, bt.expand(B, -1).contiguous(), tokens, scale)
@@ -80,7 +81,7 @@ def check_chunk(q, pool, bt, ctx, scale, dt, look):
     for b in look:
         want, r = attend(q[b], pool, bt, [ctx + i + 1 for i in range(n_new)], scale, dt)
         err = (got[b].double() - want).norm(dim=-1)
-        tol = half * want.norm(dim=-1) + most * r
+        tol = half * (want.norm(dim=-1) + math.sqrt(d) * torch.finfo(dt).smallest_normal) + most * r
         assert (err <= tol).all(), (b, float((err / want.norm(dim=-1)).max()), float((err / tol).max()))
 
 
@@ -94,3 +95,31 @@ def test_chunk_over_a_long_run(n_new, hq, d, keys, dtype):
     pool, bt = stored(randn(keys, 1, d, seed=1), randn(keys, 1, d, seed=2), dt)
     q = randn(152, n_new, hq, d, seed=3).to(dt)
     check_chunk(q, pool, bt, keys - n_new, 1 / math.sqrt(d), dt, (0, 77, 151))
+
+
+def sink_case(keys, weight, at, d, dt, shape, seed):
+    """Keys of N(0, 1) scores and values, and one, whose value is 0, that takes `weight` of
+    every query's softmax: along dimension 0 of q, where the others are 0."""
+    scale = 1 / math.sqrt(d)
+    k, v = randn(keys, 1, d, seed=seed), randn(keys, 1, d, seed=seed + 1)
+    k[:, :, 0] = 0
+    v[at] = 0
+    k[at] = 0
+    k[at, :, 0] = math.log(weight / (1 - weight) * keys * math.exp(0.5)) / (8 * scale)
+    q = randn(*shape, d, seed=seed + 2)
+    q[..., 0] = 8
+    pool, bt = stored(k, v, dt)
+    return q.to(dt), pool, bt, scale
+
+
+# one item a CTA at least, so that a run holds the sink and many other keys; 28, 56 and
+# 160 rows a kv head: one row tile, the same, and two
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new,hq,d,keys,weight,at", [
+    (7, 4, 128, 32768, 0.99, 0), (7, 4, 128, 32768, 0.999, 9000), (14, 4, 64, 131072, 0.99, 0),
+    (7, 4, 128, 131072, 0.999, 0), (40, 4, 128, 32768, 0.999, 0), (40, 4, 64, 8192, 0.99, 5000),
+    (300, 1, 128, 32768, 0.99, 3)])
+def test_chunk_below_a_sink(n_new, hq, d, keys, weight, at, dtype):
+    dt = DT[dtype]
+    q, pool, bt, scale = sink_case(keys, weight, at, d, dt, (152, n_new, hq), seed=n_new)
+    check_chunk(q, pool, bt, keys - n_new, scale, dt, (0, 77, 151))
