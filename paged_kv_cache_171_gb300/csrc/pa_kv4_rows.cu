@@ -6,7 +6,7 @@
 // into the tensor cores as they are (exact in 16 bits) and the scales and
 // zeros are applied outside,
 //   s_t = scale_k[t] (q . (c_t - 8)) + zero_k[t] sum q
-//   O   = sum_t (p_t scale_v[t]) (c_t - 8),   z = sum_t p_t zero_v[t]
+//   O   = sum_t (p_t scale_v[t]) (c_t - 7.5),   z = sum_t p_t (zero_v[t] - scale_v[t] / 2)
 // so a page costs no dequantisation beyond turning nibbles into 16-bit floats.
 //
 // Operand form.  mma.sync m16n8k16 with the tokens (then the head dimensions)
@@ -17,13 +17,16 @@
 // order of tokens, is permuted alike) two nibbles four places apart in one
 // word, or the same nibble of two tokens' words, form an operand register.
 // The tensor cores align the addends of a sum to the largest and round toward zero, so
-// operands are centred first: (x & 0x000f000f) | 0x64006400 is 1024 + c, minus 1032;
+// operands are centred first.  K: (x & 0x000f000f) | 0x64006400 is 1024 + c, minus 1032;
 // (x & 0x00f000f0) | 0x64006400 is 1024 + 16 c, times 1/16 minus 72; both exact.
-// Codes as they are (one AND, as fp16 subnormals) would save the 64 subtractions a page,
-// but sums that carry 8 sum q or 8 sum p lose the last bits of the result: for K
-// measured 1.3e-6 of the result's norm against 2e-7 (8% faster), for V 1e-4.  q is
-// scaled by a power of two a row (its largest magnitude near 2^15; exact in fp16 down
-// to 2^-39 of that).
+// V: the fp16 subnormals x & 0x000f000f = c 2^-24 and x & 0x00f000f0 = c 2^-20, by one
+// FMA each (c - 7.5) 2^-9, exact too; codes of a row lie evenly about 7.5, so that the
+// sums do not grow with the number of keys where the result's terms cancel (with c - 8
+// rows over 131072 keys were off by 1.2e-5, so by 7e-7; plain fp32: 1e-6).
+// Codes as they are (one AND) would save the subtractions, but sums that carry 8 sum q
+// or 8 sum p lose the last bits of the result: for K measured 1.3e-6 of the result's
+// norm against 2e-7 (8% faster), for V 1e-4.  q is scaled by a power of two a row (its
+// largest magnitude near 2^15; exact in fp16 down to 2^-39 of that).
 // The weights p scale_v enter as two fp16 terms (head and remainder, 22 bits), relative
 // to a power of two above the largest |scale_v| so far and multiplied by 2^7: they stay
 // below 2^15 and the second term reaches 2^-32 of the largest.  With at most 4 rows
@@ -127,6 +130,14 @@ __device__ __forceinline__ uint32_t sub_1032(uint32_t x) {
 __device__ __forceinline__ uint32_t sixteenth_sub_72(uint32_t x) {
   const __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&x), __float2half2_rn(0.0625f),
                             __float2half2_rn(-72.f));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// (c - 7.5) 2^-9 of the fp16 subnormals c 2^-K, exact.
+template <int K>
+__device__ __forceinline__ uint32_t centred(uint32_t x) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&x), __float2half2_rn(1 << (K - 9)),
+                            __float2half2_rn(-7.5f / 512.f));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
@@ -687,7 +698,8 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         l2 = __fadd2_rn(l2, pr);
         const float x = v[u].x * v_inv;
         float2 wt = make_float2(pr.x * x, pr.y * x);
-        float2 zt = make_float2(v[u].y, v[u].y);
+        const float mid = fmaf(-0.5f, v[u].x, v[u].y);  // of the row
+        float2 zt = make_float2(mid, mid);
         if (OUT16 && edge) {  // a key that this row does not see may not be finite
           if (s[u].x == -INFINITY) wt.x = zt.x = 0.f;
           if (s[u].y == -INFINITY) wt.y = zt.y = 0.f;
@@ -738,10 +750,10 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
 #pragma unroll
             for (int pg = 0; pg < kPair; ++pg) {
               const uint32_t xs = x[pg] >> (8 * u), ys = y[pg] >> (8 * u);
-              a[pg][0] = sub_1032((xs & 0x000f000fu) | 0x64006400u);
-              a[pg][1] = sixteenth_sub_72((xs & 0x00f000f0u) | 0x64006400u);
-              a[pg][2] = sub_1032((ys & 0x000f000fu) | 0x64006400u);
-              a[pg][3] = sixteenth_sub_72((ys & 0x00f000f0u) | 0x64006400u);
+              a[pg][0] = centred<24>(xs & 0x000f000fu);
+              a[pg][1] = centred<20>(xs & 0x00f000f0u);
+              a[pg][2] = centred<24>(ys & 0x000f000fu);
+              a[pg][3] = centred<20>(ys & 0x00f000f0u);
             }
             float t[4];
             if constexpr (WIDE) {
@@ -776,7 +788,7 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
     }
     cp_async_wait();  // the next part's q
     team_sync(team);  // the part before this one has been merged
-    const float back = v_ref * 0x1p-7f;
+    const float back = v_ref * 0x1p2f;  // V's operands are over 2^9, the weights over 2^-7
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
       float2 a = make_float2(o[k][0].x, o[k][1].x), b = make_float2(o[k][0].y, o[k][1].y);

@@ -97,6 +97,24 @@ def test_chunk_over_a_long_run(n_new, hq, d, keys, dtype):
     check_chunk(q, pool, bt, keys - n_new, 1 / math.sqrt(d), dt, (0, 77, 151))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,d,keys", [(4, 128, 32768), (8, 128, 131072), (3, 64, 131072)])
+def test_decode_over_a_long_run(hq, d, keys, dtype):
+    """One item a team of warps.  A score is off by at most 8 roundings of a partial sum, 4 in
+    powers of two (2.6e-6 of a weight), a weight's two terms and its exponential by 2^-21, and
+    the sums, a few times the result, by as much as a plain fp32 evaluation's (1e-6)."""
+    dt, scale = DT[dtype], 1 / math.sqrt(d)
+    pool, bt = stored(randn(keys, 1, d, seed=1), randn(keys, 1, d, seed=2), dt)
+    q = randn(608, hq, d, seed=3).to(dt)
+    tokens = torch.full((608,), keys, dtype=torch.int32, device="cuda")
+    got = pa.decode_kv4(q, pool, bt.expand(608, -1).contiguous(), tokens, scale)
+    assert pa.pa_last_device_error() == 0
+    for b in (0, 300, 607):
+        want, _ = attend(q[b:b + 1], pool, bt, [keys], scale, dt)
+        err = (got[b].double() - want[0]).norm(dim=-1) / want[0].norm(dim=-1)
+        assert err.max() <= 5e-6, (b, float(err.max()))
+
+
 def sink_case(keys, weight, at, d, dt, shape, seed):
     """Keys of N(0, 1) scores and values, and one, whose value is 0, that takes `weight` of
     every query's softmax: along dimension 0 of q, where the others are 0."""
