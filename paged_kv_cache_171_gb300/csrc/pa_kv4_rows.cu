@@ -29,7 +29,11 @@
 // largest magnitude near 2^15; exact in fp16 down to 2^-39 of that).
 // The weights p scale_v enter as two fp16 terms (head and remainder, 22 bits), relative
 // to a power of two above the largest |scale_v| so far and multiplied by 2^7: they stay
-// below 2^15 and the second term reaches 2^-32 of the largest.  With at most 4 rows
+// below 2^15.  The remainder, at most 2^3, is multiplied by 2^12 and summed in an
+// accumulator of its own, so it still holds weights below the head's range, in steps of
+// 2^-43 of the largest (at the head's scale it ended where the head does: 32k keys beside
+// one that takes 0.99 of the weight came out 4e-4 off, now 9e-7); and l keeps what its
+// last rounding lost.  With at most 4 rows
 // (WIDE false) columns 4-7 repeat columns 0-3 and carry the second terms: one MMA does
 // both.  The weights, in the accumulator's layout (token, row), become the second
 // product's operand (row, token) by movmatrix.  The sums of each two pages are taken in
@@ -65,6 +69,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleSlack = 8.0f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
+constexpr float kRemLift = 4096.f;  // of the weights' remainders
 constexpr int kWarps = 4, kStages = 2, kTile = 8;  // query rows a tile
 constexpr int kPair = 2;         // pages a stage holds
 constexpr int kTeams = 4;        // teams of kWarps warps a CTA, one CTA an SM
@@ -560,8 +565,10 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
     // per row 2 lc (x) and 2 lc + 1 (y): the running max, negated, the sums l and z
     float2 nm = make_float2(-kNoKey, -kNoKey);
     float2 l2 = make_float2(0.f, 0.f), z2 = make_float2(0.f, 0.f);
+    float2 l_rest = make_float2(0.f, 0.f);  // what l lost to its last rounding
     float v_ref = 0.f, v_inv = 0.f;  // reference of scale_v (a power of two), 2^7 / it
-    const float rem = lc < 2 ? 0.f : -1.f;  // this lane's columns carry remainder terms
+    // !WIDE: columns 4-7 carry 2^12 (weight - head), the others the weight
+    const float lift = lc < 2 ? 1.f : kRemLift, rem = lc < 2 ? 0.f : -kRemLift;
 
     // Keys that every row of the tile sees and this part holds end here.
     const int part_end = (part.pg0 + part.n_pg) * kPageSize;
@@ -672,6 +679,7 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         float2 c = make_float2(ex2(-nm.x - n0), ex2(-nm.y - n1));
         nm = make_float2(-n0, -n1);
         l2 = __fmul2_rn(l2, c);
+        l_rest = __fmul2_rn(l_rest, c);
         z2 = __fmul2_rn(z2, c);
         if (vtop > v_ref) {
           // a power of two above it, and at least 2^-100
@@ -692,10 +700,11 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
 
       // ---- weights, as the second product's operand
       uint32_t hi[2 * kPair], lo[2 * kPair];
+      float2 sum = l_rest;  // small weights add up before they meet a large l
 #pragma unroll
       for (int u = 0; u < 2 * kPair; ++u) {
         const float2 pr = make_float2(ex2(d[u].x), ex2(d[u].y));
-        l2 = __fadd2_rn(l2, pr);
+        sum = __fadd2_rn(sum, pr);
         const float x = v[u].x * v_inv;
         float2 wt = make_float2(pr.x * x, pr.y * x);
         const float mid = fmaf(-0.5f, v[u].x, v[u].y);  // of the row
@@ -709,12 +718,19 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         const float2 back = unpack2<false>(head);
         if constexpr (WIDE) {
           hi[u] = transpose8x8(head);
-          lo[u] = transpose8x8(pack2<false>(wt.x - back.x, wt.y - back.y));
+          lo[u] = transpose8x8(pack2<false>((wt.x - back.x) * kRemLift, (wt.y - back.y) * kRemLift));
         } else {  // the head term again, or the remainder
-          const float2 mine = make_float2(fmaf(rem, back.x, wt.x), fmaf(rem, back.y, wt.y));
+          const float2 mine = __ffma2_rn(make_float2(rem, rem), back,
+                                         __fmul2_rn(wt, make_float2(lift, lift)));
           hi[u] = transpose8x8(pack2<false>(mine.x, mine.y));
           lo[u] = 0;
         }
+      }
+
+      {
+        const float2 l_new = __fadd2_rn(l2, sum);
+        l_rest = __fadd2_rn(sum, __fadd2_rn(l2, make_float2(-l_new.x, -l_new.y)));
+        l2 = l_new;
       }
 
       // ---- O[dimension][row] += V^T P, the chunk's sum in an accumulator of its own
@@ -756,15 +772,16 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
               a[pg][3] = centred<20>(ys & 0x00f000f0u);
             }
             float t[4];
+            float2 (&ok)[2] = o[4 * j + 2 * h + u];
             if constexpr (WIDE) {
               mma_from_zero(t, a[0], lo[0], lo[1]);
               mma16816<false>(t, a[1], lo[2], lo[3]);
-              mma16816<false>(t, a[0], hi[0], hi[1]);
-            } else {
-              mma_from_zero(t, a[0], hi[0], hi[1]);
+              const float2 down = make_float2(1.f / kRemLift, 1.f / kRemLift);
+              ok[0] = __ffma2_rn(make_float2(t[0], t[1]), down, ok[0]);
+              ok[1] = __ffma2_rn(make_float2(t[2], t[3]), down, ok[1]);
             }
+            mma_from_zero(t, a[0], hi[0], hi[1]);
             mma16816<false>(t, a[1], hi[2], hi[3]);
-            float2 (&ok)[2] = o[4 * j + 2 * h + u];
             ok[0] = __fadd2_rn(ok[0], make_float2(t[0], t[1]));
             ok[1] = __fadd2_rn(ok[1], make_float2(t[2], t[3]));
           }
@@ -793,10 +810,10 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
     for (int k = 0; k < MT; ++k) {
       float2 a = make_float2(o[k][0].x, o[k][1].x), b = make_float2(o[k][0].y, o[k][1].y);
       if constexpr (!WIDE) {  // columns 4-7 hold the remainder terms of 0-3
-        a.x += __shfl_xor_sync(kFull, a.x, 2);
-        a.y += __shfl_xor_sync(kFull, a.y, 2);
-        b.x += __shfl_xor_sync(kFull, b.x, 2);
-        b.y += __shfl_xor_sync(kFull, b.y, 2);
+        a.x = fmaf(__shfl_xor_sync(kFull, a.x, 2), 1.f / kRemLift, a.x);
+        a.y = fmaf(__shfl_xor_sync(kFull, a.y, 2), 1.f / kRemLift, a.y);
+        b.x = fmaf(__shfl_xor_sync(kFull, b.x, 2), 1.f / kRemLift, b.x);
+        b.y = fmaf(__shfl_xor_sync(kFull, b.y, 2), 1.f / kRemLift, b.y);
       }
       if (WIDE || lc < 2) {
         float *dst = mer_o + (warp * kTile + 2 * lc) * L::kRowStride + (D / 8) * ln + 2 * k;

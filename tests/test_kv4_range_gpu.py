@@ -141,3 +141,33 @@ def test_chunk_below_a_sink(n_new, hq, d, keys, weight, at, dtype):
     dt = DT[dtype]
     q, pool, bt, scale = sink_case(keys, weight, at, d, dt, (152, n_new, hq), seed=n_new)
     check_chunk(q, pool, bt, keys - n_new, scale, dt, (0, 77, 151))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,d,keys,weight,at", [
+    (4, 128, 32768, 0.99, 0), (8, 128, 32768, 0.99, 7000), (3, 64, 131072, 0.99, 0),
+    (8, 64, 131072, 0.999, 0), (1, 128, 32768, 0.999, 5), (12, 128, 32768, 0.999, 20000)])
+def test_decode_below_a_sink(hq, d, keys, weight, at, dtype):
+    """One item a team of warps.  Scores whose terms add up to at most 16 in powers of two
+    are off by at most 12 roundings of 2^-23 of that, 1.6e-5 of a weight; a weight's two
+    terms and its exponential by 2^-21; the sums of a row, whose middles add up to some 60
+    times the result while it cancels, by about that times 2^-23 (7e-6): 2.4e-5 in all."""
+    dt = DT[dtype]
+    q, pool, bt, scale = sink_case(keys, weight, at, d, dt, (608, hq), seed=hq)
+    tokens = torch.full((608,), keys, dtype=torch.int32, device="cuda")
+    got = pa.decode_kv4(q, pool, bt.expand(608, -1).contiguous(), tokens, scale)
+    assert pa.pa_last_device_error() == 0
+    for b in (0, 300, 607):
+        want, _ = attend(q[b:b + 1], pool, bt, [keys], scale, dt)
+        err = (got[b].double() - want[0]).norm(dim=-1) / want[0].norm(dim=-1)
+        assert err.max() <= 2.4e-5, (b, float(err.max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new,hq,d,keys,weight", [
+    (2, 4, 128, 131072, 0.99), (1, 1, 64, 131072, 0.999), (3, 5, 128, 65536, 0.999)])
+def test_short_chunk_below_a_sink(n_new, hq, d, keys, weight, dtype):
+    """Up to 16 rows a kv head, which take the decode's kernel."""
+    dt = DT[dtype]
+    q, pool, bt, scale = sink_case(keys, weight, 11, d, dt, (608, n_new, hq), seed=n_new)
+    check_chunk(q, pool, bt, keys - n_new, scale, dt, (0, 300, 607))
