@@ -12,6 +12,11 @@
 //    the largest magnitude of 32 keys (k_ref, v_ref).  K and V are then off by two half
 //    steps of 2^-11 and P by one, well below the bf16 result's own rounding of 2^-8, and
 //    the softmax works on S as it comes: a factor for each 32 keys in its exponent.
+//    Operands reach up to 2^-7 in fp16, which has all its bits down to 2^-14: where a
+//    key's largest magnitude is below 2^-5 of the reference, that is lowered by as much
+//    (K's by 2^15 at most, V's by 2^11, which P gives up), and each key is converted over
+//    a power of two of its own before it is moved there.  At the common reference one key
+//    1024 times the others, whatever its weight, left those 31 with an error of 1.3%.
 //  * fp16: that would be as much as the result's rounding, so the codes enter the
 //    products exactly, as 2 c - 15 ((x & 0x001e001e) | 0x64006400 is 1024 + 2 c, x the
 //    word shifted left by one), and the softmax threads apply the rest: with the row's
@@ -407,12 +412,28 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
       k = make_float2(0.f, __int_as_float(0x7fc00000));
       v = make_float2(0.f, 0.f);
     }
-    float k_top = EXACT ? 0.f : fmaf(8.f, fabsf(k.x), fabsf(k.y));  // a NaN does not count
-    float v_top = EXACT ? fabsf(v.x) : fmaf(8.f, fabsf(v.x), fabsf(v.y));
-    // no float is negative here, so their bits are in their order
-    if (!EXACT) k_top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(k_top, 0.f))));
-    v_top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(v_top, 0.f))));
-    const float k_ref = EXACT ? 1.f : above(k_top), v_ref = above(v_top);
+    // the row's largest magnitude (a NaN does not count) and the 32 rows'; no float is
+    // negative here, so their bits are in their order
+    const float k_own = EXACT ? 0.f : fmaxf(fmaf(8.f, fabsf(k.x), fabsf(k.y)), 0.f);
+    const float v_own = fmaxf(EXACT ? fabsf(v.x) : fmaf(8.f, fabsf(v.x), fabsf(v.y)), 0.f);
+    auto top_of = [](float own) {
+      return above(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(own))));
+    };
+    const float k_ref = EXACT ? 1.f : top_of(k_own), v_ref = top_of(v_own);
+    // How far the reference is lowered for rows below 2^-5 of it (other than zero).
+    int k_span = 0, v_span = 0;
+    auto small = [](float own, float ref) { return own > 0.f && own * 32.f < ref; };
+    if (!EXACT && __builtin_expect(
+                      __any_sync(kFull, small(k_own, k_ref) || small(v_own, v_ref)), 0)) {
+      auto span_of = [](float own, float ref) {
+        const uint32_t least =
+            __reduce_min_sync(kFull, own > 0.f ? __float_as_uint(own) : 0x7f800000u);
+        const int span = exponent(ref) - exponent(__uint_as_float(least));
+        return span > 5 ? span : 0;
+      };
+      k_span = min(15, span_of(k_own, k_ref));
+      v_span = min(11, span_of(v_own, v_ref));
+    }
 
     const int s = t % kStages;
 #pragma unroll 1
@@ -422,7 +443,11 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
         ok = warp_wait2(bar(free + 2 * tl.first(s) + s), (t / kStages - 1) & 1,
                         bar(free + 2 * tl.last(s) + s), (t / kStages - 1) & 1, abort_flag);
       if (!ok) break;
-      const float inv = exp2i(-exponent(which ? v_ref : k_ref));
+      const int span = which ? v_span : k_span;
+      const int ref = exponent(which ? v_ref : k_ref);
+      int row_ref = ref;
+      if (__builtin_expect(span, 0)) row_ref = exponent(above(which ? v_own : k_own));
+      const float inv = exp2i(-row_ref);
       const float2 own = which ? v : k;
       // over 2^7 ref: |scale| 2^24 is at most 2^14
       const uint32_t scales = pack2<false>(own.x * inv * 0x1p17f, own.x * inv * 0x1p13f);
@@ -430,7 +455,10 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
       if (which) {
         // V's stage is free once the softmax has read these for the tile before in it
         float *refs = reinterpret_cast<float *>(smem + L::kRef) + 8 * s;
-        if (lane == 0) refs[w] = k_ref, refs[4 + w] = v_ref;
+        if (lane == 0) {
+          refs[w] = k_ref * exp2i(-k_span);
+          refs[4 + w] = v_ref * exp2i(-v_span);
+        }
         if constexpr (EXACT) {
           const int row = 32 * w + lane;
           float *m = reinterpret_cast<float *>(smem + L::kMeta) + s * (kKeys / 2) * 8 +
@@ -466,6 +494,26 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
           st_shared_v4(to ^ (u << 4), o.x, o.y, o.z, o.w);
         }
         codes[i] = v_codes[i];  // for the second round
+      }
+      if (!EXACT && __builtin_expect(span, 0)) {
+        // what this thread wrote, from its rows' own references to the lowered one
+        const float move = exp2i(max(-24, row_ref - ref + span));
+        const uint32_t moves = pack2<false>(move, move);
+#pragma unroll 1
+        for (int i = 0; i < 8 * kIters; ++i) {
+          const int k = i >> 2;
+          const int row = (k / kIters) * kPageSize + (k % kIters) * (32 / kPieces) + row_l;
+          const uint32_t by = __shfl_sync(kFull, moves, row);
+          const uint32_t at =
+              (dst + (piece >> 1) * L::kColBlk + swz128(32 * w + row, 4 * piece)) ^ ((i & 3) << 4);
+          const uint4 o = lds128(at);
+          auto times = [&](uint32_t x) {
+            const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x),
+                                      *reinterpret_cast<const __half2 *>(&by));
+            return *reinterpret_cast<const uint32_t *>(&r);
+          };
+          st_shared_v4(at, times(o.x), times(o.y), times(o.z), times(o.w));
+        }
       }
       fence_proxy_async_smem();  // generic stores -> read by the tensor cores
       __syncwarp();
@@ -879,7 +927,7 @@ __device__ __forceinline__ void cta_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(N), "n"(kThreads) : "memory");
 }
 
-// Registers a thread after the split: the softmax holds a whole row of scores.
+// Registers a thread after the split (not FEW): the softmax holds a whole row of scores.
 constexpr int kRegsLaunch = 128, kRegsMma = 64, kRegsConvert = 96, kRegsSoftmax = 176;
 static_assert(128 * (kRegsMma + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
               "register split");
@@ -893,7 +941,9 @@ __device__ __forceinline__ void set_registers() {
 
 // FEW: calls with at most 64 rows a kv head.  Both row tiles are the same rows (one Q),
 // and warps 2 and 3 of the softmax warpgroups, whose rows are none, turn the odd key
-// tiles' codes, through rings in Q_B's place.
+// tiles' codes, through rings in Q_B's place.  All keep the registers of the launch, so
+// that the two groups of converters are one copy of the code (two in the instruction
+// caches, each at its own registers: 4 x 4 queries over 32k keys 97 us, so 86).
 template <int D, bool BF16, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillParams p) {
   using L = PrefillSmem<D>;
@@ -948,8 +998,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     cta_sync<2>();
     tc::fence_after_sync();
   };
+  const int x = (warp - kSoftmaxWarp0) >> 2;  // of a softmax warpgroup
+  auto own_q = [&](const volatile TilePart &part, const Tiling &tl) {
+    if (!FEW || x == 0) load_q<D, BF16, EXACT, FEW>(p, part, tl.split, x, sb, smem, tid & 127);
+    // what this thread left in Q_B, before copies into it
+    if (FEW) fence_proxy_async_smem();
+  };
   if (warp < kConvertWarp0) {
-    set_registers<kRegsMma, false>();
+    if constexpr (!FEW) set_registers<kRegsMma, false>();
     for (int turn = 0;; ++turn) {
       const TilePart part = parts[turn & 1];
       const Tiling tl(part.row0, part.nt, p.n_rows);
@@ -977,52 +1033,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
         break;
       }
     }
-  } else if (warp < kSoftmaxWarp0) {
-    set_registers<kRegsConvert, false>();
+  } else if (warp < kSoftmaxWarp0 || (FEW && (warp & 2))) {
+    if constexpr (!FEW) set_registers<kRegsConvert, false>();
+    const int c = FEW && warp >= kSoftmaxWarp0 ? 1 : 0;
     for (int turn = 0;; ++turn) {
       const TilePart part = parts[turn & 1];
       const Tiling tl(part.row0, part.nt, p.n_rows);
+      if (c == 1) own_q(part, tl);
       begin();
-      convert_tiles<D, BF16, EXACT>(0, FEW && tl.split ? 2 : 1, warp - kConvertWarp0, p, part, sb,
-                                    bars_of(turn), smem, tl, abort_flag, lane);
+      if (c == 0 || tl.split)
+        convert_tiles<D, BF16, EXACT>(c, FEW && tl.split ? 2 : 1,
+                                      c == 0 ? warp - kConvertWarp0 : 2 * x + (warp & 1), p, part,
+                                      sb, bars_of(turn), smem, tl, abort_flag, lane);
+      if (c == 1 && tl.split) row_tiles_sync();
       finish();
       if (!part.more || *abort_flag) break;
     }
   } else {
-    set_registers<kRegsSoftmax, true>();
-    const int x = (warp - kSoftmaxWarp0) >> 2;
-    auto own_q = [&](const volatile TilePart &part, const Tiling &tl) {
-      if (!FEW || x == 0) load_q<D, BF16, EXACT, FEW>(p, part, tl.split, x, sb, smem, tid & 127);
-      // what this thread left in Q_B, before copies into it
-      if (FEW) fence_proxy_async_smem();
-    };
-    if (FEW && (warp & 2)) {
-      for (int turn = 0;; ++turn) {
-        const TilePart part = parts[turn & 1];
-        const Tiling tl(part.row0, part.nt, p.n_rows);
-        own_q(part, tl);
-        begin();
-        if (tl.split) {
-          convert_tiles<D, BF16, EXACT>(1, 2, 2 * x + (warp & 1), p, part, sb, bars_of(turn), smem,
-                                        tl, abort_flag, lane);
-          row_tiles_sync();
-        }
-        finish();
-        if (!part.more || *abort_flag) break;
-      }
-    } else {
-      for (int turn = 0;; ++turn) {
-        const volatile TilePart &part = parts[turn & 1];
-        const Tiling tl(part.row0, part.nt, p.n_rows);
-        own_q(part, tl);
-        const uint32_t tmem = begin();
-        if (x < tl.n_active)
-          softmax_tiles<D, BF16, EXACT, FEW>(p, part, x, tl, sb, bars_of(turn), tmem, smem,
-                                             abort_flag, warp, lane);
-        const bool more = part.more;
-        finish();
-        if (!more || *abort_flag) break;
-      }
+    if constexpr (!FEW) set_registers<kRegsSoftmax, true>();
+    for (int turn = 0;; ++turn) {
+      const volatile TilePart &part = parts[turn & 1];
+      const Tiling tl(part.row0, part.nt, p.n_rows);
+      own_q(part, tl);
+      const uint32_t tmem = begin();
+      if (x < tl.n_active)
+        softmax_tiles<D, BF16, EXACT, FEW>(p, part, x, tl, sb, bars_of(turn), tmem, smem,
+                                           abort_flag, warp, lane);
+      const bool more = part.more;
+      finish();
+      if (!more || *abort_flag) break;
     }
   }
   __syncthreads();
@@ -1089,7 +1128,7 @@ int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
   static ContextCache<bool> smem_set;
   if (set_smem_limit(kern, PrefillSmem<D>::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
   // the split draws on what the block was launched with; less of it would never come free
-  static std::atomic<bool> enough{false};
+  static std::atomic<bool> enough{FEW};
   if (!enough) {
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs < kRegsLaunch)

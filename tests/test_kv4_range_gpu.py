@@ -171,3 +171,45 @@ def test_short_chunk_below_a_sink(n_new, hq, d, keys, weight, dtype):
     dt = DT[dtype]
     q, pool, bt, scale = sink_case(keys, weight, 11, d, dt, (608, n_new, hq), seed=n_new)
     check_chunk(q, pool, bt, keys - n_new, scale, dt, (0, 300, 607))
+
+
+@pytest.mark.parametrize("n_new,hq,d,keys,every", [
+    (7, 4, 128, 1000, 32), (14, 4, 64, 5000, 32), (40, 4, 128, 3000, 500), (160, 2, 64, 700, 32),
+    (2, 4, 128, 1000, 32)])
+@pytest.mark.parametrize("dtype,what,factor", [
+    ("bf16", "kv", 64), ("bf16", "kv", 1024), ("bf16", "kv", 8192), ("bf16", "k", 2 ** 20),
+    ("bf16", "v", 4096), ("fp16", "kv", 1024), ("fp16", "kv", 8192)])
+def test_chunk_beside_rows_far_larger(n_new, hq, d, keys, every, dtype, what, factor):
+    """Rows `factor` times the others, of no weight (every query's score for them is far below
+    the others): their neighbours keep their digits.  The last is a token of the chunk that no
+    query but the last one sees.  28, 56, 160 and 320 rows a kv head, and 8, which take the
+    decode's kernel."""
+    dt, scale = DT[dtype], 1 / math.sqrt(d)
+    k, v = randn(keys, 1, d, seed=1), randn(keys, 1, d, seed=2)
+    k[..., 0] = 0
+    big = torch.arange(5, keys, every, device="cuda")
+    big = torch.cat((big, torch.tensor([keys - 1], device="cuda")))
+    # q . k = -8 f + 0.1 f N(0, D), f = `factor`, or 64 where only the values are larger
+    f = factor if "k" in what else 64
+    k[big] = k[big] * 0.1 * f
+    k[big, :, 0] = -f
+    if "v" in what:
+        v[big] *= factor
+    pool, bt = stored(k, v, dt)
+    q = randn(2, n_new, hq, d, seed=3)
+    q[..., 0] = 8
+    check_chunk(q.to(dt), pool, bt, keys - n_new, scale, dt, (0, 1))
+
+
+@pytest.mark.parametrize("n_new,hq,d,keys", [(7, 4, 128, 2000), (40, 4, 64, 3000)])
+@pytest.mark.parametrize("dtype,by", [("bf16", 2.0 ** -e) for e in (4, 5, 6, 7, 12, 30)] +
+                         [("fp16", 2.0 ** -12)])
+def test_chunk_beside_rows_far_smaller(n_new, hq, d, keys, dtype, by):
+    """One key and value in 32 much smaller than the others, which keep their digits."""
+    dt = DT[dtype]
+    k, v = randn(keys, 1, d, seed=1), randn(keys, 1, d, seed=2)
+    k[7::32] *= by
+    v[7::32] *= by
+    pool, bt = stored(k, v, dt)
+    q = randn(2, n_new, hq, d, seed=3).to(dt)
+    check_chunk(q, pool, bt, keys - n_new, 1 / math.sqrt(d), dt, (0, 1))
