@@ -691,6 +691,11 @@ def _device_index(t):
     return index
 
 
+# What an empty tensor, which has no address, is passed on as: the library wants every
+# pointer, and checks the other arguments, of calls with nothing to do too.
+_NOTHING = 16
+
+
 class _On:
     """Makes device `index` current, and `stream` (a torch stream or a handle, if
     given) the current stream there, so that what a call allocates belongs to the
@@ -792,13 +797,14 @@ def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, 
             q_out = torch.empty((n_tok, hq, D), dtype=dtype, device=q.device)
         else:
             _want(q_out, "q_out", dtype, (n_tok, hq, D), index)
-        q_in, q_to = q.data_ptr(), q_out.data_ptr()
+        q_in, q_to = q.data_ptr() or _NOTHING, q_out.data_ptr() or _NOTHING
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rc = entry(k_new.data_ptr(), v_new.data_ptr(), q_in, *caches, q_to, block_table.data_ptr(),
-               seq_idx.data_ptr(), pos.data_ptr(), table, n_tok, ks, vs, qs, hq, hkv, D,
-               page_size, batch, max_blocks, num_pages, max_pos, rot, bool(interleaved),
-               dtype_code(k_new), torch._C._cuda_getCurrentRawStream(index))
+    rows = (k_new.data_ptr(), v_new.data_ptr()) if n_tok else (_NOTHING, _NOTHING)
+    places = (seq_idx.data_ptr(), pos.data_ptr()) if n_tok else (_NOTHING, _NOTHING)
+    rc = entry(*rows, q_in, *caches, q_to, block_table.data_ptr(), *places, table, n_tok, ks, vs,
+               qs, hq, hkv, D, page_size, batch, max_blocks, num_pages, max_pos, rot,
+               bool(interleaved), dtype_code(k_new), torch._C._cuda_getCurrentRawStream(index))
     if rc:
         raise PAError(rc, where)
     return q_out
@@ -868,8 +874,9 @@ def read_kv4(kv_cache, block_table, seq_idx, pos, dtype=None, k_out=None, v_out=
         v_out = torch.empty(shape, dtype=dtype, device=kv_cache.device)
     _want(k_out, "k_out", dtype, shape, index)
     _want(v_out, "v_out", dtype, shape, index)
-    rc = lib().pa_read_kv4(kv_cache.data_ptr(), block_table.data_ptr(), seq_idx.data_ptr(),
-                           pos.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), n_tok, hkv, D, 16,
+    ptrs = (_NOTHING,) * 4 if n_tok == 0 else (seq_idx.data_ptr(), pos.data_ptr(),
+                                               k_out.data_ptr(), v_out.data_ptr())
+    rc = lib().pa_read_kv4(kv_cache.data_ptr(), block_table.data_ptr(), *ptrs, n_tok, hkv, D, 16,
                            batch, max_blocks, pages, dtype_code(k_out),
                            torch._C._cuda_getCurrentRawStream(index))
     if rc:
@@ -888,8 +895,9 @@ def copy_pages_kv4(kv_cache, src, dst, stream=None):
     n = src.numel()
     _want(src, "src", torch.int32, (n,), index)
     _want(dst, "dst", torch.int32, (n,), index)
-    _check(lib().pa_copy_pages_kv4(kv_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, hkv, D,
-                                   16, pages, torch._C._cuda_getCurrentRawStream(index)),
+    _check(lib().pa_copy_pages_kv4(kv_cache.data_ptr(), src.data_ptr() or _NOTHING,
+                                   dst.data_ptr() or _NOTHING, n, hkv, D, 16, pages,
+                                   torch._C._cuda_getCurrentRawStream(index)),
            "pa_copy_pages_kv4")
 
 
@@ -962,8 +970,9 @@ def prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=N
     if workspace is None:
         workspace = torch.empty(pa_prefill_kv4_workspace_size(B, n_new, hq, hkv, D, 16, mb),
                                 dtype=torch.uint8, device=q.device)
-    rc = lib().pa_prefill_kv4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-                              ctx_lens.data_ptr(), n_new, out.data_ptr(), scale, hq, hkv, D, 16,
+    q_in, q_to = (q.data_ptr(), out.data_ptr()) if n_new else (_NOTHING, _NOTHING)
+    rc = lib().pa_prefill_kv4(q_in, kv_cache.data_ptr(), block_table.data_ptr(),
+                              ctx_lens.data_ptr(), n_new, q_to, scale, hq, hkv, D, 16,
                               B, mb, pages, dtype_code(q), workspace.data_ptr(), workspace.nbytes,
                               torch._C._cuda_getCurrentRawStream(index))
     if rc:
