@@ -787,7 +787,7 @@ def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, 
     table = q_in = q_to = None
     if cos_sin is not None:
         max_pos, rot = _want_2d(cos_sin, "cos_sin", torch.float32, None, index)
-        table = cos_sin.data_ptr()
+        table = cos_sin.data_ptr() or _NOTHING
     if q is not None:
         if q.dim() != 3:
             raise ValueError(f"q: want [n_tok, n_q_heads, head_dim], got {tuple(q.shape)}")

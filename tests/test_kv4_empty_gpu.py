@@ -43,6 +43,22 @@ def test_appends_of_no_token():
     assert pa.pa_last_device_error() == 0
 
 
+def test_a_table_of_no_position_is_refused():
+    """Not taken for a call without rotation."""
+    _, _, _, _, bt = _args()
+    x = torch.ones((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    at = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = pa.kv4_cache(2, 2, 128)
+    kc = torch.zeros((2, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    none = torch.empty((0, 128), device="cuda")
+    for call in (lambda: pa.append_kv4(x, x, kv, bt, at, at, cos_sin=none),
+                 lambda: pa.append_kv_rope(x, x, kc, kc.clone(), bt, at, at, none)):
+        with pytest.raises(pa.PAError) as e:
+            call()
+        assert "PA_ERR_ROPE" in str(e.value)
+    assert (kv == 0).all() and (kc == 0).all()
+
+
 def test_read_and_copy_of_nothing():
     none, _, _, _, bt = _args()
     kv = torch.full((2, 2, 2176), 7, dtype=torch.uint8, device="cuda")
