@@ -906,8 +906,9 @@ __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile Ti
       }
 #pragma unroll
       for (int o = 1; o < kChunks; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      // 2^ex brings the row's largest magnitude into [2^14, 2^15)
-      const int ex = min(90, max(-90, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
+      // 2^ex brings the row's largest magnitude into [2^14, 2^15), or near 1 where that
+      // is near the smallest of all
+      const int ex = min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127));
       const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
       for (int u = 0; u < 4; ++u) w[u] = pack2<false>(f[u].x * up, f[u].y * up);

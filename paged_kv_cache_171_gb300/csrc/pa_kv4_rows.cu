@@ -540,8 +540,9 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         total_q += __shfl_xor_sync(kFull, total_q, o);
       }
-      // 2^ex brings the row's largest magnitude into [2^14, 2^15)
-      const int ex = min(90, max(-90, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
+      // 2^ex brings the row's largest magnitude into [2^14, 2^15), or near 1 where that
+      // is near the smallest of all
+      const int ex = min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127));
       const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
       for (int k = 0; k < KW; ++k)
@@ -631,10 +632,11 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
               mma16816<false>(acc, a, qb[2 * k + h][0], qb[2 * k + h][1]);
           }
         const float2 k0 = unpack2<BF16>(km0), k1 = unpack2<BF16>(km1);
-        s[2 * pg].x = fmaf(k0.x, f0 * acc[0], k0.y * e0);
-        s[2 * pg].y = fmaf(k0.x, f1 * acc[1], k0.y * e1);
-        s[2 * pg + 1].x = fmaf(k1.x, f0 * acc[2], k1.y * e0);
-        s[2 * pg + 1].y = fmaf(k1.x, f1 * acc[3], k1.y * e1);
+        // (f times acc might overflow where the key's scale brings it back)
+        s[2 * pg].x = fmaf(k0.x * f0, acc[0], k0.y * e0);
+        s[2 * pg].y = fmaf(k0.x * f1, acc[1], k0.y * e1);
+        s[2 * pg + 1].x = fmaf(k1.x * f0, acc[2], k1.y * e0);
+        s[2 * pg + 1].y = fmaf(k1.x * f1, acc[3], k1.y * e1);
       }
       const bool edge = key0 + kPair * kPageSize > lim_all;
       if (edge) {

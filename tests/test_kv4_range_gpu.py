@@ -213,3 +213,24 @@ def test_chunk_beside_rows_far_smaller(n_new, hq, d, keys, dtype, by):
     pool, bt = stored(k, v, dt)
     q = randn(2, n_new, hq, d, seed=3).to(dt)
     check_chunk(q, pool, bt, keys - n_new, 1 / math.sqrt(d), dt, (0, 1))
+
+
+@pytest.mark.parametrize("q_mul,k_mul,scale", [
+    (1e34, 1e-33, 0.01), (1e36, 1e-30, 1e-7), (1e-36, 1e33, 100.0), (1e-38, 1e30, 1e7)])
+@pytest.mark.parametrize("n_new,hq", [(0, 4), (0, 8), (2, 4), (7, 4), (60, 4)])
+def test_queries_near_the_ends_of_the_range(n_new, hq, q_mul, k_mul, scale):
+    """Products of bf16 queries and keys far outside fp16's range, of ordinary scores: decode
+    (n_new = 0), 8, 28 and 240 rows a kv head."""
+    dt, d, keys = torch.bfloat16, 128, 500
+    pool, bt = stored(randn(keys, 1, d, seed=1) * k_mul, randn(keys, 1, d, seed=2), dt)
+    q = (randn(2, max(n_new, 1), hq, d, seed=3) * q_mul).to(dt)
+    if n_new:
+        check_chunk(q, pool, bt, keys - n_new, scale, dt, (0, 1))
+        return
+    got = pa.decode_kv4(q[:, 0].contiguous(), pool, bt.expand(2, -1).contiguous(),
+                        torch.full((2,), keys, dtype=torch.int32, device="cuda"), scale)
+    for b in (0, 1):
+        want, _ = attend(q[b], pool, bt, [keys], scale, dt)
+        # 12 roundings of 2^-23 of a score whose terms add up to at most 200 in powers of two
+        err = (got[b].double() - want[0]).norm(dim=-1) / want[0].norm(dim=-1)
+        assert err.max() <= 12 * 200 * 2.0 ** -23, float(err.max())
