@@ -11,6 +11,11 @@
 // K and V of a page sit side by side, so a decode step fetches both with one
 // bulk copy; at head_dim 128 a block is 2176 bytes (17 lines of 128), at 64
 // 1152 (9 lines), 3.76 / 3.56 times less than in 16 bits.
+//
+// These kernels start while the kernel before them in the stream still runs, and wait for
+// it before they read.  What a kernel before may write (the blocks, tables, lengths,
+// angles) is therefore read by ordinary or L2 loads, never by ld.global.nc, which wants
+// memory that stays as it is for the kernel's whole life.
 #pragma once
 
 #include "pa_internal.h"

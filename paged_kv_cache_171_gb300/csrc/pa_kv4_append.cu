@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_rope_kernel(const Ap
         p.cos_sin + static_cast<size_t>(pos) * p.rot_dim);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float4 c = __ldg(row + 2 * t + k), s = __ldg(row + p.rot_dim / 8 + 2 * t + k);
+      const float4 c = row[2 * t + k], s = row[p.rot_dim / 8 + 2 * t + k];
       cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
       sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
     }
@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(kReadThreads) read_kv4_kernel(const ReadParams
         const uint32_t which = r >= heads, g = r - (which ? heads : 0);
         const int slot = slots[j];
         blk += g * static_cast<uint32_t>(kv4::block_bytes(D));
-        code[i] =
-            __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::code_offset(D, which, slot)) + t);
-        meta[i] = __ldg(reinterpret_cast<const uint32_t *>(blk + kv4::meta_offset(D, which, slot)));
+        auto word = [&](int at) { return reinterpret_cast<const uint32_t *>(blk + at); };
+        code[i] = __ldcg(word(kv4::code_offset(D, which, slot)) + t);
+        meta[i] = __ldcg(word(kv4::meta_offset(D, which, slot)));
         dst[i] = reinterpret_cast<uint4 *>(which ? p.v_out : p.k_out) +
                  (static_cast<size_t>(j0 + j) * heads + g) * TPR + t;
       }

@@ -182,7 +182,7 @@ struct TileWalk {
 
   static __device__ int ctx_of(const PrefillParams &p, int b, bool report) {
     const int most = p.max_blocks * kPageSize - p.n_new;
-    int t = __ldg(p.ctx_lens + b);
+    int t = p.ctx_lens[b];
     if (t < 0 || t > most) {
       if (report) record_error(p.status, PA_ERR_BAD_CTX);
       t = t < 0 ? 0 : most;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
   auto ids_of = [&](int v) {
     const int t = c + (16 * v + (lane >> 1)) * step;
     const int pg = (part.t0 + t) * kPagesTile + 2 * w + (lane & 1);
-    return t < part.nt && pg < n_pages ? __ldg(bt_row + pg) : 0;
+    return t < part.nt && pg < n_pages ? bt_row[pg] : 0;
   };
   int ids = ids_of(0), ids_next = ids_of(1);
   int issued = 0;  // the warp's pages, 2 a tile; page i sits in ring slot i % kRawPages

@@ -188,7 +188,7 @@ struct Walk {
   // the first team's scan).
   static __device__ int tokens_of(const RowsParams &p, int b, bool report) {
     const int most = p.max_blocks * kPageSize - p.n_new;
-    int t = __ldg(p.ctx_lens + b);
+    int t = p.ctx_lens[b];
     if (t < 0 || t > most) {
       if (report) record_error(p.status, PA_ERR_BAD_CTX);
       t = t < 0 ? 0 : most;
@@ -291,7 +291,7 @@ struct Feed {
   // Lane l holds the id of page l & 1 of chunk 16 w + (l >> 1), w the window.
   static __device__ int fetch_ids(const int32_t *row, int pages, int w, int lane) {
     const int pg = kWarps * kPair * (16 * w + (lane >> 1)) + (lane & 1);
-    return pg < pages ? __ldg(row + pg) : 0;
+    return pg < pages ? row[pg] : 0;
   }
   static __device__ const int32_t *row_of(const RowsParams &p, const volatile Part &s, int warp) {
     return p.block_table + static_cast<size_t>(s.b) * p.max_blocks + s.pg0 + kPair * warp;
