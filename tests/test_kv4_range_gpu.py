@@ -64,25 +64,31 @@ def attend(q, pool, bt, seen, scale, dt):
     return out, r
 
 
+def assert_rows(got, want, r, dt):
+    """A chunk's rows [nq, Hq, D] against `attend`'s.  A row's error, in the norm: half a step
+    of the result's type of the row; and, a key, the roundings of its terms, each at most U =
+    2^-11 relatively: of the weight, and in bf16 of V (twice, the second time of its row's
+    least value, up to 3 times a typical one) and of K (alike, where a score of N(0, 1)
+    products moves by as much as a product).  Independent ones add up to
+    sqrt(1 + 10 + 10) U R / sqrt(3) < 3 U R, for fp16 U R / sqrt(3); 2.5 times that are
+    allowed.  An element below the type's normal range is off by up to half a step there,
+    smallest_normal eps / 2, whatever its size: sqrt(D) of them."""
+    half, most = torch.finfo(dt).eps / 2, (8 if dt is torch.bfloat16 else 1.5) * U
+    err, size = (got.double() - want).norm(dim=-1), want.norm(dim=-1)
+    tol = half * (size + math.sqrt(want.shape[-1]) * torch.finfo(dt).smallest_normal) + most * r
+    assert (err <= tol).all(), (float((err / size).max()), float((err / tol).max()))
+
+
 def check_chunk(q, pool, bt, ctx, scale, dt, look):
     """q [B, n_new, Hq, D] over the one sequence of `bt`, in B sequences; those of `look`
-    are compared.  A row's error, in the norm: half a step of the result's type of the row;
-    and, a key, the roundings of its terms, each at most U = 2^-11 relatively: of the weight,
-    and in bf16 of V (twice, the second time of its row's least value, up to 3 times a typical
-    one) and of K (alike, where a score of N(0, 1) products moves by as much as a product).
-    Independent ones add up to sqrt(1 + 10 + 10) U R / sqrt(3) < 3 U R, for fp16 U R / sqrt(3);
-    2.5 times that are allowed.  An element below the type's normal range is off by up to half
-    a step there, smallest_normal eps / 2, whatever its size: sqrt(D) of them."""
+    are compared."""
     B, n_new, hq, d = q.shape
     tokens = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
     got = pa.prefill_kv4(q, pool, bt.expand(B, -1).contiguous(), tokens, scale)
     assert pa.pa_last_device_error() == 0
-    half, most = torch.finfo(dt).eps / 2, (8 if dt is torch.bfloat16 else 1.5) * U
     for b in look:
         want, r = attend(q[b], pool, bt, [ctx + i + 1 for i in range(n_new)], scale, dt)
-        err = (got[b].double() - want).norm(dim=-1)
-        tol = half * (want.norm(dim=-1) + math.sqrt(d) * torch.finfo(dt).smallest_normal) + most * r
-        assert (err <= tol).all(), (b, float((err / want.norm(dim=-1)).max()), float((err / tol).max()))
+        assert_rows(got[b], want, r, dt)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -234,3 +240,36 @@ def test_queries_near_the_ends_of_the_range(n_new, hq, q_mul, k_mul, scale):
         # 12 roundings of 2^-23 of a score whose terms add up to at most 200 in powers of two
         err = (got[b].double() - want[0]).norm(dim=-1) / want[0].norm(dim=-1)
         assert err.max() <= 12 * 200 * 2.0 ** -23, float(err.max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,n_new,ctx,d", [
+    (8, 2, 4, [0, 15, 16, 1000], 128), (8, 2, 7, [100, 0], 128), (4, 4, 17, [3, 200], 64),
+    (7, 1, 5, [129, 1, 127], 128), (12, 4, 33, [0, 31], 64), (24, 1, 2, [77, 500], 128),
+    (8, 1, 130, [0, 260], 128), (32, 8, 64, [500], 64), (7, 1, 150, [0, 127, 128], 128),
+    (2, 2, 257, [0, 1000], 64), (16, 4, 6, [5000, 0, 130, 9000, 64, 2, 127, 128] + [40] * 60, 128),
+    (16, 4, 70, [3000, 0, 130, 1, 6000], 128), (16, 4, 20, [20000, 3], 64)])
+def test_every_row_of_a_chunk(hq, hkv, n_new, ctx, d, dtype):
+    """Head layouts, ragged batches and items cut between runs, row by row."""
+    dt, scale = DT[dtype], 1 / math.sqrt(d)
+    lens = [t + n_new for t in ctx]
+    blocks = [-(-t // 16) for t in lens]
+    gen = torch.Generator(device="cuda").manual_seed(n_new)
+    perm = torch.randperm(sum(blocks) + 2, generator=gen, device="cuda").to(torch.int32)
+    bt = torch.full((len(lens), max(blocks)), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(blocks):
+        bt[b, :n] = perm[sum(blocks[:b]):sum(blocks[:b]) + n]
+    # what no token has written: any codes, NaN scales and zeros
+    pool = torch.randint(0, 256, (sum(blocks) + 2, hkv, ref.block_bytes(d)), generator=gen,
+                         device="cuda").to(torch.uint8)
+    pool[:, :, 16 * d:] = 255
+    seq = torch.cat([torch.full((t,), b, device="cuda") for b, t in enumerate(lens)])
+    pos = torch.cat([torch.arange(t, device="cuda") for t in lens])
+    ref.store(pool, bt, seq, pos, randn(len(pos), hkv, d, seed=1), randn(len(pos), hkv, d, seed=2), dt)
+    q = randn(len(lens), n_new, hq, d, seed=3).to(dt)
+    got = pa.prefill_kv4(q, pool, bt, torch.tensor(ctx, dtype=torch.int32, device="cuda"), scale)
+    assert pa.pa_last_device_error() == 0
+    for b, t in enumerate(ctx):
+        seen = [t + i + 1 for i in range(n_new)]
+        want, r = attend(q[b], pool, bt[b:b + 1, :blocks[b]], seen, scale, dt)
+        assert_rows(got[b], want, r, dt)
