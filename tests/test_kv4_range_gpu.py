@@ -273,3 +273,27 @@ def test_every_row_of_a_chunk(hq, hkv, n_new, ctx, d, dtype):
         seen = [t + i + 1 for i in range(n_new)]
         want, r = attend(q[b], pool, bt[b:b + 1, :blocks[b]], seen, scale, dt)
         assert_rows(got[b], want, r, dt)
+
+
+@pytest.mark.parametrize("n_new", [7, 40, 100])
+def test_rows_that_are_not_finite_beside_far_larger_ones(n_new):
+    """A NaN row of the chunk among 32 keys that span a wide range: the queries before it are
+    as without it, the others NaN."""
+    dt, d, ctx, at = torch.bfloat16, 128, 60, 3
+    k, v = randn(ctx + n_new, 1, d, seed=1), randn(ctx + n_new, 1, d, seed=2)
+    k[50] *= 2000
+    v[40] *= 3e4
+    v[52] = 0
+    pool, bt = stored(k, v, dt)
+    q = randn(1, n_new, 4, d, seed=3).to(dt)
+    tokens = torch.full((1,), ctx, dtype=torch.int32, device="cuda")
+    clean = pa.prefill_kv4(q, pool, bt, tokens, 0.09)
+    assert torch.isfinite(clean).all()
+    page, slot = int(bt[0, (ctx + at) // 16]), (ctx + at) % 16
+    for which in (0, 1):
+        bad = pool.clone()
+        bad[page, 0, 16 * d + (which * 16 + slot) * 4:][:4] = 255  # NaN scale and zero
+        got = pa.prefill_kv4(q, bad, bt, tokens, 0.09)
+        assert torch.equal(got[:, :at], clean[:, :at])
+        assert torch.isnan(got[:, at:]).all()
+    assert pa.pa_last_device_error() == 0
