@@ -35,6 +35,11 @@ __host__ __device__ constexpr int meta_offset(int head_dim, int which, int slot)
   return 16 * head_dim + (which * kPageSize + slot) * 4;
 }
 
+// a / b of numbers that are not negative; 64-bit division only where 32 bits do not hold them.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 }  // namespace kv4
 
 // The rows of an append: token j's K row of head g is k_new[j * k_stride + g *

@@ -200,9 +200,6 @@ struct TileWalk {
     for (int k = 0; k < p.n_items; ++k) n += units_of(p, ctx, k);
     return n;
   }
-  static __device__ int64_t quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-  }
   // The whole warp; lane 0 keeps the result in *out.  False: no run.
   static __device__ bool start(const PrefillParams &p, int lane, TileWalk *out) {
     TileWalk x;
@@ -217,7 +214,7 @@ struct TileWalk {
       if (lane >= o) incl += v;
     }
     const int64_t total = __shfl_sync(kFull, incl, 31) * p.n_kv_heads;
-    x.run = quotient(total + gridDim.x - 1, gridDim.x);
+    x.run = kv4::quotient(total + gridDim.x - 1, gridDim.x);
     x.w = blockIdx.x * x.run;
     x.w1 = min(total, x.w + x.run);
     if (x.w >= x.w1) return false;
@@ -236,7 +233,7 @@ struct TileWalk {
       per_head = head_units(p, ctx);
     }
     const int64_t rel = w - base;
-    const int g = static_cast<int>(quotient(rel, per_head));
+    const int g = static_cast<int>(kv4::quotient(rel, per_head));
     int u0 = static_cast<int>(rel - static_cast<int64_t>(g) * per_head), k = 0, n;
     while (u0 >= (n = units_of(p, ctx, k))) {
       u0 -= n;
@@ -251,8 +248,8 @@ struct TileWalk {
     s.ctx = ctx;
     s.t0 = max(0, u0 - p.part_tiles);
     s.nt = u1 - p.part_tiles - s.t0;  // (below 1: the run ends before the item's tiles begin)
-    s.first = static_cast<int>(quotient(i0 + p.part_tiles, run));
-    s.last = static_cast<int>(quotient(i0 + n - 1, run));
+    s.first = static_cast<int>(kv4::quotient(i0 + p.part_tiles, run));
+    s.last = static_cast<int>(kv4::quotient(i0 + n - 1, run));
     s.slot = i0 <= s.first * run ? 0 : 1;
     w = i0 + u1;
     s.more = w + p.part_tiles < w1;
@@ -302,15 +299,6 @@ __device__ __forceinline__ float exp2i(int k) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // Converter warp w of group c: keys 32 w .. 32 w + 31 (two pages) of the key tiles c,
 // c + step, .., K then V, and their references and, in the exact form, scales and zeros.
 // The pages come through a ring of the warp's own, by bulk copies 1.5 tiles ahead.
@@ -321,8 +309,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 template <int D, bool BF16, bool EXACT>
 __device__ __forceinline__ void convert_tiles(int c, int step, int w, const PrefillParams &p,
                                               const TilePart &part, uint32_t sb, uint32_t bars,
-                                              uint8_t *smem, const Tiling &tl, volatile int *abort_flag,
-                                              int lane) {
+                                              uint8_t *smem, const Tiling &tl,
+                                              volatile int *abort_flag, int lane) {
   using L = PrefillSmem<D>;
   constexpr int kBlock = kv4::block_bytes(D);
   constexpr int kPieces = D / 32;                // 16-byte pieces of a row's codes
@@ -617,10 +605,11 @@ __device__ __forceinline__ void row_tiles_sync() {  // both softmax warpgroups
 
 // Softmax warpgroup x: lane l of warp w owns row 32 (w mod 4) + l of row tile x.
 template <int D, bool BF16, bool EXACT, bool FEW>
-__device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const volatile TilePart &part, int x,
-                                              const Tiling &tl, uint32_t sb, uint32_t bars, uint32_t tmem,
-                                              uint8_t *smem, volatile int *abort_flag,
-                                              int warp, int lane) {
+__device__ __forceinline__ void softmax_tiles(const PrefillParams &p,
+                                              const volatile TilePart &part, int x,
+                                              const Tiling &tl, uint32_t sb, uint32_t bars,
+                                              uint32_t tmem, uint8_t *smem,
+                                              volatile int *abort_flag, int warp, int lane) {
   using L = PrefillSmem<D>;
   auto bar = [&](int i) { return bars + 8 * i; };
   const int r = ((warp & 3) << 5) + lane;
@@ -868,11 +857,11 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p, const vola
 }
 
 // Row tile x of Q in the operand's order of dimensions, zeros past the rows (FEW: in
-// the warps that have some; the others' S is not looked at), by 128 threads; not exact: as fp16 over a power of two a row, whose product with the score
-// factor goes to kRowF.  A thread copies chunks to where they belong and then turns its
-// own in place.  The loops are hardly unrolled: this runs once a part, and
-// straight-line code waits for its own instructions (measured 10 us a part with all 16
-// chunks unrolled, 4 so).
+// the warps that have some; the others' S is not looked at), by 128 threads; not exact:
+// as fp16 over a power of two a row, whose product with the score factor goes to kRowF.
+// A thread copies chunks to where they belong and then turns its own in place.  The loops
+// are hardly unrolled: this runs once a part, and straight-line code waits for its own
+// instructions (measured 10 us a part with all 16 chunks unrolled, 4 so).
 template <int D, bool BF16, bool EXACT, bool FEW>
 __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile TilePart &part,
                                        bool split, int x, uint32_t sb, uint8_t *smem, int th) {
@@ -1138,7 +1127,8 @@ int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
   }
   if (launch_pdl(kern, dim3(ctas), dim3(kThreads), PrefillSmem<D>::kAlloc, stream, p) !=
           cudaSuccess ||
-      launch_pdl(kv4_prefill_fold_kernel<D, BF16>, dim3(ctas, (min(p.n_rows, kItemRows) + kFoldRows - 1) / kFoldRows),
+      launch_pdl(kv4_prefill_fold_kernel<D, BF16>,
+                 dim3(ctas, (min(p.n_rows, kItemRows) + kFoldRows - 1) / kFoldRows),
                  dim3(kFoldRows * D / 4), 0, stream, p) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;

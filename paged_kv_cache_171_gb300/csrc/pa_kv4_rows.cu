@@ -113,15 +113,6 @@ struct RowsSmem {
   static_assert(kTeam % 128 == 0 && kBytes <= 232448, "shared memory of an SM");
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -201,10 +192,6 @@ struct Walk {
   }
   // Units of an item in the list: its pages behind kPartPages of its own.
   static __device__ int units_of(int tokens) { return pages_of(tokens) + kPartPages; }
-  // 64-bit division only where 32 bits do not hold the operands.
-  static __device__ int64_t quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-  }
   // The whole warp: lane l sums the pages of sequences [l per, (l + 1) per), and a
   // scan finds the sequence in which the team's run starts.  False: no run.
   // Warp-uniform results; lane 0 keeps them in *out.
@@ -228,7 +215,7 @@ struct Walk {
       if (lane >= o) incl += v;
     }
     const int64_t total = __shfl_sync(kFull, incl, 31) * heads;
-    x.run = max(quotient(total + n_teams - 1, n_teams), static_cast<int64_t>(kMinPages));
+    x.run = max(kv4::quotient(total + n_teams - 1, n_teams), static_cast<int64_t>(kMinPages));
     x.w = team * x.run;
     x.w1 = min(total, x.w + x.run);
     if (x.w >= x.w1) return false;
@@ -249,14 +236,14 @@ struct Walk {
       n_b = units_of(tokens);
     }
     const int64_t rel = w - base * heads;
-    const int item = static_cast<int>(quotient(rel, n_b));
+    const int item = static_cast<int>(kv4::quotient(rel, n_b));
     int u0 = static_cast<int>(rel - static_cast<int64_t>(item) * n_b);
     const int64_t i0 = w - u0;  // the item's first unit
     if (u0 <= kPartPages) u0 = 0;  // a boundary in an item's own units lies before it
     const int pg0 = max(0, u0 - kPartPages);
     const int u1 = static_cast<int>(min(static_cast<int64_t>(n_b), w1 - i0));
     const int g = item / p.n_sub, sub = item - g * p.n_sub;
-    const int first = static_cast<int>(quotient(i0 + kPartPages, run));
+    const int first = static_cast<int>(kv4::quotient(i0 + kPartPages, run));
     s.b = b;
     s.g = g;
     s.r0 = sub * p.tile_rows;
@@ -265,7 +252,7 @@ struct Walk {
     s.n_pg = u1 - kPartPages - pg0;
     s.tokens = tokens;
     s.first = first;
-    s.last = static_cast<int>(quotient(i0 + n_b - 1, run));
+    s.last = static_cast<int>(kv4::quotient(i0 + n_b - 1, run));
     s.slot = i0 <= first * run ? 0 : 1;
     w = i0 + u1;
     s.more = w + kPartPages < w1;
@@ -720,7 +707,8 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
         const float2 back = unpack2<false>(head);
         if constexpr (WIDE) {
           hi[u] = transpose8x8(head);
-          lo[u] = transpose8x8(pack2<false>((wt.x - back.x) * kRemLift, (wt.y - back.y) * kRemLift));
+          lo[u] = transpose8x8(
+              pack2<false>((wt.x - back.x) * kRemLift, (wt.y - back.y) * kRemLift));
         } else {  // the head term again, or the remainder
           const float2 mine = __ffma2_rn(make_float2(rem, rem), back,
                                          __fmul2_rn(wt, make_float2(lift, lift)));
