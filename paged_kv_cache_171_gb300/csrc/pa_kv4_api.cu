@@ -54,12 +54,21 @@ int append(AppendRopeLaunch &a, int page_size, int dtype, pa_stream_t stream) {
 // Whether a chunk goes to the tile kernel: by its rows (queries x group) a kv head.
 // The row kernel turns the codes once for 8 of them, the tile kernel once for 256, at
 // the price of whole operand tiles; fp16's tile form is the slower one.  Rows against
-// tiles in us, head_dim 128, rows a kv head across:
-//                                     16         24         32         64
-//   bf16  4 x 32768, 8 kv heads    97 /  95  132 /  96  168 /  95  304 /  97
-//         16 x 2000, 8 kv heads    34 /  44   43 /  45   52 /  45   90 /  45
-//   fp16  4 x 32768, 8 kv heads    97 / 132  133 / 132  168 / 134  303 / 135
-//         16 x 2000, 8 kv heads    34 /  54   43 /  54   52 /  53   90 /  54
+// tiles in us, 8 kv heads, rows a kv head across:
+//                                 8        16        24        32        64
+//   bf16  4 x 32768, 128    52 /  84  85 /  85  119 /  85  153 /  85  290 /  86
+//         4 x 32768, 64     35 /  67  56 /  68   77 /  68   98 /  68  184 /  68
+//         16 x 2000, 128    21 /  33  32 /  35   40 /  35   49 /  35   86 /  38
+//         16 x 2000, 64     15 /  27  22 /  28   28 /  28   33 /  28   56 /  29
+//         8 x 700, 128      12 /  17  15 /  17   18 /  18   18 /  18   30 /  18
+//         1 x 300, 128      10 /  12  11 /  12   11 /  12   11 /  13   11 /  14
+//   fp16  4 x 32768, 128    51 / 124  85 / 125  118 / 126  152 / 126  288 / 127
+//         4 x 32768, 64     35 /  98  56 /  98   76 /  99   98 /  99  184 /  99
+//         16 x 2000, 128    21 /  44  32 /  45   40 /  45   49 /  45   86 /  46
+//         16 x 2000, 64     15 /  35  22 /  35   28 /  35   33 /  36   56 /  36
+//         8 x 700, 128      12 /  21  15 /  21   18 /  22   18 /  22   30 /  22
+//         1 x 300, 128      10 /  12  10 /  13   11 /  13   10 /  14   11 /  15
+// (Lengths are not known to the host: a short context may take 4 us more than it need.)
 bool wants_tiles(int n_new, int n_q_heads, int n_kv_heads, bool bf16) {
   return n_new > 0 &&
          static_cast<int64_t>(n_new) * (n_q_heads / n_kv_heads) > (bf16 ? 16 : 24);

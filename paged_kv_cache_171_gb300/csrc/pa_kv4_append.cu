@@ -24,7 +24,8 @@
 // of one dependent chain), 4 once there are enough rows to fill the GPU.
 // Small CTAs at 80 registers keep 24 warps an SM and the last wave short: 4 x 512 tokens
 // 12.4 -> 11.0 us against CTAs of 256 at the compiler's 95, 4 x 2048 quantised and read
-// back 55.6 -> 48.3; at 64 registers the rows spill (17.4, 51.5).
+// back 55.6 -> 48.3, although the quantising form spills some (56 bytes stored, 72 to 96
+// loaded a thread); at 64 registers 17.4 and 51.5.
 // Measured: rotation alone, 4 x 512 tokens of 32 / 8 heads of 128: 11.0 us a call
 // (51.4 MB, 4.7 TB/s); 8191 tokens of 16 / 16 heads of 64: 19.9 us (101.7 MB, 5.1
 // TB/s).  Quantising 4 x 2048 tokens (32 / 8 heads of 128): 37 us for 169 MB, where
@@ -203,8 +204,10 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_rope_kernel(const Ap
       uint32_t zb = round16<BF16>(__fmaf_rn(8.f, s, mn), z);
       const bool fine = fabsf(range) <= FLT_MAX && fabsf(s) <= FLT_MAX && fabsf(z) <= FLT_MAX;
       if (!fine) sb = zb = BF16 ? 0x7fc0u : 0x7e00u;
-      // (x - z) / s by the reciprocal, within 2^-21 of the quotient; a row with an
-      // element that near the border between two codes is divided out
+      // (x - z) / s by the reciprocal, off by two half steps, 2^-23 of the quotient: at
+      // most 2^-20 up to 8, and a larger one (the zero's own rounding against a small
+      // scale) is clamped.  A row with an element within 1e-4 of the border between two
+      // codes is divided out.
       const bool step = fine && s > 0.f;
       const float inv = step ? __fdiv_rn(1.f, s) : 0.f;
       float c[16];

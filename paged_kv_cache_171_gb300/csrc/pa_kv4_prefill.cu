@@ -41,7 +41,7 @@
 // overlaps the other's products.  At the end A reads both O's (the lanes hold the same
 // rows) and merges the two states.  Of at most 64 rows, the softmax warps of the upper
 // rows have none: these four turn the odd key tiles' codes, the converters the even ones'
-// (4 x 4 queries, 64 / 8 heads, over 32k keys: 114 -> 102 us).
+// (4 x 4 queries, 64 / 8 heads, over 32k keys: 114 -> 102 us when it came in).
 //
 // Warp roles (one CTA an SM): warps 0 and 1 issue the MMAs of row tiles A and B, warps
 // 4-7 turn codes into the K and V operand tiles (two stages each): a warp 32 keys of
@@ -61,10 +61,11 @@
 // between CTAs leaves an fp32 state (O, m, l) a row and CTA, folded by a second kernel.
 //
 // Bound.  A long chunk: the chain of a key tile, from the codes over S and the softmax
-// to P V (tensor pipe 43% busy, issue 47%): 4 x 512 queries of 32 / 8 heads over 8192
-// tokens, bf16 285 us (2.84e11 operations, 0.99 PFLOP/s), fp16 495 us, whose softmax
-// reads 16 bytes a key and thread from shared memory.  Few rows: turning the codes (4 x 4
-// queries of 64 / 8 heads over 32k tokens 89 us, 1.6 TB/s of codes).
+// to P V (tensor pipe 45% busy, issue 49%): 4 x 512 queries of 32 / 8 heads over 8192
+// tokens, bf16 278 us (2.84e11 operations, 1.02 PFLOP/s), where every 32 keys span a wide
+// range 462; fp16 476 us, whose softmax reads 16 bytes a key and thread from shared memory
+// (tensor 27%, issue 40%).  Few rows: turning the codes (4 x 4 queries of 64 / 8 heads over
+// 32k tokens 86 us, 1.7 TB/s of codes; wide 144; fp16 126).
 #include <float.h>
 
 #include <atomic>
@@ -1172,9 +1173,9 @@ int launch_kv4_tiles(const Kv4AttentionLaunch &a, cudaStream_t stream) {
   p.num_pages = a.num_pages;
   p.n_rows = a.n_new * p.group;
   p.n_items = (p.n_rows + kItemRows - 1) / kItemRows;
-  // Us for 0, 1, 2, 4 tiles more: 4 x 32 queries of 64 / 8 heads over 32k tokens 162, 161,
-  // 157, 153, 4 x 512 of 32 / 8 heads over 8192 within 1%; up to 64 rows, whose tiles are
-  // the shorter ones, for 3, 6, 10, 14: 96, 93, 97, 98.
+  // Us for 0, 1, 2, 4 tiles: 4 x 32 queries of 64 / 8 heads over 32k tokens 151, 149, 147,
+  // 143, 4 x 512 of 32 / 8 over 8192 within 1%; up to 64 rows, whose tiles are the shorter
+  // ones, for 3, 6, 10, 14: 87, 86, 87, 88.
   p.part_tiles = p.n_rows <= kRows / 2 ? 6 : 4;
   p.page_bytes = static_cast<uint32_t>(a.n_kv_heads) * kv4::block_bytes(a.head_dim);
   if (a.head_dim == 128)

@@ -39,13 +39,15 @@
 // product's operand (row, token) by movmatrix.  The sums of each two pages are taken in
 // an accumulator of their own and added to the state with a rounding add, because the
 // tensor cores' roundings toward zero add up along a long context (measured on 32k
-// tokens, 8 rows: error 9e-6 of the result in one accumulator, 8e-7 so).
+// tokens, 8 rows, with c - 8: error 9e-6 of the result in one accumulator, 8e-7 so; with
+// c - 7.5 2e-7).
 //
 // Work split.  The pages of all (sequence, kv head, row tile) items, laid end to
 // end, are cut into equal runs: a ragged batch takes the time of its pages, not of
 // its longest sequence.  An item counts 12 pages more than it has, for what starting
-// and merging it costs (64 sequences of 128 to 8192 tokens: 97 -> 86 us; 3, 6, 10 and 16
-// pages took 89, 88, 89 and 85).  A run belongs to a team of 4 warps, and an SM holds 4
+// and merging it costs (64 sequences of 128 to 8192 tokens: 97 -> 86 us when it came in;
+// 3, 6, 10, 12 and 16 pages now take 80, 81, 82, 82 and 76 there, and 60, 51, 52, 52 and
+// 53 for 4 x 32768 of 64 / 8 heads).  A run belongs to a team of 4 warps, and an SM holds 4
 // teams in one CTA, so that they can keep step (below).  A team's warps take its
 // run's pages two by two in turn, each with its own ring of stages filled by bulk
 // copies, and merge their (m, l, O) states when an item ends.  An item cut between
@@ -53,12 +55,12 @@
 // (results do not depend on timing).  Runs go round the SMs, so that a call with few
 // of them has one an SM (1 x 512 tokens of 16 heads: 21.0 -> 14.8 us of device time).
 //
-// Bound: issue.  Turning a page's codes is some 150 of about 300 warp instructions;
-// 61% of the issue slots and 58% of the ALU's are taken, DRAM 41%.  Decode at head_dim
-// 128, a call: 8 x 4096 tokens of 32 / 32 heads 44.5 us (143 MB, 3.2 TB/s), 64
-// sequences of 128 to 8192 of 32 / 8 heads 83 us (287 MB, 3.4 TB/s), 4 x 32768 of 64 /
-// 8 heads 51 us (143 MB, 2.8 TB/s); the 16-bit cache's bytes alone would take 79, 159
-// and 79 us at the copy's bandwidth.
+// Bound: issue.  Turning a page's codes is some 150 of about 410 warp instructions a page
+// (planning and merging included); 61% of the issue slots and 52% of the ALU's are taken,
+// DRAM 43%.  Decode at head_dim 128, a call: 8 x 4096 tokens of 32 / 32 heads 42.2 us
+// (143 MB, 3.4 TB/s), 64 sequences of 128 to 8192 of 32 / 8 heads 81 us (287 MB, 3.5
+// TB/s), 4 x 32768 of 64 / 8 heads 51 us (143 MB, 2.8 TB/s); the 16-bit cache's bytes
+// alone would take 79, 159 and 79 us at the copy's bandwidth.
 #include "pa_device.cuh"
 #include "pa_kv4.cuh"
 
@@ -849,7 +851,7 @@ __global__ void __launch_bounds__(kTeams * kWarps * 32, 1)
 // folded by GROUPS groups of threads, a thread a (row, 4 dimensions), a few states a
 // step; group g takes states g, g + GROUPS, ..  One group, one CTA a team; or, where
 // few items have many states each, kTeams of each, so that a round of loads takes them
-// all (4 sequences of 32k tokens, 8 heads, 20 states: the decode took 55 us, now 51).
+// all (launch_rows_t).
 template <int D, bool BF16, bool OUT16, int GROUPS>
 __global__ void __launch_bounds__(GROUPS * kTile * D / 4) kv4_fold_kernel(const RowsParams p) {
   constexpr int kBatch = GROUPS > 1 ? 5 : 4, kState = kTile * (D + 4), kRowD = kTile * D / 4;
@@ -924,8 +926,14 @@ int launch_rows_t(const RowsParams &p, int ctas, cudaStream_t stream) {
   if (launch_pdl(kern, dim3(ctas), dim3(kTeams * kWarps * 32), RowsSmem<D>::kBytes, stream, p) !=
           cudaSuccess)
     return PA_ERR_CUDA;
-  // a CTA of kTeams groups looks after kTeams runs: worth it with at most one item a CTA
-  const bool few = static_cast<int64_t>(p.batch) * p.n_kv_heads * p.n_sub <= ctas;
+  // A CTA of kTeams groups looks after kTeams runs: worth it from about 20 states an item.
+  // One group against kTeams, us a call (head_dim 128):
+  //   76 states  1 x 131072 tokens, 8 / 1 heads  87.5 / 52.4   1 x 32768, 32 / 8  26.9 / 21.3
+  //   38         2 x 16384, 64 / 8               24.8 / 23.0
+  //   19         4 x 32768, 64 / 8               51.1 / 52.2   4 x 8192, 32 / 8   19.9 / 19.1
+  //   10         4 x 2 queries over 32768, 64 / 8  84.8 / 92.0
+  const bool few = static_cast<int64_t>(p.batch) * p.n_kv_heads * p.n_sub * 20 <=
+                   static_cast<int64_t>(ctas) * kTeams;
   const cudaError_t e =
       few ? launch_pdl(kv4_fold_kernel<D, BF16, OUT16, kTeams>, dim3(ctas),
                        dim3(kTeams * kTile * D / 4), 0, stream, p)
