@@ -8,10 +8,14 @@
 // tile is turned into operand tiles once for 256 query rows.
 //
 // Two forms, by the cache's type (EXACT below):
-//  * bf16: the converters store zero + scale (c - 8) as fp16, over a power of two above
-//    the largest magnitude of 32 keys (k_ref, v_ref).  K and V are then off by two half
-//    steps of 2^-11 and P by one, well below the bf16 result's own rounding of 2^-8, and
-//    the softmax works on S as it comes: a factor for each 32 keys in its exponent.
+//  * bf16: the converters store scale (c - 8) of K, which fp16 holds exactly (8 bits times
+//    3), and zero + scale (c - 8) of V, over a power of two above the largest magnitude of
+//    32 keys (k_ref, v_ref).  zero_k sum q comes out of the same product: 16 columns more,
+//    of which K has the zero twice and Q the sum in two terms.  So S is exact to fp32's
+//    last bits (with K rounded like V, the error in the weights grew with the scores: rows
+//    at scores of N(0, 10) were up to 1.1% off, now 0.24%); V is off by two half steps of
+//    2^-11 and P by one, well below the bf16 result's own rounding of 2^-8; and the softmax
+//    works on S as it comes: a factor for each 32 keys in its exponent.
 //    Operands reach up to 2^-7 in fp16, which has all its bits down to 2^-14: where a
 //    key's largest magnitude is below 2^-5 of the reference, that is lowered by as much
 //    (K's by 2^15 at most, V's by 2^11, which P gives up), and each key is converted over
@@ -62,10 +66,10 @@
 //
 // Bound.  A long chunk: the chain of a key tile, from the codes over S and the softmax
 // to P V (tensor pipe 45% busy, issue 49%): 4 x 512 queries of 32 / 8 heads over 8192
-// tokens, bf16 278 us (2.84e11 operations, 1.02 PFLOP/s), where every 32 keys span a wide
-// range 462; fp16 476 us, whose softmax reads 16 bytes a key and thread from shared memory
-// (tensor 27%, issue 40%).  Few rows: turning the codes (4 x 4 queries of 64 / 8 heads over
-// 32k tokens 86 us, 1.7 TB/s of codes; wide 144; fp16 126).
+// tokens, bf16 288 us (2.84e11 operations, 0.99 PFLOP/s); fp16 468 us, whose softmax reads
+// 16 bytes a key and thread from shared memory (tensor 27%, issue 40%).  Few rows: turning
+// the codes (4 x 4 queries of 64 / 8 heads over 32k tokens 86 us, 1.7 TB/s of codes; fp16
+// 126).  Where every 32 keys span a wide range, the bf16 calls take 474 and 146 us.
 #include <float.h>
 
 #include <atomic>
@@ -90,7 +94,6 @@ constexpr int kItemRows = 2 * kRows;
 constexpr int kStages = 2;                  // of K and of V
 constexpr int kConvertWarp0 = 4, kSoftmaxWarp0 = 8;
 constexpr int kThreads = 16 * 32;
-constexpr int kRawPages = 3;                // a converter warp's ring
 
 struct PrefillParams {
   const uint16_t *q;
@@ -108,24 +111,35 @@ struct PrefillParams {
   uint32_t page_bytes;
 };
 
-template <int D>
+template <int D, bool EXACT, bool FEW>
 struct PrefillSmem {
+  static constexpr int kRawPages = FEW ? 3 : 2;       // a converter warp's ring (below)
   static constexpr int kColBlk = kRows * 128;         // one 64-column block, 128 rows
   static constexpr int kTile = (D / 64) * kColBlk;    // 128 rows x D, 16 bits
   static constexpr int kQ = 0;                        // Q_A, Q_B
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
   // EXACT: per stage and pair of keys scale_k / 2 x2, mid_k x2 (both times qscale),
-  // scale_v / v_ref x2, mid_v x2.  Else kRowF: the factor of each row's S.
+  // scale_v / v_ref x2, mid_v x2.  Else the factor of each row's S.
   static constexpr int kMeta = kV + kStages * kTile;
-  static constexpr int kRowF = kMeta;
+  static constexpr int kMetaBytes = EXACT ? kStages * (kKeys / 2) * 32 : 2 * kRows * 4;
   // the converters' rings of pages: the first group's, and, where the two row tiles are
-  // one and Q_B not needed, the second group's
+  // one and Q_B not needed, the second group's (two pages a warp are enough while it turns
+  // a tile for 256 rows: 4 x 512 queries over 8192 tokens 277 us with three, 271 with two;
+  // for few rows 85 and 88)
   static constexpr int kRing = 4 * kRawPages * kv4::block_bytes(D);
-  static constexpr int kRaw = kMeta + kStages * (kKeys / 2) * 32, kRaw1 = kQ + kTile;
+  static constexpr int kRaw = kMeta + kMetaBytes, kRaw1 = kQ + kTile;
   static_assert(kRing <= kTile, "room in Q_B");
+  // Not EXACT: the 8 columns of zeros and sums behind Q's and K's, 16 bytes a row, and the
+  // zeros that stand for 8 more.
+  static constexpr int kExtra = EXACT ? 0 : kRows * 16;
+  static constexpr bool kInQ = FEW && kRing + (1 + kStages) * kExtra <= kTile;
+  static constexpr int kEnd = kRaw + kRing;
+  static constexpr int kQX = kInQ ? kRaw1 + kRing : kEnd;       // of Q_A, Q_B
+  static constexpr int kKX = kQX + (FEW ? 1 : 2) * kExtra;      // of the stages
+  static constexpr int kZeros = kInQ ? kEnd : kKX + kStages * kExtra;
   // per stage: k_ref of each 32 keys, then v_ref
-  static constexpr int kRef = kRaw + kRing;
+  static constexpr int kRef = kZeros + kExtra;
   static constexpr int kBars = kRef + kStages * 32;
   static constexpr int kSlot = kBars + 2 * 46 * 8;        // TMEM address, abort flag
   static constexpr int kPart = kSlot + 16;            // this part and the next
@@ -307,12 +321,13 @@ __device__ __forceinline__ float exp2i(int k) {
 // A row past the sequence's end stands for zeros (it may hold anything, and 0 * NaN is
 // NaN).  A key or value row that is not finite makes its key's score NaN, which
 // masking removes for the queries that do not see it, and its values zero.
-template <int D, bool BF16, bool EXACT>
+template <int D, bool BF16, bool EXACT, bool FEW>
 __device__ __forceinline__ void convert_tiles(int c, int step, int w, const PrefillParams &p,
                                               const TilePart &part, uint32_t sb, uint32_t bars,
                                               uint8_t *smem, const Tiling &tl,
                                               volatile int *abort_flag, int lane) {
-  using L = PrefillSmem<D>;
+  using L = PrefillSmem<D, EXACT, FEW>;
+  constexpr int kRawPages = L::kRawPages;
   constexpr int kBlock = kv4::block_bytes(D);
   constexpr int kPieces = D / 32;                // 16-byte pieces of a row's codes
   constexpr int kIters = kPageSize * kPieces / 32;  // pieces a lane and page
@@ -368,7 +383,7 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
     issued += max(0, n);
   };
   issue(2);
-  issue(1);
+  if constexpr (kRawPages > 2) issue(1);
 
   bool ok = true;
   int t = c;
@@ -440,7 +455,14 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
       const float2 own = which ? v : k;
       // over 2^7 ref: |scale| 2^24 is at most 2^14
       const uint32_t scales = pack2<false>(own.x * inv * 0x1p17f, own.x * inv * 0x1p13f);
-      const uint32_t zeros = pack2<false>(fmaf(-8.f, own.x, own.y) * inv * 0x1p-7f, 0.f);
+      // K's zero is not in its codes' operand but in the columns behind it
+      const uint32_t zeros =
+          pack2<false>(fmaf(-8.f, own.x, which ? own.y : 0.f) * inv * 0x1p-7f, 0.f);
+      if (!EXACT && !which) {
+        const float z = k.y * exp2i(-ref) * exp2i(span);
+        st_shared_v4(sb + L::kKX + s * L::kExtra + (32 * w + lane) * 16,
+                     pack2<false>(z, z * 0x1p-11f), 0, 0, 0);
+      }
       if (which) {
         // V's stage is free once the softmax has read these for the tile before in it
         float *refs = reinterpret_cast<float *>(smem + L::kRef) + 8 * s;
@@ -528,26 +550,31 @@ __device__ __forceinline__ void convert_tiles(int c, int step, int w, const Pref
 // MMA warp x (lane 0): S_x(0), then per key tile t: P_x(t) V_t in two key halves,
 // S_x(t + 1), which overwrites P_x in TMEM: MMAs of one thread run in order.  (Split key
 // tiles: t = x, x + 2, ..)
-template <int D, bool FEW>
+template <int D, bool EXACT, bool FEW>
 __device__ __forceinline__ void mma_tiles(int x, bool split, int nt, uint32_t sb, uint32_t bars,
                                           uint32_t tmem, int *status, volatile int *abort_flag,
                                           int lane) {
-  using L = PrefillSmem<D>;
+  using L = PrefillSmem<D, EXACT, FEW>;
   constexpr uint32_t kIdS = tc::idesc_f16(false, kRows, kKeys, false, false);
   constexpr uint32_t kIdO = tc::idesc_f16(false, kRows, D, false, true);
   auto bar = [&](int i) { return bars + 8 * i; };
   const uint64_t dq = tc::smem_desc_sw128(sb + L::kQ + (FEW ? 0 : x) * L::kTile, 16, 1024);
   const uint64_t dk0 = tc::smem_desc_sw128(sb + L::kK, 16, 1024);
   const uint64_t dv0 = tc::smem_desc_sw128(sb + L::kV, L::kColBlk, 1024);
+  // the columns behind: 8 of the tile, 8 of zeros (kZeros is behind the tiles)
+  auto extra = [&](int at) { return tc::smem_desc_plain(sb + at, L::kZeros - at, 128); };
+  const uint64_t dqx = extra(L::kQX + (FEW ? 0 : x) * L::kExtra);
+  const uint64_t dkx0 = extra(L::kKX), dkx1 = extra(L::kKX + L::kExtra);
   const uint32_t tS = tmem + x * kKeys, tO = tmem + 2 * kKeys + x * D;
   const int step = split ? 2 : 1, t_first = split ? x : 0;
   auto s_mma = [&](int t) {
     if (lane == 0) {
       const uint64_t dk = dk0 + static_cast<uint64_t>(((t % kStages) * L::kTile) >> 4);
+      if constexpr (!EXACT) tc::mma_f16(tS, dqx, t % kStages ? dkx1 : dkx0, kIdS, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = static_cast<uint64_t>(((kk >> 2) * L::kColBlk + (kk & 3) * 32) >> 4);
-        tc::mma_f16(tS, dq + off, dk + off, kIdS, kk > 0);
+        tc::mma_f16(tS, dq + off, dk + off, kIdS, !EXACT || kk > 0);
       }
       tc::commit(bar(kBarS + x));
       tc::commit(bar(kBarKFree + 2 * x + t % kStages));
@@ -611,7 +638,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p,
                                               const Tiling &tl, uint32_t sb, uint32_t bars,
                                               uint32_t tmem, uint8_t *smem,
                                               volatile int *abort_flag, int warp, int lane) {
-  using L = PrefillSmem<D>;
+  using L = PrefillSmem<D, EXACT, FEW>;
   auto bar = [&](int i) { return bars + 8 * i; };
   const int r = ((warp & 3) << 5) + lane;
   // last key that the row sees, and that every row of the tile sees
@@ -639,7 +666,7 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p,
       }
     }
   } else {
-    row_f = reinterpret_cast<const float *>(smem + L::kRowF)[xq * kRows + r];
+    row_f = reinterpret_cast<const float *>(smem + L::kMeta)[xq * kRows + r];
   }
   const float2 q2 = make_float2(qsum, qsum);
 
@@ -859,14 +886,14 @@ __device__ __forceinline__ void softmax_tiles(const PrefillParams &p,
 
 // Row tile x of Q in the operand's order of dimensions, zeros past the rows (FEW: in
 // the warps that have some; the others' S is not looked at), by 128 threads; not exact:
-// as fp16 over a power of two a row, whose product with the score factor goes to kRowF.
+// as fp16 over a power of two a row, whose product with the score factor goes to kMeta.
 // A thread copies chunks to where they belong and then turns its own in place.  The loops
 // are hardly unrolled: this runs once a part, and straight-line code waits for its own
 // instructions (measured 10 us a part with all 16 chunks unrolled, 4 so).
 template <int D, bool BF16, bool EXACT, bool FEW>
 __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile TilePart &part,
                                        bool split, int x, uint32_t sb, uint8_t *smem, int th) {
-  using L = PrefillSmem<D>;
+  using L = PrefillSmem<D, EXACT, FEW>;
   constexpr int kChunks = D / 8;  // 16-byte chunks a row
   constexpr int kStep = 128 / kChunks;
   const int c = th % kChunks, row0 = part.row0 + (split ? 0 : x * kRows), b = part.b, g = part.g;
@@ -881,33 +908,60 @@ __device__ __forceinline__ void load_q(const PrefillParams &p, const volatile Ti
       st_shared_v4(to, 0, 0, 0, 0);
   }
   cp_async_wait();
-#pragma unroll 4
-  for (int r = th / kChunks; r < rows; r += kStep) {
-    const uint32_t at = dst + swz128(r, c);
-    const uint4 v = lds128(at);
-    uint32_t w[4] = {v.x ^ p.qsign, v.y ^ p.qsign, v.z ^ p.qsign, v.w ^ p.qsign};
-    if constexpr (!EXACT) {
-      float2 f[4];
-      float top = 0.f;
+#pragma unroll 1
+  for (int r0 = th / kChunks; r0 < rows; r0 += 4 * kStep) {
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};  // of this thread's elements of four rows
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f[u] = unpack2<BF16>(w[u]);
-        top = fmaxf(top, fmaxf(fabsf(f[u].x), fabsf(f[u].y)));
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + i * kStep;
+      if (r >= rows) break;
+      const uint32_t at = dst + swz128(r, c);
+      const uint4 v = lds128(at);
+      uint32_t w[4] = {v.x ^ p.qsign, v.y ^ p.qsign, v.z ^ p.qsign, v.w ^ p.qsign};
+      if constexpr (!EXACT) {
+        float2 f[4];
+        float top = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f[u] = unpack2<BF16>(w[u]);
+          top = fmaxf(top, fmaxf(fabsf(f[u].x), fabsf(f[u].y)));
+        }
+#pragma unroll
+        for (int o = 1; o < kChunks; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        // 2^ex brings the row's largest magnitude into [2^14, 2^15), or near 1 where that
+        // is near the smallest of all
+        const int ex = min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          w[u] = pack2<false>(f[u].x * up, f[u].y * up);
+          const float2 h = unpack2<false>(w[u]);  // as the operand holds it
+          sums[i] += h.x + h.y;
+        }
+        if (c == 0)
+          reinterpret_cast<float *>(smem + L::kMeta)[x * kRows + r] =
+              p.qscale * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
       }
-#pragma unroll
-      for (int o = 1; o < kChunks; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      // 2^ex brings the row's largest magnitude into [2^14, 2^15), or near 1 where that
-      // is near the smallest of all
-      const int ex = min(120, 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = pack2<false>(f[u].x * up, f[u].y * up);
-      if (c == 0)
-        reinterpret_cast<float *>(smem + L::kRowF)[x * kRows + r] =
-            p.qscale * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+      st_shared_v4(at, __byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
+                   __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
     }
-    st_shared_v4(at, __byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
-                 __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
+    if constexpr (!EXACT) {
+      // the rows' sums: a quarter of their threads ends up with each of the four
+      const bool upper = c & (kChunks / 2), odd = c & (kChunks / 4);
+      float a = upper ? sums[2] : sums[0], b = upper ? sums[3] : sums[1];
+      a += __shfl_xor_sync(kFull, upper ? sums[0] : sums[2], kChunks / 2);
+      b += __shfl_xor_sync(kFull, upper ? sums[1] : sums[3], kChunks / 2);
+      float sum = (odd ? b : a) + __shfl_xor_sync(kFull, odd ? a : b, kChunks / 4);
+#pragma unroll
+      for (int o = kChunks / 8; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      const int r = r0 + (2 * upper + odd) * kStep;
+      if (c % (kChunks / 4) == 0 && r < rows) {  // over 2^7, in two terms
+        sum *= 0x1p-7f;
+        const float head = unpack2<false>(pack2<false>(sum, 0.f)).x;
+        st_shared_v4(sb + L::kQX + x * L::kExtra + r * 16,
+                     pack2<false>(sum, (sum - head) * 0x1p11f), 0, 0, 0);
+      }
+    }
   }
   fence_proxy_async_smem();  // generic stores -> read by the tensor cores
 }
@@ -937,8 +991,8 @@ __device__ __forceinline__ void set_registers() {
 // caches, each at its own registers: 4 x 4 queries over 32k keys 97 us, so 86).
 template <int D, bool BF16, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillParams p) {
-  using L = PrefillSmem<D>;
   constexpr bool EXACT = !BF16;
+  using L = PrefillSmem<D, EXACT, FEW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -955,6 +1009,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
     fence_mbar_init();
   };
 
+  if (!EXACT && tid < kRows) {
+    st_shared_v4(sb + L::kZeros + tid * 16, 0, 0, 0, 0);
+    fence_proxy_async_smem();  // read by the tensor cores
+  }
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_release();
   if (warp == 0) {
@@ -1002,8 +1060,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
       const Tiling tl(part.row0, part.nt, p.n_rows);
       const uint32_t tmem = begin();
       if (warp < tl.n_active)
-        mma_tiles<D, FEW>(warp, tl.split, part.nt, sb, bars_of(turn), tmem, p.status, abort_flag,
-                          lane);
+        mma_tiles<D, EXACT, FEW>(warp, tl.split, part.nt, sb, bars_of(turn), tmem, p.status,
+                                 abort_flag, lane);
       if (warp == 2 && lane == 0 && part.more) {
         if (turn > 0)
           for (int i = 0; i < kNumBars; ++i)
@@ -1033,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const PrefillP
       if (c == 1) own_q(part, tl);
       begin();
       if (c == 0 || tl.split)
-        convert_tiles<D, BF16, EXACT>(c, FEW && tl.split ? 2 : 1,
+        convert_tiles<D, BF16, EXACT, FEW>(c, FEW && tl.split ? 2 : 1,
                                       c == 0 ? warp - kConvertWarp0 : 2 * x + (warp & 1), p, part,
                                       sb, bars_of(turn), smem, tl, abort_flag, lane);
       if (c == 1 && tl.split) row_tiles_sync();
@@ -1117,7 +1175,8 @@ template <int D, bool BF16, bool FEW>
 int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
   auto kern = kv4_prefill_kernel<D, BF16, FEW>;
   static ContextCache<bool> smem_set;
-  if (set_smem_limit(kern, PrefillSmem<D>::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
+  constexpr int kSmem = PrefillSmem<D, !BF16, FEW>::kAlloc;
+  if (set_smem_limit(kern, kSmem, smem_set) != PA_OK) return PA_ERR_CUDA;
   // the split draws on what the block was launched with; less of it would never come free
   static std::atomic<bool> enough{FEW};
   if (!enough) {
@@ -1126,7 +1185,7 @@ int launch_t(const PrefillParams &p, int ctas, cudaStream_t stream) {
       return PA_ERR_CUDA;
     enough = true;
   }
-  if (launch_pdl(kern, dim3(ctas), dim3(kThreads), PrefillSmem<D>::kAlloc, stream, p) !=
+  if (launch_pdl(kern, dim3(ctas), dim3(kThreads), kSmem, stream, p) !=
           cudaSuccess ||
       launch_pdl(kv4_prefill_fold_kernel<D, BF16>,
                  dim3(ctas, (min(p.n_rows, kItemRows) + kFoldRows - 1) / kFoldRows),

@@ -93,6 +93,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
+// Descriptor of a K-major tile without a swizzle: 8 rows of 16 bytes (8 elements along K)
+// are 128 bytes in a row; LBO = byte distance between neighbours along K, SBO = between
+// 8-row groups.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo_bytes,
+                                                    uint32_t sbo_bytes) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
 // Instruction descriptor, kind::f16 with fp32 accumulation:
 //   bits 4-5 D type (1 = f32), 7-9 A type and 10-12 B type (0 = f16,
 //   1 = bf16), 15 / 16 A / B major (0 = K-major, 1 = MN-major),

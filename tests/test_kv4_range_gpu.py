@@ -67,13 +67,12 @@ def attend(q, pool, bt, seen, scale, dt):
 def assert_rows(got, want, r, dt):
     """A chunk's rows [nq, Hq, D] against `attend`'s.  A row's error, in the norm: half a step
     of the result's type of the row; and, a key, the roundings of its terms, each at most U =
-    2^-11 relatively: of the weight, and in bf16 of V (twice, the second time of its row's
-    least value, up to 3 times a typical one) and of K (alike, where a score of N(0, 1)
-    products moves by as much as a product).  Independent ones add up to
-    sqrt(1 + 10 + 10) U R / sqrt(3) < 3 U R, for fp16 U R / sqrt(3); 2.5 times that are
-    allowed.  An element below the type's normal range is off by up to half a step there,
-    smallest_normal eps / 2, whatever its size: sqrt(D) of them."""
-    half, most = torch.finfo(dt).eps / 2, (8 if dt is torch.bfloat16 else 1.5) * U
+    2^-11 relatively: of the weight, and in bf16 of V, twice, the second time of its row's
+    least value, up to 3 times a typical one.  (Scores are good to fp32's last bits.)
+    Independent ones add up to sqrt(1 + 1 + 9) U R / sqrt(3) < 2 U R, for fp16 U R / sqrt(3);
+    3 and 2.5 times that are allowed.  An element below the type's normal range is off by up
+    to half a step there, smallest_normal eps / 2, whatever its size: sqrt(D) of them."""
+    half, most = torch.finfo(dt).eps / 2, (6 if dt is torch.bfloat16 else 1.5) * U
     err, size = (got.double() - want).norm(dim=-1), want.norm(dim=-1)
     tol = half * (size + math.sqrt(want.shape[-1]) * torch.finfo(dt).smallest_normal) + most * r
     assert (err <= tol).all(), (float((err / size).max()), float((err / tol).max()))
@@ -297,3 +296,19 @@ def test_rows_that_are_not_finite_beside_far_larger_ones(n_new):
         assert torch.equal(got[:, :at], clean[:, :at])
         assert torch.isnan(got[:, at:]).all()
     assert pa.pa_last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_new,hq,d", [(2, 4, 128), (12, 4, 128), (64, 4, 64), (64, 4, 128),
+                                        (300, 1, 128)])
+@pytest.mark.parametrize("q_mul,spread", [(10, 0), (40, 0), (1, 1)])
+def test_chunk_of_large_scores(q_mul, spread, n_new, hq, d, dtype):
+    """Scores of N(0, 10) and N(0, 40), and rows whose sizes are spread by e^N(0, 1) (K) and
+    e^N(0, 2) (V): few keys share the weight, and an error in a score is one of the row."""
+    dt, keys = DT[dtype], 3000
+    k, v = randn(keys, 1, d, seed=1), randn(keys, 1, d, seed=2)
+    k *= torch.exp(spread * randn(keys, 1, 1, seed=5))
+    v *= torch.exp(2 * spread * randn(keys, 1, 1, seed=6))
+    pool, bt = stored(k, v, dt)
+    q = (randn(2, n_new, hq, d, seed=3) * q_mul).to(dt)
+    check_chunk(q, pool, bt, keys - n_new, 1 / math.sqrt(d), dt, (0, 1))
