@@ -602,8 +602,11 @@ size_t pa_decode_kv4_workspace_size(int head_dim);
  * pa_append_kv4) included; n_new from the few drafted tokens of a speculative
  * verify to a long chunk.
  *   out        device [batch][n_new][n_q_heads][head_dim] in q's dtype: a chunk's
- *              rows go into a 16-bit product, and the tensor-core sums over a
- *              long context are not good to fp32's last bits
+ *              rows go into a 16-bit product.  Weights enter the tensor cores with
+ *              11 bits (down to 2^-25 of a row's largest, in steps of 2^-35 below),
+ *              and so do the values of a bf16 cache, where keys smaller than 2^-20
+ *              and values smaller than 2^-16 of the largest of 32 neighbours lose
+ *              digits; scores are good to fp32's last bits
  *   workspace  as in pa_decode_kv4, pa_prefill_kv4_workspace_size(...) bytes
  */
 int pa_prefill_kv4(const void *q, const void *kv_cache, const int32_t *block_table,
