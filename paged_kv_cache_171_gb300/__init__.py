@@ -800,9 +800,10 @@ def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, 
         q_in, q_to = q.data_ptr() or _NOTHING, q_out.data_ptr() or _NOTHING
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rows = (k_new.data_ptr(), v_new.data_ptr()) if n_tok else (_NOTHING, _NOTHING)
-    places = (seq_idx.data_ptr(), pos.data_ptr()) if n_tok else (_NOTHING, _NOTHING)
-    rc = entry(*rows, q_in, *caches, q_to, block_table.data_ptr(), *places, table, n_tok, ks, vs,
+    k, v, seqs, at = k_new.data_ptr(), v_new.data_ptr(), seq_idx.data_ptr(), pos.data_ptr()
+    if n_tok == 0:
+        k = v = seqs = at = _NOTHING
+    rc = entry(k, v, q_in, *caches, q_to, block_table.data_ptr(), seqs, at, table, n_tok, ks, vs,
                qs, hq, hkv, D, page_size, batch, max_blocks, num_pages, max_pos, rot,
                bool(interleaved), dtype_code(k_new), torch._C._cuda_getCurrentRawStream(index))
     if rc:

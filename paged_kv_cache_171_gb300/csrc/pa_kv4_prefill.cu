@@ -280,7 +280,7 @@ __device__ __forceinline__ size_t row_at(const PrefillParams &p, int b, int g, i
 // The eight codes of a word, in the order 0 4 1 5 2 6 3 7.  EXACT: as 2 c - 15.  Else as
 // zero + scale (c - 8) over 2^7 ref: (x & 0x000f000f) is the fp16 subnormal pair
 // c 2^-24 and (x & 0x00f000f0) is c 2^-20, so with s24 = scale 2^24, s20 = scale 2^20
-// and z = zero - 8 scale a pair is one AND and one FMA.
+// and z = zero - 8 scale (K: -8 scale) a pair is one AND and one FMA.
 template <bool EXACT>
 __device__ __forceinline__ uint4 operand(uint32_t x, __half2 s24, __half2 s20, __half2 z) {
   uint32_t o[4];
@@ -316,7 +316,7 @@ __device__ __forceinline__ float exp2i(int k) {
 
 // Converter warp w of group c: keys 32 w .. 32 w + 31 (two pages) of the key tiles c,
 // c + step, .., K then V, and their references and, in the exact form, scales and zeros.
-// The pages come through a ring of the warp's own, by bulk copies 1.5 tiles ahead.
+// The pages come through a ring of the warp's own, by bulk copies a tile (FEW: 1.5) ahead.
 //
 // A row past the sequence's end stands for zeros (it may hold anything, and 0 * NaN is
 // NaN).  A key or value row that is not finite makes its key's score NaN, which
