@@ -619,6 +619,143 @@ size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_
                                      int head_dim, int page_size, int max_blocks_per_seq);
 
 /*
+ * Gathered attention weight, and eviction by it (ch. 19 "推理系统与性能工程", 19.4.3: the
+ * tokens that gathered the most attention stay, beside the first and the latest ones).
+ *   weights: device float [num_pages][n_kv_heads][page_size], 16-byte aligned: at the place
+ *   of every cached token and kv head the attention weight that queries gave it so far,
+ *   summed over the query heads of the kv head's group.
+ * Weights need no clearing: of a sequence of T tokens those at t >= T - fresh are set, the
+ * others added to (fresh >= T sets them all), so the tokens that a call is the first to
+ * see are its fresh ones.  No other place is written.  The pages of a call's sequences must
+ * be different ones wherever they hold tokens (a shared page would be added to, or moved,
+ * by several).  At most 65535 heads (PA_ERR_HEADS).
+ */
+
+/*
+ * pa_decode_weighted -- pa_decode, and the step's attention weight gathered:
+ *   out as in pa_decode, p[h][t] the softmax's weights,
+ *   weights[t][g] = (t < T - fresh ? weights[t][g] : 0) + sum of p[h][t] over g's query heads
+ * (a decode step's fresh = 1: the step's own token).  fp32 sums in a fixed order.
+ *   workspace  pa_decode_weighted_workspace_size(...) bytes, 16-byte aligned, contents on
+ *              entry do not matter, not shared by calls that overlap on the GPU; it holds
+ *              the step's scores (4 bytes a query head and token of the table)
+ * At most 1024 query heads a kv head (PA_ERR_HEADS); fresh >= 0 (PA_ERR_SHAPE).  T = 0
+ * writes zeros to out.  A page id outside the pool is read as page 0, its weights are not
+ * written, and PA_ERR_BAD_BLOCK is recorded.
+ */
+int pa_decode_weighted(const void *q, const void *k_cache, const void *v_cache, float *weights,
+                       const int32_t *block_table, const int32_t *ctx_lens, float *out,
+                       float scale, int fresh, int n_q_heads, int n_kv_heads, int head_dim,
+                       int page_size, int batch, int max_blocks_per_seq, int num_pages,
+                       pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                       pa_stream_t stream);
+size_t pa_decode_weighted_workspace_size(int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                         int page_size, int max_blocks_per_seq);
+
+/*
+ * pa_prefill_weights -- the attention weight that n_new queries of a chunk give the cached
+ * tokens, gathered: query i of sequence b, 0 <= i < n_new, sees t <= ctx_lens[b] + i as in
+ * pa_prefill_paged, T = ctx_lens[b] + n_new, and weights are as in pa_decode_weighted with
+ * p summed over the queries too.  The chunk's output is pa_prefill_paged's; this call reads
+ * no V.  The last queries of a prompt alone (a view of q, ctx_lens counted up to them) say
+ * what those look at.
+ *   q  device, query i of sequence b at b * q_batch_stride + i * q_token_stride (elements,
+ *      multiples of 8), its heads contiguous
+ *   workspace  as in pa_decode_weighted, pa_prefill_weights_workspace_size(...) bytes
+ * n_new = 0 does nothing.
+ */
+int pa_prefill_weights(const void *q, const void *k_cache, float *weights,
+                       const int32_t *block_table, const int32_t *ctx_lens, int n_new,
+                       float scale, int fresh, int64_t q_batch_stride, int64_t q_token_stride,
+                       int n_q_heads, int n_kv_heads, int head_dim, int page_size, int batch,
+                       int max_blocks_per_seq, int num_pages, pa_dtype dtype, void *workspace,
+                       size_t workspace_bytes, pa_stream_t stream);
+size_t pa_prefill_weights_workspace_size(int batch, int n_new, int n_q_heads, int n_kv_heads,
+                                         int head_dim, int page_size, int max_blocks_per_seq);
+
+/*
+ * pa_evict_kv -- keep at most `budget` tokens a sequence, chosen for each kv head.
+ *
+ * A sequence of T = ctx_lens[b] <= budget tokens keeps them all.  Of a longer one every kv
+ * head keeps t < sink_tokens, t >= T - recent_tokens, and of the others the budget -
+ * sink_tokens - recent_tokens with the largest weight (equal ones: the lowest positions; a
+ * NaN behind every number).  The kept rows of K, V and weights move, in their order, to
+ * positions 0, 1, .. of dst_table (a cached key keeps the rotation it has), and new_lens[b]
+ * = min(T, budget).
+ *   dst_table  device int32 [batch][dst_blocks_per_seq]: block_table itself (in place), or
+ *              pages that hold no token of this call's sequences (where the old pages are
+ *              shared with others)
+ *   new_lens   device int32 [batch], not ctx_lens (PA_ERR_SHAPE)
+ *   workspace  as in pa_decode_weighted, pa_evict_kv_workspace_size(...) bytes
+ * Places behind the kept rows are left as they were.  sink_tokens, recent_tokens >= 0 and
+ * their sum at most budget (PA_ERR_SHAPE).  A row whose page, old or new, is bad is not
+ * moved and PA_ERR_BAD_BLOCK recorded.
+ */
+int pa_evict_kv(void *k_cache, void *v_cache, float *weights, const int32_t *block_table,
+                const int32_t *ctx_lens, const int32_t *dst_table, int32_t *new_lens, int budget,
+                int sink_tokens, int recent_tokens, int n_kv_heads, int head_dim, int page_size,
+                int batch, int max_blocks_per_seq, int dst_blocks_per_seq, int num_pages,
+                pa_dtype dtype, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+size_t pa_evict_kv_workspace_size(int batch, int n_kv_heads, int head_dim, int page_size,
+                                  int max_blocks_per_seq, int budget);
+
+/*
+ * pa_compact_kv -- move listed rows up behind a sequence's first ctx_lens[b] tokens, in
+ * place, the same for all kv heads: row ctx_lens[b] + keep[b][j] of K, V and (if given)
+ * weights moves to position ctx_lens[b] + j for j < n_keep[b], and new_lens[b] =
+ * ctx_lens[b] + n_keep[b].  After a verify step: the accepted branch of a tree of drafted
+ * tokens.  With ctx_lens 0: a sequence cut to the listed tokens.
+ *   keep     device int32 [batch][max_keep], ascending in each row, from 0
+ *   n_keep   device int32 [batch], 0 .. max_keep
+ *   new_lens device int32 [batch], not ctx_lens (PA_ERR_SHAPE)
+ *   weights  or NULL
+ * A sequence whose list is not ascending or leaves the table, or whose n_keep is out of
+ * range, keeps nothing (new_lens[b] = ctx_lens[b]) and PA_ERR_BAD_INDEX is recorded; a row
+ * whose page is bad is not moved (PA_ERR_BAD_BLOCK).
+ */
+int pa_compact_kv(void *k_cache, void *v_cache, float *weights, const int32_t *block_table,
+                  const int32_t *ctx_lens, const int32_t *keep, const int32_t *n_keep,
+                  int max_keep, int32_t *new_lens, int n_kv_heads, int head_dim, int page_size,
+                  int batch, int max_blocks_per_seq, int num_pages, pa_dtype dtype,
+                  pa_stream_t stream);
+
+/*
+ * pa_prefill_tree -- attention of a tree of drafted tokens: the verify step where several
+ * continuations are drafted at once.
+ *
+ * Drafted token i of sequence b, 0 <= i < n_new, has its K and V at position ctx_lens[b] + i
+ * (appended before; its rotation is its depth's).  Query i sees every t < ctx_lens[b] and
+ * those drafted tokens j for which bit j % 32 of mask[b][i][j / 32] is set:
+ *   out[b][i][h] = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m) over them, rounded to dtype.
+ * A query that sees nothing gives zeros.  A drafted token's K or V that is not finite
+ * reaches only the queries that see it.  Bits from n_new on are not used.
+ *   mask       device int32 [batch][n_new][ceil(n_new / 32)] (pa_tree_mask, or any other)
+ *   out        device [batch][n_new][n_q_heads][head_dim], dtype
+ *   workspace  as in pa_decode_weighted, pa_prefill_tree_workspace_size(...) bytes; NULL
+ *              where that is 0
+ * The other arguments are pa_prefill_paged's.  At most 65535 heads (PA_ERR_HEADS).
+ */
+int pa_prefill_tree(const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *block_table, const int32_t *ctx_lens, const int32_t *mask,
+                    int n_new, void *out, float scale, int n_q_heads, int n_kv_heads,
+                    int head_dim, int page_size, int batch, int max_blocks_per_seq,
+                    int num_pages, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                    pa_stream_t stream);
+size_t pa_prefill_tree_workspace_size(int batch, int n_new, int n_q_heads, int n_kv_heads,
+                                      int head_dim, int page_size, int max_blocks_per_seq);
+
+/*
+ * pa_tree_mask -- the masks of trees given by their parents: bit j of token i's mask is set
+ * for j = i and for every ancestor j of i; depth[b][i] (or NULL) counts the ancestors, so
+ * that token i stands at position ctx + depth[b][i] of its branch.
+ *   parents  device int32 [batch][n_new], -1 (a child of the last cached token) .. i - 1; a
+ *            parent outside that range ends the branch there and records PA_ERR_BAD_INDEX
+ *   mask     device int32 [batch][n_new][ceil(n_new / 32)]
+ */
+int pa_tree_mask(const int32_t *parents, int32_t *mask, int32_t *depth, int batch, int n_new,
+                 pa_stream_t stream);
+
+/*
  * pa_last_device_error -- synchronise `stream`, then return and clear the
  * device status word (PA_OK if no kernel recorded an error since the last
  * call).  The word is shared by every stream of the device: it reports the

@@ -35,6 +35,11 @@ __all__ = [
     "pa_kv4_block_bytes", "kv4_cache", "pa_append_kv4", "append_kv4", "pa_read_kv4", "read_kv4",
     "pa_copy_pages_kv4", "copy_pages_kv4", "pa_decode_kv4", "pa_decode_kv4_workspace_size",
     "decode_kv4", "pa_prefill_kv4", "pa_prefill_kv4_workspace_size", "prefill_kv4",
+    "weight_pool", "pa_decode_weighted", "pa_decode_weighted_workspace_size", "decode_weighted",
+    "pa_prefill_weights", "pa_prefill_weights_workspace_size", "prefill_weights",
+    "pa_evict_kv", "pa_evict_kv_workspace_size", "evict_kv", "pa_compact_kv", "compact_kv",
+    "pa_prefill_tree", "pa_prefill_tree_workspace_size", "prefill_tree", "pa_tree_mask",
+    "tree_mask",
 ]
 
 BF16 = 0
@@ -133,6 +138,26 @@ def lib():
         L.pa_prefill_kv4.restype = I
         L.pa_prefill_kv4_workspace_size.argtypes = [I] * 7
         L.pa_prefill_kv4_workspace_size.restype = Z
+        L.pa_decode_weighted.argtypes = [P] * 7 + [F] + [I] * 9 + [P, Z, P]
+        L.pa_decode_weighted.restype = I
+        L.pa_decode_weighted_workspace_size.argtypes = [I] * 6
+        L.pa_decode_weighted_workspace_size.restype = Z
+        L.pa_prefill_weights.argtypes = [P] * 5 + [I, F, I, J, J] + [I] * 8 + [P, Z, P]
+        L.pa_prefill_weights.restype = I
+        L.pa_prefill_weights_workspace_size.argtypes = [I] * 7
+        L.pa_prefill_weights_workspace_size.restype = Z
+        L.pa_evict_kv.argtypes = [P] * 7 + [I] * 11 + [P, Z, P]
+        L.pa_evict_kv.restype = I
+        L.pa_evict_kv_workspace_size.argtypes = [I] * 6
+        L.pa_evict_kv_workspace_size.restype = Z
+        L.pa_compact_kv.argtypes = [P] * 7 + [I, P] + [I] * 7 + [P]
+        L.pa_compact_kv.restype = I
+        L.pa_prefill_tree.argtypes = [P] * 6 + [I, P, F] + [I] * 8 + [P, Z, P]
+        L.pa_prefill_tree.restype = I
+        L.pa_prefill_tree_workspace_size.argtypes = [I] * 7
+        L.pa_prefill_tree_workspace_size.restype = Z
+        L.pa_tree_mask.argtypes = [P] * 3 + [I, I, P]
+        L.pa_tree_mask.restype = I
         L.pa_last_device_error.argtypes = [P]
         L.pa_last_device_error.restype = I
         L.pa_selftest_wait_timeout.argtypes = [P]
@@ -487,6 +512,89 @@ def pa_prefill_kv4_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim,
                                   max_blocks_per_seq) -> int:
     return lib().pa_prefill_kv4_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim,
                                                page_size, max_blocks_per_seq)
+
+
+def pa_decode_weighted(q, k_cache, v_cache, weights, block_table, ctx_lens, out, scale, fresh,
+                       n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+                       num_pages, dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
+    rc = lib().pa_decode_weighted(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(block_table), _ptr(ctx_lens),
+        _ptr(out), float(scale), fresh, n_q_heads, n_kv_heads, head_dim, page_size, batch,
+        max_blocks_per_seq, num_pages, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "pa_decode_weighted")
+
+
+def pa_decode_weighted_workspace_size(batch, n_q_heads, n_kv_heads, head_dim, page_size,
+                                      max_blocks_per_seq) -> int:
+    return lib().pa_decode_weighted_workspace_size(batch, n_q_heads, n_kv_heads, head_dim,
+                                                   page_size, max_blocks_per_seq)
+
+
+def pa_prefill_weights(q, k_cache, weights, block_table, ctx_lens, n_new, scale, fresh,
+                       q_batch_stride, q_token_stride, n_q_heads, n_kv_heads, head_dim, page_size,
+                       batch, max_blocks_per_seq, num_pages, dtype, workspace=None,
+                       workspace_bytes=0, stream=None) -> int:
+    rc = lib().pa_prefill_weights(
+        _ptr(q), _ptr(k_cache), _ptr(weights), _ptr(block_table), _ptr(ctx_lens), n_new,
+        float(scale), fresh, q_batch_stride, q_token_stride, n_q_heads, n_kv_heads, head_dim,
+        page_size, batch, max_blocks_per_seq, num_pages, dtype, _ptr(workspace), workspace_bytes,
+        _stream(stream))
+    return _check(rc, "pa_prefill_weights")
+
+
+def pa_prefill_weights_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim, page_size,
+                                      max_blocks_per_seq) -> int:
+    return lib().pa_prefill_weights_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim,
+                                                   page_size, max_blocks_per_seq)
+
+
+def pa_evict_kv(k_cache, v_cache, weights, block_table, ctx_lens, dst_table, new_lens, budget,
+                sink_tokens, recent_tokens, n_kv_heads, head_dim, page_size, batch,
+                max_blocks_per_seq, dst_blocks_per_seq, num_pages, dtype, workspace=None,
+                workspace_bytes=0, stream=None) -> int:
+    rc = lib().pa_evict_kv(
+        _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(block_table), _ptr(ctx_lens),
+        _ptr(dst_table), _ptr(new_lens), budget, sink_tokens, recent_tokens, n_kv_heads, head_dim,
+        page_size, batch, max_blocks_per_seq, dst_blocks_per_seq, num_pages, dtype,
+        _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "pa_evict_kv")
+
+
+def pa_evict_kv_workspace_size(batch, n_kv_heads, head_dim, page_size, max_blocks_per_seq,
+                               budget) -> int:
+    return lib().pa_evict_kv_workspace_size(batch, n_kv_heads, head_dim, page_size,
+                                            max_blocks_per_seq, budget)
+
+
+def pa_compact_kv(k_cache, v_cache, weights, block_table, ctx_lens, keep, n_keep, max_keep,
+                  new_lens, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, num_pages,
+                  dtype, stream=None) -> int:
+    rc = lib().pa_compact_kv(
+        _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(block_table), _ptr(ctx_lens),
+        _ptr(keep), _ptr(n_keep), max_keep, _ptr(new_lens), n_kv_heads, head_dim, page_size,
+        batch, max_blocks_per_seq, num_pages, dtype, _stream(stream))
+    return _check(rc, "pa_compact_kv")
+
+
+def pa_prefill_tree(q, k_cache, v_cache, block_table, ctx_lens, mask, n_new, out, scale,
+                    n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
+                    num_pages, dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
+    rc = lib().pa_prefill_tree(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens), _ptr(mask),
+        n_new, _ptr(out), float(scale), n_q_heads, n_kv_heads, head_dim, page_size, batch,
+        max_blocks_per_seq, num_pages, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "pa_prefill_tree")
+
+
+def pa_prefill_tree_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim, page_size,
+                                   max_blocks_per_seq) -> int:
+    return lib().pa_prefill_tree_workspace_size(batch, n_new, n_q_heads, n_kv_heads, head_dim,
+                                                page_size, max_blocks_per_seq)
+
+
+def pa_tree_mask(parents, mask, depth, batch, n_new, stream=None) -> int:
+    rc = lib().pa_tree_mask(_ptr(parents), _ptr(mask), _ptr(depth), batch, n_new, _stream(stream))
+    return _check(rc, "pa_tree_mask")
 
 
 def pa_last_device_error(stream=None) -> int:
@@ -978,4 +1086,267 @@ def prefill_kv4(q, kv_cache, block_table, ctx_lens, scale, out=None, workspace=N
                               torch._C._cuda_getCurrentRawStream(index))
     if rc:
         raise PAError(rc, "pa_prefill_kv4")
+    return out
+
+
+# --- eviction by gathered attention weight, and trees of drafted tokens --------
+
+def weight_pool(num_pages, n_kv_heads, device="cuda"):
+    """A pool of gathered attention weights beside a 16-bit cache: float32
+    [num_pages, n_kv_heads, 16]."""
+    import torch
+    return torch.zeros((num_pages, n_kv_heads, 16), dtype=torch.float32, device=device)
+
+
+def _cache_dims(k_cache, v_cache, dtype, index):
+    """num_pages, n_kv_heads and head_dim of 16-bit caches on device `index`; v_cache may
+    be None."""
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_cache: want [pages, h_kv, 16, D], got {tuple(shape)}")
+    _want(k_cache, "k_cache", dtype, shape, index)
+    if v_cache is not None:
+        _want(v_cache, "v_cache", dtype, shape, index)
+    if shape[2] != 16:
+        raise PAError(-4, "caches")
+    return shape[0], shape[1], shape[3]
+
+
+def _scratch(workspace, need, device, index):
+    """(pointer, bytes) of the caller's workspace, or of one allocated for the call (the
+    tensor too: it has to live until the launch)."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: want a contiguous tensor on cuda:{index}")
+    return workspace, workspace.data_ptr(), workspace.nbytes
+
+
+def decode_weighted(q, k_cache, v_cache, weights, block_table, ctx_lens, scale, fresh=1, out=None,
+                    workspace=None, stream=None):
+    """pa_decode_weighted on tensors: decode()'s attention, and the weight each cached token
+    got from the step's queries gathered in weights float32 [pages, h_kv, 16] (weight_pool):
+    added, but set for the last `fresh` tokens of a sequence.  Returns fp32 [B, h_q, D].
+    workspace: any tensor of pa_decode_weighted_workspace_size(...) bytes, not shared with a
+    call that may run at the same time."""
+    import torch
+    index = _device_index(q)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return decode_weighted(q, k_cache, v_cache, weights, block_table, ctx_lens, scale,
+                                   fresh, out, workspace)
+    if q.dim() != 3:
+        raise ValueError(f"q: want [B, h_q, D], got {tuple(q.shape)}")
+    B, hq, D = q.shape
+    _want(q, "q", q.dtype, q.shape, index)
+    pages, hkv, D_cache = _cache_dims(k_cache, v_cache, q.dtype, index)
+    if D_cache != D:
+        raise ValueError(f"the cache holds head_dim {D_cache}, q has {D}")
+    _want(weights, "weights", torch.float32, (pages, hkv, 16), index)
+    _, mb = _want_2d(block_table, "block_table", torch.int32, B, index)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    if out is None:
+        out = torch.empty((B, hq, D), dtype=torch.float32, device=q.device)
+    else:
+        _want(out, "out", torch.float32, (B, hq, D), index)
+    L = lib()
+    need = 0 if workspace is not None else \
+        L.pa_decode_weighted_workspace_size(B, hq, hkv, D, 16, mb)
+    workspace, ws, ws_bytes = _scratch(workspace, need, q.device, index)
+    rc = L.pa_decode_weighted(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                              weights.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(),
+                              out.data_ptr(), scale, fresh, hq, hkv, D, 16, B, mb, pages,
+                              dtype_code(q), ws, ws_bytes,
+                              torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_decode_weighted")
+    return out
+
+
+def prefill_weights(q, k_cache, weights, block_table, ctx_lens, scale, fresh=None, workspace=None,
+                    stream=None):
+    """pa_prefill_weights on tensors: the weight that the chunk's queries q [B, n_new, h_q, D]
+    (or a view of its last ones: the heads of a token must be contiguous) give each cached
+    token, gathered in weights [pages, h_kv, 16]; ctx_lens = tokens before these queries.
+    fresh: how many of a sequence's last tokens are set, not added to (None: n_new, the
+    queries' own).  Returns weights.  workspace: any tensor of
+    pa_prefill_weights_workspace_size(...) bytes, as in decode_weighted."""
+    import torch
+    index = _device_index(q)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return prefill_weights(q, k_cache, weights, block_table, ctx_lens, scale, fresh,
+                                   workspace)
+    if q.dim() != 4:
+        raise ValueError(f"q: want [B, n_new, h_q, D], got {tuple(q.shape)}")
+    B, n_new, hq, D = q.shape
+    sb, st, sh, one = q.stride()
+    if n_new == 1:
+        st = hq * D
+    if B == 1:
+        sb = max(n_new, 1) * st
+    if one != 1 or (hq > 1 and sh != D):
+        raise ValueError(f"q: the heads of a token must be contiguous rows (strides "
+                         f"{tuple(q.stride())}); call .contiguous()")
+    pages, hkv, D_cache = _cache_dims(k_cache, None, q.dtype, index)
+    if D_cache != D:
+        raise ValueError(f"the cache holds head_dim {D_cache}, q has {D}")
+    _want(weights, "weights", torch.float32, (pages, hkv, 16), index)
+    _, mb = _want_2d(block_table, "block_table", torch.int32, B, index)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    if fresh is None:
+        fresh = n_new
+    L = lib()
+    need = 0 if workspace is not None else \
+        L.pa_prefill_weights_workspace_size(B, n_new, hq, hkv, D, 16, mb)
+    workspace, ws, ws_bytes = _scratch(workspace, need, q.device, index)
+    rc = L.pa_prefill_weights(q.data_ptr() or _NOTHING, k_cache.data_ptr(), weights.data_ptr(),
+                              block_table.data_ptr(), ctx_lens.data_ptr(), n_new, scale, fresh,
+                              sb if n_new else hq * D, st, hq, hkv, D, 16, B, mb, pages,
+                              dtype_code(q), ws, ws_bytes,
+                              torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_prefill_weights")
+    return weights
+
+
+def evict_kv(k_cache, v_cache, weights, block_table, ctx_lens, budget, sink=0, recent=0,
+             dst_table=None, new_lens=None, workspace=None, stream=None):
+    """pa_evict_kv on tensors: every sequence of more than `budget` tokens keeps, for each kv
+    head, its first `sink`, its last `recent` and the heaviest others by weights
+    [pages, h_kv, 16]; K, V and weights move to positions 0 .. in place, or to the pages of
+    dst_table int32 [B, blocks].  Returns the new lengths, int32 [B] (new_lens if given; not
+    ctx_lens itself).  workspace: any tensor of pa_evict_kv_workspace_size(...) bytes, as in
+    decode_weighted."""
+    import torch
+    index = _device_index(k_cache)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return evict_kv(k_cache, v_cache, weights, block_table, ctx_lens, budget, sink,
+                            recent, dst_table, new_lens, workspace)
+    pages, hkv, D = _cache_dims(k_cache, v_cache, k_cache.dtype, index)
+    _want(weights, "weights", torch.float32, (pages, hkv, 16), index)
+    B, mb = _want_2d(block_table, "block_table", torch.int32, None, index)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    if dst_table is None:
+        dst_table = block_table
+    _, db = _want_2d(dst_table, "dst_table", torch.int32, B, index)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+    else:
+        _want(new_lens, "new_lens", torch.int32, (B,), index)
+    L = lib()
+    need = 0 if workspace is not None else \
+        L.pa_evict_kv_workspace_size(B, hkv, D, 16, mb, budget)
+    workspace, ws, ws_bytes = _scratch(workspace, need, k_cache.device, index)
+    rc = L.pa_evict_kv(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
+                       block_table.data_ptr(), ctx_lens.data_ptr(), dst_table.data_ptr(),
+                       new_lens.data_ptr(), budget, sink, recent, hkv, D, 16, B, mb, db, pages,
+                       dtype_code(k_cache), ws, ws_bytes,
+                       torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_evict_kv")
+    return new_lens
+
+
+def compact_kv(k_cache, v_cache, block_table, ctx_lens, keep, n_keep, weights=None, new_lens=None,
+               stream=None):
+    """pa_compact_kv on tensors: rows ctx_lens[b] + keep[b, j], j < n_keep[b], of K, V and (if
+    given) weights move up to positions ctx_lens[b] + j, in place: the accepted branch of a
+    tree of drafted tokens, or (ctx_lens 0) a sequence cut to the listed tokens.  keep int32
+    [B, max_keep], ascending in each row; n_keep int32 [B].  Returns the new lengths, int32
+    [B] (new_lens if given; not ctx_lens itself)."""
+    import torch
+    index = _device_index(k_cache)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return compact_kv(k_cache, v_cache, block_table, ctx_lens, keep, n_keep, weights,
+                              new_lens)
+    pages, hkv, D = _cache_dims(k_cache, v_cache, k_cache.dtype, index)
+    if weights is not None:
+        _want(weights, "weights", torch.float32, (pages, hkv, 16), index)
+    B, mb = _want_2d(block_table, "block_table", torch.int32, None, index)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    _, most = _want_2d(keep, "keep", torch.int32, B, index)
+    _want(n_keep, "n_keep", torch.int32, (B,), index)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+    else:
+        _want(new_lens, "new_lens", torch.int32, (B,), index)
+    rc = lib().pa_compact_kv(k_cache.data_ptr(), v_cache.data_ptr(),
+                             weights.data_ptr() if weights is not None else None,
+                             block_table.data_ptr(), ctx_lens.data_ptr(),
+                             keep.data_ptr() or _NOTHING, n_keep.data_ptr(), most,
+                             new_lens.data_ptr(), hkv, D, 16, B, mb, pages, dtype_code(k_cache),
+                             torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_compact_kv")
+    return new_lens
+
+
+def tree_mask(parents, mask=None, depth=None, stream=None):
+    """pa_tree_mask on tensors: parents int32 [B, n] of the drafted tokens (-1: the last
+    cached token; a parent comes before its children).  Returns (mask int32
+    [B, n, ceil(n / 32)], depth int32 [B, n]): which drafted tokens each one sees, and how
+    many come before it on its branch (its position is the context's length plus that)."""
+    import torch
+    index = _device_index(parents)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return tree_mask(parents, mask, depth)
+    B, n = _want_2d(parents, "parents", torch.int32, None, index)
+    words = -(-n // 32)
+    if mask is None:
+        mask = torch.empty((B, n, words), dtype=torch.int32, device=parents.device)
+    else:
+        _want(mask, "mask", torch.int32, (B, n, words), index)
+    if depth is None:
+        depth = torch.empty((B, n), dtype=torch.int32, device=parents.device)
+    else:
+        _want(depth, "depth", torch.int32, (B, n), index)
+    _check(lib().pa_tree_mask(parents.data_ptr() or _NOTHING, mask.data_ptr() or _NOTHING,
+                              depth.data_ptr() or _NOTHING, B, n,
+                              torch._C._cuda_getCurrentRawStream(index)), "pa_tree_mask")
+    return mask, depth
+
+
+def prefill_tree(q, k_cache, v_cache, block_table, ctx_lens, mask, scale, out=None, workspace=None,
+                 stream=None):
+    """pa_prefill_tree on tensors: q [B, n, h_q, D], the queries of n drafted tokens a sequence,
+    whose K/V rows are cached at positions ctx_lens[b] .. ctx_lens[b] + n - 1; mask int32
+    [B, n, ceil(n / 32)] (tree_mask): bit j of row i lets token i see drafted token j.  Returns
+    [B, n, h_q, D] in q's dtype.  workspace: any tensor of
+    pa_prefill_tree_workspace_size(...) bytes, as in decode_weighted."""
+    import torch
+    index = _device_index(q)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return prefill_tree(q, k_cache, v_cache, block_table, ctx_lens, mask, scale, out,
+                                workspace)
+    if q.dim() != 4:
+        raise ValueError(f"q: want [B, n, h_q, D], got {tuple(q.shape)}")
+    B, n, hq, D = shape = q.shape
+    _want(q, "q", q.dtype, shape, index)
+    pages, hkv, D_cache = _cache_dims(k_cache, v_cache, q.dtype, index)
+    if D_cache != D:
+        raise ValueError(f"the cache holds head_dim {D_cache}, q has {D}")
+    _, mb = _want_2d(block_table, "block_table", torch.int32, B, index)
+    _want(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    _want(mask, "mask", torch.int32, (B, n, -(-n // 32)), index)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _want(out, "out", q.dtype, shape, index)
+    L = lib()
+    need = 0 if workspace is not None else \
+        L.pa_prefill_tree_workspace_size(B, n, hq, hkv, D, 16, mb)
+    workspace, ws, ws_bytes = _scratch(workspace, need, q.device, index)
+    ptrs = (q.data_ptr(), mask.data_ptr(), out.data_ptr()) if n else (_NOTHING,) * 3
+    rc = L.pa_prefill_tree(ptrs[0], k_cache.data_ptr(), v_cache.data_ptr(),
+                           block_table.data_ptr(), ctx_lens.data_ptr(), ptrs[1], n, ptrs[2],
+                           scale, hq, hkv, D, 16, B, mb, pages, dtype_code(q), ws, ws_bytes,
+                           torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PAError(rc, "pa_prefill_tree")
     return out

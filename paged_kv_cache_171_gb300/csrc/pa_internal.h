@@ -199,6 +199,12 @@ int *device_status();
 int make_rows_map(CUtensorMap *map, const void *base, uint64_t rows,
                   int head_dim, int box_rows);
 
+// Tiled tensor map over queries [batch][n_new][n_heads][head_dim], 16-bit, with strides
+// in elements (multiples of 8), box {64, heads, queries, 1}, 128-byte swizzle; queries past
+// n_new read as zeros.  Returns PA_OK or PA_ERR_CUDA.
+int make_query_map(CUtensorMap *map, const void *q, int head_dim, int n_heads, int n_new,
+                   int batch, int64_t token_stride, int64_t batch_stride, int box_heads,
+                   int box_queries);
 
 // Launch with programmatic stream serialisation (the kernel must call
 // griddep_wait() before it reads anything a predecessor may write).
