@@ -37,7 +37,8 @@ struct WeightsLaunch {
   int n_new, n_q_heads, n_kv_heads, head_dim, batch, max_blocks, num_pages, fresh;
   bool bf16;
 };
-size_t weights_workspace_bytes(int batch, int n_new, int n_q_heads, int n_kv_heads, int sms);
+size_t weights_workspace_bytes(int batch, int n_new, int n_q_heads, int n_kv_heads,
+                               int max_blocks, int sms);
 int launch_weights(const WeightsLaunch &a, cudaStream_t stream);
 
 // Eviction and compaction (pa_evict.cu).  A move takes, for every sequence and kv head,

@@ -184,7 +184,8 @@ size_t pa_prefill_weights_workspace_size(int batch, int n_new, int n_q_heads, in
       check_chunk(n_new, n_q_heads, n_kv_heads, batch, max_blocks_per_seq, page_size) ||
       n_new == 0)
     return 0;
-  return weights_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads, sms_or_default());
+  return weights_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads, max_blocks_per_seq,
+                                 sms_or_default());
 }
 
 int pa_prefill_weights(const void *q, const void *k_cache, float *weights,
@@ -208,8 +209,8 @@ int pa_prefill_weights(const void *q, const void *k_cache, float *weights,
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(weights)) return PA_ERR_ALIGN;
   if (n_new == 0) return PA_OK;
   if (!workspace ||
-      workspace_bytes <
-          weights_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads, sms_or_default()))
+      workspace_bytes < weights_workspace_bytes(batch, n_new, n_q_heads, n_kv_heads,
+                                                max_blocks_per_seq, sms_or_default()))
     return PA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PA_ERR_ALIGN;
   WeightsLaunch a;

@@ -7,24 +7,27 @@
 // V is not needed.  Two passes over S = Q K^T on the tensor cores (tcgen05, accumulators
 // in tensor memory), because a weight needs its row's final m and l, and S itself, at 4
 // bytes a pair, would cost more to store and read than to compute twice.
-//   rows pass     S[row][key]: a tile of 128 query rows stays in shared memory, K tiles of
-//                 128 keys stream by; a thread owns a row and keeps its running max m and
-//                 sum l.  Few rows: the keys are cut into ranges, one (m, l) each.
-//   columns pass  S^T[key][row]: a tile of 128 keys stays, the query tiles stream by; a
-//                 thread owns a key, so a weight is a sum within one thread, in a fixed
-//                 order and without atomics: w += 2^(s - m_row) / l_row.  Each row's
-//                 (m, 1 / l) comes from shared memory, the same for all lanes.
-// A row is a (query, head) pair of one kv head's group; a query tile is a TMA box of hb
-// heads x nq queries, so any group size and any stride of q goes.
+//   rows pass     S[row][key]: four tiles of 128 query rows are held in shared memory, K
+//                 tiles of 128 keys stream by; a thread owns a row and keeps its running
+//                 max m and sum l.  Few rows: the keys are cut into ranges, one (m, l) each.
+//   columns pass  S^T[key][row]: a thread owns a key and sums 2^(s - m_row) / l_row over the
+//                 rows, in a fixed order and without atomics; each row's (-m, 1 / l) comes
+//                 from shared memory, the same for all lanes.  Up to four row tiles (FEW):
+//                 they are held and the keys stream, each once.  More (MANY): two key tiles
+//                 are held, the row tiles stream, and a CTA goes from one pair of key tiles
+//                 to the next.
+// A row is a (query, head) pair of one kv head's group; a row tile is a TMA box of hb heads x
+// nq queries, so any group size and any stride of q goes.
 //
-// One kernel body does both: "held" tiles (HELD of them, one consumer warpgroup each) and
-// a ring of streamed tiles.  Warp 0 loads, warp 1 issues the MMAs into two S buffers a
-// held tile, warp 2 fetches the rows' (m, 1 / l) for the columns pass, warps 4 .. are the
-// consumers.  Every hand-off is an mbarrier; every wait is bounded and gives up early once
-// another role has raised the CTA's abort flag.
+// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-19 are four consumer warpgroups:
+// in the rows pass one a row tile, in the columns pass each takes 32 of a row tile's 128
+// rows, and warps 2 and 3 add the four sums of a key and update the pool.  (Two warpgroups,
+// a whole tile each, kept the exponentials' pipe 20 to 46% busy: a warp's chain of tensor
+// memory loads, maximum and sum leaves it idle.)  Every hand-off is an mbarrier; every wait
+// is bounded and gives up early once another role has raised the CTA's abort flag.
 //
-// Bound: the exponentials, two of them a pair (MUFU, 32 a cycle and SM), for chunks of
-// many rows; K's bytes for few.
+// Bound: the exponentials, two of them a pair (MUFU), for chunks of many rows; K's bytes,
+// read twice, for few.
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -38,53 +41,105 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
 constexpr int kRows = 128;                  // rows or keys of a tile
+constexpr int kThreads = 640;
+constexpr int kGroups = 4;                  // consumer warpgroups
+enum Pass { kRowsPass, kFew, kMany };
 
 struct WeightsParams {
   const int32_t *block_table, *ctx_lens;
   float *weights;
-  float2 *stats;  // [sequence x kv head][row tile][range][128]: m (log2), l
+  float2 *states;  // [sequence x kv head][row tile][range][128]: m (log2), l
+  float *stats;    // [sequence x kv head][row tile][2][128]: -m, then 1 / l
   int *status;
-  float qscale;   // scale * log2 e
+  float qscale;    // scale * log2 e
   int n_new, n_kv_heads, group, hb, nq, n_hsub, n_rt, batch, max_blocks, num_pages, fresh;
-  int n_ranges;   // key ranges of the rows pass
-  int groups;     // held-tile groups a (sequence, kv head) has
+  int n_ranges;    // key ranges of the rows pass
+  int key_ranges;  // of the columns pass (FEW)
+  int groups;      // row tile groups (rows pass), key tile pairs (MANY) of a list
+  int items;       // lists x groups (MANY)
 };
 
-template <int D, int HELD>
+template <int D, int PASS>
 struct WeightsSmem {
-  static constexpr int kStages = HELD == 2 ? 4 : 2;
+  static constexpr int kHeldTiles = PASS == kMany ? 2 : 4;
+  static constexpr int kStages = D == 128 && PASS != kMany ? 2 : 4;
   static constexpr int kColBlk = kRows * 128;          // one 64-column block
   static constexpr int kTile = (D / 64) * kColBlk;
-  static constexpr int kHeld = 0;
-  static constexpr int kRing = HELD * kTile;
-  static constexpr int kM = kRing + kStages * kTile;   // [stage][128]: -m
-  static constexpr int kL = kM + kStages * kRows * 4;  // 1 / l
-  static constexpr int kLim = kL + kStages * kRows * 4;  // last key the row sees
-  static constexpr int kBars = kLim + kStages * kRows * 4;
-  static constexpr int kSlot = kBars + 32 * 8;         // TMEM address, abort flag
+  static constexpr int kRing = kHeldTiles * kTile;
+  // [row tile or stage][2][128]: -m, 1 / l
+  static constexpr int kStats = kRing + kStages * kTile;
+  static constexpr int kPart = kStats + 4 * 2 * kRows * 4;    // [2][group][keys] sums
+  static constexpr int kPartKeys = PASS == kMany ? 2 * kRows : kRows;
+  static constexpr int kBars = kPart + 2 * kGroups * kPartKeys * 4;
+  static constexpr int kSlot = kBars + 24 * 8;                // TMEM address, abort flag
   static constexpr int kAlloc = kSlot + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory of an SM");
 };
 
 enum {
-  kBarFull = 0,   // ring stage s landed
-  kBarFree = 4,   // ring stage s read by the MMAs (commit)
-  kBarHeld = 8,   // the held tiles landed
-  kBarS = 9,      // S buffer 2 x + (j & 1) complete (commit)
-  kBarSFree = 13, // S buffer read (one arrival a consumer warp of x)
-  kBarT = 17,     // the rows' (m, 1 / l) of stage s are there
-  kBarTFree = 21, // .. have been read (one arrival a consumer warp)
-  kBarDrain = 25,
-  kNumBars = 26
+  kBarFull = 0,       // ring stage s landed
+  kBarFree = 4,       // ring stage s read (commit; MANY: and the consumers' warps)
+  kBarHeld = 8,       // the held tiles landed
+  kBarHeldFree = 9,   // MANY: .. have been read by the pair's last MMA (commit)
+  kBarS = 10,         // S buffer complete (commit)
+  kBarSFree = 14,     // S buffer read (one arrival a warp that reads it)
+  kBarT = 18,         // FEW: the rows' statistics are there (one arrival an aux warp)
+  kBarPart = 19,      // columns: the sums of buffer 0 / 1 are written (16 warps)
+  kBarPartFree = 21,  // .. have been read (2 warps)
+  kBarDrain = 23,
+  kNumBars = 24
 };
 
-// What a CTA does.
+// What a CTA does at a time.
 struct Job {
-  int b, g, ctx, T;  // T = ctx + n_new
-  int held0;         // first held tile: row tile, or key tile
-  int s0, n;         // first streamed tile, how many
+  int b, g, bg, ctx, T;  // T = ctx + n_new
+  int held0, n_held;     // held tiles: row tiles, or (MANY) key tiles
+  int s0, n;             // streamed tiles
   int range;
 };
+
+// Job number `at`; n = 0: nothing to do.
+template <int PASS>
+__device__ __forceinline__ Job job_of(const WeightsParams &p, int at, bool report) {
+  Job w;
+  if (PASS == kMany) {
+    w.bg = at / p.groups;
+    w.held0 = (at - w.bg * p.groups) * 2;
+    w.n_held = 2;
+    w.range = 0;
+  } else {
+    const int ranges = PASS == kRowsPass ? p.n_ranges : p.key_ranges;
+    w.range = at % ranges;
+    at /= ranges;
+    w.bg = at / p.groups;
+    w.held0 = (at - w.bg * p.groups) * 4;
+    w.n_held = min(4, p.n_rt - w.held0);
+  }
+  w.b = w.bg / p.n_kv_heads;
+  w.g = w.bg - w.b * p.n_kv_heads;
+  w.ctx = p.ctx_lens[w.b];
+  const int most = p.max_blocks * kPageSize - p.n_new;
+  if (w.ctx < 0 || w.ctx > most) {
+    if (report) record_error(p.status, PA_ERR_BAD_CTX);
+    w.ctx = w.ctx < 0 ? 0 : most;
+  }
+  w.T = w.ctx + p.n_new;
+  if (PASS == kMany) {
+    // row tiles whose last query sees the first held key
+    const int q = max(0, w.held0 * kRows - w.ctx);
+    w.s0 = q / p.nq * p.n_hsub;
+    w.n = w.held0 * kRows < w.T ? p.n_rt - w.s0 : 0;
+  } else {
+    // key tiles that the held rows see, cut into ranges
+    const int ranges = PASS == kRowsPass ? p.n_ranges : p.key_ranges;
+    const int last_q = min(p.n_new, ((w.held0 + w.n_held - 1) / p.n_hsub + 1) * p.nq) - 1;
+    const int tiles = (w.ctx + last_q) / kRows + 1;
+    const int per = (tiles + ranges - 1) / ranges;
+    w.s0 = w.range * per;
+    w.n = max(0, min(per, tiles - w.s0));
+  }
+  return w;
+}
 
 // One K tile (8 pages of one kv head) into shared memory.  The whole warp.
 template <int D>
@@ -93,7 +148,7 @@ __device__ __forceinline__ void load_keys(const CUtensorMap *map, const WeightsP
                                           int lane) {
   const int n_pages = (w.T + kPageSize - 1) / kPageSize;
   if (lane < 8) {
-    const int pg = 8 * tile + lane;
+    const int pg = 8 * tile + lane;  // past the end: page 0, masked
     int id = pg < n_pages ? p.block_table[static_cast<size_t>(w.b) * p.max_blocks + pg] : 0;
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
       record_error(p.status, PA_ERR_BAD_BLOCK);
@@ -134,11 +189,99 @@ __device__ __forceinline__ int query_of(const WeightsParams &p, int rt, int r) {
   return r < p.hb * p.nq && q < p.n_new ? q : -1;
 }
 
-template <int D, bool BF16, int HELD, bool COLUMNS>
-__global__ void __launch_bounds__(128 + 128 * HELD, HELD == 2 ? 1 : 2)
+// A row's ranges folded: (-m, 1 / l); (0, 0) for no row.
+__device__ __forceinline__ float2 folded(const WeightsParams &p, int bg, int rt, int r) {
+  if (query_of(p, rt, r) < 0) return make_float2(0.f, 0.f);
+  const float2 *st =
+      p.states + (static_cast<size_t>(bg) * p.n_rt + rt) * p.n_ranges * kRows + r;
+  float m = kNoKey, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.n_ranges; ++i) {
+    const float2 v = st[static_cast<size_t>(i) * kRows];
+    const float mn = fmaxf(m, v.x);
+    l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
+    m = mn;
+  }
+  return make_float2(-m, l == 0.f ? 0.f : 1.f / l);
+}
+
+// ---- rows pass: 64 scores of this thread's row at a time
+struct RowState {
+  float m;
+  float2 l;
+};
+__device__ __forceinline__ void take_scores(uint32_t (&s)[64], int key0, int lim, int lim_all,
+                                            float qs, RowState &st) {
+  // the maximum of s qs (a negative scale: from the least s); masked keys never win
+  auto extreme = [&](auto pick, float worst) {
+    if (key0 + 63 > lim_all) {
+      const int last = lim - key0;
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        if (c > last) s[c] = __float_as_uint(worst);
+    }
+    float t0 = worst, t1 = worst;
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+      t0 = pick(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      t1 = pick(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+    }
+    return pick(t0, t1, t1);
+  };
+  const float cand =
+      qs * (qs > 0.f ? extreme([](float a, float b, float c) { return max3(a, b, c); }, -INFINITY)
+                     : extreme([](float a, float b, float c) { return fminf(fminf(a, b), c); },
+                               INFINITY));
+  if (cand > st.m + kSlack) {
+    const float corr = ex2(st.m - cand);
+    st.m = cand;
+    st.l = __fmul2_rn(st.l, make_float2(corr, corr));
+  }
+  const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(-st.m, -st.m);
+  float2 e2 = make_float2(0.f, 0.f), f2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < 64; c += 4) {
+    const float2 a = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                qs2, nm2);
+    const float2 b = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                qs2, nm2);
+    e2 = __fadd2_rn(e2, make_float2(ex2(a.x), ex2(a.y)));
+    f2 = __fadd2_rn(f2, make_float2(ex2(b.x), ex2(b.y)));
+  }
+  st.l = __fadd2_rn(st.l, __fadd2_rn(e2, f2));
+}
+
+// ---- columns pass: the weights of 32 rows for this thread's key, added to `sum`.  am: the
+// rows' -m in shared memory, 1 / l behind the tile's 128; rows from `from` on see the key.
+template <bool MASKED>
+__device__ __forceinline__ void add_weights(const uint32_t (&s)[32], uint32_t am, int from,
+                                            float qs, float2 &sum, float2 &other) {
+  const float2 qs2 = make_float2(qs, qs);
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const uint4 m4 = lds128(am + c * 4), l4 = lds128(am + kRows * 4 + c * 4);
+    const float2 a = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                qs2, make_float2(__uint_as_float(m4.x), __uint_as_float(m4.y)));
+    const float2 b = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                qs2, make_float2(__uint_as_float(m4.z), __uint_as_float(m4.w)));
+    float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
+    if (MASKED) {
+      if (c < from) ea.x = 0.f;
+      if (c + 1 < from) ea.y = 0.f;
+      if (c + 2 < from) eb.x = 0.f;
+      if (c + 3 < from) eb.y = 0.f;
+    }
+    sum = __ffma2_rn(ea, make_float2(__uint_as_float(l4.x), __uint_as_float(l4.y)), sum);
+    other = __ffma2_rn(eb, make_float2(__uint_as_float(l4.z), __uint_as_float(l4.w)), other);
+  }
+}
+
+template <int D, bool BF16, int PASS>
+__global__ void __launch_bounds__(kThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const WeightsParams p) {
-  using L = WeightsSmem<D, HELD>;
+  using L = WeightsSmem<D, PASS>;
+  constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -148,65 +291,38 @@ __global__ void __launch_bounds__(128 + 128 * HELD, HELD == 2 ? 1 : 2)
   griddep_release();
   griddep_wait();
 
-  Job w;
-  {
-    int at = blockIdx.x;
-    w.range = COLUMNS ? 0 : at % p.n_ranges;
-    if (!COLUMNS) at /= p.n_ranges;
-    const int bg = at / p.groups;
-    w.held0 = (at - bg * p.groups) * HELD;
-    w.b = bg / p.n_kv_heads;
-    w.g = bg - w.b * p.n_kv_heads;
-    w.ctx = p.ctx_lens[w.b];
-    const int most = p.max_blocks * kPageSize - p.n_new;
-    if (w.ctx < 0 || w.ctx > most) {
-      if (tid == 0) record_error(p.status, PA_ERR_BAD_CTX);
-      w.ctx = w.ctx < 0 ? 0 : most;
-    }
-    w.T = w.ctx + p.n_new;
-    if (COLUMNS) {
-      if (w.held0 * kRows >= w.T) return;
-      // query tiles whose last query sees the first held key
-      const int q = max(0, w.held0 * kRows - w.ctx);
-      w.s0 = q / p.nq * p.n_hsub;
-      w.n = p.n_rt - w.s0;
-    } else {
-      // key tiles that the held rows see, cut into ranges
-      const int last_rt = min(w.held0 + HELD, p.n_rt) - 1;
-      const int last_q = min(p.n_new, (last_rt / p.n_hsub + 1) * p.nq) - 1;
-      const int tiles = (w.ctx + last_q) / kRows + 1;
-      const int per = (tiles + p.n_ranges - 1) / p.n_ranges;
-      w.s0 = w.range * per;
-      w.n = max(0, min(per, tiles - w.s0));
-      if (w.n == 0) {  // nothing of the keys is left for this range
-        for (int e = tid; e < HELD * kRows; e += blockDim.x) {
-          const int rt = w.held0 + e / kRows;
-          if (rt < p.n_rt)
-            p.stats[((static_cast<size_t>(bg) * p.n_rt + rt) * p.n_ranges + w.range) * kRows +
-                    e % kRows] = make_float2(kNoKey, 0.f);
-        }
-        return;
-      }
-    }
+  Job w = job_of<PASS>(p, blockIdx.x, tid == 0);
+  if (PASS != kMany && w.n == 0) {  // nothing of the keys is left for this range
+    if (PASS == kRowsPass)
+      for (int e = tid; e < w.n_held * kRows; e += kThreads)
+        p.states[((static_cast<size_t>(w.bg) * p.n_rt + w.held0 + e / kRows) * p.n_ranges +
+                  w.range) * kRows + e % kRows] = make_float2(kNoKey, 0.f);
+    return;
   }
 
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kSlot + 4);
   if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i >= kBarSFree && i < kBarT ? 4
-                        : i >= kBarTFree && i < kBarDrain ? 4 * HELD : 1);
+    for (int i = 0; i < kNumBars; ++i) {
+      int n = 1;
+      if (i >= kBarFree && i < kBarHeld) n = PASS == kMany ? 1 + 4 * kGroups : 1;
+      if (i >= kBarSFree && i < kBarT) n = PASS == kRowsPass ? 4 : 4 * kGroups;
+      if (i == kBarT || i >= kBarPartFree) n = 2;
+      if (i == kBarPart || i == kBarPart + 1) n = 4 * kGroups;
+      if (i == kBarDrain) n = 1;
+      mbar_init(bar(i), n);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tc::alloc(sb + L::kSlot, 256 * HELD);
+    tc::alloc(sb + L::kSlot, 512);
     tc::relinquish();
   }
   // Rows of a query tile behind its box are never written by the copies: they hold zeros.
   if (p.hb * p.nq < kRows) {
     const int r0 = p.hb * p.nq, rows = kRows - r0;
-    const int first = COLUMNS ? L::kRing : L::kHeld, n = COLUMNS ? L::kStages : HELD;
-    for (int e = tid; e < n * (D / 64) * rows * 8; e += blockDim.x) {
+    const int first = PASS == kMany ? L::kRing : 0, n = PASS == kMany ? S : L::kHeldTiles;
+    for (int e = tid; e < n * (D / 64) * rows * 8; e += kThreads) {
       const int blk = e / (rows * 8), in = e - blk * rows * 8;
       st_shared_v4(sb + first + blk * L::kColBlk + (r0 + in / 8) * 128 + (in % 8) * 16, 0u, 0u,
                    0u, 0u);
@@ -218,65 +334,100 @@ __global__ void __launch_bounds__(128 + 128 * HELD, HELD == 2 ? 1 : 2)
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
   const uint32_t q_bytes = (D / 64) * p.hb * p.nq * 128;
+  const uint32_t stats_bytes = 2 * kRows * sizeof(float);
+  // the jobs of a CTA: one, or (MANY) every gridDim.x-th item
+  auto next_job = [&](int &at) {
+    for (at += gridDim.x; PASS == kMany && at < p.items; at += gridDim.x) {
+      w = job_of<PASS>(p, at, false);
+      if (w.n > 0) return true;
+    }
+    return false;
+  };
+  int at = blockIdx.x;
+  bool more = true;
+  if (PASS == kMany && w.n == 0) more = next_job(at);
 
   if (warp == 0) {
-    // ---- loads: the held tiles, then the ring
+    // ---- loads
     bool ok = true;
-    if (lane == 0) mbar_arrive_expect_tx(bar(kBarHeld), HELD * (COLUMNS ? L::kTile : q_bytes));
-    __syncwarp();
-    for (int x = 0; x < HELD; ++x) {
-      const uint32_t dst = sb + L::kHeld + x * L::kTile;
-      if (COLUMNS)
-        load_keys<D>(&kmap, p, w, w.held0 + x, dst, bar(kBarHeld), lane);
-      else if (lane == 0)
-        // (a row tile past the last one reads it again; its rows are dropped)
-        load_queries<D>(&qmap, p, w, min(w.held0 + x, p.n_rt - 1), dst, bar(kBarHeld));
-    }
-    int j = 0;
-    for (; j < w.n; ++j) {
-      const int s = j % L::kStages;
-      if (j >= L::kStages &&
-          !(ok = warp_wait(bar(kBarFree + s), ((j / L::kStages) - 1) & 1, abort_flag)))
+    int c = 0, job = 0;  // tiles streamed, jobs done
+    for (; more && ok; more = next_job(at), ++job) {
+      if (PASS == kMany && job > 0 &&
+          !(ok = warp_wait(bar(kBarHeldFree), (job - 1) & 1, abort_flag)))
         break;
-      if (lane == 0) mbar_arrive_expect_tx(bar(kBarFull + s), COLUMNS ? q_bytes : L::kTile);
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar(kBarHeld), w.n_held * (PASS == kMany ? L::kTile : q_bytes));
       __syncwarp();
-      const uint32_t dst = sb + L::kRing + s * L::kTile;
-      if (!COLUMNS)
-        load_keys<D>(&kmap, p, w, w.s0 + j, dst, bar(kBarFull + s), lane);
-      else if (lane == 0)
-        load_queries<D>(&qmap, p, w, w.s0 + j, dst, bar(kBarFull + s));
+      for (int x = 0; x < w.n_held; ++x) {
+        if (PASS == kMany)
+          load_keys<D>(&kmap, p, w, w.held0 + x, sb + x * L::kTile, bar(kBarHeld), lane);
+        else if (lane == 0)
+          load_queries<D>(&qmap, p, w, w.held0 + x, sb + x * L::kTile, bar(kBarHeld));
+      }
+      for (int j = 0; j < w.n; ++j, ++c) {
+        const int s = c % S;
+        if (c >= S && !(ok = warp_wait(bar(kBarFree + s), ((c / S) - 1) & 1, abort_flag))) break;
+        const uint32_t full = bar(kBarFull + s), dst = sb + L::kRing + s * L::kTile;
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, PASS == kMany ? q_bytes + stats_bytes : L::kTile);
+        __syncwarp();
+        if (PASS != kMany) {
+          load_keys<D>(&kmap, p, w, w.s0 + j, dst, full, lane);
+        } else if (lane == 0) {
+          load_queries<D>(&qmap, p, w, w.s0 + j, dst, full);
+          bulk_load(sb + L::kStats + s * stats_bytes,
+                    p.stats + (static_cast<size_t>(w.bg) * p.n_rt + w.s0 + j) * 2 * kRows,
+                    stats_bytes, full);
+        }
+      }
     }
     if (!ok) {
       if (lane == 0) raise_abort(p.status, abort_flag);
-      mbar_wait(bar(kBarHeld), 0);  // copies in flight still land
-      for (int t = max(0, j - L::kStages); t < j; ++t)
-        mbar_wait(bar(kBarFull + t % L::kStages), (t / L::kStages) & 1);
+      mbar_wait(bar(kBarHeld), job & 1);  // copies in flight still land
+      for (int t = max(0, c - S); t < c; ++t) mbar_wait(bar(kBarFull + t % S), (t / S) & 1);
     }
   } else if (warp == 1) {
-    // ---- S of every held tile against each streamed one
+    // ---- S of every held tile against each streamed one; the keys' tile is the first
+    // operand in the columns pass, the rows' in the rows pass
     constexpr uint32_t kId = tc::idesc_f16(BF16, kRows, kRows, false, false);
-    const uint64_t held = tc::smem_desc_sw128(sb + L::kHeld, 16, 1024);
+    const uint64_t held = tc::smem_desc_sw128(sb, 16, 1024);
     const uint64_t ring = tc::smem_desc_sw128(sb + L::kRing, 16, 1024);
-    bool ok = warp_wait(bar(kBarHeld), 0, abort_flag);
-    for (int j = 0; j < w.n && ok; ++j) {
-      const int s = j % L::kStages;
-      if (!(ok = warp_wait(bar(kBarFull + s), (j / L::kStages) & 1, abort_flag))) break;
-      for (int x = 0; x < HELD && ok; ++x) {
-        const int buf = 2 * x + (j & 1);
-        if (j >= 2 && !(ok = warp_wait(bar(kBarSFree + buf), ((j >> 1) - 1) & 1, abort_flag)))
+    bool ok = true;
+    int c = 0, job = 0;
+    for (; more && ok; more = next_job(at), ++job) {
+      ok = warp_wait(bar(kBarHeld), job & 1, abort_flag);
+      for (int j = 0; j < w.n && ok; ++j, ++c) {
+        const int s = c % S;
+        if (!(ok = warp_wait(bar(kBarFull + s), (c / S) & 1, abort_flag))) break;
+        // MANY: both held tiles' scores go to one of two pairs of buffers
+        if (PASS == kMany && c >= 2 &&
+            !(ok = warp_wait(bar(kBarSFree + (c & 1)), ((c >> 1) - 1) & 1, abort_flag)))
           break;
-        tc::fence_after_sync();
-        if (lane == 0) {
+        for (int x = 0; x < w.n_held && ok; ++x) {
+          const int buf = PASS == kMany ? 2 * (c & 1) + x : x;
+          if (PASS != kMany && c >= 1 &&
+              !(ok = warp_wait(bar(kBarSFree + x), (c - 1) & 1, abort_flag)))
+            break;
+          tc::fence_after_sync();
+          if (lane == 0) {
+            const uint64_t h = held + ((x * L::kTile) >> 4), r = ring + ((s * L::kTile) >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = ((k >> 2) * L::kColBlk + (k & 3) * 32) >> 4;
-            tc::mma_f16(tmem + buf * kRows, held + ((x * L::kTile) >> 4) + off,
-                        ring + ((s * L::kTile) >> 4) + off, kId, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = ((k >> 2) * L::kColBlk + (k & 3) * 32) >> 4;
+              tc::mma_f16(tmem + buf * kRows, (PASS == kFew ? r : h) + off,
+                          (PASS == kFew ? h : r) + off, kId, k > 0);
+            }
+            if (PASS != kMany) tc::commit(bar(kBarS + x));
+            if (x == w.n_held - 1) {
+              if (PASS == kMany) {
+                tc::commit(bar(kBarS + (c & 1)));
+                if (j == w.n - 1) tc::commit(bar(kBarHeldFree));
+              }
+              tc::commit(bar(kBarFree + s));
+            }
           }
-          tc::commit(bar(kBarS + buf));
-          if (x == HELD - 1) tc::commit(bar(kBarFree + s));
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (!ok) {
@@ -287,178 +438,171 @@ __global__ void __launch_bounds__(128 + 128 * HELD, HELD == 2 ? 1 : 2)
       __syncwarp();
       mbar_wait(bar(kBarDrain), 0);
     }
-  } else if (COLUMNS && warp == 2) {
-    // ---- (-m, 1 / l) of the streamed tiles' rows, and the last key each one sees
-    float *sm = reinterpret_cast<float *>(smem + L::kM);
-    float *sl = reinterpret_cast<float *>(smem + L::kL);
-    int *slim = reinterpret_cast<int *>(smem + L::kLim);
-    const float2 *stats =
-        p.stats + static_cast<size_t>(w.b * p.n_kv_heads + w.g) * p.n_rt * p.n_ranges * kRows;
-    bool ok = true;
-    for (int j = 0; j < w.n; ++j) {
-      const int s = j % L::kStages, rt = w.s0 + j;
-      if (j >= L::kStages &&
-          !(ok = warp_wait(bar(kBarTFree + s), ((j / L::kStages) - 1) & 1, abort_flag)))
-        break;
-#pragma unroll
-      for (int k = 0; k < kRows / 32; ++k) {
-        const int r = lane + 32 * k, q = query_of(p, rt, r);
-        const float2 *st = stats + static_cast<size_t>(rt) * p.n_ranges * kRows + r;
-        float m = kNoKey, l = 0.f;
-        if (q >= 0)
-          for (int i = 0; i < p.n_ranges; ++i) {
-            const float2 v = st[i * kRows];
-            const float mn = fmaxf(m, v.x);
-            l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
-            m = mn;
-          }
-        sm[s * kRows + r] = q >= 0 ? -m : 0.f;
-        sl[s * kRows + r] = l == 0.f ? 0.f : 1.f / l;
-        slim[s * kRows + r] = w.ctx + q;
+  } else if (warp < 4) {
+    if (PASS != kRowsPass) {
+      // ---- (FEW: the rows' statistics, then) the consumers' sums into the pool
+      bool ok = true;
+      if (PASS == kFew) {
+        float *st = reinterpret_cast<float *>(smem + L::kStats);
+        for (int e = tid - 64; e < w.n_held * kRows; e += 64) {
+          const int rt = e / kRows, r = e % kRows;
+          const float2 v = folded(p, w.bg, rt, r);
+          st[rt * 2 * kRows + r] = v.x;
+          st[rt * 2 * kRows + kRows + r] = v.y;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarT));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarT + s));
+      int n = 0;  // sums taken
+      for (; more && ok; more = next_job(at)) {
+        for (int j = 0; j < (PASS == kFew ? w.n : 1); ++j, ++n) {
+          const int key0 = (PASS == kFew ? w.s0 + j : w.held0) * kRows;
+          float *dst[L::kPartKeys / 64];
+          float old[L::kPartKeys / 64];
+#pragma unroll
+          for (int u = 0; u < L::kPartKeys / 64; ++u) {
+            const int key = key0 + tid - 64 + 64 * u;
+            dst[u] = nullptr;
+            old[u] = 0.f;
+            if (key >= w.T) continue;
+            const int page =
+                p.block_table[static_cast<size_t>(w.b) * p.max_blocks + key / kPageSize];
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages))
+              continue;  // reported
+            dst[u] = p.weights + (static_cast<size_t>(page) * p.n_kv_heads + w.g) * kPageSize +
+                     key % kPageSize;
+            if (key < w.T - p.fresh) old[u] = *dst[u];
+          }
+          if (!(ok = warp_wait(bar(kBarPart + (n & 1)), (n >> 1) & 1, abort_flag))) break;
+          const float *part = reinterpret_cast<const float *>(smem + L::kPart) +
+                              (n & 1) * kGroups * L::kPartKeys + tid - 64;
+#pragma unroll
+          for (int u = 0; u < L::kPartKeys / 64; ++u) {
+            float sum = 0.f;
+#pragma unroll
+            for (int y = 0; y < kGroups; ++y) sum += part[y * L::kPartKeys + 64 * u];
+            if (dst[u]) *dst[u] = old[u] + sum;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarPartFree + (n & 1)));
+        }
+      }
+      if (!ok && lane == 0) raise_abort(p.status, abort_flag);
     }
-    if (!ok && lane == 0) raise_abort(p.status, abort_flag);
-  } else if (warp >= 4) {
-    // ---- consumers: lane r of held tile x is a row, or a key
-    const int x = (warp - 4) >> 2, r = ((warp & 3) << 5) + lane;
+  } else {
+    // ---- consumers
+    const int y = (warp - 4) >> 2, r = ((warp & 3) << 5) + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float qs = p.qscale;
     bool ok = true;
-    if constexpr (!COLUMNS) {
-      const int rt = w.held0 + x;
-      const int q = query_of(p, rt, r);
-      const int lim = w.ctx + max(q, 0);                            // last key row r sees
-      const int lim_all = w.ctx + min(rt / p.n_hsub * p.nq, p.n_new - 1);  // every row of x does
-      float m = kNoKey;
-      float2 l2 = make_float2(0.f, 0.f);
-      for (int j = 0; j < w.n; ++j) {
-        const int buf = 2 * x + (j & 1);
-        if (!(ok = warp_wait(bar(kBarS + buf), (j >> 1) & 1, abort_flag))) break;
-        tc::fence_after_sync();
-        uint32_t s[kRows];
+    if constexpr (PASS == kRowsPass) {
+      if (y < w.n_held) {
+        const int rt = w.held0 + y, q = query_of(p, rt, r);
+        const int lim = w.ctx + max(q, 0);                      // last key row r sees
+        const int lim_all = w.ctx + rt / p.n_hsub * p.nq;       // every row of the tile does
+        RowState st = {kNoKey, make_float2(0.f, 0.f)};
+        for (int j = 0; j < w.n; ++j) {
+          if (!(ok = warp_wait(bar(kBarS + y), j & 1, abort_flag))) break;
+          tc::fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tc::ld32(tmem + buf * kRows + lanes + 32 * c,
-                   *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-        tc::wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
-        const int key0 = (w.s0 + j) * kRows;
-        float cand;
-        // the maximum of s qs (a negative scale: from the least s); masked keys never win
-        auto extreme = [&](auto pick, float worst) {
-          if (key0 + kRows - 1 > lim_all) {
-            const int last = lim - key0;
-#pragma unroll
-            for (int c = 0; c < kRows; ++c)
-              if (c > last) s[c] = __float_as_uint(worst);
-          }
-          float t0 = worst, t1 = worst, t2 = worst, t3 = worst;
-#pragma unroll
-          for (int c = 0; c < kRows; c += 8) {
-            t0 = pick(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            t1 = pick(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-            t2 = pick(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-            t3 = pick(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-          }
-          return pick(pick(t0, t1, t2), t3, t3);
-        };
-        if (qs >= 0.f)
-          cand = extreme([](float a, float b, float c) { return max3(a, b, c); }, -INFINITY);
-        else
-          cand = extreme([](float a, float b, float c) { return fminf(fminf(a, b), c); }, INFINITY);
-        cand *= qs;  // (qs = 0: 0, or NaN where no key was seen)
-        if (cand > m + kSlack) {
-          const float corr = ex2(m - cand);
-          m = cand;
-          l2 = __fmul2_rn(l2, make_float2(corr, corr));
-        }
-        const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(-m, -m);
-        float2 e2 = make_float2(0.f, 0.f), f2 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kRows; c += 4) {
-          const float2 a = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                      qs2, nm2);
-          const float2 b = __ffma2_rn(
-              make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), qs2, nm2);
-          e2 = __fadd2_rn(e2, make_float2(ex2(a.x), ex2(a.y)));
-          f2 = __fadd2_rn(f2, make_float2(ex2(b.x), ex2(b.y)));
-        }
-        l2 = __fadd2_rn(l2, __fadd2_rn(e2, f2));
-      }
-      if (ok && rt < p.n_rt)
-        p.stats[((static_cast<size_t>(w.b * p.n_kv_heads + w.g) * p.n_rt + rt) * p.n_ranges +
-                 w.range) * kRows + r] = make_float2(m, l2.x + l2.y);
-    } else {
-      const int key = (w.held0 + x) * kRows + r;
-      const int key_end = (w.held0 + x) * kRows + kRows - 1;
-      float2 sum = make_float2(0.f, 0.f);
-      for (int j = 0; j < w.n; ++j) {
-        const int buf = 2 * x + (j & 1), st = j % L::kStages, rt = w.s0 + j;
-        if (!(ok = warp_wait2(bar(kBarS + buf), (j >> 1) & 1, bar(kBarT + st),
-                              (j / L::kStages) & 1, abort_flag)))
-          break;
-        tc::fence_after_sync();
-        // every row of the tile sees every key of this one?
-        const bool all = key_end <= w.ctx + rt / p.n_hsub * p.nq;
-        const uint32_t am = sb + L::kM + st * kRows * 4, al = sb + L::kL + st * kRows * 4;
-        const uint32_t alim = sb + L::kLim + st * kRows * 4;
-        float2 part = make_float2(0.f, 0.f), other = make_float2(0.f, 0.f);
-        const float2 qs2 = make_float2(qs, qs);
-#pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 32) {
-          uint32_t s[32];
-          tc::ld32(tmem + buf * kRows + lanes + c0, s);
-          tc::wait_ld();
-          if (c0 == kRows - 32) {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
-          }
-          auto add = [&](auto masked) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const uint4 m4 = lds128(am + (c0 + c) * 4), l4 = lds128(al + (c0 + c) * 4);
-              const float2 a = __ffma2_rn(
-                  make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), qs2,
-                  make_float2(__uint_as_float(m4.x), __uint_as_float(m4.y)));
-              const float2 b = __ffma2_rn(
-                  make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), qs2,
-                  make_float2(__uint_as_float(m4.z), __uint_as_float(m4.w)));
-              float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
-              if constexpr (decltype(masked)::value) {
-                const uint4 k4 = lds128(alim + (c0 + c) * 4);
-                if (key > static_cast<int>(k4.x)) ea.x = 0.f;
-                if (key > static_cast<int>(k4.y)) ea.y = 0.f;
-                if (key > static_cast<int>(k4.z)) eb.x = 0.f;
-                if (key > static_cast<int>(k4.w)) eb.y = 0.f;
-              }
-              part = __ffma2_rn(ea, make_float2(__uint_as_float(l4.x), __uint_as_float(l4.y)),
-                                part);
-              other = __ffma2_rn(eb, make_float2(__uint_as_float(l4.z), __uint_as_float(l4.w)),
-                                 other);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[64];
+            tc::ld32(tmem + y * kRows + lanes + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tc::ld32(tmem + y * kRows + lanes + 64 * h + 32,
+                     *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            tc::wait_ld();
+            if (h == 1) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(kBarSFree + y));
             }
-          };
-          if (all)
-            add(std::false_type{});
-          else
-            add(std::true_type{});
+            take_scores(s, (w.s0 + j) * kRows + 64 * h, lim, lim_all, qs, st);
+          }
         }
-        sum = __fadd2_rn(sum, __fadd2_rn(part, other));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarTFree + st));
+        if (ok) {
+          const float l = st.l.x + st.l.y;
+          const size_t tile = static_cast<size_t>(w.bg) * p.n_rt + rt;
+          p.states[(tile * p.n_ranges + w.range) * kRows + r] = make_float2(st.m, l);
+          if (p.n_ranges == 1) {
+            p.stats[tile * 2 * kRows + r] = q < 0 ? 0.f : -st.m;
+            p.stats[tile * 2 * kRows + kRows + r] = q < 0 || l == 0.f ? 0.f : 1.f / l;
+          }
+        }
       }
-      if (ok && key < w.T) {
-        const int page =
-            p.block_table[static_cast<size_t>(w.b) * p.max_blocks + key / kPageSize];
-        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {  // else reported
-          float *dst = p.weights + (static_cast<size_t>(page) * p.n_kv_heads + w.g) * kPageSize +
-                       key % kPageSize;
-          *dst = (key < w.T - p.fresh ? *dst : 0.f) + (sum.x + sum.y);
+    } else if constexpr (PASS == kFew) {
+      float *part = reinterpret_cast<float *>(smem + L::kPart) + y * kRows + r;
+      ok = warp_wait(bar(kBarT), 0, abort_flag);
+      for (int j = 0; j < w.n && ok; ++j) {
+        const int key0 = (w.s0 + j) * kRows, key = key0 + r;
+        float2 sum = make_float2(0.f, 0.f), other = make_float2(0.f, 0.f);
+        for (int x = 0; x < w.n_held; ++x) {
+          if (!(ok = warp_wait(bar(kBarS + x), j & 1, abort_flag))) break;
+          tc::fence_after_sync();
+          uint32_t s[32];
+          tc::ld32(tmem + x * kRows + lanes + 32 * y, s);
+          tc::wait_ld();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarSFree + x));
+          const uint32_t am = sb + L::kStats + x * stats_bytes + 32 * y * 4;
+          const int q0 = x / p.n_hsub * p.nq;  // the tile's first query
+          if (key0 + kRows - 1 <= w.ctx + q0)
+            add_weights<false>(s, am, 0, qs, sum, other);
+          else
+            add_weights<true>(s, am, (key - w.ctx - q0) * p.hb - 32 * y, qs, sum, other);
         }
+        if (!ok) break;
+        if (j >= 2 && !(ok = warp_wait(bar(kBarPartFree + (j & 1)), ((j >> 1) - 1) & 1, abort_flag)))
+          break;
+        part[(j & 1) * kGroups * kRows] = (sum.x + sum.y) + (other.x + other.y);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPart + (j & 1)));
+      }
+    } else {
+      float *part = reinterpret_cast<float *>(smem + L::kPart) + y * 2 * kRows + r;
+      int c = 0, n = 0;
+      for (; more && ok; more = next_job(at), ++n) {
+        const int key0 = w.held0 * kRows;
+        float2 sum[2], other[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) sum[x] = other[x] = make_float2(0.f, 0.f);
+        for (int j = 0; j < w.n; ++j, ++c) {
+          const int st = c % S;
+          if (!(ok = warp_wait2(bar(kBarS + (c & 1)), (c >> 1) & 1, bar(kBarFull + st),
+                                (c / S) & 1, abort_flag)))
+            break;
+          tc::fence_after_sync();
+          uint32_t s[2][32];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            tc::ld32(tmem + (2 * (c & 1) + x) * kRows + lanes + 32 * y, s[x]);
+          tc::wait_ld();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarSFree + (c & 1)));
+          const uint32_t am = sb + L::kStats + st * stats_bytes + 32 * y * 4;
+          const int q0 = (w.s0 + j) / p.n_hsub * p.nq;
+          if (key0 + 2 * kRows - 1 <= w.ctx + q0) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) add_weights<false>(s[x], am, 0, qs, sum[x], other[x]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              add_weights<true>(s[x], am, (key0 + x * kRows + r - w.ctx - q0) * p.hb - 32 * y, qs,
+                                sum[x], other[x]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarFree + st));
+        }
+        if (!ok) break;
+        if (n >= 2 && !(ok = warp_wait(bar(kBarPartFree + (n & 1)), ((n >> 1) - 1) & 1, abort_flag)))
+          break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          part[(n & 1) * kGroups * 2 * kRows + x * kRows] =
+              (sum[x].x + sum[x].y) + (other[x].x + other[x].y);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPart + (n & 1)));
       }
     }
     if (!ok && lane == 0) raise_abort(p.status, abort_flag);
@@ -467,16 +611,40 @@ __global__ void __launch_bounds__(128 + 128 * HELD, HELD == 2 ? 1 : 2)
   __syncthreads();
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::dealloc(tmem, 256 * HELD);
+    tc::dealloc(tmem, 512);
   }
 }
 
+// The rows' ranges folded for the columns pass of many row tiles.
+__global__ void __launch_bounds__(kRows) stats_kernel(const WeightsParams p) {
+  griddep_release();
+  griddep_wait();
+  const int bg = blockIdx.x / p.n_rt, rt = blockIdx.x - bg * p.n_rt, r = threadIdx.x;
+  const float2 v = folded(p, bg, rt, r);
+  p.stats[static_cast<size_t>(blockIdx.x) * 2 * kRows + r] = v.x;
+  p.stats[static_cast<size_t>(blockIdx.x) * 2 * kRows + kRows + r] = v.y;
+}
+
+// Ranges that `ctas` units of `tiles` key tiles each are cut into: the number whose waves
+// of CTAs take least, a CTA's start counting as three tiles.
+int ranges_of(int64_t ctas, int tiles, int sms) {
+  int best = 1;
+  double least = 1e30;
+  for (int r = 1; r <= 64 && r <= tiles; ++r) {
+    const double waves = static_cast<double>((ctas * r + sms - 1) / sms);
+    const double cost = waves * ((tiles + r - 1) / r + 3);
+    if (cost < 0.97 * least) {
+      least = cost;
+      best = r;
+    }
+  }
+  return best;
+}
+
 struct Plan {
-  int hb, nq, n_hsub, n_rt, ranges;
+  int hb, nq, n_hsub, n_rt, ranges, key_ranges;
 };
-// Row tiles of a kv head's rows, and the key ranges that give about every SM a CTA of two
-// of them.
-Plan plan_of(int batch, int n_new, int n_q_heads, int n_kv_heads, int sms) {
+Plan plan_of(int batch, int n_new, int n_q_heads, int n_kv_heads, int max_blocks, int sms) {
   const int group = n_q_heads / n_kv_heads;
   Plan y;
   y.hb = group;
@@ -486,21 +654,26 @@ Plan plan_of(int batch, int n_new, int n_q_heads, int n_kv_heads, int sms) {
   y.n_hsub = group / y.hb;
   y.nq = kRows / y.hb;
   y.n_rt = y.n_hsub * ((n_new + y.nq - 1) / y.nq);
-  const int64_t ctas = static_cast<int64_t>(batch) * n_kv_heads * ((y.n_rt + 1) / 2);
-  const int64_t r = sms / ctas;
-  y.ranges = static_cast<int>(r < 1 ? 1 : r > 64 ? 64 : r);
+  const int64_t lists = static_cast<int64_t>(batch) * n_kv_heads;
+  const int tiles = (max_blocks * kPageSize + kRows - 1) / kRows;
+  y.ranges = ranges_of(lists * ((y.n_rt + 3) / 4), tiles, sms);
+  y.key_ranges = ranges_of(lists, tiles, sms);
   return y;
 }
 
-template <int D, bool BF16, int HELD, bool COLUMNS>
+size_t states_bytes(int64_t lists, const Plan &y) {
+  return static_cast<size_t>(lists) * y.n_rt * y.ranges * kRows * sizeof(float2);
+}
+
+template <int D, bool BF16, int PASS>
 int launch_pass(const CUtensorMap &qmap, const CUtensorMap &kmap, const WeightsParams &p,
                 int64_t ctas, cudaStream_t stream) {
-  using L = WeightsSmem<D, HELD>;
-  auto kern = weights_kernel<D, BF16, HELD, COLUMNS>;
+  using L = WeightsSmem<D, PASS>;
+  auto kern = weights_kernel<D, BF16, PASS>;
   static ContextCache<bool> smem_set;
   if (set_smem_limit(kern, L::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(128 + 128 * HELD), L::kAlloc,
-                    stream, qmap, kmap, p) == cudaSuccess
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), L::kAlloc, stream,
+                    qmap, kmap, p) == cudaSuccess
              ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -508,18 +681,21 @@ template <int D, bool BF16>
 int launch_t(const WeightsLaunch &a, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
-  const Plan y = plan_of(a.batch, a.n_new, a.n_q_heads, a.n_kv_heads, sms);
+  const Plan y =
+      plan_of(a.batch, a.n_new, a.n_q_heads, a.n_kv_heads, a.max_blocks, sms);
   CUtensorMap qmap, kmap;
   const uint64_t rows = static_cast<uint64_t>(a.num_pages) * a.n_kv_heads * kPageSize;
   if (make_rows_map(&kmap, a.k_cache, rows, D, kPageSize) != PA_OK) return PA_ERR_CUDA;
   if (make_query_map(&qmap, a.q, D, a.n_q_heads, a.n_new, a.batch, a.q_token_stride,
                      a.q_batch_stride, y.hb, y.nq) != PA_OK)
     return PA_ERR_CUDA;
+  const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   WeightsParams p;
   p.block_table = a.block_table;
   p.ctx_lens = a.ctx_lens;
   p.weights = a.weights;
-  p.stats = static_cast<float2 *>(a.workspace);
+  p.states = static_cast<float2 *>(a.workspace);
+  p.stats = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + states_bytes(lists, y));
   p.status = a.status;
   // (a zero scale becomes a factor small enough that every weight is the same: a masked
   // score, -inf, times zero would be NaN)
@@ -537,26 +713,32 @@ int launch_t(const WeightsLaunch &a, cudaStream_t stream) {
   p.num_pages = a.num_pages;
   p.fresh = a.fresh;
   p.n_ranges = y.ranges;
-  const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
-  p.groups = (y.n_rt + 1) / 2;
-  int rc = launch_pass<D, BF16, 2, false>(qmap, kmap, p, lists * p.groups * p.n_ranges, stream);
+  p.key_ranges = y.key_ranges;
+  p.groups = (y.n_rt + 3) / 4;
+  p.items = 0;
+  int rc = launch_pass<D, BF16, kRowsPass>(qmap, kmap, p, lists * p.groups * p.n_ranges, stream);
   if (rc) return rc;
-  // few query tiles: one key tile a CTA and two CTAs an SM, so that one's start overlaps
-  // the other's work; many: two key tiles, which halves what the query tiles cost L2
-  const int key_tiles = (a.max_blocks * kPageSize + kRows - 1) / kRows;
   if (y.n_rt <= 4) {
-    p.groups = key_tiles;
-    return launch_pass<D, BF16, 1, true>(qmap, kmap, p, lists * p.groups, stream);
+    p.groups = 1;
+    return launch_pass<D, BF16, kFew>(qmap, kmap, p, lists * p.key_ranges, stream);
   }
+  if (y.ranges > 1 &&
+      launch_pdl(stats_kernel, dim3(static_cast<unsigned>(lists * y.n_rt)), dim3(kRows), 0, stream,
+                 p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const int key_tiles = (a.max_blocks * kPageSize + kRows - 1) / kRows;
   p.groups = (key_tiles + 1) / 2;
-  return launch_pass<D, BF16, 2, true>(qmap, kmap, p, lists * p.groups, stream);
+  p.items = static_cast<int>(lists * p.groups);
+  return launch_pass<D, BF16, kMany>(qmap, kmap, p, p.items < sms ? p.items : sms, stream);
 }
 
 }  // namespace
 
-size_t weights_workspace_bytes(int batch, int n_new, int n_q_heads, int n_kv_heads, int sms) {
-  const Plan y = plan_of(batch, n_new, n_q_heads, n_kv_heads, sms);
-  return static_cast<size_t>(batch) * n_kv_heads * y.n_rt * y.ranges * kRows * sizeof(float2);
+size_t weights_workspace_bytes(int batch, int n_new, int n_q_heads, int n_kv_heads,
+                               int max_blocks, int sms) {
+  const Plan y = plan_of(batch, n_new, n_q_heads, n_kv_heads, max_blocks, sms);
+  const int64_t lists = static_cast<int64_t>(batch) * n_kv_heads;
+  return states_bytes(lists, y) + static_cast<size_t>(lists) * y.n_rt * 2 * kRows * sizeof(float);
 }
 
 int launch_weights(const WeightsLaunch &a, cudaStream_t stream) {
