@@ -141,6 +141,34 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
+// One lane of a converged warp: true for the same lane each time.  MMAs issued under it
+// (and not under a test of the lane number) keep their operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The high half of a descriptor of smem_desc_sw128 with a stride of 1024 bytes; the low half
+// holds the address and (K-major tiles: 1) the leading dimension's offset.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+// mma_f16 of two K-major 128-byte-swizzled tiles given by the low halves.
+__device__ __forceinline__ void mma_f16_low(uint32_t d_tmem, uint32_t a_low, uint32_t b_low,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+
 // The mbarrier receives one arrival once every MMA this thread issued so far
 // has completed.
 __device__ __forceinline__ void commit(uint32_t bar) {

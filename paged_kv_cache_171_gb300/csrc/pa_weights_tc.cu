@@ -10,21 +10,23 @@
 //   rows pass     S[row][key]: four tiles of 128 query rows are held in shared memory, K
 //                 tiles of 128 keys stream by; a thread owns a row and keeps its running
 //                 max m and sum l.  Few rows: the keys are cut into ranges, one (m, l) each.
-//   columns pass  S^T[key][row]: a thread owns a key and sums 2^(s - m_row) / l_row over the
-//                 rows, in a fixed order and without atomics; each row's (-m, 1 / l) comes
-//                 from shared memory, the same for all lanes.  Up to four row tiles (FEW):
-//                 they are held and the keys stream, each once.  More (MANY): two key tiles
-//                 are held, the row tiles stream, and a CTA goes from one pair of key tiles
-//                 to the next.
+//   columns pass  S^T[key][row]: a thread owns a key and sums 2^(s - lse_row), lse = m +
+//                 log2 l, over the rows, in a fixed order and without atomics; the rows'
+//                 lse come from shared memory, the same for all lanes.  Up to four row tiles
+//                 (FEW): they are held and the keys stream, each once.  More (MANY): two key
+//                 tiles are held, the row tiles stream, and a CTA goes from one pair of key
+//                 tiles to the next.
 // A row is a (query, head) pair of one kv head's group; a row tile is a TMA box of hb heads x
 // nq queries, so any group size and any stride of q goes.
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-19 are four consumer warpgroups:
-// in the rows pass one a row tile, in the columns pass each takes 32 of a row tile's 128
-// rows, and warps 2 and 3 add the four sums of a key and update the pool.  (Two warpgroups,
-// a whole tile each, kept the exponentials' pipe 20 to 46% busy: a warp's chain of tensor
-// memory loads, maximum and sum leaves it idle.)  Every hand-off is an mbarrier; every wait
-// is bounded and gives up early once another role has raised the CTA's abort flag.
+// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-19 are four consumer warpgroups, warps
+// 2 and 3 add the columns pass's partial sums and update the pool.  Work reaches the consumers
+// in chunks, each with a tensor memory buffer that is free again as soon as it is in
+// registers: in the rows pass a warpgroup has a row tile; in the columns pass 128-row chunks of
+// one key tile go round the warpgroups (FEW), or two warpgroups share the chunks of both key
+// tiles, 64 rows each (MANY: a load of lse then serves two keys).
+// Rows that only fill a tile up cost no exponentials.  Every hand-off is an mbarrier; every
+// wait is bounded and gives up early once another role has raised the CTA's abort flag.
 //
 // Bound: the exponentials, two of them a pair (MUFU), for chunks of many rows; K's bytes,
 // read twice, for few.
@@ -49,7 +51,7 @@ struct WeightsParams {
   const int32_t *block_table, *ctx_lens;
   float *weights;
   float2 *states;  // [sequence x kv head][row tile][range][128]: m (log2), l
-  float *stats;    // [sequence x kv head][row tile][2][128]: -m, then 1 / l
+  float *stats;    // [sequence x kv head][row tile][128]: -(m + log2 l), -inf for no row
   int *status;
   float qscale;    // scale * log2 e
   int n_new, n_kv_heads, group, hb, nq, n_hsub, n_rt, batch, max_blocks, num_pages, fresh;
@@ -66,28 +68,27 @@ struct WeightsSmem {
   static constexpr int kColBlk = kRows * 128;          // one 64-column block
   static constexpr int kTile = (D / 64) * kColBlk;
   static constexpr int kRing = kHeldTiles * kTile;
-  // [row tile or stage][2][128]: -m, 1 / l
-  static constexpr int kStats = kRing + kStages * kTile;
-  static constexpr int kPart = kStats + 4 * 2 * kRows * 4;    // [2][group][keys] sums
+  static constexpr int kStats = kRing + kStages * kTile;      // [row tile or stage][128]
+  static constexpr int kPart = kStats + 4 * kRows * 4;        // [2][4][keys] sums
   static constexpr int kPartKeys = PASS == kMany ? 2 * kRows : kRows;
   static constexpr int kBars = kPart + 2 * kGroups * kPartKeys * 4;
-  static constexpr int kSlot = kBars + 24 * 8;                // TMEM address, abort flag
+  static constexpr int kSlot = kBars + 32 * 8;                // TMEM address, abort flag
   static constexpr int kAlloc = kSlot + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory of an SM");
 };
 
 enum {
   kBarFull = 0,       // ring stage s landed
-  kBarFree = 4,       // ring stage s read (commit; MANY: and the consumers' warps)
+  kBarFree = 4,       // ring stage s read (commit; MANY: and by the consumers' warps)
   kBarHeld = 8,       // the held tiles landed
   kBarHeldFree = 9,   // MANY: .. have been read by the pair's last MMA (commit)
-  kBarS = 10,         // S buffer complete (commit)
-  kBarSFree = 14,     // S buffer read (one arrival a warp that reads it)
-  kBarT = 18,         // FEW: the rows' statistics are there (one arrival an aux warp)
-  kBarPart = 19,      // columns: the sums of buffer 0 / 1 are written (16 warps)
-  kBarPartFree = 21,  // .. have been read (2 warps)
-  kBarDrain = 23,
-  kNumBars = 24
+  kBarS = 10,         // S buffer 0 .. 3 (MANY: pair 0, 1) complete (commit)
+  kBarSFree = 18,     // .. read (one arrival a warp that reads it)
+  kBarT = 26,         // FEW: the rows' statistics are there (one arrival an aux warp)
+  kBarPart = 27,      // columns: the sums of buffer 0 / 1 are written
+  kBarPartFree = 29,  // .. have been read (2 warps)
+  kBarDrain = 31,
+  kNumBars = 32
 };
 
 // What a CTA does at a time.
@@ -189,9 +190,19 @@ __device__ __forceinline__ int query_of(const WeightsParams &p, int rt, int r) {
   return r < p.hb * p.nq && q < p.n_new ? q : -1;
 }
 
-// A row's ranges folded: (-m, 1 / l); (0, 0) for no row.
-__device__ __forceinline__ float2 folded(const WeightsParams &p, int bg, int rt, int r) {
-  if (query_of(p, rt, r) < 0) return make_float2(0.f, 0.f);
+// Rows of tile rt that are queries: the first ones.
+__device__ __forceinline__ int rows_of(const WeightsParams &p, int rt) {
+  return min(p.nq, p.n_new - rt / p.n_hsub * p.nq) * p.hb;
+}
+
+// -(m + log2 l); a row without a key, or none at all, weighs nothing.
+__device__ __forceinline__ float stat_of(float m, float l) {
+  return l == 0.f ? -INFINITY : -(m + log2f(l));
+}
+
+// A row's ranges folded.
+__device__ __forceinline__ float folded(const WeightsParams &p, int bg, int rt, int r) {
+  if (query_of(p, rt, r) < 0) return -INFINITY;
   const float2 *st =
       p.states + (static_cast<size_t>(bg) * p.n_rt + rt) * p.n_ranges * kRows + r;
   float m = kNoKey, l = 0.f;
@@ -202,7 +213,7 @@ __device__ __forceinline__ float2 folded(const WeightsParams &p, int bg, int rt,
     l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
     m = mn;
   }
-  return make_float2(-m, l == 0.f ? 0.f : 1.f / l);
+  return stat_of(m, l);
 }
 
 // ---- rows pass: 64 scores of this thread's row at a time
@@ -251,29 +262,41 @@ __device__ __forceinline__ void take_scores(uint32_t (&s)[64], int key0, int lim
   st.l = __fadd2_rn(st.l, __fadd2_rn(e2, f2));
 }
 
-// ---- columns pass: the weights of 32 rows for this thread's key, added to `sum`.  am: the
-// rows' -m in shared memory, 1 / l behind the tile's 128; rows from `from` on see the key.
-template <bool MASKED>
-__device__ __forceinline__ void add_weights(const uint32_t (&s)[32], uint32_t am, int from,
-                                            float qs, float2 &sum, float2 &other) {
+// ---- columns pass: the weights of 32 rows for KEYS keys of this thread, added to their
+// sums (of even and odd rows).  at: the rows' -lse in shared memory; rows from `from` on see
+// the key.
+template <int KEYS, bool MASKED>
+__device__ __forceinline__ void add_weights(const uint32_t (&s)[KEYS][32], uint32_t at,
+                                            const int (&from)[KEYS], float qs,
+                                            float2 (&sum)[KEYS]) {
   const float2 qs2 = make_float2(qs, qs);
+  float2 even[KEYS], odd[KEYS];
+#pragma unroll
+  for (int x = 0; x < KEYS; ++x) even[x] = odd[x] = make_float2(0.f, 0.f);
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
-    const uint4 m4 = lds128(am + c * 4), l4 = lds128(am + kRows * 4 + c * 4);
-    const float2 a = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                qs2, make_float2(__uint_as_float(m4.x), __uint_as_float(m4.y)));
-    const float2 b = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                qs2, make_float2(__uint_as_float(m4.z), __uint_as_float(m4.w)));
-    float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
-    if (MASKED) {
-      if (c < from) ea.x = 0.f;
-      if (c + 1 < from) ea.y = 0.f;
-      if (c + 2 < from) eb.x = 0.f;
-      if (c + 3 < from) eb.y = 0.f;
+    const uint4 v = lds128(at + c * 4);
+    const float2 v0 = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    const float2 v1 = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+#pragma unroll
+    for (int x = 0; x < KEYS; ++x) {
+      const float2 a = __ffma2_rn(
+          make_float2(__uint_as_float(s[x][c]), __uint_as_float(s[x][c + 1])), qs2, v0);
+      const float2 b = __ffma2_rn(
+          make_float2(__uint_as_float(s[x][c + 2]), __uint_as_float(s[x][c + 3])), qs2, v1);
+      float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
+      if (MASKED) {
+        if (c < from[x]) ea.x = 0.f;
+        if (c + 1 < from[x]) ea.y = 0.f;
+        if (c + 2 < from[x]) eb.x = 0.f;
+        if (c + 3 < from[x]) eb.y = 0.f;
+      }
+      even[x] = __fadd2_rn(even[x], ea);
+      odd[x] = __fadd2_rn(odd[x], eb);
     }
-    sum = __ffma2_rn(ea, make_float2(__uint_as_float(l4.x), __uint_as_float(l4.y)), sum);
-    other = __ffma2_rn(eb, make_float2(__uint_as_float(l4.z), __uint_as_float(l4.w)), other);
   }
+#pragma unroll
+  for (int x = 0; x < KEYS; ++x) sum[x] = __fadd2_rn(sum[x], __fadd2_rn(even[x], odd[x]));
 }
 
 template <int D, bool BF16, int PASS>
@@ -304,11 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
-      if (i >= kBarFree && i < kBarHeld) n = PASS == kMany ? 1 + 4 * kGroups : 1;
-      if (i >= kBarSFree && i < kBarT) n = PASS == kRowsPass ? 4 : 4 * kGroups;
-      if (i == kBarT || i >= kBarPartFree) n = 2;
-      if (i == kBarPart || i == kBarPart + 1) n = 4 * kGroups;
-      if (i == kBarDrain) n = 1;
+      if (i >= kBarFree && i < kBarHeld) n = PASS == kMany ? 1 + 2 * 4 : 1;
+      if (i >= kBarSFree && i < kBarT) n = PASS == kMany ? 2 * 4 : 4;
+      if (i == kBarT || (i >= kBarPartFree && i < kBarDrain)) n = 2;
+      if (i == kBarPart || i == kBarPart + 1) n = 4 * (PASS == kMany ? kGroups : w.n_held);
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -334,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
   const uint32_t q_bytes = (D / 64) * p.hb * p.nq * 128;
-  const uint32_t stats_bytes = 2 * kRows * sizeof(float);
+  const uint32_t stats_bytes = kRows * sizeof(float);
   // the jobs of a CTA: one, or (MANY) every gridDim.x-th item
   auto next_job = [&](int &at) {
     for (at += gridDim.x; PASS == kMany && at < p.items; at += gridDim.x) {
@@ -376,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (lane == 0) {
           load_queries<D>(&qmap, p, w, w.s0 + j, dst, full);
           bulk_load(sb + L::kStats + s * stats_bytes,
-                    p.stats + (static_cast<size_t>(w.bg) * p.n_rt + w.s0 + j) * 2 * kRows,
+                    p.stats + (static_cast<size_t>(w.bg) * p.n_rt + w.s0 + j) * kRows,
                     stats_bytes, full);
         }
       }
@@ -389,49 +411,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---- S of every held tile against each streamed one; the keys' tile is the first
     // operand in the columns pass, the rows' in the rows pass
+    const uint32_t held = tc::desc_low(sb), ring = tc::desc_low(sb + L::kRing);
+    constexpr uint32_t kTileLow = L::kTile >> 4;
+    const bool issuer = tc::elect_one();
+    auto mma = [&](uint32_t dst, uint32_t a, uint32_t b, uint32_t id) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * L::kColBlk + (k & 3) * 32) >> 4;
+        tc::mma_f16_low(dst, a + off, b + off, id, k > 0);
+      }
+    };
     constexpr uint32_t kId = tc::idesc_f16(BF16, kRows, kRows, false, false);
-    const uint64_t held = tc::smem_desc_sw128(sb, 16, 1024);
-    const uint64_t ring = tc::smem_desc_sw128(sb + L::kRing, 16, 1024);
     bool ok = true;
-    int c = 0, job = 0;
+    int c = 0, job = 0, n = 0;  // tiles, jobs, chunks
     for (; more && ok; more = next_job(at), ++job) {
       ok = warp_wait(bar(kBarHeld), job & 1, abort_flag);
       for (int j = 0; j < w.n && ok; ++j, ++c) {
         const int s = c % S;
         if (!(ok = warp_wait(bar(kBarFull + s), (c / S) & 1, abort_flag))) break;
-        // MANY: both held tiles' scores go to one of two pairs of buffers
-        if (PASS == kMany && c >= 2 &&
-            !(ok = warp_wait(bar(kBarSFree + (c & 1)), ((c >> 1) - 1) & 1, abort_flag)))
-          break;
-        for (int x = 0; x < w.n_held && ok; ++x) {
-          const int buf = PASS == kMany ? 2 * (c & 1) + x : x;
-          if (PASS != kMany && c >= 1 &&
-              !(ok = warp_wait(bar(kBarSFree + x), (c - 1) & 1, abort_flag)))
-            break;
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint64_t h = held + ((x * L::kTile) >> 4), r = ring + ((s * L::kTile) >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = ((k >> 2) * L::kColBlk + (k & 3) * 32) >> 4;
-              tc::mma_f16(tmem + buf * kRows, (PASS == kFew ? r : h) + off,
-                          (PASS == kFew ? h : r) + off, kId, k > 0);
-            }
-            if (PASS != kMany) tc::commit(bar(kBarS + x));
-            if (x == w.n_held - 1) {
-              if (PASS == kMany) {
-                tc::commit(bar(kBarS + (c & 1)));
-                if (j == w.n - 1) tc::commit(bar(kBarHeldFree));
-              }
-              tc::commit(bar(kBarFree + s));
+        const uint32_t tile = ring + s * kTileLow;
+        if constexpr (PASS != kMany) {  // a chunk a row tile
+          for (int x = 0; x < w.n_held && ok; ++x, ++n) {
+            const int buf = PASS == kRowsPass ? x : n & 3;
+            const int use = PASS == kRowsPass ? c : n >> 2;
+            if (use > 0 && !(ok = warp_wait(bar(kBarSFree + buf), (use - 1) & 1, abort_flag)))
+              break;
+            tc::fence_after_sync();
+            // (FEW: as many rows as are read)
+            const uint32_t id =
+                PASS == kRowsPass ? kId
+                                  : tc::idesc_f16(BF16, kRows, (rows_of(p, x) + 31) & ~31, false,
+                                                  false);
+            const uint32_t a = held + x * kTileLow;
+            if (issuer) {
+              mma(tmem + kRows * buf, PASS == kRowsPass ? a : tile, PASS == kRowsPass ? tile : a,
+                  id);
+              tc::commit(bar(kBarS + buf));
             }
           }
-          __syncwarp();
+        } else {  // both key tiles' scores, in one of two pairs of buffers
+          if (c >= 2 && !(ok = warp_wait(bar(kBarSFree + (c & 1)), ((c >> 1) - 1) & 1, abort_flag)))
+            break;
+          tc::fence_after_sync();
+          if (issuer) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              mma(tmem + kRows * (2 * (c & 1) + x), held + x * kTileLow, tile, kId);
+            tc::commit(bar(kBarS + (c & 1)));
+            if (j == w.n - 1) tc::commit(bar(kBarHeldFree));
+          }
         }
+        if (ok && issuer) tc::commit(bar(kBarFree + s));
       }
     }
     if (!ok) {
-      if (lane == 0) {
+      if (issuer) {
         raise_abort(p.status, abort_flag);
         tc::commit(bar(kBarDrain));
       }
@@ -446,9 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *st = reinterpret_cast<float *>(smem + L::kStats);
         for (int e = tid - 64; e < w.n_held * kRows; e += 64) {
           const int rt = e / kRows, r = e % kRows;
-          const float2 v = folded(p, w.bg, rt, r);
-          st[rt * 2 * kRows + r] = v.x;
-          st[rt * 2 * kRows + kRows + r] = v.y;
+          st[e] = folded(p, w.bg, rt, r);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarT));
@@ -475,12 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = warp_wait(bar(kBarPart + (n & 1)), (n >> 1) & 1, abort_flag))) break;
           const float *part = reinterpret_cast<const float *>(smem + L::kPart) +
-                              (n & 1) * kGroups * L::kPartKeys + tid - 64;
+                              (n & 1) * 4 * L::kPartKeys + tid - 64;
 #pragma unroll
           for (int u = 0; u < L::kPartKeys / 64; ++u) {
             float sum = 0.f;
 #pragma unroll
-            for (int y = 0; y < kGroups; ++y) sum += part[y * L::kPartKeys + 64 * u];
+            for (int y = 0; y < 4; ++y)
+              if (PASS == kMany || y < w.n_held) sum += part[y * L::kPartKeys + 64 * u];
             if (dst[u]) *dst[u] = old[u] + sum;
           }
           __syncwarp();
@@ -495,27 +528,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float qs = p.qscale;
     bool ok = true;
+    // the chunk in buffer `buf` has been read
+    auto release = [&](int buf) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
+    };
     if constexpr (PASS == kRowsPass) {
       if (y < w.n_held) {
         const int rt = w.held0 + y, q = query_of(p, rt, r);
         const int lim = w.ctx + max(q, 0);                      // last key row r sees
         const int lim_all = w.ctx + rt / p.n_hsub * p.nq;       // every row of the tile does
+        const bool idle = 32 * (warp & 3) >= rows_of(p, rt);    // none of the warp's rows is one
         RowState st = {kNoKey, make_float2(0.f, 0.f)};
         for (int j = 0; j < w.n; ++j) {
           if (!(ok = warp_wait(bar(kBarS + y), j & 1, abort_flag))) break;
           tc::fence_after_sync();
+          if (idle) {
+            release(y);
+            continue;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t s[64];
-            tc::ld32(tmem + y * kRows + lanes + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(s));
-            tc::ld32(tmem + y * kRows + lanes + 64 * h + 32,
+            tc::ld32(tmem + kRows * y + 64 * h + lanes, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tc::ld32(tmem + kRows * y + 64 * h + lanes + 32,
                      *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             tc::wait_ld();
-            if (h == 1) {
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(kBarSFree + y));
-            }
+            if (h == 1) release(y);
             take_scores(s, (w.s0 + j) * kRows + 64 * h, lim, lim_all, qs, st);
           }
         }
@@ -523,86 +563,94 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float l = st.l.x + st.l.y;
           const size_t tile = static_cast<size_t>(w.bg) * p.n_rt + rt;
           p.states[(tile * p.n_ranges + w.range) * kRows + r] = make_float2(st.m, l);
-          if (p.n_ranges == 1) {
-            p.stats[tile * 2 * kRows + r] = q < 0 ? 0.f : -st.m;
-            p.stats[tile * 2 * kRows + kRows + r] = q < 0 || l == 0.f ? 0.f : 1.f / l;
-          }
+          if (p.n_ranges == 1)
+            p.stats[tile * kRows + r] = q < 0 ? -INFINITY : stat_of(st.m, l);
         }
       }
     } else if constexpr (PASS == kFew) {
-      float *part = reinterpret_cast<float *>(smem + L::kPart) + y * kRows + r;
+      float *part = reinterpret_cast<float *>(smem + L::kPart) + r;
       ok = warp_wait(bar(kBarT), 0, abort_flag);
-      for (int j = 0; j < w.n && ok; ++j) {
-        const int key0 = (w.s0 + j) * kRows, key = key0 + r;
-        float2 sum = make_float2(0.f, 0.f), other = make_float2(0.f, 0.f);
-        for (int x = 0; x < w.n_held; ++x) {
-          if (!(ok = warp_wait(bar(kBarS + x), j & 1, abort_flag))) break;
-          tc::fence_after_sync();
-          uint32_t s[32];
-          tc::ld32(tmem + x * kRows + lanes + 32 * y, s);
+      const int chunks = w.n * w.n_held;
+      int j = y / w.n_held, x = y - j * w.n_held;  // of chunk n
+      for (int n = y; n < chunks && ok; n += 4) {
+        if (!(ok = warp_wait(bar(kBarS + y), (n >> 2) & 1, abort_flag))) break;
+        tc::fence_after_sync();
+        const int key0 = (w.s0 + j) * kRows, rows = rows_of(p, x);
+        const int q0 = x / p.n_hsub * p.nq;  // the tile's first query
+        const bool all = key0 + kRows - 1 <= w.ctx + q0;  // every row sees every key
+        float2 sum[1] = {make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c0 = 0; c0 < kRows; c0 += 32) {
+          if (c0 >= rows) {
+            if (c0 - 32 < rows) release(y);
+            continue;
+          }
+          uint32_t s[1][32];
+          tc::ld32(tmem + kRows * y + lanes + c0, s[0]);
           tc::wait_ld();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarSFree + x));
-          const uint32_t am = sb + L::kStats + x * stats_bytes + 32 * y * 4;
-          const int q0 = x / p.n_hsub * p.nq;  // the tile's first query
-          if (key0 + kRows - 1 <= w.ctx + q0)
-            add_weights<false>(s, am, 0, qs, sum, other);
+          if (c0 == kRows - 32) release(y);
+          const uint32_t lse = sb + L::kStats + x * stats_bytes + c0 * 4;
+          const int from[1] = {(key0 + r - w.ctx - q0) * p.hb - c0};
+          if (all)
+            add_weights<1, false>(s, lse, from, qs, sum);
           else
-            add_weights<true>(s, am, (key - w.ctx - q0) * p.hb - 32 * y, qs, sum, other);
+            add_weights<1, true>(s, lse, from, qs, sum);
         }
-        if (!ok) break;
         if (j >= 2 && !(ok = warp_wait(bar(kBarPartFree + (j & 1)), ((j >> 1) - 1) & 1, abort_flag)))
           break;
-        part[(j & 1) * kGroups * kRows] = (sum.x + sum.y) + (other.x + other.y);
+        part[((j & 1) * 4 + x) * kRows] = sum[0].x + sum[0].y;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPart + (j & 1)));
+        for (x += 4; x >= w.n_held; x -= w.n_held) ++j;
       }
     } else {
       float *part = reinterpret_cast<float *>(smem + L::kPart) + y * 2 * kRows + r;
-      int c = 0, n = 0;
-      for (; more && ok; more = next_job(at), ++n) {
+      int c = 0, job = 0;  // tiles, jobs
+      const int pair = y & 1, half = y >> 1;  // which tiles, which 64 of their rows
+      for (; more && ok; more = next_job(at), ++job) {
         const int key0 = w.held0 * kRows;
-        float2 sum[2], other[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) sum[x] = other[x] = make_float2(0.f, 0.f);
-        for (int j = 0; j < w.n; ++j, ++c) {
-          const int st = c % S;
-          if (!(ok = warp_wait2(bar(kBarS + (c & 1)), (c >> 1) & 1, bar(kBarFull + st),
-                                (c / S) & 1, abort_flag)))
+        float2 sum[2];
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+        for (int j = 0; j < w.n; ++j) {
+          const int t = c + j, st = t % S;
+          if ((t & 1) != pair) continue;
+          if (!(ok = warp_wait2(bar(kBarS + pair), (t >> 1) & 1, bar(kBarFull + st), (t / S) & 1,
+                                abort_flag)))
             break;
           tc::fence_after_sync();
-          uint32_t s[2][32];
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            tc::ld32(tmem + (2 * (c & 1) + x) * kRows + lanes + 32 * y, s[x]);
-          tc::wait_ld();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarSFree + (c & 1)));
-          const uint32_t am = sb + L::kStats + st * stats_bytes + 32 * y * 4;
           const int q0 = (w.s0 + j) / p.n_hsub * p.nq;
-          if (key0 + 2 * kRows - 1 <= w.ctx + q0) {
+          const bool all = key0 + 2 * kRows - 1 <= w.ctx + q0;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) add_weights<false>(s[x], am, 0, qs, sum[x], other[x]);
-          } else {
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            uint32_t s[2][32];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              add_weights<true>(s[x], am, (key0 + x * kRows + r - w.ctx - q0) * p.hb - 32 * y, qs,
-                                sum[x], other[x]);
+              tc::ld32(tmem + kRows * (2 * pair + x) + lanes + 64 * half + c0, s[x]);
+            tc::wait_ld();
+            if (c0 == 32) release(pair);
+            const uint32_t lse = sb + L::kStats + st * stats_bytes + (64 * half + c0) * 4;
+            int from[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              from[x] = (key0 + x * kRows + r - w.ctx - q0) * p.hb - 64 * half - c0;
+            if (all)
+              add_weights<2, false>(s, lse, from, qs, sum);
+            else
+              add_weights<2, true>(s, lse, from, qs, sum);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarFree + st));
         }
         if (!ok) break;
-        if (n >= 2 && !(ok = warp_wait(bar(kBarPartFree + (n & 1)), ((n >> 1) - 1) & 1, abort_flag)))
+        c += w.n;
+        if (job >= 2 &&
+            !(ok = warp_wait(bar(kBarPartFree + (job & 1)), ((job >> 1) - 1) & 1, abort_flag)))
           break;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          part[(n & 1) * kGroups * 2 * kRows + x * kRows] =
-              (sum[x].x + sum[x].y) + (other[x].x + other[x].y);
+          part[(job & 1) * 4 * 2 * kRows + x * kRows] = sum[x].x + sum[x].y;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPart + (n & 1)));
+        if (lane == 0) mbar_arrive(bar(kBarPart + (job & 1)));
       }
     }
     if (!ok && lane == 0) raise_abort(p.status, abort_flag);
@@ -620,9 +668,7 @@ __global__ void __launch_bounds__(kRows) stats_kernel(const WeightsParams p) {
   griddep_release();
   griddep_wait();
   const int bg = blockIdx.x / p.n_rt, rt = blockIdx.x - bg * p.n_rt, r = threadIdx.x;
-  const float2 v = folded(p, bg, rt, r);
-  p.stats[static_cast<size_t>(blockIdx.x) * 2 * kRows + r] = v.x;
-  p.stats[static_cast<size_t>(blockIdx.x) * 2 * kRows + kRows + r] = v.y;
+  p.stats[static_cast<size_t>(blockIdx.x) * kRows + r] = folded(p, bg, rt, r);
 }
 
 // Ranges that `ctas` units of `tiles` key tiles each are cut into: the number whose waves
@@ -738,7 +784,7 @@ size_t weights_workspace_bytes(int batch, int n_new, int n_q_heads, int n_kv_hea
                                int max_blocks, int sms) {
   const Plan y = plan_of(batch, n_new, n_q_heads, n_kv_heads, max_blocks, sms);
   const int64_t lists = static_cast<int64_t>(batch) * n_kv_heads;
-  return states_bytes(lists, y) + static_cast<size_t>(lists) * y.n_rt * 2 * kRows * sizeof(float);
+  return states_bytes(lists, y) + static_cast<size_t>(lists) * y.n_rt * kRows * sizeof(float);
 }
 
 int launch_weights(const WeightsLaunch &a, cudaStream_t stream) {
