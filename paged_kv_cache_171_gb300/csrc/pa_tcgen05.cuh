@@ -108,7 +108,8 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo
 // Instruction descriptor, kind::f16 with fp32 accumulation:
 //   bits 4-5 D type (1 = f32), 7-9 A type and 10-12 B type (0 = f16,
 //   1 = bf16), 15 / 16 A / B major (0 = K-major, 1 = MN-major),
-//   17-22 N >> 3, 24-28 M >> 4.
+//   17-22 N >> 3, 24-28 M >> 4.  Bit 13 (kNegateA) turns the sign of A.
+constexpr uint32_t kNegateA = 1u << 13;
 __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int m, int n, bool a_mn_major,
                                                  bool b_mn_major) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |

@@ -21,10 +21,11 @@
 //
 // Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-19 are four consumer warpgroups, warps
 // 2 and 3 add the columns pass's partial sums and update the pool.  Work reaches the consumers
-// in chunks, each with a tensor memory buffer that is free again as soon as it is in
-// registers: in the rows pass a warpgroup has a row tile; in the columns pass 128-row chunks of
-// one key tile go round the warpgroups (FEW), or two warpgroups share the chunks of both key
-// tiles, 64 rows each (MANY: a load of lse then serves two keys).
+// in chunks of 128 x 128 scores, of which a warpgroup takes no more than fits its registers
+// at once, so that a tensor memory buffer is free again right after it is complete, and there
+// are two for each: row tile x key tile chunks go to two pairs of warpgroups in turn, half the
+// columns each (rows pass, FEW); or all four take 32 rows of both held key tiles (MANY: a load
+// of lse then serves two keys).
 // Rows that only fill a tile up cost no exponentials.  Every hand-off is an mbarrier; every
 // wait is bounded and gives up early once another role has raised the CTA's abort flag.
 //
@@ -53,7 +54,8 @@ struct WeightsParams {
   float2 *states;  // [sequence x kv head][row tile][range][128]: m (log2), l
   float *stats;    // [sequence x kv head][row tile][128]: -(m + log2 l), -inf for no row
   int *status;
-  float qscale;    // scale * log2 e
+  float qscale;    // |scale| * log2 e
+  uint32_t negate; // bit of the instruction descriptor that turns the first operand's sign
   int n_new, n_kv_heads, group, hb, nq, n_hsub, n_rt, batch, max_blocks, num_pages, fresh;
   int n_ranges;    // key ranges of the rows pass
   int key_ranges;  // of the columns pass (FEW)
@@ -64,14 +66,15 @@ struct WeightsParams {
 template <int D, int PASS>
 struct WeightsSmem {
   static constexpr int kHeldTiles = PASS == kMany ? 2 : 4;
+  // of the ring; held row tiles that there are not make room for more (up to 4)
   static constexpr int kStages = D == 128 && PASS != kMany ? 2 : 4;
   static constexpr int kColBlk = kRows * 128;          // one 64-column block
   static constexpr int kTile = (D / 64) * kColBlk;
-  static constexpr int kRing = kHeldTiles * kTile;
-  static constexpr int kStats = kRing + kStages * kTile;      // [row tile or stage][128]
-  static constexpr int kPart = kStats + 4 * kRows * 4;        // [2][4][keys] sums
+  static constexpr int kStats = (kHeldTiles + kStages) * kTile;  // [row tile or stage][128]
+  static constexpr int kPart = kStats + 4 * kRows * 4;        // [2][4 or 8][keys] sums
   static constexpr int kPartKeys = PASS == kMany ? 2 * kRows : kRows;
-  static constexpr int kBars = kPart + 2 * kGroups * kPartKeys * 4;
+  static constexpr int kParts = PASS == kMany ? kGroups : 8;  // sums a key
+  static constexpr int kBars = kPart + 2 * kParts * kPartKeys * 4;
   static constexpr int kSlot = kBars + 32 * 8;                // TMEM address, abort flag
   static constexpr int kAlloc = kSlot + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory of an SM");
@@ -142,19 +145,23 @@ __device__ __forceinline__ Job job_of(const WeightsParams &p, int at, bool repor
   return w;
 }
 
+// The page that lane l < 8 copies of key tile `tile`.
+__device__ __forceinline__ int page_of(const WeightsParams &p, const Job &w, int tile, int lane) {
+  const int pg = 8 * tile + lane;  // past the end: page 0, masked
+  int id = lane < 8 && pg * kPageSize < w.T
+               ? p.block_table[static_cast<size_t>(w.b) * p.max_blocks + pg] : 0;
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
+    record_error(p.status, PA_ERR_BAD_BLOCK);
+    id = 0;
+  }
+  return id;
+}
 // One K tile (8 pages of one kv head) into shared memory.  The whole warp.
 template <int D>
 __device__ __forceinline__ void load_keys(const CUtensorMap *map, const WeightsParams &p,
-                                          const Job &w, int tile, uint32_t dst, uint32_t bar,
+                                          const Job &w, int id, uint32_t dst, uint32_t bar,
                                           int lane) {
-  const int n_pages = (w.T + kPageSize - 1) / kPageSize;
   if (lane < 8) {
-    const int pg = 8 * tile + lane;  // past the end: page 0, masked
-    int id = pg < n_pages ? p.block_table[static_cast<size_t>(w.b) * p.max_blocks + pg] : 0;
-    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
-      record_error(p.status, PA_ERR_BAD_BLOCK);
-      id = 0;
-    }
 #pragma unroll
     for (int x = 0; x < D / 64; ++x)
       tma_load_2d(dst + x * kRows * 128 + lane * 2048, map, 64 * x,
@@ -223,26 +230,19 @@ struct RowState {
 };
 __device__ __forceinline__ void take_scores(uint32_t (&s)[64], int key0, int lim, int lim_all,
                                             float qs, RowState &st) {
-  // the maximum of s qs (a negative scale: from the least s); masked keys never win
-  auto extreme = [&](auto pick, float worst) {
-    if (key0 + 63 > lim_all) {
-      const int last = lim - key0;
+  if (key0 + 63 > lim_all) {
+    const int last = lim - key0;
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        if (c > last) s[c] = __float_as_uint(worst);
-    }
-    float t0 = worst, t1 = worst;
+    for (int c = 0; c < 64; ++c)
+      if (c > last) s[c] = __float_as_uint(-INFINITY);
+  }
+  float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < 64; c += 4) {
-      t0 = pick(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      t1 = pick(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-    }
-    return pick(t0, t1, t1);
-  };
-  const float cand =
-      qs * (qs > 0.f ? extreme([](float a, float b, float c) { return max3(a, b, c); }, -INFINITY)
-                     : extreme([](float a, float b, float c) { return fminf(fminf(a, b), c); },
-                               INFINITY));
+  for (int c = 0; c < 64; c += 4) {
+    t0 = max3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    t1 = max3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+  }
+  const float cand = fmaxf(t0, t1) * qs;
   if (cand > st.m + kSlack) {
     const float corr = ex2(st.m - cand);
     st.m = cand;
@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const WeightsParams p) {
   using L = WeightsSmem<D, PASS>;
-  constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -323,14 +322,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
+  const int S = min(4, L::kHeldTiles + L::kStages - w.n_held);  // stages of the ring
+  const uint32_t ring0 = sb + w.n_held * L::kTile;
+
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kSlot + 4);
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
-      if (i >= kBarFree && i < kBarHeld) n = PASS == kMany ? 1 + 2 * 4 : 1;
-      if (i >= kBarSFree && i < kBarT) n = PASS == kMany ? 2 * 4 : 4;
+      if (i >= kBarFree && i < kBarHeld) n = PASS == kMany ? 1 + 4 * kGroups : 1;
+      if (i >= kBarSFree && i < kBarT) n = PASS == kMany ? 4 * kGroups : PASS == kFew ? 8 : 4;
       if (i == kBarT || (i >= kBarPartFree && i < kBarDrain)) n = 2;
-      if (i == kBarPart || i == kBarPart + 1) n = 4 * (PASS == kMany ? kGroups : w.n_held);
+      if (i == kBarPart || i == kBarPart + 1) n = PASS == kMany ? 4 * kGroups : 8 * w.n_held;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Rows of a query tile behind its box are never written by the copies: they hold zeros.
   if (p.hb * p.nq < kRows) {
     const int r0 = p.hb * p.nq, rows = kRows - r0;
-    const int first = PASS == kMany ? L::kRing : 0, n = PASS == kMany ? S : L::kHeldTiles;
+    const int first = PASS == kMany ? L::kHeldTiles * L::kTile : 0;
+    const int n = PASS == kMany ? L::kStages : w.n_held;
     for (int e = tid; e < n * (D / 64) * rows * 8; e += kThreads) {
       const int blk = e / (rows * 8), in = e - blk * rows * 8;
       st_shared_v4(sb + first + blk * L::kColBlk + (r0 + in / 8) * 128 + (in % 8) * 16, 0u, 0u,
@@ -373,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- loads
     bool ok = true;
     int c = 0, job = 0;  // tiles streamed, jobs done
+    int s = 0;           // the next one's stage, and how often the ring has gone round
+    uint32_t round = 0;
     for (; more && ok; more = next_job(at), ++job) {
       if (PASS == kMany && job > 0 &&
           !(ok = warp_wait(bar(kBarHeldFree), (job - 1) & 1, abort_flag)))
@@ -382,25 +387,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       for (int x = 0; x < w.n_held; ++x) {
         if (PASS == kMany)
-          load_keys<D>(&kmap, p, w, w.held0 + x, sb + x * L::kTile, bar(kBarHeld), lane);
+          load_keys<D>(&kmap, p, w, page_of(p, w, w.held0 + x, lane), sb + x * L::kTile,
+                       bar(kBarHeld), lane);
         else if (lane == 0)
           load_queries<D>(&qmap, p, w, w.held0 + x, sb + x * L::kTile, bar(kBarHeld));
       }
+      int id = PASS != kMany ? page_of(p, w, w.s0, lane) : 0;  // of the next key tile
       for (int j = 0; j < w.n; ++j, ++c) {
-        const int s = c % S;
-        if (c >= S && !(ok = warp_wait(bar(kBarFree + s), ((c / S) - 1) & 1, abort_flag))) break;
-        const uint32_t full = bar(kBarFull + s), dst = sb + L::kRing + s * L::kTile;
+        const int here = id;
+        if (PASS != kMany && j + 1 < w.n) id = page_of(p, w, w.s0 + j + 1, lane);
+        if (c >= S && !(ok = warp_wait(bar(kBarFree + s), (round - 1) & 1, abort_flag))) break;
+        const uint32_t full = bar(kBarFull + s), dst = ring0 + s * L::kTile;
         if (lane == 0)
           mbar_arrive_expect_tx(full, PASS == kMany ? q_bytes + stats_bytes : L::kTile);
         __syncwarp();
         if (PASS != kMany) {
-          load_keys<D>(&kmap, p, w, w.s0 + j, dst, full, lane);
+          load_keys<D>(&kmap, p, w, here, dst, full, lane);
         } else if (lane == 0) {
           load_queries<D>(&qmap, p, w, w.s0 + j, dst, full);
           bulk_load(sb + L::kStats + s * stats_bytes,
                     p.stats + (static_cast<size_t>(w.bg) * p.n_rt + w.s0 + j) * kRows,
                     stats_bytes, full);
         }
+        if (++s == S) s = 0, ++round;
       }
     }
     if (!ok) {
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---- S of every held tile against each streamed one; the keys' tile is the first
     // operand in the columns pass, the rows' in the rows pass
-    const uint32_t held = tc::desc_low(sb), ring = tc::desc_low(sb + L::kRing);
+    const uint32_t held = tc::desc_low(sb), ring = tc::desc_low(ring0);
     constexpr uint32_t kTileLow = L::kTile >> 4;
     const bool issuer = tc::elect_one();
     auto mma = [&](uint32_t dst, uint32_t a, uint32_t b, uint32_t id) {
@@ -421,33 +430,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_f16_low(dst, a + off, b + off, id, k > 0);
       }
     };
-    constexpr uint32_t kId = tc::idesc_f16(BF16, kRows, kRows, false, false);
+    const uint32_t full_id = tc::idesc_f16(BF16, kRows, kRows, false, false) | p.negate;
     bool ok = true;
-    int c = 0, job = 0, n = 0;  // tiles, jobs, chunks
+    int c = 0, job = 0, n = 0, s = 0;  // tiles, jobs, chunks, the tile's stage
+    uint32_t round = 0;
+    uint32_t ids[4];  // FEW: as many rows as are read
+    if (PASS == kFew)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        ids[x] = tc::idesc_f16(BF16, kRows, (rows_of(p, x) + 31) & ~31, false, false) | p.negate;
     for (; more && ok; more = next_job(at), ++job) {
       ok = warp_wait(bar(kBarHeld), job & 1, abort_flag);
       for (int j = 0; j < w.n && ok; ++j, ++c) {
-        const int s = c % S;
-        if (!(ok = warp_wait(bar(kBarFull + s), (c / S) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(bar(kBarFull + s), round & 1, abort_flag))) break;
         const uint32_t tile = ring + s * kTileLow;
         if constexpr (PASS != kMany) {  // a chunk a row tile
-          for (int x = 0; x < w.n_held && ok; ++x, ++n) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (x >= w.n_held) break;
             const int buf = PASS == kRowsPass ? x : n & 3;
             const int use = PASS == kRowsPass ? c : n >> 2;
             if (use > 0 && !(ok = warp_wait(bar(kBarSFree + buf), (use - 1) & 1, abort_flag)))
               break;
             tc::fence_after_sync();
-            // (FEW: as many rows as are read)
-            const uint32_t id =
-                PASS == kRowsPass ? kId
-                                  : tc::idesc_f16(BF16, kRows, (rows_of(p, x) + 31) & ~31, false,
-                                                  false);
             const uint32_t a = held + x * kTileLow;
             if (issuer) {
               mma(tmem + kRows * buf, PASS == kRowsPass ? a : tile, PASS == kRowsPass ? tile : a,
-                  id);
+                  PASS == kRowsPass ? full_id : ids[x]);
               tc::commit(bar(kBarS + buf));
             }
+            ++n;
           }
         } else {  // both key tiles' scores, in one of two pairs of buffers
           if (c >= 2 && !(ok = warp_wait(bar(kBarSFree + (c & 1)), ((c >> 1) - 1) & 1, abort_flag)))
@@ -456,12 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (issuer) {
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              mma(tmem + kRows * (2 * (c & 1) + x), held + x * kTileLow, tile, kId);
+              mma(tmem + kRows * (2 * (c & 1) + x), held + x * kTileLow, tile, full_id);
             tc::commit(bar(kBarS + (c & 1)));
             if (j == w.n - 1) tc::commit(bar(kBarHeldFree));
           }
         }
         if (ok && issuer) tc::commit(bar(kBarFree + s));
+        if (++s == S) s = 0, ++round;
       }
     }
     if (!ok) {
@@ -485,39 +498,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarT));
       }
+      constexpr int U = L::kPartKeys / 64;  // keys a thread
+      struct Place {
+        float *dst;
+        float old;
+      };
+      // where key tid - 64 + 64 u of a tile lies, given its page, and what is there
+      auto page_at = [&](int key) {
+        return key < w.T ? p.block_table[static_cast<size_t>(w.b) * p.max_blocks + key / kPageSize]
+                         : -1;
+      };
+      auto place_of = [&](int key, int page) {
+        Place v = {nullptr, 0.f};
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {  // else reported
+          v.dst = p.weights + (static_cast<size_t>(page) * p.n_kv_heads + w.g) * kPageSize +
+                  key % kPageSize;
+          if (key < w.T - p.fresh) v.old = *v.dst;
+        }
+        return v;
+      };
       int n = 0;  // sums taken
       for (; more && ok; more = next_job(at)) {
-        for (int j = 0; j < (PASS == kFew ? w.n : 1); ++j, ++n) {
-          const int key0 = (PASS == kFew ? w.s0 + j : w.held0) * kRows;
-          float *dst[L::kPartKeys / 64];
-          float old[L::kPartKeys / 64];
+        const int tiles = PASS == kFew ? w.n : 1;
+        const int key0 = (PASS == kFew ? w.s0 : w.held0) * kRows + tid - 64;
+        // a tile's old weights are fetched a tile ahead, its pages two
+        int page[U];
+        Place next[U];
 #pragma unroll
-          for (int u = 0; u < L::kPartKeys / 64; ++u) {
-            const int key = key0 + tid - 64 + 64 * u;
-            dst[u] = nullptr;
-            old[u] = 0.f;
-            if (key >= w.T) continue;
-            const int page =
-                p.block_table[static_cast<size_t>(w.b) * p.max_blocks + key / kPageSize];
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages))
-              continue;  // reported
-            dst[u] = p.weights + (static_cast<size_t>(page) * p.n_kv_heads + w.g) * kPageSize +
-                     key % kPageSize;
-            if (key < w.T - p.fresh) old[u] = *dst[u];
+        for (int u = 0; u < U; ++u) {
+          next[u] = place_of(key0 + 64 * u, page_at(key0 + 64 * u));
+          if (PASS == kFew) page[u] = page_at(key0 + kRows + 64 * u);
+        }
+        for (int j = 0; j < tiles; ++j, ++n) {
+          Place here[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            here[u] = next[u];
+            if (PASS == kFew) {
+              const int key = key0 + (j + 1) * kRows + 64 * u;
+              next[u] = place_of(key, page[u]);
+              page[u] = page_at(key + kRows);
+            }
           }
           if (!(ok = warp_wait(bar(kBarPart + (n & 1)), (n >> 1) & 1, abort_flag))) break;
           const float *part = reinterpret_cast<const float *>(smem + L::kPart) +
-                              (n & 1) * 4 * L::kPartKeys + tid - 64;
+                              (n & 1) * L::kParts * L::kPartKeys + tid - 64;
+          float sum[U];
 #pragma unroll
-          for (int u = 0; u < L::kPartKeys / 64; ++u) {
-            float sum = 0.f;
+          for (int u = 0; u < U; ++u) {
+            sum[u] = 0.f;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if (PASS == kMany || y < w.n_held) sum += part[y * L::kPartKeys + 64 * u];
-            if (dst[u]) *dst[u] = old[u] + sum;
+            for (int y = 0; y < L::kParts; ++y)
+              if (PASS == kMany || y < 2 * w.n_held) sum[u] += part[y * L::kPartKeys + 64 * u];
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarPartFree + (n & 1)));
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (here[u].dst) *here[u].dst = here[u].old + sum[u];
         }
       }
       if (!ok && lane == 0) raise_abort(p.status, abort_flag);
@@ -534,29 +572,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
     };
+    const int pair = y & 1, half = y >> 1;  // the chunks it takes, and which columns
     if constexpr (PASS == kRowsPass) {
+      const int rt = w.held0 + y, q0 = rt / p.n_hsub * p.nq;
+      const int lim = w.ctx + min(q0 + r / p.hb, p.n_new - 1);  // the last key row r sees
+      const int lim_all = w.ctx + q0;                           // .. that every row does
+      const bool idle = 32 * (warp & 3) >= rows_of(p, rt);      // none of the warp's rows is one
+      RowState st = {kNoKey, make_float2(0.f, 0.f)};
       if (y < w.n_held) {
-        const int rt = w.held0 + y, q = query_of(p, rt, r);
-        const int lim = w.ctx + max(q, 0);                      // last key row r sees
-        const int lim_all = w.ctx + rt / p.n_hsub * p.nq;       // every row of the tile does
-        const bool idle = 32 * (warp & 3) >= rows_of(p, rt);    // none of the warp's rows is one
-        RowState st = {kNoKey, make_float2(0.f, 0.f)};
-        for (int j = 0; j < w.n; ++j) {
-          if (!(ok = warp_wait(bar(kBarS + y), j & 1, abort_flag))) break;
-          tc::fence_after_sync();
-          if (idle) {
-            release(y);
-            continue;
+        const uint32_t at = tmem + kRows * y + lanes;
+        // 64 keys at a time, in one copy of the code: with four (unrolled over tiles) the
+        // other warps' instructions left the cache, and each of their waits took 450 cycles
+#pragma unroll 1
+        for (int i = 0; i < 2 * w.n; ++i) {
+          if ((i & 1) == 0) {
+            if (!(ok = warp_wait(bar(kBarS + y), (i >> 1) & 1, abort_flag))) break;
+            tc::fence_after_sync();
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          if (!idle) {
             uint32_t s[64];
-            tc::ld32(tmem + kRows * y + 64 * h + lanes, *reinterpret_cast<uint32_t(*)[32]>(s));
-            tc::ld32(tmem + kRows * y + 64 * h + lanes + 32,
-                     *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            tc::ld32(at + 64 * (i & 1), *reinterpret_cast<uint32_t(*)[32]>(s));
+            tc::ld32(at + 64 * (i & 1) + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             tc::wait_ld();
-            if (h == 1) release(y);
-            take_scores(s, (w.s0 + j) * kRows + 64 * h, lim, lim_all, qs, st);
+            if (i & 1) release(y);
+            take_scores(s, w.s0 * kRows + 64 * i, lim, lim_all, qs, st);
+          } else if (i & 1) {
+            release(y);
           }
         }
         if (ok) {
@@ -564,91 +605,89 @@ __global__ void __launch_bounds__(kThreads, 1)
           const size_t tile = static_cast<size_t>(w.bg) * p.n_rt + rt;
           p.states[(tile * p.n_ranges + w.range) * kRows + r] = make_float2(st.m, l);
           if (p.n_ranges == 1)
-            p.stats[tile * kRows + r] = q < 0 ? -INFINITY : stat_of(st.m, l);
+            p.stats[tile * kRows + r] = query_of(p, rt, r) < 0 ? -INFINITY : stat_of(st.m, l);
         }
       }
     } else if constexpr (PASS == kFew) {
       float *part = reinterpret_cast<float *>(smem + L::kPart) + r;
       ok = warp_wait(bar(kBarT), 0, abort_flag);
       const int chunks = w.n * w.n_held;
-      int j = y / w.n_held, x = y - j * w.n_held;  // of chunk n
-      for (int n = y; n < chunks && ok; n += 4) {
-        if (!(ok = warp_wait(bar(kBarS + y), (n >> 2) & 1, abort_flag))) break;
+      int j = pair / w.n_held, x = pair - j * w.n_held;  // of chunk n
+      const int last_rows = rows_of(p, w.n_held - 1);    // of the last query tile's
+      for (int n = pair; n < chunks && ok; n += 2) {
+        const int buf = n & 3;
+        if (!(ok = warp_wait(bar(kBarS + buf), (n >> 2) & 1, abort_flag))) break;
         tc::fence_after_sync();
-        const int key0 = (w.s0 + j) * kRows, rows = rows_of(p, x);
-        const int q0 = x / p.n_hsub * p.nq;  // the tile's first query
+        const int key0 = (w.s0 + j) * kRows;
+        const int c0 = 64 * half;
+        const int rows = (x >= w.n_held - p.n_hsub ? last_rows : p.hb * p.nq) - c0;  // of this half
+        uint32_t s[2][1][32];
+        const uint32_t at = tmem + kRows * buf + lanes + c0;
+        if (rows > 0) tc::ld32(at, s[0][0]);
+        if (rows > 32) tc::ld32(at + 32, s[1][0]);
+        tc::wait_ld();
+        release(buf);
+        const int q0 = (p.n_hsub == 1 ? x : x / p.n_hsub) * p.nq;  // the tile's first query
         const bool all = key0 + kRows - 1 <= w.ctx + q0;  // every row sees every key
         float2 sum[1] = {make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 32) {
-          if (c0 >= rows) {
-            if (c0 - 32 < rows) release(y);
-            continue;
-          }
-          uint32_t s[1][32];
-          tc::ld32(tmem + kRows * y + lanes + c0, s[0]);
-          tc::wait_ld();
-          if (c0 == kRows - 32) release(y);
-          const uint32_t lse = sb + L::kStats + x * stats_bytes + c0 * 4;
-          const int from[1] = {(key0 + r - w.ctx - q0) * p.hb - c0};
+        for (int h = 0; h < 2; ++h) {
+          if (32 * h >= rows) break;
+          const uint32_t lse = sb + L::kStats + x * stats_bytes + (c0 + 32 * h) * 4;
+          const int from[1] = {(key0 + r - w.ctx - q0) * p.hb - c0 - 32 * h};
           if (all)
-            add_weights<1, false>(s, lse, from, qs, sum);
+            add_weights<1, false>(s[h], lse, from, qs, sum);
           else
-            add_weights<1, true>(s, lse, from, qs, sum);
+            add_weights<1, true>(s[h], lse, from, qs, sum);
         }
         if (j >= 2 && !(ok = warp_wait(bar(kBarPartFree + (j & 1)), ((j >> 1) - 1) & 1, abort_flag)))
           break;
-        part[((j & 1) * 4 + x) * kRows] = sum[0].x + sum[0].y;
+        part[((j & 1) * L::kParts + 2 * x + half) * kRows] = sum[0].x + sum[0].y;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPart + (j & 1)));
-        for (x += 4; x >= w.n_held; x -= w.n_held) ++j;
+        for (x += 2; x >= w.n_held; x -= w.n_held) ++j;
       }
     } else {
       float *part = reinterpret_cast<float *>(smem + L::kPart) + y * 2 * kRows + r;
-      int c = 0, job = 0;  // tiles, jobs
-      const int pair = y & 1, half = y >> 1;  // which tiles, which 64 of their rows
+      int c = 0, job = 0, st = 0;  // tiles, jobs, the tile's stage
+      uint32_t round = 0;
       for (; more && ok; more = next_job(at), ++job) {
         const int key0 = w.held0 * kRows;
         float2 sum[2];
         sum[0] = sum[1] = make_float2(0.f, 0.f);
-        for (int j = 0; j < w.n; ++j) {
-          const int t = c + j, st = t % S;
-          if ((t & 1) != pair) continue;
-          if (!(ok = warp_wait2(bar(kBarS + pair), (t >> 1) & 1, bar(kBarFull + st), (t / S) & 1,
+        for (int j = 0; j < w.n; ++j, ++c) {
+          const int buf = c & 1;
+          if (!(ok = warp_wait2(bar(kBarS + buf), (c >> 1) & 1, bar(kBarFull + st), round & 1,
                                 abort_flag)))
             break;
           tc::fence_after_sync();
-          const int q0 = (w.s0 + j) / p.n_hsub * p.nq;
-          const bool all = key0 + 2 * kRows - 1 <= w.ctx + q0;
+          uint32_t s[2][32];
 #pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 32) {
-            uint32_t s[2][32];
+          for (int x = 0; x < 2; ++x)
+            tc::ld32(tmem + kRows * (2 * buf + x) + lanes + 32 * y, s[x]);
+          tc::wait_ld();
+          release(buf);
+          const int q0 = (p.n_hsub == 1 ? w.s0 + j : (w.s0 + j) / p.n_hsub) * p.nq;
+          const uint32_t lse = sb + L::kStats + st * stats_bytes + 32 * y * 4;
+          int from[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              tc::ld32(tmem + kRows * (2 * pair + x) + lanes + 64 * half + c0, s[x]);
-            tc::wait_ld();
-            if (c0 == 32) release(pair);
-            const uint32_t lse = sb + L::kStats + st * stats_bytes + (64 * half + c0) * 4;
-            int from[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              from[x] = (key0 + x * kRows + r - w.ctx - q0) * p.hb - 64 * half - c0;
-            if (all)
-              add_weights<2, false>(s, lse, from, qs, sum);
-            else
-              add_weights<2, true>(s, lse, from, qs, sum);
-          }
+          for (int x = 0; x < 2; ++x)
+            from[x] = (key0 + x * kRows + r - w.ctx - q0) * p.hb - 32 * y;
+          if (key0 + 2 * kRows - 1 <= w.ctx + q0)
+            add_weights<2, false>(s, lse, from, qs, sum);
+          else
+            add_weights<2, true>(s, lse, from, qs, sum);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarFree + st));
+          if (++st == S) st = 0, ++round;
         }
         if (!ok) break;
-        c += w.n;
         if (job >= 2 &&
             !(ok = warp_wait(bar(kBarPartFree + (job & 1)), ((job >> 1) - 1) & 1, abort_flag)))
           break;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          part[(job & 1) * 4 * 2 * kRows + x * kRows] = sum[x].x + sum[x].y;
+          part[(job & 1) * L::kParts * 2 * kRows + x * kRows] = sum[x].x + sum[x].y;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPart + (job & 1)));
       }
@@ -743,10 +782,11 @@ int launch_t(const WeightsLaunch &a, cudaStream_t stream) {
   p.states = static_cast<float2 *>(a.workspace);
   p.stats = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + states_bytes(lists, y));
   p.status = a.status;
-  // (a zero scale becomes a factor small enough that every weight is the same: a masked
-  // score, -inf, times zero would be NaN)
-  p.qscale = a.scale * kLog2e;
-  if (fabsf(p.qscale) < 1e-30f) p.qscale = a.scale < 0.f ? -1e-30f : 1e-30f;
+  // The rows pass takes the maximum of the raw scores, so it needs a positive factor: a
+  // negative scale turns the first operand's sign instead, and a zero scale becomes a factor
+  // small enough that every weight is the same.
+  p.qscale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+  p.negate = a.scale < 0.f ? tc::kNegateA : 0u;
   p.n_new = a.n_new;
   p.n_kv_heads = a.n_kv_heads;
   p.group = a.n_q_heads / a.n_kv_heads;
