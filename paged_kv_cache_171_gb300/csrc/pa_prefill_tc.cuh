@@ -401,8 +401,25 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
   const int last_first = w.kmax - (w.t0 + n - 1) * kKeys + 1;
   const bool cleared = last_first < kKeys;  // the last V tile waits for the clearing
 
+  // Trees: issued by an elected lane, so that the operands stay in uniform registers, with
+  // 32-bit descriptors (a tile of 64 drafted tokens over 32k: 346 -> XXX us).
+  const bool issuer = TREE ? tc::elect_one() : lane == 0;
+  const uint32_t lq = tc::desc_low(sb + L::kQ + (IL ? 0 : x * L::kQBytes));
+  const uint32_t lk = tc::desc_low(sb + (IL ? L::kK0Il : L::kK0));
+  const uint32_t lv = tc::desc_low(sb + (IL ? L::kV0Il : L::kV0), L::kColBlk);
   auto s_mma = [&](int t) {  // S_x = Q_x K_t^T; then K stage t % SK is free for x
-    if (lane == 0) {
+    if (TREE) {
+      if (issuer) {
+        const uint32_t k = lk + (t % SK) * (L::kKVBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < KSQ; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::kColBlk + (kk & 3) * 32) >> 4;
+          tc::mma_f16_low(tSx, lq + off, k + off, kIdS, kk > 0);
+        }
+        tc::commit(bar(kBarS + x));
+        tc::commit(bar(kBarKFree + 4 * x + t % SK));
+      }
+    } else if (lane == 0) {
       const uint64_t dk = dk0 + static_cast<uint64_t>(((t % SK) * L::kKVBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < KSQ; ++kk) {
@@ -419,7 +436,24 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
   // Split rows: the remainders are in rows 64-127 of the same columns, so
   // one pass; else one or two passes as the softmax decided for the tile.
   auto pv_mma = [&](int j, int t, int h, int n_ph) {  // the j-th key tile of x is t
-    if (lane == 0) {
+    if (TREE) {
+      if (issuer) {
+        const uint32_t v = lv + (t % SV) * (L::kKVBytes >> 4) + ((4 * h * 2048) >> 4);
+        const uint32_t pa = tSx + 32 * h;
+#pragma unroll
+        for (int ph = 0; ph < 2; ++ph) {
+          if (ph >= n_ph) break;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_f16_tmem_a_low(tOx, pa + 64 * ph + 8 * kk, v + ((kk * 2048) >> 4), kIdO,
+                                   (j > 0 || h > 0 || ph > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (h == 1) {
+          tc::commit(bar(kBarVFree + 4 * x + t % SV));
+          if (j == nx - 1) tc::commit(bar(kBarO + x));
+        }
+      }
+    } else if (lane == 0) {
       const uint64_t dv = dv0 + static_cast<uint64_t>(((t % SV) * L::kKVBytes) >> 4);
       const uint32_t pa = tSx + 32 * h;
 #pragma unroll
@@ -475,7 +509,7 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
     }
   }
   if (!ok) {
-    if (lane == 0) {
+    if (issuer) {
       raise_abort(status, abort_flag);
       tc::commit(bar(kBarDrain + x));  // arrives once every MMA issued so far is done
     }
@@ -968,36 +1002,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
 
-  if (warp == kKLoadWarp || warp == kVLoadWarp) {
+  auto load_role = [&]() {
     const bool is_v = warp == kVLoadWarp;
     const int32_t *bt_row = p.block_table + static_cast<size_t>(w.b) * p.max_blocks;
     if (w.il)
-      load_tiles<D, true, TREE, BF16>(is_v, is_v ? &vmap : &kmap, sb, bt_row, n_pages, w, p.num_pages,
-                          p.n_kv_heads * 16, p.status, abort_flag, bad_v, lane);
+      load_tiles<D, true, TREE, BF16>(is_v, is_v ? &vmap : &kmap, sb, bt_row, n_pages, w,
+                                      p.num_pages, p.n_kv_heads * 16, p.status, abort_flag,
+                                      bad_v, lane);
     else
-      load_tiles<D, false, TREE, BF16>(is_v, is_v ? &vmap : &kmap, sb, bt_row, n_pages, w, p.num_pages,
-                           p.n_kv_heads * 16, p.status, abort_flag, bad_v, lane);
-  } else if (warp < 2) {
+      load_tiles<D, false, TREE, BF16>(is_v, is_v ? &vmap : &kmap, sb, bt_row, n_pages, w,
+                                       p.num_pages, p.n_kv_heads * 16, p.status, abort_flag,
+                                       bad_v, lane);
+  };
+  auto mma_role = [&]() {
     const volatile int *mode_x = mode + warp;
     if (w.sr)
       mma_tiles<D, BF16, true, true, TREE>(warp, sb, tmem, w, p.status, abort_flag, mode_x, lane);
     else if (w.il)
       mma_tiles<D, BF16, true, false, TREE>(warp, sb, tmem, w, p.status, abort_flag, mode_x, lane);
     else
-      mma_tiles<D, BF16, false, false, TREE>(warp, sb, tmem, w, p.status, abort_flag, mode_x, lane);
-  } else if (warp >= kSoftmaxWarp0) {
+      mma_tiles<D, BF16, false, false, TREE>(warp, sb, tmem, w, p.status, abort_flag, mode_x,
+                                             lane);
+  };
+  auto softmax_role = [&]() {
     float *ml = reinterpret_cast<float *>(smem + L::kML);
     float *scratch = reinterpret_cast<float *>(smem + L::kQ);
     const int x = (warp - kSoftmaxWarp0) >> 2;
     if (w.sr)
-      softmax_tiles<D, GT, BF16, true, true, TREE>(sb, tmem, p, w, abort_flag, mode + x, votes, ml,
-                                             scratch, x, warp, lane, bad_v);
+      softmax_tiles<D, GT, BF16, true, true, TREE>(sb, tmem, p, w, abort_flag, mode + x, votes,
+                                                   ml, scratch, x, warp, lane, bad_v);
     else if (w.il)
-      softmax_tiles<D, GT, BF16, true, false, TREE>(sb, tmem, p, w, abort_flag, mode + x, votes, ml,
-                                              scratch, x, warp, lane, bad_v);
+      softmax_tiles<D, GT, BF16, true, false, TREE>(sb, tmem, p, w, abort_flag, mode + x, votes,
+                                                    ml, scratch, x, warp, lane, bad_v);
     else
-      softmax_tiles<D, GT, BF16, false, false, TREE>(sb, tmem, p, w, abort_flag, mode + x, votes, ml,
-                                               scratch, x, warp, lane, bad_v);
+      softmax_tiles<D, GT, BF16, false, false, TREE>(sb, tmem, p, w, abort_flag, mode + x, votes,
+                                                     ml, scratch, x, warp, lane, bad_v);
+  };
+  if constexpr (TREE) {
+    // The softmax warpgroups take registers that the other warps do not use: of the 384 x 168
+    // the block was launched with, 128 x 80 + 256 x 208 = 63488.
+    static_assert(128 * 80 + 256 * 208 <= kThreads * 168, "the split draws on the launch's");
+    if (warp < kSoftmaxWarp0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      if (warp >= kKLoadWarp)
+        load_role();
+      else
+        mma_role();
+      __syncwarp();
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      softmax_role();
+      __syncwarp();
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+    }
+  } else if (warp == kKLoadWarp || warp == kVLoadWarp) {
+    load_role();
+  } else if (warp < 2) {
+    mma_role();
+  } else if (warp >= kSoftmaxWarp0) {
+    softmax_role();
   }
   tc::fence_before_sync();
   __syncthreads();

@@ -153,10 +153,10 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The high half of a descriptor of smem_desc_sw128 with a stride of 1024 bytes; the low half
-// holds the address and (K-major tiles: 1) the leading dimension's offset.
+// holds the address and the leading dimension's offset.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) {
-  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo_bytes = 16) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
 }
 // mma_f16 of two K-major 128-byte-swizzled tiles given by the low halves.
 __device__ __forceinline__ void mma_f16_low(uint32_t d_tmem, uint32_t a_low, uint32_t b_low,
@@ -167,6 +167,18 @@ __device__ __forceinline__ void mma_f16_low(uint32_t d_tmem, uint32_t a_low, uin
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+
+// mma_f16_tmem_a with B's descriptor given by its low half.
+__device__ __forceinline__ void mma_f16_tmem_a_low(uint32_t d_tmem, uint32_t a_tmem,
+                                                   uint32_t b_low, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 
