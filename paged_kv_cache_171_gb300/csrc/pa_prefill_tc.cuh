@@ -441,13 +441,9 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
         const uint32_t v = lv + (t % SV) * (L::kKVBytes >> 4) + ((4 * h * 2048) >> 4);
         const uint32_t pa = tSx + 32 * h;
 #pragma unroll
-        for (int ph = 0; ph < 2; ++ph) {
-          if (ph >= n_ph) break;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_f16_tmem_a_low(tOx, pa + 64 * ph + 8 * kk, v + ((kk * 2048) >> 4), kIdO,
-                                   (j > 0 || h > 0 || ph > 0 || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_f16_tmem_a_low(tOx, pa + 8 * kk, v + ((kk * 2048) >> 4), kIdO,
+                                 (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
         if (h == 1) {
           tc::commit(bar(kBarVFree + 4 * x + t % SV));
           if (j == nx - 1) tc::commit(bar(kBarO + x));
@@ -488,7 +484,7 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
         // written before the softmax's first hand-off of this tile (the
         // barrier's acquire makes it visible); rewritten only after S_x of
         // a later tile, which is issued below
-        if (!SR) n_ph = *mode_x ? 1 : 2;
+        if (!SR && !TREE) n_ph = *mode_x ? 1 : 2;
         if (TREE && t >= w.tz()) {
           const uint32_t use = (t - w.tz()) / (IL && (SV & 1) ? 2 * SV : SV);
           ok = warp_wait(bar(kBarVTree + rv.full(t)), use & 1, abort_flag);
@@ -573,7 +569,7 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
     const int jo = j - 1 + x;
     if (jo >= 0 && jo < w.n_tiles[x ^ 1]) {
       if (!warp_wait(bar(kBarP + 2 * (x ^ 1)), jo & 1, abort_flag) ||
-          !warp_wait(bar(kBarP + 2 * (x ^ 1) + 1), jo & 1, abort_flag)) {
+          (!TREE && !warp_wait(bar(kBarP + 2 * (x ^ 1) + 1), jo & 1, abort_flag))) {
         bad = true;
         break;
       }
@@ -698,6 +694,8 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
     };
     if constexpr (SR) {
       tile_p(std::integral_constant<int, 2>{}, 0);
+    } else if constexpr (TREE) {
+      tile_p(std::integral_constant<int, 1>{}, 0);
     } else {
       // Keys 0-63: head terms first (both modes need them; the weights stay
       // in s for a remainder), the warp's vote posted after the first 32
@@ -1040,10 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if constexpr (TREE) {
     // The softmax warpgroups take registers that the other warps do not use: of the 384 x 168
-    // the block was launched with, 128 x 80 + 256 x 208 = 63488.
-    static_assert(128 * 80 + 256 * 208 <= kThreads * 168, "the split draws on the launch's");
+    // the block was launched with, 128 x 72 + 256 x 216 = 64512.
+    static_assert(128 * 72 + 256 * 216 <= kThreads * 168, "the split draws on the launch's");
     if (warp < kSoftmaxWarp0) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp >= kKLoadWarp)
         load_role();
       else
@@ -1051,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       softmax_role();
       __syncwarp();
       asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
