@@ -6,8 +6,8 @@
 //
 // A weight needs the row's final m and l, which no CTA has before the last key.  So the
 // pass over K and V stores each score (4 bytes a query head and token beside the 4 D
-// bytes a kv head and token of K and V) and a second, short kernel folds the rows'
-// partial states into (m, l) and out, reads the scores back, mostly from L2, and adds
+// bytes a kv head and token of K and V), a second, short kernel folds the rows' partial
+// states into (m, l) and out, and a third reads the scores back, mostly from L2, and adds
 // e^(s - m) / l over the group.  Reading K again instead would cost 2 D bytes a token
 // and kv head: 32 to 256 bytes against 8 a query head.
 //
@@ -39,7 +39,9 @@ constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its f
 constexpr int kWarps = 8;                   // a CTA, one CTA an SM
 constexpr int kTile = 8;                    // query rows a tile
 constexpr int kMinPages = 2;                // least pages a run has
-constexpr int kFoldThreads = 256;
+constexpr int kFoldThreads = 256;           // of the second and third kernel
+constexpr int kFoldTokens = 512;            // of the third, a round
+constexpr int kFoldElements = 32;           // of the second, a CTA
 
 struct WeightedParams {
   const uint16_t *q;
@@ -47,11 +49,13 @@ struct WeightedParams {
   float *out, *weights;
   float *states;  // [item + warp][kTile][D + 4]: O, m (log2), l
   int2 *span;     // [item]: first and last warp that holds a part of it
+  float2 *rows;   // [sequence][query head]: m, 1 / l
   float *scores;  // per tile [T][rows], tiles at (first row) * max_tokens
   int *status;
   float qscale;   // scale * log2 e
   int n_q_heads, n_kv_heads, group, n_sub, tile_rows, batch, max_blocks, num_pages, fresh;
-  int seg_tokens, segs;  // tokens a CTA of the second kernel looks after, CTAs an item
+  int parts;             // CTAs a list of the second kernel
+  int seg_tokens, segs;  // tokens a CTA of the third looks after, CTAs a list
 };
 
 template <int D>
@@ -370,105 +374,174 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
-// The second kernel: CTA (sequence x kv head, segment).  The rows' states are folded into
-// (m, 1 / l), one warp a row; out's elements are shared out among the segments' CTAs; then
-// a thread a token adds the group's weights to the pool.
+// Folds the states of a list's (sequence x kv head's) elements [e0, e1): an element is four
+// dimensions of a row.  Eight neighbouring threads go over its states, eight loads ahead of
+// the arithmetic, and join theirs by shuffles; no barrier.  out gets O / l, `rows` the (m, 1 / l)
+// of rows whose first element is among these.
 template <int D>
-__global__ void __launch_bounds__(kFoldThreads) weighted_fold_kernel(const WeightedParams p) {
-  extern __shared__ float2 rows[];  // [group]: m, 1 / l
-  const int bg = blockIdx.x / p.segs, seg = blockIdx.x - bg * p.segs;
-  const int b = bg / p.n_kv_heads, g = bg - b * p.n_kv_heads;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  griddep_release();
-  griddep_wait();  // the states and scores
-  const int tokens = tokens_of(p, b, false);
-  const int seg0 = seg * p.seg_tokens;
-  if (seg0 > 0 && seg0 >= tokens) return;
-  const int segs = max(1, (tokens + p.seg_tokens - 1) / p.seg_tokens);
-
-  for (int r = warp; r < p.group; r += kFoldThreads / 32) {
-    const int sub = r / p.tile_rows, rr = r - sub * p.tile_rows;
+__device__ __forceinline__ void fold_elements(const WeightedParams &p, int bg, int e0, int e1,
+                                              float2 *rows) {
+  constexpr int kOver = 8, kAhead = 4;
+  const int2 first_span = p.span[bg * p.n_sub];
+  for (int eb = e0; eb < e1; eb += kFoldThreads / kOver) {
+    const int e = eb + threadIdx.x / kOver;
+    const bool real = e < e1;
+    const int r = real ? e / (D / 4) : e0 / (D / 4), d = 4 * (e % (D / 4));
+    const int sub = p.n_sub == 1 ? 0 : r / p.tile_rows, rr = r - sub * p.tile_rows;
     const int item = bg * p.n_sub + sub;
-    const int2 span = p.span[item];
+    const int2 span = p.n_sub == 1 ? first_span : p.span[item];
+    const float *states = p.states + (static_cast<size_t>(item) * kTile + rr) * (D + 4);
     float m = kNoKey, l = 0.f;
-    for (int c = span.x + lane; c <= span.y; c += 32) {
-      const float2 ml = *reinterpret_cast<const float2 *>(
-          p.states + ((static_cast<size_t>(item) + c) * kTile + rr) * (D + 4) + D);
-      const float mn = fmaxf(m, ml.x);
-      l = l * ex2(m - mn) + ml.y * ex2(ml.x - mn);
-      m = mn;
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-      const float mo = __shfl_xor_sync(kFull, m, x), lo = __shfl_xor_sync(kFull, l, x);
-      const float mn = fmaxf(m, mo);
-      l = l * ex2(m - mn) + lo * ex2(mo - mn);
-      m = mn;
-    }
-    if (lane == 0) rows[r] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
-  }
-  __syncthreads();
-
-  // ---- out: four dimensions of a row at a time, a warp each, lanes over the states
-  const int n_el = p.group * (D / 4);
-  const int e0 = static_cast<int>(static_cast<int64_t>(n_el) * seg / segs);
-  const int e1 = static_cast<int>(static_cast<int64_t>(n_el) * (seg + 1) / segs);
-  for (int e = e0 + warp; e < e1; e += kFoldThreads / 32) {
-    const int r = e / (D / 4), d = 4 * (e % (D / 4));
-    const int sub = r / p.tile_rows, rr = r - sub * p.tile_rows;
-    const int item = bg * p.n_sub + sub;
-    const int2 span = p.span[item];
-    const float2 row = rows[r];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = span.x + lane; c <= span.y; c += 32) {
-      const float *s = p.states + ((static_cast<size_t>(item) + c) * kTile + rr) * (D + 4);
-      const float f = ex2(s[D] - row.x);
-      const float4 v = *reinterpret_cast<const float4 *>(s + d);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+    auto join = [&](float mo, float lo, float4 v) {
+      const float mn = fmaxf(m, mo), a = ex2(m - mn), f = ex2(mo - mn);
+      l = fmaf(lo, f, l * a);
+      acc.x = fmaf(v.x, f, acc.x * a);
+      acc.y = fmaf(v.y, f, acc.y * a);
+      acc.z = fmaf(v.z, f, acc.z * a);
+      acc.w = fmaf(v.w, f, acc.w * a);
+      m = mn;
+    };
+    for (int c = span.x + threadIdx.x % kOver; c <= span.y; c += kOver * kAhead) {
+      float2 ml[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {  // past the last state, it again
+        const float *s =
+            states + static_cast<size_t>(min(c + u * kOver, span.y)) * kTile * (D + 4);
+        ml[u] = *reinterpret_cast<const float2 *>(s + D);
+        v[u] = *reinterpret_cast<const float4 *>(s + d);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (c + u * kOver <= span.y) join(ml[u].x, ml[u].y, v[u]);
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-      acc.x += __shfl_xor_sync(kFull, acc.x, x);
-      acc.y += __shfl_xor_sync(kFull, acc.y, x);
-      acc.z += __shfl_xor_sync(kFull, acc.z, x);
-      acc.w += __shfl_xor_sync(kFull, acc.w, x);
+    for (int x = kOver / 2; x > 0; x >>= 1) {
+      float4 v;
+      const float mo = __shfl_xor_sync(kFull, m, x), lo = __shfl_xor_sync(kFull, l, x);
+      v.x = __shfl_xor_sync(kFull, acc.x, x);
+      v.y = __shfl_xor_sync(kFull, acc.y, x);
+      v.z = __shfl_xor_sync(kFull, acc.z, x);
+      v.w = __shfl_xor_sync(kFull, acc.w, x);
+      join(mo, lo, v);
     }
-    if (lane == 0)
-      *reinterpret_cast<float4 *>(
-          p.out + (static_cast<size_t>(b) * p.n_q_heads + g * p.group + r) * D + d) =
-          make_float4(acc.x * row.y, acc.y * row.y, acc.z * row.y, acc.w * row.y);
+    if (!real || threadIdx.x % kOver != 0) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (d == 0) rows[r] = make_float2(m, inv);
+    *reinterpret_cast<float4 *>(p.out + (static_cast<size_t>(bg) * p.group + r) * D + d) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   }
+}
 
-  // ---- weights: a thread a token
-  const int t1 = min(tokens, seg0 + p.seg_tokens);
-  const size_t row0 = static_cast<size_t>(b) * p.n_q_heads + g * p.group;
+// Adds the group's weights for the tokens of a list's segment, two tokens a thread, so that
+// the two rounds of loads (page and scores; old weight) are covered by many threads.
+// NR: rows of a kv head where all of them are one tile of 1, 2, 4 or 8, else 0.
+template <int NR>
+__device__ __forceinline__ void add_tokens(const WeightedParams &p, int bg, int seg,
+                                           const float2 *rows) {
+  constexpr int U = kFoldTokens / kFoldThreads;  // tokens a thread
+  const int b = bg / p.n_kv_heads, g = bg - b * p.n_kv_heads;
+  const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
   const size_t max_tokens = static_cast<size_t>(p.max_blocks) * kPageSize;
-  for (int t = seg0 + tid; t < t1; t += kFoldThreads) {
-    const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + t / kPageSize];
-    float sum = 0.f;
-    for (int r0 = 0; r0 < p.group; r0 += p.tile_rows) {
-      const int n_r = min(p.tile_rows, p.group - r0);
-      const float *s = p.scores + (row0 + r0) * max_tokens + static_cast<size_t>(t) * n_r;
-      if (n_r % 4 == 0) {
-        for (int r = 0; r < n_r; r += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(s + r);
-          sum += ex2(v.x - rows[r0 + r].x) * rows[r0 + r].y;
-          sum += ex2(v.y - rows[r0 + r + 1].x) * rows[r0 + r + 1].y;
-          sum += ex2(v.z - rows[r0 + r + 2].x) * rows[r0 + r + 2].y;
-          sum += ex2(v.w - rows[r0 + r + 3].x) * rows[r0 + r + 3].y;
+  const size_t row0 = static_cast<size_t>(bg) * p.group;
+  const int tokens = tokens_of(p, b, false);
+  const int t1 = min(tokens, (seg + 1) * p.seg_tokens);
+  for (int t0 = seg * p.seg_tokens; t0 < t1; t0 += kFoldTokens) {
+    int page[U];
+    float sc[U][NR > 0 ? NR : 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + threadIdx.x + kFoldThreads * u;
+      page[u] = t < t1 ? table[t / kPageSize] : -1;
+      if constexpr (NR > 0) {
+        if (t >= t1) continue;
+        const float *s = p.scores + row0 * max_tokens + static_cast<size_t>(t) * NR;
+        if constexpr (NR == 1) {
+          sc[u][0] = s[0];
+        } else if constexpr (NR == 2) {
+          const float2 v = *reinterpret_cast<const float2 *>(s);
+          sc[u][0] = v.x, sc[u][1] = v.y;
+        } else {
+#pragma unroll
+          for (int r = 0; r < NR; r += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(s + r);
+            sc[u][r] = v.x, sc[u][r + 1] = v.y, sc[u][r + 2] = v.z, sc[u][r + 3] = v.w;
+          }
         }
-      } else {
-        for (int r = 0; r < n_r; ++r) sum += ex2(s[r] - rows[r0 + r].x) * rows[r0 + r].y;
       }
     }
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;  // reported
-    float *w = p.weights + (static_cast<size_t>(page) * p.n_kv_heads + g) * kPageSize +
-               t % kPageSize;
-    *w = (t < tokens - p.fresh ? *w : 0.f) + sum;
+    float *dst[U];
+    float sum[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + threadIdx.x + kFoldThreads * u;
+      dst[u] = nullptr;
+      sum[u] = 0.f;
+      if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(p.num_pages)) {
+        dst[u] = p.weights + (static_cast<size_t>(page[u]) * p.n_kv_heads + g) * kPageSize +
+                 t % kPageSize;  // (a bad page has been reported)
+        if (t < tokens - p.fresh) sum[u] = *dst[u];
+      }
+    }
+    float add[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) add[u] = 0.f;
+    if constexpr (NR > 0) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float2 row = rows[r];
+#pragma unroll
+        for (int u = 0; u < U; ++u) add[u] += ex2(sc[u][r] - row.x) * row.y;
+      }
+    } else {
+      for (int r0 = 0; r0 < p.group; r0 += p.tile_rows) {
+        const int n_r = min(p.tile_rows, p.group - r0);
+        for (int r = 0; r < n_r; ++r) {
+          const float2 row = rows[r0 + r];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int t = t0 + threadIdx.x + kFoldThreads * u;
+            if (dst[u])
+              add[u] += ex2(p.scores[(row0 + r0) * max_tokens + static_cast<size_t>(t) * n_r + r] -
+                            row.x) * row.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (dst[u]) *dst[u] = sum[u] + add[u];
   }
+}
+
+// The second and third kernel: CTA (list, part of its elements), CTA (list, segment).
+template <int D>
+__global__ void __launch_bounds__(kFoldThreads) weighted_fold_kernel(const WeightedParams p) {
+  griddep_release();
+  griddep_wait();  // the states
+  const int bg = blockIdx.x / p.parts, part = blockIdx.x - bg * p.parts, n = p.group * (D / 4);
+  fold_elements<D>(p, bg, part * kFoldElements, min(n, (part + 1) * kFoldElements),
+                   p.rows + static_cast<size_t>(bg) * p.group);
+}
+template <int NR>
+__global__ void __launch_bounds__(kFoldThreads) weighted_add_kernel(const WeightedParams p) {
+  griddep_release();
+  griddep_wait();  // the rows and the scores
+  const int bg = blockIdx.x / p.segs;
+  add_tokens<NR>(p, bg, blockIdx.x - bg * p.segs, p.rows + static_cast<size_t>(bg) * p.group);
+}
+
+// Both in one, a CTA a list: tables of one segment (a launch less: the host's call bounds
+// those; 1 x 512 tokens of 16 heads XXX us).
+template <int D, int NR>
+__global__ void __launch_bounds__(kFoldThreads) weighted_both_kernel(const WeightedParams p) {
+  griddep_release();
+  griddep_wait();
+  float2 *rows = p.rows + static_cast<size_t>(blockIdx.x) * p.group;
+  fold_elements<D>(p, blockIdx.x, 0, p.group * (D / 4), rows);
+  __syncthreads();
+  add_tokens<NR>(p, blockIdx.x, 0, rows);
 }
 
 // Row tiles of a group: as few as there can be, of nearly equal size.
@@ -479,7 +552,7 @@ void tiles_of(int group, int *n_sub, int *rows) {
 }
 
 struct Layout {
-  size_t span, scores, bytes;
+  size_t span, rows, scores, bytes;
 };
 Layout layout_of(int batch, int n_q_heads, int n_kv_heads, int head_dim, int max_blocks,
                  int sms) {
@@ -488,7 +561,8 @@ Layout layout_of(int batch, int n_q_heads, int n_kv_heads, int head_dim, int max
   const size_t items = static_cast<size_t>(batch) * n_kv_heads * n_sub;
   Layout y;
   y.span = (items + static_cast<size_t>(sms) * kWarps) * kTile * (head_dim + 4) * sizeof(float);
-  y.scores = (y.span + items * sizeof(int2) + 15) & ~size_t(15);
+  y.rows = (y.span + items * sizeof(int2) + 15) & ~size_t(15);
+  y.scores = (y.rows + static_cast<size_t>(batch) * n_q_heads * sizeof(float2) + 15) & ~size_t(15);
   y.bytes = y.scores + static_cast<size_t>(batch) * n_q_heads * max_blocks * kPageSize *
                            sizeof(float);
   return y;
@@ -515,6 +589,7 @@ int launch_t(const WeightedLaunch &a, cudaStream_t stream) {
   p.weights = a.weights;
   p.states = reinterpret_cast<float *>(ws);
   p.span = reinterpret_cast<int2 *>(ws + y.span);
+  p.rows = reinterpret_cast<float2 *>(ws + y.rows);
   p.scores = reinterpret_cast<float *>(ws + y.scores);
   p.status = a.status;
   p.qscale = a.scale * kLog2e;
@@ -526,18 +601,37 @@ int launch_t(const WeightedLaunch &a, cudaStream_t stream) {
   p.max_blocks = a.max_blocks;
   p.num_pages = a.num_pages;
   p.fresh = a.fresh;
-  // about 16 CTAs an SM if every sequence filled its table, of 256 tokens or more
-  const int64_t all = static_cast<int64_t>(a.max_blocks) * kPageSize * a.batch * a.n_kv_heads;
-  const int64_t seg = (all / (16 * sms) + 255) / 256 * 256;
-  p.seg_tokens = static_cast<int>(seg < 256 ? 256 : seg);
+  // a round of tokens a CTA, more where full tables would make it over 128 CTAs an SM
+  const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
+  const int64_t rounds = (static_cast<int64_t>(a.max_blocks) * kPageSize + kFoldTokens - 1) /
+                         kFoldTokens;
+  const int64_t most = 128 * sms / lists > 1 ? 128 * sms / lists : 1;  // CTAs a list
+  const bool both = rounds <= 2;
+  p.seg_tokens = static_cast<int>(both ? rounds : (rounds + most - 1) / most) * kFoldTokens;
+  p.segs = (a.max_blocks * kPageSize + p.seg_tokens - 1) / p.seg_tokens;
+  p.parts = (p.group * (D / 4) + kFoldElements - 1) / kFoldElements;
   if (launch_pdl(kern, dim3(sms), dim3(kWarps * 32), WeightedSmem<D>::kAlloc, stream, kmap, vmap,
                  p) != cudaSuccess)
     return PA_ERR_CUDA;
-  p.segs = (a.max_blocks * kPageSize + p.seg_tokens - 1) / p.seg_tokens;
-  const dim3 grid(static_cast<unsigned>(a.batch) * a.n_kv_heads * p.segs);
-  return launch_pdl(weighted_fold_kernel<D>, grid, dim3(kFoldThreads),
-                    p.group * sizeof(float2), stream, p) == cudaSuccess
-             ? PA_OK : PA_ERR_CUDA;
+  const int rows_known = p.n_sub == 1 ? p.group : 0;
+  const dim3 block(kFoldThreads);
+  if (both) {
+    auto kern2 = rows_known == 8 ? weighted_both_kernel<D, 8>
+                 : rows_known == 4 ? weighted_both_kernel<D, 4>
+                 : rows_known == 2 ? weighted_both_kernel<D, 2>
+                 : rows_known == 1 ? weighted_both_kernel<D, 1> : weighted_both_kernel<D, 0>;
+    return launch_pdl(kern2, dim3(static_cast<unsigned>(lists)), block, 0, stream, p) ==
+                   cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  if (launch_pdl(weighted_fold_kernel<D>, dim3(static_cast<unsigned>(lists) * p.parts), block, 0,
+                 stream, p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  auto add = rows_known == 8 ? weighted_add_kernel<8>
+             : rows_known == 4 ? weighted_add_kernel<4>
+             : rows_known == 2 ? weighted_add_kernel<2>
+             : rows_known == 1 ? weighted_add_kernel<1> : weighted_add_kernel<0>;
+  return launch_pdl(add, dim3(static_cast<unsigned>(lists) * p.segs), block, 0, stream, p) ==
+                 cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
