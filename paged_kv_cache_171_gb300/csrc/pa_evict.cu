@@ -5,10 +5,12 @@
 // to the lowest position; a NaN weight behind every number).  The kept rows of K, V and
 // weights move to positions 0, 1, .. in their order.
 //
-// select_kernel: one CTA a (sequence, kv head).  The weights become 32-bit keys of the same
-// order; a radix select over digits of 11, 11 and 10 bits finds the least key kept and how
-// many of its ties are; then each warp numbers the kept ones of a span of tokens by ballots
-// and writes their positions.
+// select_kernel: a cluster of up to 8 CTAs a (sequence, kv head), each with a part of the
+// candidates in its shared memory as 32-bit keys of the weights' order.  A radix select over
+// digits of 11, 11 and 10 bits finds the least key kept and how many of its ties are: a CTA's
+// histogram each, every CTA sums them through distributed shared memory and picks the same
+// bin.  Then each warp numbers the kept ones of a span of tokens by ballots and writes their
+// positions.
 //
 // move_kernel: row src[j] to position j, where src is ascending, so src[j] >= j: the list
 // may be worked off in place from its start, if a row is stored only when every row of the
@@ -26,10 +28,11 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 49152;  // keys of a row that shared memory holds
 constexpr int kSelSmem = kSelKeys * 4;
 constexpr int kBins = 2048;
+constexpr int kLoadAhead = 4;    // tokens a thread fetches at a time
 
 struct SelectParams {
   const float *weights;
@@ -39,6 +42,7 @@ struct SelectParams {
   int32_t *new_lens;
   int *status;
   int n_kv_heads, batch, max_blocks, num_pages, budget, sink, recent;
+  int held_keys;   // keys that a CTA's shared memory has room for
 };
 
 // Ascending with the weight; NaN below every number, -0 as 0.
@@ -57,28 +61,48 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums) {
   }
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
+  int before = lane < warp ? warp_sums[lane] : 0;  // of the warps before this one
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, s, o);
-      if (lane >= o) s += x;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  if (warp > 0) v += warp_sums[warp - 1];
-  __syncthreads();
+  for (int o = kSelWarps / 2; o > 0; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
+  return v + __shfl_sync(kFull, before, 0);
+}
+
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ int cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+// Every thread of the cluster: shared memory written before it is seen behind it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Four words at the place in rank `rank`'s shared memory that p has in this CTA's.
+__device__ __forceinline__ int4 load_of(const int *p, int rank) {
+  uint32_t at;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at));
   return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins];
-  __shared__ int sums[32], sums2[32];
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ int sums[3][kSelWarps], sums2[kSelWarps];
   __shared__ int pick[2];
+  __shared__ __align__(16) int counts[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.n_kv_heads, h = blockIdx.x - b * p.n_kv_heads;
+  const int rank = cluster_rank(), ranks = cluster_size();
+  const int bh = blockIdx.x / ranks, b = bh / p.n_kv_heads, h = bh - b * p.n_kv_heads;
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
   griddep_release();
   griddep_wait();
   const int most = p.max_blocks * kPageSize;
@@ -87,15 +111,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     if (tid == 0) record_error(p.status, PA_ERR_BAD_CTX);
     T = T < 0 ? 0 : most;
   }
-  if (tid == 0 && h == 0) {
+  if (tid == 0 && h == 0 && rank == 0) {
     p.n_kept[b] = T > p.budget ? p.budget : -1 - T;
     p.new_lens[b] = min(T, p.budget);
   }
-  if (T <= p.budget) return;
+  if (T <= p.budget) return;  // the whole cluster
   const int32_t *row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-  const int lo = p.sink, hi = T - p.recent;  // the candidates
-  auto load_key = [&](int t) {
-    const int page = row[t / kPageSize];
+  int32_t *kept = p.kept + static_cast<size_t>(bh) * p.budget;
+  const int c0 = p.sink, c1 = T - p.recent;  // the candidates
+  // what stays anyway
+  for (int t = rank * kSelThreads + tid; t < c0; t += ranks * kSelThreads) kept[t] = t;
+  for (int t = c1 + rank * kSelThreads + tid; t < T; t += ranks * kSelThreads)
+    kept[p.budget - (T - t)] = t;
+  int need = p.budget - p.sink - p.recent;
+  if (need == 0) return;  // the whole cluster
+
+  // ---- this CTA's candidates [lo, hi), as keys
+  const int part = (c1 - c0 + ranks - 1) / ranks;
+  const int lo = min(c1, c0 + rank * part), hi = min(c1, lo + part);
+  auto page_at = [&](int t) { return row[t / kPageSize]; };
+  auto key_in = [&](int page, int t) {
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
       record_error(p.status, PA_ERR_BAD_BLOCK);
       return 0u;
@@ -103,66 +138,79 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     return key_of(p.weights[(static_cast<size_t>(page) * p.n_kv_heads + h) * kPageSize +
                             t % kPageSize]);
   };
-  const bool held = hi - lo <= kSelKeys;
-  if (held) {
-#pragma unroll 4
-    for (int t = lo + tid; t < hi; t += kSelThreads) keys[t - lo] = load_key(t);
-    __syncthreads();
+  const bool held = part <= p.held_keys;
+  __syncthreads();  // the histograms are clear
+  if (held) {  // with the first digit's histogram
+    for (int t0 = lo + tid; t0 < hi; t0 += kLoadAhead * kSelThreads) {
+      int page[kLoadAhead];
+      uint32_t k[kLoadAhead];
+#pragma unroll
+      for (int u = 0; u < kLoadAhead; ++u)
+        page[u] = t0 + u * kSelThreads < hi ? page_at(t0 + u * kSelThreads) : 0;
+#pragma unroll
+      for (int u = 0; u < kLoadAhead; ++u)
+        if (t0 + u * kSelThreads < hi) k[u] = key_in(page[u], t0 + u * kSelThreads);
+#pragma unroll
+      for (int u = 0; u < kLoadAhead; ++u)
+        if (t0 + u * kSelThreads < hi) {
+          keys[t0 + u * kSelThreads - lo] = k[u];
+          atomicAdd(&hist[0][k[u] >> 21], 1);
+        }
+    }
   }
-  auto key_at = [&](int t) { return held ? keys[t - lo] : load_key(t); };
+  auto key_at = [&](int t) { return held ? keys[t - lo] : key_in(page_at(t), t); };
 
   // ---- the least key kept, and how many of its ties
-  int need = p.budget - p.sink - p.recent;
-  uint32_t least = 0xffffffffu;  // none of the candidates
-  if (need > 0) {
-    uint32_t prefix = 0, known = 0;
-    int shift = 21, bits = 11;
-    for (int pass = 0; pass < 3; ++pass) {
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      const uint32_t mask = (1u << bits) - 1;
+  uint32_t prefix = 0, known = 0;
+  int shift = 21, bits = 11;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const uint32_t mask = (1u << bits) - 1;
+    if (pass > 0 || !held)
       for (int t = lo + tid; t < hi; t += kSelThreads) {
         const uint32_t k = key_at(t);
-        if ((k & known) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+        if ((k & known) == prefix) atomicAdd(&hist[pass][(k >> shift) & mask], 1);
       }
-      __syncthreads();
-      // thread i looks after bins kBins - 1 - 2 i and the one below: from the top
-      const int b0 = kBins - 1 - 2 * tid;
-      const int c0 = hist[b0], c1 = hist[b0 - 1];
-      const int incl = block_scan(c0 + c1, sums);
-      const int before = incl - c0 - c1;
-      if (before < need && need <= incl) {
-        const bool first = need <= before + c0;
-        pick[0] = first ? b0 : b0 - 1;
-        pick[1] = need - before - (first ? 0 : c0);
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(pick[0]) << shift;
-      known |= mask << shift;
-      need = pick[1];
-      __syncthreads();
-      shift = pass == 0 ? 10 : 0;
-      bits = pass == 0 ? 11 : 10;
+    cluster_sync();
+    // thread i looks after kPer bins from kBins - 1 - kPer i down
+    constexpr int kPer = kBins / kSelThreads;
+    const int b0 = kBins - 1 - kPer * tid;
+    int n[kPer], total = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) n[u] = 0;
+    for (int k = 0; k < ranks; ++k) {
+      const int4 v = load_of(&hist[pass][b0 + 1 - kPer], k);
+      n[0] += v.w, n[1] += v.z, n[2] += v.y, n[3] += v.x;
     }
-    least = prefix;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) total += n[u];
+    int before = block_scan(total, sums[pass]) - total;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      if (before < need && need <= before + n[u]) {
+        pick[0] = b0 - u;
+        pick[1] = need - before;
+      }
+      before += n[u];
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(pick[0]) << shift;
+    known |= mask << shift;
+    need = pick[1];
+    __syncthreads();  // (the next pass writes them behind a barrier of its own)
+    shift = pass == 0 ? 10 : 0;
+    bits = pass == 0 ? 11 : 10;
   }
+  const uint32_t least = prefix;
   const int ties = need;  // of key `least` that are kept
 
   // ---- positions of the kept: warp w numbers those of its span of tokens
-  const int span = ((T + 31) / 32 + 31) / 32 * 32;
-  const int t0 = warp * span, t1 = min(T, t0 + span);
+  const int span = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int t0 = lo + warp * span, t1 = min(hi, t0 + span);
   auto look = [&](int t, uint32_t *more, uint32_t *tie) {
-    bool m = false, e = false;
-    if (t < t1) {
-      m = t < lo || t >= hi;
-      if (!m && p.budget > p.sink + p.recent) {
-        const uint32_t k = key_at(t);
-        m = k > least;
-        e = k == least;
-      }
-    }
-    *more = __ballot_sync(kFull, m);
-    *tie = __ballot_sync(kFull, e);
+    const uint32_t k = t < t1 ? key_at(t) : 0u;
+    *more = __ballot_sync(kFull, t < t1 && k > least);
+    *tie = __ballot_sync(kFull, t < t1 && k == least);
   };
   int n_more = 0, n_tie = 0;
   uint32_t more, tie;
@@ -172,29 +220,39 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     n_tie += __popc(tie);
   }
   if (lane == 0) {
-    sums[warp] = n_more;
+    sums[0][warp] = n_more;
     sums2[warp] = n_tie;
   }
   __syncthreads();
   int at_more = 0, at_tie = 0;  // before the warp's span
   for (int w = 0; w < warp; ++w) {
-    at_more += sums[w];
+    at_more += sums[0][w];
     at_tie += sums2[w];
   }
-  int32_t *kept = p.kept + static_cast<size_t>(blockIdx.x) * p.budget;
+  if (warp == kSelWarps - 1 && lane == 0) {
+    counts[0] = at_more + n_more;
+    counts[1] = at_tie + n_tie;
+  }
+  cluster_sync();
+  for (int k = 0; k < rank; ++k) {
+    const int4 v = load_of(counts, k);
+    at_more += v.x;
+    at_tie += v.y;
+  }
   const uint32_t below = (1u << lane) - 1;
   for (int t = t0; t < t1; t += 32) {
     look(t + lane, &more, &tie);
     const int my_tie = at_tie + __popc(tie & below);
     const bool stays = (more >> lane & 1) || ((tie >> lane & 1) && my_tie < ties);
-    if (stays) kept[at_more + __popc(more & below) + min(my_tie, ties)] = t + lane;
+    if (stays) kept[c0 + at_more + __popc(more & below) + min(my_tie, ties)] = t + lane;
     at_more += __popc(more);
     at_tie += __popc(tie);
   }
+  cluster_sync();  // the others have read this CTA's shared memory
 }
 
 // ---- the move
-constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+constexpr int kMoveThreads = 256, kMoveUnroll = 4, kMovePart = 2048;
 
 struct MoveParams {
   char *k_cache, *v_cache;
@@ -209,70 +267,64 @@ struct MoveParams {
   int n_kv_heads, row_bytes, strips, max_blocks, dst_blocks, num_pages, max_keep;
 };
 
-// V: what a thread moves of a row; LPR threads a row.
+// V: what a thread moves of a row; lpr threads a row.  The rows' places are looked up a part
+// of the list at a time, so that nothing but the rows is waited for in the loop.
 template <typename V>
-__device__ __forceinline__ void move_rows(const MoveParams &p, char *base, size_t head_bytes,
-                                          int row_bytes, int offset, int lpr, int b, int h,
-                                          const int32_t *list, int n, int first) {
+__device__ __forceinline__ void move_rows(const MoveParams &p, char *base, int row_bytes,
+                                          int offset, int lpr, int b, int h, const int32_t *list,
+                                          int n, int first, int *from, int *to) {
   const int tid = threadIdx.x;
   const int per = kMoveThreads / lpr;  // rows a step
-  const int r = tid / lpr, c = offset + (tid % lpr) * static_cast<int>(sizeof(V));
+  const int r = tid / lpr;
+  base += offset + (tid % lpr) * static_cast<int>(sizeof(V));
   const int32_t *src_row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
   const int32_t *dst_row = p.dst_table + static_cast<size_t>(b) * p.dst_blocks;
-  const size_t page_bytes = head_bytes * p.n_kv_heads;
-  const size_t head = h * head_bytes;
-  auto place = [&](const int32_t *table, int blocks, int pos, size_t *off) {
+  auto place = [&](const int32_t *table, int blocks, int pos) {  // row of the pool, or -1
     const int page = pos / kPageSize < blocks ? table[pos / kPageSize] : -1;
-    *off = page * page_bytes + head + static_cast<size_t>(pos % kPageSize) * row_bytes + c;
-    return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-  };
-  struct Step {
-    size_t src[kMoveUnroll], dst[kMoveUnroll];
-    unsigned real;  // bit u: row u is to be moved
-  };
-  auto plan = [&](int j0, Step &s) {
-    s.real = 0;
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int j = j0 + u * per + r;
-      s.src[u] = s.dst[u] = 0;
-      if (j < n) {
-        const int from = first + (list ? list[j] : j);
-        const bool ok = place(src_row, p.max_blocks, from, &s.src[u]) &
-                        place(dst_row, p.dst_blocks, first + j, &s.dst[u]);
-        if (!ok)
-          record_error(p.status, PA_ERR_BAD_BLOCK);
-        else if (s.src[u] != s.dst[u])
-          s.real |= 1u << u;
-      }
-    }
+    return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)
+               ? (page * p.n_kv_heads + h) * kPageSize + pos % kPageSize : -1;
   };
   const int rows = per * kMoveUnroll;
-  Step now, then;
   V v[kMoveUnroll], w[kMoveUnroll];
-  auto load = [&](const Step &s, V (&x)[kMoveUnroll]) {
+  for (int part = 0; part < n; part += kMovePart) {
+    const int m = min(kMovePart, n - part);
+    if (part > 0) __syncthreads();  // the places before have been used
+#pragma unroll 4
+    for (int i = tid; i < m; i += kMoveThreads) {
+      const int j = part + i;
+      const int src = place(src_row, p.max_blocks, first + (list ? list[j] : j));
+      const int dst = place(dst_row, p.dst_blocks, first + j);
+      if (src < 0 || dst < 0) record_error(p.status, PA_ERR_BAD_BLOCK);
+      from[i] = src;
+      to[i] = src < 0 || src == dst ? -1 : dst;  // -1: not moved
+    }
+    __syncthreads();
+    auto load = [&](int i0, V (&x)[kMoveUnroll]) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (s.real >> u & 1) x[u] = __ldcg(reinterpret_cast<const V *>(base + s.src[u]));
-  };
-  plan(0, now);
-  load(now, v);
-  plan(rows, then);
-  for (int j0 = 0; j0 < n; j0 += rows) {
-    load(then, w);
-    __syncthreads();  // every row up to this chunk's last has been loaded
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int i = i0 + u * per + r;
+        if (i < m && to[i] >= 0)
+          x[u] = __ldcg(reinterpret_cast<const V *>(base + static_cast<size_t>(from[i]) * row_bytes));
+      }
+    };
+    load(0, v);
+    for (int i0 = 0; i0 < m; i0 += rows) {
+      load(i0 + rows, w);
+      __syncthreads();  // every row up to this chunk's last has been loaded
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (now.real >> u & 1) *reinterpret_cast<V *>(base + now.dst[u]) = v[u];
-    now = then;
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) v[u] = w[u];
-    plan(j0 + 2 * rows, then);
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int i = i0 + u * per + r;
+        if (i < m && to[i] >= 0)
+          *reinterpret_cast<V *>(base + static_cast<size_t>(to[i]) * row_bytes) = v[u];
+        v[u] = w[u];
+      }
+    }
   }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
   __shared__ int bad;
+  __shared__ int from[kMovePart], to[kMovePart];
   const int tid = threadIdx.x;
   const int bh = blockIdx.x, b = bh / p.n_kv_heads, h = bh - b * p.n_kv_heads;
   const int plane = blockIdx.y;  // strips of K, strips of V, the weights
@@ -312,13 +364,12 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
     if (tid == 0 && h == 0 && plane == 0) p.new_lens[b] = first + n;
   }
   if (plane == 2 * p.strips) {
-    move_rows<float>(p, reinterpret_cast<char *>(p.weights), kPageSize * sizeof(float),
-                     sizeof(float), 0, 1, b, h, list, n, first);
+    move_rows<float>(p, reinterpret_cast<char *>(p.weights), sizeof(float), 0, 1, b, h, list, n,
+                     first, from, to);
   } else {
     const int strip = plane % p.strips, bytes = p.row_bytes / p.strips;
-    move_rows<uint4>(p, plane < p.strips ? p.k_cache : p.v_cache,
-                     static_cast<size_t>(kPageSize) * p.row_bytes, p.row_bytes, strip * bytes,
-                     bytes / 16, b, h, list, n, first);
+    move_rows<uint4>(p, plane < p.strips ? p.k_cache : p.v_cache, p.row_bytes, strip * bytes,
+                     bytes / 16, b, h, list, n, first, from, to);
   }
 }
 
@@ -373,11 +424,28 @@ int launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   static ContextCache<bool> smem_set;
   if (set_smem_limit(select_kernel, kSelSmem, smem_set) != PA_OK) return PA_ERR_CUDA;
   const int64_t most = static_cast<int64_t>(a.max_blocks) * kPageSize;
-  const int64_t keys = most - a.sink - a.recent;
-  const size_t smem = keys <= 0 ? 0 : (keys < kSelKeys ? keys : kSelKeys) * 4;
-  if (launch_pdl(select_kernel, dim3(static_cast<unsigned>(a.batch) * a.n_kv_heads),
-                 dim3(kSelThreads), smem, stream, s) != cudaSuccess)
-    return PA_ERR_CUDA;
+  const int64_t keys = most - a.sink - a.recent > 0 ? most - a.sink - a.recent : 0;
+  // Few lists of many tokens: a cluster each, of 2048 keys or more a CTA (8 lists of 32768:
+  // XXX us with 1 CTA, XXX with 8).
+  const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
+  int ranks = 1;
+  while (ranks < 8 && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks) ranks *= 2;
+  const int64_t part = (keys + ranks - 1) / ranks;
+  s.held_keys = static_cast<int>(part < kSelKeys ? part : kSelKeys);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(lists * ranks));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = s.held_keys * sizeof(uint32_t);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, select_kernel, s) != cudaSuccess) return PA_ERR_CUDA;
   MoveParams p = {};
   p.list = s.kept;
   p.n_kept = s.n_kept;
