@@ -31,7 +31,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 49152;  // keys of a row that shared memory holds
 constexpr int kSelSmem = kSelKeys * 4;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048, kMaxRanks = 8;
 constexpr int kLoadAhead = 4;    // tokens a thread fetches at a time
 
 struct SelectParams {
@@ -178,10 +178,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     int n[kPer], total = 0;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) n[u] = 0;
-    for (int k = 0; k < ranks; ++k) {
-      const int4 v = load_of(&hist[pass][b0 + 1 - kPer], k);
-      n[0] += v.w, n[1] += v.z, n[2] += v.y, n[3] += v.x;
-    }
+    int4 v[kMaxRanks];
+#pragma unroll
+    for (int k = 0; k < kMaxRanks; ++k)  // all on their way at once
+      if (k < ranks) v[k] = load_of(&hist[pass][b0 + 1 - kPer], k);
+#pragma unroll
+    for (int k = 0; k < kMaxRanks; ++k)
+      if (k < ranks) n[0] += v[k].w, n[1] += v[k].z, n[2] += v[k].y, n[3] += v[k].x;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) total += n[u];
     int before = block_scan(total, sums[pass]) - total;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
 }
 
 // ---- the move
-constexpr int kMoveThreads = 256, kMoveUnroll = 4, kMovePart = 2048;
+constexpr int kMoveMaxThreads = 1024, kMoveUnroll = 4, kMovePart = 2048;
 
 struct MoveParams {
   char *k_cache, *v_cache;
@@ -274,7 +277,8 @@ __device__ __forceinline__ void move_rows(const MoveParams &p, char *base, int r
                                           int offset, int lpr, int b, int h, const int32_t *list,
                                           int n, int first, int *from, int *to) {
   const int tid = threadIdx.x;
-  const int per = kMoveThreads / lpr;  // rows a step
+  const int threads = blockDim.x;
+  const int per = threads / lpr;  // rows a step
   const int r = tid / lpr;
   base += offset + (tid % lpr) * static_cast<int>(sizeof(V));
   const int32_t *src_row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
@@ -290,7 +294,7 @@ __device__ __forceinline__ void move_rows(const MoveParams &p, char *base, int r
     const int m = min(kMovePart, n - part);
     if (part > 0) __syncthreads();  // the places before have been used
 #pragma unroll 4
-    for (int i = tid; i < m; i += kMoveThreads) {
+    for (int i = tid; i < m; i += threads) {
       const int j = part + i;
       const int src = place(src_row, p.max_blocks, first + (list ? list[j] : j));
       const int dst = place(dst_row, p.dst_blocks, first + j);
@@ -322,7 +326,7 @@ __device__ __forceinline__ void move_rows(const MoveParams &p, char *base, int r
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveMaxThreads) move_kernel(const MoveParams p) {
   __shared__ int bad;
   __shared__ int from[kMovePart], to[kMovePart];
   const int tid = threadIdx.x;
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
     __syncthreads();
     if (!bad) {  // ascending, and within the table
       bool wrong = false;
-      for (int j = tid; j < n; j += kMoveThreads) {
+      for (int j = tid; j < n; j += blockDim.x) {
         const int at = list[j], before = j > 0 ? list[j - 1] : -1;
         wrong |= at <= before || at >= most - first;
       }
@@ -373,7 +377,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
   }
 }
 
-int launch_move(const EvictLaunch &a, MoveParams &p, cudaStream_t stream) {
+// longest: rows of a list at most.
+int launch_move(const EvictLaunch &a, MoveParams &p, int longest, cudaStream_t stream) {
   p.k_cache = static_cast<char *>(a.k_cache);
   p.v_cache = static_cast<char *>(a.v_cache);
   p.weights = a.weights;
@@ -386,13 +391,17 @@ int launch_move(const EvictLaunch &a, MoveParams &p, cudaStream_t stream) {
   p.max_blocks = a.max_blocks;
   p.dst_blocks = a.dst_blocks;
   p.num_pages = a.num_pages;
-  // as many strips as give every SM four CTAs, of 32 bytes or more
+  // As many strips as give every SM a CTA, of 32 bytes or more, and CTAs of 1024 threads, so
+  // that one has 64 KB in flight: with four CTAs of 256 an SM instead, 1 x 4096 of 32768 tokens
+  // takes 52 us (37), 4 x 4096 of 8192 42 (32), 32 x 2048 110 (109).  Short lists: one chunk of
+  // 256 threads.
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   p.strips = 1;
-  while (p.strips < p.row_bytes / 32 && lists * p.strips * 2 < 4 * sms_or_default())
-    p.strips *= 2;
+  while (p.strips < p.row_bytes / 32 && lists * p.strips * 2 < sms_or_default()) p.strips *= 2;
+  const int threads = static_cast<int64_t>(longest) * (p.row_bytes / p.strips / 16) <=
+                              256 * kMoveUnroll ? 256 : kMoveMaxThreads;
   const dim3 grid(static_cast<unsigned>(lists), 2 * p.strips + (a.weights ? 1 : 0));
-  return launch_pdl(move_kernel, grid, dim3(kMoveThreads), 0, stream, p) == cudaSuccess
+  return launch_pdl(move_kernel, grid, dim3(threads), 0, stream, p) == cudaSuccess
              ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -429,7 +438,7 @@ int launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   // XXX us with 1 CTA, XXX with 8).
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   int ranks = 1;
-  while (ranks < 8 && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks) ranks *= 2;
+  while (ranks < kMaxRanks && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks) ranks *= 2;
   const int64_t part = (keys + ranks - 1) / ranks;
   s.held_keys = static_cast<int>(part < kSelKeys ? part : kSelKeys);
   cudaLaunchConfig_t cfg = {};
@@ -451,7 +460,7 @@ int launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   p.n_kept = s.n_kept;
   p.list_stride_b = static_cast<int64_t>(a.n_kv_heads) * a.budget;
   p.list_stride_h = a.budget;
-  return launch_move(a, p, stream);
+  return launch_move(a, p, static_cast<int>(a.budget < most ? a.budget : most), stream);
 }
 
 int launch_compact(const EvictLaunch &a, cudaStream_t stream) {
@@ -461,7 +470,7 @@ int launch_compact(const EvictLaunch &a, cudaStream_t stream) {
   p.ctx_lens = a.ctx_lens;
   p.n_keep = a.n_keep;
   p.max_keep = a.max_keep;
-  return launch_move(a, p, stream);
+  return launch_move(a, p, a.max_keep, stream);
 }
 
 }  // namespace pa
