@@ -521,6 +521,22 @@ int pa_append_kv_rope(const void *k_new, const void *v_new, const void *q, void 
                       int interleaved, pa_dtype dtype, pa_stream_t stream);
 
 /*
+ * pa_append_kv_rope_at -- pa_append_kv_rope with the positions to rotate by given apart from
+ * the places: token j is stored at position pos[j] and turned by cos_sin[rope_pos[j]].  The
+ * tokens of a drafted tree lie behind each other in the cache, but several of them stand at
+ * one position of their branches (pa_tree_mask's depth).  rope_pos: device int32 [n_tok],
+ * 0 .. max_pos - 1 (a token outside is skipped, PA_ERR_BAD_INDEX).
+ */
+int pa_append_kv_rope_at(const void *k_new, const void *v_new, const void *q, void *k_cache,
+                         void *v_cache, void *q_out, const int32_t *block_table,
+                         const int32_t *seq_idx, const int32_t *pos, const int32_t *rope_pos,
+                         const float *cos_sin, int n_tok, int64_t k_stride, int64_t v_stride,
+                         int64_t q_stride, int n_q_heads, int n_kv_heads, int head_dim,
+                         int page_size, int batch, int max_blocks_per_seq, int num_pages,
+                         int max_pos, int rot_dim, int interleaved, pa_dtype dtype,
+                         pa_stream_t stream);
+
+/*
  * The 4-bit cache.  One pool holds K and V:
  *   kv_cache: [num_pages][n_kv_heads][pa_kv4_block_bytes(head_dim)] bytes, and a
  *   block (one page of one kv head) is

@@ -31,7 +31,7 @@ __all__ = [
     "prefill_split", "pa_decode_cascade", "pa_decode_cascade_workspace_size",
     "decode_cascade",
     "append_kv",
-    "pa_append_kv_rope", "append_kv_rope", "rope_table",
+    "pa_append_kv_rope", "pa_append_kv_rope_at", "append_kv_rope", "rope_table",
     "pa_kv4_block_bytes", "kv4_cache", "pa_append_kv4", "append_kv4", "pa_read_kv4", "read_kv4",
     "pa_copy_pages_kv4", "copy_pages_kv4", "pa_decode_kv4", "pa_decode_kv4_workspace_size",
     "decode_kv4", "pa_prefill_kv4", "pa_prefill_kv4_workspace_size", "prefill_kv4",
@@ -122,6 +122,8 @@ def lib():
         J = ctypes.c_int64
         L.pa_append_kv_rope.argtypes = [P] * 10 + [I, J, J, J] + [I] * 11 + [P]
         L.pa_append_kv_rope.restype = I
+        L.pa_append_kv_rope_at.argtypes = [P] * 11 + [I, J, J, J] + [I] * 11 + [P]
+        L.pa_append_kv_rope_at.restype = I
         L.pa_kv4_block_bytes.argtypes = [I]
         L.pa_kv4_block_bytes.restype = Z
         L.pa_append_kv4.argtypes = [P] * 9 + [I, J, J, J] + [I] * 11 + [P]
@@ -450,6 +452,19 @@ def pa_append_kv_rope(k_new, v_new, q, k_cache, v_cache, q_out, block_table, seq
         q_stride, n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq,
         num_pages, max_pos, rot_dim, int(interleaved), dtype, _stream(stream))
     return _check(rc, "pa_append_kv_rope")
+
+
+def pa_append_kv_rope_at(k_new, v_new, q, k_cache, v_cache, q_out, block_table, seq_idx, pos,
+                         rope_pos, cos_sin, n_tok, k_stride, v_stride, q_stride, n_q_heads,
+                         n_kv_heads, head_dim, page_size, batch, max_blocks_per_seq, num_pages,
+                         max_pos, rot_dim, interleaved, dtype, stream=None) -> int:
+    rc = lib().pa_append_kv_rope_at(
+        _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(q_out),
+        _ptr(block_table), _ptr(seq_idx), _ptr(pos), _ptr(rope_pos), _ptr(cos_sin), n_tok,
+        k_stride, v_stride, q_stride, n_q_heads, n_kv_heads, head_dim, page_size, batch,
+        max_blocks_per_seq, num_pages, max_pos, rot_dim, int(interleaved), dtype,
+        _stream(stream))
+    return _check(rc, "pa_append_kv_rope_at")
 
 
 def pa_kv4_block_bytes(head_dim) -> int:
@@ -875,7 +890,7 @@ def _kv4_dims(kv_cache, index):
 
 
 def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, hkv_cache, D_cache,
-            block_table, seq_idx, pos, cos_sin, interleaved, index):
+            block_table, seq_idx, pos, cos_sin, interleaved, index, rope_pos=None):
     """The common part of the two rotated appends, on the current stream of device
     `index`: `entry` with `caches` (pointers)."""
     import torch
@@ -911,8 +926,12 @@ def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, 
     k, v, seqs, at = k_new.data_ptr(), v_new.data_ptr(), seq_idx.data_ptr(), pos.data_ptr()
     if n_tok == 0:
         k = v = seqs = at = _NOTHING
-    rc = entry(k, v, q_in, *caches, q_to, block_table.data_ptr(), seqs, at, table, n_tok, ks, vs,
-               qs, hq, hkv, D, page_size, batch, max_blocks, num_pages, max_pos, rot,
+    turn = ()
+    if rope_pos is not None:
+        _want(rope_pos, "rope_pos", i32, (n_tok,), index)
+        turn = (rope_pos.data_ptr() or _NOTHING,)
+    rc = entry(k, v, q_in, *caches, q_to, block_table.data_ptr(), seqs, at, *turn, table, n_tok,
+               ks, vs, qs, hq, hkv, D, page_size, batch, max_blocks, num_pages, max_pos, rot,
                bool(interleaved), dtype_code(k_new), torch._C._cuda_getCurrentRawStream(index))
     if rc:
         raise PAError(rc, where)
@@ -920,25 +939,27 @@ def _append(entry, where, k_new, v_new, q, q_out, caches, num_pages, page_size, 
 
 
 def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, cos_sin, q=None,
-                   q_out=None, interleaved=False, stream=None):
+                   q_out=None, interleaved=False, stream=None, rope_pos=None):
     """pa_append_kv_rope on tensors: k_new, v_new [n_tok, h_kv, D] and q
     [n_tok, h_q, D] may be views with any token stride (a fused projection's
     output); cos_sin float32 [max_pos, rot_dim] (rope_table).  Writes the caches
     [pages, h_kv, 16, D]; returns the rotated q ([n_tok, h_q, D], q_out if
-    given), or None without q."""
+    given), or None without q.  rope_pos int32 [n_tok]: positions to rotate by, where
+    they are not pos (pa_append_kv_rope_at: the tokens of a drafted tree)."""
     index = _device_index(k_new)
     if _elsewhere(index, stream):
         with _On(index, stream):
             return append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos,
-                                  cos_sin, q, q_out, interleaved)
+                                  cos_sin, q, q_out, interleaved, rope_pos=rope_pos)
     if cos_sin is None or k_cache.dim() != 4:
         raise ValueError("append_kv_rope wants cos_sin and caches [pages, h_kv, 16, D]")
     pages, hkv, P, D = shape = k_cache.shape
     _want(k_cache, "k_cache", k_new.dtype, shape, index)
     _want(v_cache, "v_cache", k_new.dtype, shape, index)
-    return _append(lib().pa_append_kv_rope, "pa_append_kv_rope", k_new, v_new, q, q_out,
+    entry = lib().pa_append_kv_rope if rope_pos is None else lib().pa_append_kv_rope_at
+    return _append(entry, "pa_append_kv_rope", k_new, v_new, q, q_out,
                    (k_cache.data_ptr(), v_cache.data_ptr()), pages, P, hkv, D, block_table,
-                   seq_idx, pos, cos_sin, interleaved, index)
+                   seq_idx, pos, cos_sin, interleaved, index, rope_pos)
 
 
 def append_kv4(k_new, v_new, kv_cache, block_table, seq_idx, pos, cos_sin=None, q=None,

@@ -56,6 +56,7 @@ struct AppendRopeLaunch {
   int n_tok, n_q_heads, n_kv_heads, head_dim, batch, max_blocks, num_pages;
   int max_pos, rot_dim;
   bool interleaved, bf16;
+  const int32_t *turn_pos = nullptr;  // positions to rotate by; null: pos
 };
 int launch_append_rope(const AppendRopeLaunch &a, cudaStream_t stream);
 

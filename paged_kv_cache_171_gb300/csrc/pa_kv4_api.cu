@@ -123,6 +123,24 @@ int pa_append_kv_rope(const void *k_new, const void *v_new, const void *q, void 
   return append(a, page_size, dtype, stream);
 }
 
+int pa_append_kv_rope_at(const void *k_new, const void *v_new, const void *q, void *k_cache,
+                         void *v_cache, void *q_out, const int32_t *block_table,
+                         const int32_t *seq_idx, const int32_t *pos, const int32_t *rope_pos,
+                         const float *cos_sin, int n_tok, int64_t k_stride, int64_t v_stride,
+                         int64_t q_stride, int n_q_heads, int n_kv_heads, int head_dim,
+                         int page_size, int batch, int max_blocks_per_seq, int num_pages,
+                         int max_pos, int rot_dim, int interleaved, pa_dtype dtype,
+                         pa_stream_t stream) {
+  if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !seq_idx || !pos ||
+      !rope_pos || !cos_sin || !q != !q_out)
+    return PA_ERR_NULL;
+  AppendRopeLaunch a = {k_new, v_new, q, q_out, k_cache, v_cache, nullptr, block_table, seq_idx,
+                        pos, cos_sin, nullptr, k_stride, v_stride, q_stride, n_tok, n_q_heads,
+                        n_kv_heads, head_dim, batch, max_blocks_per_seq, num_pages, max_pos,
+                        rot_dim, interleaved != 0, false, rope_pos};
+  return append(a, page_size, dtype, stream);
+}
+
 size_t pa_kv4_block_bytes(int head_dim) {
   return head_dim == 64 || head_dim == 128 ? kv4::block_bytes(head_dim) : 0;
 }

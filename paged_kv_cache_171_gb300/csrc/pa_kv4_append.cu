@@ -48,6 +48,7 @@ struct AppendParams {
   uint16_t *q_out, *k_cache, *v_cache;
   uint8_t *kv4;
   const int32_t *block_table, *seq_idx, *pos;
+  const int32_t *turn_pos;  // or null: pos
   const float *cos_sin;
   int *status;
   int64_t k_stride, v_stride, q_stride, total;
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_rope_kernel(const Ap
   const int r0 = static_cast<int>(unit - j * p.row_lanes);
 
   const int b = p.seq_idx[j], pos = p.pos[j];
+  const int at = p.turn_pos ? p.turn_pos[j] : pos;  // the position it is rotated by
   const bool turn = p.cos_sin != nullptr;
   const int half_chunks = p.rot_dim / 16;         // chunks of rotated first elements
   const bool mine = turn && t < half_chunks;      // this thread's chunks are rotated
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_rope_kernel(const Ap
 
   const bool reporter = t == 0 && r0 == 0;
   if (b < 0 || b >= p.batch || pos < 0 || pos >= p.max_blocks * kPageSize ||
-      (turn && pos >= p.max_pos)) {
+      (turn && (at < 0 || at >= p.max_pos))) {
     if (reporter) record_error(p.status, PA_ERR_BAD_INDEX);
     return;
   }
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_rope_kernel(const Ap
   float cs[8], sn[8];
   if (mine) {
     const float4 *row = reinterpret_cast<const float4 *>(
-        p.cos_sin + static_cast<size_t>(pos) * p.rot_dim);
+        p.cos_sin + static_cast<size_t>(at) * p.rot_dim);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float4 c = row[2 * t + k], s = row[p.rot_dim / 8 + 2 * t + k];
@@ -251,6 +253,7 @@ int launch_append_t(const AppendRopeLaunch &a, cudaStream_t stream) {
   p.block_table = a.block_table;
   p.seq_idx = a.seq_idx;
   p.pos = a.pos;
+  p.turn_pos = a.turn_pos;
   p.cos_sin = a.cos_sin;
   p.status = a.status;
   p.k_stride = a.k_stride;
