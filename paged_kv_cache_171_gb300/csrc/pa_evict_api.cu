@@ -22,7 +22,10 @@ int check_weighted(int n_q_heads, int n_kv_heads, int head_dim, int page_size, i
                    int max_blocks, int num_pages, int dtype) {
   const int rc = check_lists(n_q_heads, n_kv_heads, head_dim, page_size, batch, max_blocks,
                              num_pages, dtype);
-  return rc ? rc : n_q_heads / n_kv_heads > kMaxGroup ? PA_ERR_HEADS : PA_OK;
+  if (rc) return rc;
+  if (n_q_heads / n_kv_heads > kMaxGroup) return PA_ERR_HEADS;
+  // CTAs of the second kernel, and items, in 32 bits
+  return static_cast<int64_t>(batch) * n_q_heads >= (int64_t(1) << 30) ? PA_ERR_SHAPE : PA_OK;
 }
 
 // A chunk's rows a kv head and its CTAs in 32 bits.

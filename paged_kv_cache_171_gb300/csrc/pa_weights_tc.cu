@@ -713,12 +713,13 @@ __global__ void __launch_bounds__(kRows) stats_kernel(const WeightsParams p) {
 // Ranges that `ctas` units of `tiles` key tiles each are cut into: the number whose waves
 // of CTAs take least, a CTA's start counting as three tiles.
 int ranges_of(int64_t ctas, int tiles, int sms) {
+  if (ctas >= 8 * sms) return 1;
   int best = 1;
-  double least = 1e30;
+  int64_t least = INT64_MAX;
   for (int r = 1; r <= 64 && r <= tiles; ++r) {
-    const double waves = static_cast<double>((ctas * r + sms - 1) / sms);
-    const double cost = waves * ((tiles + r - 1) / r + 3);
-    if (cost < 0.97 * least) {
+    const int waves = (static_cast<int>(ctas) * r + sms - 1) / sms;
+    const int64_t cost = static_cast<int64_t>(waves) * ((tiles + r - 1) / r + 3);
+    if (cost < least - least / 32) {  // more ranges only for more than 3%
       least = cost;
       best = r;
     }
