@@ -20,7 +20,9 @@
 // chunk c is stored.  Strips are independent of each other: no CTA waits for another,
 // however few lists there are.
 //
-// Bound: memory, 8 D bytes a kept token and kv head (K and V read and written).
+// Bound: memory, 8 D bytes a kept token and kv head (K and V read and written).  32 sequences
+// of 2000 to 4096 tokens to 2048: 109 us, of which 17 to 19 select and 89 move 0.5 GB.  Few
+// long lists: the chain of passes and barriers (1 x 32768 to 4096, 8 lists: 36 us, 21 select).
 #include "pa_device.cuh"
 #include "pa_evict.h"
 
@@ -435,7 +437,7 @@ int launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   const int64_t most = static_cast<int64_t>(a.max_blocks) * kPageSize;
   const int64_t keys = most - a.sink - a.recent > 0 ? most - a.sink - a.recent : 0;
   // Few lists of many tokens: a cluster each, of 2048 keys or more a CTA (8 lists of 32768:
-  // XXX us with 1 CTA, XXX with 8).
+  // 68 us with 1 CTA, 21 with 8; the call with the move 57 and 36).
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   int ranks = 1;
   while (ranks < kMaxRanks && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks) ranks *= 2;

@@ -84,6 +84,13 @@
 // A drafted key that a row does not see has P = 0, but 0 times a V that is not finite is NaN
 // in the MMA: the V load warp replaces such values by 0 in the tiles with drafted keys and
 // raises a flag, with which the rows that do see them add them at the end.
+// A tree's weights take one 16-bit term throughout (split rows: two, which cost nothing there).
+// Rounding changes each weight by half a step at most, so a dimension of the output by
+// sum_t w_t |v_t| times 2^-9 (bf16) or 2^-12 (fp16) at most, while the output itself is rounded
+// to half a step of the same type: the result is within about two roundings of the exact one.
+// The remainder's P V MMAs and the vote cost more than that is worth (4 x 64 drafted tokens
+// of 64 heads over 32k: 255 us with them, 205 without).  B's softmax waits for the first half
+// of A's P alone, not for both (285 -> 255 us; no wait at all: 298, a quarter: as the half).
 #pragma once
 
 #include <type_traits>
@@ -402,7 +409,7 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
   const bool cleared = last_first < kKeys;  // the last V tile waits for the clearing
 
   // Trees: issued by an elected lane, so that the operands stay in uniform registers, with
-  // 32-bit descriptors (a tile of 64 drafted tokens over 32k: 346 -> XXX us).
+  // 32-bit descriptors (a tile of 64 drafted tokens over 32k: 346 -> 328 us).
   const bool issuer = TREE ? tc::elect_one() : lane == 0;
   const uint32_t lq = tc::desc_low(sb + L::kQ + (IL ? 0 : x * L::kQBytes));
   const uint32_t lk = tc::desc_low(sb + (IL ? L::kK0Il : L::kK0));
@@ -1038,7 +1045,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if constexpr (TREE) {
     // The softmax warpgroups take registers that the other warps do not use: of the 384 x 168
-    // the block was launched with, 128 x 72 + 256 x 216 = 64512.
+    // the block was launched with, 128 x 72 + 256 x 216 = 64512.  A row's 128 scores and its
+    // P then stay in registers (spilt before: 328 -> 285 us).
     static_assert(128 * 72 + 256 * 216 <= kThreads * 168, "the split draws on the launch's");
     if (warp < kSoftmaxWarp0) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");

@@ -25,6 +25,10 @@
 // An item cut between warps leaves a partial state a warp; states are numbered item +
 // warp, which grows along the list, so that the second kernel finds an item's in order
 // and results do not depend on timing.
+//
+// Bound: memory.  64 sequences of 128 to 8192 tokens, 32/8 heads of 128: 201 us, of which
+// 179 are the pass over K and V (6.1 TB/s with the scores it writes), 9 the fold and 13 the
+// weights.  4 x 32768, 64/8 heads: 110 us (92, 6 and 11).
 #include "pa_device.cuh"
 #include "pa_evict.h"
 #include "pa_tcgen05.cuh"
@@ -532,8 +536,8 @@ __global__ void __launch_bounds__(kFoldThreads) weighted_add_kernel(const Weight
   add_tokens<NR>(p, bg, blockIdx.x - bg * p.segs, p.rows + static_cast<size_t>(bg) * p.group);
 }
 
-// Both in one, a CTA a list: tables of one segment (a launch less: the host's call bounds
-// those; 1 x 512 tokens of 16 heads XXX us).
+// Both in one, a CTA a list: tables of two rounds at most.  A launch less: the host's call
+// bounds those (1 x 512 tokens of 16 heads, calls on end: 15.0 us apart, 12.5 in one).
 template <int D, int NR>
 __global__ void __launch_bounds__(kFoldThreads) weighted_both_kernel(const WeightedParams p) {
   griddep_release();
