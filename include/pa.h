@@ -701,7 +701,7 @@ size_t pa_prefill_weights_workspace_size(int batch, int n_new, int n_q_heads, in
  *   dst_table  device int32 [batch][dst_blocks_per_seq]: block_table itself (in place), or
  *              pages that hold no token of this call's sequences (where the old pages are
  *              shared with others)
- *   new_lens   device int32 [batch], not ctx_lens (PA_ERR_SHAPE)
+ *   new_lens   device int32 [batch], apart from ctx_lens and the tables (PA_ERR_SHAPE)
  *   workspace  as in pa_decode_weighted, pa_evict_kv_workspace_size(...) bytes
  * Places behind the kept rows are left as they were.  sink_tokens, recent_tokens >= 0 and
  * their sum at most budget (PA_ERR_SHAPE).  A row whose page, old or new, is bad is not
@@ -723,7 +723,7 @@ size_t pa_evict_kv_workspace_size(int batch, int n_kv_heads, int head_dim, int p
  * tokens.  With ctx_lens 0: a sequence cut to the listed tokens.
  *   keep     device int32 [batch][max_keep], ascending in each row, from 0
  *   n_keep   device int32 [batch], 0 .. max_keep
- *   new_lens device int32 [batch], not ctx_lens (PA_ERR_SHAPE)
+ *   new_lens device int32 [batch], apart from the call's other arrays (PA_ERR_SHAPE)
  *   weights  or NULL
  * A sequence whose list is not ascending or leaves the table, or whose n_keep is out of
  * range, keeps nothing (new_lens[b] = ctx_lens[b]) and PA_ERR_BAD_INDEX is recorded; a row

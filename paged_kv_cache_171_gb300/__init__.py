@@ -1237,8 +1237,8 @@ def evict_kv(k_cache, v_cache, weights, block_table, ctx_lens, budget, sink=0, r
     """pa_evict_kv on tensors: every sequence of more than `budget` tokens keeps, for each kv
     head, its first `sink`, its last `recent` and the heaviest others by weights
     [pages, h_kv, 16]; K, V and weights move to positions 0 .. in place, or to the pages of
-    dst_table int32 [B, blocks].  Returns the new lengths, int32 [B] (new_lens if given; not
-    ctx_lens itself).  workspace: any tensor of pa_evict_kv_workspace_size(...) bytes, as in
+    dst_table int32 [B, blocks].  Returns the new lengths, int32 [B] (new_lens if given;
+    apart from the call's other tensors).  workspace: any tensor of pa_evict_kv_workspace_size(...) bytes, as in
     decode_weighted."""
     import torch
     index = _device_index(k_cache)
@@ -1277,7 +1277,7 @@ def compact_kv(k_cache, v_cache, block_table, ctx_lens, keep, n_keep, weights=No
     given) weights move up to positions ctx_lens[b] + j, in place: the accepted branch of a
     tree of drafted tokens, or (ctx_lens 0) a sequence cut to the listed tokens.  keep int32
     [B, max_keep], ascending in each row; n_keep int32 [B].  Returns the new lengths, int32
-    [B] (new_lens if given; not ctx_lens itself)."""
+    [B] (new_lens if given; apart from the call's other tensors)."""
     import torch
     index = _device_index(k_cache)
     if _elsewhere(index, stream):

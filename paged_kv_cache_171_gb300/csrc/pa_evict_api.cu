@@ -16,6 +16,12 @@ int check_lists(int n_q_heads, int n_kv_heads, int head_dim, int page_size, int 
   return static_cast<int64_t>(batch) * n_kv_heads >= (int64_t(1) << 24) ? PA_ERR_SHAPE : PA_OK;
 }
 
+// Whether two device arrays of n and m 32-bit words have one in common.
+bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return n > 0 && m > 0 && x < y + 4 * m && y < x + 4 * n;
+}
+
 constexpr int kMaxGroup = 1024;  // rows whose (m, 1 / l) shared memory holds
 
 int check_weighted(int n_q_heads, int n_kv_heads, int head_dim, int page_size, int batch,
@@ -120,8 +126,12 @@ int pa_evict_kv(void *k_cache, void *v_cache, float *weights, const int32_t *blo
   if (dst_blocks_per_seq <= 0 ||
       static_cast<int64_t>(dst_blocks_per_seq) * page_size > (int64_t(1) << 30))
     return PA_ERR_SHAPE;
-  if (ctx_lens == new_lens) return PA_ERR_SHAPE;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights)) return PA_ERR_ALIGN;
+  // read by some CTAs while another writes the new lengths
+  if (overlap(new_lens, batch, ctx_lens, batch) ||
+      overlap(new_lens, batch, block_table, int64_t(batch) * max_blocks_per_seq) ||
+      overlap(new_lens, batch, dst_table, int64_t(batch) * dst_blocks_per_seq))
+    return PA_ERR_SHAPE;
   if (!workspace ||
       workspace_bytes < evict_workspace_bytes(batch, n_kv_heads, max_blocks_per_seq, budget))
     return PA_ERR_WORKSPACE;
@@ -159,8 +169,11 @@ int pa_compact_kv(void *k_cache, void *v_cache, float *weights, const int32_t *b
                        num_pages, dtype);
   if (rc) return rc;
   if (max_keep < 0 || max_keep > max_blocks_per_seq * page_size) return PA_ERR_SHAPE;
-  if (ctx_lens == new_lens) return PA_ERR_SHAPE;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights)) return PA_ERR_ALIGN;
+  if (overlap(new_lens, batch, ctx_lens, batch) || overlap(new_lens, batch, n_keep, batch) ||
+      overlap(new_lens, batch, keep, int64_t(batch) * max_keep) ||
+      overlap(new_lens, batch, block_table, int64_t(batch) * max_blocks_per_seq))
+    return PA_ERR_SHAPE;
   EvictLaunch a = {};
   if ((rc = current_status_ptr(&a.status))) return rc;
   a.k_cache = k_cache;

@@ -58,6 +58,7 @@ struct WeightedParams {
   int *status;
   float qscale;   // scale * log2 e
   int n_q_heads, n_kv_heads, group, n_sub, tile_rows, batch, max_blocks, num_pages, fresh;
+  int workers;           // warps of the first kernel
   int parts;             // CTAs a list of the second kernel
   int seg_tokens, segs;  // tokens a CTA of the third looks after, CTAs a list
 };
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ln = lane >> 2, lc = lane & 3;
-  const int n_workers = gridDim.x * kWarps, worker = warp * gridDim.x + blockIdx.x;
+  const int n_workers = p.workers, worker = warp * gridDim.x + blockIdx.x;
   const uint32_t ring = smem_u32(smem) + warp * L::kStages * L::kStage;
   const uint32_t bars = smem_u32(smem) + L::kBars + warp * L::kStages * 8;
   if (lane == 0) {
@@ -386,14 +387,20 @@ template <int D>
 __device__ __forceinline__ void fold_elements(const WeightedParams &p, int bg, int e0, int e1,
                                               float2 *rows) {
   constexpr int kOver = 8, kAhead = 4;
-  const int2 first_span = p.span[bg * p.n_sub];
+  // The warps that hold an item.  Where one gave up, the place was not written: whatever it
+  // holds stays within the states.
+  auto span_of = [&](int item) {
+    const int2 s = p.span[item];
+    return make_int2(max(s.x, 0), min(s.y, p.workers - 1));
+  };
+  const int2 first_span = span_of(bg * p.n_sub);
   for (int eb = e0; eb < e1; eb += kFoldThreads / kOver) {
     const int e = eb + threadIdx.x / kOver;
     const bool real = e < e1;
     const int r = real ? e / (D / 4) : e0 / (D / 4), d = 4 * (e % (D / 4));
     const int sub = p.n_sub == 1 ? 0 : r / p.tile_rows, rr = r - sub * p.tile_rows;
     const int item = bg * p.n_sub + sub;
-    const int2 span = p.n_sub == 1 ? first_span : p.span[item];
+    const int2 span = p.n_sub == 1 ? first_span : span_of(item);
     const float *states = p.states + (static_cast<size_t>(item) * kTile + rr) * (D + 4);
     float m = kNoKey, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -611,6 +618,7 @@ int launch_t(const WeightedLaunch &a, cudaStream_t stream) {
                          kFoldTokens;
   const int64_t most = 128 * sms / lists > 1 ? 128 * sms / lists : 1;  // CTAs a list
   const bool both = rounds <= 2;
+  p.workers = sms * kWarps;
   p.seg_tokens = static_cast<int>(both ? rounds : (rounds + most - 1) / most) * kFoldTokens;
   p.segs = (a.max_blocks * kPageSize + p.seg_tokens - 1) / p.seg_tokens;
   p.parts = (p.group * (D / 4) + kFoldElements - 1) / kFoldElements;

@@ -82,6 +82,19 @@ def test_compact_refuses(L):
            (2, P + 4, -8)])
 
 
+def test_new_lengths_lie_apart_from_what_the_calls_read(L):
+    A = [0x1000 * (i + 1) for i in range(8)]
+    evict = [A[0], A[1], A[2], A[3], A[4], A[5], 0, 64, 4, 16, 8, 128, 16, 2, 8, 8, 16, 0, A[6],
+             1 << 20, None]
+    for near in (A[4], A[4] + 4, A[4] - 4, A[3] + 60, A[5] + 60):
+        evict[6] = near
+        assert L.pa_evict_kv(*evict) == -5, near
+    compact = [A[0], A[1], None, A[3], A[4], A[5], A[6], 10, 0, 8, 128, 16, 2, 8, 16, 0, None]
+    for near in (A[4] + 4, A[4] - 4, A[5] + 76, A[6], A[6] + 4, A[6] - 4, A[3] + 60):
+        compact[8] = near
+        assert L.pa_compact_kv(*compact) == -5, near
+
+
 def test_tree_refuses(L):
     need = L.pa_prefill_tree_workspace_size(1, 8, 32, 8, 128, 16, 4096)
     assert need > 0
