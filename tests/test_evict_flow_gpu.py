@@ -69,6 +69,7 @@ def test_a_drafted_tree_is_verified_and_a_branch_accepted(dt, inter):
             assert torch.equal(qs[-1], q[b, i])  # rotated by its depth
             want = pa.decode(qs[-1:], *caches, bt[b:b + 1], _i32([t + len(path)]), 0.125)
             # both are within a few half steps of the values: the 16-bit weights' and result's
+            # four roundings of values up to 4: the rotated q and k, the weights, the output
             tol = 4 * torch.finfo(dt).eps / 2 * 4.0
             assert (out[b, i].float() - want[0]).abs().max() < tol
 

@@ -137,6 +137,8 @@ def test_a_chain_is_the_causal_chunk():
     got = _check(case, chain, 0.1)
     q, k, v, bt, ctx = (x.cuda() for x in case)
     other = pa.prefill(q, k.nan_to_num(), v.nan_to_num(), bt, ctx, 0.1).cpu()
+    # the chunk's own bound, and a tree's two roundings (of its weights and of its output) of
+    # values up to 4, 2 x 2^-8 x 4, taken a little short
     assert (got.float() - other).abs().max() < 2e-3 + 3e-2
 
 
