@@ -21,19 +21,21 @@
 //
 // Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-19 are four consumer warpgroups, warps
 // 2 and 3 add the columns pass's partial sums and update the pool.  Work reaches the consumers
-// in chunks of 128 x 128 scores, of which a warpgroup takes no more than fits its registers
-// at once, so that a tensor memory buffer is free again right after it is complete, and there
-// are two for each: row tile x key tile chunks go to two pairs of warpgroups in turn, half the
-// columns each (rows pass, FEW); or all four take 32 rows of both held key tiles (MANY: a load
-// of lse then serves two keys).
+// in chunks of 128 x 128 scores, which they read 64 columns at a time, so that a chunk's buffer
+// in tensor memory is free again before its last scores have been worked off.  FEW: chunks go
+// to the four warpgroups in turn, whatever their row tile (half a chunk each, in two pairs of
+// warpgroups, pays each hand-off twice: 2 x 33 tokens of 64/8 heads over 32k 62 us, whole ones
+// 42).  Rows pass: a warpgroup a row tile, or, of one or two row tiles, four or two in turn
+// (128 and 256 rows over 32k: 67 -> 61 and 78 -> 71 us for both passes).  MANY: all four take
+// 32 rows of both held key tiles (a load of lse then serves two keys).
 // Rows that only fill a tile up cost no exponentials.  Every hand-off is an mbarrier; every
 // wait is bounded and gives up early once another role has raised the CTA's abort flag.
 //
 // Bound: the exponentials, two of them a pair (MUFU), and the MMAs, about as long, for chunks
-// of many rows: 4 x 512 tokens of 32/8 heads over 8192, 244 us (rows pass 120, columns pass
-// 131 less its overlap), the exponential pipe busy 52 to 61% of the cycles and the tensor pipe
-// 51 to 60%.  For few rows the hand-off of a tile from the loads to the MMA to the warpgroups:
-// 2 x 33 tokens of 64/8 heads over 32k, 101 us (45 and 62) for 134 MB of K read twice.
+// of many rows: 4 x 512 tokens of 32/8 heads over 8192, 242 us (rows pass 119, columns pass
+// 129), the exponential pipe busy 52 to 61% of the cycles and the tensor pipe 51 to 60%.  For
+// few rows the same two with every hand-off in sight: 2 x 33 tokens of 64/8 heads over 32k,
+// 87 us (44 and 42) for 134 MB of K read twice.
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -49,6 +51,7 @@ constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its f
 constexpr int kRows = 128;                  // rows or keys of a tile
 constexpr int kThreads = 640;
 constexpr int kGroups = 4;                  // consumer warpgroups
+constexpr int kNumBars = 36;
 enum Pass { kRowsPass, kFew, kMany };
 
 struct WeightsParams {
@@ -76,9 +79,12 @@ struct WeightsSmem {
   static constexpr int kStats = (kHeldTiles + kStages) * kTile;  // [row tile or stage][128]
   static constexpr int kPart = kStats + 4 * kRows * 4;        // [2][4 or 8][keys] sums
   static constexpr int kPartKeys = PASS == kMany ? 2 * kRows : kRows;
-  static constexpr int kParts = PASS == kMany ? kGroups : 8;  // sums a key
-  static constexpr int kBars = kPart + 2 * kParts * kPartKeys * 4;
-  static constexpr int kSlot = kBars + 32 * 8;                // TMEM address, abort flag
+  static constexpr int kParts = 4;  // sums a key: of each warpgroup (MANY) or row tile (FEW)
+  // Buffers of sums.  FEW: four, so that a warpgroup that writes to one at key tile j, and
+  // waits for it there, has done so at j - 4 too, and so never misses a phase of its barrier.
+  static constexpr int kPartBufs = PASS == kMany ? 2 : 4;
+  static constexpr int kBars = kPart + kPartBufs * kParts * kPartKeys * 4;
+  static constexpr int kSlot = kBars + kNumBars * 8;          // TMEM address, abort flag
   static constexpr int kAlloc = kSlot + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory of an SM");
 };
@@ -90,11 +96,9 @@ enum {
   kBarHeldFree = 9,   // MANY: .. have been read by the pair's last MMA (commit)
   kBarS = 10,         // S buffer 0 .. 3 (MANY: pair 0, 1) complete (commit)
   kBarSFree = 18,     // .. read (one arrival a warp that reads it)
-  kBarT = 26,         // FEW: the rows' statistics are there (one arrival an aux warp)
-  kBarPart = 27,      // columns: the sums of buffer 0 / 1 are written
-  kBarPartFree = 29,  // .. have been read (2 warps)
-  kBarDrain = 31,
-  kNumBars = 32
+  kBarPart = 26,      // columns: the sums of buffer 0 .. are written
+  kBarPartFree = 30,  // .. have been read (2 warps)
+  kBarDrain = 34,
 };
 
 // What a CTA does at a time.
@@ -159,16 +163,22 @@ __device__ __forceinline__ int page_of(const WeightsParams &p, const Job &w, int
   }
   return id;
 }
-// One K tile (8 pages of one kv head) into shared memory.  The whole warp.
+// One K tile (8 pages of one kv head) into shared memory.  The whole warp; an elected lane
+// issues the copies (eight lanes, two each: a pass 1 to 2% longer).
 template <int D>
 __device__ __forceinline__ void load_keys(const CUtensorMap *map, const WeightsParams &p,
                                           const Job &w, int id, uint32_t dst, uint32_t bar,
                                           int lane) {
-  if (lane < 8) {
+  const int row = (id * p.n_kv_heads + w.g) * kPageSize;
+  int at[kRows / kPageSize];
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x)
-      tma_load_2d(dst + x * kRows * 128 + lane * 2048, map, 64 * x,
-                  (id * p.n_kv_heads + w.g) * kPageSize, bar);
+  for (int k = 0; k < kRows / kPageSize; ++k) at[k] = __shfl_sync(0xffffffffu, row, k);
+  if (tc::elect_one()) {
+#pragma unroll
+    for (int k = 0; k < kRows / kPageSize; ++k)
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_2d(dst + x * kRows * 128 + k * 2048, map, 64 * x, at[k], bar);
   }
   __syncwarp();
 }
@@ -333,9 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       int n = 1;
       if (i >= kBarFree && i < kBarHeld) n = PASS == kMany ? 1 + 4 * kGroups : 1;
-      if (i >= kBarSFree && i < kBarT) n = PASS == kMany ? 4 * kGroups : PASS == kFew ? 8 : 4;
-      if (i == kBarT || (i >= kBarPartFree && i < kBarDrain)) n = 2;
-      if (i == kBarPart || i == kBarPart + 1) n = PASS == kMany ? 4 * kGroups : 8 * w.n_held;
+      if (i >= kBarSFree && i < kBarPart) n = PASS == kMany ? 4 * kGroups : 4;
+      if (i >= kBarPartFree && i < kBarDrain) n = 2;
+      if (i >= kBarPart && i < kBarPartFree) n = PASS == kMany ? 4 * kGroups : 4 * w.n_held;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -363,6 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
   const uint32_t q_bytes = (D / 64) * p.hb * p.nq * 128;
   const uint32_t stats_bytes = kRows * sizeof(float);
+  // Row tiles that the rows pass's warpgroups take in turn: one or two, or a warpgroup each.
+  const int turns = w.n_held <= 2 ? w.n_held : kGroups;
   // the jobs of a CTA: one, or (MANY) every gridDim.x-th item
   auto next_job = [&](int &at) {
     for (at += gridDim.x; PASS == kMany && at < p.items; at += gridDim.x) {
@@ -451,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             if (x >= w.n_held) break;
-            const int buf = PASS == kRowsPass ? x : n & 3;
-            const int use = PASS == kRowsPass ? c : n >> 2;
+            const int buf = PASS == kRowsPass && turns == kGroups ? x : n & 3;
+            const int use = PASS == kRowsPass && turns == kGroups ? c : n >> 2;
             if (use > 0 && !(ok = warp_wait(bar(kBarSFree + buf), (use - 1) & 1, abort_flag)))
               break;
             tc::fence_after_sync();
@@ -490,17 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 4) {
     if (PASS != kRowsPass) {
-      // ---- (FEW: the rows' statistics, then) the consumers' sums into the pool
+      // ---- the consumers' sums into the pool
       bool ok = true;
-      if (PASS == kFew) {
-        float *st = reinterpret_cast<float *>(smem + L::kStats);
-        for (int e = tid - 64; e < w.n_held * kRows; e += 64) {
-          const int rt = e / kRows, r = e % kRows;
-          st[e] = folded(p, w.bg, rt, r);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarT));
-      }
       constexpr int U = L::kPartKeys / 64;  // keys a thread
       struct Place {
         float *dst;
@@ -543,19 +546,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               page[u] = page_at(key + kRows);
             }
           }
-          if (!(ok = warp_wait(bar(kBarPart + (n & 1)), (n >> 1) & 1, abort_flag))) break;
+          const int buf = n % L::kPartBufs;
+          if (!(ok = warp_wait(bar(kBarPart + buf), (n / L::kPartBufs) & 1, abort_flag))) break;
           const float *part = reinterpret_cast<const float *>(smem + L::kPart) +
-                              (n & 1) * L::kParts * L::kPartKeys + tid - 64;
+                              buf * L::kParts * L::kPartKeys + tid - 64;
           float sum[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             sum[u] = 0.f;
 #pragma unroll
             for (int y = 0; y < L::kParts; ++y)
-              if (PASS == kMany || y < 2 * w.n_held) sum[u] += part[y * L::kPartKeys + 64 * u];
+              if (PASS == kMany || y < w.n_held) sum[u] += part[y * L::kPartKeys + 64 * u];
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarPartFree + (n & 1)));
+          if (lane == 0) mbar_arrive(bar(kBarPartFree + buf));
 #pragma unroll
           for (int u = 0; u < U; ++u)
             if (here[u].dst) *here[u].dst = here[u].old + sum[u];
@@ -575,21 +579,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
     };
-    const int pair = y & 1, half = y >> 1;  // the chunks it takes, and which columns
     if constexpr (PASS == kRowsPass) {
-      const int rt = w.held0 + y, q0 = rt / p.n_hsub * p.nq;
+      // One or two row tiles: several warpgroups take the key tiles of one in turn.
+      const int x = y % turns, step = kGroups / turns;
+      const int rt = w.held0 + x, q0 = rt / p.n_hsub * p.nq;
       const int lim = w.ctx + min(q0 + r / p.hb, p.n_new - 1);  // the last key row r sees
       const int lim_all = w.ctx + q0;                           // .. that every row does
       const bool idle = 32 * (warp & 3) >= rows_of(p, rt);      // none of the warp's rows is one
       RowState st = {kNoKey, make_float2(0.f, 0.f)};
-      if (y < w.n_held) {
+      if (x < w.n_held) {
         const uint32_t at = tmem + kRows * y + lanes;
+        uint32_t uses = 0;  // of the buffer
         // 64 keys at a time, in one copy of the code: with four (unrolled over tiles) the
         // other warps' instructions left the cache, and each of their waits took 450 cycles
 #pragma unroll 1
-        for (int i = 0; i < 2 * w.n; ++i) {
+        for (int i = y / turns * 2; i < 2 * w.n;) {
           if ((i & 1) == 0) {
-            if (!(ok = warp_wait(bar(kBarS + y), (i >> 1) & 1, abort_flag))) break;
+            if (!(ok = warp_wait(bar(kBarS + y), uses & 1, abort_flag))) break;
+            ++uses;
             tc::fence_after_sync();
           }
           if (!idle) {
@@ -602,53 +609,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (i & 1) {
             release(y);
           }
+          i += (i & 1) ? 2 * step - 1 : 1;
         }
-        if (ok) {
-          const float l = st.l.x + st.l.y;
-          const size_t tile = static_cast<size_t>(w.bg) * p.n_rt + rt;
-          p.states[(tile * p.n_ranges + w.range) * kRows + r] = make_float2(st.m, l);
-          if (p.n_ranges == 1)
-            p.stats[tile * kRows + r] = query_of(p, rt, r) < 0 ? -INFINITY : stat_of(st.m, l);
+      }
+      float m = st.m, l = st.l.x + st.l.y;
+      if (step > 1) {
+        // Their states folded, through the row tiles' place: every chunk is complete, so those
+        // have been read.
+        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+        float2 *all = reinterpret_cast<float2 *>(smem);
+        all[y * kRows + r] = make_float2(m, l);
+        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+        for (int k = y + turns; k < kGroups; k += turns) {
+          const float2 v = all[k * kRows + r];
+          const float mn = fmaxf(m, v.x);
+          l = l * ex2(m - mn) + v.y * ex2(v.x - mn);
+          m = mn;
         }
+      }
+      if (ok && y < w.n_held) {
+        const size_t tile = static_cast<size_t>(w.bg) * p.n_rt + rt;
+        p.states[(tile * p.n_ranges + w.range) * kRows + r] = make_float2(m, l);
+        if (p.n_ranges == 1)
+          p.stats[tile * kRows + r] = query_of(p, rt, r) < 0 ? -INFINITY : stat_of(m, l);
       }
     } else if constexpr (PASS == kFew) {
       float *part = reinterpret_cast<float *>(smem + L::kPart) + r;
-      ok = warp_wait(bar(kBarT), 0, abort_flag);
+      {  // the rows' statistics, a row a thread
+        float *stats = reinterpret_cast<float *>(smem + L::kStats);
+        const int e = tid - (kThreads - kGroups * kRows);
+        if (e < w.n_held * kRows) stats[e] = folded(p, w.bg, e / kRows, e % kRows);
+        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+      }
       const int chunks = w.n * w.n_held;
-      int j = pair / w.n_held, x = pair - j * w.n_held;  // of chunk n
-      const int last_rows = rows_of(p, w.n_held - 1);    // of the last query tile's
-      for (int n = pair; n < chunks && ok; n += 2) {
-        const int buf = n & 3;
-        if (!(ok = warp_wait(bar(kBarS + buf), (n >> 2) & 1, abort_flag))) break;
+      int j = y / w.n_held, x = y - j * w.n_held;      // of chunk n
+      const int last_rows = rows_of(p, w.n_held - 1);  // of the last query tile's
+      for (int n = y; n < chunks && ok; n += kGroups) {
+        if (!(ok = warp_wait(bar(kBarS + y), (n >> 2) & 1, abort_flag))) break;
         tc::fence_after_sync();
         const int key0 = (w.s0 + j) * kRows;
-        const int c0 = 64 * half;
-        const int rows = (x >= w.n_held - p.n_hsub ? last_rows : p.hb * p.nq) - c0;  // of this half
-        uint32_t s[2][1][32];
-        const uint32_t at = tmem + kRows * buf + lanes + c0;
-        if (rows > 0) tc::ld32(at, s[0][0]);
-        if (rows > 32) tc::ld32(at + 32, s[1][0]);
-        tc::wait_ld();
-        release(buf);
+        const int rows = x >= w.n_held - p.n_hsub ? last_rows : p.hb * p.nq;
         const int q0 = (p.n_hsub == 1 ? x : x / p.n_hsub) * p.nq;  // the tile's first query
         const bool all = key0 + kRows - 1 <= w.ctx + q0;  // every row sees every key
         float2 sum[1] = {make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int c0 = 0; c0 < rows; c0 += 64) {
+          uint32_t s[2][1][32];
+          const uint32_t at = tmem + kRows * y + lanes + c0;
+          tc::ld32(at, s[0][0]);
+          if (rows > c0 + 32) tc::ld32(at + 32, s[1][0]);
+          tc::wait_ld();
+          if (c0 + 64 >= rows) release(y);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (32 * h >= rows) break;
-          const uint32_t lse = sb + L::kStats + x * stats_bytes + (c0 + 32 * h) * 4;
-          const int from[1] = {(key0 + r - w.ctx - q0) * p.hb - c0 - 32 * h};
-          if (all)
-            add_weights<1, false>(s[h], lse, from, qs, sum);
-          else
-            add_weights<1, true>(s[h], lse, from, qs, sum);
+          for (int h = 0; h < 2; ++h) {
+            if (c0 + 32 * h >= rows) break;
+            const uint32_t lse = sb + L::kStats + x * stats_bytes + (c0 + 32 * h) * 4;
+            const int from[1] = {(key0 + r - w.ctx - q0) * p.hb - c0 - 32 * h};
+            if (all)
+              add_weights<1, false>(s[h], lse, from, qs, sum);
+            else
+              add_weights<1, true>(s[h], lse, from, qs, sum);
+          }
         }
-        if (j >= 2 && !(ok = warp_wait(bar(kBarPartFree + (j & 1)), ((j >> 1) - 1) & 1, abort_flag)))
+        if (j >= 4 && !(ok = warp_wait(bar(kBarPartFree + (j & 3)), ((j >> 2) - 1) & 1, abort_flag)))
           break;
-        part[((j & 1) * L::kParts + 2 * x + half) * kRows] = sum[0].x + sum[0].y;
+        part[((j & 3) * L::kParts + x) * kRows] = sum[0].x + sum[0].y;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPart + (j & 1)));
-        for (x += 2; x >= w.n_held; x -= w.n_held) ++j;
+        if (lane == 0) mbar_arrive(bar(kBarPart + (j & 3)));
+        for (x += kGroups; x >= w.n_held; x -= w.n_held) ++j;
       }
     } else {
       float *part = reinterpret_cast<float *>(smem + L::kPart) + y * 2 * kRows + r;

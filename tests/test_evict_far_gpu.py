@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_171_gb300 as pa
+from tests import evict_reference as ref
 from tests.test_evict_flow_gpu import WRITTEN, _built, _loop, _results  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +60,23 @@ def test_one_query_for_a_whole_batch_is_refused():
     with pytest.raises(pa.PAError):
         pa.prefill_weights(s["qs"][:1].expand(3, -1, -1, -1), s["k"], s["w"], s["bt"], s["ctx"], 0.1)
     assert torch.equal(s["w"], w)
+
+
+@pytest.mark.parametrize("n", [1, 4, 16, 24, 32, 40, 64])
+def test_few_queries_over_many_key_tiles(n):
+    """One to four row tiles (8 n rows) beside which every CTA has some twenty key tiles, so that
+    each of its buffers goes round several times; twice, with the same bits."""
+    lens = [20000, 18901]
+    dt = torch.bfloat16
+    k, _, w, bt, _ = ref.pool([t + n for t in lens], 8, 64, dt, n)
+    ctx = torch.tensor(lens, dtype=torch.int32)
+    q = torch.randn((2, n, 64, 64), generator=torch.Generator().manual_seed(n + 1)).to(dt)
+    got = []
+    for _ in range(2):
+        gw = w.cuda()
+        pa.prefill_weights(q.cuda(), k.cuda(), gw, bt.cuda(), ctx.cuda(), 0.2)
+        got.append(gw.cpu())
+    assert pa.pa_last_device_error() == 0
+    new, bound = ref.chunk_weights(q, k, w, bt, ctx, 0.2, n)
+    assert ((got[0].double() - new).abs() <= bound).all()
+    assert torch.equal(*got)
