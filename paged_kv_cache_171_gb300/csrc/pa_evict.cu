@@ -8,8 +8,9 @@
 // select_kernel: a cluster of up to 8 CTAs a (sequence, kv head), each with a part of the
 // candidates in its shared memory as 32-bit keys of the weights' order.  A radix select over
 // digits of 11, 11 and 10 bits finds the least key kept and how many of its ties are: a CTA's
-// histogram each, every CTA sums them through distributed shared memory and picks the same
-// bin.  Then each warp numbers the kept ones of a span of tokens by ballots and writes their
+// histogram each, and its sums over 32 bins; one warp of every CTA adds the sums of all CTAs up
+// through distributed shared memory, then the 32 bins of the one that matters, and picks the
+// same bin as the others (with all 2048 bins read by every CTA 1 x 32768 to 4096 took 36 us).  Then each warp numbers the kept ones of a span of tokens by ballots and writes their
 // positions.
 //
 // move_kernel: row src[j] to position j, where src is ascending, so src[j] >= j: the list
@@ -33,7 +34,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 49152;  // keys of a row that shared memory holds
 constexpr int kSelSmem = kSelKeys * 4;
-constexpr int kBins = 2048, kMaxRanks = 8;
+constexpr int kBins = 2048, kCoarse = kBins / 32, kMaxRanks = 8;
 constexpr int kLoadAhead = 4;    // tokens a thread fetches at a time
 
 struct SelectParams {
@@ -53,20 +54,14 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return w != w ? 0u : u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
-// Inclusive sum over the CTA's threads.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sum over the warp.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(kFull, v, o);
     if (lane >= o) v += x;
   }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  int before = lane < warp ? warp_sums[lane] : 0;  // of the warps before this one
-#pragma unroll
-  for (int o = kSelWarps / 2; o > 0; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
-  return v + __shfl_sync(kFull, before, 0);
+  return v;
 }
 
 __device__ __forceinline__ int cluster_rank() {
@@ -84,21 +79,29 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Four words at the place in rank `rank`'s shared memory that p has in this CTA's.
-__device__ __forceinline__ int4 load_of(const int *p, int rank) {
+// Two words (or one) at the place in rank `rank`'s shared memory that p has in this CTA's.
+__device__ __forceinline__ uint32_t place_in(const int *p, int rank) {
   uint32_t at;
-  int4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(at));
+  return at;
+}
+__device__ __forceinline__ int2 load2_of(const int *p, int rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y) : "r"(place_in(p, rank)));
+  return v;
+}
+__device__ __forceinline__ int load_of(const int *p, int rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(place_in(p, rank)));
   return v;
 }
 
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[3][kBins];
-  __shared__ int sums[3][kSelWarps], sums2[kSelWarps];
+  __shared__ __align__(16) int coarse[3][kCoarse];  // sums of 32 bins
+  __shared__ int sums[kSelWarps], sums2[kSelWarps];
   __shared__ int pick[2];
   __shared__ __align__(16) int counts[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -173,30 +176,43 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         const uint32_t k = key_at(t);
         if ((k & known) == prefix) atomicAdd(&hist[pass][(k >> shift) & mask], 1);
       }
+    __syncthreads();
+    {
+      static_assert(kBins == 4 * kSelThreads, "four bins a thread");
+      const int4 v = *reinterpret_cast<const int4 *>(&hist[pass][4 * tid]);
+      int n = v.x + v.y + v.z + v.w;
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) n += __shfl_xor_sync(kFull, n, x);
+      if (tid % 8 == 0) coarse[pass][tid / 8] = n;
+    }
     cluster_sync();
-    // thread i looks after kPer bins from kBins - 1 - kPer i down
-    constexpr int kPer = kBins / kSelThreads;
-    const int b0 = kBins - 1 - kPer * tid;
-    int n[kPer], total = 0;
+    if (warp == 0) {
+      // From the top: which 32 bins, then which of them.  Lane i looks after two sums, the
+      // (2 i + 1)-th and (2 i + 2)-th, then after a bin.
+      int2 v[kMaxRanks];
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) n[u] = 0;
-    int4 v[kMaxRanks];
+      for (int k = 0; k < kMaxRanks; ++k)  // all on their way at once
+        v[k] = k < ranks ? load2_of(&coarse[pass][kCoarse - 2 - 2 * lane], k) : make_int2(0, 0);
+      int first = 0, second = 0;
 #pragma unroll
-    for (int k = 0; k < kMaxRanks; ++k)  // all on their way at once
-      if (k < ranks) v[k] = load_of(&hist[pass][b0 + 1 - kPer], k);
+      for (int k = 0; k < kMaxRanks; ++k) first += v[k].y, second += v[k].x;
+      int before = warp_scan(first + second, lane) - first - second;
+      const bool here = before < need && need <= before + first + second;
+      const int src = __ffs(__ballot_sync(kFull, here)) - 1;
+      const bool low = need > before + first;
+      if (low) before += first;
+      const int bin = 32 * (__shfl_sync(kFull, kCoarse - 1 - 2 * lane - low, src) + 1) - 1 - lane;
+      const int rest = need - __shfl_sync(kFull, before, src);
+      int n[kMaxRanks], total = 0;
 #pragma unroll
-    for (int k = 0; k < kMaxRanks; ++k)
-      if (k < ranks) n[0] += v[k].w, n[1] += v[k].z, n[2] += v[k].y, n[3] += v[k].x;
+      for (int k = 0; k < kMaxRanks; ++k) n[k] = k < ranks ? load_of(&hist[pass][bin], k) : 0;
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) total += n[u];
-    int before = block_scan(total, sums[pass]) - total;
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      if (before < need && need <= before + n[u]) {
-        pick[0] = b0 - u;
-        pick[1] = need - before;
+      for (int k = 0; k < kMaxRanks; ++k) total += n[k];
+      before = warp_scan(total, lane) - total;
+      if (before < rest && rest <= before + total) {
+        pick[0] = bin;
+        pick[1] = rest - before;
       }
-      before += n[u];
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(pick[0]) << shift;
@@ -225,13 +241,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     n_tie += __popc(tie);
   }
   if (lane == 0) {
-    sums[0][warp] = n_more;
+    sums[warp] = n_more;
     sums2[warp] = n_tie;
   }
   __syncthreads();
   int at_more = 0, at_tie = 0;  // before the warp's span
   for (int w = 0; w < warp; ++w) {
-    at_more += sums[0][w];
+    at_more += sums[w];
     at_tie += sums2[w];
   }
   if (warp == kSelWarps - 1 && lane == 0) {
@@ -240,7 +256,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   }
   cluster_sync();
   for (int k = 0; k < rank; ++k) {
-    const int4 v = load_of(counts, k);
+    const int2 v = load2_of(counts, k);
     at_more += v.x;
     at_tie += v.y;
   }
