@@ -22,8 +22,8 @@
 // however few lists there are.
 //
 // Bound: memory, 8 D bytes a kept token and kv head (K and V read and written).  32 sequences
-// of 2000 to 4096 tokens to 2048: 109 us, of which 17 to 19 select and 89 move 0.5 GB.  Few
-// long lists: the chain of passes and barriers (1 x 32768 to 4096, 8 lists: 36 us, 21 select).
+// of 2000 to 4096 tokens to 2048: 107 us, of which 16 select and 90 move 0.5 GB.  Few
+// long lists: the chain of passes and barriers (1 x 32768 to 4096, 8 lists: 26 us, 17 select).
 #include "pa_device.cuh"
 #include "pa_evict.h"
 
@@ -409,13 +409,13 @@ int launch_move(const EvictLaunch &a, MoveParams &p, int longest, cudaStream_t s
   p.max_blocks = a.max_blocks;
   p.dst_blocks = a.dst_blocks;
   p.num_pages = a.num_pages;
-  // As many strips as give every SM a CTA, of 32 bytes or more, and CTAs of 1024 threads, so
-  // that one has 64 KB in flight: with four CTAs of 256 an SM instead, 1 x 4096 of 32768 tokens
-  // takes 52 us (37), 4 x 4096 of 8192 42 (32), 32 x 2048 110 (109).  Short lists: one chunk of
-  // 256 threads.
+  // As many strips, of 32 bytes or more, as make one wave of CTAs, one an SM (4 x 4096 of 8192
+  // tokens: 128 CTAs 26 us, 256 32), and CTAs of 1024 threads, so that one has 64 KB in flight:
+  // with four CTAs of 256 an SM instead, 1 x 4096 of 32768 took 52 us for 37, 4 x 4096 of 8192
+  // 42 for 32, 32 x 2048 110 for 109.  Short lists: one chunk of 256 threads.
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   p.strips = 1;
-  while (p.strips < p.row_bytes / 32 && lists * p.strips * 2 < sms_or_default()) p.strips *= 2;
+  while (p.strips < p.row_bytes / 32 && lists * p.strips * 4 <= sms_or_default()) p.strips *= 2;
   const int threads = static_cast<int64_t>(longest) * (p.row_bytes / p.strips / 16) <=
                               256 * kMoveUnroll ? 256 : kMoveMaxThreads;
   const dim3 grid(static_cast<unsigned>(lists), 2 * p.strips + (a.weights ? 1 : 0));
@@ -453,7 +453,7 @@ int launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   const int64_t most = static_cast<int64_t>(a.max_blocks) * kPageSize;
   const int64_t keys = most - a.sink - a.recent > 0 ? most - a.sink - a.recent : 0;
   // Few lists of many tokens: a cluster each, of 2048 keys or more a CTA (8 lists of 32768:
-  // 68 us with 1 CTA, 21 with 8; the call with the move 57 and 36).
+  // 68 us with 1 CTA, 21 with 8, and 17 since the sums are taken in two steps).
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   int ranks = 1;
   while (ranks < kMaxRanks && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks) ranks *= 2;
