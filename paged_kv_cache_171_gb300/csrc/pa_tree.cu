@@ -13,7 +13,7 @@
 // and no more (two or three waves of shorter ranges: 205 -> 216 us and up, for a start and
 // a merge each).  4 x 64 drafted tokens of 64 heads over 32768: 205 us, 1.34 PFLOP/s, the
 // tensor pipe busy 65% of the cycles that a CTA runs and waiting for the softmax in the
-// others.  16 x 60 of 32 heads over 1000 to 32000: 100 us; equal parts of every sequence
+// others.  16 x 60 of 32 heads over 500 to 8000: 100 us; equal parts of every sequence
 // leave the CTAs of the longest one the last to end.
 #include "pa_evict.h"
 #include "pa_prefill_tc.cuh"
