@@ -76,6 +76,7 @@ __device__ __forceinline__ int cluster_size() {
 }
 // Every thread of the cluster: shared memory written before it is seen behind it.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // the aligned forms want whole warps
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }

@@ -236,6 +236,12 @@ __device__ __forceinline__ float folded(const WeightsParams &p, int bg, int rt, 
   return stat_of(m, l);
 }
 
+// Joins the consumer warpgroups.
+__device__ __forceinline__ void consumers_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+}
+
 // ---- rows pass: 64 scores of this thread's row at a time
 struct RowState {
   float m;
@@ -616,10 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (step > 1) {
         // Their states folded, through the row tiles' place: every chunk is complete, so those
         // have been read.
-        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+        consumers_sync();
         float2 *all = reinterpret_cast<float2 *>(smem);
         all[y * kRows + r] = make_float2(m, l);
-        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+        consumers_sync();
         for (int k = y + turns; k < kGroups; k += turns) {
           const float2 v = all[k * kRows + r];
           const float mn = fmaxf(m, v.x);
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *stats = reinterpret_cast<float *>(smem + L::kStats);
         const int e = tid - (kThreads - kGroups * kRows);
         if (e < w.n_held * kRows) stats[e] = folded(p, w.bg, e / kRows, e % kRows);
-        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * kRows) : "memory");
+        consumers_sync();
       }
       const int chunks = w.n * w.n_held;
       int j = y / w.n_held, x = y - j * w.n_held;      // of chunk n
