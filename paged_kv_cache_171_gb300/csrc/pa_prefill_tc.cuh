@@ -536,6 +536,12 @@ __device__ __forceinline__ bool softmax_pair_sync_any(bool c) {
 __device__ __forceinline__ void softmax_group_sync() {
   asm volatile("bar.sync 2, 128;" ::: "memory");
 }
+// Barriers 3, 4 and 5 join a warpgroup (0: the MMA and copy warps): its warps have to meet
+// between two changes of their registers (setmaxnreg).
+__device__ __forceinline__ void warpgroup_sync(int wg) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(3 + wg) : "memory");
+}
 // Softmax warpgroup x (warps 4 + 4 x .. 7 + 4 x): lane l of warp w owns TMEM
 // lane r = 32 (w % 4) + l of row tile x, i.e. row rr = r (split rows:
 // r mod 64): query qx[x] + rr / GT, head hbase + rr % GT.
@@ -1054,12 +1060,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_role();
       else
         mma_role();
-      __syncwarp();
+      warpgroup_sync(0);
       asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       softmax_role();
-      __syncwarp();
+      warpgroup_sync(warp >> 2);
       asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
     }
   } else if (warp == kKLoadWarp || warp == kVLoadWarp) {
