@@ -525,6 +525,7 @@ __device__ __forceinline__ void mma_tiles(int x, uint32_t sb, uint32_t tmem, con
 // returns whether any thread passed true; barrier 2 joins warps 4-7.
 __device__ __forceinline__ bool softmax_pair_sync_any(bool c) {
   uint32_t any;
+  __syncwarp();  // here and below: the aligned forms want whole warps
   asm volatile(
       "{\n\t.reg .pred q, p;\n\tsetp.ne.u32 q, %1, 0;\n\t"
       "bar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -534,6 +535,7 @@ __device__ __forceinline__ bool softmax_pair_sync_any(bool c) {
   return any != 0;
 }
 __device__ __forceinline__ void softmax_group_sync() {
+  __syncwarp();
   asm volatile("bar.sync 2, 128;" ::: "memory");
 }
 // Barriers 3, 4 and 5 join a warpgroup (0: the MMA and copy warps): its warps have to meet
@@ -631,6 +633,7 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
       m = mn;
       lp = __fmul2_rn(lp, make_float2(corr, corr));
     }
+    __syncwarp();  // lanes part above; stores to tensor memory want the whole warp
     // ---- this row's vote: one term of P for this key tile if the tile's
     // largest weight 2^(cand - m) is below 1/16 of the weight of the earlier
     // tiles (NaN while m = -inf: two terms); the warpgroup votes below
@@ -838,6 +841,7 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
     uint32_t o[32];
+    __syncwarp();  // lanes part in the wait above and in what follows
     load_o(c, o);
     if (SR) {
 #pragma unroll
@@ -969,6 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
+    __syncwarp();
     // S_A: columns 0-127, S_B: 128-255, O_A: 256 .. 256+D-1, O_B: 256+D .. 256+2D-1
     tc::alloc(sb + L::kSlot, 512);
     tc::relinquish();

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
+    __syncwarp();
     tc::alloc(sb + L::kSlot, 512);
     tc::relinquish();
   }
@@ -607,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!idle) {
             uint32_t s[64];
+            __syncwarp();  // lanes part where their maxima move; the loads want the whole warp
             tc::ld32(at + 64 * (i & 1), *reinterpret_cast<uint32_t(*)[32]>(s));
             tc::ld32(at + 64 * (i & 1) + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             tc::wait_ld();
