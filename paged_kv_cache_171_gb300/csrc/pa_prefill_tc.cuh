@@ -85,9 +85,13 @@
 // in the MMA: the V load warp replaces such values by 0 in the tiles with drafted keys and
 // raises a flag, with which the rows that do see them add them at the end.
 // A tree's weights take one 16-bit term throughout (split rows: two, which cost nothing there).
-// Rounding changes each weight by half a step at most, so a dimension of the output by
-// sum_t w_t |v_t| times 2^-9 (bf16) or 2^-12 (fp16) at most, while the output itself is rounded
-// to half a step of the same type: the result is within about two roundings of the exact one.
+// Rounding changes each weight by half a step at most, 2^-8 (bf16) or 2^-11 (fp16) of itself, so
+// a dimension of the output by as much of sum_t w_t |v_t|, while the output itself is rounded to
+// half a step of the same type.  fp16 holds no weight below 2^-14 to that: P is therefore 2^7 p
+// there (p <= 2^8, so at most 2^15), which O and l share and O / l does not see, and weights
+// down to 2^-21 of the row's reference are rounded as the others, smaller ones by 2^-32 of the
+// reference at most.  (Without the factor the contribution of 16000 keys beside a sink 16 nats
+// above them was 2 to 6% off, beside one 17.5 nats above them nearly all of it lost.)
 // The remainder's P V MMAs and the vote cost more than that is worth (4 x 64 drafted tokens
 // of 64 heads over 32k: 255 us with them, 205 without).  B's softmax waits for the first half
 // of A's P alone, not for both (285 -> 255 us; no wait at all: 298, a quarter: as the half).
@@ -573,6 +577,8 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
   const uint32_t tSx = tmem + x * kKeys + lane_base;      // S_x, then P_x
   const uint32_t tOx = tmem + 2 * kKeys + x * D + lane_base;
   const float qs = p.qscale;
+  // trees in fp16: P = 2^7 times the weights, in l as in O
+  constexpr float kLift = TREE && !BF16 ? 7.f : 0.f;
   const int nt = w.n_tiles[x];
 
   bool bad = false;
@@ -638,7 +644,7 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
     // largest weight 2^(cand - m) is below 1/16 of the weight of the earlier
     // tiles (NaN while m = -inf: two terms); the warpgroup votes below
     const bool fine = 16.f * ex2(cand - m) < lp.x + lp.y;
-    const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: weights are 0
+    const float nm = m == -INFINITY ? 0.f : kLift - m;  // nothing seen yet: weights are 0
     const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
 
     auto head = [&](int ch, int k, uint32_t &hi) {  // packed fp32x2: one instruction per pair
