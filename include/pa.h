@@ -745,8 +745,9 @@ int pa_compact_kv(void *k_cache, void *v_cache, float *weights, const int32_t *b
  *   out[b][i][h] = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m) over them, rounded to dtype.
  * The weights of the sum above are rounded to dtype too, those of the sum below are not: besides
  * the result's own rounding an element is off by up to half a step (2^-8 bf16, 2^-11 fp16) of
- * sum_t w_t |v_t|, w_t the normalised weights.  In fp16 weights below 2^-21 of the row's largest
- * are off by up to 2^-32 of it instead.
+ * sum_t w_t |v_t|, w_t the normalised weights, and by 2^-23 of it for every 16 keys (the tensor
+ * cores cut their sums off: up to 7e-4 over 131072 keys of one sign).  In fp16 weights below 2^-21
+ * of the row's largest are off by up to 2^-32 of it instead.
  * A query that sees nothing gives zeros.  A drafted token's K or V that is not finite
  * reaches only the queries that see it.  Bits from n_new on are not used.
  *   mask       device int32 [batch][n_new][ceil(n_new / 32)] (pa_tree_mask, or any other)

@@ -647,12 +647,17 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
     const float nm = m == -INFINITY ? 0.f : kLift - m;  // nothing seen yet: weights are 0
     const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
 
+    float2 tile = make_float2(0.f, 0.f);  // trees: the tile's sums, added to the running ones
+                                          // once, so that small weights count beside large ones
     auto head = [&](int ch, int k, uint32_t &hi) {  // packed fp32x2: one instruction per pair
       const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[32 * ch + 2 * k]),
                                               __uint_as_float(s[32 * ch + 2 * k + 1])),
                                   qs2, nm2);
       const float2 pp = make_float2(ex2(e.x), ex2(e.y));
-      lp = __fadd2_rn(lp, pp);
+      if (TREE)
+        tile = __fadd2_rn(tile, pp);
+      else
+        lp = __fadd2_rn(lp, pp);
       hi = pack2<BF16>(pp.x, pp.y);
       return pp;
     };
@@ -767,6 +772,7 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
       else
         tile_p(std::integral_constant<int, 0>{}, 2);
     }
+    if (TREE) lp = __fadd2_rn(lp, tile);
   }
   tc::wait_st();
   if (nt == 0) return;

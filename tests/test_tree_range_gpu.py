@@ -64,3 +64,29 @@ def test_the_others_beside_a_sink(above, n, hq, at):
     want, bound = _bound(*case, seen, 0.1)
     off = (got.double() - want).abs() - bound
     assert (off <= 0).all(), (off.max().item(), (off / want.abs()).max().item())
+
+
+@pytest.mark.parametrize("n", [4, 12, 20])
+def test_small_weights_count_beside_a_large_one(n):
+    """262144 keys 15 nats below a sink: each weighs 2.57 of the last places of a running sum that
+    holds the sink's, so added one by one they would count as 3."""
+    t, dt, hq, scale = 262144, torch.float16, 8, 0.1
+    q, k, v, bt, ctx = _sink(t, n, hq, dt, 15, 0, 4)
+    k[..., 1:] *= 0.25
+    seen, _ = _seen(_parents(1, n, n))
+    many = [x.expand(COPIES, *x.shape[1:]).contiguous() for x in (q, bt, ctx, ref.bits(seen))]
+    got = _run(many[0], k, v, many[1], many[2], many[3], scale)[0].double()
+    kk, vv = ref.rows(k, bt, 0, t + n)[0], ref.rows(v, bt, 0, t + n)[0]
+    half = torch.finfo(dt).eps / 2
+    for i in (0, n - 1):
+        vis = torch.cat((torch.ones(t, dtype=torch.bool), seen[0, i]))[None]
+        p, l, err = ref.attention(q[0, i:i + 1].double(), kk, vis, scale)
+        want, size = p[0] @ vv, p[0] @ vv.abs()
+        # Roundings of the result and of the weights; fp32's scores, exponentials and sums (a
+        # half step a tile of 128 keys, and 32 for the tile's own); the tensor cores', which cut
+        # the running sum off after each 16 keys, 2^-23 of it; fp16's last places of 2^7 p.
+        bound = half * want.abs() + size * (half * 1.01 + err[0] + 2 * ref.H32 * (t / 128 + 32)
+                                            + t / 16 * 2.0 ** -23)
+        bound += 2.0 ** -32 * vv[vis[0]].abs().sum(0) / l[0]
+        off = (got[i] - want).abs() - bound
+        assert (off <= 0).all(), (off.max().item(), ((got[i] - want) / want).mean().item())
