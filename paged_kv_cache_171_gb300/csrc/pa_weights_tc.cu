@@ -281,6 +281,26 @@ __device__ __forceinline__ void take_scores(uint32_t (&s)[64], int key0, int lim
   st.l = __fadd2_rn(st.l, __fadd2_rn(e2, f2));
 }
 
+// Rows from `until` on only fill a tile up: zeros, which weigh nothing (lse = inf), but whose
+// score at a key with a value that is not finite is NaN, and with it the key's sum.  The last of
+// 32 tells; their scores are set to 0 then.  The whole warp.  (4 x 512 of 32/8 heads over 7680: 223
+// -> 225 us, 2 x 33 of 64/8 over 32k: 87 -> 89; masks in the sums themselves: 226 and 88, but 8%
+// more for groups that leave each tile padded; these by themselves, from q and K, where a sum is
+// NaN: 220 and 91.)
+template <int KEYS>
+__device__ __forceinline__ void clear_padding(uint32_t (&s)[KEYS][32], int until) {
+  if (until >= 32) return;
+  bool any = false;
+#pragma unroll
+  for (int x = 0; x < KEYS; ++x) any |= __uint_as_float(s[x][31]) != 0.f;
+  if (!__any_sync(0xffffffffu, any)) return;
+#pragma unroll
+  for (int x = 0; x < KEYS; ++x)
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c >= until) s[x][c] = 0u;
+}
+
 // ---- columns pass: the weights of 32 rows for KEYS keys of this thread, added to their
 // sums (of even and odd rows).  at: the rows' -lse in shared memory; rows from `from` on see
 // the key.
@@ -673,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c0 + 32 * h >= rows) break;
             const uint32_t lse = sb + L::kStats + x * stats_bytes + (c0 + 32 * h) * 4;
             const int from[1] = {(key0 + r - w.ctx - q0) * p.hb - c0 - 32 * h};
+            clear_padding(s[h], rows - c0 - 32 * h);
             if (all)
               add_weights<1, false>(s[h], lse, from, qs, sum);
             else
@@ -712,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             from[x] = (key0 + x * kRows + r - w.ctx - q0) * p.hb - 32 * y;
+          clear_padding(s, min(p.nq, p.n_new - q0) * p.hb - 32 * y);
           if (key0 + 2 * kRows - 1 <= w.ctx + q0)
             add_weights<2, false>(s, lse, from, qs, sum);
           else
