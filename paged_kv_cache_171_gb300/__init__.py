@@ -956,8 +956,8 @@ def append_kv_rope(k_new, v_new, k_cache, v_cache, block_table, seq_idx, pos, co
     pages, hkv, P, D = shape = k_cache.shape
     _want(k_cache, "k_cache", k_new.dtype, shape, index)
     _want(v_cache, "v_cache", k_new.dtype, shape, index)
-    entry = lib().pa_append_kv_rope if rope_pos is None else lib().pa_append_kv_rope_at
-    return _append(entry, "pa_append_kv_rope", k_new, v_new, q, q_out,
+    where = "pa_append_kv_rope" if rope_pos is None else "pa_append_kv_rope_at"
+    return _append(getattr(lib(), where), where, k_new, v_new, q, q_out,
                    (k_cache.data_ptr(), v_cache.data_ptr()), pages, P, hkv, D, block_table,
                    seq_idx, pos, cos_sin, interleaved, index, rope_pos)
 
