@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 
 
 def _case(n, hq, hkv, d, dt, lens, value):
-    """Queries whose dimension 0 is positive; keys 7, 150 and the last but one hold `value` there."""
+    """Queries whose dimension 0 is positive; keys 7, 150 and the last but one hold `value`
+    there."""
     k, v, w, bt, _ = ref.pool([t + n for t in lens], hkv, d, dt, n + hq)
     q = torch.randn((len(lens), n, hq, d), generator=torch.Generator().manual_seed(n)).to(dt)
     q[..., 0] = q[..., 0].abs() + 0.25
