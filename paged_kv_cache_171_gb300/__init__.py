@@ -1238,8 +1238,8 @@ def evict_kv(k_cache, v_cache, weights, block_table, ctx_lens, budget, sink=0, r
     head, its first `sink`, its last `recent` and the heaviest others by weights
     [pages, h_kv, 16]; K, V and weights move to positions 0 .. in place, or to the pages of
     dst_table int32 [B, blocks].  Returns the new lengths, int32 [B] (new_lens if given;
-    apart from the call's other tensors).  workspace: any tensor of pa_evict_kv_workspace_size(...) bytes, as in
-    decode_weighted."""
+    apart from the call's other tensors).  workspace: any tensor of
+    pa_evict_kv_workspace_size(...) bytes, as in decode_weighted."""
     import torch
     index = _device_index(k_cache)
     if _elsewhere(index, stream):

@@ -10,8 +10,8 @@
 // digits of 11, 11 and 10 bits finds the least key kept and how many of its ties are: a CTA's
 // histogram each, and its sums over 32 bins; one warp of every CTA adds the sums of all CTAs up
 // through distributed shared memory, then the 32 bins of the one that matters, and picks the
-// same bin as the others (with all 2048 bins read by every CTA 1 x 32768 to 4096 took 36 us).  Then each warp numbers the kept ones of a span of tokens by ballots and writes their
-// positions.
+// same bin as the others (with all 2048 bins read by every CTA 1 x 32768 to 4096 took 36 us).
+// Then each warp numbers the kept ones of a span of tokens by ballots and writes their positions.
 //
 // move_kernel: row src[j] to position j, where src is ascending, so src[j] >= j: the list
 // may be worked off in place from its start, if a row is stored only when every row of the
@@ -327,7 +327,8 @@ __device__ __forceinline__ void move_rows(const MoveParams &p, char *base, int r
       for (int u = 0; u < kMoveUnroll; ++u) {
         const int i = i0 + u * per + r;
         if (i < m && to[i] >= 0)
-          x[u] = __ldcg(reinterpret_cast<const V *>(base + static_cast<size_t>(from[i]) * row_bytes));
+          x[u] = __ldcg(
+              reinterpret_cast<const V *>(base + static_cast<size_t>(from[i]) * row_bytes));
       }
     };
     load(0, v);
@@ -457,7 +458,8 @@ int launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   // 68 us with 1 CTA, 21 with 8, and 17 since the sums are taken in two steps).
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;
   int ranks = 1;
-  while (ranks < kMaxRanks && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks) ranks *= 2;
+  while (ranks < kMaxRanks && lists * ranks * 2 <= sms_or_default() && keys >= 2 * 2048 * ranks)
+    ranks *= 2;
   const int64_t part = (keys + ranks - 1) / ranks;
   s.held_keys = static_cast<int>(part < kSelKeys ? part : kSelKeys);
   cudaLaunchConfig_t cfg = {};

@@ -700,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               add_weights<1, true>(s[h], lse, from, qs, sum);
           }
         }
-        if (j >= 4 && !(ok = warp_wait(bar(kBarPartFree + (j & 3)), ((j >> 2) - 1) & 1, abort_flag)))
+        if (j >= 4 &&
+            !(ok = warp_wait(bar(kBarPartFree + (j & 3)), ((j >> 2) - 1) & 1, abort_flag)))
           break;
         part[((j & 3) * L::kParts + x) * kRows] = sum[0].x + sum[0].y;
         __syncwarp();
