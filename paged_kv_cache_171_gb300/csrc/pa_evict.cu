@@ -22,8 +22,8 @@
 // however few lists there are.
 //
 // Bound: memory, 8 D bytes a kept token and kv head (K and V read and written).  32 sequences
-// of 2000 to 4096 tokens to 2048: 107 us, of which 16 select and 90 move 0.5 GB.  Few
-// long lists: the chain of passes and barriers (1 x 32768 to 4096, 8 lists: 26 us, 17 select).
+// of 2000 to 4096 tokens to 2048: 108 us, of which 16 select and 90 move 0.5 GB.  Few
+// long lists: the chain of passes and barriers (1 x 32768 to 4096, 8 lists: 30 us, 17 select).
 #include "pa_device.cuh"
 #include "pa_evict.h"
 
@@ -411,8 +411,8 @@ int launch_move(const EvictLaunch &a, MoveParams &p, int longest, cudaStream_t s
   p.max_blocks = a.max_blocks;
   p.dst_blocks = a.dst_blocks;
   p.num_pages = a.num_pages;
-  // As many strips, of 32 bytes or more, as make one wave of CTAs, one an SM (4 x 4096 of 8192
-  // tokens: 128 CTAs 26 us, 256 32), and CTAs of 1024 threads, so that one has 64 KB in flight:
+  // As many strips, of 32 bytes or more, as make one wave of K's and V's CTAs, one an SM (4 x 4096
+  // of 8192 tokens: 128 CTAs 26 us, 256 32; with the weights' plane 160 CTAs, 29), and CTAs of 1024 threads, so that one has 64 KB in flight:
   // with four CTAs of 256 an SM instead, 1 x 4096 of 32768 took 52 us for 37, 4 x 4096 of 8192
   // 42 for 32, 32 x 2048 110 for 109.  Short lists: one chunk of 256 threads.
   const int64_t lists = static_cast<int64_t>(a.batch) * a.n_kv_heads;

@@ -53,14 +53,14 @@
 // order, and its phase parity stays exact.
 //
 // One or two terms of P.  Rounding a weight p to 16 bits changes it by at
-// most 2^-9 p (bf16), and the output row by sum_t w_t d_t v_t (w = p / l,
-// |d_t| <= 2^-9): on short or peaked rows that can exceed the 2e-3 absolute
+// most 2^-8 p (bf16), and the output row by sum_t w_t d_t v_t (w = p / l,
+// |d_t| <= 2^-8): on short or peaked rows that can exceed the 2e-3 absolute
 // bound, so there P keeps a remainder term.  A row tile's key tile j takes
 // one term when, in every row, the tile's largest weight is below 1/16 of
 // the weight l already accumulated over the tiles before it.  Then
 // sum over such tiles of sum_t w_t^2 <= max_j (pmax_j / l) <= 1/16, and the
 // rounding error of the single-term tiles has an rms of at most
-// 2^-9 / sqrt(3) * rms(v) / 4.  The first tile of every row tile (l = 0)
+// 2^-8 / sqrt(3) * rms(v) / 4.  The first tile of every row tile (l = 0)
 // and any tile that holds a new dominant key take two terms.  The four
 // warps of a softmax warpgroup vote per key tile: each posts its warp's
 // vote and arrives on an mbarrier after the head terms of its first 32

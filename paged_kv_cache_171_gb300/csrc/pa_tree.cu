@@ -11,9 +11,9 @@
 //
 // Bound: the MMAs, 4 D a row and key; two CTAs never share an SM, so the ranges fill one wave
 // and no more (two or three waves of shorter ranges: 205 -> 216 us and up, for a start and
-// a merge each).  4 x 64 drafted tokens of 64 heads over 32768: 205 us, 1.34 PFLOP/s, the
-// tensor pipe busy 65% of the cycles that a CTA runs and waiting for the softmax in the
-// others.  16 x 60 of 32 heads over 500 to 8000: 100 us; equal parts of every sequence
+// a merge each).  4 x 64 drafted tokens of 64 heads over 32768: 217 us with new inputs each
+// call, 1.27 PFLOP/s (203 with the same ones), the tensor pipe busy 65% of the cycles that a CTA
+// runs and waiting for the softmax in the others.  16 x 60 of 32 heads over 500 to 8000: 100 us; equal parts of every sequence
 // leave the CTAs of the longest one the last to end.
 #include "pa_evict.h"
 #include "pa_prefill_tc.cuh"

@@ -15,7 +15,7 @@
 // rows and up to 8 query rows as the columns: S = K Q^T straight from the page's tile by
 // ldmatrix, O = V^T P by its transposing form, P from the accumulators by movmatrix.  The
 // weights p enter as bf16 in three terms (24 bits) or as fp16 in two (22 bits, of 2^7 p,
-// so down to 2^-32 of the row's largest): one term would leave 2^-9 or 2^-12 of every
+// so down to 2^-32 of the row's largest): one term would leave up to 2^-8 or 2^-11 of every
 // weight in an fp32 result.  A page's sum has an accumulator of its own that a rounding
 // add joins to the state, because the tensor cores' sums round toward zero.
 //

@@ -32,10 +32,10 @@
 // wait is bounded and gives up early once another role has raised the CTA's abort flag.
 //
 // Bound: the exponentials, two of them a pair (MUFU), and the MMAs, about as long, for chunks
-// of many rows: 4 x 512 tokens of 32/8 heads over 8192, 242 us (rows pass 119, columns pass
-// 129), the exponential pipe busy 52 to 61% of the cycles and the tensor pipe 51 to 60%.  For
+// of many rows: 4 x 512 tokens of 32/8 heads over 8192, 246 us (rows pass 119, columns pass
+// 129), the exponential pipe busy 51 to 60% of the cycles and the tensor pipe 50 to 59%.  For
 // few rows the same two with every hand-off in sight: 2 x 33 tokens of 64/8 heads over 32k,
-// 87 us (44 and 42) for 134 MB of K read twice.
+// 89 us (44 and 44) for 134 MB of K read twice.
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -77,7 +77,7 @@ struct WeightsSmem {
   static constexpr int kColBlk = kRows * 128;          // one 64-column block
   static constexpr int kTile = (D / 64) * kColBlk;
   static constexpr int kStats = (kHeldTiles + kStages) * kTile;  // [row tile or stage][128]
-  static constexpr int kPart = kStats + 4 * kRows * 4;        // [2][4 or 8][keys] sums
+  static constexpr int kPart = kStats + 4 * kRows * 4;        // [kPartBufs][kParts][keys] sums
   static constexpr int kPartKeys = PASS == kMany ? 2 * kRows : kRows;
   static constexpr int kParts = 4;  // sums a key: of each warpgroup (MANY) or row tile (FEW)
   // Buffers of sums.  FEW: four, so that a warpgroup that writes to one at key tile j, and
