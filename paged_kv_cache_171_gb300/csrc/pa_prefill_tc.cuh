@@ -632,14 +632,11 @@ __device__ __forceinline__ void softmax_tiles(uint32_t sb, uint32_t tmem, const 
     }
     const float cand = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * qs;
     const bool need = cand > m + kSlack;
-    float corr = 1.f;
-    if (need) {
-      const float mn = fmaxf(m, cand);
-      corr = ex2(m - mn);  // 0 while m was still -inf
-      m = mn;
-      lp = __fmul2_rn(lp, make_float2(corr, corr));
-    }
-    __syncwarp();  // lanes part above; stores to tensor memory want the whole warp
+    const float mn = need ? cand : m;  // (no branch: lanes that part would not meet again before
+                                       // the whole warp's stores to tensor memory)
+    const float corr = need ? ex2(m - mn) : 1.f;  // 0 while m was still -inf
+    m = mn;
+    lp = __fmul2_rn(lp, make_float2(corr, corr));
     // ---- this row's vote: one term of P for this key tile if the tile's
     // largest weight 2^(cand - m) is below 1/16 of the weight of the earlier
     // tiles (NaN while m = -inf: two terms); the warpgroup votes below
