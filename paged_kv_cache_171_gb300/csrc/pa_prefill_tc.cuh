@@ -118,6 +118,7 @@ constexpr int kKeys = 128;       // keys per K/V tile (8 pages)
 constexpr int kKLoadWarp = 2, kVLoadWarp = 3;
 constexpr int kSoftmaxWarp0 = 4;
 constexpr int kThreads = 12 * 32;
+constexpr int kTreeRegs = 168;   // registers a thread that a tree's CTA is launched with
 
 struct TcParams {
   const uint16_t *q;
@@ -1065,9 +1066,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if constexpr (TREE) {
     // The softmax warpgroups take registers that the other warps do not use: of the 384 x 168
-    // the block was launched with, 128 x 72 + 256 x 216 = 64512.  A row's 128 scores and its
-    // P then stay in registers (spilt before: 328 -> 285 us).
-    static_assert(128 * 72 + 256 * 216 <= kThreads * 168, "the split draws on the launch's");
+    // the block was launched with (which the host makes sure of), 128 x 72 + 256 x 216 = 64512.
+    // A row's 128 scores and its P then stay in registers (spilt before: 328 -> 285 us).
+    static_assert(128 * 72 + 256 * 216 <= kThreads * kTreeRegs, "the split draws on the launch's");
+    static_assert(kTreeRegs == 168, "what the warpgroups go back to");
     if (warp < kSoftmaxWarp0) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp >= kKLoadWarp)

@@ -116,12 +116,26 @@ __global__ void __launch_bounds__(128)
   if (depth) depth[at] = up;
 }
 
+// Whether `kern` is launched with the registers that its setmaxnreg split adds up to; of fewer
+// its softmax warps would wait for ever.
+template <class K>
+bool launched_with(K *kern, int registers, ContextCache<bool> &known) {
+  bool fits = false;
+  if (known.get(current_context_id(), &fits)) return fits;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return false;
+  fits = attr.numRegs >= registers;
+  known.put(current_context_id(), fits);
+  return fits;
+}
+
 template <int D, bool BF16>
 int launch_t(const TreeLaunch &a, cudaStream_t stream) {
   using L = TcSmem<D>;
   auto kern = prefill_tc_kernel<D, 1, BF16, true>;
-  static ContextCache<bool> smem_set;
+  static ContextCache<bool> smem_set, regs_known;
   if (set_smem_limit(kern, L::kAlloc, smem_set) != PA_OK) return PA_ERR_CUDA;
+  if (!launched_with(kern, kTreeRegs, regs_known)) return PA_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   const Plan y = plan_of(a.batch, a.n_new, a.n_q_heads, a.n_kv_heads, a.max_blocks, sms);
