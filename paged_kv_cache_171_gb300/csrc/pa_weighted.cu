@@ -16,7 +16,9 @@
 // ldmatrix, O = V^T P by its transposing form, P from the accumulators by movmatrix.  The
 // weights p enter as bf16 in three terms (24 bits) or as fp16 in two (22 bits, of 2^7 p,
 // so down to 2^-32 of the row's largest): one term would leave up to 2^-8 or 2^-11 of every
-// weight in an fp32 result.  A page's sum has an accumulator of its own that a rounding
+// weight in an fp32 result.  The normaliser takes the weights of 16 pages at a time: added one
+// by one to a sum that holds an attention sink's, weights 14 to 17 nats below it round to whole
+// last places of that sum (2e-4 of the result over 32768 keys, now 4e-6).  A page's sum has an accumulator of its own that a rounding
 // add joins to the state, because the tensor cores' sums round toward zero.
 //
 // Work split.  The pages of all (sequence, kv head, tile of 8 query rows) items, laid end
@@ -43,6 +45,7 @@ constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its f
 constexpr int kWarps = 8;                   // a CTA, one CTA an SM
 constexpr int kTile = 8;                    // query rows a tile
 constexpr int kMinPages = 2;                // least pages a run has
+constexpr int kSumPages = 16;               // whose weights are summed before they join l
 constexpr int kFoldThreads = 256;           // of the second and third kernel
 constexpr int kFoldTokens = 512;            // of the third, a round
 constexpr int kFoldElements = 32;           // of the second, a CTA
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
     for (int k = 0; k < KS; ++k) o[k][0] = o[k][1] = make_float2(0.f, 0.f);
     float2 m = make_float2(kNoKey, kNoKey), l = make_float2(0.f, 0.f);
+    float2 some = make_float2(0.f, 0.f);  // of up to kSumPages pages, then part of l
     float *score = p.scores + static_cast<size_t>(row0) * p.max_blocks * kPageSize;
 
     for (int i = 0; i < n && at.tokens > 0; ++i) {
@@ -314,6 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const float2 c = make_float2(ex2(m.x - a), ex2(m.y - b));
         m = make_float2(a, b);
         l = __fmul2_rn(l, c);
+        some = __fmul2_rn(some, c);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           o[k][0] = __fmul2_rn(o[k][0], c);
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float2 w = make_float2(ex2(s[2 * u] - m.x), ex2(s[2 * u + 1] - m.y));
-        l = __fadd2_rn(l, w);
+        some = __fadd2_rn(some, w);
         if (!BF16) w = make_float2(w.x * 128.f, w.y * 128.f);
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {
@@ -349,9 +354,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         o[k][0] = __fadd2_rn(o[k][0], make_float2(t[0], t[1]));
         o[k][1] = __fadd2_rn(o[k][1], make_float2(t[2], t[3]));
       }
+      if (i % kSumPages == kSumPages - 1) {
+        l = __fadd2_rn(l, some);
+        some = make_float2(0.f, 0.f);
+      }
       __syncwarp();  // the stage has been read by every lane
       issue();
     }
+    l = __fadd2_rn(l, some);
 
     // ---- the part's state
 #pragma unroll
