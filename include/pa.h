@@ -652,7 +652,7 @@ size_t pa_prefill_kv4_workspace_size(int batch, int n_new, int n_q_heads, int n_
  *   out as in pa_decode, p[h][t] the softmax's weights,
  *   weights[t][g] = (t < T - fresh ? weights[t][g] : 0) + sum of p[h][t] over g's query heads
  * (a decode step's fresh = 1: the step's own token).  fp32 sums in a fixed order; in out's, fp16
- * caches hold p to 22 bits, and to 2^-32 of the row's largest (bf16: 24 bits).
+ * caches hold p to 22 bits, and to 2^-38 of the row's largest (bf16: 24 bits).
  *   workspace  pa_decode_weighted_workspace_size(...) bytes, 16-byte aligned, contents on
  *              entry do not matter, not shared by calls that overlap on the GPU; it holds
  *              the step's scores (4 bytes a query head and token of the table)

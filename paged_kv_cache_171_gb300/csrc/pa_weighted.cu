@@ -14,12 +14,13 @@
 // Operand form.  mma.sync m16n8k16 with the tokens (then the head dimensions) as the 16
 // rows and up to 8 query rows as the columns: S = K Q^T straight from the page's tile by
 // ldmatrix, O = V^T P by its transposing form, P from the accumulators by movmatrix.  The
-// weights p enter as bf16 in three terms (24 bits) or as fp16 in two (22 bits, of 2^7 p,
-// so down to 2^-32 of the row's largest): one term would leave up to 2^-8 or 2^-11 of every
-// weight in an fp32 result.  The normaliser takes the weights of 16 pages at a time: added one
-// by one to a sum that holds an attention sink's, weights 14 to 17 nats below it round to whole
-// last places of that sum (2e-4 of the result over 32768 keys, now 4e-6).  A page's sum has an accumulator of its own that a rounding
-// add joins to the state, because the tensor cores' sums round toward zero.
+// weights p enter as bf16 in three terms (24 bits) or as fp16 in two (22 bits, of 2^13 p,
+// so down to 2^-38 of the row's largest; p is at most 2^2 there, 2^8 in bf16): one term would
+// leave up to 2^-8 or 2^-11 of every weight in an fp32 result.  The normaliser takes the
+// weights of 16 pages at a time: added one by one to a sum that holds an attention sink's,
+// weights 14 to 17 nats below it round to whole last places of that sum (2e-4 of the result
+// over 32768 keys, now 4e-6).  A page's sum has an accumulator of its own that a rounding add
+// joins to the state, because the tensor cores' sums round toward zero.
 //
 // Work split.  The pages of all (sequence, kv head, tile of 8 query rows) items, laid end
 // to end, are cut into equal runs, one a warp: eight warps an SM, each with a ring of
@@ -39,7 +40,6 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleSlack = 8.0f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNoKey = -3.402823466e38f;  // running max of a row before its first key
 constexpr int kWarps = 8;                   // a CTA, one CTA an SM
@@ -125,6 +125,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const __grid_constant__ CUtensorMap vmap, const WeightedParams p) {
   using L = WeightedSmem<D>;
   constexpr int KS = D / 16, kTerms = BF16 ? 3 : 2;
+  // How far (log2) scores may pass the reference; fp16's weights fill its range above that.
+  // (Slack 0 to 8 in fp16: the same time.  2^7 p left 1e-4 behind a sink 17 nats above 32768 keys.)
+  constexpr int kSlack = BF16 ? 8 : 2;
+  constexpr float kLift = BF16 ? 1.f : static_cast<float>(1 << (15 - kSlack));
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
       // ---- move the references when a score outgrows them
       const float grow = fmaxf(fmaxf(s[0], s[2]) - m.x, fmaxf(s[1], s[3]) - m.y);
-      if (__any_sync(kFull, grow > kRescaleSlack)) {
+      if (__any_sync(kFull, grow > kSlack)) {
         float a = fmaxf(s[0], s[2]), b = fmaxf(s[1], s[3]);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int u = 0; u < 2; ++u) {
         float2 w = make_float2(ex2(s[2 * u] - m.x), ex2(s[2 * u + 1] - m.y));
         some = __fadd2_rn(some, w);
-        if (!BF16) w = make_float2(w.x * 128.f, w.y * 128.f);
+        if (!BF16) w = make_float2(w.x * kLift, w.y * kLift);
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {
           const uint32_t head = pack2<BF16>(w.x, w.y);
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       l.y += __shfl_xor_sync(kFull, l.y, x);
     }
     float *state = p.states + (static_cast<size_t>(item) + worker) * (kTile * (D + 4));
-    const float down = BF16 ? 1.f : 1.f / 128.f;
+    constexpr float down = 1.f / kLift;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (2 * lc + u >= n_r) continue;

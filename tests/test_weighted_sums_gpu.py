@@ -50,3 +50,29 @@ def test_small_weights_count_beside_a_large_one(dt):
     for c in some.tolist():
         gw = w[c * pages:(c + 1) * pages, 0].reshape(-1).cpu().double()
         assert ((gw - add).abs() <= wb).all(), ((gw - add).abs() / add).max().item()
+
+
+@pytest.mark.parametrize("above", [15, 17, 18.5])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_a_result_made_up_of_small_weights(above, dt):
+    """32768 keys far below a sink that has no value: the result is theirs alone, so it has the
+    relative error that their weights are held with."""
+    t, d, hq, scale = 32768, 64, 2, 0.1
+    gen = torch.Generator().manual_seed(2)
+    k = torch.zeros((t // 16, 1, 16, d))
+    k[..., 1:] = torch.randn(k[..., 1:].shape, generator=gen) * 0.005
+    v = torch.randn(k.shape, generator=gen) * 0.3 + 0.5
+    for page in range(0, t // 16, 8):  # one a part of the sequence, wherever it is cut
+        k[page, 0, 0] = 0
+        k[page, 0, 0, 0] = above
+        v[page, 0, 0] = 0
+    q = torch.randn((1, hq, d), generator=gen)
+    q[..., 0] = 10
+    k, v, q = k.to(dt), v.to(dt), q.to(dt)
+    bt = torch.arange(t // 16, dtype=torch.int32)[None]
+    w = torch.zeros((t // 16, 1, 16))
+    ctx = torch.tensor([t], dtype=torch.int32)
+    got = pa.decode_weighted(q.cuda(), k.cuda(), v.cuda(), w.cuda(), bt.cuda(), ctx.cuda(), scale)
+    assert pa.pa_last_device_error() == 0
+    out, bound, _, _ = ref.weighted_decode(q, k, v, w, bt, ctx, scale, 1)
+    assert ((got.cpu().double() - out).abs() <= bound).all(), ((got.cpu() - out) / out).abs().max()
